@@ -302,6 +302,130 @@ metis_status metis_mxfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, c
                               const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, float *C,
                               int64_t ldc, void *stream);
 
+/* ------------------------------------------------------------------- int8
+ * A third operand format for the same linear layer: 8-bit integers with one
+ * binary32 scale per line, a line being what one output row or column of the
+ * product reduces over (a token's activations, an output channel's weights).
+ * For the products that lose too much in 4 bits, and for serving.  With a the
+ * largest magnitude of the line, in binary32 (RN: rounded to nearest),
+ *   s = max(RN(a / 127), 2^-126),  inv = RN(1 / s),  y = RN(x inv),
+ *   code = y rounded to the nearest integer, ties to even (METIS_RNE), or
+ *          floor(y) + [u < y - floor(y)] (METIS_SR),
+ * clamped to [-127, 127], where u is 2^-16 times the 16-bit Philox draw of
+ * (seed, tag with role 0, step) at the element's row-major position
+ * i * cols + j in M, the same draw for both orientations.
+ *
+ * metis_i8: n_outer lines of k_len codes each, at a row pitch of
+ * metis_int8_pitch(k_len) bytes (k_len rounded up to 128); the bytes behind
+ * k_len in a row are zero (the quantiser writes them so).  codes is 16-byte
+ * aligned.  Device buffers owned by the caller.
+ *
+ * metis_int8_quantize: M is rows x cols, row-major with leading dimension ld,
+ * bf16 or fp32.  axes: METIS_AXIS1 fills ax1 (K along a row: rows lines of
+ * cols codes), METIS_AXIS0 fills ax0 (K down a column: cols lines of rows
+ * codes, the quantised transpose); an orientation not asked for may be NULL.
+ * A non-finite element sets the numeric flag of metis_status_sync and leaves
+ * unspecified codes.  ws holds metis_int8_quantize_workspace(rows, cols,
+ * axes) bytes, 16-byte aligned.  rows == 0 or cols == 0 returns METIS_OK with
+ * nothing enqueued.
+ *
+ * metis_int8_gemm: C = diag(s_A) (A B^T) diag(s_B), row-major with leading
+ * dimension ldc >= B->n_outer, binary32 or bf16 (c_dtype).  A and B have the
+ * same k_len, at most 133056 (METIS_E_UNSUPPORTED above): sums are exact in
+ * int32, and an output is RN(RN(RN(sum) s_A) s_B), rounded once more for
+ * bf16.  n_outer == 0 on either side is a no-op, k_len == 0 invalid.
+ *
+ * metis_int8_linear: Y = X-hat W-hat for serving: X (tokens x k_len, bf16 or
+ * fp32) is quantised to nearest with one scale per token and multiplied with
+ * W, the K-down-the-columns orientation of a weight (n_outer output channels
+ * of k_len codes).  Equal to metis_int8_quantize along METIS_AXIS1 followed
+ * by metis_int8_gemm, bit for bit.  ws holds
+ * metis_int8_linear_workspace(tokens, k_len) bytes, 256-byte aligned.
+ *
+ * Argument errors return synchronously; nothing is allocated. */
+typedef struct {
+  int8_t *codes;
+  float *scales;   /* n_outer binary32 */
+  int64_t n_outer;
+  int64_t k_len;
+} metis_i8;
+
+int64_t metis_int8_pitch(int64_t k_len);
+size_t metis_int8_quantize_workspace(int64_t rows, int64_t cols, int32_t axes);
+metis_status metis_int8_quantize(const void *M, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                                 int32_t axes, int32_t rounding, uint64_t seed, uint32_t tag, int64_t step,
+                                 const metis_i8 *ax0, const metis_i8 *ax1, void *ws, size_t ws_bytes,
+                                 void *stream);
+metis_status metis_int8_gemm(const metis_i8 *A, const metis_i8 *B, void *C, int32_t c_dtype, int64_t ldc,
+                             void *stream);
+size_t metis_int8_linear_workspace(int64_t tokens, int64_t k_len);
+metis_status metis_int8_linear(const void *X, int32_t dtype, int64_t tokens, int64_t ldx, const metis_i8 *W,
+                               void *Y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ AdamW
+ * The update of the master weights from the layers' gradients, many tensors
+ * at once.  Per element, each operation rounded to binary32, g the gradient
+ * (times *clip where clip is not NULL):
+ *   m' = b1 m + (1 - b1) g,  v' = b2 v + ((1 - b2) g) g,  r' = sqrt(v'),
+ *   p' = p (1 - lr wd) - lr / (1 - b1^t) * m' / (r' / sqrt(1 - b2^t) + eps).
+ * An element for which m', v' or p' is not finite keeps p, m and v and sets
+ * the numeric flag of metis_status_sync.
+ *
+ * metis_adamw_tensor: n elements, contiguous; param binary32 (METIS_F32) or
+ * bf16, grad binary32 or bf16.  state_bits 32: m and v are binary32 arrays
+ * (v the second moment), the scales unused.  state_bits 8: m and v are arrays
+ * of E4M3 bytes (v holds r = sqrt(second moment)) in blocks of 256
+ * consecutive elements with one binary32 scale each (m_scale, v_scale:
+ * ceil(n / 256) values): value = E4M3(code) * scale.  The scale is
+ * 2^(floor(log2 amax) - 7), at least 2^-126; a positive r never rounds to
+ * zero.  All-zero codes and scales are the initial state.  The update uses
+ * the new moments before they are rounded.
+ * rounding: METIS_RNE, or METIS_SR for 8-bit states and bf16 parameters:
+ * element e takes word e & 3 of the Philox block of counter (e >> 2, tag with
+ * role 6, t), the low half for m and the high half for r; a bf16 parameter
+ * takes the low half of role 7's word.
+ * t: the step, counted from 1: `step`, or where step_count is not NULL the
+ * int64 that it points to in device memory when the kernel runs (for graphs;
+ * every other value is fixed at the call).
+ * A tensor must not appear twice in a call, and tensors must not overlap.
+ * Small tensors share launches; the tensor list is read before the call
+ * returns.
+ *
+ * metis_grad_norm: out[0] = the square root of the sum of squares over all
+ * tensors' gradients (only grad, grad_dtype and n are read), summed in
+ * binary64 in an order fixed by the sizes; out[1] = min(1, max_norm / (norm +
+ * 1e-6)), NaN if the norm is.  out: two binary32 in device memory; out + 1
+ * serves as metis_adamw_config.clip.  ws holds
+ * metis_grad_norm_workspace(tensors, count) bytes, 8-byte aligned. */
+typedef struct {
+  void *param;
+  const void *grad;
+  void *m;
+  void *v;
+  float *m_scale;
+  float *v_scale;
+  int64_t n;
+  int32_t param_dtype; /* metis_dtype */
+  int32_t grad_dtype;  /* metis_dtype */
+  int32_t state_bits;  /* 32 or 8 */
+  uint32_t tag;        /* layer << 16 | operand << 12 */
+} metis_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;              /* >= 1 (ignored with step_count) */
+  const int64_t *step_count; /* device, or NULL */
+  const float *clip;         /* device, or NULL */
+  uint64_t seed;
+  int32_t rounding;          /* metis_rounding */
+} metis_adamw_config;
+
+metis_status metis_adamw_step(const metis_adamw_tensor *tensors, int64_t count, const metis_adamw_config *cfg,
+                              void *stream);
+size_t metis_grad_norm_workspace(const metis_adamw_tensor *tensors, int64_t count);
+metis_status metis_grad_norm(const metis_adamw_tensor *tensors, int64_t count, double max_norm, float *out,
+                             void *ws, size_t ws_bytes, void *stream);
+
 /* Kernel timing for benchmarks.  metis_timing_enable(capacity) creates
  * capacity pairs of HIP events (0 disables timing and releases them); while
  * enabled, each main split-GEMM kernel (kind 0; d = M, N, K, K-extension) and

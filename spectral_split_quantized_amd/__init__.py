@@ -6,4 +6,4 @@ makes seeded synthetic inputs.  The library is loaded on first use, and a
 missing library is an error (there is no fallback path).
 """
 
-__all__ = ["metis", "synth"]
+__all__ = ["layer", "metis", "optim", "synth"]

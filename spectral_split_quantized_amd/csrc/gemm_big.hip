@@ -5,6 +5,7 @@
 #include "gemm_launch.hpp"
 #include "gemm_reg.hpp"
 #include "mxfp4_gemm.hpp"
+#include "int8_gemm.hpp"
 
 namespace metis {
 
@@ -22,6 +23,24 @@ hipError_t launch_mx_gemm(const MxGemmParams& g, hipStream_t st) {
   const int64_t tiles = ceil_div<int64_t>(g.M, 256) * ceil_div<int64_t>(g.N, 256);
   if (tiles <= 0) return hipSuccess;
   hipLaunchKernelGGL((mx_gemm_kernel<2, 2, 4, 4>), dim3((unsigned)tiles), dim3(256), 0, st, g);
+  return hipGetLastError();
+}
+
+hipError_t launch_i8_gemm(const I8GemmParams& g, hipStream_t st) {
+  if (g.M <= 64) {
+    const dim3 grid((unsigned)ceil_div<int64_t>(g.N, 16), 1);
+    if (g.M <= 16) hipLaunchKernelGGL((i8_gemm_skinny_kernel<8, 1, 4>), grid, dim3(512), 0, st, g);
+    else if (g.M <= 32) hipLaunchKernelGGL((i8_gemm_skinny_kernel<8, 2, 4>), grid, dim3(512), 0, st, g);
+    else hipLaunchKernelGGL((i8_gemm_skinny_kernel<8, 4, 2>), grid, dim3(512), 0, st, g);
+    return hipGetLastError();
+  }
+  const int64_t big = ceil_div<int64_t>(g.M, 256) * ceil_div<int64_t>(g.N, 256);
+  if (big >= 256) {
+    hipLaunchKernelGGL((i8_gemm_kernel<2, 2, 4, 4>), dim3((unsigned)big), dim3(256), 0, st, g);
+  } else {
+    const int64_t tiles = ceil_div<int64_t>(g.M, 128) * ceil_div<int64_t>(g.N, 128);
+    hipLaunchKernelGGL((i8_gemm_kernel<2, 2, 2, 2>), dim3((unsigned)tiles), dim3(256), 0, st, g);
+  }
   return hipGetLastError();
 }
 

@@ -18,4 +18,10 @@ struct MxGemmParams;
 // and 16-byte aligned code and scale rows.
 hipError_t launch_mx_gemm(const MxGemmParams& g, hipStream_t st);
 
+struct I8GemmParams;
+
+// C = diag(s_a) A B^T diag(s_b) of two int8 operands; code rows 16-byte
+// aligned with a pitch that is a multiple of 128.
+hipError_t launch_i8_gemm(const I8GemmParams& g, hipStream_t st);
+
 }  // namespace metis

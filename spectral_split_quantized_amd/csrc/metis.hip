@@ -24,6 +24,9 @@
 #include "rsvd.hpp"
 #include "mxfp4.hpp"
 #include "mxfp4_gemm.hpp"
+#include "int8.hpp"
+#include "int8_gemm.hpp"
+#include "adamw.hpp"
 
 using namespace metis;
 
@@ -1130,6 +1133,109 @@ metis_status stream_after(hipStream_t waiter, hipStream_t from, hipEvent_t e) {
   return err == hipSuccess ? METIS_OK : fail(METIS_E_HIP, "stream order: %s", hipGetErrorString(err));
 }
 
+// --------------------------------------------------------------- int8 --
+
+metis_status int8_check(const metis_i8* q, const char* what, int64_t n_outer, int64_t k_len) {
+  if (!q) return fail(METIS_E_INVALID, "%s: null operand", what);
+  if (q->n_outer != n_outer || q->k_len != k_len || n_outer < 0 || k_len < 0)
+    return fail(METIS_E_INVALID, "%s: %lld lines of %lld, not %lld of %lld", what, (long long)q->n_outer,
+                (long long)q->k_len, (long long)n_outer, (long long)k_len);
+  if (n_outer && k_len && (!q->codes || !q->scales)) return fail(METIS_E_INVALID, "%s: null pointer", what);
+  if (((uintptr_t)q->codes & 15) || ((uintptr_t)q->scales & 3))
+    return fail(METIS_E_INVALID, "%s: codes not 16-byte aligned", what);
+  return METIS_OK;
+}
+
+struct I8Ws {
+  float *part0, *part1;
+};
+
+I8Ws carve_int8(Carver& cv, int64_t rows, int64_t cols, int axes) {
+  I8Ws w{};
+  if (!(axes & METIS_AXIS0)) return w;
+  w.part0 = cv.take<float>((size_t)(ceil_div<int64_t>(rows, kI8Tile) * cols));
+  if (axes & METIS_AXIS1) w.part1 = cv.take<float>((size_t)(ceil_div<int64_t>(cols, kI8Tile) * rows));
+  return w;
+}
+
+template <bool SR>
+void launch_int8_rows(const I8QuantParams& q, hipStream_t st) {
+  const dim3 grid((unsigned)q.rows);
+  const int64_t chunks = i8_pitch(q.cols) >> 3;
+  if (chunks <= 64) hipLaunchKernelGGL((i8_quant_rows_kernel<1, 1, SR>), grid, dim3(64), 0, st, q);
+  else if (chunks <= 256) hipLaunchKernelGGL((i8_quant_rows_kernel<4, 1, SR>), grid, dim3(256), 0, st, q);
+  else if (chunks <= 1024) hipLaunchKernelGGL((i8_quant_rows_kernel<8, 2, SR>), grid, dim3(512), 0, st, q);
+  else hipLaunchKernelGGL((i8_quant_rows_kernel<8, 4, SR>), grid, dim3(512), 0, st, q);
+}
+
+metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols, int64_t ld, int axes, int rounding,
+                            uint64_t seed, uint32_t tag, int64_t step, const metis_i8* ax0, const metis_i8* ax1,
+                            const I8Ws& w, hipStream_t st) {
+  I8QuantParams q{};
+  q.src = M;
+  q.dtype = dtype;
+  q.rows = rows, q.cols = cols, q.ld = ld;
+  q.vec = ((uintptr_t)M & 15) == 0 && (ld * (dtype == METIS_BF16 ? 2 : 4)) % 16 == 0;
+  if (axes & METIS_AXIS0) q.codes0 = ax0->codes, q.scales0 = ax0->scales;
+  if (axes & METIS_AXIS1) q.codes1 = ax1->codes, q.scales1 = ax1->scales;
+  q.part0 = w.part0, q.part1 = w.part1;
+  q.sr = rounding == METIS_SR;
+  q.seed = seed, q.tag = tag_with_role(tag, kRoleResid), q.step = (uint32_t)step;
+  if (axes == METIS_AXIS1) {
+    if (q.sr) launch_int8_rows<true>(q, st);
+    else launch_int8_rows<false>(q, st);
+    LAUNCH_CHECK();
+    return METIS_OK;
+  }
+  const dim3 tiles((unsigned)(ceil_div<int64_t>(rows, kI8Tile) * ceil_div<int64_t>(cols, kI8Tile)));
+  hipLaunchKernelGGL(i8_amax_kernel, tiles, dim3(256), 0, st, q);
+  LAUNCH_CHECK();
+  hipLaunchKernelGGL(i8_scales_kernel, dim3(grid1(cols + (q.part1 ? rows : 0), 256)), dim3(256), 0, st, q);
+  LAUNCH_CHECK();
+  if (q.sr) hipLaunchKernelGGL((i8_quant_tile_kernel<true>), tiles, dim3(256), 0, st, q);
+  else hipLaunchKernelGGL((i8_quant_tile_kernel<false>), tiles, dim3(256), 0, st, q);
+  LAUNCH_CHECK();
+  return METIS_OK;
+}
+
+metis_status int8_gemm_check(const metis_i8* A, const metis_i8* B, const void* C, int c_dtype, int64_t ldc) {
+  if (A->k_len != B->k_len)
+    return fail(METIS_E_INVALID, "int8_gemm: inner dimensions %lld and %lld", (long long)A->k_len, (long long)B->k_len);
+  if (A->k_len < 1) return fail(METIS_E_INVALID, "int8_gemm: k_len %lld", (long long)A->k_len);
+  if (A->k_len > kI8MaxK) return fail(METIS_E_UNSUPPORTED, "int8_gemm: k_len %lld > %lld", (long long)A->k_len, (long long)kI8MaxK);
+  if (!dtype_ok(c_dtype)) return fail(METIS_E_INVALID, "int8_gemm: output dtype %d", c_dtype);
+  if (ldc < B->n_outer) return fail(METIS_E_INVALID, "int8_gemm: ldc %lld < %lld", (long long)ldc, (long long)B->n_outer);
+  if (A->n_outer && B->n_outer && !C) return fail(METIS_E_INVALID, "int8_gemm: null output");
+  if ((uintptr_t)C & (c_dtype == METIS_F32 ? 3 : 1)) return fail(METIS_E_INVALID, "int8_gemm: misaligned output");
+  if (ceil_div<int64_t>(A->n_outer, 128) * ceil_div<int64_t>(B->n_outer, 128) > INT32_MAX)
+    return fail(METIS_E_UNSUPPORTED, "int8_gemm: %lld x %lld", (long long)A->n_outer, (long long)B->n_outer);
+  return METIS_OK;
+}
+
+metis_status run_int8_gemm(const metis_i8* A, const metis_i8* B, void* C, int c_dtype, int64_t ldc, hipStream_t st) {
+  const metis_status s = int8_gemm_check(A, B, C, c_dtype, ldc);
+  if (s != METIS_OK) return s;
+  if (A->n_outer == 0 || B->n_outer == 0) return METIS_OK;
+  const I8GemmParams g{A->n_outer, B->n_outer, i8_pitch(A->k_len), A->codes, B->codes, A->scales, B->scales,
+                       C, ldc, c_dtype == METIS_BF16};
+  const hipError_t e = launch_i8_gemm(g, st);
+  if (e != hipSuccess) return fail(METIS_E_HIP, "int8_gemm launch: %s", hipGetErrorString(e));
+  return METIS_OK;
+}
+
+// -------------------------------------------------------------- AdamW --
+
+metis_status adamw_grad_check(const metis_adamw_tensor& a, int64_t i, const char* what) {
+  if (a.n < 0) return fail(METIS_E_INVALID, "%s: tensor %lld: n %lld", what, (long long)i, (long long)a.n);
+  if (a.n > (int64_t)INT32_MAX * kAdamWork)
+    return fail(METIS_E_UNSUPPORTED, "%s: tensor %lld: n %lld", what, (long long)i, (long long)a.n);
+  if (!dtype_ok(a.grad_dtype)) return fail(METIS_E_INVALID, "%s: tensor %lld: grad dtype %d", what, (long long)i, a.grad_dtype);
+  if (a.n && !a.grad) return fail(METIS_E_INVALID, "%s: tensor %lld: null gradient", what, (long long)i);
+  if ((uintptr_t)a.grad & (a.grad_dtype == METIS_F32 ? 3 : 1))
+    return fail(METIS_E_INVALID, "%s: tensor %lld: misaligned gradient", what, (long long)i);
+  return METIS_OK;
+}
+
 }  // namespace
 
 // =================================================================== ABI ===
@@ -1541,6 +1647,218 @@ metis_status metis_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, c
   const hipError_t e = launch_mx_gemm(g, st);
   if (e != hipSuccess) return fail(METIS_E_HIP, "mxfp4_gemm launch: %s", hipGetErrorString(e));
   timing_end(tr, st);
+  return METIS_OK;
+}
+
+// --------------------------------------------------------------- int8 --
+
+int64_t metis_int8_pitch(int64_t k_len) { return k_len < 0 ? 0 : i8_pitch(k_len); }
+
+size_t metis_int8_quantize_workspace(int64_t rows, int64_t cols, int32_t axes) {
+  Carver cv(nullptr, 0);
+  if (rows > 0 && cols > 0) carve_int8(cv, rows, cols, axes);
+  return cv.used() ? cv.used() : 256;
+}
+
+metis_status metis_int8_quantize(const void* M, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int32_t axes,
+                                 int32_t rounding, uint64_t seed, uint32_t tag, int64_t step, const metis_i8* ax0,
+                                 const metis_i8* ax1, void* ws, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(dtype)) return fail(METIS_E_INVALID, "int8_quantize: dtype %d", dtype);
+  if (rows < 0 || cols < 0 || ld < cols)
+    return fail(METIS_E_INVALID, "int8_quantize: shape %lld x %lld, ld %lld", (long long)rows, (long long)cols,
+                (long long)ld);
+  if (axes < 1 || axes > (METIS_AXIS0 | METIS_AXIS1)) return fail(METIS_E_INVALID, "int8_quantize: axes %d", axes);
+  if (rounding != METIS_RNE && rounding != METIS_SR) return fail(METIS_E_INVALID, "int8_quantize: rounding %d", rounding);
+  if (step < 0) return fail(METIS_E_INVALID, "int8_quantize: step %lld", (long long)step);
+  metis_status s;
+  if ((axes & METIS_AXIS0) && (s = int8_check(ax0, "int8_quantize: ax0", cols, rows)) != METIS_OK) return s;
+  if ((axes & METIS_AXIS1) && (s = int8_check(ax1, "int8_quantize: ax1", rows, cols)) != METIS_OK) return s;
+  if (rows == 0 || cols == 0) return METIS_OK;
+  if (!M) return fail(METIS_E_INVALID, "int8_quantize: null input");
+  if (rows > INT32_MAX || ceil_div<int64_t>(rows, kI8Tile) * ceil_div<int64_t>(cols, kI8Tile) > INT32_MAX)
+    return fail(METIS_E_UNSUPPORTED, "int8_quantize: %lld x %lld", (long long)rows, (long long)cols);
+  Carver cv(ws, ws_bytes);
+  const I8Ws w = carve_int8(cv, rows, cols, axes);
+  if (cv.used() > 0 && (!ws || cv.used() > ws_bytes))
+    return fail(METIS_E_WORKSPACE, "workspace %zu < %zu", ws_bytes, cv.used());
+  if ((s = ensure_device_tables()) != METIS_OK) return s;
+  return run_int8_quant(M, dtype, rows, cols, ld, axes, rounding, seed, tag, step, ax0, ax1, w, (hipStream_t)stream);
+}
+
+metis_status metis_int8_gemm(const metis_i8* A, const metis_i8* B, void* C, int32_t c_dtype, int64_t ldc,
+                             void* stream) {
+  if (!A || !B) return fail(METIS_E_INVALID, "int8_gemm: null operand");
+  metis_status s;
+  if ((s = int8_check(A, "int8_gemm: A", A->n_outer, A->k_len)) != METIS_OK) return s;
+  if ((s = int8_check(B, "int8_gemm: B", B->n_outer, B->k_len)) != METIS_OK) return s;
+  return run_int8_gemm(A, B, C, c_dtype, ldc, (hipStream_t)stream);
+}
+
+size_t metis_int8_linear_workspace(int64_t tokens, int64_t k_len) {
+  if (tokens <= 0 || k_len <= 0) return 256;
+  Carver cv(nullptr, 0);
+  cv.take<int8_t>((size_t)(tokens * i8_pitch(k_len)));
+  cv.take<float>((size_t)tokens);
+  return cv.used();
+}
+
+metis_status metis_int8_linear(const void* X, int32_t dtype, int64_t tokens, int64_t ldx, const metis_i8* W, void* Y,
+                               int32_t y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  if (!W) return fail(METIS_E_INVALID, "int8_linear: null weight");
+  metis_status s;
+  if ((s = int8_check(W, "int8_linear: W", W->n_outer, W->k_len)) != METIS_OK) return s;
+  if (!dtype_ok(dtype)) return fail(METIS_E_INVALID, "int8_linear: dtype %d", dtype);
+  if (tokens < 0 || tokens > INT32_MAX || ldx < W->k_len)
+    return fail(METIS_E_INVALID, "int8_linear: %lld tokens, ldx %lld, k_len %lld", (long long)tokens, (long long)ldx,
+                (long long)W->k_len);
+  Carver cv(ws, ws_bytes);
+  const int64_t pitch = i8_pitch(W->k_len);
+  metis_i8 xq{cv.take<int8_t>((size_t)(tokens * pitch)), nullptr, tokens, W->k_len};
+  xq.scales = cv.take<float>((size_t)tokens);
+  if (tokens == 0 || W->n_outer == 0) return METIS_OK;
+  if (!X) return fail(METIS_E_INVALID, "int8_linear: null input");
+  if (!ws || cv.used() > ws_bytes) return fail(METIS_E_WORKSPACE, "workspace %zu < %zu", ws_bytes, cv.used());
+  if ((uintptr_t)ws & 15) return fail(METIS_E_INVALID, "int8_linear: workspace not 16-byte aligned");
+  if ((s = int8_gemm_check(&xq, W, Y, y_dtype, ldy)) != METIS_OK) return s;
+  if ((s = ensure_device_tables()) != METIS_OK) return s;
+  hipStream_t st = (hipStream_t)stream;
+  if ((s = run_int8_quant(X, dtype, tokens, W->k_len, ldx, METIS_AXIS1, METIS_RNE, 0, 0, 0, nullptr, &xq, I8Ws{}, st)) !=
+      METIS_OK)
+    return s;
+  return run_int8_gemm(&xq, W, Y, y_dtype, ldy, st);
+}
+
+// -------------------------------------------------------------- AdamW --
+
+metis_status metis_adamw_step(const metis_adamw_tensor* tensors, int64_t count, const metis_adamw_config* cfg,
+                              void* stream) {
+  if (count < 0 || (count && !tensors) || !cfg) return fail(METIS_E_INVALID, "adamw_step: null argument");
+  if (!(cfg->lr >= 0) || !(cfg->eps >= 0) || !(cfg->weight_decay >= 0) || !isfinite(cfg->lr) || !isfinite(cfg->eps) ||
+      !isfinite(cfg->weight_decay))
+    return fail(METIS_E_INVALID, "adamw_step: lr %g, eps %g, weight_decay %g", cfg->lr, cfg->eps, cfg->weight_decay);
+  if (!(cfg->beta1 >= 0 && cfg->beta1 < 1 && cfg->beta2 >= 0 && cfg->beta2 < 1))
+    return fail(METIS_E_INVALID, "adamw_step: betas %g, %g", cfg->beta1, cfg->beta2);
+  if (cfg->rounding != METIS_RNE && cfg->rounding != METIS_SR)
+    return fail(METIS_E_INVALID, "adamw_step: rounding %d", cfg->rounding);
+  if (!cfg->step_count && cfg->step < 1) return fail(METIS_E_INVALID, "adamw_step: step %lld", (long long)cfg->step);
+  metis_status s;
+  for (int64_t i = 0; i < count; ++i) {
+    const metis_adamw_tensor& a = tensors[i];
+    if ((s = adamw_grad_check(a, i, "adamw_step")) != METIS_OK) return s;
+    if (!dtype_ok(a.param_dtype)) return fail(METIS_E_INVALID, "adamw_step: tensor %lld: param dtype %d", (long long)i, a.param_dtype);
+    if (a.state_bits != 8 && a.state_bits != 32)
+      return fail(METIS_E_INVALID, "adamw_step: tensor %lld: state_bits %d", (long long)i, a.state_bits);
+    if (a.n && (!a.param || !a.m || !a.v || (a.state_bits == 8 && (!a.m_scale || !a.v_scale))))
+      return fail(METIS_E_INVALID, "adamw_step: tensor %lld: null pointer", (long long)i);
+    if (((uintptr_t)a.param & (a.param_dtype == METIS_F32 ? 3 : 1)) ||
+        (a.state_bits == 32 && (((uintptr_t)a.m | (uintptr_t)a.v) & 3)) ||
+        (a.state_bits == 8 && (((uintptr_t)a.m_scale | (uintptr_t)a.v_scale) & 3)))
+      return fail(METIS_E_INVALID, "adamw_step: tensor %lld: misaligned pointer", (long long)i);
+  }
+  if ((s = ensure_device_tables()) != METIS_OK) return s;
+  AdamTable t{};
+  t.b1 = (float)cfg->beta1, t.c1 = (float)(1.0 - cfg->beta1);
+  t.b2 = (float)cfg->beta2, t.c2 = (float)(1.0 - cfg->beta2);
+  t.eps = (float)cfg->eps, t.decay = (float)(1.0 - cfg->lr * cfg->weight_decay);
+  t.lr = cfg->lr, t.db1 = cfg->beta1, t.db2 = cfg->beta2;
+  t.step_count = cfg->step_count;
+  t.clip = cfg->clip;
+  t.seed = cfg->seed;
+  if (!cfg->step_count) {
+    t.step_size = (float)(cfg->lr / (1.0 - pow(cfg->beta1, (double)cfg->step)));
+    t.inv_c2 = (float)(1.0 / sqrt(1.0 - pow(cfg->beta2, (double)cfg->step)));
+    t.step = (uint32_t)cfg->step;
+  }
+  const bool sr = cfg->rounding == METIS_SR;
+  hipStream_t st = (hipStream_t)stream;
+  // one pass per combination of types, a launch per table of tensors
+  for (int kind = 0; kind < 8; ++kind) {
+    const bool eight = kind & 4;
+    t.p_bf16 = (kind & 1) != 0;
+    t.g_bf16 = (kind & 2) != 0;
+    t.count = 0;
+    uint64_t groups = 0;
+    auto flush = [&]() -> metis_status {
+      if (!t.count) return METIS_OK;
+      const dim3 grid((unsigned)groups), block(256);
+      if (eight && sr) hipLaunchKernelGGL((adamw_kernel<true, true>), grid, block, 0, st, t);
+      else if (eight) hipLaunchKernelGGL((adamw_kernel<true, false>), grid, block, 0, st, t);
+      else if (sr && t.p_bf16) hipLaunchKernelGGL((adamw_kernel<false, true>), grid, block, 0, st, t);
+      else hipLaunchKernelGGL((adamw_kernel<false, false>), grid, block, 0, st, t);
+      LAUNCH_CHECK();
+      t.count = 0;
+      groups = 0;
+      return METIS_OK;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+      const metis_adamw_tensor& a = tensors[i];
+      if (a.n == 0 || ((a.param_dtype == METIS_BF16) | (a.grad_dtype == METIS_BF16) << 1 | (a.state_bits == 8) << 2) != kind)
+        continue;
+      const uint64_t need = (uint64_t)ceil_div<int64_t>(a.n, kAdamWork);
+      if (t.count == kAdamTensors || groups + need > INT32_MAX)
+        if ((s = flush()) != METIS_OK) return s;
+      const int k = t.count++;
+      t.first[k] = (uint32_t)groups;
+      t.tag[k] = a.tag;
+      t.p[k] = a.param, t.g[k] = a.grad, t.m[k] = a.m, t.v[k] = a.v;
+      t.ms[k] = a.m_scale, t.vs[k] = a.v_scale, t.n[k] = a.n;
+      groups += need;
+    }
+    if ((s = flush()) != METIS_OK) return s;
+  }
+  return METIS_OK;
+}
+
+size_t metis_grad_norm_workspace(const metis_adamw_tensor* tensors, int64_t count) {
+  size_t parts = 0;
+  for (int64_t i = 0; tensors && i < count; ++i)
+    if (tensors[i].n > 0) parts += (size_t)ceil_div<int64_t>(tensors[i].n, kNormWork);
+  return std::max<size_t>(256, parts * sizeof(double));
+}
+
+metis_status metis_grad_norm(const metis_adamw_tensor* tensors, int64_t count, double max_norm, float* out, void* ws,
+                             size_t ws_bytes, void* stream) {
+  if (count < 0 || (count && !tensors) || !out) return fail(METIS_E_INVALID, "grad_norm: null argument");
+  if (!(max_norm > 0)) return fail(METIS_E_INVALID, "grad_norm: max_norm %g", max_norm);
+  metis_status s;
+  for (int64_t i = 0; i < count; ++i)
+    if ((s = adamw_grad_check(tensors[i], i, "grad_norm")) != METIS_OK) return s;
+  const size_t need = metis_grad_norm_workspace(tensors, count);
+  if (!ws || ws_bytes < need) return fail(METIS_E_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
+  if ((uintptr_t)ws & 7) return fail(METIS_E_INVALID, "grad_norm: workspace not 8-byte aligned");
+  hipStream_t st = (hipStream_t)stream;
+  NormTable t{};
+  t.part = (double*)ws;
+  int64_t base = 0;
+  for (int bf16 = 0; bf16 < 2; ++bf16) {
+    t.g_bf16 = bf16;
+    t.count = 0;
+    uint64_t groups = 0;
+    auto flush = [&]() -> metis_status {
+      if (!t.count) return METIS_OK;
+      t.base = base;
+      hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)groups), dim3(256), 0, st, t);
+      LAUNCH_CHECK();
+      base += (int64_t)groups;
+      t.count = 0;
+      groups = 0;
+      return METIS_OK;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+      const metis_adamw_tensor& a = tensors[i];
+      if (a.n == 0 || (a.grad_dtype == METIS_BF16) != (bf16 == 1)) continue;
+      const uint64_t k = (uint64_t)ceil_div<int64_t>(a.n, kNormWork);
+      if (t.count == kNormTensors || groups + k > INT32_MAX)
+        if ((s = flush()) != METIS_OK) return s;
+      t.first[t.count] = (uint32_t)groups;
+      t.g[t.count] = a.grad;
+      t.n[t.count++] = a.n;
+      groups += k;
+    }
+    if ((s = flush()) != METIS_OK) return s;
+  }
+  hipLaunchKernelGGL(grad_norm_final_kernel, dim3(1), dim3(1024), 0, st, t.part, base, max_norm, out);
+  LAUNCH_CHECK();
   return METIS_OK;
 }
 

@@ -17,7 +17,7 @@ import torch
 
 from . import metis
 
-__all__ = ["MetisLinear", "set_step"]
+__all__ = ["MetisLinear", "Int8Linear", "Int8Frozen", "set_step"]
 
 
 class _MetisLinearFn(torch.autograd.Function):
@@ -90,8 +90,96 @@ class MetisLinear(torch.nn.Module):
         return _MetisLinearFn.apply(x, self.weight, self)
 
 
+class _Int8LinearFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, mod):
+        x2 = x.reshape(-1, x.shape[-1])
+        # the same orientations as above: X along both axes (Y and dW), W
+        # along both (Y and dX); an orientation whose product is not wanted is
+        # left out
+        need_x, need_w = ctx.needs_input_grad[:2]
+        qx = metis.int8_quantize(x2, metis.AXIS1 | (metis.AXIS0 if need_w else 0))
+        qw = metis.int8_quantize(w, metis.AXIS0 | (metis.AXIS1 if need_x else 0))
+        y = metis.int8_gemm(qx.ax1, qw.ax0, out_dtype=x.dtype)
+        ctx.qx, ctx.qw = qx.ax0, qw.ax1
+        ctx.lead, ctx.x_dtype = x.shape[:-1], x.dtype
+        ctx.rounding, ctx.seed, ctx.tag, ctx.step = mod.rounding, mod.seed, mod.tags["D"], mod.step
+        return y.reshape(*ctx.lead, w.shape[1])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        d2 = dy.reshape(-1, dy.shape[-1])
+        if d2.shape[1] > 1 and d2.stride(1) != 1 or d2.shape[0] > 1 and d2.stride(0) < d2.shape[1]:
+            d2 = d2.contiguous()
+        qd = metis.int8_quantize(d2, (metis.AXIS1 if need_x else 0) | (metis.AXIS0 if need_w else 0),
+                                 rounding=ctx.rounding, seed=ctx.seed, tag=ctx.tag, step=ctx.step)
+        dx = dw = None
+        if need_x:
+            dx = metis.int8_gemm(qd.ax1, ctx.qw, out_dtype=ctx.x_dtype).reshape(*ctx.lead, ctx.qw.outer)
+        if need_w:
+            dw = metis.int8_gemm(ctx.qx, qd.ax0)
+        return dx, dw, None
+
+
+class Int8Linear(torch.nn.Module):
+    """y = x W (no bias) with all three products in int8: X, W and the output
+    gradient D carry one scale per token or channel, along the axis that each
+    product reduces over.
+
+    X and W are rounded to nearest, D stochastically (``rounding`` "sr", the
+    default, with the draws of ``seed``, ``layer`` and the step that
+    :func:`set_step` sets) or to nearest ("rne").  x is bfloat16 or float32;
+    y and its gradient have x's type, the weight (``in_features x
+    out_features``) and its gradient are float32.  ``frozen()`` gives the
+    serving form, with the weight quantised once."""
+
+    def __init__(self, in_features, out_features, rounding="sr", seed=0, layer=0, device="cuda", weight=None):
+        super().__init__()
+        if rounding not in ("sr", "rne"):
+            raise ValueError("rounding must be 'sr' or 'rne', got %r" % (rounding,))
+        if weight is None:
+            weight = torch.empty(in_features, out_features, dtype=torch.float32, device=device)
+            torch.nn.init.normal_(weight, std=in_features ** -0.5)
+        if tuple(weight.shape) != (in_features, out_features):
+            raise ValueError("weight must be in_features x out_features")
+        self.weight = torch.nn.Parameter(weight.to(device=device, dtype=torch.float32).contiguous())
+        self.rounding = metis.SR if rounding == "sr" else metis.RNE
+        self.seed, self.step = seed, 0
+        self.tags = {"D": metis.make_tag(layer, metis.OPERAND_D)}
+
+    def forward(self, x):
+        if x.shape[-1] != self.weight.shape[0]:
+            raise ValueError("x has %d features, the layer %d" % (x.shape[-1], self.weight.shape[0]))
+        return _Int8LinearFn.apply(x, self.weight, self)
+
+    def frozen(self):
+        """The serving form of this layer with its present weight."""
+        with torch.no_grad():
+            return Int8Frozen(metis.int8_quantize(self.weight, metis.AXIS0).ax0)
+
+
+class Int8Frozen(torch.nn.Module):
+    """y = x W for serving, W held as int8 with one scale per output channel;
+    the tokens of x are quantised in the call.  No gradients."""
+
+    def __init__(self, w):
+        super().__init__()
+        self.k_len = w.k_len
+        self.register_buffer("codes", w.codes)
+        self.register_buffer("scales", w.scales)
+
+    @torch.no_grad()
+    def forward(self, x):
+        w = metis.I8.__new__(metis.I8)
+        w.codes, w.scales, w.outer, w.k_len = self.codes, self.scales, self.codes.shape[0], self.k_len
+        y = metis.int8_linear(x.reshape(-1, x.shape[-1]), w)
+        return y.reshape(*x.shape[:-1], w.outer)
+
+
 def set_step(model, step):
-    """Set the training step of every MetisLinear in ``model``."""
+    """Set the training step of every MetisLinear and Int8Linear in ``model``."""
     for m in model.modules():
-        if isinstance(m, MetisLinear):
+        if isinstance(m, (MetisLinear, Int8Linear)):
             m.step = step

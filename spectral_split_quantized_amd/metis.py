@@ -8,6 +8,7 @@ library is missing the first call raises; there is no fallback.
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -46,6 +47,18 @@ class _Q4(ctypes.Structure):
                 ("k_len", ctypes.c_int64)]
 
 
+class _I8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("n_outer", ctypes.c_int64),
+                ("k_len", ctypes.c_int64)]
+
+
+class _AdamWConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("step_count", ctypes.c_void_p), ("clip", ctypes.c_void_p), ("seed", ctypes.c_uint64),
+                ("rounding", ctypes.c_int32)]
+
+
 class _QOperand(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("k", ctypes.c_int32),
                 ("S", ctypes.c_void_p), ("U", _Q4), ("V", _Q4), ("R_ax0", _Q4), ("R_ax1", _Q4)]
@@ -79,6 +92,25 @@ def load():
     lib.metis_mxfp4_quantize.restype = i32
     lib.metis_mxfp4_gemm.argtypes = [P, P, P, P, i64, i64, i64, P, i64, P]
     lib.metis_mxfp4_gemm.restype = i32
+    lib.metis_int8_pitch.argtypes = [i64]
+    lib.metis_int8_pitch.restype = i64
+    lib.metis_int8_quantize_workspace.argtypes = [i64, i64, i32]
+    lib.metis_int8_quantize_workspace.restype = sz
+    lib.metis_int8_quantize.argtypes = [P, i32, i64, i64, i64, i32, i32, ctypes.c_uint64, u32, i64,
+                                        ctypes.POINTER(_I8), ctypes.POINTER(_I8), P, sz, P]
+    lib.metis_int8_quantize.restype = i32
+    lib.metis_int8_gemm.argtypes = [ctypes.POINTER(_I8), ctypes.POINTER(_I8), P, i32, i64, P]
+    lib.metis_int8_gemm.restype = i32
+    lib.metis_int8_linear_workspace.argtypes = [i64, i64]
+    lib.metis_int8_linear_workspace.restype = sz
+    lib.metis_int8_linear.argtypes = [P, i32, i64, i64, ctypes.POINTER(_I8), P, i32, i64, P, sz, P]
+    lib.metis_int8_linear.restype = i32
+    lib.metis_adamw_step.argtypes = [P, i64, ctypes.POINTER(_AdamWConfig), P]
+    lib.metis_adamw_step.restype = i32
+    lib.metis_grad_norm_workspace.argtypes = [P, i64]
+    lib.metis_grad_norm_workspace.restype = sz
+    lib.metis_grad_norm.argtypes = [P, i64, ctypes.c_double, P, P, sz, P]
+    lib.metis_grad_norm.restype = i32
     lib.metis_decompose.argtypes = [P, i32, i64, i64, i64, ctypes.POINTER(Config), i32, u32, i64,
                                     ctypes.POINTER(_Factors), P, sz, P]
     lib.metis_decompose.restype = i32
@@ -418,7 +450,6 @@ def status_sync():
 
 def omega_table_bits():
     """The library's 65536 bf16 bit patterns of the Gaussian quantile table (host only)."""
-    import numpy as np
     out = np.zeros(65536, dtype=np.uint16)
     load().metis_omega_table(out.ctypes.data_as(ctypes.c_void_p))
     return out
@@ -446,7 +477,6 @@ def timing_kinds(mask):
 
 def timing_read(max_records=1 << 16):
     """[(kind, ms, d0, d1, d2, d3), ...] for the recorded kernels (and reset)."""
-    import numpy as np
     ms = np.zeros(max_records, dtype=np.float32)
     shape = np.zeros(5 * max_records, dtype=np.int64)
     n = load().metis_timing_read(ms.ctypes.data_as(ctypes.c_void_p),
@@ -499,3 +529,288 @@ def mxfp4_gemm(a, b, C=None):
     _check(lib.metis_mxfp4_gemm(_ptr(a.codes), _ptr(a.scales), _ptr(b.codes), _ptr(b.scales), a.outer,
                                 b.outer, a.k_len, _ptr(C), C.stride(0), _stream()))
     return C
+
+
+# ------------------------------------------------------------------ int8 --
+
+def _on_device(*tensors):
+    """Context with the tensors' GPU current, whose current stream the call
+    uses; they must all be on one GPU."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise ValueError("the operands must be on one GPU, got %s" % sorted(str(d) for d in devices))
+    return torch.cuda.device(next(iter(devices)))
+
+
+def _leading(T):
+    """Leading dimension of a row-major view (a lone row's stride says nothing)."""
+    return T.stride(0) if T.shape[0] > 1 else max(T.stride(0), T.shape[1])
+
+
+def int8_pitch(k_len):
+    """Bytes between code rows of k_len codes (metis_int8_pitch)."""
+    return (k_len + 127) // 128 * 128
+
+
+class I8:
+    """One int8 operand (metis_i8): codes [outer, int8_pitch(k_len)] with zeros
+    behind k_len, one float32 scale per line."""
+
+    def __init__(self, outer, k_len, device="cuda"):
+        self.codes = torch.empty(outer, int8_pitch(k_len), dtype=torch.int8, device=device)
+        self.scales = torch.empty(outer, dtype=torch.float32, device=device)
+        self.outer, self.k_len = outer, k_len
+
+    @classmethod
+    def from_codes(cls, codes, scales):
+        """An operand of given codes (int8, outer x k_len, without -128) and
+        scales (outer), copied into the library's layout."""
+        if codes.dtype != torch.int8 or codes.dim() != 2 or scales.dtype != torch.float32 \
+                or tuple(scales.shape) != (codes.shape[0],):
+            raise ValueError("codes must be an int8 matrix and scales float32 with one value per row")
+        q = cls(codes.shape[0], codes.shape[1], codes.device)
+        q.codes.zero_()
+        q.codes[:, :q.k_len].copy_(codes)
+        q.scales.copy_(scales)
+        return q
+
+    def dequantize(self):
+        """The float32 matrix (outer x k_len) that the codes stand for."""
+        return self.codes[:, :self.k_len].float() * self.scales[:, None]
+
+    def _c(self):
+        if self.codes.dtype != torch.int8 or not self.codes.is_contiguous() \
+                or tuple(self.codes.shape) != (self.outer, int8_pitch(self.k_len)):
+            raise ValueError("codes must be a contiguous int8 matrix of %d x %d" % (self.outer, int8_pitch(self.k_len)))
+        if self.scales.dtype != torch.float32 or not self.scales.is_contiguous() \
+                or tuple(self.scales.shape) != (self.outer,):
+            raise ValueError("scales must be %d contiguous float32 values" % self.outer)
+        return _I8(self.codes.data_ptr(), self.scales.data_ptr(), self.outer, self.k_len)
+
+
+class I8Operand:
+    """A matrix (rows x cols) quantised along the requested K axes: ax1 with
+    one scale per row, ax0 the quantised transpose with one per column."""
+
+    def __init__(self, rows, cols, axes, device="cuda"):
+        if axes not in (AXIS0, AXIS1, AXIS0 | AXIS1):
+            raise ValueError("axes must be AXIS0, AXIS1 or both, got %r" % (axes,))
+        self.rows, self.cols, self.axes = rows, cols, axes
+        self.ax0 = I8(cols, rows, device) if axes & AXIS0 else None
+        self.ax1 = I8(rows, cols, device) if axes & AXIS1 else None
+
+
+def int8_quantize(M, axes=AXIS1, out=None, rounding=RNE, seed=0, tag=0, step=0, workspace=None):
+    """int8 codes and scales of M (metis_int8_quantize) along the requested
+    axes, rounded to nearest (RNE) or stochastically (SR, draws from seed, tag
+    and step)."""
+    _rows_check(M)
+    rows, cols = M.shape
+    dtype = _dtype_code(M)
+    if out is None:
+        out = I8Operand(rows, cols, axes, M.device)
+    elif (out.rows, out.cols, out.axes) != (rows, cols, axes):
+        raise ValueError("out holds a %d x %d operand with axes %d, not %d x %d with %d"
+                         % (out.rows, out.cols, out.axes, rows, cols, axes))
+    c0, c1 = (None if q is None else q._c() for q in (out.ax0, out.ax1))
+    parts = [t for q in (out.ax0, out.ax1) if q is not None for t in (q.codes, q.scales)]
+    with _on_device(M, *parts):
+        lib = load()
+        need = lib.metis_int8_quantize_workspace(rows, cols, axes)
+        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, M.device)
+        _check(lib.metis_int8_quantize(_ptr(M), dtype, rows, cols, _leading(M), axes, int(rounding), seed, tag, step,
+                                       None if c0 is None else ctypes.byref(c0),
+                                       None if c1 is None else ctypes.byref(c1), _ptr(ws), ws.numel(), _stream()))
+    return out
+
+
+def _int8_out(T, rows, cols, name):
+    if T.dtype not in (torch.float32, torch.bfloat16) or tuple(T.shape) != (rows, cols) \
+            or (cols > 1 and T.stride(1) != 1):
+        raise ValueError("%s must be a float32 or bfloat16 %d x %d row-major matrix" % (name, rows, cols))
+    return T
+
+
+def int8_gemm(a, b, C=None, out_dtype=torch.float32):
+    """C = A-hat B-hat^T of two int8 operands (metis_int8_gemm), float32 or
+    bfloat16."""
+    if a.k_len != b.k_len:
+        raise ValueError("inner dimensions differ: %d and %d" % (a.k_len, b.k_len))
+    if C is None:
+        C = torch.empty(a.outer, b.outer, dtype=out_dtype, device=a.codes.device)
+    _int8_out(C, a.outer, b.outer, "C")
+    ac, bc = a._c(), b._c()
+    with _on_device(a.codes, a.scales, b.codes, b.scales, C):
+        _check(load().metis_int8_gemm(ctypes.byref(ac), ctypes.byref(bc), _ptr(C), _dtype_code(C), _leading(C),
+                                      _stream()))
+    return C
+
+
+def int8_linear(x, w, Y=None, out_dtype=None, workspace=None):
+    """Y = X-hat W-hat (metis_int8_linear): the rows of x quantised to nearest
+    in the call, w the weight's int8 operand with one line per output channel;
+    Y in x's type unless out_dtype or Y says otherwise."""
+    _rows_check(x)
+    dtype = _dtype_code(x)
+    tokens = x.shape[0]
+    if x.shape[1] != w.k_len:
+        raise ValueError("inner dimensions differ: %d and %d" % (x.shape[1], w.k_len))
+    if Y is None:
+        Y = torch.empty(tokens, w.outer, dtype=out_dtype or x.dtype, device=x.device)
+    _int8_out(Y, tokens, w.outer, "Y")
+    wc = w._c()
+    with _on_device(x, w.codes, w.scales, Y):
+        lib = load()
+        need = lib.metis_int8_linear_workspace(tokens, w.k_len)
+        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, x.device)
+        _check(lib.metis_int8_linear(_ptr(x), dtype, tokens, _leading(x), ctypes.byref(wc), _ptr(Y), _dtype_code(Y),
+                                     _leading(Y), _ptr(ws), ws.numel(), _stream()))
+    return Y
+
+
+# ----------------------------------------------------------------- AdamW --
+
+STATE_BLOCK = 256  # consecutive elements that share a scale of an 8-bit state
+
+# metis_adamw_tensor
+_ADAMW_TENSOR = np.dtype([("param", "<u8"), ("grad", "<u8"), ("m", "<u8"), ("v", "<u8"), ("m_scale", "<u8"),
+                          ("v_scale", "<u8"), ("n", "<i8"), ("param_dtype", "<i4"), ("grad_dtype", "<i4"),
+                          ("state_bits", "<i4"), ("tag", "<u4")])
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def adamw_state(n, bits=8, device="cuda"):
+    """Initial states of n elements: (m, v, m_scale, v_scale).  32 bits: two
+    float32 arrays and no scales; 8 bits: two float8_e4m3fn arrays, v holding
+    the square root of the second moment, with one float32 scale per
+    STATE_BLOCK elements."""
+    if bits == 32:
+        return (torch.zeros(n, dtype=torch.float32, device=device), torch.zeros(n, dtype=torch.float32, device=device),
+                None, None)
+    if bits != 8:
+        raise ValueError("state bits must be 8 or 32, got %r" % (bits,))
+    codes = [torch.zeros(n, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+    blocks = (n + STATE_BLOCK - 1) // STATE_BLOCK
+    return (*codes, *(torch.zeros(blocks, dtype=torch.float32, device=device) for _ in range(2)))
+
+
+_numel, _ptr_of = torch.Tensor.numel, torch.Tensor.data_ptr
+_device_of, _contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+
+
+def _tensor_list(tensors, sizes, device, what, dtypes=None):
+    """Addresses of tensors that must be contiguous, on one GPU and of the given sizes."""
+    if list(map(_numel, tensors)) != sizes or not all(map(_contiguous, tensors)):
+        raise ValueError("%s must be contiguous and of the parameters' sizes" % what)
+    if sizes and set(map(_device_of, tensors)) != {device}:
+        raise ValueError("%s must be on the parameters' GPU" % what)
+    if dtypes is not None and not {t.dtype for t in tensors} <= dtypes:
+        raise TypeError("%s must be of %s, got %s" % (what, sorted(map(str, dtypes)),
+                                                      sorted(str(t.dtype) for t in tensors)))
+    return list(map(_ptr_of, tensors))
+
+
+def _grad_table(grads, table=None):
+    """The gradients' part of a tensor table."""
+    if table is None:
+        table = np.zeros(len(grads), _ADAMW_TENSOR)
+        table["n"] = list(map(_numel, grads))
+        device = grads[0].get_device() if grads else -1
+    else:
+        table, device = table
+        if len(grads) != len(table):
+            raise ValueError("%d gradients for %d parameters" % (len(grads), len(table)))
+    if grads and device < 0:
+        raise ValueError("gradients must be on a GPU")
+    table["grad"] = _tensor_list(grads, table["n"].tolist(), device, "gradients", _DTYPES.keys())
+    table["grad_dtype"] = [_DTYPES[g.dtype] for g in grads]
+    return table, device
+
+
+def _adamw_table(params, ms, vs, m_scales, v_scales, tags):
+    n = len(params)
+    if not all(len(x) == n for x in (ms, vs, m_scales, v_scales)) or (tags is not None and len(tags) != n):
+        raise ValueError("parameters, states and scales must be lists of one length")
+    table = np.zeros(n, _ADAMW_TENSOR)
+    if not n:
+        return table, -1
+    device = params[0].get_device()
+    if device < 0:
+        raise ValueError("parameters must be on a GPU")
+    sizes = list(map(_numel, params))
+    table["n"] = sizes
+    table["param"] = _tensor_list(params, sizes, device, "parameters", _DTYPES.keys())
+    table["param_dtype"] = [_DTYPES[p.dtype] for p in params]
+    eight = [s is not None for s in m_scales]
+    if eight != [s is not None for s in v_scales]:
+        raise ValueError("a parameter's two states must have the same width")
+    table["state_bits"] = np.where(eight, 8, 32)
+    for name, states, scales in (("m", ms, m_scales), ("v", vs, v_scales)):
+        table[name] = _tensor_list(states, sizes, device, "states")
+        for s, e in zip(states, eight):
+            if s.dtype != (torch.float8_e4m3fn if e else torch.float32):
+                raise TypeError("states must be float32, or float8_e4m3fn with scales; got %s" % s.dtype)
+        some = [s for s in scales if s is not None]
+        addr = _tensor_list(some, [(k + STATE_BLOCK - 1) // STATE_BLOCK for k, e in zip(sizes, eight) if e], device,
+                            "scales", {torch.float32})
+        table[name + "_scale"][np.asarray(eight, bool)] = addr
+    for name in ("param", "m", "v"):
+        addr = [a for a, k in zip(table[name].tolist(), sizes) if k]
+        if len(set(addr)) != len(addr):
+            raise ValueError("a parameter or a state appears twice")
+    table["tag"] = tags if tags is not None else [make_tag(i, OPERAND_W) for i in range(n)]
+    return table, device
+
+
+def _adamw_run(table, device, lr, betas, eps, weight_decay, step, clip, rounding, seed):
+    on_device = isinstance(step, torch.Tensor)
+    if on_device and (step.dtype != torch.int64 or step.numel() != 1 or step.get_device() != device):
+        raise ValueError("a step count tensor must be one int64 on the parameters' GPU")
+    if clip is not None and (clip.dtype != torch.float32 or clip.numel() != 1 or clip.get_device() != device):
+        raise ValueError("clip must be one float32 on the parameters' GPU")
+    cfg = _AdamWConfig(lr, betas[0], betas[1], eps, weight_decay, 0 if on_device else int(step),
+                       step.data_ptr() if on_device else None, None if clip is None else clip.data_ptr(),
+                       seed, int(rounding))
+    with torch.cuda.device(device):
+        _check(load().metis_adamw_step(ctypes.c_void_p(table.ctypes.data), len(table), ctypes.byref(cfg), _stream()))
+
+
+def adamw_step(params, grads, ms, vs, m_scales=None, v_scales=None, *, lr, betas=(0.9, 0.999), eps=1e-8,
+               weight_decay=0.0, step, clip=None, rounding=RNE, seed=0, tags=None):
+    """One AdamW step over lists of tensors, in place (metis_adamw_step).
+
+    params and grads: float32 or bfloat16; ms, vs and the scales as
+    adamw_state makes them (scales None, or None for a tensor: 32-bit states).
+    step: the step's number from 1, or a one-element int64 tensor holding it.
+    clip: one float32 factor for the gradients (grad_norm's second value).
+    tags select the draws of stochastic rounding (by default make_tag(i,
+    OPERAND_W) for the i-th parameter)."""
+    none = [None] * len(params)
+    table, device = _adamw_table(params, ms, vs, none if m_scales is None else m_scales,
+                                 none if v_scales is None else v_scales, tags)
+    _grad_table(grads, (table, device))
+    if len(params):
+        _adamw_run(table, device, lr, betas, eps, weight_decay, step, clip, rounding, seed)
+
+
+def _grad_norm_run(table, device, max_norm, out, workspace=None):
+    lib = load()
+    ptr = ctypes.c_void_p(table.ctypes.data)
+    with torch.cuda.device(device):
+        need = lib.metis_grad_norm_workspace(ptr, len(table))
+        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, out.device)
+        _check(lib.metis_grad_norm(ptr, len(table), max_norm, _ptr(out), _ptr(ws), ws.numel(), _stream()))
+    return out
+
+
+def grad_norm(grads, max_norm=float("inf"), out=None, workspace=None):
+    """The 2-norm over all gradients and the factor that clips it to max_norm,
+    as two float32 on the GPU (metis_grad_norm)."""
+    if not len(grads):
+        raise ValueError("grad_norm needs a gradient")
+    table, device = _grad_table(grads)
+    if out is None:
+        out = torch.empty(2, dtype=torch.float32, device=grads[0].device)
+    if out.dtype != torch.float32 or out.numel() != 2 or not out.is_contiguous() or out.get_device() != device:
+        raise ValueError("out must be two float32 on the gradients' GPU")
+    return _grad_norm_run(table, device, max_norm, out, workspace)
