@@ -143,7 +143,8 @@ def prepare(case, seed):
         else:
             (s["m"], s["ms"]), (s["v"], s["vs"]) = _encode(m, False), _encode(r, True)
         if own:
-            views = {k: _views(s[k], sizes, counts) for k in ("p", "g", "m", "v")}
+            views = {k: _views(s[k], sizes, counts) for k in ("p", "g")}
+            views.update({k: _views(v, sizes, counts) for k, v in _adamw_outputs(s, {}).items() if k in ("m", "v")})
             for p, gr in zip(views["p"], views["g"]):
                 p.requires_grad_(True)
                 p.grad = gr
