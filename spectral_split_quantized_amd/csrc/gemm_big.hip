@@ -2,6 +2,8 @@
 // an instruction-level-parallelism scheduling strategy; see build.py).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "gemm_launch.hpp"
 #include "gemm_reg.hpp"
 #include "mxfp4_gemm.hpp"
@@ -36,10 +38,13 @@ hipError_t launch_i8_gemm(const I8GemmParams& g, hipStream_t st) {
   }
   const int64_t big = ceil_div<int64_t>(g.M, 256) * ceil_div<int64_t>(g.N, 256);
   if (big >= 256) {
-    hipLaunchKernelGGL((i8_gemm_kernel<2, 2, 4, 4>), dim3((unsigned)big), dim3(256), 0, st, g);
+    if (g.bf16) hipLaunchKernelGGL((i8_gemm_kernel<2, 4, 4, true>), dim3(256), dim3(512), 0, st, g);
+    else hipLaunchKernelGGL((i8_gemm_kernel<2, 4, 4, false>), dim3(256), dim3(512), 0, st, g);
   } else {
     const int64_t tiles = ceil_div<int64_t>(g.M, 128) * ceil_div<int64_t>(g.N, 128);
-    hipLaunchKernelGGL((i8_gemm_kernel<2, 2, 2, 2>), dim3((unsigned)tiles), dim3(256), 0, st, g);
+    const dim3 grid((unsigned)std::min<int64_t>(512, ceil_div<int64_t>(tiles, 8) * 8));
+    if (g.bf16) hipLaunchKernelGGL((i8_gemm_kernel<2, 2, 2, true>), grid, dim3(256), 0, st, g);
+    else hipLaunchKernelGGL((i8_gemm_kernel<2, 2, 2, false>), grid, dim3(256), 0, st, g);
   }
   return hipGetLastError();
 }

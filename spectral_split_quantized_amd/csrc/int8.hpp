@@ -9,7 +9,7 @@
 // rounding of the extremes.  The floor 2^-126 keeps s and inv normal (an
 // all-zero line has codes 0).  u = h 2^-16 with h the 16-bit Philox draw of
 // the element's row-major position in M, the same for both orientations.
-// Code rows have a pitch of K rounded up to 128 bytes with zeros behind K, so
+// Code rows have a pitch of K rounded up to 256 bytes with zeros behind K, so
 // the product's K loop has no tail.
 //
 // Both orientations together take one sweep for the row and column maxima and
@@ -21,7 +21,7 @@
 
 namespace metis {
 
-constexpr int kI8Pitch = 128;
+constexpr int kI8Pitch = 256;
 
 __host__ __device__ inline int64_t i8_pitch(int64_t k) { return (k + kI8Pitch - 1) / kI8Pitch * kI8Pitch; }
 
@@ -241,12 +241,12 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
   // transposed codes: column c at words c * kPitch .. + 31 (four rows a word)
   constexpr int kPitch = 33;
   __shared__ uint32_t tr[kI8Tile * kPitch];
-  const int64_t tiles_n = ceil_div<int64_t>(p.cols, kI8Tile);
+  const int64_t pitch0 = i8_pitch(p.rows), pitch1 = i8_pitch(p.cols);
+  const int64_t tiles_n = pitch1 / kI8Tile;
   const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
   const int cc = threadIdx.x & 15, rg = threadIdx.x >> 4;
   const int64_t c = tn * kI8Tile + cc * 8;
   const int n = (int)min((int64_t)8, max((int64_t)0, p.cols - c));
-  const int64_t pitch0 = i8_pitch(p.rows), pitch1 = i8_pitch(p.cols);
   float inv0[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) inv0[j] = j < n ? i8_inverse(p.scales0[c + j]) : 0.0f;

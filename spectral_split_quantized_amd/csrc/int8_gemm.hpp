@@ -12,10 +12,10 @@
 
 namespace metis {
 
-constexpr int64_t kI8MaxK = 133056;  // multiple of 128; 127^2 * 133056 < 2^31
+constexpr int64_t kI8MaxK = 133056;  // 127^2 * 133056 < 2^31
 
 struct I8GemmParams {
-  int64_t M, N, pitch;     // pitch: K rounded up to 128, zeros behind K
+  int64_t M, N, pitch;     // pitch: K rounded up to 256, zeros behind K
   const int8_t* a;         // [M][pitch]
   const int8_t* b;         // [N][pitch]
   const float* sa;         // [M]
@@ -33,128 +33,259 @@ __device__ inline uint16_t i8_bf16(float v) {  // nearest, ties to even; v is fi
   return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
-// 256 threads as WM x WN waves, each TM x TN tiles of 32 x 32.  The codes
-// travel global -> LDS by DMA into a two-slot ring, one K-stage of 128 bytes
-// ahead, in the swizzled image of the FP4 kernels: a row's 128 bytes as
-// 16-byte chunks, chunk c of row R at ((R / 8) * 64 + (R % 8) * 8 +
-// (c ^ (R % 8))) * 16.  The instruction's lane l takes 16 K-consecutive bytes
-// of row l % 32; lane half h of sub-step kk reads chunk 2 kk + h of both
-// operands, so the order along K is the same on both sides.  Rows past M / N
-// repeat the last row (never stored).
-template <int WM, int WN, int TM, int TN>
-__global__ __launch_bounds__(WM * WN * 64) void i8_gemm_kernel(I8GemmParams p) {
+// Global -> LDS load of 16 bytes a lane to LDS address lds + 16 lane (base and
+// lds wave-uniform).  As assembly, so that the compiler does not wait for the
+// loads in flight before every LDS read: it cannot tell the ring's slots
+// apart.  The ring's own waits order them.
+__device__ __forceinline__ void dma16_async(const int8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// LDS operations of one wave complete in order; this keeps the compiler's order
+__device__ __forceinline__ void wave_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// WM x WN waves of TM x 2 tiles of 32 x 32, one workgroup for many tiles of
+// C.  The codes travel global -> LDS by DMA into a two-slot ring of K-stages
+// of 128 bytes; a row's 16-byte chunk c lies at R * 128 + (c ^ (R / 2 % 8)) *
+// 16, so that the 16 lanes that read LDS together hit all 64 banks once.
+// The instruction's lane l takes 16 K-consecutive bytes of row l % 32; lane
+// half h of sub-step kk reads chunk 2 kk + h of both operands.  B is the
+// instruction's first operand, so a lane ends up with one row of C and runs
+// of four consecutive columns.
+//
+// A stage is four sub-steps; each reads the next sub-step's fragments from
+// LDS under its matrix instructions.  In the last one every wave holds the
+// stage's fragments, so its slot takes the stage after next, and the first
+// fragments of the next stage (landed by then) are read.  The stages of one
+// tile follow those of the one before without a gap: the last two stages
+// already fetch the next tile's first, and the epilogue, which has LDS of its
+// own, stands between two matrix instructions.
+//
+// Rows past M / N repeat the last row (never stored).
+template <int WM, int WN, int TM, bool BF16>
+__global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p) {
+  constexpr int TN = 2;
   constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
   constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128;
   constexpr int PA = BM / 8 / NW, PB = BN / 8 / NW;
   static_assert(PA * 8 * NW == BM && PB * 8 * NW == BN, "DMA split");
   __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
-  using S0 = std::integral_constant<int, 0>;
-  using S1 = std::integral_constant<int, 1>;
-  auto slot = [&](auto s) -> uint8_t* {
-    if constexpr (decltype(s)::value == 0) return st0;
-    else return st1;
-  };
+  __shared__ __attribute__((aligned(16))) uint8_t ep[NW * 4096];
 
-  const int tid = threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN;
   const int64_t tiles_m = ceil_div<int64_t>(p.M, BM), tiles_n = ceil_div<int64_t>(p.N, BN);
-  const int64_t tile = remap_tile(blockIdx.x, tiles_m, tiles_n);
-  const int64_t m0 = (tile / tiles_n) * BM, n0 = (tile % tiles_n) * BN;
-  const int64_t nk = p.pitch >> 7;
+  const int64_t total = tiles_m * tiles_n, chunk = ceil_div<int64_t>(total, 8);
+  const int nk = (int)(p.pitch >> 7);  // even
 
-  i32x16_t acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = i32x16_t{};
+  // Workgroups go round the 8 XCDs; each XCD takes a contiguous run of tiles,
+  // in groups of 8 tile rows, so that its CUs share rows of both operands in
+  // its L2.  Sequence number q -> first row and column, or none.
+  auto locate = [&](int64_t q, int64_t& m0, int64_t& n0) {
+    const int64_t t = (q & 7) * chunk + (q >> 3);
+    if ((q >> 3) >= chunk || t >= total) return false;
+    const int64_t g = t / (8 * tiles_n), in = t - g * 8 * tiles_n, rows = min(tiles_m - g * 8, (int64_t)8);
+    m0 = (g * 8 + in % rows) * BM;
+    n0 = in / rows * BN;
+    return true;
+  };
+  int64_t q = blockIdx.x, m0, n0;
+  if (!locate(q, m0, n0)) return;
 
-  // a DMA moves 8 rows; its lanes' offsets from the tile's first row fit 32
-  // bits (256 rows of at most 133056 bytes)
-  const int dr = lane >> 3, dc = (lane & 7) ^ dr;
-  const int8_t* ga = p.a + m0 * p.pitch;
-  const int8_t* gb = p.b + n0 * p.pitch;
+  // the DMA source: a DMA moves 8 rows, its lanes' offsets from the tile's
+  // first row fit 32 bits (256 rows of at most 133120 bytes)
+  const int8_t *ga, *gb;
   uint32_t oa[PA], ob[PB];
+  auto source = [&](int64_t m, int64_t n) {
+    ga = p.a + m * p.pitch;
+    gb = p.b + n * p.pitch;
 #pragma unroll
-  for (int d = 0; d < PA; ++d)
-    oa[d] = (uint32_t)(min((int64_t)((wave + d * NW) * 8 + dr), p.M - 1 - m0) * p.pitch) + 16 * dc;
+    for (int d = 0; d < PA; ++d) {
+      const int r = (wave + d * NW) * 8 + (lane >> 3);
+      oa[d] = (uint32_t)(min((int64_t)r, p.M - 1 - m) * p.pitch) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+    }
 #pragma unroll
-  for (int d = 0; d < PB; ++d)
-    ob[d] = (uint32_t)(min((int64_t)((wave + d * NW) * 8 + dr), p.N - 1 - n0) * p.pitch) + 16 * dc;
-  auto issue = [&](int64_t kt, auto s) {
+    for (int d = 0; d < PB; ++d) {
+      const int r = (wave + d * NW) * 8 + (lane >> 3);
+      ob[d] = (uint32_t)(min((int64_t)r, p.N - 1 - n) * p.pitch) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+    }
+  };
+  auto issue = [&](uint8_t* st) {
+    const uint32_t at = lds_offset(st) + wave * 1024;
 #pragma unroll
-    for (int d = 0; d < PA; ++d) dma16(ga + kt * 128 + oa[d], slot(s) + (wave + d * NW) * 1024);
+    for (int d = 0; d < PA; ++d) dma16_async(ga, oa[d], at + d * NW * 1024);
 #pragma unroll
-    for (int d = 0; d < PB; ++d) dma16(gb + kt * 128 + ob[d], slot(s) + A_BYTES + (wave + d * NW) * 1024);
+    for (int d = 0; d < PB; ++d) dma16_async(gb, ob[d], at + A_BYTES + d * NW * 1024);
+    ga += 128;
+    gb += 128;
   };
 
-  const int hh = lane >> 5, li = lane & 31, lr8 = li & 7;
-  auto stage = [&](auto s) {
-    i32x4_t fa[2][TM], fb[2][TN];
-    auto read = [&](int kk, int buf) {
-      const int sw = ((2 * kk + hh) ^ lr8) * 16 + lr8 * 128;
+  const int hh = lane >> 5, li = lane & 31, sx = (li >> 1) & 7;
+  i32x16_t acc[TM][TN];
+  i32x4_t fa[2][TM], fb[2][TN];
+  auto read = [&](const uint8_t* st, int kk) {
+    const int at = li * 128 + ((2 * kk + hh) ^ sx) * 16;
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
-        fa[buf][i] = *(const i32x4_t*)(slot(s) + ((wm * TM + i) * 32 + li) / 8 * 1024 + sw);
+    for (int i = 0; i < TM; ++i) fa[kk & 1][i] = *(const i32x4_t*)(st + (wm * TM + i) * 4096 + at);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb[kk & 1][j] = *(const i32x4_t*)(st + A_BYTES + (wn * TN + j) * 4096 + at);
+  };
+  auto multiply = [&](int kk) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        fb[buf][j] = *(const i32x4_t*)(slot(s) + A_BYTES + ((wn * TN + j) * 32 + li) / 8 * 1024 + sw);
-    };
-    read(0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[kk & 1][j], fa[kk & 1][i], acc[i][j], 0, 0, 0);
+    // one LDS read after each of the first matrix instructions
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const int cur = kk & 1;
-      if (kk < 3) read(kk + 1, cur ^ 1);
+    for (int t = 0; t < TM * TN; ++t) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (t < TM + TN) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto stage = [&](uint8_t* cur, const uint8_t* next) {
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+      read(cur, kk + 1);
+      multiply(kk);
+    }
+    __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (0 << 8));  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    issue(cur);
+    read(next, 0);
+    multiply(3);
+  };
+
+  source(m0, n0);
+  issue(st0);
+  issue(st1);
+  ring_barrier();
+  read(st0, 0);
+  const bool vec = ((uintptr_t)p.C & 15) == 0 && (p.ldc * (BF16 ? 2 : 4)) % 16 == 0;
+  for (bool more = true; more;) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = i32x16_t{};
+    for (int kt = 2; kt < nk; kt += 2) {
+      stage(st0, st1);
+      stage(st1, st0);
+    }
+    // the last two stages fetch the next tile's first two (or, behind the
+    // last tile, its own once more)
+    int64_t m1 = m0, n1 = n0;
+    q += gridDim.x;
+    more = locate(q, m1, n1);
+    source(m1, n1);
+    const int64_t row0 = m0 + wm * TM * 32, col0 = n0 + wn * TN * 32;
+    float sa[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sa[i] = p.sa[min(row0 + i * 32 + li, p.M - 1)];
+    const float sb = p.sb[min(col0 + lane, p.N - 1)];
+    stage(st0, st1);
+    stage(st1, st0);
+
+    // epilogue: the lane holds row li of each tile and columns 8 g + 4 hh + v.
+    // Its lane indices are taken anew, so that the addresses made of them do
+    // not occupy registers all through the main loop.
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    const int li = el & 31, hh = el >> 5, sx = (li >> 1) & 7;
+    uint8_t* const my = ep + wave * 4096;
+    *(float*)(my + el * 4) = sb;
+    wave_fence();
+    float4 sc[TN][4];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) sc[j][g] = *(const float4*)(my + (j * 32 + 8 * g + 4 * hh) * 4);
+    wave_fence();
+    const int rr = el >> 3, rc = el & 7;  // read back: 8 rows of 8 chunks
+    auto value = [&](int i, int j, int g, float (&c)[4]) {
+      const float s[4] = {sc[j][g].x, sc[j][g].y, sc[j][g].z, sc[j][g].w};
+#pragma unroll
+      for (int v = 0; v < 4; ++v) c[v] = (float)acc[i][j][4 * g + v] * sa[i] * s[v];
+    };
+    if constexpr (BF16) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {  // 32 rows of 64 columns: chunks of 8 values
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float c[4];
+            value(i, j, g, c);
+            *(uint2*)(my + li * 128 + ((j * 4 + g) ^ sx) * 16 + hh * 8) =
+                make_uint2(i8_bf16(c[0]) | (uint32_t)i8_bf16(c[1]) << 16, i8_bf16(c[2]) | (uint32_t)i8_bf16(c[3]) << 16);
+          }
+        wave_fence();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = k * 8 + rr;
+          const u32x4_t w = *(const u32x4_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
+          const int64_t row = row0 + i * 32 + r, col = col0 + rc * 8;
+          uint16_t* const at = (uint16_t*)p.C + row * p.ldc + col;
+          if (row < p.M) {
+            if (vec && col + 8 <= p.N) {
+              __builtin_nontemporal_store(w, (u32x4_t*)at);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (col + e < p.N) at[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            }
+          }
+        }
+        wave_fence();
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[cur][i], fb[cur][j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < TN; ++j) {  // 32 rows of 32 columns: chunks of 4 values
 #pragma unroll
-      for (int t = 0; t < TM * TN; ++t) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
-        if (kk < 3 && t < TM + TN) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
-      }
-      __builtin_amdgcn_sched_barrier(0);
+          for (int g = 0; g < 4; ++g) {
+            float c[4];
+            value(i, j, g, c);
+            *(float4*)(my + li * 128 + ((2 * g + hh) ^ sx) * 16) = make_float4(c[0], c[1], c[2], c[3]);
+          }
+          wave_fence();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = k * 8 + rr;
+            const u32x4_t w = *(const u32x4_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
+            const int64_t row = row0 + i * 32 + r, col = col0 + j * 32 + rc * 4;
+            float* const at = (float*)p.C + row * p.ldc + col;
+            if (row < p.M) {
+              if (vec && col + 4 <= p.N) {
+                __builtin_nontemporal_store(w, (u32x4_t*)at);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (col + e < p.N) at[e] = __uint_as_float(w[e]);
+              }
+            }
+          }
+          wave_fence();
+        }
     }
-  };
-
-  issue(0, S0{});
-  ring_barrier();
-  for (int64_t kt = 0; kt < nk; kt += 2) {
-    // past the last stage the DMAs repeat data into a slot never read again
-    issue(kt + 1 < nk ? kt + 1 : kt, S1{});
-    stage(S0{});
-    ring_barrier();
-    if (kt + 1 < nk) {
-      issue(kt + 2 < nk ? kt + 2 : kt, S0{});
-      stage(S1{});
-      ring_barrier();
-    }
+    m0 = m1;
+    n0 = n1;
   }
-
-  // epilogue: lane holds column lane % 32 and rows 8 (v / 4) + 4 (lane / 32) + v % 4
-  float sb[TN];
-#pragma unroll
-  for (int j = 0; j < TN; ++j) sb[j] = p.sb[min(n0 + (wn * TN + j) * 32 + li, p.N - 1)];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int64_t row = m0 + (wm * TM + i) * 32 + 8 * (v >> 2) + 4 * hh + (v & 3);
-      if (row >= p.M) continue;
-      const float sa = p.sa[row];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int64_t col = n0 + (wn * TN + j) * 32 + li;
-        if (col >= p.N) continue;
-        const float c = (float)acc[i][j][v] * sa * sb[j];
-        if (p.bf16) ((uint16_t*)p.C)[row * p.ldc + col] = i8_bf16(c);
-        else __builtin_nontemporal_store(c, (float*)p.C + row * p.ldc + col);
-      }
-    }
-  }
+  // no load may land in LDS that a later workgroup owns
+  __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (15 << 8));
 }
 
 // Few rows of A (tokens): one workgroup of NW waves per 16 rows of B, the
@@ -175,7 +306,7 @@ __global__ __launch_bounds__(64 * NW) void i8_gemm_skinny_kernel(I8GemmParams p)
   i32x4_t acc[TM];
 #pragma unroll
   for (int i = 0; i < TM; ++i) acc[i] = i32x4_t{};
-  const int64_t steps = p.pitch >> 6;  // even
+  const int64_t steps = p.pitch >> 6;  // a multiple of 4
   for (int64_t s0 = (int64_t)wave * U; s0 < steps; s0 += NW * U) {
     i32x4_t fb[U], fa[U][TM];
 #pragma unroll

@@ -1192,8 +1192,10 @@ metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols
   LAUNCH_CHECK();
   hipLaunchKernelGGL(i8_scales_kernel, dim3(grid1(cols + (q.part1 ? rows : 0), 256)), dim3(256), 0, st, q);
   LAUNCH_CHECK();
-  if (q.sr) hipLaunchKernelGGL((i8_quant_tile_kernel<true>), tiles, dim3(256), 0, st, q);
-  else hipLaunchKernelGGL((i8_quant_tile_kernel<false>), tiles, dim3(256), 0, st, q);
+  // the zeros behind K are written too
+  const dim3 padded((unsigned)(i8_pitch(rows) / kI8Tile * (i8_pitch(cols) / kI8Tile)));
+  if (q.sr) hipLaunchKernelGGL((i8_quant_tile_kernel<true>), padded, dim3(256), 0, st, q);
+  else hipLaunchKernelGGL((i8_quant_tile_kernel<false>), padded, dim3(256), 0, st, q);
   LAUNCH_CHECK();
   return METIS_OK;
 }
@@ -1675,7 +1677,7 @@ metis_status metis_int8_quantize(const void* M, int32_t dtype, int64_t rows, int
   if ((axes & METIS_AXIS1) && (s = int8_check(ax1, "int8_quantize: ax1", rows, cols)) != METIS_OK) return s;
   if (rows == 0 || cols == 0) return METIS_OK;
   if (!M) return fail(METIS_E_INVALID, "int8_quantize: null input");
-  if (rows > INT32_MAX || ceil_div<int64_t>(rows, kI8Tile) * ceil_div<int64_t>(cols, kI8Tile) > INT32_MAX)
+  if (rows > INT32_MAX || cols > INT32_MAX || i8_pitch(rows) / kI8Tile * (i8_pitch(cols) / kI8Tile) > INT32_MAX)
     return fail(METIS_E_UNSUPPORTED, "int8_quantize: %lld x %lld", (long long)rows, (long long)cols);
   Carver cv(ws, ws_bytes);
   const I8Ws w = carve_int8(cv, rows, cols, axes);
