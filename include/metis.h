@@ -333,14 +333,17 @@ metis_status metis_mxfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, c
  * dimension ldc >= B->n_outer, binary32 or bf16 (c_dtype).  A and B have the
  * same k_len, at most 133056 (METIS_E_UNSUPPORTED above): sums are exact in
  * int32, and an output is RN(RN(RN(sum) s_A) s_B), rounded once more for
- * bf16.  n_outer == 0 on either side is a no-op, k_len == 0 invalid.
+ * bf16.  n_outer == 0 on either side is a no-op, k_len == 0 invalid.  ws
+ * holds metis_int8_gemm_workspace(A->n_outer, B->n_outer, k_len) bytes (0:
+ * may be NULL), 16-byte aligned: a product with few outputs is cut along K.
  *
  * metis_int8_linear: Y = X-hat W-hat for serving: X (tokens x k_len, bf16 or
  * fp32) is quantised to nearest with one scale per token and multiplied with
  * W, the K-down-the-columns orientation of a weight (n_outer output channels
  * of k_len codes).  Equal to metis_int8_quantize along METIS_AXIS1 followed
  * by metis_int8_gemm, bit for bit.  ws holds
- * metis_int8_linear_workspace(tokens, k_len) bytes, 256-byte aligned.
+ * metis_int8_linear_workspace(tokens, W->n_outer, k_len) bytes (0: may be
+ * NULL), 256-byte aligned.
  *
  * Argument errors return synchronously; nothing is allocated. */
 typedef struct {
@@ -356,9 +359,10 @@ metis_status metis_int8_quantize(const void *M, int32_t dtype, int64_t rows, int
                                  int32_t axes, int32_t rounding, uint64_t seed, uint32_t tag, int64_t step,
                                  const metis_i8 *ax0, const metis_i8 *ax1, void *ws, size_t ws_bytes,
                                  void *stream);
+size_t metis_int8_gemm_workspace(int64_t M, int64_t N, int64_t k_len);
 metis_status metis_int8_gemm(const metis_i8 *A, const metis_i8 *B, void *C, int32_t c_dtype, int64_t ldc,
-                             void *stream);
-size_t metis_int8_linear_workspace(int64_t tokens, int64_t k_len);
+                             void *ws, size_t ws_bytes, void *stream);
+size_t metis_int8_linear_workspace(int64_t tokens, int64_t n_outer, int64_t k_len);
 metis_status metis_int8_linear(const void *X, int32_t dtype, int64_t tokens, int64_t ldx, const metis_i8 *W,
                                void *Y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
 

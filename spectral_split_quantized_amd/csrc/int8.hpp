@@ -12,12 +12,14 @@
 // Code rows have a pitch of K rounded up to 256 bytes with zeros behind K, so
 // the product's K loop has no tail.
 //
-// Both orientations together take one sweep for the row and column maxima and
+// Columns, or both orientations together, take one sweep for the maxima and
 // one for the codes.  Rows alone take one sweep: a row stays in registers
 // between its maximum and its codes.
 #pragma once
 
 #include "quant.hpp"
+#include "int8_gemm.hpp"
+#include "quant_fast.hpp"
 
 namespace metis {
 
@@ -35,7 +37,8 @@ struct I8QuantParams {
   float* scales0;    // [cols]
   float* scales1;    // [rows]
   float* part0;      // [row tiles][cols] column maxima of a tile
-  float* part1;      // [column tiles][rows] row maxima of a tile
+  float* part1;      // [column tiles][rows] row maxima of a tile, or null
+  int amax_rows;     // rows of a wave in the first sweep
   int sr;
   uint64_t seed;
   uint32_t tag, step;
@@ -44,22 +47,24 @@ struct I8QuantParams {
 __device__ inline float i8_scale(float amax) { return fmaxf(__fdiv_rn(amax, 127.0f), 0x1p-126f); }
 __device__ inline float i8_inverse(float scale) { return __fdiv_rn(1.0f, scale); }
 
-// u: the draw times 2^-16, or a negative value to round to nearest
+// u: the draw times 2^-16 (SR).  v_fract_f32 is y - floor(y) rounded to
+// binary32 but kept below 1, where u < 1 decides the same.
 template <bool SR>
 __device__ inline int i8_code(float x, float inv, float u) {
   const float y = x * inv;
-  float c;
   if constexpr (SR) {
-    const float k = floorf(y);
-    c = k + (u < y - k ? 1.0f : 0.0f);
+    const int c = __float2int_rd(y) + (u < __builtin_amdgcn_fractf(y) ? 1 : 0);
+    return max(-127, min(127, c));
   } else {
-    c = rintf(y);
+    return (int)fminf(fmaxf(rintf(y), -127.0f), 127.0f);
   }
-  return (int)fminf(fmaxf(c, -127.0f), 127.0f);
 }
 
+// low bytes of four codes
 __device__ inline uint32_t pack4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)(d & 255) << 24;
+  const uint32_t lo = __builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x0C0C0400u);
+  const uint32_t hi = __builtin_amdgcn_perm((uint32_t)d, (uint32_t)c, 0x04000C0Cu);
+  return lo | hi;
 }
 
 // eight consecutive elements of a row from column c (n of them exist)
@@ -177,63 +182,71 @@ __global__ __launch_bounds__(64 * W) void i8_quant_rows_kernel(I8QuantParams p) 
 
 // ------------------------------------------------- columns, or both sides --
 //
-// Tiles of 128 rows x 128 columns, 256 threads: thread t holds the column
-// chunk 8 (t % 16) .. + 7 of rows 4 (t / 16) .. + 3 and of the 64 rows further
-// down.  The first sweep leaves each tile's row and column maxima, a small
-// kernel joins them into scales, and the second sweep writes the codes, the
-// transposed ones through LDS.
+// Two sweeps.  The first leaves, for tiles of 4 R rows x 512 columns, each
+// column's and row's largest magnitude in the tile; a wave covers 512 columns
+// of R rows, lane l the columns 8 l .. + 7.  The second sweep joins the
+// maxima of its own 128 rows and columns into scales (the first workgroups
+// along each side store them) and writes the codes, the transposed ones
+// through LDS: 256 threads on 128 x 128, thread t the column chunk
+// 8 (t % 16) .. + 7 of rows 4 (t / 16) .. + 3 and of the rows 64 further down.
 constexpr int kI8Tile = 128;
+constexpr int kI8AmaxCols = 512;
 
-__global__ __launch_bounds__(256) void i8_amax_kernel(I8QuantParams p) {
-  __shared__ float cmax[16][kI8Tile];
-  const int64_t tiles_n = ceil_div<int64_t>(p.cols, kI8Tile);
-  const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
-  const int cc = threadIdx.x & 15, rg = threadIdx.x >> 4;
-  const int64_t c = tn * kI8Tile + cc * 8;
-  const int n = (int)min((int64_t)8, max((int64_t)0, p.cols - c));
-  float x[8][8], cm[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t row = tm * kI8Tile + rg * 4 + (i & 3) + (i >> 2) * 64;
-    i8_load8(p, min(row, p.rows - 1), c, row < p.rows ? n : 0, x[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t row = tm * kI8Tile + rg * 4 + (i & 3) + (i >> 2) * 64;
-    float rm = i8_absmax8(x[i], 0.0f, bad);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], fabsf(x[i][j]));
-    if (p.part1) {
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) rm = fmaxf(rm, __shfl_xor(rm, o, 64));
-      if (cc == 0 && row < p.rows) p.part1[tn * p.rows + row] = rm;
-    }
-  }
-  if (bad) raise_status(kStatusNonFinite);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) cmax[rg][cc * 8 + j] = cm[j];
-  __syncthreads();
-  if (threadIdx.x < kI8Tile && tn * kI8Tile + threadIdx.x < p.cols) {
-    float m = 0.0f;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) m = fmaxf(m, cmax[r][threadIdx.x]);
-    p.part0[tm * p.cols + tn * kI8Tile + threadIdx.x] = m;
-  }
+// rows of a wave in the first sweep: long runs leave few maxima to join, short
+// ones fill the chip
+inline int i8_amax_rows(int64_t rows, int64_t cols) {
+  const int64_t wide = (cols + kI8AmaxCols - 1) / kI8AmaxCols;
+  int r = 64;
+  while (r > 8 && (rows + 4 * r - 1) / (4 * r) * wide < 1024) r >>= 1;
+  return r;
 }
 
-// scales of the columns (first n0 threads), then of the rows
-__global__ __launch_bounds__(256) void i8_scales_kernel(I8QuantParams p) {
-  const int64_t n1 = p.part1 ? p.rows : 0;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= p.cols + n1) return;
-  const bool col = id < p.cols;
-  const int64_t i = col ? id : id - p.cols, n = col ? p.cols : p.rows;
-  const int64_t tiles = ceil_div<int64_t>(col ? p.rows : p.cols, kI8Tile);
-  const float* part = col ? p.part0 : p.part1;
-  float m = 0.0f;
-  for (int64_t t = 0; t < tiles; ++t) m = fmaxf(m, part[t * n + i]);
-  (col ? p.scales0 : p.scales1)[i] = i8_scale(m);
+__global__ __launch_bounds__(256) void i8_amax_kernel(I8QuantParams p) {
+  __shared__ uint32_t cmax[4][kI8AmaxCols];
+  const int64_t tiles_n = ceil_div<int64_t>(p.cols, kI8AmaxCols);
+  const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t c = tn * kI8AmaxCols + lane * 8;
+  const int n = (int)min((int64_t)8, max((int64_t)0, p.cols - c));
+  const int64_t row0 = (tm * 4 + wave) * p.amax_rows;
+  uint32_t cm[8] = {0, 0, 0, 0, 0, 0, 0, 0}, mine = 0, top = 0;
+  for (int r0 = 0; r0 < p.amax_rows; r0 += 8) {
+    float x[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = row0 + r0 + i;
+      i8_load8(p, min(row, p.rows - 1), c, row < p.rows ? n : 0, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t rm = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // magnitudes order like their bits, NaN above all
+        const uint32_t a = __float_as_uint(x[i][j]) & 0x7FFFFFFFu;
+        cm[j] = max(cm[j], a);
+        rm = max(rm, a);
+      }
+      if (p.part1) {
+        rm = wave_max_u32(rm);
+        mine = lane == r0 + i ? rm : mine;
+      }
+    }
+  }
+  if (p.part1 && lane < p.amax_rows && row0 + lane < p.rows) p.part1[tn * p.rows + row0 + lane] = __uint_as_float(mine);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    cmax[wave][lane * 8 + j] = cm[j];
+    top = max(top, cm[j]);
+  }
+  if (top >= 0x7F800000u) raise_status(kStatusNonFinite);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kI8AmaxCols; k += 256) {
+    const int i = k + threadIdx.x;
+    const int64_t col = tn * kI8AmaxCols + i;
+    if (col < p.cols)
+      p.part0[tm * p.cols + col] = __uint_as_float(max(max(cmax[0][i], cmax[1][i]), max(cmax[2][i], cmax[3][i])));
+  }
 }
 
 template <bool SR>
@@ -241,42 +254,73 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
   // transposed codes: column c at words c * kPitch .. + 31 (four rows a word)
   constexpr int kPitch = 33;
   __shared__ uint32_t tr[kI8Tile * kPitch];
+  __shared__ float inv[2][kI8Tile];  // columns, rows
   const int64_t pitch0 = i8_pitch(p.rows), pitch1 = i8_pitch(p.cols);
   const int64_t tiles_n = pitch1 / kI8Tile;
   const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
   const int cc = threadIdx.x & 15, rg = threadIdx.x >> 4;
   const int64_t c = tn * kI8Tile + cc * 8;
   const int n = (int)min((int64_t)8, max((int64_t)0, p.cols - c));
+  float x[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = tm * kI8Tile + rg * 4 + (i & 3) + (i >> 2) * 64;
+    i8_load8(p, min(row, p.rows - 1), c, row < p.rows ? n : 0, x[i]);
+  }
+  {  // the 128 columns' and rows' scales: two threads a line join its maxima
+    const int i = threadIdx.x & (kI8Tile - 1), odd = threadIdx.x >> 7;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const float* part = side ? p.part1 : p.part0;
+      const int64_t line = (side ? tm : tn) * kI8Tile + i, lines = side ? p.rows : p.cols;
+      const int tiles = (int)(side ? ceil_div<int64_t>(p.cols, kI8AmaxCols) : ceil_div<int64_t>(p.rows, 4 * p.amax_rows));
+      float m = 0.0f;
+      if (part && line < lines) {
+        for (int t = odd; t < tiles; t += 32) {
+          float v[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = part[(int64_t)min(t + 2 * k, tiles - 1) * lines + line];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) m = fmaxf(m, v[k]);
+        }
+      }
+      if (odd) inv[side][i] = m;
+      __syncthreads();
+      if (!odd) {
+        const float s = i8_scale(fmaxf(m, inv[side][i]));
+        inv[side][i] = i8_inverse(s);
+        if (part && line < lines && (side ? tn == 0 : tm == 0)) (side ? p.scales1 : p.scales0)[line] = s;
+      }
+    }
+  }
+  __syncthreads();
   float inv0[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) inv0[j] = j < n ? i8_inverse(p.scales0[c + j]) : 0.0f;
+  for (int j = 0; j < 8; ++j) inv0[j] = inv[0][cc * 8 + j];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    float x[4][8];
-    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    int w[8][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t row = tm * kI8Tile + half * 64 + rg * 4 + i;
-      i8_load8(p, min(row, p.rows - 1), c, row < p.rows ? n : 0, x[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = tm * kI8Tile + half * 64 + rg * 4 + i;
+      const int r = half * 64 + rg * 4 + i;
+      const int64_t row = tm * kI8Tile + r;
+      const float (&v)[8] = x[half * 4 + i];
       float u[8];
       if constexpr (SR) i8_draws8(p, (uint64_t)row * p.cols + c, u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] |= (uint32_t)(i8_code<SR>(x[i][j], inv0[j], SR ? u[j] : 0.0f) & 255) << (8 * i);
+      for (int j = 0; j < 8; ++j) w[j][i] = i8_code<SR>(v[j], inv0[j], SR ? u[j] : 0.0f);
       if (p.codes1 && row < p.rows) {
-        const float inv = i8_inverse(p.scales1[row]);
+        const float inv1 = inv[1][r];
         int q[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = i8_code<SR>(x[i][j], inv, SR ? u[j] : 0.0f);
+        for (int j = 0; j < 8; ++j) q[j] = i8_code<SR>(v[j], inv1, SR ? u[j] : 0.0f);
         *(uint2*)(p.codes1 + row * pitch1 + c) =
             make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
       }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) tr[(cc * 8 + j) * kPitch + half * 16 + rg] = w[j];
+    for (int j = 0; j < 8; ++j)
+      tr[(cc * 8 + j) * kPitch + half * 16 + rg] = pack4(w[j][0], w[j][1], w[j][2], w[j][3]);
   }
   __syncthreads();
   // 8 threads write a column's 128 bytes
@@ -287,6 +331,114 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
     const uint32_t* t = tr + (ci + 32 * k) * kPitch + part * 4;
     if (col < p.cols)
       *(uint4*)(p.codes0 + col * pitch0 + tm * kI8Tile + part * 16) = make_uint4(t[0], t[1], t[2], t[3]);
+  }
+}
+
+// ------------------------------------------------ serving, a few tokens --
+//
+// y = x W-hat in one launch: one workgroup of NW waves per 16 output
+// channels.  Each wave first sends off its loads of W (U x 64 bytes of 16
+// rows), then the workgroup quantises the tokens into LDS, as the row
+// quantiser does, while they are under way.  The instruction is
+// 16 x 16 x 64: lane l takes 16 bytes of row l % 16 at 16 (l / 16).
+constexpr int kI8FewTokens = 4;
+constexpr int kI8FewBytes = 32768;  // codes of all tokens in LDS
+
+struct I8FewParams {
+  I8QuantParams x;  // src, dtype, rows (tokens), cols (K), ld, vec
+  int64_t N, pitch;
+  const int8_t* w;  // [N][pitch]
+  const float* sw;  // [N]
+  void* Y;
+  int64_t ldy;
+  int bf16;         // Y is bf16 (else fp32)
+};
+
+template <int NW, int U>
+__global__ __launch_bounds__(64 * NW) void i8_linear_few_kernel(I8FewParams p) {
+  constexpr int T = 64 * NW, CH = 2;  // chunks of eight a thread keeps of a row
+  __shared__ __attribute__((aligned(16))) int8_t codes[kI8FewBytes];
+  __shared__ float red[NW], sx[kI8FewTokens];
+  __shared__ i32x4_t sum[NW - 1][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, hq = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int M = (int)p.x.rows, steps = (int)(p.pitch >> 6);
+  const int8_t* const w = p.w + min(n0 + li, p.N - 1) * p.pitch + 16 * hq;
+  i32x4_t fw[U];
+  auto fetch = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) fw[u] = s0 + u < steps ? *(const i32x4_t*)(w + (int64_t)(s0 + u) * 64) : i32x4_t{};
+  };
+  fetch(wave * U);
+
+  const int64_t chunks = p.pitch >> 3;  // the zero padding included
+  for (int m = 0; m < M; ++m) {
+    float x[CH][8], top = 0.0f;
+    bool bad = false;
+    auto load = [&](int64_t ch, float (&v)[8]) {
+      i8_load8(p.x, m, ch * 8, (int)min((int64_t)8, max((int64_t)0, p.x.cols - ch * 8)), v);
+    };
+#pragma unroll
+    for (int j = 0; j < CH; ++j) load(threadIdx.x + T * j, x[j]);
+#pragma unroll
+    for (int j = 0; j < CH; ++j) top = i8_absmax8(x[j], top, bad);
+    for (int64_t ch = threadIdx.x + T * CH; ch < chunks; ch += T) {
+      float v[8];
+      load(ch, v);
+      top = i8_absmax8(v, top, bad);
+    }
+    top = wave_max(top);
+    if (lane == 0) red[wave] = top;
+    __syncthreads();
+    top = red[0];
+#pragma unroll
+    for (int k = 1; k < NW; ++k) top = fmaxf(top, red[k]);
+    __syncthreads();  // red is free for the next token
+    if (bad) raise_status(kStatusNonFinite);
+    const float s = i8_scale(top), inv = i8_inverse(s);
+    if (threadIdx.x == 0) sx[m] = s;
+    auto put = [&](int64_t ch, const float (&v)[8]) {
+      int q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = i8_code<false>(v[i], inv, 0.0f);
+      *(uint2*)(codes + m * p.pitch + ch * 8) = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+    };
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+      if (threadIdx.x + T * j < chunks) put(threadIdx.x + T * j, x[j]);
+    for (int64_t ch = threadIdx.x + T * CH; ch < chunks; ch += T) {
+      float v[8];
+      load(ch, v);
+      put(ch, v);
+    }
+  }
+  __syncthreads();
+
+  i32x4_t acc{};
+  const int8_t* const a = codes + min(li, M - 1) * p.pitch + 16 * hq;
+  for (int s0 = wave * U; s0 < steps; s0 += NW * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const i32x4_t fx = li < M && s0 + u < steps ? *(const i32x4_t*)(a + (s0 + u) * 64) : i32x4_t{};
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fx, fw[u], acc, 0, 0, 0);
+    }
+    if (s0 + NW * U < steps) fetch(s0 + NW * U);
+  }
+  if (wave > 0) sum[wave - 1][lane] = acc;
+  __syncthreads();
+  // lane holds column lane % 16 and rows 4 (lane / 16) + v: the first 16 lanes hold the tokens
+  const int64_t col = n0 + li;
+  if (wave > 0 || hq > 0 || col >= p.N) return;
+#pragma unroll
+  for (int k = 0; k < NW - 1; ++k) acc += sum[k][lane];
+  const float sb = p.sw[col];
+#pragma unroll
+  for (int v = 0; v < kI8FewTokens; ++v) {
+    if (v >= M) break;
+    const float c = (float)acc[v] * sx[v] * sb;
+    if (p.bf16) ((uint16_t*)p.Y)[v * p.ldy + col] = i8_bf16(c);
+    else ((float*)p.Y)[v * p.ldy + col] = c;
   }
 }
 

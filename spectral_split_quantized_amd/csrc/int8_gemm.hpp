@@ -6,7 +6,7 @@
 // RN(RN(RN(sum) s_a) s_b) in binary32, rounded once more for bf16.
 #pragma once
 
-#include <type_traits>
+#include <algorithm>
 
 #include "gemm_common.hpp"
 
@@ -23,7 +23,38 @@ struct I8GemmParams {
   void* C;
   int64_t ldc;
   int bf16;                // C is bf16 (else fp32)
+  int splits;              // K is cut into this many runs of
+  int run;                 // `run` stages of 128 (the last may be shorter), all even
+  int32_t* part;           // [splits][M][N] partial sums, or null with one run
 };
+
+// Which kernel a product takes, and its cut of K.
+struct I8Plan {
+  int tile;    // rows of A a workgroup: 256 (x 256), 128 or 64 (x 128), 16 (x 16, few tokens)
+  int splits, run;
+};
+
+inline I8Plan i8_plan(int64_t M, int64_t N, int64_t pitch) {
+  const int stages = (int)(pitch >> 7);
+  I8Plan pl{256, 1, stages};
+  if (M <= 16) {
+    pl.tile = 16;
+    return pl;
+  }
+  if (ceil_div<int64_t>(M, 256) * ceil_div<int64_t>(N, 256) >= 256) return pl;
+  pl.tile = M <= 64 || ceil_div<int64_t>(M, 128) * ceil_div<int64_t>(N, 128) < 256 ? 64 : 128;
+  const int64_t tiles = ceil_div<int64_t>(M, pl.tile) * ceil_div<int64_t>(N, 128);
+  const int least = M <= 64 ? 4 : 16;  // stages of a run
+  int64_t s = std::min<int64_t>(512 / tiles, stages / least);
+  if (s > 1) {
+    pl.run = (int)(ceil_div<int64_t>(stages, s) + 1) / 2 * 2;
+    pl.splits = (int)ceil_div<int64_t>(stages, pl.run);
+    if (pl.splits == 1) pl.run = stages;
+  }
+  return pl;
+}
+
+enum I8Out { kOutF32, kOutBF16, kOutPart };
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
@@ -72,7 +103,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 // own, stands between two matrix instructions.
 //
 // Rows past M / N repeat the last row (never stored).
-template <int WM, int WN, int TM, bool BF16>
+template <int WM, int WN, int TM, I8Out OUT>
 __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p) {
   constexpr int TN = 2;
   constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
@@ -85,40 +116,48 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN;
-  const int64_t tiles_m = ceil_div<int64_t>(p.M, BM), tiles_n = ceil_div<int64_t>(p.N, BN);
-  const int64_t total = tiles_m * tiles_n, chunk = ceil_div<int64_t>(total, 8);
-  const int nk = (int)(p.pitch >> 7);  // even
+  // (fewer than 2^31 units: 32-bit divisions)
+  const uint32_t tiles_m = (uint32_t)ceil_div<int64_t>(p.M, BM), tiles_n = (uint32_t)ceil_div<int64_t>(p.N, BN);
+  const uint32_t total = tiles_m * tiles_n * p.splits, chunk = (total + 7) / 8;
+  const int stages = (int)(p.pitch >> 7);  // even
 
   // Workgroups go round the 8 XCDs; each XCD takes a contiguous run of tiles,
   // in groups of 8 tile rows, so that its CUs share rows of both operands in
-  // its L2.  Sequence number q -> first row and column, or none.
-  auto locate = [&](int64_t q, int64_t& m0, int64_t& n0) {
-    const int64_t t = (q & 7) * chunk + (q >> 3);
-    if ((q >> 3) >= chunk || t >= total) return false;
-    const int64_t g = t / (8 * tiles_n), in = t - g * 8 * tiles_n, rows = min(tiles_m - g * 8, (int64_t)8);
-    m0 = (g * 8 + in % rows) * BM;
-    n0 = in / rows * BN;
+  // its L2; the runs of K of one tile follow each other.  Sequence number q ->
+  // first row and column and the run, or none.
+  auto locate = [&](uint32_t q, int64_t& m0, int64_t& n0, int& split) {
+    const uint32_t ts = (q & 7) * chunk + (q >> 3);
+    if ((q >> 3) >= chunk || ts >= total) return false;
+    const uint32_t t = p.splits == 1 ? ts : ts / p.splits;
+    split = (int)(ts - t * p.splits);
+    const uint32_t g = t / (8 * tiles_n), in = t - g * 8 * tiles_n, rows = min(tiles_m - g * 8, 8u);
+    const uint32_t col = in / rows;
+    m0 = (int64_t)(g * 8 + in - col * rows) * BM;
+    n0 = (int64_t)col * BN;
     return true;
   };
-  int64_t q = blockIdx.x, m0, n0;
-  if (!locate(q, m0, n0)) return;
+  uint32_t q = blockIdx.x;
+  int64_t m0, n0;
+  int split;
+  if (!locate(q, m0, n0, split)) return;
 
   // the DMA source: a DMA moves 8 rows, its lanes' offsets from the tile's
   // first row fit 32 bits (256 rows of at most 133120 bytes)
   const int8_t *ga, *gb;
   uint32_t oa[PA], ob[PB];
-  auto source = [&](int64_t m, int64_t n) {
-    ga = p.a + m * p.pitch;
-    gb = p.b + n * p.pitch;
+  auto source = [&](int64_t m, int64_t n, int s) {
+    ga = p.a + m * p.pitch + (int64_t)s * p.run * 128;
+    gb = p.b + n * p.pitch + (int64_t)s * p.run * 128;
+    const int last_a = (int)min(p.M - 1 - m, (int64_t)BM), last_b = (int)min(p.N - 1 - n, (int64_t)BN);
 #pragma unroll
     for (int d = 0; d < PA; ++d) {
       const int r = (wave + d * NW) * 8 + (lane >> 3);
-      oa[d] = (uint32_t)(min((int64_t)r, p.M - 1 - m) * p.pitch) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+      oa[d] = (uint32_t)min(r, last_a) * (uint32_t)p.pitch + 16 * ((lane & 7) ^ ((r >> 1) & 7));
     }
 #pragma unroll
     for (int d = 0; d < PB; ++d) {
       const int r = (wave + d * NW) * 8 + (lane >> 3);
-      ob[d] = (uint32_t)(min((int64_t)r, p.N - 1 - n) * p.pitch) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+      ob[d] = (uint32_t)min(r, last_b) * (uint32_t)p.pitch + 16 * ((lane & 7) ^ ((r >> 1) & 7));
     }
   };
   auto issue = [&](uint8_t* st) {
@@ -169,13 +208,14 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
     multiply(3);
   };
 
-  source(m0, n0);
+  source(m0, n0, split);
   issue(st0);
   issue(st1);
   ring_barrier();
   read(st0, 0);
-  const bool vec = ((uintptr_t)p.C & 15) == 0 && (p.ldc * (BF16 ? 2 : 4)) % 16 == 0;
+  const bool vec = ((uintptr_t)p.C & 15) == 0 && (p.ldc * (OUT == kOutBF16 ? 2 : 4)) % 16 == 0;
   for (bool more = true; more;) {
+    const int nk = min(p.run, stages - split * p.run);
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -187,9 +227,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
     // the last two stages fetch the next tile's first two (or, behind the
     // last tile, its own once more)
     int64_t m1 = m0, n1 = n0;
+    int split1 = split;
     q += gridDim.x;
-    more = locate(q, m1, n1);
-    source(m1, n1);
+    more = locate(q, m1, n1, split1);
+    source(m1, n1, split1);
     const int64_t row0 = m0 + wm * TM * 32, col0 = n0 + wn * TN * 32;
     float sa[TM];
 #pragma unroll
@@ -217,9 +258,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
     auto value = [&](int i, int j, int g, float (&c)[4]) {
       const float s[4] = {sc[j][g].x, sc[j][g].y, sc[j][g].z, sc[j][g].w};
 #pragma unroll
-      for (int v = 0; v < 4; ++v) c[v] = (float)acc[i][j][4 * g + v] * sa[i] * s[v];
+      for (int v = 0; v < 4; ++v)
+        c[v] = OUT == kOutPart ? __int_as_float(acc[i][j][4 * g + v]) : (float)acc[i][j][4 * g + v] * sa[i] * s[v];
     };
-    if constexpr (BF16) {
+    if constexpr (OUT == kOutBF16) {
 #pragma unroll
       for (int i = 0; i < TM; ++i) {  // 32 rows of 64 columns: chunks of 8 values
 #pragma unroll
@@ -267,7 +309,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
             const int r = k * 8 + rr;
             const u32x4_t w = *(const u32x4_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
             const int64_t row = row0 + i * 32 + r, col = col0 + j * 32 + rc * 4;
-            float* const at = (float*)p.C + row * p.ldc + col;
+            float* const at = (float*)p.C + (OUT == kOutPart ? split * p.M * p.ldc : 0) + row * p.ldc + col;
             if (row < p.M) {
               if (vec && col + 4 <= p.N) {
                 __builtin_nontemporal_store(w, (u32x4_t*)at);
@@ -283,48 +325,81 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
     }
     m0 = m1;
     n0 = n1;
+    split = split1;
   }
   // no load may land in LDS that a later workgroup owns
   __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (15 << 8));
 }
 
-// Few rows of A (tokens): one workgroup of NW waves per 16 rows of B, the
-// waves taking turns along K in steps of U x 64 bytes, so that a wave keeps
-// U loads of B in flight; the partial sums meet in LDS.  The instruction is
-// 16 x 16 x 64: lane l takes 16 bytes of row l % 16 at 16 (l / 16).  TM tiles
-// of 16 tokens.
-template <int NW, int TM, int U>
+// C from the partial sums of the runs of K: 4 values a thread.
+template <bool BF16>
+__global__ __launch_bounds__(64) void i8_join_kernel(I8GemmParams p) {
+  const int64_t per_row = (p.N + 3) >> 2, id = (int64_t)blockIdx.x * 64 + threadIdx.x;
+  if (id >= p.M * per_row) return;
+  const int64_t row = id / per_row, col = (id - row * per_row) * 4;
+  const int n = (int)min((int64_t)4, p.N - col);
+  const int32_t* at = p.part + row * p.N + col;
+  int sum[4] = {0, 0, 0, 0};
+  const bool vec = n == 4 && (p.N & 3) == 0;
+  for (int s = 0; s < p.splits; s += 8) {  // eight loads in flight
+    i32x4_t v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[k] = i32x4_t{};
+      if (s + k < p.splits) {
+        const int32_t* from = at + (int64_t)(s + k) * p.M * p.N;
+        if (vec) {
+          v[k] = *(const i32x4_t*)from;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e < n) v[k][e] = from[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += v[k][e];
+  }
+  const float sa = p.sa[row];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (e >= n) break;
+    const float c = (float)sum[e] * sa * p.sb[col + e];
+    if constexpr (BF16) ((uint16_t*)p.C)[row * p.ldc + col + e] = i8_bf16(c);
+    else ((float*)p.C)[row * p.ldc + col + e] = c;
+  }
+}
+
+// At most 16 rows of A (tokens): one workgroup of NW waves per 16 rows of B,
+// the waves taking turns along K in steps of U x 64 bytes, so that a wave
+// keeps U loads of B in flight; the partial sums meet in LDS.  The
+// instruction is 16 x 16 x 64: lane l takes 16 bytes of row l % 16 at
+// 16 (l / 16).
+template <int NW, int U>
 __global__ __launch_bounds__(64 * NW) void i8_gemm_skinny_kernel(I8GemmParams p) {
-  __shared__ i32x4_t red[NW > 1 ? NW - 1 : 1][TM][64];
+  __shared__ i32x4_t red[NW - 1][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, hq = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * TM);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int8_t* b = p.b + min(n0 + li, p.N - 1) * p.pitch + 16 * hq;
-  const int8_t* a[TM];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) a[i] = p.a + min(m0 + 16 * i + li, p.M - 1) * p.pitch + 16 * hq;
-  i32x4_t acc[TM];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) acc[i] = i32x4_t{};
+  const bool have = li < p.M;  // lanes without a token fetch nothing
+  const int8_t* a = p.a + min((int64_t)li, p.M - 1) * p.pitch + 16 * hq;
+  i32x4_t acc{};
   const int64_t steps = p.pitch >> 6;  // a multiple of 4
   for (int64_t s0 = (int64_t)wave * U; s0 < steps; s0 += NW * U) {
-    i32x4_t fb[U], fa[U][TM];
+    i32x4_t fb[U], fa[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t s = s0 + u;
       fb[u] = s < steps ? *(const i32x4_t*)(b + s * 64) : i32x4_t{};
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[u][i] = s < steps ? *(const i32x4_t*)(a[i] + s * 64) : i32x4_t{};
+      fa[u] = s < steps && have ? *(const i32x4_t*)(a + s * 64) : i32x4_t{};
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < TM; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[u][i], fb[u], acc[i], 0, 0, 0);
+    for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[u], fb[u], acc, 0, 0, 0);
   }
-  if (wave > 0) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) red[wave - 1][i][lane] = acc[i];
-  }
+  if (wave > 0) red[wave - 1][lane] = acc;
   __syncthreads();
   if (wave > 0) return;
   // lane holds column lane % 16 and rows 4 (lane / 16) + v
@@ -332,17 +407,14 @@ __global__ __launch_bounds__(64 * NW) void i8_gemm_skinny_kernel(I8GemmParams p)
   if (col >= p.N) return;
   const float sb = p.sb[col];
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
+  for (int w = 0; w < NW - 1; ++w) acc += red[w][lane];
 #pragma unroll
-    for (int w = 0; w < NW - 1; ++w) acc[i] += red[w][i][lane];
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t row = m0 + 16 * i + 4 * hq + v;
-      if (row >= p.M) continue;
-      const float c = (float)acc[i][v] * p.sa[row] * sb;
-      if (p.bf16) ((uint16_t*)p.C)[row * p.ldc + col] = i8_bf16(c);
-      else ((float*)p.C)[row * p.ldc + col] = c;
-    }
+  for (int v = 0; v < 4; ++v) {
+    const int64_t row = 4 * hq + v;
+    if (row >= p.M) continue;
+    const float c = (float)acc[v] * p.sa[row] * sb;
+    if (p.bf16) ((uint16_t*)p.C)[row * p.ldc + col] = i8_bf16(c);
+    else ((float*)p.C)[row * p.ldc + col] = c;
   }
 }
 

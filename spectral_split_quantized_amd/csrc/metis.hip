@@ -1153,9 +1153,18 @@ struct I8Ws {
 I8Ws carve_int8(Carver& cv, int64_t rows, int64_t cols, int axes) {
   I8Ws w{};
   if (!(axes & METIS_AXIS0)) return w;
-  w.part0 = cv.take<float>((size_t)(ceil_div<int64_t>(rows, kI8Tile) * cols));
-  if (axes & METIS_AXIS1) w.part1 = cv.take<float>((size_t)(ceil_div<int64_t>(cols, kI8Tile) * rows));
+  w.part0 = cv.take<float>((size_t)(ceil_div<int64_t>(rows, 4 * i8_amax_rows(rows, cols)) * cols));
+  if (axes & METIS_AXIS1) w.part1 = cv.take<float>((size_t)(ceil_div<int64_t>(cols, kI8AmaxCols) * rows));
   return w;
+}
+
+I8QuantParams int8_input(const void* M, int dtype, int64_t rows, int64_t cols, int64_t ld) {
+  I8QuantParams q{};
+  q.src = M;
+  q.dtype = dtype;
+  q.rows = rows, q.cols = cols, q.ld = ld;
+  q.vec = ((uintptr_t)M & 15) == 0 && (ld * (dtype == METIS_BF16 ? 2 : 4)) % 16 == 0;
+  return q;
 }
 
 template <bool SR>
@@ -1171,11 +1180,7 @@ void launch_int8_rows(const I8QuantParams& q, hipStream_t st) {
 metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols, int64_t ld, int axes, int rounding,
                             uint64_t seed, uint32_t tag, int64_t step, const metis_i8* ax0, const metis_i8* ax1,
                             const I8Ws& w, hipStream_t st) {
-  I8QuantParams q{};
-  q.src = M;
-  q.dtype = dtype;
-  q.rows = rows, q.cols = cols, q.ld = ld;
-  q.vec = ((uintptr_t)M & 15) == 0 && (ld * (dtype == METIS_BF16 ? 2 : 4)) % 16 == 0;
+  I8QuantParams q = int8_input(M, dtype, rows, cols, ld);
   if (axes & METIS_AXIS0) q.codes0 = ax0->codes, q.scales0 = ax0->scales;
   if (axes & METIS_AXIS1) q.codes1 = ax1->codes, q.scales1 = ax1->scales;
   q.part0 = w.part0, q.part1 = w.part1;
@@ -1187,10 +1192,9 @@ metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols
     LAUNCH_CHECK();
     return METIS_OK;
   }
-  const dim3 tiles((unsigned)(ceil_div<int64_t>(rows, kI8Tile) * ceil_div<int64_t>(cols, kI8Tile)));
+  q.amax_rows = i8_amax_rows(rows, cols);
+  const dim3 tiles((unsigned)(ceil_div<int64_t>(rows, 4 * q.amax_rows) * ceil_div<int64_t>(cols, kI8AmaxCols)));
   hipLaunchKernelGGL(i8_amax_kernel, tiles, dim3(256), 0, st, q);
-  LAUNCH_CHECK();
-  hipLaunchKernelGGL(i8_scales_kernel, dim3(grid1(cols + (q.part1 ? rows : 0), 256)), dim3(256), 0, st, q);
   LAUNCH_CHECK();
   // the zeros behind K are written too
   const dim3 padded((unsigned)(i8_pitch(rows) / kI8Tile * (i8_pitch(cols) / kI8Tile)));
@@ -1198,6 +1202,28 @@ metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols
   else hipLaunchKernelGGL((i8_quant_tile_kernel<false>), padded, dim3(256), 0, st, q);
   LAUNCH_CHECK();
   return METIS_OK;
+}
+
+struct I8LinearWs {
+  int8_t* codes;
+  float* scales;
+  int32_t* part;
+};
+
+// A few tokens go in one launch: every workgroup quantises them itself, so
+// their bytes, read by each, must stay small against the 16 rows of W that it
+// multiplies them with.
+bool int8_few(int64_t tokens, int64_t k_len) {
+  return tokens <= kI8FewTokens && tokens * i8_pitch(k_len) <= kI8FewBytes;
+}
+
+I8LinearWs carve_int8_linear(Carver& cv, int64_t tokens, int64_t n_outer, int64_t k_len) {
+  I8LinearWs w{};
+  if (int8_few(tokens, k_len)) return w;
+  w.codes = cv.take<int8_t>((size_t)(tokens * i8_pitch(k_len)));
+  w.scales = cv.take<float>((size_t)tokens);
+  w.part = (int32_t*)cv.take<char>(i8_gemm_workspace(tokens, n_outer, i8_pitch(k_len)));
+  return w;
 }
 
 metis_status int8_gemm_check(const metis_i8* A, const metis_i8* B, const void* C, int c_dtype, int64_t ldc) {
@@ -1214,12 +1240,10 @@ metis_status int8_gemm_check(const metis_i8* A, const metis_i8* B, const void* C
   return METIS_OK;
 }
 
-metis_status run_int8_gemm(const metis_i8* A, const metis_i8* B, void* C, int c_dtype, int64_t ldc, hipStream_t st) {
-  const metis_status s = int8_gemm_check(A, B, C, c_dtype, ldc);
-  if (s != METIS_OK) return s;
-  if (A->n_outer == 0 || B->n_outer == 0) return METIS_OK;
+metis_status run_int8_gemm(const metis_i8* A, const metis_i8* B, void* C, int c_dtype, int64_t ldc, int32_t* part,
+                           hipStream_t st) {
   const I8GemmParams g{A->n_outer, B->n_outer, i8_pitch(A->k_len), A->codes, B->codes, A->scales, B->scales,
-                       C, ldc, c_dtype == METIS_BF16};
+                       C, ldc, c_dtype == METIS_BF16, 1, 0, part};
   const hipError_t e = launch_i8_gemm(g, st);
   if (e != hipSuccess) return fail(METIS_E_HIP, "int8_gemm launch: %s", hipGetErrorString(e));
   return METIS_OK;
@@ -1687,20 +1711,28 @@ metis_status metis_int8_quantize(const void* M, int32_t dtype, int64_t rows, int
   return run_int8_quant(M, dtype, rows, cols, ld, axes, rounding, seed, tag, step, ax0, ax1, w, (hipStream_t)stream);
 }
 
-metis_status metis_int8_gemm(const metis_i8* A, const metis_i8* B, void* C, int32_t c_dtype, int64_t ldc,
-                             void* stream) {
+size_t metis_int8_gemm_workspace(int64_t M, int64_t N, int64_t k_len) {
+  return k_len < 1 ? 0 : i8_gemm_workspace(M, N, i8_pitch(k_len));
+}
+
+metis_status metis_int8_gemm(const metis_i8* A, const metis_i8* B, void* C, int32_t c_dtype, int64_t ldc, void* ws,
+                             size_t ws_bytes, void* stream) {
   if (!A || !B) return fail(METIS_E_INVALID, "int8_gemm: null operand");
   metis_status s;
   if ((s = int8_check(A, "int8_gemm: A", A->n_outer, A->k_len)) != METIS_OK) return s;
   if ((s = int8_check(B, "int8_gemm: B", B->n_outer, B->k_len)) != METIS_OK) return s;
-  return run_int8_gemm(A, B, C, c_dtype, ldc, (hipStream_t)stream);
+  if ((s = int8_gemm_check(A, B, C, c_dtype, ldc)) != METIS_OK) return s;
+  if (A->n_outer == 0 || B->n_outer == 0) return METIS_OK;
+  const size_t need = metis_int8_gemm_workspace(A->n_outer, B->n_outer, A->k_len);
+  if (need && (!ws || ws_bytes < need)) return fail(METIS_E_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
+  if (need && ((uintptr_t)ws & 15)) return fail(METIS_E_INVALID, "int8_gemm: workspace not 16-byte aligned");
+  return run_int8_gemm(A, B, C, c_dtype, ldc, (int32_t*)ws, (hipStream_t)stream);
 }
 
-size_t metis_int8_linear_workspace(int64_t tokens, int64_t k_len) {
-  if (tokens <= 0 || k_len <= 0) return 256;
+size_t metis_int8_linear_workspace(int64_t tokens, int64_t n_outer, int64_t k_len) {
+  if (tokens <= 0 || n_outer <= 0 || k_len <= 0) return 0;
   Carver cv(nullptr, 0);
-  cv.take<int8_t>((size_t)(tokens * i8_pitch(k_len)));
-  cv.take<float>((size_t)tokens);
+  carve_int8_linear(cv, tokens, n_outer, k_len);
   return cv.used();
 }
 
@@ -1713,21 +1745,34 @@ metis_status metis_int8_linear(const void* X, int32_t dtype, int64_t tokens, int
   if (tokens < 0 || tokens > INT32_MAX || ldx < W->k_len)
     return fail(METIS_E_INVALID, "int8_linear: %lld tokens, ldx %lld, k_len %lld", (long long)tokens, (long long)ldx,
                 (long long)W->k_len);
-  Carver cv(ws, ws_bytes);
-  const int64_t pitch = i8_pitch(W->k_len);
-  metis_i8 xq{cv.take<int8_t>((size_t)(tokens * pitch)), nullptr, tokens, W->k_len};
-  xq.scales = cv.take<float>((size_t)tokens);
+  metis_i8 xq{nullptr, nullptr, tokens, W->k_len};
+  if ((s = int8_gemm_check(&xq, W, Y, y_dtype, ldy)) != METIS_OK) return s;
   if (tokens == 0 || W->n_outer == 0) return METIS_OK;
   if (!X) return fail(METIS_E_INVALID, "int8_linear: null input");
-  if (!ws || cv.used() > ws_bytes) return fail(METIS_E_WORKSPACE, "workspace %zu < %zu", ws_bytes, cv.used());
+  Carver cv(ws, ws_bytes);
+  const I8LinearWs w = carve_int8_linear(cv, tokens, W->n_outer, W->k_len);
+  if (cv.used() && (!ws || cv.used() > ws_bytes))
+    return fail(METIS_E_WORKSPACE, "workspace %zu < %zu", ws_bytes, cv.used());
   if ((uintptr_t)ws & 15) return fail(METIS_E_INVALID, "int8_linear: workspace not 16-byte aligned");
-  if ((s = int8_gemm_check(&xq, W, Y, y_dtype, ldy)) != METIS_OK) return s;
   if ((s = ensure_device_tables()) != METIS_OK) return s;
+  xq.codes = w.codes;
+  xq.scales = w.scales;
   hipStream_t st = (hipStream_t)stream;
+  if (int8_few(tokens, W->k_len)) {
+    I8FewParams f{};
+    f.x = int8_input(X, dtype, tokens, W->k_len, ldx);
+    f.N = W->n_outer, f.pitch = i8_pitch(W->k_len), f.w = W->codes, f.sw = W->scales;
+    f.Y = Y, f.ldy = ldy, f.bf16 = y_dtype == METIS_BF16;
+    const dim3 grid((unsigned)ceil_div<int64_t>(W->n_outer, 16));
+    if (f.pitch <= 4096) hipLaunchKernelGGL((i8_linear_few_kernel<4, 16>), grid, dim3(256), 0, st, f);
+    else hipLaunchKernelGGL((i8_linear_few_kernel<8, 8>), grid, dim3(512), 0, st, f);
+    LAUNCH_CHECK();
+    return METIS_OK;
+  }
   if ((s = run_int8_quant(X, dtype, tokens, W->k_len, ldx, METIS_AXIS1, METIS_RNE, 0, 0, 0, nullptr, &xq, I8Ws{}, st)) !=
       METIS_OK)
     return s;
-  return run_int8_gemm(&xq, W, Y, y_dtype, ldy, st);
+  return run_int8_gemm(&xq, W, Y, y_dtype, ldy, w.part, st);
 }
 
 // -------------------------------------------------------------- AdamW --

@@ -99,9 +99,11 @@ def load():
     lib.metis_int8_quantize.argtypes = [P, i32, i64, i64, i64, i32, i32, ctypes.c_uint64, u32, i64,
                                         ctypes.POINTER(_I8), ctypes.POINTER(_I8), P, sz, P]
     lib.metis_int8_quantize.restype = i32
-    lib.metis_int8_gemm.argtypes = [ctypes.POINTER(_I8), ctypes.POINTER(_I8), P, i32, i64, P]
+    lib.metis_int8_gemm_workspace.argtypes = [i64, i64, i64]
+    lib.metis_int8_gemm_workspace.restype = sz
+    lib.metis_int8_gemm.argtypes = [ctypes.POINTER(_I8), ctypes.POINTER(_I8), P, i32, i64, P, sz, P]
     lib.metis_int8_gemm.restype = i32
-    lib.metis_int8_linear_workspace.argtypes = [i64, i64]
+    lib.metis_int8_linear_workspace.argtypes = [i64, i64, i64]
     lib.metis_int8_linear_workspace.restype = sz
     lib.metis_int8_linear.argtypes = [P, i32, i64, i64, ctypes.POINTER(_I8), P, i32, i64, P, sz, P]
     lib.metis_int8_linear.restype = i32
@@ -533,13 +535,32 @@ def mxfp4_gemm(a, b, C=None):
 
 # ------------------------------------------------------------------ int8 --
 
+class _NoSwitch:
+    """A device context that has nothing to do."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SWITCH = _NoSwitch()
+
+
+def _device_context(device):
+    """Context in which GPU ``device`` is current."""
+    return _NO_SWITCH if device == torch.cuda.current_device() else torch.cuda.device(device)
+
+
 def _on_device(*tensors):
     """Context with the tensors' GPU current, whose current stream the call
     uses; they must all be on one GPU."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
-        raise ValueError("the operands must be on one GPU, got %s" % sorted(str(d) for d in devices))
-    return torch.cuda.device(next(iter(devices)))
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != device or device < 0:
+            raise ValueError("the operands must be on one GPU, got %s" % sorted({str(t.device) for t in tensors}))
+    return _device_context(device)
 
 
 def _leading(T):
@@ -550,6 +571,10 @@ def _leading(T):
 def int8_pitch(k_len):
     """Bytes between code rows of k_len codes (metis_int8_pitch)."""
     return (k_len + 255) // 256 * 256
+
+
+def _raw_stream():
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 class I8:
@@ -579,13 +604,12 @@ class I8:
         return self.codes[:, :self.k_len].float() * self.scales[:, None]
 
     def _c(self):
-        if self.codes.dtype != torch.int8 or not self.codes.is_contiguous() \
-                or tuple(self.codes.shape) != (self.outer, int8_pitch(self.k_len)):
+        codes, scales = self.codes, self.scales
+        if codes.dtype != torch.int8 or codes.shape != (self.outer, int8_pitch(self.k_len)) or not codes.is_contiguous():
             raise ValueError("codes must be a contiguous int8 matrix of %d x %d" % (self.outer, int8_pitch(self.k_len)))
-        if self.scales.dtype != torch.float32 or not self.scales.is_contiguous() \
-                or tuple(self.scales.shape) != (self.outer,):
+        if scales.dtype != torch.float32 or scales.shape != (self.outer,) or not scales.is_contiguous():
             raise ValueError("scales must be %d contiguous float32 values" % self.outer)
-        return _I8(self.codes.data_ptr(), self.scales.data_ptr(), self.outer, self.k_len)
+        return _I8(codes.data_ptr(), scales.data_ptr(), self.outer, self.k_len)
 
 
 class I8Operand:
@@ -616,11 +640,12 @@ def int8_quantize(M, axes=AXIS1, out=None, rounding=RNE, seed=0, tag=0, step=0, 
     parts = [t for q in (out.ax0, out.ax1) if q is not None for t in (q.codes, q.scales)]
     with _on_device(M, *parts):
         lib = load()
-        need = lib.metis_int8_quantize_workspace(rows, cols, axes)
-        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, M.device)
-        _check(lib.metis_int8_quantize(_ptr(M), dtype, rows, cols, _leading(M), axes, int(rounding), seed, tag, step,
+        need = lib.metis_int8_quantize_workspace(rows, cols, axes) if axes & AXIS0 else 0  # rows alone need none
+        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, M.device) if need else None
+        _check(lib.metis_int8_quantize(M.data_ptr(), dtype, rows, cols, _leading(M), axes, rounding, seed, tag, step,
                                        None if c0 is None else ctypes.byref(c0),
-                                       None if c1 is None else ctypes.byref(c1), _ptr(ws), ws.numel(), _stream()))
+                                       None if c1 is None else ctypes.byref(c1), _ptr(ws), need if ws is None else ws.numel(),
+                                       _raw_stream()))
     return out
 
 
@@ -631,7 +656,7 @@ def _int8_out(T, rows, cols, name):
     return T
 
 
-def int8_gemm(a, b, C=None, out_dtype=torch.float32):
+def int8_gemm(a, b, C=None, out_dtype=torch.float32, workspace=None):
     """C = A-hat B-hat^T of two int8 operands (metis_int8_gemm), float32 or
     bfloat16."""
     if a.k_len != b.k_len:
@@ -641,8 +666,11 @@ def int8_gemm(a, b, C=None, out_dtype=torch.float32):
     _int8_out(C, a.outer, b.outer, "C")
     ac, bc = a._c(), b._c()
     with _on_device(a.codes, a.scales, b.codes, b.scales, C):
-        _check(load().metis_int8_gemm(ctypes.byref(ac), ctypes.byref(bc), _ptr(C), _dtype_code(C), _leading(C),
-                                      _stream()))
+        lib = load()
+        need = lib.metis_int8_gemm_workspace(a.outer, b.outer, a.k_len)
+        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, C.device) if need else None
+        _check(lib.metis_int8_gemm(ctypes.byref(ac), ctypes.byref(bc), C.data_ptr(), _dtype_code(C), _leading(C),
+                                   None if ws is None else ws.data_ptr(), need if ws is None else ws.numel(), _raw_stream()))
     return C
 
 
@@ -661,10 +689,11 @@ def int8_linear(x, w, Y=None, out_dtype=None, workspace=None):
     wc = w._c()
     with _on_device(x, w.codes, w.scales, Y):
         lib = load()
-        need = lib.metis_int8_linear_workspace(tokens, w.k_len)
-        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, x.device)
-        _check(lib.metis_int8_linear(_ptr(x), dtype, tokens, _leading(x), ctypes.byref(wc), _ptr(Y), _dtype_code(Y),
-                                     _leading(Y), _ptr(ws), ws.numel(), _stream()))
+        need = lib.metis_int8_linear_workspace(tokens, w.outer, w.k_len)
+        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, x.device) if need else None
+        _check(lib.metis_int8_linear(x.data_ptr(), dtype, tokens, _leading(x), ctypes.byref(wc), Y.data_ptr(),
+                                     _dtype_code(Y), _leading(Y), None if ws is None else ws.data_ptr(), need if ws is None else ws.numel(),
+                                     _raw_stream()))
     return Y
 
 
@@ -727,6 +756,42 @@ def _grad_table(grads, table=None):
     return table, device
 
 
+class _AdamWTable:
+    """The table of one list of tensors, kept between steps: what it holds is
+    compared with the tensors' present addresses and sizes, and it is made
+    again where they differ."""
+
+    def __init__(self):
+        self.key, self.table, self.device = None, None, -1
+        self.grad_dtype = None
+
+    def update(self, params, grads, states, tags):
+        """(table, device) for this step; states are (m, v, m_scale, v_scale)
+        lists, with None where a tensor has no scales; tags are the draws'
+        layer numbers."""
+        key = [list(map(_numel, params)), list(map(_ptr_of, params)), tags]
+        for column in states:
+            try:
+                key.append(list(map(_ptr_of, column)))
+            except TypeError:  # some without scales
+                key.append([None if s is None else s.data_ptr() for s in column])
+        if key != self.key:
+            self.table, self.device = _adamw_table(params, *states, [make_tag(i, OPERAND_W) for i in tags])
+            self.key, self.grad_dtype = key, None
+        if list(map(_numel, grads)) != key[0] or not all(map(_contiguous, grads)):
+            raise ValueError("gradients must be contiguous and of the parameters' sizes")
+        if set(map(_device_of, grads)) != {self.device}:
+            raise ValueError("gradients must be on the parameters' GPU")
+        dtypes = [g.dtype for g in grads]
+        if dtypes != self.grad_dtype:
+            if not set(dtypes) <= _DTYPES.keys():
+                raise TypeError("gradients must be float32 or bfloat16, got %s" % sorted(map(str, set(dtypes))))
+            self.table["grad_dtype"] = [_DTYPES[d] for d in dtypes]
+            self.grad_dtype = dtypes
+        self.table["grad"] = list(map(_ptr_of, grads))
+        return self.table, self.device
+
+
 def _adamw_table(params, ms, vs, m_scales, v_scales, tags):
     n = len(params)
     if not all(len(x) == n for x in (ms, vs, m_scales, v_scales)) or (tags is not None and len(tags) != n):
@@ -771,8 +836,8 @@ def _adamw_run(table, device, lr, betas, eps, weight_decay, step, clip, rounding
     cfg = _AdamWConfig(lr, betas[0], betas[1], eps, weight_decay, 0 if on_device else int(step),
                        step.data_ptr() if on_device else None, None if clip is None else clip.data_ptr(),
                        seed, int(rounding))
-    with torch.cuda.device(device):
-        _check(load().metis_adamw_step(ctypes.c_void_p(table.ctypes.data), len(table), ctypes.byref(cfg), _stream()))
+    with _device_context(device):
+        _check(load().metis_adamw_step(table.ctypes.data, len(table), ctypes.byref(cfg), _raw_stream()))
 
 
 def adamw_step(params, grads, ms, vs, m_scales=None, v_scales=None, *, lr, betas=(0.9, 0.999), eps=1e-8,
@@ -795,11 +860,11 @@ def adamw_step(params, grads, ms, vs, m_scales=None, v_scales=None, *, lr, betas
 
 def _grad_norm_run(table, device, max_norm, out, workspace=None):
     lib = load()
-    ptr = ctypes.c_void_p(table.ctypes.data)
-    with torch.cuda.device(device):
+    ptr = table.ctypes.data
+    with _device_context(device):
         need = lib.metis_grad_norm_workspace(ptr, len(table))
         ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, out.device)
-        _check(lib.metis_grad_norm(ptr, len(table), max_norm, _ptr(out), _ptr(ws), ws.numel(), _stream()))
+        _check(lib.metis_grad_norm(ptr, len(table), max_norm, out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream()))
     return out
 
 

@@ -50,6 +50,7 @@ class AdamW(torch.optim.Optimizer):
         self.seed, self.max_norm, self.capturable = seed, max_norm, capturable
         self.grad_norm = None
         self._clip = None
+        self._tables = {}
 
     def _init_state(self, p):
         eight = self.state_bits == 8 and p.numel() >= self.min_8bit_size
@@ -72,32 +73,36 @@ class AdamW(torch.optim.Optimizer):
             raise RuntimeError("an AdamW step needs capturable=True to be captured into a graph")
         calls, first = [], 0
         for group in self.param_groups:
-            everyone = group["params"]
-            params = [p for p in everyone if p.grad is not None]
-            if self.capturable and len(params) != len(everyone):
-                raise RuntimeError("with capturable=True every parameter needs a gradient")
-            tags = range(first, first + len(everyone))
-            if len(params) != len(everyone):
-                tags = [i for i, p in zip(tags, everyone) if p.grad is not None]
-            first += len(everyone)
-            states = [self.state.get(p) or self._init_state(p) for p in params]
+            params = group["params"]
+            grads = [p.grad for p in params]
+            tags = range(first, first + len(params))
+            first += len(params)
+            if any(g is None for g in grads):
+                if self.capturable:
+                    raise RuntimeError("with capturable=True every parameter needs a gradient")
+                have = [i for i, g in enumerate(grads) if g is not None]
+                params, grads, tags = ([x[i] for i in have] for x in (params, grads, tags))
+            if not params:
+                continue
+            states = [self.state[p] or self._init_state(p) for p in params]
             # parameters that missed steps have counts of their own
-            counts = [0] if self.capturable else sorted({s["step"] for s in states})
-            for count in counts:
-                some = range(len(params)) if len(counts) == 1 else [i for i, s in enumerate(states) if s["step"] == count]
-                if len(some):
-                    calls.append((group, [params[i] for i in some], [states[i] for i in some], [tags[i] for i in some]))
+            counts = {0} if self.capturable else {s["step"] for s in states}
+            if len(counts) == 1:
+                calls.append((group, params, grads, states, tags))
+                continue
+            for count in sorted(counts):
+                some = [i for i, s in enumerate(states) if s["step"] == count]
+                calls.append((group, *([x[i] for i in some] for x in (params, grads, states, tags))))
         if not calls:
             return loss
         tables = []
-        for _, params, states, tags in calls:
-            table, device = metis._adamw_table(
-                params, [s["exp_avg"] for s in states], [s["exp_avg_sq"] for s in states],
-                [s.get("exp_avg_scale") for s in states], [s.get("exp_avg_sq_scale") for s in states],
-                [metis.make_tag(i, metis.OPERAND_W) for i in tags])
-            grads = [p.grad if p.grad.is_contiguous() else p.grad.contiguous() for p in params]
-            metis._grad_table(grads, (table, device))
-            tables.append((table, device, grads))
+        for k, (_, params, grads, states, tags) in enumerate(calls):
+            if not all(map(torch.Tensor.is_contiguous, grads)):
+                grads = [g.contiguous() for g in grads]
+            columns = ([s["exp_avg"] for s in states], [s["exp_avg_sq"] for s in states],
+                       [s.get("exp_avg_scale") for s in states], [s.get("exp_avg_sq_scale") for s in states])
+            kept = self._tables.setdefault(k, metis._AdamWTable())
+            tables.append((*kept.update(params, grads, columns, tags), grads))
         if len({d for _, d, _ in tables}) != 1:
             raise ValueError("the parameters must be on one GPU")
         device, clip = tables[0][1], None
@@ -107,7 +112,7 @@ class AdamW(torch.optim.Optimizer):
             whole = tables[0][0] if len(tables) == 1 else metis.np.concatenate([t for t, _, _ in tables])
             metis._grad_norm_run(whole, device, self.max_norm, self._clip)
             self.grad_norm, clip = self._clip[0], self._clip[1]
-        for (group, _, states, _), (table, device, _) in zip(calls, tables):
+        for (group, _, _, states, _), (table, device, _) in zip(calls, tables):
             if self.capturable:
                 torch._foreach_add_([s["step"] for s in states], 1)
                 count = states[0]["step"]

@@ -46,8 +46,8 @@ def test_quantize_argument_errors():
 def test_gemm_and_linear_argument_errors():
     lib = metis.load()
 
-    def gemm(a, b, C=D, dt=1, ldc=64):
-        return lib.metis_int8_gemm(ctypes.byref(a), ctypes.byref(b), C, dt, ldc, None)
+    def gemm(a, b, C=D, dt=1, ldc=64, ws=D, n=1 << 30):
+        return lib.metis_int8_gemm(ctypes.byref(a), ctypes.byref(b), C, dt, ldc, ws, n, None)
 
     assert gemm(_i8(8, 128), _i8(64, 129)) == metis.E_INVALID
     assert gemm(_i8(8, 0), _i8(64, 0)) == metis.E_INVALID
@@ -57,6 +57,10 @@ def test_gemm_and_linear_argument_errors():
     assert gemm(_i8(8, 128), _i8(64, 128), dt=2) == metis.E_INVALID
     assert gemm(_i8(8, 128), _i8(64, 128), C=ctypes.c_void_p(4098)) == metis.E_INVALID
     assert gemm(_i8(0, 128, None, None), _i8(64, 128)) == metis.OK
+    assert lib.metis_int8_gemm_workspace(40, 64, 8192) > 0
+    assert gemm(_i8(40, 8192), _i8(64, 8192), n=16) == metis.E_WORKSPACE
+    assert gemm(_i8(40, 8192), _i8(64, 8192), ws=None) == metis.E_WORKSPACE
+    assert gemm(_i8(40, 8192), _i8(64, 8192), ws=ctypes.c_void_p(4104)) == metis.E_INVALID
 
     def linear(w, X=D, dt=0, tokens=2, ldx=128, ldy=64, ws=D, n=1 << 20):
         return lib.metis_int8_linear(X, dt, tokens, ldx, ctypes.byref(w), D, 0, ldy, ws, n, None)
@@ -66,10 +70,12 @@ def test_gemm_and_linear_argument_errors():
     assert linear(_i8(64, 128), tokens=-1) == metis.E_INVALID
     assert linear(_i8(64, 128), ldx=127) == metis.E_INVALID
     assert linear(_i8(64, 128), ldy=63) == metis.E_INVALID
-    assert linear(_i8(64, 128), n=64) == metis.E_WORKSPACE
+    assert linear(_i8(64, 128), tokens=5, n=64) == metis.E_WORKSPACE
+    assert linear(_i8(64, 128), tokens=5, ws=None) == metis.E_WORKSPACE
+    assert lib.metis_int8_linear_workspace(4, 64, 128) == 0  # a few tokens need none
     assert linear(_i8(64, 0), ldx=0) == metis.E_INVALID
     assert linear(_i8(64, 128), tokens=0) == metis.OK
-    assert lib.metis_int8_linear_workspace(7, 129) >= 7 * 256 + 28
+    assert lib.metis_int8_linear_workspace(7, 64, 129) >= 7 * 256 + 28
 
 
 def test_pitch_and_layout():
