@@ -334,36 +334,43 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
   }
 }
 
-// ------------------------------------------------ serving, a few tokens --
+// ------------------------------------------------- serving, single token --
 //
 // y = x W-hat in one launch: one workgroup of NW waves per 16 output
-// channels.  Each wave first sends off its loads of W (U x 64 bytes of 16
-// rows), then the workgroup quantises the tokens into LDS, as the row
-// quantiser does, while they are under way.  The instruction is
-// 16 x 16 x 64: lane l takes 16 bytes of row l % 16 at 16 (l / 16).
-constexpr int kI8FewTokens = 4;
-constexpr int kI8FewBytes = 32768;  // codes of all tokens in LDS
+// channels, the waves taking turns along K in steps of U x 64 bytes.  The
+// workgroup sends off its loads of the token, then each wave its first loads
+// of W (16 rows); loads return in order, so the token is quantised into LDS,
+// as the row quantiser does it, while W is under way.  The instruction is
+// 16 x 16 x 64: lane l takes 16 bytes of row l % 16 at 16 (l / 16); the
+// token is the only row of the first operand that is not zero.
+// CH: chunks of eight elements a thread holds of the token.
+constexpr int64_t kI8TokenPitch = 16384;  // longest token: 512 threads of 4 chunks
 
-struct I8FewParams {
-  I8QuantParams x;  // src, dtype, rows (tokens), cols (K), ld, vec
+struct I8TokenParams {
+  I8QuantParams x;  // src, dtype, rows = 1, cols = K, ld, vec
   int64_t N, pitch;
   const int8_t* w;  // [N][pitch]
   const float* sw;  // [N]
-  void* Y;
-  int64_t ldy;
-  int bf16;         // Y is bf16 (else fp32)
+  void* y;
+  int bf16;         // y is bf16 (else fp32)
 };
 
-template <int NW, int U>
-__global__ __launch_bounds__(64 * NW) void i8_linear_few_kernel(I8FewParams p) {
-  constexpr int T = 64 * NW, CH = 2;  // chunks of eight a thread keeps of a row
-  __shared__ __attribute__((aligned(16))) int8_t codes[kI8FewBytes];
-  __shared__ float red[NW], sx[kI8FewTokens];
-  __shared__ i32x4_t sum[NW - 1][64];
+template <int NW, int U, int CH>
+__global__ __launch_bounds__(64 * NW, 4) void i8_linear_token_kernel(I8TokenParams p) {
+  constexpr int T = 64 * NW;
+  __shared__ __attribute__((aligned(16))) int8_t codes[T * CH * 8];
+  __shared__ float red[NW];
+  __shared__ int sum[NW][16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, hq = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int M = (int)p.x.rows, steps = (int)(p.pitch >> 6);
+  const int steps = (int)(p.pitch >> 6);
+  float x[CH][8];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    const int64_t c = ((int64_t)threadIdx.x + T * j) * 8;
+    i8_load8(p.x, 0, c, (int)min((int64_t)8, max((int64_t)0, p.x.cols - c)), x[j]);
+  }
   const int8_t* const w = p.w + min(n0 + li, p.N - 1) * p.pitch + 16 * hq;
   i32x4_t fw[U];
   auto fetch = [&](int s0) {
@@ -372,74 +379,46 @@ __global__ __launch_bounds__(64 * NW) void i8_linear_few_kernel(I8FewParams p) {
   };
   fetch(wave * U);
 
-  const int64_t chunks = p.pitch >> 3;  // the zero padding included
-  for (int m = 0; m < M; ++m) {
-    float x[CH][8], top = 0.0f;
-    bool bad = false;
-    auto load = [&](int64_t ch, float (&v)[8]) {
-      i8_load8(p.x, m, ch * 8, (int)min((int64_t)8, max((int64_t)0, p.x.cols - ch * 8)), v);
-    };
+  float top = 0.0f;
+  bool bad = false;
 #pragma unroll
-    for (int j = 0; j < CH; ++j) load(threadIdx.x + T * j, x[j]);
+  for (int j = 0; j < CH; ++j) top = i8_absmax8(x[j], top, bad);
+  top = wave_max(top);
+  if (lane == 0) red[wave] = top;
+  __syncthreads();
 #pragma unroll
-    for (int j = 0; j < CH; ++j) top = i8_absmax8(x[j], top, bad);
-    for (int64_t ch = threadIdx.x + T * CH; ch < chunks; ch += T) {
-      float v[8];
-      load(ch, v);
-      top = i8_absmax8(v, top, bad);
-    }
-    top = wave_max(top);
-    if (lane == 0) red[wave] = top;
-    __syncthreads();
-    top = red[0];
+  for (int k = 0; k < NW; ++k) top = fmaxf(top, red[k]);
+  if (bad) raise_status(kStatusNonFinite);
+  const float s = i8_scale(top), inv = i8_inverse(s);
 #pragma unroll
-    for (int k = 1; k < NW; ++k) top = fmaxf(top, red[k]);
-    __syncthreads();  // red is free for the next token
-    if (bad) raise_status(kStatusNonFinite);
-    const float s = i8_scale(top), inv = i8_inverse(s);
-    if (threadIdx.x == 0) sx[m] = s;
-    auto put = [&](int64_t ch, const float (&v)[8]) {
-      int q[8];
+  for (int j = 0; j < CH; ++j) {
+    int q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = i8_code<false>(v[i], inv, 0.0f);
-      *(uint2*)(codes + m * p.pitch + ch * 8) = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
-    };
-#pragma unroll
-    for (int j = 0; j < CH; ++j)
-      if (threadIdx.x + T * j < chunks) put(threadIdx.x + T * j, x[j]);
-    for (int64_t ch = threadIdx.x + T * CH; ch < chunks; ch += T) {
-      float v[8];
-      load(ch, v);
-      put(ch, v);
-    }
+    for (int i = 0; i < 8; ++i) q[i] = i8_code<false>(x[j][i], inv, 0.0f);
+    *(uint2*)(codes + (threadIdx.x + T * j) * 8) = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
   }
   __syncthreads();
 
   i32x4_t acc{};
-  const int8_t* const a = codes + min(li, M - 1) * p.pitch + 16 * hq;
   for (int s0 = wave * U; s0 < steps; s0 += NW * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const i32x4_t fx = li < M && s0 + u < steps ? *(const i32x4_t*)(a + (s0 + u) * 64) : i32x4_t{};
+      const i32x4_t fx = li == 0 && s0 + u < steps ? *(const i32x4_t*)(codes + (s0 + u) * 64 + 16 * hq) : i32x4_t{};
       acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fx, fw[u], acc, 0, 0, 0);
     }
     if (s0 + NW * U < steps) fetch(s0 + NW * U);
   }
-  if (wave > 0) sum[wave - 1][lane] = acc;
+  // the token's sums: first value of the first 16 lanes, one a column
+  if (lane < 16) sum[wave][lane] = acc[0];
   __syncthreads();
-  // lane holds column lane % 16 and rows 4 (lane / 16) + v: the first 16 lanes hold the tokens
-  const int64_t col = n0 + li;
-  if (wave > 0 || hq > 0 || col >= p.N) return;
+  const int64_t col = n0 + threadIdx.x;
+  if (threadIdx.x >= 16 || col >= p.N) return;
+  int total = 0;
 #pragma unroll
-  for (int k = 0; k < NW - 1; ++k) acc += sum[k][lane];
-  const float sb = p.sw[col];
-#pragma unroll
-  for (int v = 0; v < kI8FewTokens; ++v) {
-    if (v >= M) break;
-    const float c = (float)acc[v] * sx[v] * sb;
-    if (p.bf16) ((uint16_t*)p.Y)[v * p.ldy + col] = i8_bf16(c);
-    else ((float*)p.Y)[v * p.ldy + col] = c;
-  }
+  for (int k = 0; k < NW; ++k) total += sum[k][threadIdx.x];
+  const float c = (float)total * s * p.sw[col];
+  if (p.bf16) ((uint16_t*)p.y)[col] = i8_bf16(c);
+  else ((float*)p.y)[col] = c;
 }
 
 }  // namespace metis

@@ -1210,16 +1210,12 @@ struct I8LinearWs {
   int32_t* part;
 };
 
-// A few tokens go in one launch: every workgroup quantises them itself, so
-// their bytes, read by each, must stay small against the 16 rows of W that it
-// multiplies them with.
-bool int8_few(int64_t tokens, int64_t k_len) {
-  return tokens <= kI8FewTokens && tokens * i8_pitch(k_len) <= kI8FewBytes;
-}
+// One token takes one launch, which needs no workspace.
+bool int8_token(int64_t tokens, int64_t k_len) { return tokens == 1 && i8_pitch(k_len) <= kI8TokenPitch; }
 
 I8LinearWs carve_int8_linear(Carver& cv, int64_t tokens, int64_t n_outer, int64_t k_len) {
   I8LinearWs w{};
-  if (int8_few(tokens, k_len)) return w;
+  if (int8_token(tokens, k_len)) return w;
   w.codes = cv.take<int8_t>((size_t)(tokens * i8_pitch(k_len)));
   w.scales = cv.take<float>((size_t)tokens);
   w.part = (int32_t*)cv.take<char>(i8_gemm_workspace(tokens, n_outer, i8_pitch(k_len)));
@@ -1758,14 +1754,12 @@ metis_status metis_int8_linear(const void* X, int32_t dtype, int64_t tokens, int
   xq.codes = w.codes;
   xq.scales = w.scales;
   hipStream_t st = (hipStream_t)stream;
-  if (int8_few(tokens, W->k_len)) {
-    I8FewParams f{};
-    f.x = int8_input(X, dtype, tokens, W->k_len, ldx);
-    f.N = W->n_outer, f.pitch = i8_pitch(W->k_len), f.w = W->codes, f.sw = W->scales;
-    f.Y = Y, f.ldy = ldy, f.bf16 = y_dtype == METIS_BF16;
+  if (int8_token(tokens, W->k_len)) {
+    const I8TokenParams f{int8_input(X, dtype, 1, W->k_len, ldx), W->n_outer, i8_pitch(W->k_len), W->codes, W->scales, Y,
+                          y_dtype == METIS_BF16};
     const dim3 grid((unsigned)ceil_div<int64_t>(W->n_outer, 16));
-    if (f.pitch <= 4096) hipLaunchKernelGGL((i8_linear_few_kernel<4, 16>), grid, dim3(256), 0, st, f);
-    else hipLaunchKernelGGL((i8_linear_few_kernel<8, 8>), grid, dim3(512), 0, st, f);
+    if (f.pitch <= 4096) hipLaunchKernelGGL((i8_linear_token_kernel<4, 16, 2>), grid, dim3(256), 0, st, f);
+    else hipLaunchKernelGGL((i8_linear_token_kernel<8, 8, 4>), grid, dim3(512), 0, st, f);
     LAUNCH_CHECK();
     return METIS_OK;
   }

@@ -211,7 +211,7 @@ def test_operands_beyond_32_bit_offsets():
 
 
 @pytest.mark.parametrize("dtype,out", [(torch.bfloat16, None), (torch.float32, None), (torch.bfloat16, torch.float32)])
-@pytest.mark.parametrize("tokens,k,n", [(1, 64, 16), (1, 4096, 1000), (2, 1337, 257), (3, 14000, 50), (4, 8192, 33), (4, 300, 1000),
+@pytest.mark.parametrize("tokens,k,n", [(1, 64, 16), (1, 4096, 1000), (1, 4097, 33), (1, 16384, 50), (1, 16385, 20), (2, 1337, 257),
                                         (5, 200, 64), (16, 513, 100),
                                         (37, 5000, 300), (64, 128, 128), (65, 300, 400), (500, 260, 390)])
 def test_linear_equals_its_parts(tokens, k, n, dtype, out):
@@ -224,10 +224,10 @@ def test_linear_equals_its_parts(tokens, k, n, dtype, out):
     assert y.dtype == want.dtype and torch.equal(y.cpu(), want)
 
 
-@pytest.mark.parametrize("tokens", [3, 5])
+@pytest.mark.parametrize("tokens", [1, 3])
 def test_linear_non_finite_token_is_reported(tokens):
     x = torch.randn(tokens, 256, device="cuda")
-    x[1, 100] = float("nan")
+    x[-1, 100] = float("nan")
     metis.int8_linear(x, _upload(_random(np.random.default_rng(1), 40, 256)))
     with pytest.raises(metis.MetisError):
         metis.status_sync()

@@ -72,7 +72,7 @@ def test_gemm_and_linear_argument_errors():
     assert linear(_i8(64, 128), ldy=63) == metis.E_INVALID
     assert linear(_i8(64, 128), tokens=5, n=64) == metis.E_WORKSPACE
     assert linear(_i8(64, 128), tokens=5, ws=None) == metis.E_WORKSPACE
-    assert lib.metis_int8_linear_workspace(4, 64, 128) == 0  # a few tokens need none
+    assert lib.metis_int8_linear_workspace(1, 64, 128) == 0  # a single token needs none
     assert linear(_i8(64, 0), ldx=0) == metis.E_INVALID
     assert linear(_i8(64, 128), tokens=0) == metis.OK
     assert lib.metis_int8_linear_workspace(7, 64, 129) >= 7 * 256 + 28
