@@ -316,7 +316,7 @@ metis_status metis_mxfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, c
  * i * cols + j in M, the same draw for both orientations.
  *
  * metis_i8: n_outer lines of k_len codes each, at a row pitch of
- * metis_int8_pitch(k_len) bytes (k_len rounded up to 256); the bytes behind
+ * metis_int8_pitch(k_len) bytes (k_len rounded up to 128); the bytes behind
  * k_len in a row are zero (the quantiser writes them so).  codes is 16-byte
  * aligned.  Device buffers owned by the caller.
  *

@@ -30,18 +30,18 @@ hipError_t launch_mx_gemm(const MxGemmParams& g, hipStream_t st) {
 
 namespace {
 
-template <int WM, int WN, int TM>
+template <int WM, int WN, int TM, int NS, int ER>
 void launch_i8_tiles(const I8GemmParams& g, hipStream_t st) {
   const int64_t units = ceil_div<int64_t>(g.M, WM * TM * 32) * ceil_div<int64_t>(g.N, WN * 64) * g.splits;
   // workgroups that fit the chip at once: one of 8 waves a CU, or two of 4
   const dim3 grid((unsigned)std::min<int64_t>(256 * (8 / (WM * WN)), ceil_div<int64_t>(units, 8) * 8));
   const dim3 block(WM * WN * 64);
-  if constexpr (WM * WN == 4) {  // the large tiles take the products that fill the chip without a cut
+  if constexpr (TM == 1) {  // the larger tiles take the products that fill the chip without a cut
     if (g.splits > 1) {
       I8GemmParams q = g;
       q.C = g.part;
       q.ldc = g.N;
-      hipLaunchKernelGGL((i8_gemm_kernel<WM, WN, TM, kOutPart>), grid, block, 0, st, q);
+      hipLaunchKernelGGL((i8_gemm_kernel<WM, WN, TM, NS, ER, kOutPart>), grid, block, 0, st, q);
       const dim3 join((unsigned)ceil_div<int64_t>(g.M * ((g.N + 3) >> 2), 64));
       if (g.bf16) hipLaunchKernelGGL((i8_join_kernel<true>), join, dim3(64), 0, st, g);
       else hipLaunchKernelGGL((i8_join_kernel<false>), join, dim3(64), 0, st, g);
@@ -49,9 +49,9 @@ void launch_i8_tiles(const I8GemmParams& g, hipStream_t st) {
     }
   }
   if (g.bf16) {
-    hipLaunchKernelGGL((i8_gemm_kernel<WM, WN, TM, kOutBF16>), grid, block, 0, st, g);
+    hipLaunchKernelGGL((i8_gemm_kernel<WM, WN, TM, NS, ER, kOutBF16>), grid, block, 0, st, g);
   } else {
-    hipLaunchKernelGGL((i8_gemm_kernel<WM, WN, TM, kOutF32>), grid, block, 0, st, g);
+    hipLaunchKernelGGL((i8_gemm_kernel<WM, WN, TM, NS, ER, kOutF32>), grid, block, 0, st, g);
   }
 }
 
@@ -68,9 +68,10 @@ hipError_t launch_i8_gemm(const I8GemmParams& in, hipStream_t st) {
   const I8Plan pl = i8_plan(g.M, g.N, g.pitch);
   g.splits = pl.splits;
   g.run = pl.run;
-  if (pl.tile == 256) launch_i8_tiles<2, 4, 4>(g, st);
-  else if (pl.tile == 128) launch_i8_tiles<2, 2, 2>(g, st);
-  else if (pl.tile == 64) launch_i8_tiles<2, 2, 1>(g, st);
+  if (pl.tile == 256) launch_i8_tiles<2, 4, 4, 2, 32>(g, st);
+  else if (pl.tile == 128) launch_i8_tiles<2, 2, 2, 2, 32>(g, st);
+  else if (pl.tile == 64 && pl.slots == 3) launch_i8_tiles<2, 2, 1, 3, 16>(g, st);
+  else if (pl.tile == 64) launch_i8_tiles<2, 2, 1, 2, 32>(g, st);
   else {
     // one batch of loads for the whole row where four waves can hold it
     // (16 x 4096 bytes: 13.1 us at 14336 rows of B against 14.6 with eight

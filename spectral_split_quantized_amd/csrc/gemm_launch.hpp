@@ -23,7 +23,7 @@ hipError_t launch_mx_gemm(const MxGemmParams& g, hipStream_t st);
 struct I8GemmParams;
 
 // C = diag(s_a) A B^T diag(s_b) of two int8 operands; code rows 16-byte
-// aligned with a pitch that is a multiple of 256.  part: i8_gemm_workspace
+// aligned with a pitch that is a multiple of 128.  part: i8_gemm_workspace
 // bytes (0: may be null), 16-byte aligned; splits and run are set here.
 size_t i8_gemm_workspace(int64_t M, int64_t N, int64_t pitch);
 hipError_t launch_i8_gemm(const I8GemmParams& g, hipStream_t st);

@@ -9,7 +9,7 @@
 // rounding of the extremes.  The floor 2^-126 keeps s and inv normal (an
 // all-zero line has codes 0).  u = h 2^-16 with h the 16-bit Philox draw of
 // the element's row-major position in M, the same for both orientations.
-// Code rows have a pitch of K rounded up to 256 bytes with zeros behind K, so
+// Code rows have a pitch of K rounded up to 128 bytes with zeros behind K, so
 // the product's K loop has no tail.
 //
 // Columns, or both orientations together, take one sweep for the maxima and
@@ -23,7 +23,7 @@
 
 namespace metis {
 
-constexpr int kI8Pitch = 256;
+constexpr int kI8Pitch = 128;
 
 __host__ __device__ inline int64_t i8_pitch(int64_t k) { return (k + kI8Pitch - 1) / kI8Pitch * kI8Pitch; }
 

@@ -7,6 +7,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_common.hpp"
 
@@ -15,7 +16,7 @@ namespace metis {
 constexpr int64_t kI8MaxK = 133056;  // 127^2 * 133056 < 2^31
 
 struct I8GemmParams {
-  int64_t M, N, pitch;     // pitch: K rounded up to 256, zeros behind K
+  int64_t M, N, pitch;     // pitch: K rounded up to 128, zeros behind K
   const int8_t* a;         // [M][pitch]
   const int8_t* b;         // [N][pitch]
   const float* sa;         // [M]
@@ -24,33 +25,40 @@ struct I8GemmParams {
   int64_t ldc;
   int bf16;                // C is bf16 (else fp32)
   int splits;              // K is cut into this many runs of
-  int run;                 // `run` stages of 128 (the last may be shorter), all even
+  int run;                 // `run` stages of 128 (the last may be shorter)
   int32_t* part;           // [splits][M][N] partial sums, or null with one run
 };
 
-// Which kernel a product takes, and its cut of K.
+// Which kernel a product takes, and its cut of K.  Times in us.
 struct I8Plan {
   int tile;    // rows of A a workgroup: 256 (x 256), 128 or 64 (x 128), 16 (x 16, few tokens)
+  int slots;   // of the ring
   int splits, run;
 };
 
+// (weights from HBM; M x N x K)
 inline I8Plan i8_plan(int64_t M, int64_t N, int64_t pitch) {
   const int stages = (int)(pitch >> 7);
-  I8Plan pl{256, 1, stages};
-  if (M <= 16) {
-    pl.tile = 16;
-    return pl;
-  }
-  if (ceil_div<int64_t>(M, 256) * ceil_div<int64_t>(N, 256) >= 256) return pl;
-  pl.tile = M <= 64 || ceil_div<int64_t>(M, 128) * ceil_div<int64_t>(N, 128) < 256 ? 64 : 128;
-  const int64_t tiles = ceil_div<int64_t>(M, pl.tile) * ceil_div<int64_t>(N, 128);
-  const int least = M <= 64 ? 4 : 16;  // stages of a run
-  int64_t s = std::min<int64_t>(512 / tiles, stages / least);
+  auto tiles = [&](int m, int n) { return ceil_div<int64_t>(M, m) * ceil_div<int64_t>(N, n); };
+  if (M <= 16) return {16, 0, 1, stages};
+  // the largest tile that still gives every CU one (4096^3: 60 against 69 with
+  // 128 x 128; 2048 x 4096 x 4096: 48 against 36)
+  if (tiles(256, 256) >= 256) return {256, 2, 1, stages};
+  if (tiles(128, 128) >= 256) return {128, 2, 1, stages};  // 300 x 14336 x 4096: 30, 35 with 64 rows
+  // K is cut where the tiles leave half the CUs idle, in runs long enough that
+  // they outweigh their sums, 8 bytes an output each (37 x 4096 x 14336, 32
+  // tiles: 52 whole, 18 in 8 runs, 22 in 16; 64 x 14336 x 4096, 112 tiles: 21
+  // whole, 20 in 2, 24 in 4; 200 x 4096 x 4096, 128 tiles: 15 whole, 16 in 2)
+  const int64_t t = tiles(64, 128);
+  const int64_t s = t < 128 ? std::min<int64_t>({256 / t, stages / (M <= 128 ? 8 : 16), 8}) : 1;
+  I8Plan pl{64, 2, 1, stages};
   if (s > 1) {
-    pl.run = (int)(ceil_div<int64_t>(stages, s) + 1) / 2 * 2;
+    pl.run = (int)ceil_div<int64_t>(stages, s);
     pl.splits = (int)ceil_div<int64_t>(stages, pl.run);
-    if (pl.splits == 1) pl.run = stages;
   }
+  // a third slot hides more latency (200 x 4096 x 4096: 15 against 19), two
+  // start sooner where K is short (1000 x 2304 x 768: 8 against 9)
+  if (stages >= 16) pl.slots = 3;
   return pl;
 }
 
@@ -86,40 +94,39 @@ __device__ __forceinline__ void wave_fence() {
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 // WM x WN waves of TM x 2 tiles of 32 x 32, one workgroup for many tiles of
-// C.  The codes travel global -> LDS by DMA into a two-slot ring of K-stages
-// of 128 bytes; a row's 16-byte chunk c lies at R * 128 + (c ^ (R / 2 % 8)) *
-// 16, so that the 16 lanes that read LDS together hit all 64 banks once.
-// The instruction's lane l takes 16 K-consecutive bytes of row l % 32; lane
-// half h of sub-step kk reads chunk 2 kk + h of both operands.  B is the
-// instruction's first operand, so a lane ends up with one row of C and runs
-// of four consecutive columns.
+// C.  The codes travel global -> LDS by DMA into a ring of NS slots, each one
+// K-stage of 128 bytes; a row's 16-byte chunk c lies at R * 128 +
+// (c ^ (R / 2 % 8)) * 16, so that the 16 lanes that read LDS together hit all
+// 64 banks once.  The instruction's lane l takes 16 K-consecutive bytes of row
+// l % 32; lane half h of sub-step kk reads chunk 2 kk + h of both operands.
+// B is the instruction's first operand, so a lane ends up with one row of C
+// and runs of four consecutive columns.
 //
 // A stage is four sub-steps; each reads the next sub-step's fragments from
 // LDS under its matrix instructions.  In the last one every wave holds the
-// stage's fragments, so its slot takes the stage after next, and the first
+// stage's fragments, so its slot takes the stage NS ahead, and the first
 // fragments of the next stage (landed by then) are read.  The stages of one
-// tile follow those of the one before without a gap: the last two stages
-// already fetch the next tile's first, and the epilogue, which has LDS of its
-// own, stands between two matrix instructions.
+// tile follow those of the one before without a gap: the loads run NS stages
+// ahead of the products, across tiles, and the epilogue, which has LDS of its
+// own (ER rows a wave), stands between two matrix instructions.
 //
 // Rows past M / N repeat the last row (never stored).
-template <int WM, int WN, int TM, I8Out OUT>
+template <int WM, int WN, int TM, int NS, int ER, I8Out OUT>
 __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p) {
   constexpr int TN = 2;
   constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
   constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128;
   constexpr int PA = BM / 8 / NW, PB = BN / 8 / NW;
-  static_assert(PA * 8 * NW == BM && PB * 8 * NW == BN, "DMA split");
-  __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t ep[NW * 4096];
+  static_assert(PA * 8 * NW == BM && PB * 8 * NW == BN && (NS - 1) * (PA + PB) < 64, "DMA split");
+  __shared__ __attribute__((aligned(16))) uint8_t ring[NS * STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t ep[NW * ER * 128];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN;
   // (fewer than 2^31 units: 32-bit divisions)
   const uint32_t tiles_m = (uint32_t)ceil_div<int64_t>(p.M, BM), tiles_n = (uint32_t)ceil_div<int64_t>(p.N, BN);
   const uint32_t total = tiles_m * tiles_n * p.splits, chunk = (total + 7) / 8;
-  const int stages = (int)(p.pitch >> 7);  // even
+  const int stages = (int)(p.pitch >> 7);
 
   // Workgroups go round the 8 XCDs; each XCD takes a contiguous run of tiles,
   // in groups of 8 tile rows, so that its CUs share rows of both operands in
@@ -136,18 +143,20 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
     n0 = (int64_t)col * BN;
     return true;
   };
-  uint32_t q = blockIdx.x;
+  uint32_t q = blockIdx.x, qi = q;  // of the products, of the loads
   int64_t m0, n0;
   int split;
   if (!locate(q, m0, n0, split)) return;
 
-  // the DMA source: a DMA moves 8 rows, its lanes' offsets from the tile's
-  // first row fit 32 bits (256 rows of at most 133120 bytes)
+  // the loads: a DMA moves 8 rows, its lanes' offsets from the tile's first
+  // row fit 32 bits (256 rows of at most 133120 bytes)
   const int8_t *ga, *gb;
   uint32_t oa[PA], ob[PB];
+  int left;  // stages of the tile still to load
   auto source = [&](int64_t m, int64_t n, int s) {
     ga = p.a + m * p.pitch + (int64_t)s * p.run * 128;
     gb = p.b + n * p.pitch + (int64_t)s * p.run * 128;
+    left = min(p.run, stages - s * p.run);
     const int last_a = (int)min(p.M - 1 - m, (int64_t)BM), last_b = (int)min(p.N - 1 - n, (int64_t)BN);
 #pragma unroll
     for (int d = 0; d < PA; ++d) {
@@ -160,25 +169,34 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
       ob[d] = (uint32_t)min(r, last_b) * (uint32_t)p.pitch + 16 * ((lane & 7) ^ ((r >> 1) & 7));
     }
   };
-  auto issue = [&](uint8_t* st) {
-    const uint32_t at = lds_offset(st) + wave * 1024;
+  const uint32_t base = lds_offset(ring) + wave * 1024;
+  auto issue = [&](int slot) {
+    if (left == 0) {  // on to the next tile, or, behind the last one, the same once more
+      int64_t m = m0, n = n0;
+      int s = split;
+      qi += gridDim.x;
+      locate(qi, m, n, s);
+      source(m, n, s);
+    }
+    const uint32_t at = base + slot * STAGE;
 #pragma unroll
     for (int d = 0; d < PA; ++d) dma16_async(ga, oa[d], at + d * NW * 1024);
 #pragma unroll
     for (int d = 0; d < PB; ++d) dma16_async(gb, ob[d], at + A_BYTES + d * NW * 1024);
     ga += 128;
     gb += 128;
+    --left;
   };
 
   const int hh = lane >> 5, li = lane & 31, sx = (li >> 1) & 7;
   i32x16_t acc[TM][TN];
   i32x4_t fa[2][TM], fb[2][TN];
-  auto read = [&](const uint8_t* st, int kk) {
-    const int at = li * 128 + ((2 * kk + hh) ^ sx) * 16;
+  auto read = [&](int slot, int kk) {
+    const uint8_t* const st = ring + slot * STAGE + li * 128 + ((2 * kk + hh) ^ sx) * 16;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) fa[kk & 1][i] = *(const i32x4_t*)(st + (wm * TM + i) * 4096 + at);
+    for (int i = 0; i < TM; ++i) fa[kk & 1][i] = *(const i32x4_t*)(st + (wm * TM + i) * 4096);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) fb[kk & 1][j] = *(const i32x4_t*)(st + A_BYTES + (wn * TN + j) * 4096 + at);
+    for (int j = 0; j < TN; ++j) fb[kk & 1][j] = *(const i32x4_t*)(st + A_BYTES + (wn * TN + j) * 4096);
   };
   auto multiply = [&](int kk) {
 #pragma unroll
@@ -194,50 +212,49 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto stage = [&](uint8_t* cur, const uint8_t* next) {
-#pragma unroll
-    for (int kk = 0; kk < 3; ++kk) {
-      read(cur, kk + 1);
-      multiply(kk);
-    }
-    __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (0 << 8));  // vmcnt(0) lgkmcnt(0)
+  // this wave's LDS reads are done and at most N of its loads in flight: with
+  // the barrier, a stage has landed and the one before it is read out
+  auto landed = [&](auto in_flight) {
+    constexpr int N = decltype(in_flight)::value;
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | (7 << 4) | (0 << 8));  // vmcnt(N) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    issue(cur);
-    read(next, 0);
-    multiply(3);
   };
+  using First = std::integral_constant<int, (NS - 1) * (PA + PB)>;
+  using Left = std::integral_constant<int, (NS - 2) * (PA + PB)>;
 
   source(m0, n0, split);
-  issue(st0);
-  issue(st1);
-  ring_barrier();
-  read(st0, 0);
+#pragma unroll
+  for (int s = 0; s < NS; ++s) issue(s);
+  landed(First{});
+  read(0, 0);
+  int slot = 0;
   const bool vec = ((uintptr_t)p.C & 15) == 0 && (p.ldc * (OUT == kOutBF16 ? 2 : 4)) % 16 == 0;
   for (bool more = true; more;) {
     const int nk = min(p.run, stages - split * p.run);
+    const int64_t row0 = m0 + wm * TM * 32, col0 = n0 + wn * TN * 32;
+    float sa[TM], sb = 0.0f;
+    if constexpr (OUT != kOutPart) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) sa[i] = p.sa[min(row0 + i * 32 + li, p.M - 1)];
+      sb = p.sb[min(col0 + lane, p.N - 1)];
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = i32x16_t{};
-    for (int kt = 2; kt < nk; kt += 2) {
-      stage(st0, st1);
-      stage(st1, st0);
-    }
-    // the last two stages fetch the next tile's first two (or, behind the
-    // last tile, its own once more)
-    int64_t m1 = m0, n1 = n0;
-    int split1 = split;
-    q += gridDim.x;
-    more = locate(q, m1, n1, split1);
-    source(m1, n1, split1);
-    const int64_t row0 = m0 + wm * TM * 32, col0 = n0 + wn * TN * 32;
-    float sa[TM];
+    for (int kt = 0; kt < nk; ++kt) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = p.sa[min(row0 + i * 32 + li, p.M - 1)];
-    const float sb = p.sb[min(col0 + lane, p.N - 1)];
-    stage(st0, st1);
-    stage(st1, st0);
+      for (int kk = 0; kk < 3; ++kk) {
+        read(slot, kk + 1);
+        multiply(kk);
+      }
+      landed(Left{});
+      issue(slot);
+      slot = slot + 1 == NS ? 0 : slot + 1;
+      read(slot, 0);
+      multiply(3);
+    }
 
     // epilogue: the lane holds row li of each tile and columns 8 g + 4 hh + v.
     // Its lane indices are taken anew, so that the addresses made of them do
@@ -245,15 +262,17 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
     int el = lane;
     asm volatile("" : "+v"(el));
     const int li = el & 31, hh = el >> 5, sx = (li >> 1) & 7;
-    uint8_t* const my = ep + wave * 4096;
-    *(float*)(my + el * 4) = sb;
-    wave_fence();
+    uint8_t* const my = ep + wave * (ER * 128);
     float4 sc[TN][4];
+    if constexpr (OUT != kOutPart) {
+      *(float*)(my + el * 4) = sb;
+      wave_fence();
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+      for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) sc[j][g] = *(const float4*)(my + (j * 32 + 8 * g + 4 * hh) * 4);
-    wave_fence();
+        for (int g = 0; g < 4; ++g) sc[j][g] = *(const float4*)(my + (j * 32 + 8 * g + 4 * hh) * 4);
+      wave_fence();
+    }
     const int rr = el >> 3, rc = el & 7;  // read back: 8 rows of 8 chunks
     auto value = [&](int i, int j, int g, float (&c)[4]) {
       const float s[4] = {sc[j][g].x, sc[j][g].y, sc[j][g].z, sc[j][g].w};
@@ -261,71 +280,56 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
       for (int v = 0; v < 4; ++v)
         c[v] = OUT == kOutPart ? __int_as_float(acc[i][j][4 * g + v]) : (float)acc[i][j][4 * g + v] * sa[i] * s[v];
     };
-    if constexpr (OUT == kOutBF16) {
+    // bf16: 32 rows of 64 columns a tile row, in chunks of 8 values; else 32
+    // rows of 32 columns, chunks of 4
+    constexpr int COLS = OUT == kOutBF16 ? 64 : 32, PER = COLS / 8;
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {  // 32 rows of 64 columns: chunks of 8 values
+    for (int i = 0; i < TM; ++i) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+      for (int j0 = 0; j0 < TN; j0 += COLS / 32) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float c[4];
-            value(i, j, g, c);
-            *(uint2*)(my + li * 128 + ((j * 4 + g) ^ sx) * 16 + hh * 8) =
-                make_uint2(i8_bf16(c[0]) | (uint32_t)i8_bf16(c[1]) << 16, i8_bf16(c[2]) | (uint32_t)i8_bf16(c[3]) << 16);
-          }
-        wave_fence();
+        for (int r0 = 0; r0 < 32; r0 += ER) {
+          if (ER == 32 || li / ER == r0 / ER) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = k * 8 + rr;
-          const u32x4_t w = *(const u32x4_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
-          const int64_t row = row0 + i * 32 + r, col = col0 + rc * 8;
-          uint16_t* const at = (uint16_t*)p.C + row * p.ldc + col;
-          if (row < p.M) {
-            if (vec && col + 8 <= p.N) {
-              __builtin_nontemporal_store(w, (u32x4_t*)at);
-            } else {
+            for (int j = j0; j < j0 + COLS / 32; ++j)
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (col + e < p.N) at[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-            }
-          }
-        }
-        wave_fence();
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {  // 32 rows of 32 columns: chunks of 4 values
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float c[4];
-            value(i, j, g, c);
-            *(float4*)(my + li * 128 + ((2 * g + hh) ^ sx) * 16) = make_float4(c[0], c[1], c[2], c[3]);
+              for (int g = 0; g < 4; ++g) {
+                float c[4];
+                value(i, j, g, c);
+                uint8_t* const row = my + (li % ER) * 128;
+                if constexpr (OUT == kOutBF16)
+                  *(uint2*)(row + ((j * 4 + g) ^ sx) * 16 + hh * 8) =
+                      make_uint2(i8_bf16(c[0]) | (uint32_t)i8_bf16(c[1]) << 16, i8_bf16(c[2]) | (uint32_t)i8_bf16(c[3]) << 16);
+                else
+                  *(float4*)(row + ((2 * g + hh) ^ sx) * 16) = make_float4(c[0], c[1], c[2], c[3]);
+              }
           }
           wave_fence();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < ER / 8; ++k) {
             const int r = k * 8 + rr;
             const u32x4_t w = *(const u32x4_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
-            const int64_t row = row0 + i * 32 + r, col = col0 + j * 32 + rc * 4;
-            float* const at = (float*)p.C + (OUT == kOutPart ? split * p.M * p.ldc : 0) + row * p.ldc + col;
-            if (row < p.M) {
-              if (vec && col + 4 <= p.N) {
-                __builtin_nontemporal_store(w, (u32x4_t*)at);
-              } else {
+            const int64_t row = row0 + i * 32 + r0 + r, col = col0 + j0 * 32 + rc * PER;
+            if (row >= p.M) continue;
+            const int64_t at = (OUT == kOutPart ? split * p.M * p.ldc : 0) + row * p.ldc + col;
+            if (vec && col + PER <= p.N) {
+              u32x4_t* const to = OUT == kOutBF16 ? (u32x4_t*)((uint16_t*)p.C + at) : (u32x4_t*)((float*)p.C + at);
+              __builtin_nontemporal_store(w, to);
+            } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (col + e < p.N) at[e] = __uint_as_float(w[e]);
+              for (int e = 0; e < PER; ++e) {
+                if (col + e >= p.N) break;
+                if constexpr (OUT == kOutBF16) ((uint16_t*)p.C)[at + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                else ((float*)p.C)[at + e] = __uint_as_float(w[e]);
               }
             }
           }
           wave_fence();
         }
+      }
     }
-    m0 = m1;
-    n0 = n1;
-    split = split1;
+    q += gridDim.x;
+    more = locate(q, m0, n0, split);
   }
   // no load may land in LDS that a later workgroup owns
   __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (15 << 8));
@@ -387,7 +391,7 @@ __global__ __launch_bounds__(64 * NW) void i8_gemm_skinny_kernel(I8GemmParams p)
   const bool have = li < p.M;  // lanes without a token fetch nothing
   const int8_t* a = p.a + min((int64_t)li, p.M - 1) * p.pitch + 16 * hq;
   i32x4_t acc{};
-  const int64_t steps = p.pitch >> 6;  // a multiple of 4
+  const int64_t steps = p.pitch >> 6;
   for (int64_t s0 = (int64_t)wave * U; s0 < steps; s0 += NW * U) {
     i32x4_t fb[U], fa[U];
 #pragma unroll

@@ -570,7 +570,7 @@ def _leading(T):
 
 def int8_pitch(k_len):
     """Bytes between code rows of k_len codes (metis_int8_pitch)."""
-    return (k_len + 255) // 256 * 256
+    return (k_len + 127) // 128 * 128
 
 
 def _raw_stream():

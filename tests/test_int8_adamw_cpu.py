@@ -83,7 +83,7 @@ def test_pitch_and_layout():
     for k in (0, 1, 255, 256, 257, 4096):
         assert lib.metis_int8_pitch(k) == metis.int8_pitch(k) >= k
     q = metis.I8.from_codes(torch.full((3, 5), -7, dtype=torch.int8), torch.tensor([1.0, 2.0, 4.0]))
-    assert tuple(q.codes.shape) == (3, 256) and not q.codes[:, 5:].any()
+    assert tuple(q.codes.shape) == (3, 128) and not q.codes[:, 5:].any()
     assert q.dequantize()[2].tolist() == [-28.0] * 5
 
 
