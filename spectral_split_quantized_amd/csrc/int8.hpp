@@ -53,7 +53,9 @@ template <bool SR>
 __device__ inline int i8_code(float x, float inv, float u) {
   const float y = x * inv;
   if constexpr (SR) {
-    const int c = __float2int_rd(y) + (u < __builtin_amdgcn_fractf(y) ? 1 : 0);
+    int c;  // floor(y) in one instruction
+    asm("v_cvt_flr_i32_f32 %0, %1" : "=v"(c) : "v"(y));
+    c += u < __builtin_amdgcn_fractf(y) ? 1 : 0;
     return max(-127, min(127, c));
   } else {
     return (int)fminf(fmaxf(rintf(y), -127.0f), 127.0f);

@@ -1174,7 +1174,7 @@ void launch_int8_rows(const I8QuantParams& q, hipStream_t st) {
   if (chunks <= 64) hipLaunchKernelGGL((i8_quant_rows_kernel<1, 1, SR>), grid, dim3(64), 0, st, q);
   else if (chunks <= 256) hipLaunchKernelGGL((i8_quant_rows_kernel<4, 1, SR>), grid, dim3(256), 0, st, q);
   else if (chunks <= 1024) hipLaunchKernelGGL((i8_quant_rows_kernel<8, 2, SR>), grid, dim3(512), 0, st, q);
-  else hipLaunchKernelGGL((i8_quant_rows_kernel<8, 4, SR>), grid, dim3(512), 0, st, q);
+  else hipLaunchKernelGGL((i8_quant_rows_kernel<16, 2, SR>), grid, dim3(1024), 0, st, q);
 }
 
 metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols, int64_t ld, int axes, int rounding,

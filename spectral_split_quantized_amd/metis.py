@@ -758,8 +758,9 @@ def _grad_table(grads, table=None):
 
 class _AdamWTable:
     """The table of one list of tensors, kept between steps: what it holds is
-    compared with the tensors' present addresses and sizes, and it is made
-    again where they differ."""
+    compared with the tensors' present addresses, sizes and types, and it is
+    made again where they differ.  (A gradient is on its parameter's device:
+    torch sees to that.)  The gradients given to it are contiguous."""
 
     def __init__(self):
         self.key, self.table, self.device = None, None, -1
@@ -769,25 +770,24 @@ class _AdamWTable:
         """(table, device) for this step; states are (m, v, m_scale, v_scale)
         lists, with None where a tensor has no scales; tags are the draws'
         layer numbers."""
-        key = [list(map(_numel, params)), list(map(_ptr_of, params)), tags]
+        sizes = list(map(_numel, grads))
+        key = [sizes, list(map(_ptr_of, params)), tags]
         for column in states:
             try:
                 key.append(list(map(_ptr_of, column)))
             except TypeError:  # some without scales
                 key.append([None if s is None else s.data_ptr() for s in column])
-        if key != self.key:
-            self.table, self.device = _adamw_table(params, *states, [make_tag(i, OPERAND_W) for i in tags])
-            self.key, self.grad_dtype = key, None
-        if list(map(_numel, grads)) != key[0] or not all(map(_contiguous, grads)):
-            raise ValueError("gradients must be contiguous and of the parameters' sizes")
-        if set(map(_device_of, grads)) != {self.device}:
-            raise ValueError("gradients must be on the parameters' GPU")
         dtypes = [g.dtype for g in grads]
-        if dtypes != self.grad_dtype:
+        if key != self.key or dtypes != self.grad_dtype:
+            if list(map(_numel, params)) != sizes:
+                raise ValueError("gradients must be of the parameters' sizes")
+            self.table, self.device = _adamw_table(params, *states, [make_tag(i, OPERAND_W) for i in tags])
+            if set(map(_device_of, grads)) != {self.device}:
+                raise ValueError("gradients must be on the parameters' GPU")
             if not set(dtypes) <= _DTYPES.keys():
                 raise TypeError("gradients must be float32 or bfloat16, got %s" % sorted(map(str, set(dtypes))))
             self.table["grad_dtype"] = [_DTYPES[d] for d in dtypes]
-            self.grad_dtype = dtypes
+            self.key, self.grad_dtype = key, dtypes
         self.table["grad"] = list(map(_ptr_of, grads))
         return self.table, self.device
 

@@ -77,7 +77,7 @@ class AdamW(torch.optim.Optimizer):
             grads = [p.grad for p in params]
             tags = range(first, first + len(params))
             first += len(params)
-            if any(g is None for g in grads):
+            if True in [g is None for g in grads]:
                 if self.capturable:
                     raise RuntimeError("with capturable=True every parameter needs a gradient")
                 have = [i for i, g in enumerate(grads) if g is not None]
