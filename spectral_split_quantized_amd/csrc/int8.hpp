@@ -47,8 +47,11 @@ struct I8QuantParams {
 __device__ inline float i8_scale(float amax) { return fmaxf(__fdiv_rn(amax, 127.0f), 0x1p-126f); }
 __device__ inline float i8_inverse(float scale) { return __fdiv_rn(1.0f, scale); }
 
-// u: the draw times 2^-16 (SR).  v_fract_f32 is y - floor(y) rounded to
-// binary32 but kept below 1, where u < 1 decides the same.
+// The code, in the low byte of the result.  To nearest: y kept within +-127
+// (an integer, so before the rounding as well as after it) plus 1.5 2^23,
+// whose unit is 1: the sum's rounding to nearest even leaves the integer in
+// its low bits.  SR: u is the draw times 2^-16; v_fract_f32 is y - floor(y)
+// rounded to binary32 but kept below 1, where u < 1 decides the same.
 template <bool SR>
 __device__ inline int i8_code(float x, float inv, float u) {
   const float y = x * inv;
@@ -58,7 +61,7 @@ __device__ inline int i8_code(float x, float inv, float u) {
     c += u < __builtin_amdgcn_fractf(y) ? 1 : 0;
     return max(-127, min(127, c));
   } else {
-    return (int)fminf(fmaxf(rintf(y), -127.0f), 127.0f);
+    return __float_as_int(__builtin_amdgcn_fmed3f(y, -127.0f, 127.0f) + 12582912.0f);
   }
 }
 
@@ -69,30 +72,71 @@ __device__ inline uint32_t pack4(int a, int b, int c, int d) {
   return lo | hi;
 }
 
+// eight consecutive elements at an address that 16 divides
+__device__ inline void i8_load8_vec(const void* at, int dtype, float (&x)[8]) {
+  if (dtype == 0) {
+    const uint4 q = *(const uint4*)at;
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 a = *(const float4*)at, b = *((const float4*)at + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+}
+
 // eight consecutive elements of a row from column c (n of them exist)
 __device__ inline void i8_load8(const I8QuantParams& p, int64_t row, int64_t c, int n, float (&x)[8]) {
   const int64_t at = row * p.ld + c;
   if (n == 8 && p.vec) {
-    if (p.dtype == 0) {
-      const uint4 q = *(const uint4*)((const uint16_t*)p.src + at);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
-      const float4 a = *(const float4*)((const float*)p.src + at), b = *(const float4*)((const float*)p.src + at + 4);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
+    i8_load8_vec((const char*)p.src + (at << (p.dtype ? 2 : 1)), p.dtype, x);
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = i < n ? load_as_float(p.src, p.dtype, at + i) : 0.0f;
 }
 
-// draws (times 2^-16) of the row-major positions e .. e + 7
+// the same eight elements as they lie in memory
+template <bool BF16>
+struct I8Raw8 {
+  uint32_t w[BF16 ? 4 : 8];
+
+  __device__ void load_vec(const void* at) {
+    const uint4 a = *(const uint4*)at;
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    if constexpr (!BF16) {
+      const uint4 b = *((const uint4*)at + 1);
+      w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
+  }
+  __device__ void load(const I8QuantParams& p, int64_t row, int64_t c, int n) {
+    const int64_t at = row * p.ld + c;
+    if (n == 8 && p.vec) {
+      load_vec((const char*)p.src + at * (BF16 ? 2 : 4));
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 4 : 8); ++i) {
+      if constexpr (BF16) {
+        const uint32_t lo = 2 * i < n ? ((const uint16_t*)p.src)[at + 2 * i] : 0;
+        w[i] = lo | (2 * i + 1 < n ? (uint32_t)((const uint16_t*)p.src)[at + 2 * i + 1] << 16 : 0);
+      } else {
+        w[i] = i < n ? ((const uint32_t*)p.src)[at + i] : 0;
+      }
+    }
+  }
+  __device__ float operator[](int i) const {
+    if constexpr (BF16) return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    else return __uint_as_float(w[i]);
+  }
+};
+
+// draws (times 2^-16) of the row-major positions e .. e + 7: the halves of one
+// Philox block, or of two where e is no multiple of 8
 __device__ inline void i8_draws8(const I8QuantParams& p, uint64_t e, float (&u)[8]) {
   const Philox4 b0 = philox_block(e >> 3, p.tag, p.step, p.seed);
   const uint32_t o = (uint32_t)(e & 7);
@@ -251,39 +295,53 @@ __global__ __launch_bounds__(256) void i8_amax_kernel(I8QuantParams p) {
   }
 }
 
-template <bool SR>
+template <bool SR, bool BF16>
 __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
   // transposed codes: column c at words c * kPitch .. + 31 (four rows a word)
   constexpr int kPitch = 33;
   __shared__ uint32_t tr[kI8Tile * kPitch];
   __shared__ float inv[2][kI8Tile];  // columns, rows
   const int64_t pitch0 = i8_pitch(p.rows), pitch1 = i8_pitch(p.cols);
-  const int64_t tiles_n = pitch1 / kI8Tile;
-  const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
+  const uint32_t tiles_n = (uint32_t)(pitch1 / kI8Tile);
+  const uint32_t tm = blockIdx.x / tiles_n, tn = blockIdx.x - tm * tiles_n;
+  const int64_t r0 = (int64_t)tm * kI8Tile, c0 = (int64_t)tn * kI8Tile;
   const int cc = threadIdx.x & 15, rg = threadIdx.x >> 4;
-  const int64_t c = tn * kI8Tile + cc * 8;
-  const int n = (int)min((int64_t)8, max((int64_t)0, p.cols - c));
-  float x[8][8];
+  // a whole tile addresses its elements by a uniform base and a 32-bit offset
+  const bool whole = r0 + kI8Tile <= p.rows && c0 + kI8Tile <= p.cols;
+  I8Raw8<BF16> x[8];  // unpacked where they are used: 8 of 16 bytes or 8 of 32 a thread
+  if (whole && p.vec && p.ld < (1 << 22)) {
+    constexpr int sh = BF16 ? 1 : 2;
+    const uint32_t off = ((uint32_t)(rg * 4) * (uint32_t)p.ld + cc * 8) << sh;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t row = tm * kI8Tile + rg * 4 + (i & 3) + (i >> 2) * 64;
-    i8_load8(p, min(row, p.rows - 1), c, row < p.rows ? n : 0, x[i]);
+    for (int i = 0; i < 8; ++i) {
+      const char* base = (const char*)p.src + (((r0 + (i & 3) + (i >> 2) * 64) * p.ld + c0) << sh);
+      x[i].load_vec(base + off);
+    }
+  } else {
+    const int n = (int)min((int64_t)8, max((int64_t)0, p.cols - c0 - cc * 8));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = r0 + rg * 4 + (i & 3) + (i >> 2) * 64;
+      x[i].load(p, min(row, p.rows - 1), c0 + cc * 8, row < p.rows ? n : 0);
+    }
   }
-  {  // the 128 columns' and rows' scales: two threads a line join its maxima
-    const int i = threadIdx.x & (kI8Tile - 1), odd = threadIdx.x >> 7;
+  {  // the 128 columns' and rows' scales: two threads a line, of different waves, join its maxima
+    const int i = threadIdx.x & (kI8Tile - 1), odd = __builtin_amdgcn_readfirstlane(threadIdx.x >> 7);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const float* part = side ? p.part1 : p.part0;
-      const int64_t line = (side ? tm : tn) * kI8Tile + i, lines = side ? p.rows : p.cols;
+      const int64_t first = side ? r0 : c0, lines = side ? p.rows : p.cols;
       const int tiles = (int)(side ? ceil_div<int64_t>(p.cols, kI8AmaxCols) : ceil_div<int64_t>(p.rows, 4 * p.amax_rows));
+      const bool have = part && first + i < lines;
+      const uint32_t at = have ? i : 0;
       float m = 0.0f;
-      if (part && line < lines) {
-        for (int t = odd; t < tiles; t += 32) {
-          float v[16];
+      if (part) {
+        for (int t = odd; t < tiles; t += 16) {
+          float v[8];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = part[(int64_t)min(t + 2 * k, tiles - 1) * lines + line];
+          for (int k = 0; k < 8; ++k) v[k] = (part + first + (int64_t)min(t + 2 * k, tiles - 1) * lines)[at];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) m = fmaxf(m, v[k]);
+          for (int k = 0; k < 8; ++k) m = fmaxf(m, v[k]);
         }
       }
       if (odd) inv[side][i] = m;
@@ -291,7 +349,7 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
       if (!odd) {
         const float s = i8_scale(fmaxf(m, inv[side][i]));
         inv[side][i] = i8_inverse(s);
-        if (part && line < lines && (side ? tn == 0 : tm == 0)) (side ? p.scales1 : p.scales0)[line] = s;
+        if (have && (side ? tn == 0 : tm == 0)) (side ? p.scales1 : p.scales0)[first + i] = s;
       }
     }
   }
@@ -299,25 +357,29 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
   float inv0[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) inv0[j] = inv[0][cc * 8 + j];
+  const uint32_t off1 = (uint32_t)(rg * 4) * (uint32_t)pitch1 + cc * 8;
+  uint64_t e = (uint64_t)(r0 + rg * 4) * p.cols + c0 + cc * 8;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     int w[8][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = half * 64 + rg * 4 + i;
-      const int64_t row = tm * kI8Tile + r;
-      const float (&v)[8] = x[half * 4 + i];
+      const I8Raw8<BF16>& v = x[half * 4 + i];
       float u[8];
-      if constexpr (SR) i8_draws8(p, (uint64_t)row * p.cols + c, u);
+      if constexpr (SR) {
+        i8_draws8(p, e, u);
+        e += i < 3 ? p.cols : 61 * p.cols;
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j][i] = i8_code<SR>(v[j], inv0[j], SR ? u[j] : 0.0f);
-      if (p.codes1 && row < p.rows) {
+      if (p.codes1 && (whole || r0 + r < p.rows)) {
         const float inv1 = inv[1][r];
         int q[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) q[j] = i8_code<SR>(v[j], inv1, SR ? u[j] : 0.0f);
-        *(uint2*)(p.codes1 + row * pitch1 + c) =
-            make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+        int8_t* base = p.codes1 + (r0 + half * 64 + i) * pitch1 + c0;
+        *(uint2*)(base + off1) = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
       }
     }
 #pragma unroll
@@ -327,12 +389,13 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
   __syncthreads();
   // 8 threads write a column's 128 bytes
   const int ci = threadIdx.x >> 3, part = threadIdx.x & 7;
+  int8_t* const out = p.codes0 + c0 * pitch0 + r0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t col = tn * kI8Tile + ci + 32 * k;
-    const uint32_t* t = tr + (ci + 32 * k) * kPitch + part * 4;
-    if (col < p.cols)
-      *(uint4*)(p.codes0 + col * pitch0 + tm * kI8Tile + part * 16) = make_uint4(t[0], t[1], t[2], t[3]);
+    const int col = ci + 32 * k;
+    const uint32_t* t = tr + col * kPitch + part * 4;
+    if (whole || c0 + col < p.cols)
+      *(uint4*)(out + col * pitch0 + part * 16) = make_uint4(t[0], t[1], t[2], t[3]);
   }
 }
 

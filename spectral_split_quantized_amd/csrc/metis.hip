@@ -1173,6 +1173,7 @@ void launch_int8_rows(const I8QuantParams& q, hipStream_t st) {
   const int64_t chunks = i8_pitch(q.cols) >> 3;
   if (chunks <= 64) hipLaunchKernelGGL((i8_quant_rows_kernel<1, 1, SR>), grid, dim3(64), 0, st, q);
   else if (chunks <= 256) hipLaunchKernelGGL((i8_quant_rows_kernel<4, 1, SR>), grid, dim3(256), 0, st, q);
+  else if (chunks <= 512) hipLaunchKernelGGL((i8_quant_rows_kernel<4, 2, SR>), grid, dim3(256), 0, st, q);
   else if (chunks <= 1024) hipLaunchKernelGGL((i8_quant_rows_kernel<8, 2, SR>), grid, dim3(512), 0, st, q);
   else hipLaunchKernelGGL((i8_quant_rows_kernel<16, 2, SR>), grid, dim3(1024), 0, st, q);
 }
@@ -1198,8 +1199,11 @@ metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols
   LAUNCH_CHECK();
   // the zeros behind K are written too
   const dim3 padded((unsigned)(i8_pitch(rows) / kI8Tile * (i8_pitch(cols) / kI8Tile)));
-  if (q.sr) hipLaunchKernelGGL((i8_quant_tile_kernel<true>), padded, dim3(256), 0, st, q);
-  else hipLaunchKernelGGL((i8_quant_tile_kernel<false>), padded, dim3(256), 0, st, q);
+  const bool bf16 = dtype == METIS_BF16;
+  if (q.sr && bf16) hipLaunchKernelGGL((i8_quant_tile_kernel<true, true>), padded, dim3(256), 0, st, q);
+  else if (q.sr) hipLaunchKernelGGL((i8_quant_tile_kernel<true, false>), padded, dim3(256), 0, st, q);
+  else if (bf16) hipLaunchKernelGGL((i8_quant_tile_kernel<false, true>), padded, dim3(256), 0, st, q);
+  else hipLaunchKernelGGL((i8_quant_tile_kernel<false, false>), padded, dim3(256), 0, st, q);
   LAUNCH_CHECK();
   return METIS_OK;
 }
