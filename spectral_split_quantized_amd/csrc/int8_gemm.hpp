@@ -75,10 +75,17 @@ __device__ inline uint16_t i8_bf16(float v) {  // nearest, ties to even; v is fi
 // Global -> LDS load of 16 bytes a lane to LDS address lds + 16 lane (base and
 // lds wave-uniform).  As assembly, so that the compiler does not wait for the
 // loads in flight before every LDS read: it cannot tell the ring's slots
-// apart.  The ring's own waits order them.
+// apart.  The ring's own waits order them.  A wait state stands between the
+// write of M0 and its use, and five before the first use of a base, which a
+// vector instruction just before may have written.
+template <bool FIRST>
 __device__ __forceinline__ void dma16_async(const int8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-               : "memory", "m0");
+  if constexpr (FIRST)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+                 : "memory", "m0");
 }
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
@@ -179,10 +186,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
       source(m, n, s);
     }
     const uint32_t at = base + slot * STAGE;
+    dma16_async<true>(ga, oa[0], at);
 #pragma unroll
-    for (int d = 0; d < PA; ++d) dma16_async(ga, oa[d], at + d * NW * 1024);
+    for (int d = 1; d < PA; ++d) dma16_async<false>(ga, oa[d], at + d * NW * 1024);
+    dma16_async<true>(gb, ob[0], at + A_BYTES);
 #pragma unroll
-    for (int d = 0; d < PB; ++d) dma16_async(gb, ob[d], at + A_BYTES + d * NW * 1024);
+    for (int d = 1; d < PB; ++d) dma16_async<false>(gb, ob[d], at + A_BYTES + d * NW * 1024);
     ga += 128;
     gb += 128;
     --left;

@@ -13,6 +13,8 @@ The weight is stored as in the pages' notation, ``in_features x
 out_features`` (Y = X W), as an fp32 master.
 """
 
+import weakref
+
 import torch
 
 from . import metis
@@ -90,19 +92,27 @@ class MetisLinear(torch.nn.Module):
         return _MetisLinearFn.apply(x, self.weight, self)
 
 
+def _rows(x):
+    """x as a matrix of its last dimension's rows, row-major (a copy where it is not)."""
+    x = x.reshape(-1, x.shape[-1])
+    rows, cols = x.shape
+    return x if (cols <= 1 or x.stride(1) == 1) and (rows <= 1 or x.stride(0) >= cols) else x.contiguous()
+
+
 class _Int8LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, mod):
-        x2 = x.reshape(-1, x.shape[-1])
+        need_x, need_w = ctx.needs_input_grad[:2]
+        if need_x or need_w:
+            mod._watch(ctx)
         # the same orientations as above: X along both axes (Y and dW), W
         # along both (Y and dX); an orientation whose product is not wanted is
         # left out
-        need_x, need_w = ctx.needs_input_grad[:2]
-        qx = metis.int8_quantize(x2, metis.AXIS1 | (metis.AXIS0 if need_w else 0))
+        qx = metis.int8_quantize(_rows(x), metis.AXIS1 | (metis.AXIS0 if need_w else 0))
         qw = metis.int8_quantize(w, metis.AXIS0 | (metis.AXIS1 if need_x else 0))
         y = metis.int8_gemm(qx.ax1, qw.ax0, out_dtype=x.dtype)
         ctx.qx, ctx.qw = qx.ax0, qw.ax1
-        ctx.lead, ctx.x_dtype = x.shape[:-1], x.dtype
+        ctx.lead, ctx.x_dtype, ctx.w_shape = x.shape[:-1], x.dtype, w.shape
         ctx.rounding, ctx.seed, ctx.tag, ctx.step = mod.rounding, mod.seed, mod.tags["D"], mod.step
         return y.reshape(*ctx.lead, w.shape[1])
 
@@ -110,12 +120,14 @@ class _Int8LinearFn(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad[:2]
-        d2 = dy.reshape(-1, dy.shape[-1])
-        if d2.shape[1] > 1 and d2.stride(1) != 1 or d2.shape[0] > 1 and d2.stride(0) < d2.shape[1]:
-            d2 = d2.contiguous()
+        d2 = _rows(dy)
+        dx = dw = None
+        if d2.shape[0] == 0:  # no tokens: sums over nothing
+            dx = dy.new_zeros((*ctx.lead, ctx.w_shape[0]), dtype=ctx.x_dtype) if need_x else None
+            dw = dy.new_zeros(ctx.w_shape, dtype=torch.float32) if need_w else None
+            return dx, dw, None
         qd = metis.int8_quantize(d2, (metis.AXIS1 if need_x else 0) | (metis.AXIS0 if need_w else 0),
                                  rounding=ctx.rounding, seed=ctx.seed, tag=ctx.tag, step=ctx.step)
-        dx = dw = None
         if need_x:
             dx = metis.int8_gemm(qd.ax1, ctx.qw, out_dtype=ctx.x_dtype).reshape(*ctx.lead, ctx.qw.outer)
         if need_w:
@@ -148,6 +160,25 @@ class Int8Linear(torch.nn.Module):
         self.rounding = metis.SR if rounding == "sr" else metis.RNE
         self.seed, self.step = seed, 0
         self.tags = {"D": metis.make_tag(layer, metis.OPERAND_D)}
+        self._eager = weakref.WeakSet()  # graphs recorded outside a capture, while they live
+
+    def _watch(self, ctx):
+        """Refuses to record a graph in a capture while one from outside it
+        lives: both would accumulate the weight's gradient through one node,
+        which belongs to the other's stream, and joining that stream from a
+        capture ends the process."""
+        if not torch.cuda.is_available() or not torch.cuda.is_current_stream_capturing():
+            self._eager.add(ctx)
+        elif len(self._eager):
+            raise RuntimeError("a graph of this layer from outside the capture is alive: drop its outputs first")
+
+    def __getstate__(self):
+        state = super().__getstate__() if hasattr(super(), "__getstate__") else self.__dict__
+        return {k: v for k, v in state.items() if k != "_eager"}
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self._eager = weakref.WeakSet()
 
     def forward(self, x):
         if x.shape[-1] != self.weight.shape[0]:
@@ -174,7 +205,7 @@ class Int8Frozen(torch.nn.Module):
     def forward(self, x):
         w = metis.I8.__new__(metis.I8)
         w.codes, w.scales, w.outer, w.k_len = self.codes, self.scales, self.codes.shape[0], self.k_len
-        y = metis.int8_linear(x.reshape(-1, x.shape[-1]), w)
+        y = metis.int8_linear(_rows(x), w)
         return y.reshape(*x.shape[:-1], w.outer)
 
 

@@ -12,6 +12,8 @@ from . import metis
 
 __all__ = ["AdamW"]
 
+_SETTINGS = ("state_bits", "min_8bit_size", "rounding", "seed", "max_norm", "capturable")
+
 
 class AdamW(torch.optim.Optimizer):
     """AdamW with decoupled weight decay.
@@ -69,7 +71,8 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        if not self.capturable and torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+        capturing = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+        if capturing and not self.capturable:
             raise RuntimeError("an AdamW step needs capturable=True to be captured into a graph")
         calls, first = [], 0
         for group in self.param_groups:
@@ -84,7 +87,11 @@ class AdamW(torch.optim.Optimizer):
                 params, grads, tags = ([x[i] for i in have] for x in (params, grads, tags))
             if not params:
                 continue
-            states = [self.state[p] or self._init_state(p) for p in params]
+            states = [self.state[p] for p in params]
+            if not all(states):
+                if capturing:
+                    raise RuntimeError("take one AdamW step before the capture: the states' first zeros would be captured")
+                states = [s or self._init_state(p) for p, s in zip(params, states)]
             # parameters that missed steps have counts of their own
             counts = {0} if self.capturable else {s["step"] for s in states}
             if len(counts) == 1:
@@ -124,6 +131,14 @@ class AdamW(torch.optim.Optimizer):
                 for s in states:
                     s["step"] = count
         return loss
+
+    def __getstate__(self):
+        return {**super().__getstate__(), **{k: getattr(self, k) for k in _SETTINGS}}
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self.grad_norm = self._clip = None
+        self._tables = {}
 
     def load_state_dict(self, state_dict):
         """As torch's, but the states keep their own types (torch would cast

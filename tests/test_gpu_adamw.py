@@ -10,6 +10,8 @@ the hardware reciprocal (two half units) and the two products after it.  A
 bf16 parameter adds half a unit, 2^-8 relative to nearest, a whole one
 stochastically."""
 
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -374,6 +376,46 @@ def test_uncapturable_step_is_refused_in_a_capture():
             opt.step()
     graph.replay()
     torch.cuda.synchronize()
+
+
+def test_first_step_in_a_capture_is_refused():
+    ps, g = _params(5)
+    opt = optim.AdamW(ps, capturable=True)
+    _set_grads(ps, g)
+    x = torch.zeros(1, device="cuda")
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        x += 1
+        with pytest.raises(RuntimeError, match="before the capture"):
+            opt.step()
+
+
+def test_replaced_parameters_gradients_and_states_are_seen():
+    """Between steps: a parameter's data on new memory, gradients of another
+    type and layout, states moved by hand, and the optimizer copied."""
+    ps, g = _params(6, ((70, 80), (4100,)))
+    twins = [torch.nn.Parameter(p.detach().clone()) for p in ps]
+    opt, ref = (optim.AdamW(x, lr=1e-2, seed=1) for x in (ps, twins))
+    for t in range(5):
+        _set_grads(ps, g)
+        for a, b in zip(ps, twins):
+            b.grad = a.grad.clone()
+        if t == 1:
+            ps[0].data = ps[0].detach().clone()
+        if t == 2:
+            ps[0].grad = ps[0].grad.T.contiguous().T
+        if t == 3:
+            for s in opt.state.values():
+                s["exp_avg"] = s["exp_avg"].clone()
+                s["exp_avg_scale"] = s["exp_avg_scale"].clone()
+        if t == 4:
+            opt = copy.deepcopy(opt)
+            for a, p in zip(ps, opt.param_groups[0]["params"]):
+                p.grad = a.grad
+            ps = opt.param_groups[0]["params"]
+        opt.step()
+        ref.step()
+        assert all(torch.equal(a, b) for a, b in zip(ps, twins))
+    metis.status_sync()
 
 
 def test_quantised_network_trains():

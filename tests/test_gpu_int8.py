@@ -311,6 +311,68 @@ def test_layer_partial_gradients_batched_input_and_frozen_form():
     metis.status_sync()
 
 
+def test_layer_odd_inputs():
+    """Transposed, expanded and one-dimensional inputs, and no tokens at all."""
+    g = torch.Generator().manual_seed(4)
+    lin = Int8Linear(48, 20, weight=torch.randn(48, 20, generator=g).cuda(), rounding="rne")
+    x = torch.randn(48, 30, generator=g).cuda()
+    assert torch.equal(lin(x.T), lin(x.T.contiguous()))
+    one = torch.randn(48, generator=g).cuda()
+    want = lin(one[None].contiguous())
+    assert torch.equal(lin(one), want[0]) and torch.equal(lin(one.expand(5, 48)), want.expand(5, 20))
+    frozen = lin.frozen()
+    assert torch.equal(frozen(one), want[0]) and torch.equal(frozen(x.T), lin(x.T))
+    none = torch.zeros(2, 0, 48, device="cuda", requires_grad=True)
+    y = lin(none)
+    assert tuple(y.shape) == (2, 0, 20) and tuple(frozen(none).shape) == (2, 0, 20)
+    y.sum().backward()
+    assert tuple(none.grad.shape) == (2, 0, 48) and not lin.weight.grad.any()
+    metis.status_sync()
+
+
+def test_layer_in_a_graph():
+    """A forward and backward pass captured and replayed on new inputs, and
+    refused while a graph from outside the capture lives."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    lin = Int8Linear(64, 40, weight=torch.randn(64, 40, generator=g, device="cuda"))
+    x = torch.randn(50, 64, generator=g, device="cuda", requires_grad=True)
+    d = torch.randn(50, 40, generator=g, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lin(x).backward(d)
+    torch.cuda.current_stream().wait_stream(side)
+    x.grad = lin.weight.grad = None
+    alive = lin(x.detach())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        d += 0
+        with pytest.raises(RuntimeError, match="alive"):
+            lin(x)
+    del alive
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lin(x)
+        y.backward(d)
+    for i in range(3):
+        xi = torch.randn(50, 64, generator=g, device="cuda") * (i + 1)
+        di = torch.randn(50, 40, generator=g, device="cuda")
+        with torch.no_grad():
+            x.copy_(xi)
+            d.copy_(di)
+        x.grad.zero_()
+        lin.weight.grad.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        twin = Int8Linear(64, 40, weight=lin.weight.detach())
+        xt = xi.clone().requires_grad_(True)
+        yt = twin(xt)
+        yt.backward(di)
+        assert torch.equal(y, yt) and torch.equal(x.grad, xt.grad) and torch.equal(lin.weight.grad, twin.weight.grad)
+    metis.status_sync()
+
+
 def test_other_stream_and_graph_replays():
     """Calls on a side stream, and a captured linear replayed on new inputs
     between eager work."""
