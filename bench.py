@@ -644,6 +644,43 @@ def measure_mxfp4(m, X, W, t_last, nvfp4_gemm_ms, reps=10, sample_rows=256):
                     "no tensor scale, no spectral split; y_rel_fro_err_vs_exact rounds to nearest, _sr stochastically)"}
 
 
+def measure_int8(m, X, W, nvfp4_gemm_ms, reps=10, sample_rows=256):
+    """The int8 variant: the gate projection's operands with one scale per
+    token and output channel, rounded to nearest, multiplied on the int8
+    matrix instruction.  Median times of ``reps`` calls (HIP events) and the
+    forward error against the exact product on sampled rows."""
+    import torch
+    T, H = X.shape
+    F = W.shape[1]
+
+    def median_ms(fn):
+        fn()
+        ev = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)) for _ in range(reps)]
+        for a, b in ev:
+            a.record()
+            fn()
+            b.record()
+        torch.cuda.synchronize()
+        return sorted(a.elapsed_time(b) for a, b in ev)[reps // 2]
+
+    qx, qw = m.int8_quantize(X, m.AXIS1), m.int8_quantize(W, m.AXIS0)
+    C = torch.empty(T, F, dtype=torch.bfloat16, device=X.device)
+    q_ms = median_ms(lambda: (m.int8_quantize(X, m.AXIS1, out=qx), m.int8_quantize(W, m.AXIS0, out=qw)))
+    g_ms = median_ms(lambda: m.int8_gemm(qx.ax1, qw.ax0, C))
+    m.status_sync()
+    tops = 2.0 * T * F * H / (g_ms * 1e-3) / 1e12
+    idx = torch.arange(0, T, T // sample_rows, device=X.device)
+    exact = X[idx].float() @ W.float()
+    Y = m.int8_linear(X[idx], qw.ax0, out_dtype=torch.float32)
+    err = float(torch.linalg.norm(Y - exact) / torch.linalg.norm(exact))
+    return {"shape_MNK": [T, F, H], "gemm_ms": round(g_ms, 4), "gemm_tops": round(tops, 1),
+            "roofline": {"bound": "mfma", "achieved": round(tops, 1), "peak": 5030.0, "unit": "TOP/s",
+                         "frac": round(tops / 5030.0, 4), "dtype": "int8 x int8, int32 sums, bf16 output"},
+            "nvfp4_split_gemm_ms": round(nvfp4_gemm_ms, 4) if nvfp4_gemm_ms else None,
+            "quantize_both_operands_ms": round(q_ms, 3), "y_rel_fro_err_vs_exact": round(err, 6),
+            "note": "a third format: one scale per token and channel, rounded to nearest, no spectral split"}
+
+
 def decompose_timed(M, cfg, sample, tag, t, f, workspace=None):
     """metis_decompose on the current stream, timed with HIP events: (total
     ms, sketch ms, projection + rediagonalisation ms), the last two from the
@@ -984,7 +1021,8 @@ def measure_training_loop(dev, steps=48, periods=(1, 8, 32), tokens=8192, lr=2e-
     import torch
     import torch.nn.functional as Fn
     from spectral_split_quantized_amd import synth
-    from spectral_split_quantized_amd.layer import MetisLinear, set_step
+    from spectral_split_quantized_amd.layer import Int8Linear, MetisLinear, set_step
+    from spectral_split_quantized_amd.optim import AdamW
     H, F_, k = 768, 3072, 12
 
     def weight(r, c, seed):
@@ -1001,18 +1039,24 @@ def measure_training_loop(dev, steps=48, periods=(1, 8, 32), tokens=8192, lr=2e-
             y = Fn.gelu(x.float() @ t1) @ t2
         return x, y
 
-    def run(period):
+    def run(period, adamw8=False):
+        """period None: float32; "int8": int8 layers; else the split's refresh
+        period.  adamw8: the library's AdamW with 8-bit states, no decay."""
         if period is None:
             w1 = torch.nn.Parameter(s1.clone())
             w2 = torch.nn.Parameter(s2.clone())
             params = [w1, w2]
             fwd = lambda x: Fn.gelu(x.float() @ w1) @ w2
+        elif period == "int8":
+            l1, l2 = Int8Linear(H, F_, weight=s1.clone(), layer=0), Int8Linear(F_, H, weight=s2.clone(), layer=1)
+            params = [l1.weight, l2.weight]
+            fwd = lambda x: l2(Fn.gelu(l1(x.float())))
         else:
             l1 = MetisLinear(H, F_, k, l_k=82, refresh=period, weight=s1.clone(), layer=0, device=dev)
             l2 = MetisLinear(F_, H, k, l_k=82, refresh=period, weight=s2.clone(), layer=1, device=dev)
             params = [l1.weight, l2.weight]
             fwd = lambda x: l2(Fn.gelu(l1(x.float())))
-        opt = torch.optim.Adam(params, lr=lr)
+        opt = AdamW(params, lr=lr, weight_decay=0.0) if adamw8 else torch.optim.Adam(params, lr=lr)
         rec = {"loss": [], "ms": [], "align_w": [], "align_x": [], "drift_w": [], "drift_x": []}
         prev = None
         for t in range(steps):
@@ -1037,7 +1081,7 @@ def measure_training_loop(dev, steps=48, periods=(1, 8, 32), tokens=8192, lr=2e-
             torch.cuda.synchronize()
             rec["ms"].append(1e3 * (time.perf_counter() - t0))
             rec["loss"].append(float(loss.detach()))
-            if period is not None:
+            if period not in (None, "int8"):
                 # the right factors this step used: sketched at its last refresh, rotated since
                 rec["align_w"].append(_captured(w_now, l1.factors["W"].V, cur[0]))
                 rec["align_x"].append(_captured(x, l1.factors["X"].V, cur[1]))
@@ -1063,6 +1107,11 @@ def measure_training_loop(dev, steps=48, periods=(1, 8, 32), tokens=8192, lr=2e-
             "ms_per_step": mean(r["ms"][2:]),
             "cached_factor_energy": {"W1": mean(r["align_w"]), "X": mean(r["align_x"]),
                                         "W1_min": round(min(r["align_w"]), 5), "X_min": round(min(r["align_x"]), 5)}}
+    for name, period in (("float32_adamw8", None), ("int8_adamw8", "int8"), ("refresh_8_adamw8", 8)):
+        r = run(period, adamw8=True)
+        out[name] = {"loss_first": round(r["loss"][0], 5), "loss_last8": mean(r["loss"][-8:]), "ms_per_step": mean(r["ms"][2:])}
+    out["adamw8_note"] = ("the same runs (and one with int8 layers) with the library's AdamW: states in 8 bits, rounded "
+                          "stochastically, no weight decay")
     out["energy_note"] = ("share of the operand's best rank-k energy ||M Q||^2 / ||M V_k||^2 that a k-dim right subspace "
                           "captures (1 = as good as the exact top-k): cached_factor_energy for the factor each step used, "
                           "previous_step_subspace_energy for the previous step's exact top-k subspace (the float32 run)")
@@ -1225,6 +1274,9 @@ def main():
         extras["mxfp4_variant"] = measure_mxfp4(mlp.metis, inputs["X_gu"][t_last % len(inputs["X_gu"])],
                                                 inputs["W_gate"][t_last % len(inputs["W_gate"])], t_last,
                                                 roofline["avg_ms"])
+        log("int8 variant")
+        extras["int8_variant"] = measure_int8(mlp.metis, inputs["X_gu"][t_last % len(inputs["X_gu"])],
+                                              inputs["W_gate"][t_last % len(inputs["W_gate"])], roofline["avg_ms"])
         for name in LAYER_CONFIGS:
             log("single projection %s" % name)
             extras.setdefault("layers", {})[name] = measure_layer(dev, name)
