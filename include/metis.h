@@ -331,8 +331,8 @@ metis_status metis_mxfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, c
  *
  * metis_int8_gemm: C = diag(s_A) (A B^T) diag(s_B), row-major with leading
  * dimension ldc >= B->n_outer, binary32 or bf16 (c_dtype).  A and B have the
- * same k_len, at most 133056 (METIS_E_UNSUPPORTED above): sums are exact in
- * int32, and an output is RN(RN(RN(sum) s_A) s_B), rounded once more for
+ * same k_len, at most 131071 (METIS_E_UNSUPPORTED above): sums are exact in
+ * int32 for codes of any value, and an output is RN(RN(RN(sum) s_A) s_B), rounded once more for
  * bf16.  n_outer == 0 on either side is a no-op, k_len == 0 invalid.  ws
  * holds metis_int8_gemm_workspace(A->n_outer, B->n_outer, k_len) bytes (0:
  * may be NULL), 16-byte aligned: a product with few outputs is cut along K.

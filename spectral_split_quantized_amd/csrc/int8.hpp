@@ -357,7 +357,7 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
   float inv0[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) inv0[j] = inv[0][cc * 8 + j];
-  const uint32_t off1 = (uint32_t)(rg * 4) * (uint32_t)pitch1 + cc * 8;
+  const int64_t off1 = rg * 4 * pitch1 + cc * 8;
   uint64_t e = (uint64_t)(r0 + rg * 4) * p.cols + c0 + cc * 8;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {

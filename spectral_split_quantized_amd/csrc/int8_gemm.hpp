@@ -1,7 +1,7 @@
 // int8_gemm.hpp -- C = diag(s_a) (A B^T) diag(s_b) of two int8 operands
 // (format: int8.hpp) on gfx950's int8 matrix instructions.
 //
-// Products are summed exactly in int32 (K <= kI8MaxK keeps |sum| <= 127^2 K
+// Products are summed exactly in int32 (K <= kI8MaxK keeps |sum| <= 128^2 K
 // below 2^31, so any split of K gives the same sum); an output is
 // RN(RN(RN(sum) s_a) s_b) in binary32, rounded once more for bf16.
 #pragma once
@@ -13,7 +13,7 @@
 
 namespace metis {
 
-constexpr int64_t kI8MaxK = 133056;  // 127^2 * 133056 < 2^31
+constexpr int64_t kI8MaxK = 131071;
 
 struct I8GemmParams {
   int64_t M, N, pitch;     // pitch: K rounded up to 128, zeros behind K
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
   if (!locate(q, m0, n0, split)) return;
 
   // the loads: a DMA moves 8 rows, its lanes' offsets from the tile's first
-  // row fit 32 bits (256 rows of at most 133120 bytes)
+  // row fit 32 bits (256 rows of at most 131072 bytes)
   const int8_t *ga, *gb;
   uint32_t oa[PA], ob[PB];
   int left;  // stages of the tile still to load

@@ -1707,6 +1707,7 @@ metis_status metis_int8_quantize(const void* M, int32_t dtype, int64_t rows, int
   const I8Ws w = carve_int8(cv, rows, cols, axes);
   if (cv.used() > 0 && (!ws || cv.used() > ws_bytes))
     return fail(METIS_E_WORKSPACE, "workspace %zu < %zu", ws_bytes, cv.used());
+  if (cv.used() > 0 && ((uintptr_t)ws & 15)) return fail(METIS_E_INVALID, "int8_quantize: workspace not 16-byte aligned");
   if ((s = ensure_device_tables()) != METIS_OK) return s;
   return run_int8_quant(M, dtype, rows, cols, ld, axes, rounding, seed, tag, step, ax0, ax1, w, (hipStream_t)stream);
 }
@@ -1753,7 +1754,7 @@ metis_status metis_int8_linear(const void* X, int32_t dtype, int64_t tokens, int
   const I8LinearWs w = carve_int8_linear(cv, tokens, W->n_outer, W->k_len);
   if (cv.used() && (!ws || cv.used() > ws_bytes))
     return fail(METIS_E_WORKSPACE, "workspace %zu < %zu", ws_bytes, cv.used());
-  if ((uintptr_t)ws & 15) return fail(METIS_E_INVALID, "int8_linear: workspace not 16-byte aligned");
+  if (cv.used() && ((uintptr_t)ws & 15)) return fail(METIS_E_INVALID, "int8_linear: workspace not 16-byte aligned");
   if ((s = ensure_device_tables()) != METIS_OK) return s;
   xq.codes = w.codes;
   xq.scales = w.scales;

@@ -563,6 +563,16 @@ def _on_device(*tensors):
     return _device_context(device)
 
 
+def _space(workspace, need, device):
+    """The workspace to use: the caller's where it holds ``need`` bytes, else a
+    new one (none for 0 bytes)."""
+    if workspace is None or workspace.numel() < need:
+        return _workspace(need, device) if need else None
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on %s" % device)
+    return workspace
+
+
 def _leading(T):
     """Leading dimension of a row-major view (a lone row's stride says nothing)."""
     return T.stride(0) if T.shape[0] > 1 else max(T.stride(0), T.shape[1])
@@ -588,8 +598,8 @@ class I8:
 
     @classmethod
     def from_codes(cls, codes, scales):
-        """An operand of given codes (int8, outer x k_len, without -128) and
-        scales (outer), copied into the library's layout."""
+        """An operand of given codes (int8, outer x k_len) and scales (outer),
+        copied into the library's layout."""
         if codes.dtype != torch.int8 or codes.dim() != 2 or scales.dtype != torch.float32 \
                 or tuple(scales.shape) != (codes.shape[0],):
             raise ValueError("codes must be an int8 matrix and scales float32 with one value per row")
@@ -641,7 +651,7 @@ def int8_quantize(M, axes=AXIS1, out=None, rounding=RNE, seed=0, tag=0, step=0, 
     with _on_device(M, *parts):
         lib = load()
         need = lib.metis_int8_quantize_workspace(rows, cols, axes) if axes & AXIS0 else 0  # rows alone need none
-        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, M.device) if need else None
+        ws = _space(workspace, need, M.device)
         _check(lib.metis_int8_quantize(M.data_ptr(), dtype, rows, cols, _leading(M), axes, rounding, seed, tag, step,
                                        None if c0 is None else ctypes.byref(c0),
                                        None if c1 is None else ctypes.byref(c1), _ptr(ws), need if ws is None else ws.numel(),
@@ -668,7 +678,7 @@ def int8_gemm(a, b, C=None, out_dtype=torch.float32, workspace=None):
     with _on_device(a.codes, a.scales, b.codes, b.scales, C):
         lib = load()
         need = lib.metis_int8_gemm_workspace(a.outer, b.outer, a.k_len)
-        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, C.device) if need else None
+        ws = _space(workspace, need, C.device)
         _check(lib.metis_int8_gemm(ctypes.byref(ac), ctypes.byref(bc), C.data_ptr(), _dtype_code(C), _leading(C),
                                    None if ws is None else ws.data_ptr(), need if ws is None else ws.numel(), _raw_stream()))
     return C
@@ -690,7 +700,7 @@ def int8_linear(x, w, Y=None, out_dtype=None, workspace=None):
     with _on_device(x, w.codes, w.scales, Y):
         lib = load()
         need = lib.metis_int8_linear_workspace(tokens, w.outer, w.k_len)
-        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, x.device) if need else None
+        ws = _space(workspace, need, x.device)
         _check(lib.metis_int8_linear(x.data_ptr(), dtype, tokens, _leading(x), ctypes.byref(wc), Y.data_ptr(),
                                      _dtype_code(Y), _leading(Y), None if ws is None else ws.data_ptr(), need if ws is None else ws.numel(),
                                      _raw_stream()))
@@ -771,7 +781,7 @@ class _AdamWTable:
         lists, with None where a tensor has no scales; tags are the draws'
         layer numbers."""
         sizes = list(map(_numel, grads))
-        key = [sizes, list(map(_ptr_of, params)), tags]
+        key = [sizes, list(map(_numel, params)), list(map(_ptr_of, params)), tags]
         for column in states:
             try:
                 key.append(list(map(_ptr_of, column)))
@@ -779,7 +789,7 @@ class _AdamWTable:
                 key.append([None if s is None else s.data_ptr() for s in column])
         dtypes = [g.dtype for g in grads]
         if key != self.key or dtypes != self.grad_dtype:
-            if list(map(_numel, params)) != sizes:
+            if key[1] != sizes:
                 raise ValueError("gradients must be of the parameters' sizes")
             self.table, self.device = _adamw_table(params, *states, [make_tag(i, OPERAND_W) for i in tags])
             if set(map(_device_of, grads)) != {self.device}:
@@ -863,7 +873,7 @@ def _grad_norm_run(table, device, max_norm, out, workspace=None):
     ptr = table.ctypes.data
     with _device_context(device):
         need = lib.metis_grad_norm_workspace(ptr, len(table))
-        ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, out.device)
+        ws = _space(workspace, need, out.device)
         _check(lib.metis_grad_norm(ptr, len(table), max_norm, out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream()))
     return out
 

@@ -378,6 +378,23 @@ def test_uncapturable_step_is_refused_in_a_capture():
     torch.cuda.synchronize()
 
 
+def test_closure_and_no_gradients():
+    p = torch.nn.Parameter(torch.ones(5, device="cuda"))
+    opt = optim.AdamW([p], lr=0.1, weight_decay=0.0, state_bits=32)
+
+    def closure():
+        opt.zero_grad()
+        loss = (p * p).sum()
+        loss.backward()
+        return loss
+
+    assert opt.step(closure).item() == 5.0 and bool((p < 1).all())
+    before = p.detach().clone()
+    opt.zero_grad()
+    opt.step()
+    assert torch.equal(p, before)
+
+
 def test_first_step_in_a_capture_is_refused():
     ps, g = _params(5)
     opt = optim.AdamW(ps, capturable=True)

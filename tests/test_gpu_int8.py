@@ -125,6 +125,21 @@ def test_quantize_non_finite_sets_numeric_status(axes, bad):
     metis.status_sync()
 
 
+@pytest.mark.parametrize("rows,cols", [(3, 1 << 25), (1 << 22, 3)])
+def test_quantize_very_long_lines(rows, cols):
+    """One long axis, both orientations: sampled lines against the definition."""
+    say("int8 quantize %d x %d" % (rows, cols))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, cols, generator=g, device="cuda")
+    q = metis.int8_quantize(x, BOTH)
+    metis.status_sync()
+    for got, y in ((q.ax1, x), (q.ax0, x.T)):
+        some = torch.tensor(sorted({0, y.shape[0] // 2, y.shape[0] - 1}), device="cuda")
+        codes, scales = int8.quantize(_np(y[some].contiguous()), 1)
+        assert np.array_equal(got.scales[some].cpu().numpy(), scales)
+        assert np.array_equal(got.codes[some][:, :got.k_len].cpu().numpy(), codes)
+
+
 def test_quantize_empty_is_a_no_op():
     for shape in ((0, 5), (5, 0), (0, 0)):
         q = metis.int8_quantize(torch.zeros(shape, device="cuda"), BOTH)
@@ -148,14 +163,16 @@ def test_gemm_equals_definition(m, n, k, out):
 
 @pytest.mark.parametrize("m", [5, 300])
 def test_gemm_longest_sums_stay_in_int32(m):
-    """k_len at its limit with every product at 127^2, and one beyond it refused."""
-    k = 133056
+    """k_len at its limit with every product at 127^2 and at 128^2, and one beyond it refused."""
+    k = 131071
     say("int8 gemm longest k, %d rows" % m)
     ones = lambda r: metis.I8.from_codes(torch.full((r, k), 127, dtype=torch.int8, device="cuda"),  # noqa: E731
                                          torch.ones(r, device="cuda"))
     C = metis.int8_gemm(ones(m), ones(9))
+    low = metis.I8.from_codes(torch.full((9, k), -128, dtype=torch.int8, device="cuda"), torch.ones(9, device="cuda"))
+    C2 = metis.int8_gemm(low, low)
     metis.status_sync()
-    assert bool((C == float(np.float32(127 * 127 * k))).all())
+    assert bool((C == float(np.float32(127 * 127 * k))).all()) and bool((C2 == float(np.float32(128 * 128 * k))).all())
     with pytest.raises(metis.MetisError) as ei:
         metis.int8_gemm(metis.I8(m, k + 1), metis.I8(9, k + 1))
     assert ei.value.status == metis.E_UNSUPPORTED
@@ -222,6 +239,32 @@ def test_linear_equals_its_parts(tokens, k, n, dtype, out):
     metis.status_sync()
     want = torch.from_numpy(_gemm32(int8.quantize(_np(x)), w)).to(out or dtype)
     assert y.dtype == want.dtype and torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens", [1, 5, 40])
+def test_linear_of_misaligned_and_strided_views(tokens, dtype):
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    wide = torch.randn(tokens, 777, generator=g, device="cuda").to(dtype)
+    w = _upload(_random(np.random.default_rng(tokens), 60, 701))
+    buf = torch.full((tokens, 70), 7.0, dtype=dtype, device="cuda")
+    y = metis.int8_linear(wide[:, 3:704], w, Y=buf[:, 5:65])
+    metis.status_sync()
+    assert torch.equal(y, metis.int8_linear(wide[:, 3:704].contiguous(), w))
+    assert bool((buf[:, :5] == 7).all()) and bool((buf[:, 65:] == 7).all())
+
+
+def test_workspaces():
+    """A caller's workspace is used where it is large enough and refused on another device."""
+    x = torch.randn(200, 300, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    a, b = metis.int8_quantize(x, BOTH, workspace=ws), metis.int8_quantize(x, BOTH)
+    assert torch.equal(a.ax0.codes, b.ax0.codes)
+    q = metis.int8_quantize(torch.randn(20, 4096, device="cuda")).ax1
+    assert torch.equal(metis.int8_gemm(q, q, workspace=ws), metis.int8_gemm(q, q))
+    for call in (lambda w: metis.int8_quantize(x, BOTH, workspace=w), lambda w: metis.grad_norm([x], workspace=w)):
+        with pytest.raises(ValueError, match="workspace"):
+            call(torch.empty(1 << 20, dtype=torch.uint8))
 
 
 @pytest.mark.parametrize("tokens", [1, 3])

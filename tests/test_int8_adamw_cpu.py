@@ -40,6 +40,7 @@ def test_quantize_argument_errors():
     assert _quant(ax1=_i8(64, 48, codes=None)) == metis.E_INVALID
     assert _quant(axes=1, ax0=_i8(48, 64), ws=D, n=16) == metis.E_WORKSPACE
     assert _quant(axes=1, ax0=_i8(48, 64), ws=None) == metis.E_WORKSPACE
+    assert _quant(axes=1, ax0=_i8(48, 64), ws=ctypes.c_void_p(4100)) == metis.E_INVALID
     assert _quant(rows=0, ax1=_i8(0, 48, None, None)) == metis.OK  # nothing to do
 
 
@@ -51,7 +52,7 @@ def test_gemm_and_linear_argument_errors():
 
     assert gemm(_i8(8, 128), _i8(64, 129)) == metis.E_INVALID
     assert gemm(_i8(8, 0), _i8(64, 0)) == metis.E_INVALID
-    assert gemm(_i8(8, 133057), _i8(64, 133057)) == metis.E_UNSUPPORTED
+    assert gemm(_i8(8, 131072), _i8(64, 131072)) == metis.E_UNSUPPORTED
     assert gemm(_i8(8, 128), _i8(64, 128), ldc=63) == metis.E_INVALID
     assert gemm(_i8(8, 128), _i8(64, 128), C=None) == metis.E_INVALID
     assert gemm(_i8(8, 128), _i8(64, 128), dt=2) == metis.E_INVALID
