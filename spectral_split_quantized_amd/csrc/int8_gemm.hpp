@@ -314,23 +314,42 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void i8_gemm_kernel(I8GemmParams p
               }
           }
           wave_fence();
+          const int64_t split0 = OUT == kOutPart ? split * p.M * p.ldc : 0;
+          if (vec) {
 #pragma unroll
-          for (int k = 0; k < ER / 8; ++k) {
-            const int r = k * 8 + rr;
-            const u32x4_t w = *(const u32x4_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
-            const int64_t row = row0 + i * 32 + r0 + r, col = col0 + j0 * 32 + rc * PER;
-            if (row >= p.M) continue;
-            const int64_t at = (OUT == kOutPart ? split * p.M * p.ldc : 0) + row * p.ldc + col;
-            if (vec && col + PER <= p.N) {
-              u32x4_t* const to = OUT == kOutBF16 ? (u32x4_t*)((uint16_t*)p.C + at) : (u32x4_t*)((float*)p.C + at);
-              __builtin_nontemporal_store(w, to);
-            } else {
+            for (int k = 0; k < ER / 8; ++k) {
+              const int r = k * 8 + rr;
+              const u32x4_t w = *(const u32x4_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
+              const int64_t row = row0 + i * 32 + r0 + r, col = col0 + j0 * 32 + rc * PER;
+              if (row >= p.M) continue;
+              const int64_t at = split0 + row * p.ldc + col;
+              if (col + PER <= p.N) {
+                u32x4_t* const to = OUT == kOutBF16 ? (u32x4_t*)((uint16_t*)p.C + at) : (u32x4_t*)((float*)p.C + at);
+                __builtin_nontemporal_store(w, to);
+              } else {
 #pragma unroll
-              for (int e = 0; e < PER; ++e) {
-                if (col + e >= p.N) break;
-                if constexpr (OUT == kOutBF16) ((uint16_t*)p.C)[at + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-                else ((float*)p.C)[at + e] = __uint_as_float(w[e]);
+                for (int e = 0; e < PER; ++e) {
+                  if (col + e >= p.N) break;
+                  if constexpr (OUT == kOutBF16) ((uint16_t*)p.C)[at + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                  else ((float*)p.C)[at + e] = __uint_as_float(w[e]);
+                }
               }
+            }
+          } else {
+            // rows of any alignment: neighbouring lanes write neighbouring
+            // values (4096 x 4095 x 4096 to fp32: 72 us; 86 with four values a lane)
+            constexpr int RS = 64 / COLS;  // rows a store
+            const int c = el & (COLS - 1);
+            const int64_t col = col0 + j0 * 32 + c;
+#pragma unroll
+            for (int k = 0; k < ER / RS; ++k) {
+              const int r = k * RS + el / COLS;
+              const uint8_t* const from = my + r * 128 + ((c / PER) ^ ((r >> 1) & 7)) * 16;
+              const int64_t row = row0 + i * 32 + r0 + r;
+              if (row >= p.M || col >= p.N) continue;
+              const int64_t at = split0 + row * p.ldc + col;
+              if constexpr (OUT == kOutBF16) ((uint16_t*)p.C)[at] = *((const uint16_t*)from + c % PER);
+              else ((float*)p.C)[at] = *((const float*)from + c % PER);
             }
           }
           wave_fence();
