@@ -18,6 +18,12 @@
 // far less than E4M3's spacing of an eighth, so to nearest a state would not
 // move at all; stochastically it moves by the right amount on average.  A
 // positive r never becomes zero, which would turn m / r into m / eps.
+//
+// A wave takes four state blocks, a lane four consecutive elements of each, so
+// a block's maxima are joined inside the wave and every load of the wave is in
+// flight at once.  Bound by HBM: 176 M binary32 elements in 908 us with 32-bit
+// states (28 bytes an element, 5.4 TB/s) and in 530 us with 8-bit states
+// rounded stochastically (16.06 bytes, 5.3 TB/s); a copy runs at 5.1.
 #pragma once
 
 #include "common.hpp"
@@ -280,7 +286,9 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t) {
 // ------------------------------------------------------------ global norm --
 //
 // Squares are exact in binary64 and summed there, in an order that the sizes
-// alone fix, so the norm does not depend on how the work is spread.
+// alone fix, so the norm does not depend on how the work is spread.  One read
+// of the gradients (148 tensors, 57 MB: 18 us in two launches), then a
+// workgroup that joins the partial sums (2 us).
 __global__ __launch_bounds__(256) void grad_norm_kernel(NormTable t) {
   __shared__ double red[4];
   const int ti = table_index<kNormTensors>(t.first, t.count, blockIdx.x);
