@@ -1,4 +1,4 @@
-"""Build libmetis.so in-tree with hipcc for gfx950.
+"""Build libmetis.so in-tree with hipcc for gfx950, and _tensors.so.
 
 Usage: python -m spectral_split_quantized_amd.build
 """
@@ -11,6 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 OUT = os.path.join(HERE, "libmetis.so")
+TENSORS_OUT = os.path.join(HERE, "_tensors.so")
 
 # translation units and their extra flags: the register-dequant GEMM is
 # scheduled for instruction-level parallelism (its expansion instructions
@@ -40,7 +41,27 @@ def _run(cmd, verbose):
     subprocess.run(cmd, check=True)
 
 
+def build_tensors(verbose=False):
+    """_tensors.so: the extension that reads tensor lists (host code against
+    torch's headers)."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    cmd = [hipcc, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, os.path.join(CSRC, "tensors.cpp"),
+           "-I", sysconfig.get_paths()["include"]]
+    cmd += [a for d in include_paths() for a in ("-isystem", d)]
+    cmd += [a for d in library_paths() for a in ("-L", d)] + ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    tmp = TENSORS_OUT + ".tmp"
+    _run(cmd + ["-o", tmp], verbose)
+    os.replace(tmp, TENSORS_OUT)
+    return TENSORS_OUT
+
+
 def build(verbose=False):
+    build_tensors(verbose)
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     os.makedirs(OBJ, exist_ok=True)
     objs = []

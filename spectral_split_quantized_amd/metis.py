@@ -715,7 +715,16 @@ STATE_BLOCK = 256  # consecutive elements that share a scale of an 8-bit state
 _ADAMW_TENSOR = np.dtype([("param", "<u8"), ("grad", "<u8"), ("m", "<u8"), ("v", "<u8"), ("m_scale", "<u8"),
                           ("v_scale", "<u8"), ("n", "<i8"), ("param_dtype", "<i4"), ("grad_dtype", "<i4"),
                           ("state_bits", "<i4"), ("tag", "<u4")])
-_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _tensors():
+    """The extension that reads tensor lists into tables (raises if it has not
+    been built)."""
+    try:
+        from . import _tensors as ext
+    except ImportError as e:
+        raise ImportError("_tensors.so cannot be loaded (%s); run python -m spectral_split_quantized_amd.build" % e) from e
+    return ext
 
 
 def adamw_state(n, bits=8, device="cuda"):
@@ -733,108 +742,8 @@ def adamw_state(n, bits=8, device="cuda"):
     return (*codes, *(torch.zeros(blocks, dtype=torch.float32, device=device) for _ in range(2)))
 
 
-_numel, _ptr_of = torch.Tensor.numel, torch.Tensor.data_ptr
-_device_of, _contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
-
-
-def _tensor_list(tensors, sizes, device, what, dtypes=None):
-    """Addresses of tensors that must be contiguous, on one GPU and of the given sizes."""
-    if list(map(_numel, tensors)) != sizes or not all(map(_contiguous, tensors)):
-        raise ValueError("%s must be contiguous and of the parameters' sizes" % what)
-    if sizes and set(map(_device_of, tensors)) != {device}:
-        raise ValueError("%s must be on the parameters' GPU" % what)
-    if dtypes is not None and not {t.dtype for t in tensors} <= dtypes:
-        raise TypeError("%s must be of %s, got %s" % (what, sorted(map(str, dtypes)),
-                                                      sorted(str(t.dtype) for t in tensors)))
-    return list(map(_ptr_of, tensors))
-
-
-def _grad_table(grads, table=None):
-    """The gradients' part of a tensor table."""
-    if table is None:
-        table = np.zeros(len(grads), _ADAMW_TENSOR)
-        table["n"] = list(map(_numel, grads))
-        device = grads[0].get_device() if grads else -1
-    else:
-        table, device = table
-        if len(grads) != len(table):
-            raise ValueError("%d gradients for %d parameters" % (len(grads), len(table)))
-    if grads and device < 0:
-        raise ValueError("gradients must be on a GPU")
-    table["grad"] = _tensor_list(grads, table["n"].tolist(), device, "gradients", _DTYPES.keys())
-    table["grad_dtype"] = [_DTYPES[g.dtype] for g in grads]
-    return table, device
-
-
-class _AdamWTable:
-    """The table of one list of tensors, kept between steps: what it holds is
-    compared with the tensors' present addresses, sizes and types, and it is
-    made again where they differ.  (A gradient is on its parameter's device:
-    torch sees to that.)  The gradients given to it are contiguous."""
-
-    def __init__(self):
-        self.key, self.table, self.device = None, None, -1
-        self.grad_dtype = None
-
-    def update(self, params, grads, states, tags):
-        """(table, device) for this step; states are (m, v, m_scale, v_scale)
-        lists, with None where a tensor has no scales; tags are the draws'
-        layer numbers."""
-        sizes = list(map(_numel, grads))
-        key = [sizes, list(map(_numel, params)), list(map(_ptr_of, params)), tags]
-        for column in states:
-            try:
-                key.append(list(map(_ptr_of, column)))
-            except TypeError:  # some without scales
-                key.append([None if s is None else s.data_ptr() for s in column])
-        dtypes = [g.dtype for g in grads]
-        if key != self.key or dtypes != self.grad_dtype:
-            if key[1] != sizes:
-                raise ValueError("gradients must be of the parameters' sizes")
-            self.table, self.device = _adamw_table(params, *states, [make_tag(i, OPERAND_W) for i in tags])
-            if set(map(_device_of, grads)) != {self.device}:
-                raise ValueError("gradients must be on the parameters' GPU")
-            if not set(dtypes) <= _DTYPES.keys():
-                raise TypeError("gradients must be float32 or bfloat16, got %s" % sorted(map(str, set(dtypes))))
-            self.table["grad_dtype"] = [_DTYPES[d] for d in dtypes]
-            self.key, self.grad_dtype = key, dtypes
-        self.table["grad"] = list(map(_ptr_of, grads))
-        return self.table, self.device
-
-
-def _adamw_table(params, ms, vs, m_scales, v_scales, tags):
-    n = len(params)
-    if not all(len(x) == n for x in (ms, vs, m_scales, v_scales)) or (tags is not None and len(tags) != n):
-        raise ValueError("parameters, states and scales must be lists of one length")
-    table = np.zeros(n, _ADAMW_TENSOR)
-    if not n:
-        return table, -1
-    device = params[0].get_device()
-    if device < 0:
-        raise ValueError("parameters must be on a GPU")
-    sizes = list(map(_numel, params))
-    table["n"] = sizes
-    table["param"] = _tensor_list(params, sizes, device, "parameters", _DTYPES.keys())
-    table["param_dtype"] = [_DTYPES[p.dtype] for p in params]
-    eight = [s is not None for s in m_scales]
-    if eight != [s is not None for s in v_scales]:
-        raise ValueError("a parameter's two states must have the same width")
-    table["state_bits"] = np.where(eight, 8, 32)
-    for name, states, scales in (("m", ms, m_scales), ("v", vs, v_scales)):
-        table[name] = _tensor_list(states, sizes, device, "states")
-        for s, e in zip(states, eight):
-            if s.dtype != (torch.float8_e4m3fn if e else torch.float32):
-                raise TypeError("states must be float32, or float8_e4m3fn with scales; got %s" % s.dtype)
-        some = [s for s in scales if s is not None]
-        addr = _tensor_list(some, [(k + STATE_BLOCK - 1) // STATE_BLOCK for k, e in zip(sizes, eight) if e], device,
-                            "scales", {torch.float32})
-        table[name + "_scale"][np.asarray(eight, bool)] = addr
-    for name in ("param", "m", "v"):
-        addr = [a for a, k in zip(table[name].tolist(), sizes) if k]
-        if len(set(addr)) != len(addr):
-            raise ValueError("a parameter or a state appears twice")
-    table["tag"] = tags if tags is not None else [make_tag(i, OPERAND_W) for i in range(n)]
-    return table, device
+def _table(n):
+    return np.empty(n, _ADAMW_TENSOR)
 
 
 def _adamw_run(table, device, lr, betas, eps, weight_decay, step, clip, rounding, seed):
@@ -861,9 +770,9 @@ def adamw_step(params, grads, ms, vs, m_scales=None, v_scales=None, *, lr, betas
     tags select the draws of stochastic rounding (by default make_tag(i,
     OPERAND_W) for the i-th parameter)."""
     none = [None] * len(params)
-    table, device = _adamw_table(params, ms, vs, none if m_scales is None else m_scales,
-                                 none if v_scales is None else v_scales, tags)
-    _grad_table(grads, (table, device))
+    table = _table(len(params))
+    device = _tensors().fill(list(params), list(grads), list(ms), list(vs), none if m_scales is None else list(m_scales),
+                             none if v_scales is None else list(v_scales), None if tags is None else list(tags), table)
     if len(params):
         _adamw_run(table, device, lr, betas, eps, weight_decay, step, clip, rounding, seed)
 
@@ -883,7 +792,8 @@ def grad_norm(grads, max_norm=float("inf"), out=None, workspace=None):
     as two float32 on the GPU (metis_grad_norm)."""
     if not len(grads):
         raise ValueError("grad_norm needs a gradient")
-    table, device = _grad_table(grads)
+    table = _table(len(grads))
+    device = _tensors().fill_grads(list(grads), table)
     if out is None:
         out = torch.empty(2, dtype=torch.float32, device=grads[0].device)
     if out.dtype != torch.float32 or out.numel() != 2 or not out.is_contiguous() or out.get_device() != device:

@@ -12,6 +12,7 @@ from . import metis
 
 __all__ = ["AdamW"]
 
+_STATES = ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")
 _SETTINGS = ("state_bits", "min_8bit_size", "rounding", "seed", "max_norm", "capturable")
 
 
@@ -52,7 +53,6 @@ class AdamW(torch.optim.Optimizer):
         self.seed, self.max_norm, self.capturable = seed, max_norm, capturable
         self.grad_norm = None
         self._clip = None
-        self._tables = {}
 
     def _init_state(self, p):
         eight = self.state_bits == 8 and p.numel() >= self.min_8bit_size
@@ -74,57 +74,32 @@ class AdamW(torch.optim.Optimizer):
         capturing = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
         if capturing and not self.capturable:
             raise RuntimeError("an AdamW step needs capturable=True to be captured into a graph")
-        calls, first = [], 0
+        ext, calls, first = metis._tensors(), [], 0  # calls: (group, table, device, step count, states, gradients)
         for group in self.param_groups:
             params = group["params"]
-            grads = [p.grad for p in params]
-            tags = range(first, first + len(params))
+            table = metis._table(len(params))
+            found = ext.fill_state(params, self.state, first, not self.capturable, table)
+            if found is not None:
+                calls.append((group, table, *found, None))
+            else:
+                calls.extend(self._sorted_calls(group, first, capturing))
             first += len(params)
-            if True in [g is None for g in grads]:
-                if self.capturable:
-                    raise RuntimeError("with capturable=True every parameter needs a gradient")
-                have = [i for i, g in enumerate(grads) if g is not None]
-                params, grads, tags = ([x[i] for i in have] for x in (params, grads, tags))
-            if not params:
-                continue
-            states = [self.state[p] for p in params]
-            if not all(states):
-                if capturing:
-                    raise RuntimeError("take one AdamW step before the capture: the states' first zeros would be captured")
-                states = [s or self._init_state(p) for p, s in zip(params, states)]
-            # parameters that missed steps have counts of their own
-            counts = {0} if self.capturable else {s["step"] for s in states}
-            if len(counts) == 1:
-                calls.append((group, params, grads, states, tags))
-                continue
-            for count in sorted(counts):
-                some = [i for i, s in enumerate(states) if s["step"] == count]
-                calls.append((group, *([x[i] for i in some] for x in (params, grads, states, tags))))
         if not calls:
             return loss
-        tables = []
-        for k, (_, params, grads, states, tags) in enumerate(calls):
-            if not all(map(torch.Tensor.is_contiguous, grads)):
-                grads = [g.contiguous() for g in grads]
-            columns = ([s["exp_avg"] for s in states], [s["exp_avg_sq"] for s in states],
-                       [s.get("exp_avg_scale") for s in states], [s.get("exp_avg_sq_scale") for s in states])
-            kept = self._tables.setdefault(k, metis._AdamWTable())
-            tables.append((*kept.update(params, grads, columns, tags), grads))
-        if len({d for _, d, _ in tables}) != 1:
+        device, clip = calls[0][2], None
+        if any(c[2] != device for c in calls):
             raise ValueError("the parameters must be on one GPU")
-        device, clip = tables[0][1], None
         if self.max_norm is not None:
             if self._clip is None or self._clip.get_device() != device:
                 self._clip = torch.empty(2, dtype=torch.float32, device=torch.device("cuda", device))
-            whole = tables[0][0] if len(tables) == 1 else metis.np.concatenate([t for t, _, _ in tables])
+            whole = calls[0][1] if len(calls) == 1 else metis.np.concatenate([c[1] for c in calls])
             metis._grad_norm_run(whole, device, self.max_norm, self._clip)
             self.grad_norm, clip = self._clip[0], self._clip[1]
-        for (group, _, _, states, _), (table, device, _) in zip(calls, tables):
+        for group, table, device, count, states, _ in calls:
             if self.capturable:
                 torch._foreach_add_([s["step"] for s in states], 1)
-                count = states[0]["step"]
             else:
-                count = states[0]["step"] + 1
+                count += 1
             metis._adamw_run(table, device, group["lr"], group["betas"], group["eps"], group["weight_decay"], count, clip,
                              self.rounding, self.seed)
             if not self.capturable:
@@ -132,13 +107,37 @@ class AdamW(torch.optim.Optimizer):
                     s["step"] = count
         return loss
 
+    def _sorted_calls(self, group, first, capturing):
+        """A group's calls where its parameters are not all alike: without a
+        gradient (left out), without a state (made), with a gradient to be
+        copied into rows, or with step counts of their own (a call each)."""
+        have = [(first + i, p) for i, p in enumerate(group["params"]) if p.grad is not None]
+        if self.capturable and len(have) != len(group["params"]):
+            raise RuntimeError("with capturable=True every parameter needs a gradient")
+        new = [p for _, p in have if not self.state[p]]
+        if new and capturing:
+            raise RuntimeError("take one AdamW step before the capture: the states' first zeros would be captured")
+        for p in new:
+            self._init_state(p)
+        calls = []
+        for count in [None] if self.capturable else sorted({self.state[p]["step"] for _, p in have}):
+            some = [(i, p) for i, p in have if count is None or self.state[p]["step"] == count]
+            if not some:
+                continue
+            params, states = [p for _, p in some], [self.state[p] for _, p in some]
+            grads = [p.grad.contiguous() for p in params]
+            table = metis._table(len(params))
+            device = metis._tensors().fill(params, grads, *([s.get(k) for s in states] for k in _STATES),
+                                           [metis.make_tag(i, metis.OPERAND_W) for i, _ in some], table)
+            calls.append((group, table, device, states[0]["step"], states, grads))
+        return calls
+
     def __getstate__(self):
         return {**super().__getstate__(), **{k: getattr(self, k) for k in _SETTINGS}}
 
     def __setstate__(self, state):
         super().__setstate__(state)
         self.grad_norm = self._clip = None
-        self._tables = {}
 
     def load_state_dict(self, state_dict):
         """As torch's, but the states keep their own types (torch would cast

@@ -258,6 +258,42 @@ def test_more_than_two_to_the_31_elements():
     assert out[0].item() == pytest.approx(3 ** 0.5, rel=2.0 ** -23)
 
 
+def test_lists_are_checked():
+    """What the library would write twice, or past an end, is refused before anything is enqueued."""
+    buf = torch.zeros(200, device="cuda")
+    g = torch.ones(100, device="cuda")
+    new = lambda n=1: [torch.zeros(100, device="cuda") for _ in range(n)]  # noqa: E731
+
+    def step(p, grads, m, v, ms=None, vs=None):
+        metis.adamw_step(p, grads, m, v, ms, vs, lr=1.0, step=1)
+
+    a, b = buf[:100], buf[99:199]
+    for p, m, v in (([a, a], new(2), new(2)), ([a, b], new(2), new(2)), ([a], [a], new()), ([a], new(), [buf[50:150]])):
+        with pytest.raises(ValueError, match="twice"):
+            step(p, [g] * len(p), m, v)
+    m = new()
+    with pytest.raises(ValueError, match="twice"):
+        step([a], [g], m, m)
+    for p, gr, m, v in (([a], [g[:99]], new(), new()), ([a], [g], [m[0][:99]], new()), ([buf[::2]], [g], new(), new()),
+                        ([a], [torch.ones(200, device="cuda")[::2]], new(), new()), ([a], [g.cpu()], new(), new())):
+        with pytest.raises(ValueError):
+            step(p, gr, m, v)
+    for p, gr, m, v in (([a], [g.half()], new(), new()), ([a.half()], [g], new(), new()), ([a], [g], [m[0].half()], new()),
+                        ([a], [g], [m[0].to(torch.float8_e4m3fn)], new()), ([a], [None], new(), new())):
+        with pytest.raises(TypeError):
+            step(p, gr, m, v)
+    c, d, cs, ds = metis.adamw_state(100, 8)
+    with pytest.raises(ValueError):
+        step([a], [g], [c], [d], [cs], [None])
+    with pytest.raises(ValueError):
+        step([a], [g], [c], [d], [cs], [ds[:0]])
+    with pytest.raises(TypeError):
+        step([a], [g], new(), new(), [cs], [ds])
+    step([a], [g], [c], [d], [cs], [ds])
+    metis.status_sync()
+    assert bool((a == -1).all()) and not buf[100:].any()
+
+
 # ----------------------------------------------------------- the optimizer --
 
 def _params(seed=0, sizes=((50, 90), (90,), (64, 64), (1,))):
