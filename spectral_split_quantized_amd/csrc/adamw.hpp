@@ -23,7 +23,8 @@
 // a block's maxima are joined inside the wave and every load of the wave is in
 // flight at once.  Bound by HBM: 176 M binary32 elements in 908 us with 32-bit
 // states (28 bytes an element, 5.4 TB/s) and in 530 us with 8-bit states
-// rounded stochastically (16.06 bytes, 5.3 TB/s); a copy runs at 5.1.
+// rounded stochastically (16.06 bytes, 5.3 TB/s); a copy runs at 5.1.  With 8
+// bits the vector units are close behind: 92 instructions an element.
 #pragma once
 
 #include "common.hpp"
@@ -103,7 +104,14 @@ __device__ inline int table_index(const uint32_t* first, int count, uint32_t bid
   return __builtin_amdgcn_readfirstlane(found - 1);
 }
 
-__device__ inline bool is_finite_bits(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+// neither NaN nor infinite: one class compare
+__device__ inline bool is_finite_class(float x) { return __builtin_amdgcn_classf(x, 0x1F8); }
+
+// E4M3 byte I of a word
+template <int I>
+__device__ inline float state_decode(uint32_t w) {
+  return __builtin_amdgcn_cvt_f32_fp8((int)w, I);
+}
 
 // four consecutive values from element e (n of them exist)
 __device__ inline void load4(const void* base, bool bf16, int64_t e, int n, bool vec, float (&x)[4]) {
@@ -208,35 +216,54 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t) {
   for (int b = 0; b < NB; ++b) {
     const int64_t e = (block0 + b) * kStateBlock + lane * 4;
     if ((block0 + b) * kStateBlock >= n) break;
-    float r[4];
+    float r[4], m1[4], v1[4], r1[4], p1[4];
+    if constexpr (EIGHT) {
+      m[b][0] = state_decode<0>(mc[b]), m[b][1] = state_decode<1>(mc[b]);
+      m[b][2] = state_decode<2>(mc[b]), m[b][3] = state_decode<3>(mc[b]);
+      r[0] = state_decode<0>(vc[b]), r[1] = state_decode<1>(vc[b]);
+      r[2] = state_decode<2>(vc[b]), r[3] = state_decode<3>(vc[b]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m[b][i] *= ms[b];
+        r[i] *= vs[b];
+        v[b][i] = r[i] * r[i];
+      }
+    }
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float gr = t.clip ? g[b][i] * gs : g[b][i];
+      m1[i] = t.b1 * m[b][i] + t.c1 * gr;
+      v1[i] = t.b2 * v[b][i] + t.c2 * gr * gr;
+      r1[i] = sqrtf(v1[i]);
+      // the hardware reciprocal is within one unit in the last place, far
+      // below what the parameter's own rounding leaves of the step
+      const float upd = m1[i] * __builtin_amdgcn_rcpf(r1[i] * inv_c2 + t.eps);
+      p1[i] = p[b][i] * t.decay - step_size * upd;
+      // an m' that is not finite makes p' so, unless v' is not finite either
+      ok &= is_finite_class(v1[i]) && is_finite_class(p1[i]);
+    }
+    if (!__all(ok)) {  // rare: such elements keep what they had (places behind the end do not count)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (is_finite_class(v1[i]) && is_finite_class(p1[i])) continue;
+        bad |= i < cnt[b];
+        m1[i] = m[b][i];
+        v1[i] = v[b][i];
+        r1[i] = EIGHT ? r[i] : 0.0f;
+        p1[i] = p[b][i];
+      }
+    }
     uint32_t am = 0, ar = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      m[b][i] = m1[i];
+      v[b][i] = v1[i];
+      r[i] = r1[i];
+      p[b][i] = p1[i];
       if constexpr (EIGHT) {
-        m[b][i] = e4m3_decode_hw(mc[b] >> (8 * i) & 255u) * ms[b];
-        r[i] = e4m3_decode_hw(vc[b] >> (8 * i) & 255u) * vs[b];
-        v[b][i] = r[i] * r[i];
-      }
-      const float gr = t.clip ? g[b][i] * gs : g[b][i];
-      const float m1 = t.b1 * m[b][i] + t.c1 * gr;
-      const float v1 = t.b2 * v[b][i] + t.c2 * gr * gr;
-      const float r1 = sqrtf(v1);
-      // the hardware reciprocal is within one unit in the last place, far
-      // below what the parameter's own rounding leaves of the step
-      const float upd = m1 * __builtin_amdgcn_rcpf(r1 * inv_c2 + t.eps);
-      const float p1 = p[b][i] * t.decay - step_size * upd;
-      const bool ok = is_finite_bits(m1) && is_finite_bits(v1) && is_finite_bits(p1);
-      bad |= !ok && i < cnt[b];
-      if (ok) {
-        m[b][i] = m1;
-        v[b][i] = v1;
-        p[b][i] = p1;
-        r[i] = r1;
-      }
-      if constexpr (EIGHT) {
-        if (i >= cnt[b]) m[b][i] = r[i] = 0.0f;
-        am = max(am, __float_as_uint(m[b][i]) & 0x7FFFFFFFu);
-        ar = max(ar, __float_as_uint(r[i]));
+        am = max(am, __float_as_uint(m1[i]) & 0x7FFFFFFFu);
+        ar = max(ar, __float_as_uint(r1[i]));
       }
     }
     if (t.p_bf16) {
