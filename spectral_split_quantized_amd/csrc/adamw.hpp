@@ -53,12 +53,15 @@ __host__ __device__ inline int state_exponent(uint32_t amax_bits) {
   return e < -126 ? -126 : e;
 }
 
-constexpr int kAdamTensors = 56;    // a launch's table stays below 4 KB of kernel arguments
+// A launch's table of tensors travels as its kernel argument, at most 4 KB:
+// nothing to copy or to keep, and a capture records it by value.
 constexpr int kAdamWork = 4096;     // elements of one workgroup: 4 waves of 4 state blocks
-constexpr int kNormTensors = 128;
+constexpr int kNormTensors = 192;
 constexpr int kNormWork = 16384;
 
+template <bool EIGHT>
 struct AdamTable {
+  static constexpr int kTensors = EIGHT ? 60 : 80, kScales = EIGHT ? kTensors : 1;
   int count, p_bf16, g_bf16;
   float b1, c1, b2, c2, eps, decay;  // c1 = 1 - b1, c2 = 1 - b2, decay = 1 - lr wd
   float step_size, inv_c2;           // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
@@ -67,17 +70,17 @@ struct AdamTable {
   const float* clip;                 // gradient factor, or null
   uint64_t seed;
   uint32_t step;
-  uint32_t first[kAdamTensors];      // first workgroup of each tensor
-  uint32_t tag[kAdamTensors];
-  void* p[kAdamTensors];
-  const void* g[kAdamTensors];
-  void* m[kAdamTensors];
-  void* v[kAdamTensors];
-  float* ms[kAdamTensors];
-  float* vs[kAdamTensors];
-  int64_t n[kAdamTensors];
+  uint32_t first[kTensors];          // first workgroup of each tensor
+  uint32_t tag[kTensors];
+  void* p[kTensors];
+  const void* g[kTensors];
+  void* m[kTensors];
+  void* v[kTensors];
+  float* ms[kScales];
+  float* vs[kScales];
+  int64_t n[kTensors];
 };
-static_assert(sizeof(AdamTable) <= 4096, "kernel arguments");
+static_assert(sizeof(AdamTable<true>) <= 4096 && sizeof(AdamTable<false>) <= 4096, "kernel arguments");
 
 struct NormTable {
   int count, g_bf16;
@@ -162,9 +165,9 @@ __device__ inline void store_codes4(uint8_t* base, int64_t e, int n, bool vec, u
 __device__ inline float pow2_float(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126..127
 
 template <bool EIGHT, bool SR>
-__global__ __launch_bounds__(256) void adamw_kernel(AdamTable t) {
+__global__ __launch_bounds__(256) void adamw_kernel(AdamTable<EIGHT> t) {
   constexpr int NB = 4;  // state blocks a wave
-  const int ti = table_index<kAdamTensors>(t.first, t.count, blockIdx.x);
+  const int ti = table_index<AdamTable<EIGHT>::kTensors>(t.first, t.count, blockIdx.x);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t n = t.n[ti];
   const int64_t block0 = (int64_t)(blockIdx.x - t.first[ti]) * (kAdamWork / kStateBlock) + wave * NB;
@@ -314,7 +317,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable t) {
 //
 // Squares are exact in binary64 and summed there, in an order that the sizes
 // alone fix, so the norm does not depend on how the work is spread.  One read
-// of the gradients (148 tensors, 57 MB: 18 us in two launches), then a
+// of the gradients (148 tensors, 57 MB), then a
 // workgroup that joins the partial sums (2 us).
 __global__ __launch_bounds__(256) void grad_norm_kernel(NormTable t) {
   __shared__ double red[4];

@@ -1251,6 +1251,55 @@ metis_status run_int8_gemm(const metis_i8* A, const metis_i8* B, void* C, int c_
 
 // -------------------------------------------------------------- AdamW --
 
+// The tensors of one combination of types: bit 0 bf16 parameters, bit 1 bf16
+// gradients, bit 2 (EIGHT) 8-bit states.
+template <bool EIGHT>
+metis_status adamw_kind(const metis_adamw_tensor* tensors, int64_t count, const metis_adamw_config& cfg, int kind,
+                        hipStream_t st) {
+  AdamTable<EIGHT> t{};
+  t.p_bf16 = (kind & 1) != 0;
+  t.g_bf16 = (kind & 2) != 0;
+  t.b1 = (float)cfg.beta1, t.c1 = (float)(1.0 - cfg.beta1);
+  t.b2 = (float)cfg.beta2, t.c2 = (float)(1.0 - cfg.beta2);
+  t.eps = (float)cfg.eps, t.decay = (float)(1.0 - cfg.lr * cfg.weight_decay);
+  t.lr = cfg.lr, t.db1 = cfg.beta1, t.db2 = cfg.beta2;
+  t.step_count = cfg.step_count;
+  t.clip = cfg.clip;
+  t.seed = cfg.seed;
+  if (!cfg.step_count) {
+    t.step_size = (float)(cfg.lr / (1.0 - pow(cfg.beta1, (double)cfg.step)));
+    t.inv_c2 = (float)(1.0 / sqrt(1.0 - pow(cfg.beta2, (double)cfg.step)));
+    t.step = (uint32_t)cfg.step;
+  }
+  const bool sr = cfg.rounding == METIS_SR && (EIGHT || t.p_bf16);
+  uint64_t groups = 0;
+  auto flush = [&]() -> metis_status {
+    if (!t.count) return METIS_OK;
+    if (sr) hipLaunchKernelGGL((adamw_kernel<EIGHT, true>), dim3((unsigned)groups), dim3(256), 0, st, t);
+    else hipLaunchKernelGGL((adamw_kernel<EIGHT, false>), dim3((unsigned)groups), dim3(256), 0, st, t);
+    LAUNCH_CHECK();
+    t.count = 0;
+    groups = 0;
+    return METIS_OK;
+  };
+  metis_status s;
+  for (int64_t i = 0; i < count; ++i) {
+    const metis_adamw_tensor& a = tensors[i];
+    if (a.n == 0 || ((a.param_dtype == METIS_BF16) | (a.grad_dtype == METIS_BF16) << 1 | (a.state_bits == 8) << 2) != kind)
+      continue;
+    const uint64_t need = (uint64_t)ceil_div<int64_t>(a.n, kAdamWork);
+    if (t.count == AdamTable<EIGHT>::kTensors || groups + need > INT32_MAX)
+      if ((s = flush()) != METIS_OK) return s;
+    const int k = t.count++;
+    t.first[k] = (uint32_t)groups;
+    t.tag[k] = a.tag;
+    t.p[k] = a.param, t.g[k] = a.grad, t.m[k] = a.m, t.v[k] = a.v, t.n[k] = a.n;
+    if constexpr (EIGHT) t.ms[k] = a.m_scale, t.vs[k] = a.v_scale;
+    groups += need;
+  }
+  return flush();
+}
+
 metis_status adamw_grad_check(const metis_adamw_tensor& a, int64_t i, const char* what) {
   if (a.n < 0) return fail(METIS_E_INVALID, "%s: tensor %lld: n %lld", what, (long long)i, (long long)a.n);
   if (a.n > (int64_t)INT32_MAX * kAdamWork)
@@ -1802,55 +1851,11 @@ metis_status metis_adamw_step(const metis_adamw_tensor* tensors, int64_t count, 
       return fail(METIS_E_INVALID, "adamw_step: tensor %lld: misaligned pointer", (long long)i);
   }
   if ((s = ensure_device_tables()) != METIS_OK) return s;
-  AdamTable t{};
-  t.b1 = (float)cfg->beta1, t.c1 = (float)(1.0 - cfg->beta1);
-  t.b2 = (float)cfg->beta2, t.c2 = (float)(1.0 - cfg->beta2);
-  t.eps = (float)cfg->eps, t.decay = (float)(1.0 - cfg->lr * cfg->weight_decay);
-  t.lr = cfg->lr, t.db1 = cfg->beta1, t.db2 = cfg->beta2;
-  t.step_count = cfg->step_count;
-  t.clip = cfg->clip;
-  t.seed = cfg->seed;
-  if (!cfg->step_count) {
-    t.step_size = (float)(cfg->lr / (1.0 - pow(cfg->beta1, (double)cfg->step)));
-    t.inv_c2 = (float)(1.0 / sqrt(1.0 - pow(cfg->beta2, (double)cfg->step)));
-    t.step = (uint32_t)cfg->step;
-  }
-  const bool sr = cfg->rounding == METIS_SR;
-  hipStream_t st = (hipStream_t)stream;
   // one pass per combination of types, a launch per table of tensors
   for (int kind = 0; kind < 8; ++kind) {
-    const bool eight = kind & 4;
-    t.p_bf16 = (kind & 1) != 0;
-    t.g_bf16 = (kind & 2) != 0;
-    t.count = 0;
-    uint64_t groups = 0;
-    auto flush = [&]() -> metis_status {
-      if (!t.count) return METIS_OK;
-      const dim3 grid((unsigned)groups), block(256);
-      if (eight && sr) hipLaunchKernelGGL((adamw_kernel<true, true>), grid, block, 0, st, t);
-      else if (eight) hipLaunchKernelGGL((adamw_kernel<true, false>), grid, block, 0, st, t);
-      else if (sr && t.p_bf16) hipLaunchKernelGGL((adamw_kernel<false, true>), grid, block, 0, st, t);
-      else hipLaunchKernelGGL((adamw_kernel<false, false>), grid, block, 0, st, t);
-      LAUNCH_CHECK();
-      t.count = 0;
-      groups = 0;
-      return METIS_OK;
-    };
-    for (int64_t i = 0; i < count; ++i) {
-      const metis_adamw_tensor& a = tensors[i];
-      if (a.n == 0 || ((a.param_dtype == METIS_BF16) | (a.grad_dtype == METIS_BF16) << 1 | (a.state_bits == 8) << 2) != kind)
-        continue;
-      const uint64_t need = (uint64_t)ceil_div<int64_t>(a.n, kAdamWork);
-      if (t.count == kAdamTensors || groups + need > INT32_MAX)
-        if ((s = flush()) != METIS_OK) return s;
-      const int k = t.count++;
-      t.first[k] = (uint32_t)groups;
-      t.tag[k] = a.tag;
-      t.p[k] = a.param, t.g[k] = a.grad, t.m[k] = a.m, t.v[k] = a.v;
-      t.ms[k] = a.m_scale, t.vs[k] = a.v_scale, t.n[k] = a.n;
-      groups += need;
-    }
-    if ((s = flush()) != METIS_OK) return s;
+    s = kind & 4 ? adamw_kind<true>(tensors, count, *cfg, kind, (hipStream_t)stream)
+                 : adamw_kind<false>(tensors, count, *cfg, kind, (hipStream_t)stream);
+    if (s != METIS_OK) return s;
   }
   return METIS_OK;
 }
