@@ -21,10 +21,10 @@
 //
 // A wave takes four state blocks, a lane four consecutive elements of each, so
 // a block's maxima are joined inside the wave and every load of the wave is in
-// flight at once.  Bound by HBM: 176 M binary32 elements in 908 us with 32-bit
-// states (28 bytes an element, 5.4 TB/s) and in 530 us with 8-bit states
-// rounded stochastically (16.06 bytes, 5.3 TB/s); a copy runs at 5.1.  With 8
-// bits the vector units are close behind: 92 instructions an element.
+// flight at once.  Bound by HBM: 176 M binary32 elements in 816-910 us with
+// 32-bit states (28 bytes an element, 5.4-6.0 TB/s) and in 470-530 us with 8-bit
+// states rounded stochastically (16.06 bytes, 5.3-6.0 TB/s); a copy runs at 5.1.  With 8
+// bits the vector units are close behind: 94 instructions an element.
 #pragma once
 
 #include "common.hpp"
