@@ -101,8 +101,10 @@ def _rows(x):
 
 class _Int8LinearFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, mod):
-        need_x, need_w = ctx.needs_input_grad[:2]
+    def forward(ctx, x, w, mod, record):
+        # needs_input_grad says nothing of torch.no_grad(): record is the
+        # caller's grad mode (inside a forward it is always off)
+        need_x, need_w = (record and need for need in ctx.needs_input_grad[:2])
         if need_x or need_w:
             mod._watch(ctx)
         # the same orientations as above: X along both axes (Y and dW), W
@@ -125,14 +127,14 @@ class _Int8LinearFn(torch.autograd.Function):
         if d2.shape[0] == 0:  # no tokens: sums over nothing
             dx = dy.new_zeros((*ctx.lead, ctx.w_shape[0]), dtype=ctx.x_dtype) if need_x else None
             dw = dy.new_zeros(ctx.w_shape, dtype=torch.float32) if need_w else None
-            return dx, dw, None
+            return dx, dw, None, None
         qd = metis.int8_quantize(d2, (metis.AXIS1 if need_x else 0) | (metis.AXIS0 if need_w else 0),
                                  rounding=ctx.rounding, seed=ctx.seed, tag=ctx.tag, step=ctx.step)
         if need_x:
             dx = metis.int8_gemm(qd.ax1, ctx.qw, out_dtype=ctx.x_dtype).reshape(*ctx.lead, ctx.qw.outer)
         if need_w:
             dw = metis.int8_gemm(ctx.qx, qd.ax0)
-        return dx, dw, None
+        return dx, dw, None, None
 
 
 class Int8Linear(torch.nn.Module):
@@ -183,7 +185,7 @@ class Int8Linear(torch.nn.Module):
     def forward(self, x):
         if x.shape[-1] != self.weight.shape[0]:
             raise ValueError("x has %d features, the layer %d" % (x.shape[-1], self.weight.shape[0]))
-        return _Int8LinearFn.apply(x, self.weight, self)
+        return _Int8LinearFn.apply(x, self.weight, self, torch.is_grad_enabled())
 
     def frozen(self):
         """The serving form of this layer with its present weight."""

@@ -133,6 +133,29 @@ def test_set_step_reaches_both_kinds():
     assert net[1].tags["D"] == metis.make_tag(3, metis.OPERAND_D)
 
 
+@pytest.mark.parametrize("mode,x_grad,w_grad,axes", [
+    (torch.no_grad, True, True, (2, 1)), (torch.inference_mode, False, True, (2, 1)), (torch.enable_grad, False, False, (2, 1)),
+    (torch.enable_grad, False, True, (3, 1)), (torch.enable_grad, True, False, (2, 3)), (torch.enable_grad, True, True, (3, 3))])
+def test_forward_quantises_what_its_gradients_need(monkeypatch, mode, x_grad, w_grad, axes):
+    """The orientations of X and W that a forward pass asks for, and whether it
+    counts as a graph that lives: without a gradient to come, neither."""
+    asked = []
+
+    def quantize(m, ax, **kw):
+        asked.append(ax)
+        return metis.I8Operand(m.shape[0], m.shape[1], ax, "cpu")
+
+    monkeypatch.setattr(metis, "int8_quantize", quantize)
+    monkeypatch.setattr(metis, "int8_gemm", lambda a, b, out_dtype: torch.zeros(a.outer, b.outer, dtype=out_dtype))
+    lin = Int8Linear(6, 4, device="cpu")
+    lin.weight.requires_grad_(w_grad)
+    x = torch.zeros(3, 6, requires_grad=x_grad)
+    with mode():
+        y = lin(x)
+    assert tuple(asked) == axes and (metis.AXIS0, metis.AXIS1) == (1, 2)
+    assert len(lin._eager) == (axes != (2, 1)) and y.requires_grad == (axes != (2, 1))
+
+
 def _adamw(tensor=None, count=1, **cfg):
     t = np.zeros(max(count, 1), metis._ADAMW_TENSOR)
     for name in ("param", "grad", "m", "v", "m_scale", "v_scale"):
