@@ -141,7 +141,9 @@ class AdamW(torch.optim.Optimizer):
 
     def load_state_dict(self, state_dict):
         """As torch's, but the states keep their own types (torch would cast
-        8-bit codes to the parameters' type)."""
+        8-bit codes to the parameters' type), and the step count takes the
+        form that ``capturable`` asks for.  States are new memory: capture a
+        step anew after loading."""
         super().load_state_dict(state_dict)
         saved = {i: p for group, here in zip(state_dict["param_groups"], self.param_groups)
                  for i, p in zip(group["params"], here["params"])}
@@ -150,3 +152,8 @@ class AdamW(torch.optim.Optimizer):
                 p = saved[i]
                 self.state[p] = {k: v.detach().clone().to(p.device) if isinstance(v, torch.Tensor) else v
                                  for k, v in state.items()}
+                step = self.state[p].get("step")
+                if self.capturable and step is not None:
+                    self.state[p]["step"] = torch.as_tensor(step, dtype=torch.int64, device=p.device)
+                elif isinstance(step, torch.Tensor):
+                    self.state[p]["step"] = int(step)

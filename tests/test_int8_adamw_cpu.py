@@ -229,3 +229,18 @@ def test_optimizer_refusals():
     cap = optim.AdamW([p, q], capturable=True)
     with pytest.raises(RuntimeError, match="gradient"):
         cap.step()
+
+
+@pytest.mark.parametrize("saved,here", [(False, False), (False, True), (True, False), (True, True)])
+def test_step_counts_follow_the_loading_optimizer(saved, here):
+    """A checkpoint's step counts, host integers or tensors, in the form that the loading optimizer advances."""
+    p = torch.nn.Parameter(torch.zeros(300))
+    opt = optim.AdamW([p], capturable=saved, min_8bit_size=1)
+    opt._init_state(p)["step"] += 7
+    other = optim.AdamW([torch.nn.Parameter(torch.zeros(300))], capturable=here, min_8bit_size=1)
+    other.load_state_dict(opt.state_dict())
+    (state,) = other.state.values()
+    assert state["step"] == 7 and isinstance(state["step"], torch.Tensor if here else int)
+    if here:
+        assert state["step"].dtype == torch.int64 and state["step"] is not opt.state[p]["step"]
+    assert state["exp_avg"].dtype == torch.float8_e4m3fn and opt.state[p]["step"] == 7
