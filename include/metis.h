@@ -391,7 +391,8 @@ metis_status metis_int8_linear(const void *X, int32_t dtype, int64_t tokens, int
  * t: the step, counted from 1: `step`, or where step_count is not NULL the
  * int64 that it points to in device memory when the kernel runs (for graphs;
  * every other value is fixed at the call).
- * A tensor must not appear twice in a call, and tensors must not overlap.
+ * No array that is written may appear twice in a call or overlap another one,
+ * a gradient included; gradients may overlap each other.
  * Small tensors share launches; the tensor list is read before the call
  * returns.
  *

@@ -11,7 +11,6 @@
 #include <algorithm>
 #include <exception>
 #include <string>
-#include <utility>
 #include <vector>
 
 #include "../../include/metis.h"
@@ -85,17 +84,22 @@ void put_states(metis_adamw_tensor& row, const at::Tensor& m, const at::Tensor& 
   row.v_scale = (float*)address(*vs, blocks, device, "scales");
 }
 
-// No two of the written arrays share memory.
+// No two of the written arrays share memory, and no gradient with one of them.
 void check_apart(const metis_adamw_tensor* rows, size_t n) {
-  std::vector<std::pair<const char*, const char*>> used;
-  used.reserve(5 * n);
-  auto add = [&](const void* p, int64_t bytes) {
-    if (bytes) used.emplace_back((const char*)p, (const char*)p + bytes);
+  struct Span {
+    uintptr_t begin, end;
+    bool written;
+  };
+  std::vector<Span> used;
+  used.reserve(6 * n);
+  auto add = [&](const void* p, int64_t bytes, bool written = true) {
+    if (bytes) used.push_back({(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, written});
   };
   for (size_t i = 0; i < n; ++i) {
     const metis_adamw_tensor& r = rows[i];
     const int64_t state = r.state_bits == 8 ? r.n : 4 * r.n;
     add(r.param, r.n * (r.param_dtype == METIS_F32 ? 4 : 2));
+    add(r.grad, r.n * (r.grad_dtype == METIS_F32 ? 4 : 2), false);
     add(r.m, state);
     add(r.v, state);
     if (r.state_bits == 8) {
@@ -103,10 +107,14 @@ void check_apart(const metis_adamw_tensor* rows, size_t n) {
       add(r.v_scale, (r.n + kStateBlock - 1) / kStateBlock * 4);
     }
   }
-  std::sort(used.begin(), used.end());
-  for (size_t i = 1; i < used.size(); ++i)
-    if (used[i].first < used[i - 1].second)
-      refuse(PyExc_ValueError, "a parameter or a state appears twice, or two of them overlap");
+  std::sort(used.begin(), used.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t read_end = 0, written_end = 0;  // the farthest ends so far
+  for (const Span& s : used) {
+    if (s.begin < written_end || (s.written && s.begin < read_end))
+      refuse(PyExc_ValueError, "a parameter or a state appears twice, or two of them (or one and a gradient) overlap");
+    uintptr_t& end = s.written ? written_end : read_end;
+    end = std::max(end, s.end);
+  }
 }
 
 uint32_t default_tag(int64_t i) { return (uint32_t)(i & 0xFFFF) << 16 | (uint32_t)METIS_OPERAND_W << 12; }

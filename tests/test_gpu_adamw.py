@@ -294,6 +294,24 @@ def test_lists_are_checked():
     assert bool((a == -1).all()) and not buf[100:].any()
 
 
+def test_gradients_may_share_memory_but_not_with_what_is_written():
+    buf = torch.zeros(300, device="cuda")
+    new = lambda n=1: [torch.zeros(100, device="cuda") for _ in range(n)]  # noqa: E731
+    before = buf.clone()
+    for g, p, m, v in ((buf[50:150], buf[:100], new(), new()), (buf[:100], buf[:100], new(), new()),
+                       (buf[50:150], torch.zeros(100, device="cuda"), [buf[100:200]], new()),
+                       (buf[199:299], torch.zeros(100, device="cuda"), new(), [buf[100:200]]),
+                       (buf[:100].view(torch.bfloat16)[100:], buf[50:150], new(), new())):
+        with pytest.raises(ValueError, match="overlap"):
+            metis.adamw_step([p], [g[:100]], m, v, lr=1.0, step=1)
+    torch.cuda.synchronize()
+    assert torch.equal(buf, before)
+    p, buf[:] = new(2), 1.0
+    metis.adamw_step([*p, buf[200:]], [buf[:100], buf[50:150], buf[100:200]], new(3), new(3), lr=1.0, step=1)
+    metis.status_sync()
+    assert all(bool((x == -1).all()) for x in p) and not buf[200:].any() and bool((buf[:200] == 1).all())
+
+
 # ----------------------------------------------------------- the optimizer --
 
 def _params(seed=0, sizes=((50, 90), (90,), (64, 64), (1,))):
