@@ -550,7 +550,7 @@ _NO_SWITCH = _NoSwitch()
 
 def _device_context(device):
     """Context in which GPU ``device`` is current."""
-    return _NO_SWITCH if device == torch.cuda.current_device() else torch.cuda.device(device)
+    return _NO_SWITCH if device == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _on_device(*tensors):
@@ -584,7 +584,7 @@ def int8_pitch(k_len):
 
 
 def _raw_stream():
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 class I8:
@@ -619,7 +619,11 @@ class I8:
             raise ValueError("codes must be a contiguous int8 matrix of %d x %d" % (self.outer, int8_pitch(self.k_len)))
         if scales.dtype != torch.float32 or scales.shape != (self.outer,) or not scales.is_contiguous():
             raise ValueError("scales must be %d contiguous float32 values" % self.outer)
-        return _I8(codes.data_ptr(), scales.data_ptr(), self.outer, self.k_len)
+        return self._new_c()
+
+    def _new_c(self):
+        """_c() of an operand just made, which needs no checks."""
+        return _I8(self.codes.data_ptr(), self.scales.data_ptr(), self.outer, self.k_len)
 
 
 class I8Operand:
@@ -643,18 +647,21 @@ def int8_quantize(M, axes=AXIS1, out=None, rounding=RNE, seed=0, tag=0, step=0, 
     dtype = _dtype_code(M)
     if out is None:
         out = I8Operand(rows, cols, axes, M.device)
-    elif (out.rows, out.cols, out.axes) != (rows, cols, axes):
-        raise ValueError("out holds a %d x %d operand with axes %d, not %d x %d with %d"
-                         % (out.rows, out.cols, out.axes, rows, cols, axes))
-    c0, c1 = (None if q is None else q._c() for q in (out.ax0, out.ax1))
-    parts = [t for q in (out.ax0, out.ax1) if q is not None for t in (q.codes, q.scales)]
+        c0, c1 = out.ax0 and out.ax0._new_c(), out.ax1 and out.ax1._new_c()
+        parts = ()
+    else:
+        if (out.rows, out.cols, out.axes) != (rows, cols, axes):
+            raise ValueError("out holds a %d x %d operand with axes %d, not %d x %d with %d"
+                             % (out.rows, out.cols, out.axes, rows, cols, axes))
+        c0, c1 = out.ax0 and out.ax0._c(), out.ax1 and out.ax1._c()
+        parts = [t for q in (out.ax0, out.ax1) if q for t in (q.codes, q.scales)]
     with _on_device(M, *parts):
         lib = load()
         need = lib.metis_int8_quantize_workspace(rows, cols, axes) if axes & AXIS0 else 0  # rows alone need none
         ws = _space(workspace, need, M.device)
         _check(lib.metis_int8_quantize(M.data_ptr(), dtype, rows, cols, _leading(M), axes, rounding, seed, tag, step,
-                                       None if c0 is None else ctypes.byref(c0),
-                                       None if c1 is None else ctypes.byref(c1), _ptr(ws), need if ws is None else ws.numel(),
+                                       c0 and ctypes.byref(c0),
+                                       c1 and ctypes.byref(c1), _ptr(ws), need if ws is None else ws.numel(),
                                        _raw_stream()))
     return out
 
