@@ -209,16 +209,16 @@ PyObject* fill_grads(PyObject*, PyObject* args) {
 
 PyObject* names[5];  // "step" and the states' keys
 
-// fill_state(params, state, first_tag, same_step, table) -> (device, step,
+// fill_state(params, state, first_tag, counts_on_gpu, table) -> (device, step,
 // states), the optimizer's form: gradients from the parameters, states from
 // the optimizer's dict of dicts.  None where a parameter has no gradient or no
-// state yet, a gradient is not contiguous, or (same_step) the step counts
-// differ: the caller sorts those out and uses fill.
+// state yet, a gradient is not contiguous, or the step counts differ (those on
+// the GPU: are not one tensor): the caller sorts those out and uses fill.
 PyObject* fill_state(PyObject*, PyObject* args) {
   PyObject *params, *state, *buffer;
   long long first;
-  int same_step;
-  if (!PyArg_ParseTuple(args, "OOLpO", &params, &state, &first, &same_step, &buffer)) return nullptr;
+  int counts_on_gpu;
+  if (!PyArg_ParseTuple(args, "OOLpO", &params, &state, &first, &counts_on_gpu, &buffer)) return nullptr;
   return guarded([&]() -> PyObject* {
     if (!PyList_Check(params) || !PyDict_Check(state)) refuse(PyExc_ValueError, "parameters must be a list and state a dict");
     const Py_ssize_t n = PyList_GET_SIZE(params);
@@ -251,7 +251,8 @@ PyObject* fill_state(PyObject*, PyObject* args) {
       if (i == 0) {
         device = device_of(p, "parameters");
         step = v[0];
-      } else if (same_step && v[0] != step) {
+      } else if (v[0] != step) {
+        if (counts_on_gpu) Py_RETURN_NONE;
         const int equal = PyObject_RichCompareBool(v[0], step, Py_EQ);
         if (equal < 0) return nullptr;
         if (!equal) Py_RETURN_NONE;

@@ -29,6 +29,9 @@ class AdamW(torch.optim.Optimizer):
     ``capturable``: the step count lives on the GPU, so that a step captured
     into a graph advances it on every replay (lr and the other values are
     those of the capture); every parameter then needs a gradient in every step.
+    Parameters whose counts are equal share one count tensor, and each of a
+    group's count tensors takes a call of its own; to set one parameter's count
+    by hand, give its state a new tensor.
 
     Elements whose update is not finite are left as they are, and the next
     ``metis.status_sync`` reports it.  Parameters are float32 or bfloat16, on
@@ -54,11 +57,13 @@ class AdamW(torch.optim.Optimizer):
         self.grad_norm = None
         self._clip = None
 
-    def _init_state(self, p):
+    def _init_state(self, p, count=None):
+        """A new state; ``count``: the step count tensor it shares, if any."""
+        if count is None:
+            count = torch.zeros((), dtype=torch.int64, device=p.device) if self.capturable else 0
         eight = self.state_bits == 8 and p.numel() >= self.min_8bit_size
         m, v, ms, vs = metis.adamw_state(p.numel(), 8 if eight else 32, p.device)
-        state = {"step": torch.zeros((), dtype=torch.int64, device=p.device) if self.capturable else 0,
-                 "exp_avg": m.view(p.shape), "exp_avg_sq": v.view(p.shape)}
+        state = {"step": count, "exp_avg": m.view(p.shape), "exp_avg_sq": v.view(p.shape)}
         if eight:
             state.update(exp_avg_scale=ms, exp_avg_sq_scale=vs)
         self.state[p] = state
@@ -78,7 +83,7 @@ class AdamW(torch.optim.Optimizer):
         for group in self.param_groups:
             params = group["params"]
             table = metis._table(len(params))
-            found = ext.fill_state(params, self.state, first, not self.capturable, table)
+            found = ext.fill_state(params, self.state, first, self.capturable, table)
             if found is not None:
                 calls.append((group, table, *found, None))
             else:
@@ -95,10 +100,10 @@ class AdamW(torch.optim.Optimizer):
             whole = calls[0][1] if len(calls) == 1 else metis.np.concatenate([c[1] for c in calls])
             metis._grad_norm_run(whole, device, self.max_norm, self._clip)
             self.grad_norm, clip = self._clip[0], self._clip[1]
+        if self.capturable:
+            torch._foreach_add_(list({id(c[3]): c[3] for c in calls}.values()), 1)
         for group, table, device, count, states, _ in calls:
-            if self.capturable:
-                torch._foreach_add_([s["step"] for s in states], 1)
-            else:
+            if not self.capturable:
                 count += 1
             metis._adamw_run(table, device, group["lr"], group["betas"], group["eps"], group["weight_decay"], count, clip,
                              self.rounding, self.seed)
@@ -110,20 +115,23 @@ class AdamW(torch.optim.Optimizer):
     def _sorted_calls(self, group, first, capturing):
         """A group's calls where its parameters are not all alike: without a
         gradient (left out), without a state (made), with a gradient to be
-        copied into rows, or with step counts of their own (a call each)."""
+        copied into rows, or with step counts of their own (a call each; counts
+        on the GPU are told apart as tensors, their values stay there)."""
         have = [(first + i, p) for i, p in enumerate(group["params"]) if p.grad is not None]
         if self.capturable and len(have) != len(group["params"]):
             raise RuntimeError("with capturable=True every parameter needs a gradient")
         new = [p for _, p in have if not self.state[p]]
         if new and capturing:
             raise RuntimeError("take one AdamW step before the capture: the states' first zeros would be captured")
+        count = torch.zeros((), dtype=torch.int64, device=new[0].device) if new and self.capturable else None
         for p in new:
-            self._init_state(p)
+            self._init_state(p, count)
+        sets = {}
+        for i, p in have:
+            count = self.state[p]["step"]
+            sets.setdefault(id(count) if self.capturable else count, []).append((i, p))
         calls = []
-        for count in [None] if self.capturable else sorted({self.state[p]["step"] for _, p in have}):
-            some = [(i, p) for i, p in have if count is None or self.state[p]["step"] == count]
-            if not some:
-                continue
+        for _, some in sets.items() if self.capturable else sorted(sets.items()):
             params, states = [p for _, p in some], [self.state[p] for _, p in some]
             grads = [p.grad.contiguous() for p in params]
             table = metis._table(len(params))
@@ -147,6 +155,7 @@ class AdamW(torch.optim.Optimizer):
         super().load_state_dict(state_dict)
         saved = {i: p for group, here in zip(state_dict["param_groups"], self.param_groups)
                  for i, p in zip(group["params"], here["params"])}
+        counts = {}
         for i, state in state_dict["state"].items():
             if i in saved:
                 p = saved[i]
@@ -154,6 +163,9 @@ class AdamW(torch.optim.Optimizer):
                                  for k, v in state.items()}
                 step = self.state[p].get("step")
                 if self.capturable and step is not None:
-                    self.state[p]["step"] = torch.as_tensor(step, dtype=torch.int64, device=p.device)
+                    key = (p.device, int(step))  # equal counts: one tensor
+                    if key not in counts:
+                        counts[key] = torch.tensor(key[1], dtype=torch.int64, device=p.device)
+                    self.state[p]["step"] = counts[key]
                 elif isinstance(step, torch.Tensor):
                     self.state[p]["step"] = int(step)

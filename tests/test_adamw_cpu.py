@@ -1,0 +1,95 @@
+"""The optimizer's host side (no GPU work): the library's calls are recorded
+in place of being run."""
+
+import types
+
+import pytest
+import torch
+
+from spectral_split_quantized_amd import metis, optim
+
+
+@pytest.fixture
+def runs(monkeypatch):
+    """Per call of the step: (its parameters, its number, the number's tensor or None)."""
+    calls, filled = [], []
+
+    def fill(params, *rest):
+        filled.append((rest[-1], params))
+        return 0
+
+    def run(table, device, lr, betas, eps, weight_decay, step, *_):
+        (params,) = [p for t, p in filled if t is table]
+        calls.append((params, int(step), step if isinstance(step, torch.Tensor) else None))
+
+    ext = types.SimpleNamespace(fill=fill, fill_state=lambda *a: None)
+    monkeypatch.setattr(metis, "_tensors", lambda: ext)
+    monkeypatch.setattr(metis, "_adamw_run", run)
+    return calls
+
+
+def _params(n, grads=True):
+    ps = [torch.nn.Parameter(torch.zeros(4)) for _ in range(n)]
+    for p in ps:
+        p.grad = torch.ones(4) if grads else None
+    return ps
+
+
+def _taken(runs):
+    """{parameter: step's number} of the recorded calls."""
+    return {p: t for params, t, _ in runs for p in params}
+
+
+@pytest.mark.parametrize("saved", [False, True])
+def test_loaded_counts_that_differ_are_stepped_each_by_its_own(runs, saved):
+    """A parameter without a gradient in some steps has a count of its own,
+    also after loading into an optimizer whose counts are on the GPU."""
+    src = optim.AdamW(_params(3), capturable=saved)
+    for p, t in zip(src.param_groups[0]["params"], (1000, 3, 1000)):
+        src._init_state(p)["step"] = torch.tensor(t) if saved else t
+    ps = _params(3)
+    opt = optim.AdamW(ps, capturable=True)
+    opt.load_state_dict(src.state_dict())
+    for t in (1, 2):
+        runs.clear()
+        opt.step()
+        taken = _taken(runs)
+        assert [taken[p] for p in ps] == [1000 + t, 3 + t, 1000 + t] and len(runs) == 2
+        assert [int(opt.state[p]["step"]) for p in ps] == [1000 + t, 3 + t, 1000 + t]
+        for params, _, count in runs:  # the tensor that a replay reads is the one that the state shows
+            assert all(opt.state[p]["step"] is count for p in params)
+
+
+def test_a_parameter_that_joins_late_starts_at_its_own_first_step(runs):
+    ps = _params(3)
+    opt = optim.AdamW(ps[:2], capturable=True)
+    opt.step()
+    opt.step()
+    opt.add_param_group({"params": ps[2:]})
+    runs.clear()
+    opt.step()
+    assert [_taken(runs)[p] for p in ps] == [3, 3, 1]
+    # in one group: a state dict that lacks a parameter
+    state = opt.state_dict()
+    del state["state"][1]
+    ps = _params(3)
+    other = optim.AdamW([{"params": ps[:2]}, {"params": ps[2:]}], capturable=True)
+    other.load_state_dict(state)
+    runs.clear()
+    other.step()
+    assert [_taken(runs)[p] for p in ps] == [4, 1, 2]
+
+
+def test_equal_counts_are_one_tensor_advanced_once(runs):
+    """One call for all, over groups too, and a count shared by two groups goes up by one."""
+    ps = _params(4)
+    opt = optim.AdamW([{"params": ps[:2]}, {"params": ps[2:]}], capturable=True)
+    opt.step()
+    assert len(runs) == 2
+    again = optim.AdamW([{"params": ps[:2]}, {"params": ps[2:]}], capturable=True)
+    again.load_state_dict(opt.state_dict())
+    assert len({id(s["step"]) for s in again.state.values()}) == 1
+    runs.clear()
+    again.step()
+    assert len(runs) == 2 and all(int(s["step"]) == 2 for s in again.state.values())
+    assert all(int(s["step"]) == 1 for s in opt.state.values())  # loading takes copies
