@@ -14,7 +14,8 @@ stochastically: with d the 20 fraction bits that binary32 has beyond E4M3's
 three (of y + 2**-6 below 2**-6, where the grid is 2**-9), the code goes up iff
 d + 16 h >= 2**20 for the 16-bit draw h.  Draws: element e takes word e & 3 of
 the 32-bit layout (philox.words) with role 6, the low half for m and the high
-half for sqrt(v).  A positive sqrt(v) never gets code 0.
+half for sqrt(v).  A positive sqrt(v) never gets code 0.  A value that is not
+finite gets the code of NaN and has no part in its block's scale.
 """
 
 import numpy as np
@@ -59,6 +60,8 @@ def _grid():
 def encode(x, h=None, positive=False):
     """(codes uint8, scales float32) of x, nearest or with 16-bit draws h."""
     x = np.asarray(x, np.float32)
+    nan = ~np.isfinite(x)
+    x = np.where(nan, np.float32(0), x)
     s = scales(x)
     y = np.abs(x).astype(np.float64) / np.repeat(s.astype(np.float64), BLOCK)[:len(x)]
     grid = _grid()
@@ -76,7 +79,7 @@ def encode(x, h=None, positive=False):
         d = np.round(frac * 2 ** 20).astype(np.int64)         # exact: 20 bits
         c = lo + (d + 16 * np.asarray(h, np.int64) >= 2 ** 20)
         c = np.where(y < 2.0 ** -6, c - 8, c)
-    c = c.astype(np.uint8)
+    c = np.where(nan, 0x7F, c).astype(np.uint8)
     if positive:
         return np.where((x != 0) & (c == 0), 1, c).astype(np.uint8), s
     return (c | np.where(x < 0, 0x80, 0)).astype(np.uint8), s
@@ -85,8 +88,11 @@ def encode(x, h=None, positive=False):
 def decode(codes, s):
     """The binary32 values of codes with their blocks' scales."""
     codes = np.asarray(codes, np.uint8)
-    v = formats.e4m3_decode(codes & 0x7F) * np.where(codes & 0x80, -1.0, 1.0)
-    return (v * np.repeat(np.asarray(s, np.float64), BLOCK)[:len(codes)]).astype(np.float32)
+    nan = codes & 0x7F == 0x7F
+    v = formats.e4m3_decode(np.where(nan, 0, codes & 0x7F)) * np.where(codes & 0x80, -1.0, 1.0)
+    with np.errstate(invalid="ignore"):  # a scale that is not finite
+        v = v * np.repeat(np.asarray(s, np.float64), BLOCK)[:len(codes)]
+    return np.where(nan, np.nan, v).astype(np.float32)
 
 
 def draws(n, seed, tag, t, role=ROLE_MOMENTS):

@@ -6,7 +6,8 @@
 //   m' = b1 m + (1 - b1) g,   v' = b2 v + ((1 - b2) g) g,   r' = sqrt(v'),
 //   p' = p (1 - lr wd) - (lr / (1 - b1^t)) m' / (r' / sqrt(1 - b2^t) + eps).
 // An element whose m', v' or p' is not finite keeps p, m and v and raises the
-// numeric flag.
+// numeric flag.  A stored 8-bit moment that is itself not finite stays NaN and
+// has no part in its block's scale.
 //
 // 8-bit states: E4M3 codes of m and of r = sqrt(v) (the square root halves
 // the exponent range that v needs) in blocks of 256 consecutive elements,
@@ -233,6 +234,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable<EIGHT> t) {
       }
     }
     bool ok = true;
+    uint32_t nan_m = 0, nan_r = 0;  // codes of moments that stay NaN
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float gr = t.clip ? g[b][i] * gs : g[b][i];
@@ -253,8 +255,12 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable<EIGHT> t) {
         bad |= i < cnt[b];
         m1[i] = m[b][i];
         v1[i] = v[b][i];
-        r1[i] = EIGHT ? r[i] : 0.0f;
+        r1[i] = EIGHT ? fabsf(r[i]) : 0.0f;
         p1[i] = p[b][i];
+        if constexpr (EIGHT) {  // as zeros they leave the block's maxima to the others
+          if (!is_finite_class(m1[i])) m1[i] = 0.0f, nan_m |= 0x7Fu << (8 * i);
+          if (!is_finite_class(r1[i])) r1[i] = 0.0f, nan_r |= 0x7Fu << (8 * i);
+        }
       }
     }
     uint32_t am = 0, ar = 0;
@@ -299,8 +305,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable<EIGHT> t) {
         wm |= (cm | (m[b][i] < 0.0f ? 0x80u : 0u)) << (8 * i);
         wr |= cr << (8 * i);
       }
-      store_codes4((uint8_t*)mp, e, cnt[b], vec, wm);
-      store_codes4((uint8_t*)vp, e, cnt[b], vec, wr);
+      store_codes4((uint8_t*)mp, e, cnt[b], vec, wm | nan_m);
+      store_codes4((uint8_t*)vp, e, cnt[b], vec, wr | nan_r);
       if (lane == 0) {
         t.ms[ti][block0 + b] = pow2_float(em);
         t.vs[ti][block0 + b] = pow2_float(er);

@@ -3,9 +3,11 @@ in place of being run."""
 
 import types
 
+import numpy as np
 import pytest
 import torch
 
+from oracle import adamw
 from spectral_split_quantized_amd import metis, optim
 
 
@@ -93,3 +95,16 @@ def test_equal_counts_are_one_tensor_advanced_once(runs):
     again.step()
     assert len(runs) == 2 and all(int(s["step"]) == 2 for s in again.state.values())
     assert all(int(s["step"]) == 1 for s in opt.state.values())  # loading takes copies
+
+
+def test_oracle_keeps_values_that_are_not_finite_out_of_the_scale():
+    x = np.linspace(0.1, 1.0, 300).astype(np.float32)
+    want, s = adamw.encode(x)
+    for bad in (np.nan, np.inf, -np.inf):
+        y = x.copy()
+        y[[3, 280]] = bad
+        codes, scales = adamw.encode(y)
+        good = np.setdiff1d(np.arange(300), [3, 280])
+        assert np.array_equal(scales, s) and np.array_equal(codes[good], want[good])
+        d = adamw.decode(codes, scales)
+        assert np.isnan(d[[3, 280]]).all() and np.isfinite(d[good]).all()

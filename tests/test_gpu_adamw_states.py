@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import adamw
 from spectral_split_quantized_amd import metis, optim
 
 from gpu_helpers import say
@@ -76,3 +77,76 @@ def test_counts_that_differ_in_a_captured_step(bits):
         check()
     assert [int(opt.state[p]["step"]) for p in ps] == [9, 7, 9]
     metis.status_sync()
+
+
+BETAS, EPS = (0.9, 0.999), 1e-8
+
+
+class Eight:
+    """One tensor with 8-bit states that hold given moments."""
+
+    def __init__(self, n, seed):
+        rng = np.random.default_rng(seed)
+        rnd = lambda s: (rng.standard_normal(n) * s * np.exp(rng.standard_normal(n))).astype(np.float32)  # noqa: E731
+        self.p, self.g = torch.from_numpy(rnd(0.02)).cuda(), torch.from_numpy(rnd(1e-3)).cuda()
+        (m, ms), (v, vs) = adamw.encode(rnd(1e-3)), adamw.encode(np.abs(rnd(1e-3)), positive=True)
+        self.m, self.v = (torch.from_numpy(c).cuda().view(torch.float8_e4m3fn) for c in (m, v))
+        self.ms, self.vs = torch.from_numpy(ms).cuda(), torch.from_numpy(vs).cuda()
+
+    def codes(self):
+        return [t.view(torch.uint8).cpu().numpy() for t in (self.m, self.v)]
+
+    def scales(self):
+        return [t.cpu().numpy() for t in (self.ms, self.vs)]
+
+    def expect(self, bad, t, rounding, seed):
+        """(m codes, scales), (r codes, scales) after a step in which the
+        elements ``bad`` keep their moments."""
+        (mc, vc), (ms, vs) = self.codes(), self.scales()
+        m, r = adamw.decode(mc, ms), adamw.decode(vc, vs)
+        with np.errstate(all="ignore"):
+            m1, _, r1 = adamw.moments(self.g.cpu().numpy(), m, r * r, *BETAS)
+        m1[bad], r1[bad] = m[bad], np.abs(r[bad])
+        lo, hi = adamw.draws(len(m), seed, metis.make_tag(0, metis.OPERAND_W), t) if rounding == "sr" else (None, None)
+        return adamw.encode(m1, lo), adamw.encode(r1, hi, True)
+
+    def step(self, t, rounding, seed):
+        metis.adamw_step([self.p], [self.g], [self.m], [self.v], [self.ms], [self.vs], lr=1e-2, betas=BETAS, eps=EPS, step=t,
+                         rounding=metis.SR if rounding == "sr" else metis.RNE, seed=seed)
+
+    def check(self, want):
+        (mc, vc), (ms, vs) = self.codes(), self.scales()
+        assert np.array_equal(ms, want[0][1]) and np.array_equal(vs, want[1][1])
+        assert np.array_equal(mc, want[0][0]) and np.array_equal(vc, want[1][0])
+
+
+def _reported():
+    with pytest.raises(metis.MetisError) as ei:
+        metis.status_sync()
+    assert ei.value.status == metis.E_NUMERIC
+
+
+@pytest.mark.parametrize("rounding", ["rne", "sr"])
+def test_stored_nan_stays_in_its_element(rounding):
+    """NaN codes in a state, a NaN, an infinite and a negative r in damaged
+    blocks: the elements keep what they had, their neighbours go on."""
+    say("adamw, NaN in stored states, %s" % rounding)
+    s = Eight(1500, 3)
+    s.m.view(torch.uint8)[5], s.m.view(torch.uint8)[6] = 0x7F, 0xFF      # NaN in m
+    s.v.view(torch.uint8)[300] = 0x7F                                    # NaN in r
+    s.ms[2], s.vs[3] = float("nan"), float("inf")                        # a block of each
+    s.v.view(torch.uint8)[1030] |= 0x80                                  # a negative r whose update is not finite
+    s.g[1030] = float("nan")
+    bad = np.array([5, 6, 300, *range(512, 1024), 1030])
+    before = s.p.clone()
+    for t in (1, 2):
+        want = s.expect(bad, t, rounding, 9)
+        s.step(t, rounding, 9)
+        _reported()
+        s.check(want)
+    assert torch.equal(s.p[bad], before[bad])
+    good = np.setdiff1d(np.arange(1500), bad)
+    assert bool((s.p[good] != before[good]).all()) and bool(torch.isfinite(s.p).all())
+    mc, vc = s.codes()
+    assert set(np.flatnonzero(mc & 0x7F == 0x7F)) == {5, 6, *range(512, 768)}
+    assert set(np.flatnonzero(vc & 0x7F == 0x7F)) == {300, *range(768, 1024)}
