@@ -373,7 +373,9 @@ metis_status metis_int8_linear(const void *X, int32_t dtype, int64_t tokens, int
  *   m' = b1 m + (1 - b1) g,  v' = b2 v + ((1 - b2) g) g,  r' = sqrt(v'),
  *   p' = p (1 - lr wd) - lr / (1 - b1^t) * m' / (r' / sqrt(1 - b2^t) + eps).
  * An element for which m', v' or p' is not finite keeps p, m and v and sets
- * the numeric flag of metis_status_sync.  A stored 8-bit moment that is itself
+ * the numeric flag of metis_status_sync.  8-bit moments are kept as values and
+ * encoded again with their block's new scale (a larger neighbour coarsens them;
+ * a kept r above zero stays above zero).  A stored 8-bit moment that is itself
  * not finite stays NaN; the other elements of its block go on.
  *
  * metis_adamw_tensor: n elements, contiguous; param binary32 (METIS_F32) or

@@ -6,8 +6,9 @@
 //   m' = b1 m + (1 - b1) g,   v' = b2 v + ((1 - b2) g) g,   r' = sqrt(v'),
 //   p' = p (1 - lr wd) - (lr / (1 - b1^t)) m' / (r' / sqrt(1 - b2^t) + eps).
 // An element whose m', v' or p' is not finite keeps p, m and v and raises the
-// numeric flag.  A stored 8-bit moment that is itself not finite stays NaN and
-// has no part in its block's scale.
+// numeric flag.  8-bit moments are kept as values, which are encoded again: the
+// block has one scale, and its other elements move it.  A stored 8-bit moment
+// that is itself not finite stays NaN and has no part in its block's scale.
 //
 // 8-bit states: E4M3 codes of m and of r = sqrt(v) (the square root halves
 // the exponent range that v needs) in blocks of 256 consecutive elements,

@@ -33,8 +33,9 @@ class AdamW(torch.optim.Optimizer):
     group's count tensors takes a call of its own; to set one parameter's count
     by hand, give its state a new tensor.
 
-    Elements whose update is not finite are left as they are, and the next
-    ``metis.status_sync`` reports it.  Parameters are float32 or bfloat16, on
+    Elements whose update is not finite are left as they are (8-bit moments are
+    encoded again with their block's scale, which the other elements may have
+    raised), and the next ``metis.status_sync`` reports it.  Parameters are float32 or bfloat16, on
     one GPU and contiguous."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=8,

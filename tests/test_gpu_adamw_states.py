@@ -150,3 +150,23 @@ def test_stored_nan_stays_in_its_element(rounding):
     mc, vc = s.codes()
     assert set(np.flatnonzero(mc & 0x7F == 0x7F)) == {5, 6, *range(512, 768)}
     assert set(np.flatnonzero(vc & 0x7F == 0x7F)) == {300, *range(768, 1024)}
+
+
+@pytest.mark.parametrize("rounding", ["rne", "sr"])
+def test_kept_moments_are_encoded_with_the_blocks_new_scale(rounding):
+    """Gradients that are not finite beside one that raises the block's scales
+    by many powers of two: every code and scale as the definition has it."""
+    say("adamw, kept moments beside a new maximum, %s" % rounding)
+    s = Eight(1100, 4)
+    bad = np.array([0, 7, 255, 260, 700, 1099])
+    s.g[bad] = torch.tensor([float("nan"), float("inf"), float("-inf"), 1e30, float("nan"), -1e25], device="cuda")
+    s.g[20], s.g[300], s.g[1090] = 0.5, 30.0, -4.0
+    before, kept = s.p.clone(), [c[bad] for c in s.codes()]
+    want = s.expect(bad, 7, rounding, 11)
+    assert any((w[0][bad] != k).any() for w, k in zip(want, kept))  # the case is met
+    s.step(7, rounding, 11)
+    _reported()
+    s.check(want)
+    assert torch.equal(s.p[bad], before[bad])
+    r = adamw.decode(s.codes()[1], s.scales()[1])
+    assert ((r[bad] > 0) == (kept[1] > 0)).all()
