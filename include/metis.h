@@ -329,6 +329,10 @@ metis_status metis_mxfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, c
  * axes) bytes, 16-byte aligned.  rows == 0 or cols == 0 returns METIS_OK with
  * nothing enqueued.
  *
+ * metis_int8_quantize_counted: the same with the step read from the int64 at
+ * step_count in device memory when the kernels run (for graphs, whose replays
+ * would otherwise all take the draws of one step).
+ *
  * metis_int8_gemm: C = diag(s_A) (A B^T) diag(s_B), row-major with leading
  * dimension ldc >= B->n_outer, binary32 or bf16 (c_dtype).  A and B have the
  * same k_len, at most 131071 (METIS_E_UNSUPPORTED above): sums are exact in
@@ -359,6 +363,10 @@ metis_status metis_int8_quantize(const void *M, int32_t dtype, int64_t rows, int
                                  int32_t axes, int32_t rounding, uint64_t seed, uint32_t tag, int64_t step,
                                  const metis_i8 *ax0, const metis_i8 *ax1, void *ws, size_t ws_bytes,
                                  void *stream);
+metis_status metis_int8_quantize_counted(const void *M, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                                         int32_t axes, int32_t rounding, uint64_t seed, uint32_t tag,
+                                         const int64_t *step_count, const metis_i8 *ax0, const metis_i8 *ax1,
+                                         void *ws, size_t ws_bytes, void *stream);
 size_t metis_int8_gemm_workspace(int64_t M, int64_t N, int64_t k_len);
 metis_status metis_int8_gemm(const metis_i8 *A, const metis_i8 *B, void *C, int32_t c_dtype, int64_t ldc,
                              void *ws, size_t ws_bytes, void *stream);

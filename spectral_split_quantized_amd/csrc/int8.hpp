@@ -42,6 +42,9 @@ struct I8QuantParams {
   int sr;
   uint64_t seed;
   uint32_t tag, step;
+  const int64_t* step_count;  // the step in device memory, or null: `step`
+
+  __device__ uint32_t step_now() const { return step_count ? (uint32_t)*step_count : step; }
 };
 
 __device__ inline float i8_scale(float amax) { return fmaxf(__fdiv_rn(amax, 127.0f), 0x1p-126f); }
@@ -137,15 +140,15 @@ struct I8Raw8 {
 
 // draws (times 2^-16) of the row-major positions e .. e + 7: the halves of one
 // Philox block, or of two where e is no multiple of 8
-__device__ inline void i8_draws8(const I8QuantParams& p, uint64_t e, float (&u)[8]) {
-  const Philox4 b0 = philox_block(e >> 3, p.tag, p.step, p.seed);
+__device__ inline void i8_draws8(const I8QuantParams& p, uint32_t step, uint64_t e, float (&u)[8]) {
+  const Philox4 b0 = philox_block(e >> 3, p.tag, step, p.seed);
   const uint32_t o = (uint32_t)(e & 7);
   if (o == 0) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) u[i] = (float)philox_half_of(b0, i) * 0x1p-16f;
     return;
   }
-  const Philox4 b1 = philox_block((e >> 3) + 1, p.tag, p.step, p.seed);
+  const Philox4 b1 = philox_block((e >> 3) + 1, p.tag, step, p.seed);
   uint32_t h[16];
 #pragma unroll
   for (int i = 0; i < 8; ++i) h[i] = philox_half_of(b0, i), h[8 + i] = philox_half_of(b1, i);
@@ -209,9 +212,10 @@ __global__ __launch_bounds__(64 * W) void i8_quant_rows_kernel(I8QuantParams p) 
   if (bad) raise_status(kStatusNonFinite);
   const float s = i8_scale(m), inv = i8_inverse(s);
   if (threadIdx.x == 0) p.scales1[row] = s;
+  const uint32_t step = SR ? p.step_now() : 0;
   auto put = [&](int64_t ch, const float (&y)[8]) {
     float u[8];
-    if constexpr (SR) i8_draws8(p, (uint64_t)row * p.cols + ch * 8, u);
+    if constexpr (SR) i8_draws8(p, step, (uint64_t)row * p.cols + ch * 8, u);
     int q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = i8_code<SR>(y[i], inv, SR ? u[i] : 0.0f);
@@ -369,6 +373,7 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
   for (int j = 0; j < 8; ++j) inv0[j] = inv[0][cc * 8 + j];
   const int64_t off1 = rg * 4 * pitch1 + cc * 8;
   uint64_t e = (uint64_t)(r0 + rg * 4) * p.cols + c0 + cc * 8;
+  const uint32_t step = SR ? p.step_now() : 0;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     int w[8][4];
@@ -378,7 +383,7 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
       const I8Raw8<BF16>& v = x[half * 4 + i];
       float u[8];
       if constexpr (SR) {
-        i8_draws8(p, e, u);
+        i8_draws8(p, step, e, u);
         e += i < 3 ? p.cols : 61 * p.cols;
       }
 #pragma unroll

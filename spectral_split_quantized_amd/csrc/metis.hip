@@ -1179,14 +1179,15 @@ void launch_int8_rows(const I8QuantParams& q, hipStream_t st) {
 }
 
 metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols, int64_t ld, int axes, int rounding,
-                            uint64_t seed, uint32_t tag, int64_t step, const metis_i8* ax0, const metis_i8* ax1,
-                            const I8Ws& w, hipStream_t st) {
+                            uint64_t seed, uint32_t tag, int64_t step, const int64_t* step_count, const metis_i8* ax0,
+                            const metis_i8* ax1, const I8Ws& w, hipStream_t st) {
   I8QuantParams q = int8_input(M, dtype, rows, cols, ld);
   if (axes & METIS_AXIS0) q.codes0 = ax0->codes, q.scales0 = ax0->scales;
   if (axes & METIS_AXIS1) q.codes1 = ax1->codes, q.scales1 = ax1->scales;
   q.part0 = w.part0, q.part1 = w.part1;
   q.sr = rounding == METIS_SR;
   q.seed = seed, q.tag = tag_with_role(tag, kRoleResid), q.step = (uint32_t)step;
+  q.step_count = step_count;
   if (axes == METIS_AXIS1) {
     if (q.sr) launch_int8_rows<true>(q, st);
     else launch_int8_rows<false>(q, st);
@@ -1206,6 +1207,35 @@ metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols
   else hipLaunchKernelGGL((i8_quant_tile_kernel<false, false>), padded, dim3(256), 0, st, q);
   LAUNCH_CHECK();
   return METIS_OK;
+}
+
+// the step from the host, or (step_count not null) from device memory
+metis_status int8_quantize_at(const void* M, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int32_t axes,
+                              int32_t rounding, uint64_t seed, uint32_t tag, int64_t step,
+                              const int64_t* step_count, const metis_i8* ax0, const metis_i8* ax1, void* ws,
+                              size_t ws_bytes, void* stream) {
+  if (!dtype_ok(dtype)) return fail(METIS_E_INVALID, "int8_quantize: dtype %d", dtype);
+  if (rows < 0 || cols < 0 || ld < cols)
+    return fail(METIS_E_INVALID, "int8_quantize: shape %lld x %lld, ld %lld", (long long)rows, (long long)cols,
+                (long long)ld);
+  if (axes < 1 || axes > (METIS_AXIS0 | METIS_AXIS1)) return fail(METIS_E_INVALID, "int8_quantize: axes %d", axes);
+  if (rounding != METIS_RNE && rounding != METIS_SR) return fail(METIS_E_INVALID, "int8_quantize: rounding %d", rounding);
+  if (step < 0) return fail(METIS_E_INVALID, "int8_quantize: step %lld", (long long)step);
+  metis_status s;
+  if ((axes & METIS_AXIS0) && (s = int8_check(ax0, "int8_quantize: ax0", cols, rows)) != METIS_OK) return s;
+  if ((axes & METIS_AXIS1) && (s = int8_check(ax1, "int8_quantize: ax1", rows, cols)) != METIS_OK) return s;
+  if (rows == 0 || cols == 0) return METIS_OK;
+  if (!M) return fail(METIS_E_INVALID, "int8_quantize: null input");
+  if (rows > INT32_MAX || cols > INT32_MAX || i8_pitch(rows) / kI8Tile * (i8_pitch(cols) / kI8Tile) > INT32_MAX)
+    return fail(METIS_E_UNSUPPORTED, "int8_quantize: %lld x %lld", (long long)rows, (long long)cols);
+  Carver cv(ws, ws_bytes);
+  const I8Ws w = carve_int8(cv, rows, cols, axes);
+  if (cv.used() > 0 && (!ws || cv.used() > ws_bytes))
+    return fail(METIS_E_WORKSPACE, "workspace %zu < %zu", ws_bytes, cv.used());
+  if (cv.used() > 0 && ((uintptr_t)ws & 15)) return fail(METIS_E_INVALID, "int8_quantize: workspace not 16-byte aligned");
+  if ((s = ensure_device_tables()) != METIS_OK) return s;
+  return run_int8_quant(M, dtype, rows, cols, ld, axes, rounding, seed, tag, step, step_count, ax0, ax1, w,
+                        (hipStream_t)stream);
 }
 
 struct I8LinearWs {
@@ -1738,27 +1768,17 @@ size_t metis_int8_quantize_workspace(int64_t rows, int64_t cols, int32_t axes) {
 metis_status metis_int8_quantize(const void* M, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int32_t axes,
                                  int32_t rounding, uint64_t seed, uint32_t tag, int64_t step, const metis_i8* ax0,
                                  const metis_i8* ax1, void* ws, size_t ws_bytes, void* stream) {
-  if (!dtype_ok(dtype)) return fail(METIS_E_INVALID, "int8_quantize: dtype %d", dtype);
-  if (rows < 0 || cols < 0 || ld < cols)
-    return fail(METIS_E_INVALID, "int8_quantize: shape %lld x %lld, ld %lld", (long long)rows, (long long)cols,
-                (long long)ld);
-  if (axes < 1 || axes > (METIS_AXIS0 | METIS_AXIS1)) return fail(METIS_E_INVALID, "int8_quantize: axes %d", axes);
-  if (rounding != METIS_RNE && rounding != METIS_SR) return fail(METIS_E_INVALID, "int8_quantize: rounding %d", rounding);
-  if (step < 0) return fail(METIS_E_INVALID, "int8_quantize: step %lld", (long long)step);
-  metis_status s;
-  if ((axes & METIS_AXIS0) && (s = int8_check(ax0, "int8_quantize: ax0", cols, rows)) != METIS_OK) return s;
-  if ((axes & METIS_AXIS1) && (s = int8_check(ax1, "int8_quantize: ax1", rows, cols)) != METIS_OK) return s;
-  if (rows == 0 || cols == 0) return METIS_OK;
-  if (!M) return fail(METIS_E_INVALID, "int8_quantize: null input");
-  if (rows > INT32_MAX || cols > INT32_MAX || i8_pitch(rows) / kI8Tile * (i8_pitch(cols) / kI8Tile) > INT32_MAX)
-    return fail(METIS_E_UNSUPPORTED, "int8_quantize: %lld x %lld", (long long)rows, (long long)cols);
-  Carver cv(ws, ws_bytes);
-  const I8Ws w = carve_int8(cv, rows, cols, axes);
-  if (cv.used() > 0 && (!ws || cv.used() > ws_bytes))
-    return fail(METIS_E_WORKSPACE, "workspace %zu < %zu", ws_bytes, cv.used());
-  if (cv.used() > 0 && ((uintptr_t)ws & 15)) return fail(METIS_E_INVALID, "int8_quantize: workspace not 16-byte aligned");
-  if ((s = ensure_device_tables()) != METIS_OK) return s;
-  return run_int8_quant(M, dtype, rows, cols, ld, axes, rounding, seed, tag, step, ax0, ax1, w, (hipStream_t)stream);
+  return int8_quantize_at(M, dtype, rows, cols, ld, axes, rounding, seed, tag, step, nullptr, ax0, ax1, ws, ws_bytes,
+                          stream);
+}
+
+metis_status metis_int8_quantize_counted(const void* M, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                                         int32_t axes, int32_t rounding, uint64_t seed, uint32_t tag,
+                                         const int64_t* step_count, const metis_i8* ax0, const metis_i8* ax1, void* ws,
+                                         size_t ws_bytes, void* stream) {
+  if (!step_count || ((uintptr_t)step_count & 7)) return fail(METIS_E_INVALID, "int8_quantize: step count pointer");
+  return int8_quantize_at(M, dtype, rows, cols, ld, axes, rounding, seed, tag, 0, step_count, ax0, ax1, ws, ws_bytes,
+                          stream);
 }
 
 size_t metis_int8_gemm_workspace(int64_t M, int64_t N, int64_t k_len) {
@@ -1817,7 +1837,7 @@ metis_status metis_int8_linear(const void* X, int32_t dtype, int64_t tokens, int
     LAUNCH_CHECK();
     return METIS_OK;
   }
-  if ((s = run_int8_quant(X, dtype, tokens, W->k_len, ldx, METIS_AXIS1, METIS_RNE, 0, 0, 0, nullptr, &xq, I8Ws{}, st)) !=
+  if ((s = run_int8_quant(X, dtype, tokens, W->k_len, ldx, METIS_AXIS1, METIS_RNE, 0, 0, 0, nullptr, nullptr, &xq, I8Ws{}, st)) !=
       METIS_OK)
     return s;
   return run_int8_gemm(&xq, W, Y, y_dtype, ldy, w.part, st);

@@ -99,14 +99,19 @@ def _rows(x):
     return x if (cols <= 1 or x.stride(1) == 1) and (rows <= 1 or x.stride(0) >= cols) else x.contiguous()
 
 
+def _capturing():
+    return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+
+
 class _Int8LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, mod, record):
         # needs_input_grad says nothing of torch.no_grad(): record is the
         # caller's grad mode (inside a forward it is always off)
         need_x, need_w = (record and need for need in ctx.needs_input_grad[:2])
+        capturing = (need_x or need_w) and _capturing()
         if need_x or need_w:
-            mod._watch(ctx)
+            mod._watch(ctx, capturing)
         # the same orientations as above: X along both axes (Y and dW), W
         # along both (Y and dX); an orientation whose product is not wanted is
         # left out
@@ -115,7 +120,8 @@ class _Int8LinearFn(torch.autograd.Function):
         y = metis.int8_gemm(qx.ax1, qw.ax0, out_dtype=x.dtype)
         ctx.qx, ctx.qw = qx.ax0, qw.ax1
         ctx.lead, ctx.x_dtype, ctx.w_shape = x.shape[:-1], x.dtype, w.shape
-        ctx.rounding, ctx.seed, ctx.tag, ctx.step = mod.rounding, mod.seed, mod.tags["D"], mod.step
+        ctx.rounding, ctx.seed, ctx.tag = mod.rounding, mod.seed, mod.tags["D"]
+        ctx.step = mod._count if capturing and mod._count is not None else mod.step
         return y.reshape(*ctx.lead, w.shape[1])
 
     @staticmethod
@@ -144,10 +150,12 @@ class Int8Linear(torch.nn.Module):
 
     X and W are rounded to nearest, D stochastically (``rounding`` "sr", the
     default, with the draws of ``seed``, ``layer`` and the step that
-    :func:`set_step` sets) or to nearest ("rne").  x is bfloat16 or float32;
-    y and its gradient have x's type, the weight (``in_features x
-    out_features``) and its gradient are float32.  ``frozen()`` gives the
-    serving form, with the weight quantised once."""
+    :func:`set_step` sets) or to nearest ("rne").  Passes captured into a graph
+    read the step on the GPU: set it between replays, on their stream, and a
+    replay takes its draws.  x is bfloat16 or float32; y and its gradient have
+    x's type, the weight (``in_features x out_features``) and its gradient are
+    float32.  ``frozen()`` gives the serving form, with the weight quantised
+    once."""
 
     def __init__(self, in_features, out_features, rounding="sr", seed=0, layer=0, device="cuda", weight=None):
         super().__init__()
@@ -160,27 +168,58 @@ class Int8Linear(torch.nn.Module):
             raise ValueError("weight must be in_features x out_features")
         self.weight = torch.nn.Parameter(weight.to(device=device, dtype=torch.float32).contiguous())
         self.rounding = metis.SR if rounding == "sr" else metis.RNE
-        self.seed, self.step = seed, 0
+        self.seed, self._step, self._count = seed, 0, None
         self.tags = {"D": metis.make_tag(layer, metis.OPERAND_D)}
+        self._make_count()
         self._eager = weakref.WeakSet()  # graphs recorded outside a capture, while they live
 
-    def _watch(self, ctx):
+    @property
+    def step(self):
+        """The training step, which selects the draws."""
+        return self._step
+
+    @step.setter
+    def step(self, step):
+        if self._count is not None:
+            if _capturing():
+                raise RuntimeError("set the step outside the capture: replays read the one that is set then")
+            self._count.fill_(step)
+        self._step = step
+
+    def _make_count(self):
+        # the step on the weight's GPU, for captured passes; the same memory for
+        # as long as the weight stays there
+        if self.rounding != metis.SR or not self.weight.is_cuda:
+            self._count = None
+        elif self._count is None or self._count.device != self.weight.device:
+            with torch.inference_mode(False):
+                self._count = torch.full((), self._step, dtype=torch.int64, device=self.weight.device)
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        self._make_count()
+        return self
+
+    def _watch(self, ctx, capturing):
         """Refuses to record a graph in a capture while one from outside it
         lives: both would accumulate the weight's gradient through one node,
         which belongs to the other's stream, and joining that stream from a
         capture ends the process."""
-        if not torch.cuda.is_available() or not torch.cuda.is_current_stream_capturing():
+        if not capturing:
             self._eager.add(ctx)
         elif len(self._eager):
             raise RuntimeError("a graph of this layer from outside the capture is alive: drop its outputs first")
 
     def __getstate__(self):
         state = super().__getstate__() if hasattr(super(), "__getstate__") else self.__dict__
-        return {k: v for k, v in state.items() if k != "_eager"}
+        return {k: v for k, v in state.items() if k not in ("_eager", "_count")}
 
     def __setstate__(self, state):
+        state = dict(state)
+        state.setdefault("_step", state.pop("step", 0))  # "step": saved before it was on the GPU too
         super().__setstate__(state)
-        self._eager = weakref.WeakSet()
+        self._eager, self._count = weakref.WeakSet(), None
+        self._make_count()
 
     def forward(self, x):
         if x.shape[-1] != self.weight.shape[0]:

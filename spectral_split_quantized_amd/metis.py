@@ -99,6 +99,9 @@ def load():
     lib.metis_int8_quantize.argtypes = [P, i32, i64, i64, i64, i32, i32, ctypes.c_uint64, u32, i64,
                                         ctypes.POINTER(_I8), ctypes.POINTER(_I8), P, sz, P]
     lib.metis_int8_quantize.restype = i32
+    lib.metis_int8_quantize_counted.argtypes = [P, i32, i64, i64, i64, i32, i32, ctypes.c_uint64, u32, P,
+                                                ctypes.POINTER(_I8), ctypes.POINTER(_I8), P, sz, P]
+    lib.metis_int8_quantize_counted.restype = i32
     lib.metis_int8_gemm_workspace.argtypes = [i64, i64, i64]
     lib.metis_int8_gemm_workspace.restype = sz
     lib.metis_int8_gemm.argtypes = [ctypes.POINTER(_I8), ctypes.POINTER(_I8), P, i32, i64, P, sz, P]
@@ -641,10 +644,13 @@ class I8Operand:
 def int8_quantize(M, axes=AXIS1, out=None, rounding=RNE, seed=0, tag=0, step=0, workspace=None):
     """int8 codes and scales of M (metis_int8_quantize) along the requested
     axes, rounded to nearest (RNE) or stochastically (SR, draws from seed, tag
-    and step)."""
+    and step; a one-element int64 tensor is read when the kernels run)."""
     _rows_check(M)
     rows, cols = M.shape
     dtype = _dtype_code(M)
+    counted = isinstance(step, torch.Tensor)
+    if counted and (step.dtype != torch.int64 or step.numel() != 1):
+        raise ValueError("a step count tensor must be one int64")
     if out is None:
         out = I8Operand(rows, cols, axes, M.device)
         c0, c1 = out.ax0 and out.ax0._new_c(), out.ax1 and out.ax1._new_c()
@@ -655,14 +661,14 @@ def int8_quantize(M, axes=AXIS1, out=None, rounding=RNE, seed=0, tag=0, step=0, 
                              % (out.rows, out.cols, out.axes, rows, cols, axes))
         c0, c1 = out.ax0 and out.ax0._c(), out.ax1 and out.ax1._c()
         parts = [t for q in (out.ax0, out.ax1) if q for t in (q.codes, q.scales)]
-    with _on_device(M, *parts):
+    with _on_device(M, *parts, *((step,) if counted else ())):
         lib = load()
         need = lib.metis_int8_quantize_workspace(rows, cols, axes) if axes & AXIS0 else 0  # rows alone need none
         ws = _space(workspace, need, M.device)
-        _check(lib.metis_int8_quantize(M.data_ptr(), dtype, rows, cols, _leading(M), axes, rounding, seed, tag, step,
-                                       c0 and ctypes.byref(c0),
-                                       c1 and ctypes.byref(c1), _ptr(ws), need if ws is None else ws.numel(),
-                                       _raw_stream()))
+        quantize = lib.metis_int8_quantize_counted if counted else lib.metis_int8_quantize
+        _check(quantize(M.data_ptr(), dtype, rows, cols, _leading(M), axes, rounding, seed, tag,
+                        step.data_ptr() if counted else step, c0 and ctypes.byref(c0), c1 and ctypes.byref(c1),
+                        _ptr(ws), need if ws is None else ws.numel(), _raw_stream()))
     return out
 
 

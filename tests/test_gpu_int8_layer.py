@@ -1,0 +1,91 @@
+"""GPU tests of the int8 layer beside its formulas: captured passes and their
+steps.  The passes are defined to the last bit, so comparisons are for
+equality."""
+
+import copy
+
+import pytest
+import torch
+
+from spectral_split_quantized_amd import metis
+from spectral_split_quantized_amd.layer import Int8Linear, set_step
+
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+BOTH = metis.AXIS0 | metis.AXIS1
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need an MI355X; none is visible")
+    metis.load()
+    torch.cuda.set_device(0)
+
+
+@pytest.mark.parametrize("axes", [metis.AXIS0, metis.AXIS1, BOTH])
+def test_quantize_with_a_step_on_the_gpu(axes):
+    say("int8 quantize, step on the GPU, axes %d" % axes)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(130, 333, generator=g, device="cuda")
+    count = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for step in (0, 1, 7, 2 ** 31 + 5):
+        count.fill_(step)
+        a = metis.int8_quantize(x, axes, rounding=metis.SR, seed=3, tag=9, step=count)
+        b = metis.int8_quantize(x, axes, rounding=metis.SR, seed=3, tag=9, step=step)
+        for p, q in ((a.ax0, b.ax0), (a.ax1, b.ax1)):
+            assert (p is None) == (q is None)
+            assert p is None or torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales)
+    metis.status_sync()
+
+
+def test_captured_layer_takes_the_draws_of_the_step_that_is_set():
+    say("int8 layer, replays at different steps")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    lin = Int8Linear(64, 40, weight=torch.randn(64, 40, generator=g, device="cuda"), seed=2, layer=3)
+    x = torch.randn(50, 64, generator=g, device="cuda", requires_grad=True)
+    d = torch.randn(50, 40, generator=g, device="cuda")
+    set_step(lin, 11)
+    lin(x).backward(d)
+    torch.cuda.synchronize()
+    x.grad = lin.weight.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lin(x)
+        y.backward(d)
+        with pytest.raises(RuntimeError, match="outside the capture"):
+            set_step(lin, 12)
+    seen = []
+    for step in (None, 12, 13, 13, 5):  # None: the step that was set before the capture
+        if step is not None:
+            set_step(lin, step)
+        assert lin.step == (11 if step is None else step)
+        x.grad.zero_()
+        lin.weight.grad.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        twin = Int8Linear(64, 40, weight=lin.weight.detach(), seed=2, layer=3)
+        twin.step = lin.step
+        xt = x.detach().clone().requires_grad_(True)
+        yt = twin(xt)
+        yt.backward(d)
+        assert torch.equal(y, yt) and torch.equal(x.grad, xt.grad) and torch.equal(lin.weight.grad, twin.weight.grad)
+        seen.append(x.grad.clone())
+    assert torch.equal(seen[2], seen[3]) and not any(torch.equal(seen[i], seen[j]) for i, j in ((0, 1), (1, 2), (2, 4)))
+    metis.status_sync()
+
+
+def test_step_follows_copies_and_moves():
+    lin = Int8Linear(16, 8)
+    lin.step = 4
+    twin = copy.deepcopy(lin)
+    twin.step = 6
+    moved = Int8Linear(16, 8, device="cpu")
+    moved.step = 9
+    moved = moved.to("cuda").float()
+    assert [(m.step, m._count.item()) for m in (lin, twin, moved)] == [(4, 4), (6, 6), (9, 9)]
+    at = lin._count.data_ptr()  # a captured graph's address
+    assert lin.to("cuda").float()._count.data_ptr() == at
+    assert Int8Linear(16, 8, rounding="rne")._count is None and moved.cpu()._count is None

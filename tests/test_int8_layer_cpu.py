@@ -1,0 +1,41 @@
+"""The int8 layer's and binding's host side (no GPU work)."""
+
+import copy
+import ctypes
+import pickle
+
+import pytest
+import torch
+
+from spectral_split_quantized_amd import metis
+from spectral_split_quantized_amd.layer import Int8Linear
+
+D = ctypes.c_void_p(4096)  # aligned stand-in, never dereferenced
+
+
+def test_step_count_pointer_and_tensor_are_checked():
+    lib = metis.load()
+
+    def counted(count, ax1=True, rounding=1):
+        q = metis._I8(4096, 4096, 64, 48)
+        return lib.metis_int8_quantize_counted(D, 0, 64, 48, 48, 2, rounding, 0, 0, count, None,
+                                               ctypes.byref(q) if ax1 else None, None, 0, None)
+
+    assert counted(None) == metis.E_INVALID and counted(ctypes.c_void_p(4100)) == metis.E_INVALID
+    assert counted(D, ax1=False) == metis.E_INVALID and counted(D, rounding=2) == metis.E_INVALID
+    x = torch.zeros(4, 8)
+    for bad in (torch.zeros(1), torch.zeros(2, dtype=torch.int64), torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="int64"):
+            metis.int8_quantize(x, step=bad)
+
+
+def test_step_survives_copies():
+    lin = Int8Linear(4, 6, device="cpu")
+    lin.step = 5
+    state = lin.__getstate__()
+    state["step"] = state.pop("_step")  # as saved when the step was a plain attribute
+    old = Int8Linear.__new__(Int8Linear)
+    old.__setstate__(state)
+    for m in (copy.deepcopy(lin), pickle.loads(pickle.dumps(lin)), lin.float(), old):
+        assert m.step == 5 and torch.equal(m.weight, lin.weight)
+    assert list(lin.state_dict()) == ["weight"]
