@@ -117,6 +117,12 @@ void check_apart(const metis_adamw_tensor* rows, size_t n) {
   }
 }
 
+// Tells autograd of the write to come, so that a graph that saved the parameter
+// refuses its backward pass.
+void mark_written(const at::Tensor& p) {
+  if (!p.is_inference()) p.unsafeGetTensorImpl()->bump_version();
+}
+
 uint32_t default_tag(int64_t i) { return (uint32_t)(i & 0xFFFF) << 16 | (uint32_t)METIS_OPERAND_W << 12; }
 
 // A writable buffer of n rows.
@@ -183,6 +189,7 @@ PyObject* fill(PyObject*, PyObject* args) {
       }
     }
     check_apart(t.rows, (size_t)n);
+    for (Py_ssize_t i = 0; i < n; ++i) mark_written(tensor(item(params, i), "parameters"));
     return PyLong_FromLong(device);
   });
 }
@@ -267,6 +274,7 @@ PyObject* fill_state(PyObject*, PyObject* args) {
       PyList_SET_ITEM(states, i, s);
     }
     check_apart(t.rows, (size_t)n);
+    for (Py_ssize_t i = 0; i < n; ++i) mark_written(tensor(item(params, i), "parameters"));
     return Py_BuildValue("(iOO)", device, step, states);
   });
 }

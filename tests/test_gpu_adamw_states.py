@@ -170,3 +170,26 @@ def test_kept_moments_are_encoded_with_the_blocks_new_scale(rounding):
     assert torch.equal(s.p[bad], before[bad])
     r = adamw.decode(s.codes()[1], s.scales()[1])
     assert ((r[bad] > 0) == (kept[1] > 0)).all()
+
+
+def test_autograd_sees_the_write():
+    """A graph that saved a parameter refuses its backward pass after a step,
+    as after any write in place."""
+    p = torch.nn.Parameter(torch.ones(5, device="cuda"))
+    opt = optim.AdamW([p], state_bits=32)
+    for _ in range(2):  # the first step makes the states, the second finds them
+        loss = (p * p).sum()
+        p.grad = torch.ones(5, device="cuda")
+        opt.step()
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+    q = torch.ones(5, device="cuda")
+    m, v, _, _ = metis.adamw_state(5, 32)
+    before = q._version
+    metis.adamw_step([q], [torch.ones(5, device="cuda")], [m], [v], lr=0.1, step=1)
+    assert q._version == before + 1
+    with torch.inference_mode():
+        r = torch.ones(5, device="cuda")
+    metis.adamw_step([r], [torch.ones(5, device="cuda")], [m], [v], lr=0.1, step=2)  # has no versions
+    metis.status_sync()
+    assert bool((r < 1).all())
