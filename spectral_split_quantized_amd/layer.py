@@ -99,6 +99,9 @@ def _rows(x):
     return x if (cols <= 1 or x.stride(1) == 1) and (rows <= 1 or x.stride(0) >= cols) else x.contiguous()
 
 
+_EAGER = weakref.WeakSet()  # nodes of Int8Linear recorded outside a capture, while their graphs live
+
+
 def _capturing():
     return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
 
@@ -111,7 +114,7 @@ class _Int8LinearFn(torch.autograd.Function):
         need_x, need_w = (record and need for need in ctx.needs_input_grad[:2])
         capturing = (need_x or need_w) and _capturing()
         if need_x or need_w:
-            mod._watch(ctx, capturing)
+            mod._watch(ctx, (x, w), capturing)
         # the same orientations as above: X along both axes (Y and dW), W
         # along both (Y and dX); an orientation whose product is not wanted is
         # left out
@@ -171,7 +174,6 @@ class Int8Linear(torch.nn.Module):
         self.seed, self._step, self._count = seed, 0, None
         self.tags = {"D": metis.make_tag(layer, metis.OPERAND_D)}
         self._make_count()
-        self._eager = weakref.WeakSet()  # graphs recorded outside a capture, while they live
 
     @property
     def step(self):
@@ -200,25 +202,34 @@ class Int8Linear(torch.nn.Module):
         self._make_count()
         return self
 
-    def _watch(self, ctx, capturing):
+    @property
+    def _eager(self):
+        """This layer's nodes of graphs from outside a capture that live."""
+        return [c for c in _EAGER if c.layer() is self]
+
+    def _watch(self, ctx, inputs, capturing):
         """Refuses to record a graph in a capture while one from outside it
-        lives: both would accumulate the weight's gradient through one node,
-        which belongs to the other's stream, and joining that stream from a
-        capture ends the process."""
+        lives, of this layer or of another with the same weight or input: both
+        would accumulate a leaf's gradient through one node, which belongs to
+        the other's stream, and joining that stream from a capture ends the
+        process.  (A living graph holds its leaves, so their ids are theirs.)"""
+        leaves = {id(t) for t in inputs if t.requires_grad and t.is_leaf}
         if not capturing:
-            self._eager.add(ctx)
-        elif len(self._eager):
-            raise RuntimeError("a graph of this layer from outside the capture is alive: drop its outputs first")
+            ctx.layer, ctx.leaves = weakref.ref(self), leaves
+            _EAGER.add(ctx)
+        elif any(c.layer() is self or not leaves.isdisjoint(c.leaves) for c in _EAGER):
+            raise RuntimeError("a graph of this layer from outside the capture is alive, or one with the same weight or "
+                               "input: drop its outputs first")
 
     def __getstate__(self):
         state = super().__getstate__() if hasattr(super(), "__getstate__") else self.__dict__
-        return {k: v for k, v in state.items() if k not in ("_eager", "_count")}
+        return {k: v for k, v in state.items() if k != "_count"}
 
     def __setstate__(self, state):
         state = dict(state)
         state.setdefault("_step", state.pop("step", 0))  # "step": saved before it was on the GPU too
         super().__setstate__(state)
-        self._eager, self._count = weakref.WeakSet(), None
+        self._count = None
         self._make_count()
 
     def forward(self, x):

@@ -7,7 +7,7 @@ import pickle
 import pytest
 import torch
 
-from spectral_split_quantized_amd import metis
+from spectral_split_quantized_amd import layer, metis
 from spectral_split_quantized_amd.layer import Int8Linear
 
 D = ctypes.c_void_p(4096)  # aligned stand-in, never dereferenced
@@ -39,3 +39,39 @@ def test_step_survives_copies():
     for m in (copy.deepcopy(lin), pickle.loads(pickle.dumps(lin)), lin.float(), old):
         assert m.step == 5 and torch.equal(m.weight, lin.weight)
     assert list(lin.state_dict()) == ["weight"]
+
+
+@pytest.fixture
+def stubbed(monkeypatch):
+    """The layer's calls answered with operands and products of zeros."""
+    monkeypatch.setattr(metis, "int8_quantize", lambda m, axes, **kw: metis.I8Operand(*m.shape, axes, "cpu"))
+    monkeypatch.setattr(metis, "int8_gemm", lambda a, b, out_dtype=torch.float32: torch.zeros(a.outer, b.outer, dtype=out_dtype))
+    return monkeypatch
+
+
+@pytest.mark.parametrize("shared", ["weight", "input", "layer"])
+def test_capture_is_refused_while_an_eager_graph_of_a_shared_leaf_lives(stubbed, shared):
+    """Two layers with one weight or one input, or one layer whose weight is
+    computed: recording in a capture would meet the eager graph's leaf."""
+    a, b = Int8Linear(4, 6, device="cpu"), Int8Linear(4, 6, device="cpu")
+    leaf = torch.randn(3, 4, requires_grad=True)
+    x, z = leaf, torch.randn(3, 4, requires_grad=True)
+    if shared == "weight":
+        b.weight = a.weight
+    elif shared == "input":
+        z = leaf
+    else:
+        b = a
+        a.weight.requires_grad_(False)
+    alive = a(x)
+    with stubbed.context() as inside:
+        inside.setattr(layer, "_capturing", lambda: True)
+        with pytest.raises(RuntimeError, match="alive"):
+            b(z)
+        free = Int8Linear(4, 6, device="cpu")  # shares nothing
+        assert free(torch.randn(3, 4, requires_grad=True)).requires_grad
+        with torch.no_grad():
+            b(z)  # records nothing
+        del alive
+        assert b(z).requires_grad
+    assert not a._eager and not b._eager  # what a capture records does not count
