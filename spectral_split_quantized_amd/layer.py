@@ -106,6 +106,21 @@ def _capturing():
     return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
 
 
+def _product(a, b, dtype):
+    """A-hat B-hat^T of two int8 operands.  Lines longer than a product's int32
+    sums allow are taken in runs, whose binary32 products are added."""
+    if a.k_len <= metis.INT8_MAX_K:
+        return metis.int8_gemm(a, b, out_dtype=dtype)
+    run = metis.INT8_MAX_K // 128 * 128
+    total = None
+    for k in range(0, a.k_len, run):
+        n = min(run, a.k_len - k)
+        cut = [metis.I8.wrap(q.codes[:, k:k + metis.int8_pitch(n)].contiguous(), q.scales, n) for q in (a, b)]
+        part = metis.int8_gemm(*cut, out_dtype=torch.float32)
+        total = part if total is None else total.add_(part)
+    return total.to(dtype)
+
+
 class _Int8LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, mod, record):
@@ -120,7 +135,7 @@ class _Int8LinearFn(torch.autograd.Function):
         # left out
         qx = metis.int8_quantize(_rows(x), metis.AXIS1 | (metis.AXIS0 if need_w else 0))
         qw = metis.int8_quantize(w, metis.AXIS0 | (metis.AXIS1 if need_x else 0))
-        y = metis.int8_gemm(qx.ax1, qw.ax0, out_dtype=x.dtype)
+        y = _product(qx.ax1, qw.ax0, x.dtype)
         ctx.qx, ctx.qw = qx.ax0, qw.ax1
         ctx.lead, ctx.x_dtype, ctx.w_shape = x.shape[:-1], x.dtype, w.shape
         ctx.rounding, ctx.seed, ctx.tag = mod.rounding, mod.seed, mod.tags["D"]
@@ -140,9 +155,9 @@ class _Int8LinearFn(torch.autograd.Function):
         qd = metis.int8_quantize(d2, (metis.AXIS1 if need_x else 0) | (metis.AXIS0 if need_w else 0),
                                  rounding=ctx.rounding, seed=ctx.seed, tag=ctx.tag, step=ctx.step)
         if need_x:
-            dx = metis.int8_gemm(qd.ax1, ctx.qw, out_dtype=ctx.x_dtype).reshape(*ctx.lead, ctx.qw.outer)
+            dx = _product(qd.ax1, ctx.qw, ctx.x_dtype).reshape(*ctx.lead, ctx.qw.outer)
         if need_w:
-            dw = metis.int8_gemm(ctx.qx, qd.ax0)
+            dw = _product(ctx.qx, qd.ax0, torch.float32)
         return dx, dw, None, None
 
 
@@ -157,7 +172,9 @@ class Int8Linear(torch.nn.Module):
     read the step on the GPU: set it between replays, on their stream, and a
     replay takes its draws.  x is bfloat16 or float32; y and its gradient have
     x's type, the weight (``in_features x out_features``) and its gradient are
-    float32.  ``frozen()`` gives the serving form, with the weight quantised
+    float32.  A product over more than 131071 (tokens, for the weight's
+    gradient) is taken in runs of codes, whose binary32 products are added; the
+    scales are those of whole lines.  ``frozen()`` gives the serving form, with the weight quantised
     once."""
 
     def __init__(self, in_features, out_features, rounding="sr", seed=0, layer=0, device="cuda", weight=None):
@@ -245,7 +262,8 @@ class Int8Linear(torch.nn.Module):
 
 class Int8Frozen(torch.nn.Module):
     """y = x W for serving, W held as int8 with one scale per output channel;
-    the tokens of x are quantised in the call.  No gradients."""
+    the tokens of x are quantised in the call.  At most 131071 inputs.  No
+    gradients."""
 
     def __init__(self, w):
         super().__init__()
@@ -255,8 +273,7 @@ class Int8Frozen(torch.nn.Module):
 
     @torch.no_grad()
     def forward(self, x):
-        w = metis.I8.__new__(metis.I8)
-        w.codes, w.scales, w.outer, w.k_len = self.codes, self.scales, self.codes.shape[0], self.k_len
+        w = metis.I8.wrap(self.codes, self.scales, self.k_len)
         y = metis.int8_linear(_rows(x), w)
         return y.reshape(*x.shape[:-1], w.outer)
 

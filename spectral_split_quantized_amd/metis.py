@@ -581,6 +581,9 @@ def _leading(T):
     return T.stride(0) if T.shape[0] > 1 else max(T.stride(0), T.shape[1])
 
 
+INT8_MAX_K = 131071  # longest line of a product (metis_int8_gemm)
+
+
 def int8_pitch(k_len):
     """Bytes between code rows of k_len codes (metis_int8_pitch)."""
     return (k_len + 127) // 128 * 128
@@ -610,6 +613,13 @@ class I8:
         q.codes.zero_()
         q.codes[:, :q.k_len].copy_(codes)
         q.scales.copy_(scales)
+        return q
+
+    @classmethod
+    def wrap(cls, codes, scales, k_len):
+        """An operand on memory that has the library's layout already."""
+        q = cls.__new__(cls)
+        q.codes, q.scales, q.outer, q.k_len = codes, scales, codes.shape[0], k_len
         return q
 
     def dequantize(self):

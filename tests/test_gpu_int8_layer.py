@@ -4,9 +4,11 @@ equality."""
 
 import copy
 
+import numpy as np
 import pytest
 import torch
 
+from oracle import int8
 from spectral_split_quantized_amd import metis
 from spectral_split_quantized_amd.layer import Int8Linear, set_step
 
@@ -89,3 +91,41 @@ def test_step_follows_copies_and_moves():
     at = lin._count.data_ptr()  # a captured graph's address
     assert lin.to("cuda").float()._count.data_ptr() == at
     assert Int8Linear(16, 8, rounding="rne")._count is None and moved.cpu()._count is None
+
+
+def _runs(a, b):
+    """(the product in binary64, a bound of the binary32 errors): codes and
+    scales of both sides, cut in runs of 130944 codes.  A run's product has
+    three roundings of an exact sum, a sum of runs one for each addition."""
+    total, size = 0.0, 0.0
+    for k in range(0, a[0].shape[1], 130944):
+        x, y = (q[0][:, k:k + 130944].astype(np.float64) for q in (a, b))
+        part = x @ y.T * a[1].astype(np.float64)[:, None] * b[1].astype(np.float64)
+        total, size = total + part, size + np.abs(part)
+    return total, 2.0 ** -24 * 1.001 * (3 + a[0].shape[1] // 130944) * size
+
+
+@pytest.mark.parametrize("tokens,cin,cout", [(131071, 6, 5), (131072, 20, 24), (262200, 5, 3), (5, 3, 131200), (4, 131200, 7)])
+def test_reductions_longer_than_one_product(tokens, cin, cout):
+    """Every product of the layer over more codes than int32 sums hold: tokens
+    for dW, output features for dX, input features for Y."""
+    say("int8 layer, %d tokens, %d -> %d" % (tokens, cin, cout))
+    g = torch.Generator().manual_seed(tokens)
+    x, w, d = (torch.randn(s, generator=g) for s in ((tokens, cin), (cin, cout), (tokens, cout)))
+    lin = Int8Linear(cin, cout, seed=2, weight=w.cuda())
+    lin.step = 3
+    xg = x.cuda().requires_grad_(True)
+    y = lin(xg)
+    y.backward(d.cuda())
+    metis.status_sync()
+    x, w, d = x.numpy(), w.numpy(), d.numpy()
+    q, sr = int8.quantize, ("sr", 2, metis.make_tag(0, metis.OPERAND_D), 3)
+    for got, a, b in ((y, q(x, 1), q(w, 0)), (xg.grad, q(d, 1, *sr), q(w, 1)), (lin.weight.grad, q(x, 0), q(d, 0, *sr))):
+        want, bound = _runs(a, b)
+        assert np.all(np.abs(got.detach().cpu().numpy() - want) <= bound)
+    # bfloat16: the sum of the runs is rounded once
+    xb = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    got = lin(xb)
+    want, bound = _runs(q(xb.float().cpu().numpy(), 1), q(w, 0))
+    assert got.dtype == torch.bfloat16
+    assert np.all(np.abs(got.detach().float().cpu().numpy() - want) <= bound + 2.0 ** -8 * (np.abs(want) + bound))

@@ -75,3 +75,34 @@ def test_capture_is_refused_while_an_eager_graph_of_a_shared_leaf_lives(stubbed,
         del alive
         assert b(z).requires_grad
     assert not a._eager and not b._eager  # what a capture records does not count
+
+
+def test_longest_line_of_a_product():
+    lib = metis.load()
+
+    def gemm(k):
+        a, b = metis._I8(4096, 4096, 0, k), metis._I8(4096, 4096, 64, k)  # no rows: nothing is enqueued
+        return lib.metis_int8_gemm(ctypes.byref(a), ctypes.byref(b), D, 1, 64, None, 0, None)
+
+    assert gemm(metis.INT8_MAX_K) == metis.OK and gemm(metis.INT8_MAX_K + 1) == metis.E_UNSUPPORTED
+
+
+def test_long_reductions_are_cut_into_products_that_fit(stubbed):
+    """No product of the layer is asked for more than its limit, and the runs cover every code once."""
+    asked = []
+
+    def gemm(a, b, out_dtype=torch.float32):
+        assert a.k_len == b.k_len and a.codes.shape == (a.outer, metis.int8_pitch(a.k_len)) and a.codes.is_contiguous()
+        asked.append(a.k_len)
+        return torch.ones(a.outer, b.outer, dtype=out_dtype)
+
+    stubbed.setattr(metis, "int8_gemm", gemm)
+    for tokens, cin, cout, runs in ((131071, 2, 3, [2, 3, 131071]), (131072, 2, 3, [2, 3, 130944, 128]),
+                                    (2, 3, 262000, [3, 130944, 130944, 112, 2]), (2, 140000, 3, [130944, 9056, 3, 2])):
+        asked.clear()
+        lin = Int8Linear(cin, cout, device="cpu")
+        x = torch.zeros(tokens, cin, requires_grad=True)
+        y = lin(x)
+        y.sum().backward()
+        assert asked == runs
+        assert y[0, 0].item() == (2 if cin > 131071 else 1) and lin.weight.grad[0, 0].item() == (2 if tokens > 131071 else 1)
