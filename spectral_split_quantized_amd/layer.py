@@ -271,6 +271,26 @@ class Int8Frozen(torch.nn.Module):
         self.register_buffer("codes", w.codes)
         self.register_buffer("scales", w.scales)
 
+    def get_extra_state(self):
+        """The number of inputs, which the padded codes do not tell."""
+        return torch.tensor(self.k_len)
+
+    def set_extra_state(self, state):
+        pass  # compared before anything is loaded
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs):
+        key, codes = prefix + "_extra_state", state_dict.get(prefix + "codes")
+        if key in state_dict:
+            k_len = int(state_dict[key])
+        else:  # saved without it: codes behind this layer's inputs must be the padding's zeros
+            k_len = self.k_len if codes is None or not codes[:, self.k_len:].any() else "more"
+        if k_len != self.k_len:
+            error_msgs.append("size mismatch for %scodes: a layer of %s inputs, here %d" % (prefix, k_len, self.k_len))
+            return
+        super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs)
+        if key in missing_keys:
+            missing_keys.remove(key)
+
     @torch.no_grad()
     def forward(self, x):
         w = metis.I8.wrap(self.codes, self.scales, self.k_len)

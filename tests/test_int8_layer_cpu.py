@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from spectral_split_quantized_amd import layer, metis
-from spectral_split_quantized_amd.layer import Int8Linear
+from spectral_split_quantized_amd.layer import Int8Frozen, Int8Linear
 
 D = ctypes.c_void_p(4096)  # aligned stand-in, never dereferenced
 
@@ -106,3 +106,36 @@ def test_long_reductions_are_cut_into_products_that_fit(stubbed):
         y.sum().backward()
         assert asked == runs
         assert y[0, 0].item() == (2 if cin > 131071 else 1) and lin.weight.grad[0, 0].item() == (2 if tokens > 131071 else 1)
+
+
+def _frozen(k, n=3, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    codes = torch.randint(1, 128, (n, k), generator=g, dtype=torch.int8)
+    return Int8Frozen(metis.I8.from_codes(codes, torch.rand(n, generator=g) + 0.5))
+
+
+@pytest.mark.parametrize("there", [96, 97, 128])
+@pytest.mark.parametrize("nested", [False, True])
+def test_frozen_states_of_another_input_size_are_refused(there, nested):
+    """All of these have code rows of 128 bytes."""
+    wrap = (lambda m: torch.nn.Sequential(torch.nn.Identity(), m)) if nested else (lambda m: m)
+    for here in (96, 97, 128):
+        src, dst = _frozen(there), _frozen(here, seed=1)
+        before = dst.codes.clone()
+        if here == there:
+            assert not any(wrap(dst).load_state_dict(wrap(src).state_dict()))
+            assert torch.equal(dst.codes, src.codes) and torch.equal(dst.scales, src.scales)
+        else:
+            with pytest.raises(RuntimeError, match="size mismatch"):
+                wrap(dst).load_state_dict(wrap(src).state_dict())
+            assert torch.equal(dst.codes, before) and dst.k_len == here
+
+
+def test_frozen_states_saved_without_the_input_size():
+    state = _frozen(97).state_dict()
+    assert int(state.pop("_extra_state")) == 97
+    same = _frozen(97, seed=1)
+    same.load_state_dict(state)
+    assert torch.equal(same.codes, state["codes"])
+    with pytest.raises(RuntimeError, match="size mismatch"):
+        _frozen(96).load_state_dict(state)
