@@ -271,6 +271,13 @@ class Int8Frozen(torch.nn.Module):
         self.register_buffer("codes", w.codes)
         self.register_buffer("scales", w.scales)
 
+    def _apply(self, fn, recurse=True):
+        scales = self.scales
+        super()._apply(fn, recurse)
+        if self.scales.dtype != torch.float32:  # the format's, whatever type the model takes
+            self.scales = scales.to(self.scales.device)
+        return self
+
     def get_extra_state(self):
         """The number of inputs, which the padded codes do not tell."""
         return torch.tensor(self.k_len)

@@ -129,3 +129,13 @@ def test_reductions_longer_than_one_product(tokens, cin, cout):
     want, bound = _runs(q(xb.float().cpu().numpy(), 1), q(w, 0))
     assert got.dtype == torch.bfloat16
     assert np.all(np.abs(got.detach().float().cpu().numpy() - want) <= bound + 2.0 ** -8 * (np.abs(want) + bound))
+
+
+def test_frozen_form_in_a_model_cast_to_bfloat16():
+    g = torch.Generator().manual_seed(2)
+    lin = Int8Linear(96, 40, weight=torch.randn(96, 40, generator=g).cuda(), rounding="rne")
+    x = torch.randn(7, 96, generator=g).to(torch.bfloat16).cuda()
+    frozen = lin.frozen()
+    want = frozen(x)
+    assert torch.equal(frozen.to(torch.bfloat16)(x), want) and torch.equal(frozen.cpu().bfloat16().cuda()(x), want)
+    metis.status_sync()

@@ -139,3 +139,14 @@ def test_frozen_states_saved_without_the_input_size():
     assert torch.equal(same.codes, state["codes"])
     with pytest.raises(RuntimeError, match="size mismatch"):
         _frozen(96).load_state_dict(state)
+
+
+@pytest.mark.parametrize("cast", [lambda m: m.to(torch.bfloat16), lambda m: m.half(), lambda m: m.double(),
+                                  lambda m: m.bfloat16().float(), lambda m: m.to("cpu")])
+def test_frozen_scales_keep_their_type_and_values(cast):
+    m = _frozen(20)
+    codes, scales = m.codes.clone(), m.scales.clone()
+    out = cast(torch.nn.Sequential(m, torch.nn.Linear(2, 2)))
+    assert out[0] is m and m.scales.dtype == torch.float32 and torch.equal(m.scales, scales)
+    assert m.codes.dtype == torch.int8 and torch.equal(m.codes, codes) and list(m.state_dict()) == ["codes", "scales", "_extra_state"]
+    metis.I8.wrap(m.codes, m.scales, m.k_len)._c()  # an operand that the library takes
