@@ -25,7 +25,9 @@ class AdamW(torch.optim.Optimizer):
     parameter's place and the step) or "rne" for 8-bit states and bfloat16
     parameters; to nearest, 8-bit states cannot follow slow changes.
     ``max_norm``: clip the gradients' norm over all groups; ``grad_norm`` then
-    holds the last step's norm, a one-element tensor on the GPU.
+    holds the last step's norm, a one-element tensor on the GPU, new in each
+    step (with ``capturable`` one tensor that every step and replay writes:
+    clone what is to be kept).
     ``capturable``: the step count lives on the GPU, so that a step captured
     into a graph advances it on every replay (lr and the other values are
     those of the capture); every parameter then needs a gradient in every step.
@@ -96,7 +98,7 @@ class AdamW(torch.optim.Optimizer):
         if any(c[2] != device for c in calls):
             raise ValueError("the parameters must be on one GPU")
         if self.max_norm is not None:
-            if self._clip is None or self._clip.get_device() != device:
+            if not self.capturable or self._clip is None or self._clip.get_device() != device:
                 self._clip = torch.empty(2, dtype=torch.float32, device=torch.device("cuda", device))
             whole = calls[0][1] if len(calls) == 1 else metis.np.concatenate([c[1] for c in calls])
             metis._grad_norm_run(whole, device, self.max_norm, self._clip)

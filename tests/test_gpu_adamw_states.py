@@ -193,3 +193,17 @@ def test_autograd_sees_the_write():
     metis.adamw_step([r], [torch.ones(5, device="cuda")], [m], [v], lr=0.1, step=2)  # has no versions
     metis.status_sync()
     assert bool((r < 1).all())
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_norms_kept_over_steps(capturable):
+    """Each step's norm is a tensor of its own; with capturable, one that every step writes."""
+    p = torch.nn.Parameter(torch.zeros(9, device="cuda"))
+    opt = optim.AdamW([p], max_norm=1.0, state_bits=32, capturable=capturable)
+    norms = []
+    for t in range(1, 4):
+        p.grad = torch.full((9,), float(t), device="cuda")
+        opt.step()
+        norms.append(opt.grad_norm)
+    assert [n.item() for n in norms] == ([9.0] * 3 if capturable else [3.0, 6.0, 9.0])
+    metis.status_sync()
