@@ -136,7 +136,7 @@ class _Int8LinearFn(torch.autograd.Function):
         qx = metis.int8_quantize(_rows(x), metis.AXIS1 | (metis.AXIS0 if need_w else 0))
         qw = metis.int8_quantize(w, metis.AXIS0 | (metis.AXIS1 if need_x else 0))
         y = _product(qx.ax1, qw.ax0, x.dtype)
-        ctx.qx, ctx.qw = qx.ax0, qw.ax1
+        ctx.save_for_backward(*(t for q in (qx.ax0, qw.ax1) for t in ((q.codes, q.scales) if q else (None, None))))
         ctx.lead, ctx.x_dtype, ctx.w_shape = x.shape[:-1], x.dtype, w.shape
         ctx.rounding, ctx.seed, ctx.tag = mod.rounding, mod.seed, mod.tags["D"]
         ctx.step = mod._count if capturing and mod._count is not None else mod.step
@@ -152,12 +152,13 @@ class _Int8LinearFn(torch.autograd.Function):
             dx = dy.new_zeros((*ctx.lead, ctx.w_shape[0]), dtype=ctx.x_dtype) if need_x else None
             dw = dy.new_zeros(ctx.w_shape, dtype=torch.float32) if need_w else None
             return dx, dw, None, None
+        xc, xs, wc, ws = ctx.saved_tensors
         qd = metis.int8_quantize(d2, (metis.AXIS1 if need_x else 0) | (metis.AXIS0 if need_w else 0),
                                  rounding=ctx.rounding, seed=ctx.seed, tag=ctx.tag, step=ctx.step)
         if need_x:
-            dx = _product(qd.ax1, ctx.qw, ctx.x_dtype).reshape(*ctx.lead, ctx.qw.outer)
+            dx = _product(qd.ax1, metis.I8.wrap(wc, ws, ctx.w_shape[1]), ctx.x_dtype).reshape(*ctx.lead, ctx.w_shape[0])
         if need_w:
-            dw = _product(ctx.qx, qd.ax0, torch.float32)
+            dw = _product(metis.I8.wrap(xc, xs, d2.shape[0]), qd.ax0, torch.float32)
         return dx, dw, None, None
 
 

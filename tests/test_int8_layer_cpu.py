@@ -3,6 +3,7 @@
 import copy
 import ctypes
 import pickle
+import weakref
 
 import pytest
 import torch
@@ -150,3 +151,35 @@ def test_frozen_scales_keep_their_type_and_values(cast):
     assert out[0] is m and m.scales.dtype == torch.float32 and torch.equal(m.scales, scales)
     assert m.codes.dtype == torch.int8 and torch.equal(m.codes, codes) and list(m.state_dict()) == ["codes", "scales", "_extra_state"]
     metis.I8.wrap(m.codes, m.scales, m.k_len)._c()  # an operand that the library takes
+
+
+@pytest.mark.parametrize("x_grad,w_grad,kept", [(True, True, 4), (True, False, 2), (False, True, 2)])
+def test_saved_codes_pass_hooks_and_are_freed(stubbed, x_grad, w_grad, kept):
+    """What the backward pass needs is saved as autograd saves tensors: hooks
+    see it, a backward pass frees it, a second one is refused."""
+    lin = Int8Linear(4, 6, device="cpu")
+    lin.weight.requires_grad_(w_grad)
+    packed, unpacked = [], []
+
+    def pack(t):
+        packed.append(t)
+        return t.clone()
+
+    def unpack(t):
+        unpacked.append(t)
+        return t
+
+    x = torch.zeros(3, 4, requires_grad=x_grad)
+    with torch.autograd.graph.saved_tensors_hooks(pack, unpack):
+        y = lin(x)
+    assert len(packed) == kept and {t.dtype for t in packed} == {torch.int8, torch.float32}
+    y.sum().backward()
+    assert len(unpacked) == kept
+    with pytest.raises(RuntimeError, match="second time"):
+        y.sum().backward()
+    z = lin(x)
+    codes = [weakref.ref(t) for t in z.grad_fn.saved_tensors if t is not None]
+    assert len(codes) == kept
+    z.sum().backward(retain_graph=True)
+    z.sum().backward()
+    assert not any(r() is not None for r in codes) and z.grad_fn is not None
