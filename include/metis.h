@@ -327,7 +327,8 @@ metis_status metis_mxfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, c
  * A non-finite element sets the numeric flag of metis_status_sync and leaves
  * unspecified codes.  ws holds metis_int8_quantize_workspace(rows, cols,
  * axes) bytes, 16-byte aligned.  rows == 0 or cols == 0 returns METIS_OK with
- * nothing enqueued.
+ * nothing enqueued.  rows and cols are below 2^31 and, with METIS_AXIS0,
+ * ceil(rows / 128) * ceil(cols / 128) below 2^24 (METIS_E_UNSUPPORTED above).
  *
  * metis_int8_quantize_counted: the same with the step read from the int64 at
  * step_count in device memory when the kernels run (for graphs, whose replays
@@ -404,8 +405,9 @@ metis_status metis_int8_linear(const void *X, int32_t dtype, int64_t tokens, int
  * every other value is fixed at the call).
  * No array that is written may appear twice in a call or overlap another one,
  * a gradient included; gradients may overlap each other.
- * Small tensors share launches; the tensor list is read before the call
- * returns.
+ * A tensor has at most 4096 (2^24 - 1) elements (METIS_E_UNSUPPORTED above), here
+ * and in metis_grad_norm.  Small tensors share launches; the tensor list is
+ * read before the call returns.
  *
  * metis_grad_norm: out[0] = the square root of the sum of squares over all
  * tensors' gradients (only grad, grad_dtype and n are read), summed in

@@ -76,10 +76,16 @@ hipError_t launch_i8_gemm(const I8GemmParams& in, hipStream_t st) {
     // one batch of loads for the whole row where four waves can hold it
     // (16 x 4096 bytes: 13.1 us at 14336 rows of B against 14.6 with eight
     // waves of four loads; at 14336 bytes 14.8 against 13.5)
-    const dim3 grid((unsigned)ceil_div<int64_t>(g.N, 16));
-    const int64_t steps = g.pitch >> 6;
-    if (steps > 32 && steps <= 64) hipLaunchKernelGGL((i8_gemm_skinny_kernel<4, 16>), grid, dim3(256), 0, st, g);
-    else hipLaunchKernelGGL((i8_gemm_skinny_kernel<8, 4>), grid, dim3(512), 0, st, g);
+    const int64_t steps = g.pitch >> 6, lines = max_groups(512) * 16;
+    for (int64_t n0 = 0; n0 < in.N; n0 += lines) {
+      g.N = std::min(lines, in.N - n0);
+      g.b = in.b + n0 * in.pitch;
+      g.sb = in.sb + n0;
+      g.C = (char*)in.C + n0 * (in.bf16 ? 2 : 4);
+      const dim3 grid((unsigned)ceil_div<int64_t>(g.N, 16));
+      if (steps > 32 && steps <= 64) hipLaunchKernelGGL((i8_gemm_skinny_kernel<4, 16>), grid, dim3(256), 0, st, g);
+      else hipLaunchKernelGGL((i8_gemm_skinny_kernel<8, 4>), grid, dim3(512), 0, st, g);
+    }
   }
   return hipGetLastError();
 }

@@ -7,6 +7,9 @@
 
 namespace metis {
 
+// Workgroups that one launch takes: a dispatch has fewer than 2^32 work items.
+inline int64_t max_groups(int64_t threads) { return (int64_t)UINT32_MAX / threads; }
+
 struct GemmParams;
 
 // C = alpha A B^T (+ K-extension) with 256 x 256 tiles; requires K % 256 == 0

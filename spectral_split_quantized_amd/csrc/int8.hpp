@@ -31,6 +31,7 @@ struct I8QuantParams {
   const void* src;
   int dtype;
   int64_t rows, cols, ld;
+  int64_t row0;      // first row of this launch (rows alone)
   bool vec;          // rows start 16-byte aligned and ld keeps them so
   int8_t* codes0;    // [cols][i8_pitch(rows)] or null
   int8_t* codes1;    // [rows][i8_pitch(cols)] or null
@@ -183,7 +184,7 @@ template <int W, int CH, bool SR>
 __global__ __launch_bounds__(64 * W) void i8_quant_rows_kernel(I8QuantParams p) {
   constexpr int T = 64 * W;
   __shared__ float red[W];
-  const int64_t row = blockIdx.x;
+  const int64_t row = p.row0 + blockIdx.x;
   const int64_t chunks = i8_pitch(p.cols) >> 3;  // the zero padding included
   float x[CH][8];
   float m = 0.0f;

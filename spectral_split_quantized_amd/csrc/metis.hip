@@ -1168,15 +1168,25 @@ I8QuantParams int8_input(const void* M, int dtype, int64_t rows, int64_t cols, i
 }
 
 template <bool SR>
-void launch_int8_rows(const I8QuantParams& q, hipStream_t st) {
-  const dim3 grid((unsigned)q.rows);
+void launch_int8_rows(I8QuantParams q, hipStream_t st) {
   const int64_t chunks = i8_pitch(q.cols) >> 3;
-  if (chunks <= 64) hipLaunchKernelGGL((i8_quant_rows_kernel<1, 1, SR>), grid, dim3(64), 0, st, q);
-  else if (chunks <= 256) hipLaunchKernelGGL((i8_quant_rows_kernel<4, 1, SR>), grid, dim3(256), 0, st, q);
-  else if (chunks <= 512) hipLaunchKernelGGL((i8_quant_rows_kernel<4, 2, SR>), grid, dim3(256), 0, st, q);
-  else if (chunks <= 1024) hipLaunchKernelGGL((i8_quant_rows_kernel<8, 2, SR>), grid, dim3(512), 0, st, q);
-  else hipLaunchKernelGGL((i8_quant_rows_kernel<16, 2, SR>), grid, dim3(1024), 0, st, q);
+  const int threads = chunks <= 64 ? 64 : chunks <= 512 ? 256 : chunks <= 1024 ? 512 : 1024;
+  for (q.row0 = 0; q.row0 < q.rows; q.row0 += max_groups(threads)) {
+    const dim3 grid((unsigned)std::min(max_groups(threads), q.rows - q.row0)), block(threads);
+    if (chunks <= 64) hipLaunchKernelGGL((i8_quant_rows_kernel<1, 1, SR>), grid, block, 0, st, q);
+    else if (chunks <= 256) hipLaunchKernelGGL((i8_quant_rows_kernel<4, 1, SR>), grid, block, 0, st, q);
+    else if (chunks <= 512) hipLaunchKernelGGL((i8_quant_rows_kernel<4, 2, SR>), grid, block, 0, st, q);
+    else if (chunks <= 1024) hipLaunchKernelGGL((i8_quant_rows_kernel<8, 2, SR>), grid, block, 0, st, q);
+    else hipLaunchKernelGGL((i8_quant_rows_kernel<16, 2, SR>), grid, block, 0, st, q);
+  }
 }
+
+// Tiles of the two sweeps along the columns.
+int64_t i8_amax_tiles(int64_t rows, int64_t cols) {
+  return ceil_div<int64_t>(rows, 4 * i8_amax_rows(rows, cols)) * ceil_div<int64_t>(cols, kI8AmaxCols);
+}
+// (the zeros behind K are written too)
+int64_t i8_code_tiles(int64_t rows, int64_t cols) { return i8_pitch(rows) / kI8Tile * (i8_pitch(cols) / kI8Tile); }
 
 metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols, int64_t ld, int axes, int rounding,
                             uint64_t seed, uint32_t tag, int64_t step, const int64_t* step_count, const metis_i8* ax0,
@@ -1195,11 +1205,9 @@ metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols
     return METIS_OK;
   }
   q.amax_rows = i8_amax_rows(rows, cols);
-  const dim3 tiles((unsigned)(ceil_div<int64_t>(rows, 4 * q.amax_rows) * ceil_div<int64_t>(cols, kI8AmaxCols)));
-  hipLaunchKernelGGL(i8_amax_kernel, tiles, dim3(256), 0, st, q);
+  hipLaunchKernelGGL(i8_amax_kernel, dim3((unsigned)i8_amax_tiles(rows, cols)), dim3(256), 0, st, q);
   LAUNCH_CHECK();
-  // the zeros behind K are written too
-  const dim3 padded((unsigned)(i8_pitch(rows) / kI8Tile * (i8_pitch(cols) / kI8Tile)));
+  const dim3 padded((unsigned)i8_code_tiles(rows, cols));
   const bool bf16 = dtype == METIS_BF16;
   if (q.sr && bf16) hipLaunchKernelGGL((i8_quant_tile_kernel<true, true>), padded, dim3(256), 0, st, q);
   else if (q.sr) hipLaunchKernelGGL((i8_quant_tile_kernel<true, false>), padded, dim3(256), 0, st, q);
@@ -1226,7 +1234,8 @@ metis_status int8_quantize_at(const void* M, int32_t dtype, int64_t rows, int64_
   if ((axes & METIS_AXIS1) && (s = int8_check(ax1, "int8_quantize: ax1", rows, cols)) != METIS_OK) return s;
   if (rows == 0 || cols == 0) return METIS_OK;
   if (!M) return fail(METIS_E_INVALID, "int8_quantize: null input");
-  if (rows > INT32_MAX || cols > INT32_MAX || i8_pitch(rows) / kI8Tile * (i8_pitch(cols) / kI8Tile) > INT32_MAX)
+  if (rows > INT32_MAX || cols > INT32_MAX ||
+      ((axes & METIS_AXIS0) && (i8_code_tiles(rows, cols) > max_groups(256) || i8_amax_tiles(rows, cols) > max_groups(256))))
     return fail(METIS_E_UNSUPPORTED, "int8_quantize: %lld x %lld", (long long)rows, (long long)cols);
   Carver cv(ws, ws_bytes);
   const I8Ws w = carve_int8(cv, rows, cols, axes);
@@ -1318,7 +1327,7 @@ metis_status adamw_kind(const metis_adamw_tensor* tensors, int64_t count, const 
     if (a.n == 0 || ((a.param_dtype == METIS_BF16) | (a.grad_dtype == METIS_BF16) << 1 | (a.state_bits == 8) << 2) != kind)
       continue;
     const uint64_t need = (uint64_t)ceil_div<int64_t>(a.n, kAdamWork);
-    if (t.count == AdamTable<EIGHT>::kTensors || groups + need > INT32_MAX)
+    if (t.count == AdamTable<EIGHT>::kTensors || groups + need > (uint64_t)max_groups(256))
       if ((s = flush()) != METIS_OK) return s;
     const int k = t.count++;
     t.first[k] = (uint32_t)groups;
@@ -1332,7 +1341,7 @@ metis_status adamw_kind(const metis_adamw_tensor* tensors, int64_t count, const 
 
 metis_status adamw_grad_check(const metis_adamw_tensor& a, int64_t i, const char* what) {
   if (a.n < 0) return fail(METIS_E_INVALID, "%s: tensor %lld: n %lld", what, (long long)i, (long long)a.n);
-  if (a.n > (int64_t)INT32_MAX * kAdamWork)
+  if (a.n > max_groups(256) * kAdamWork)
     return fail(METIS_E_UNSUPPORTED, "%s: tensor %lld: n %lld", what, (long long)i, (long long)a.n);
   if (!dtype_ok(a.grad_dtype)) return fail(METIS_E_INVALID, "%s: tensor %lld: grad dtype %d", what, (long long)i, a.grad_dtype);
   if (a.n && !a.grad) return fail(METIS_E_INVALID, "%s: tensor %lld: null gradient", what, (long long)i);
@@ -1831,10 +1840,18 @@ metis_status metis_int8_linear(const void* X, int32_t dtype, int64_t tokens, int
   if (int8_token(tokens, W->k_len)) {
     const I8TokenParams f{int8_input(X, dtype, 1, W->k_len, ldx), W->n_outer, i8_pitch(W->k_len), W->codes, W->scales, Y,
                           y_dtype == METIS_BF16};
-    const dim3 grid((unsigned)ceil_div<int64_t>(W->n_outer, 16));
-    if (f.pitch <= 4096) hipLaunchKernelGGL((i8_linear_token_kernel<4, 16, 2>), grid, dim3(256), 0, st, f);
-    else hipLaunchKernelGGL((i8_linear_token_kernel<8, 8, 4>), grid, dim3(512), 0, st, f);
-    LAUNCH_CHECK();
+    const int64_t lines = max_groups(512) * 16;
+    for (int64_t n0 = 0; n0 < W->n_outer; n0 += lines) {
+      I8TokenParams g = f;
+      g.N = std::min(lines, f.N - n0);
+      g.w += n0 * f.pitch;
+      g.sw += n0;
+      g.y = (char*)f.y + n0 * (f.bf16 ? 2 : 4);
+      const dim3 grid((unsigned)ceil_div<int64_t>(g.N, 16));
+      if (f.pitch <= 4096) hipLaunchKernelGGL((i8_linear_token_kernel<4, 16, 2>), grid, dim3(256), 0, st, g);
+      else hipLaunchKernelGGL((i8_linear_token_kernel<8, 8, 4>), grid, dim3(512), 0, st, g);
+      LAUNCH_CHECK();
+    }
     return METIS_OK;
   }
   if ((s = run_int8_quant(X, dtype, tokens, W->k_len, ldx, METIS_AXIS1, METIS_RNE, 0, 0, 0, nullptr, nullptr, &xq, I8Ws{}, st)) !=
@@ -1919,7 +1936,7 @@ metis_status metis_grad_norm(const metis_adamw_tensor* tensors, int64_t count, d
       const metis_adamw_tensor& a = tensors[i];
       if (a.n == 0 || (a.grad_dtype == METIS_BF16) != (bf16 == 1)) continue;
       const uint64_t k = (uint64_t)ceil_div<int64_t>(a.n, kNormWork);
-      if (t.count == kNormTensors || groups + k > INT32_MAX)
+      if (t.count == kNormTensors || groups + k > (uint64_t)max_groups(256))
         if ((s = flush()) != METIS_OK) return s;
       t.first[t.count] = (uint32_t)groups;
       t.g[t.count] = a.grad;

@@ -1,6 +1,7 @@
 """The optimizer's host side (no GPU work): the library's calls are recorded
 in place of being run."""
 
+import ctypes
 import types
 
 import numpy as np
@@ -108,3 +109,19 @@ def test_oracle_keeps_values_that_are_not_finite_out_of_the_scale():
         assert np.array_equal(scales, s) and np.array_equal(codes[good], want[good])
         d = adamw.decode(codes, scales)
         assert np.isnan(d[[3, 280]]).all() and np.isfinite(d[good]).all()
+
+
+def test_tensors_beyond_a_launch_are_refused():
+    """A launch of 256 threads a workgroup takes fewer than 2^24 of them, each 4096 elements."""
+    lib = metis.load()
+    t = np.zeros(1, metis._ADAMW_TENSOR)
+    for name in ("param", "grad", "m", "v", "m_scale", "v_scale"):
+        t[name] = 4096
+    t["state_bits"], t["param_dtype"], t["grad_dtype"] = 8, 1, 1
+    ptr, most = ctypes.c_void_p(t.ctypes.data), (2 ** 24 - 1) * 4096
+    cfg = metis._AdamWConfig(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1)
+    t["n"] = most + 1
+    assert lib.metis_adamw_step(ptr, 1, ctypes.byref(cfg), None) == metis.E_UNSUPPORTED
+    assert lib.metis_grad_norm(ptr, 1, 1.0, ptr, ptr, 1 << 62, None) == metis.E_UNSUPPORTED
+    t["n"] = most
+    assert lib.metis_grad_norm(ptr, 1, 1.0, ptr, ptr, 8, None) == metis.E_WORKSPACE  # admitted, as far as the workspace

@@ -139,3 +139,52 @@ def test_frozen_form_in_a_model_cast_to_bfloat16():
     want = frozen(x)
     assert torch.equal(frozen.to(torch.bfloat16)(x), want) and torch.equal(frozen.cpu().bfloat16().cuda()(x), want)
     metis.status_sync()
+
+
+def test_more_rows_than_one_launch_takes():
+    """2^24 rows of 256 threads each are 2^32 work items: rows on both sides of
+    the cut, against the same rows alone and the definition's draws."""
+    rows, cols = (1 << 24) + 300, 520
+    say("int8 quantize %d rows" % rows)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    part = torch.randn(1000, cols, generator=g, device="cuda").to(torch.bfloat16)
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[:1000] = part
+    x[-1000:] = part
+    q = metis.int8_quantize(x).ax1
+    want = metis.int8_quantize(part).ax1
+    for s in (slice(0, 1000), slice(rows - 1000, rows)):
+        assert torch.equal(q.codes[s], want.codes) and torch.equal(q.scales[s], want.scales)
+    assert not q.codes[1000:-1000].any()
+    q = metis.int8_quantize(x, rounding=metis.SR, seed=5, tag=1, step=2).ax1
+    metis.status_sync()
+    from oracle import philox
+    for row in (0, rows - 1000, rows - 301, rows - 300, rows - 1):
+        e0 = row * cols
+        u = philox.halves(np.arange(e0, e0 + cols, dtype=np.uint64), 5, 1, 2) / 65536
+        xr = x[row].float().cpu().numpy()
+        y = xr * (np.float32(1) / np.float32(np.abs(xr).max() / np.float32(127)))
+        code = np.floor(y) + (u < y - np.floor(y))
+        assert np.array_equal(q.codes[row, :cols].cpu().numpy(), np.clip(code, -127, 127).astype(np.int8))
+
+
+def test_more_output_channels_than_one_launch_takes():
+    """The kernels for a few tokens take 16 channels a workgroup of up to 512 threads."""
+    n, k = (1 << 27) + 100, 100
+    say("int8 linear to %d channels" % n)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    base = metis.I8.from_codes(torch.randint(-127, 128, (1000, k), generator=g, dtype=torch.int8, device="cuda"),
+                               torch.rand(1000, generator=g, device="cuda"))
+    w = metis.I8(n, k)
+    w.codes.zero_()
+    w.scales.fill_(1.0)
+    for s in (slice(0, 1000), slice(n - 1000, n)):
+        w.codes[s] = base.codes
+        w.scales[s] = base.scales
+    for tokens in (1, 2):
+        x = torch.randn(tokens, k, generator=g, device="cuda")
+        for out in (torch.float32, torch.bfloat16):
+            y = metis.int8_linear(x, w, out_dtype=out)
+            want = metis.int8_linear(x, base, out_dtype=out)
+            assert torch.equal(y[:, :1000], want) and torch.equal(y[:, -1000:], want) and not y[:, 1000:-1000].any()
+    metis.status_sync()

@@ -183,3 +183,19 @@ def test_saved_codes_pass_hooks_and_are_freed(stubbed, x_grad, w_grad, kept):
     z.sum().backward(retain_graph=True)
     z.sum().backward()
     assert not any(r() is not None for r in codes) and z.grad_fn is not None
+
+
+def test_sizes_beyond_a_launch_are_refused():
+    """A launch of 256 threads a workgroup takes fewer than 2^24 of them."""
+    lib = metis.load()
+
+    def quant(rows, cols, axes):
+        a, b = metis._I8(4096, 4096, cols, rows), metis._I8(4096, 4096, rows, cols)
+        return lib.metis_int8_quantize(D, 0, rows, cols, cols, axes, 0, 0, 0, 0, ctypes.byref(a), ctypes.byref(b), D, 16, None)
+
+    most = (2 ** 24 - 1) * 128
+    for axes in (1, 3):
+        assert quant(most, 128, axes) == metis.E_WORKSPACE  # admitted, as far as the workspace
+        for rows, cols in ((most + 1, 128), (most, 129), (2 ** 31 - 1, 1), (128, most + 1), (2 ** 20, 2 ** 20)):
+            assert quant(rows, cols, axes) == metis.E_UNSUPPORTED
+    assert quant(2 ** 31, 1, 2) == metis.E_UNSUPPORTED
