@@ -17,7 +17,8 @@ _SETTINGS = ("state_bits", "min_8bit_size", "rounding", "seed", "max_norm", "cap
 
 
 class AdamW(torch.optim.Optimizer):
-    """AdamW with decoupled weight decay.
+    """AdamW with decoupled weight decay.  By default its states are in 8 bits,
+    rounded stochastically; ``state_bits=32`` is the plain optimizer.
 
     ``state_bits``: 8 holds both moments in E4M3 with a scale per 256 elements
     (parameters of fewer than ``min_8bit_size`` elements keep 32 bits), 32 in
