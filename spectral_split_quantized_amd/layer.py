@@ -102,8 +102,8 @@ def _rows(x):
 _EAGER = weakref.WeakSet()  # nodes of Int8Linear recorded outside a capture, while their graphs live
 
 
-def _capturing():
-    return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+def _capturing(t):
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
 
 
 def _product(a, b, dtype):
@@ -127,16 +127,18 @@ class _Int8LinearFn(torch.autograd.Function):
         # needs_input_grad says nothing of torch.no_grad(): record is the
         # caller's grad mode (inside a forward it is always off)
         need_x, need_w = (record and need for need in ctx.needs_input_grad[:2])
-        capturing = (need_x or need_w) and _capturing()
+        capturing = False
         if need_x or need_w:
-            mod._watch(ctx, (x, w), capturing)
+            capturing = _capturing(x)
+            mod._watch(ctx, [id(t) for t, need in ((x, need_x), (w, need_w)) if need and t.is_leaf], capturing)
         # the same orientations as above: X along both axes (Y and dW), W
         # along both (Y and dX); an orientation whose product is not wanted is
         # left out
         qx = metis.int8_quantize(_rows(x), metis.AXIS1 | (metis.AXIS0 if need_w else 0))
         qw = metis.int8_quantize(w, metis.AXIS0 | (metis.AXIS1 if need_x else 0))
         y = _product(qx.ax1, qw.ax0, x.dtype)
-        ctx.save_for_backward(*(t for q in (qx.ax0, qw.ax1) for t in ((q.codes, q.scales) if q else (None, None))))
+        q0, q1 = qx.ax0, qw.ax1
+        ctx.save_for_backward(q0 and q0.codes, q0 and q0.scales, q1 and q1.codes, q1 and q1.scales)
         ctx.lead, ctx.x_dtype, ctx.w_shape = x.shape[:-1], x.dtype, w.shape
         ctx.rounding, ctx.seed, ctx.tag = mod.rounding, mod.seed, mod.tags["D"]
         ctx.step = mod._count if capturing and mod._count is not None else mod.step
@@ -201,7 +203,7 @@ class Int8Linear(torch.nn.Module):
     @step.setter
     def step(self, step):
         if self._count is not None:
-            if _capturing():
+            if _capturing(self._count):
                 raise RuntimeError("set the step outside the capture: replays read the one that is set then")
             self._count.fill_(step)
         self._step = step
@@ -225,17 +227,16 @@ class Int8Linear(torch.nn.Module):
         """This layer's nodes of graphs from outside a capture that live."""
         return [c for c in _EAGER if c.layer() is self]
 
-    def _watch(self, ctx, inputs, capturing):
+    def _watch(self, ctx, leaves, capturing):
         """Refuses to record a graph in a capture while one from outside it
         lives, of this layer or of another with the same weight or input: both
         would accumulate a leaf's gradient through one node, which belongs to
         the other's stream, and joining that stream from a capture ends the
         process.  (A living graph holds its leaves, so their ids are theirs.)"""
-        leaves = {id(t) for t in inputs if t.requires_grad and t.is_leaf}
         if not capturing:
             ctx.layer, ctx.leaves = weakref.ref(self), leaves
             _EAGER.add(ctx)
-        elif any(c.layer() is self or not leaves.isdisjoint(c.leaves) for c in _EAGER):
+        elif any(c.layer() is self or any(i in c.leaves for i in leaves) for c in _EAGER):
             raise RuntimeError("a graph of this layer from outside the capture is alive, or one with the same weight or "
                                "input: drop its outputs first")
 

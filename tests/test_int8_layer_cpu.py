@@ -66,7 +66,7 @@ def test_capture_is_refused_while_an_eager_graph_of_a_shared_leaf_lives(stubbed,
         a.weight.requires_grad_(False)
     alive = a(x)
     with stubbed.context() as inside:
-        inside.setattr(layer, "_capturing", lambda: True)
+        inside.setattr(layer, "_capturing", lambda t: True)
         with pytest.raises(RuntimeError, match="alive"):
             b(z)
         free = Int8Linear(4, 6, device="cpu")  # shares nothing
