@@ -173,7 +173,9 @@ class Int8Linear(torch.nn.Module):
     default, with the draws of ``seed``, ``layer`` and the step that
     :func:`set_step` sets) or to nearest ("rne").  Passes captured into a graph
     read the step on the GPU: set it between replays, on their stream, and a
-    replay takes its draws.  x is bfloat16 or float32; y and its gradient have
+    replay takes its draws.  Recording in a capture is refused while a graph
+    from outside it lives (so with torch.cuda.make_graphed_callables, which
+    keeps its last warm-up pass).  x is bfloat16 or float32; y and its gradient have
     x's type, the weight (``in_features x out_features``) and its gradient are
     float32.  A product over more than 131071 (tokens, for the weight's
     gradient) is taken in runs of codes, whose binary32 products are added; the

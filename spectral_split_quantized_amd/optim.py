@@ -58,8 +58,8 @@ class AdamW(torch.optim.Optimizer):
         self.state_bits, self.min_8bit_size = state_bits, min_8bit_size
         self.rounding = metis.SR if rounding == "sr" else metis.RNE
         self.seed, self.max_norm, self.capturable = seed, max_norm, capturable
-        self.grad_norm = None
-        self._clip = None
+        self.grad_norm = self._clip = None
+        self._apart = {}
 
     def _init_state(self, p, count=None):
         """A new state; ``count``: the step count tensor it shares, if any."""
@@ -119,8 +119,7 @@ class AdamW(torch.optim.Optimizer):
     def _sorted_calls(self, group, first, capturing):
         """A group's calls where its parameters are not all alike: without a
         gradient (left out), without a state (made), with a gradient to be
-        copied into rows, or with step counts of their own (a call each; counts
-        on the GPU are told apart as tensors, their values stay there)."""
+        copied into rows, or with step counts of their own (a call each)."""
         have = [(first + i, p) for i, p in enumerate(group["params"]) if p.grad is not None]
         if self.capturable and len(have) != len(group["params"]):
             raise RuntimeError("with capturable=True every parameter needs a gradient")
@@ -130,6 +129,8 @@ class AdamW(torch.optim.Optimizer):
         count = torch.zeros((), dtype=torch.int64, device=new[0].device) if new and self.capturable else None
         for p in new:
             self._init_state(p, count)
+        if self.capturable and not capturing:
+            self._share_counts([self.state[p] for _, p in have])
         sets = {}
         for i, p in have:
             count = self.state[p]["step"]
@@ -144,12 +145,26 @@ class AdamW(torch.optim.Optimizer):
             calls.append((group, table, device, states[0]["step"], states, grads))
         return calls
 
+    def _share_counts(self, states):
+        """One tensor for equal counts on the GPU.  Reads them, once for tensors
+        that turn out to differ: they go up together from then on."""
+        counts = {id(s["step"]): s["step"] for s in states}
+        if len(counts) < 2 or counts.keys() <= self._apart.keys():
+            return
+        first, shared = {}, {}
+        for (i, c), value in zip(counts.items(), torch.cat([c.reshape(1) for c in counts.values()]).tolist()):
+            shared[i] = first.setdefault(value, c)
+        for s in states:
+            s["step"] = shared[id(s["step"])]
+        self._apart.update((id(c), c) for c in first.values())
+
     def __getstate__(self):
         return {**super().__getstate__(), **{k: getattr(self, k) for k in _SETTINGS}}
 
     def __setstate__(self, state):
         super().__setstate__(state)
         self.grad_norm = self._clip = None
+        self._apart = {}
 
     def load_state_dict(self, state_dict):
         """As torch's, but the states keep their own types (torch would cast

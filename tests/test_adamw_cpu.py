@@ -98,6 +98,26 @@ def test_equal_counts_are_one_tensor_advanced_once(runs):
     assert all(int(s["step"]) == 1 for s in opt.state.values())  # loading takes copies
 
 
+def test_equal_counts_on_tensors_of_their_own_are_joined(runs, monkeypatch):
+    """States set by hand or by another loader, a count tensor each: one call a
+    value, and the values are read once, not in every step."""
+    ps = _params(5)
+    opt = optim.AdamW(ps, capturable=True)
+    for p, t in zip(ps, (7, 7, 2, 7, 2)):
+        opt._init_state(p)["step"] = torch.tensor(t)
+    read, cat = [], torch.cat
+    monkeypatch.setattr(torch, "cat", lambda ts: read.append(len(ts)) or cat(ts))
+    for k in (1, 2, 3):
+        runs.clear()
+        opt.step()
+        assert [_taken(runs)[p] for p in ps] == [7 + k, 7 + k, 2 + k, 7 + k, 2 + k] and len(runs) == 2
+    assert read == [5]
+    opt.state[ps[4]]["step"] = torch.tensor(10)  # set by hand to what the first ones have
+    runs.clear()
+    opt.step()
+    assert [_taken(runs)[p] for p in ps] == [11, 11, 6, 11, 11] and len(runs) == 2 and read == [5, 3]
+
+
 def test_oracle_keeps_values_that_are_not_finite_out_of_the_scale():
     x = np.linspace(0.1, 1.0, 300).astype(np.float32)
     want, s = adamw.encode(x)
