@@ -23,10 +23,12 @@
 //
 // A wave takes four state blocks, a lane four consecutive elements of each, so
 // a block's maxima are joined inside the wave and every load of the wave is in
-// flight at once.  Bound by HBM: 176 M binary32 elements in 816-910 us with
-// 32-bit states (28 bytes an element, 5.4-6.0 TB/s) and in 470-530 us with 8-bit
-// states rounded stochastically (16.06 bytes, 5.3-6.0 TB/s); a copy runs at 5.1.  With 8
-// bits the vector units are close behind: 94 instructions an element.
+// flight at once.  Bound by HBM: 176 M binary32 elements in 827-915 us with
+// 32-bit states (28 bytes an element, 5.4-6.0 TB/s between cards) and in 536 us
+// with 8-bit states rounded stochastically (16.06 bytes, 5.3 TB/s); a copy runs
+// at 5.1.  bf16 parameters and gradients with 32-bit states: 783 us (24 bytes,
+// 5.4 TB/s).  With 8 bits the vector units are close behind: 95 instructions an
+// element.
 #pragma once
 
 #include "common.hpp"
@@ -324,8 +326,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamTable<EIGHT> t) {
 //
 // Squares are exact in binary64 and summed there, in an order that the sizes
 // alone fix, so the norm does not depend on how the work is spread.  One read
-// of the gradients (148 tensors, 57 MB), then a
-// workgroup that joins the partial sums (2 us).
+// of the gradients (148 tensors, 57 MB: 12 us), then a workgroup that joins the
+// partial sums (4 us, latency).
 __global__ __launch_bounds__(256) void grad_norm_kernel(NormTable t) {
   __shared__ double red[4];
   const int ti = table_index<kNormTensors>(t.first, t.count, blockIdx.x);

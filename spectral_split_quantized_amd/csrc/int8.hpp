@@ -176,10 +176,10 @@ __device__ inline float i8_absmax8(const float (&x)[8], float m, bool& bad) {
 //
 // One workgroup of 64 W threads per row; each thread holds CH chunks of eight
 // elements (chunk t + 64 W j).  Longer rows are read a second time (from L2).
-// Bound by HBM to nearest (16384 x 4096 bf16: 31 us, 201 MB) and by the vector
-// units stochastically (45 us: ten Philox rounds for eight elements); W CH 512
+// Bound by HBM to nearest (16384 x 4096 bf16: 32 us, 201 MB) and by the vector
+// units stochastically (48 us: ten Philox rounds for eight elements); W CH 512
 // elements cover the row with as few idle threads as the sizes allow (4096
-// columns: 4 waves of two chunks 31 us, 8 waves half idle 42).
+// columns: 4 waves of two chunks 32 us, 8 waves half idle 42).
 template <int W, int CH, bool SR>
 __global__ __launch_bounds__(64 * W) void i8_quant_rows_kernel(I8QuantParams p) {
   constexpr int T = 64 * W;
@@ -245,10 +245,12 @@ __global__ __launch_bounds__(64 * W) void i8_quant_rows_kernel(I8QuantParams p) 
 // through LDS: 256 threads on 128 x 128, thread t the column chunk
 // 8 (t % 16) .. + 7 of rows 4 (t / 16) .. + 3 and of the rows 64 further down,
 // so that both orientations are written in whole 128-byte lines.
-// 16384 x 4096 bf16, both orientations: the first sweep 24 us (134 MB, the
+// 16384 x 4096 bf16, both orientations: the first sweep 23 us (134 MB, the
 // second reading of them comes partly from the last-level cache), the second
-// 53 us to nearest (268 MB, the rate of a copy) and 75 us stochastically
-// (vector units: Philox and two roundings an element).  Scales joined in a
+// 52 us to nearest (268 MB, the rate of a copy) and 73 us stochastically
+// (vector units: Philox and two roundings an element).  Every tile joins the
+// maxima of its lines, 68 KB here and more with every row: 131072 rows take
+// 995 us, 13.6 times as long.  Scales joined in a
 // kernel of their own cost 39 us at one thread a line.
 constexpr int kI8Tile = 128;
 constexpr int kI8AmaxCols = 512;
@@ -425,7 +427,7 @@ __global__ __launch_bounds__(256) void i8_quant_tile_kernel(I8QuantParams p) {
 // 16 x 16 x 64: lane l takes 16 bytes of row l % 16 at 16 (l / 16); the
 // token is the only row of the first operand that is not zero.
 // CH: chunks of eight elements a thread holds of the token.
-// Bound by the weight's bytes: 4096 -> 14336 in 13.1 us (58.7 MB, 4.5 TB/s);
+// Bound by the weight's bytes: 4096 -> 14336 in 13.4 us (58.7 MB, 4.4 TB/s);
 // quantiser and product as two launches 16.7.
 constexpr int64_t kI8TokenPitch = 16384;  // longest token: 512 threads of 4 chunks
 

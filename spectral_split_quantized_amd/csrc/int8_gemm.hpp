@@ -117,11 +117,11 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 // ahead of the products, across tiles, and the epilogue, which has LDS of its
 // own (ER rows a wave), stands between two matrix instructions.
 //
-// 16384 x 14336 x 4096 to bf16, 256 x 256 tiles of 8 waves: 770 us, 2.5 POP/s.
-// The matrix cores are busy 64% of the cycles and power holds the clock at 1.7
-// to 1.9 GHz, so fewer idle cycles buy less than their share of time.  LDS is
-// active 27% of them; four waves of 128 x 128 read less of it but leave a SIMD
-// one wave, whose waits nothing fills (1320 us against 1110 at that stage).
+// 16384 x 14336 x 4096 to bf16, 256 x 256 tiles of 8 waves: 766 us, 2.5 POP/s.
+// The matrix cores are busy 66% of the cycles, at a clock of 1.66 GHz (both
+// under counters), and LDS is active 28% of them; four waves of 128 x 128 read
+// less of it but leave a SIMD one wave, whose waits nothing fills (1320 us
+// against 1110 at that stage).
 //
 // Rows past M / N repeat the last row (never stored).
 template <int WM, int WN, int TM, int NS, int ER, I8Out OUT>
@@ -416,8 +416,8 @@ __global__ __launch_bounds__(64) void i8_join_kernel(I8GemmParams p) {
 // the waves taking turns along K in steps of U x 64 bytes, so that a wave
 // keeps U loads of B in flight; the partial sums meet in LDS.  The
 // instruction is 16 x 16 x 64: lane l takes 16 bytes of row l % 16 at
-// 16 (l / 16).  Bound by B's bytes (1 x 14336 x 4096: 13.5 us, 4.3 TB/s) and,
-// towards 16 tokens, by fetching A again for every 16 rows of B (20 us).
+// 16 (l / 16).  Bound by B's bytes (1 x 14336 x 4096: 12.1 us, 4.9 TB/s) and,
+// towards 16 tokens, by fetching A again for every 16 rows of B (17.8 us).
 template <int NW, int U>
 __global__ __launch_bounds__(64 * NW) void i8_gemm_skinny_kernel(I8GemmParams p) {
   __shared__ i32x4_t red[NW - 1][64];
