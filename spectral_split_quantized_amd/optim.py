@@ -105,7 +105,10 @@ class AdamW(torch.optim.Optimizer):
             metis._grad_norm_run(whole, device, self.max_norm, self._clip)
             self.grad_norm, clip = self._clip[0], self._clip[1]
         if self.capturable:
-            torch._foreach_add_(list({id(c[3]): c[3] for c in calls}.values()), 1)
+            counts = {id(c[3]): c[3] for c in calls}
+            if capturing:
+                self._apart.update(counts)
+            torch._foreach_add_(list(counts.values()), 1)
         for group, table, device, count, states, _ in calls:
             if not self.capturable:
                 count += 1
@@ -146,17 +149,17 @@ class AdamW(torch.optim.Optimizer):
         return calls
 
     def _share_counts(self, states):
-        """One tensor for equal counts on the GPU.  Reads them, once for tensors
-        that turn out to differ: they go up together from then on."""
-        counts = {id(s["step"]): s["step"] for s in states}
-        if len(counts) < 2 or counts.keys() <= self._apart.keys():
-            return
+        """One tensor for equal counts on the GPU, of tensors that come here for
+        the first time: those read before differ and go up together, and those
+        of a capture are its replays'."""
+        new = {id(s["step"]): s["step"] for s in states if id(s["step"]) not in self._apart}
         first, shared = {}, {}
-        for (i, c), value in zip(counts.items(), torch.cat([c.reshape(1) for c in counts.values()]).tolist()):
-            shared[i] = first.setdefault(value, c)
-        for s in states:
-            s["step"] = shared[id(s["step"])]
-        self._apart.update((id(c), c) for c in first.values())
+        if len(new) > 1:
+            for (i, c), value in zip(new.items(), torch.cat([c.reshape(1) for c in new.values()]).tolist()):
+                shared[i] = first.setdefault(value, c)
+            for s in states:
+                s["step"] = shared.get(id(s["step"]), s["step"])
+        self._apart.update((id(s["step"]), s["step"]) for s in states)
 
     def __getstate__(self):
         return {**super().__getstate__(), **{k: getattr(self, k) for k in _SETTINGS}}

@@ -112,10 +112,24 @@ def test_equal_counts_on_tensors_of_their_own_are_joined(runs, monkeypatch):
         opt.step()
         assert [_taken(runs)[p] for p in ps] == [7 + k, 7 + k, 2 + k, 7 + k, 2 + k] and len(runs) == 2
     assert read == [5]
-    opt.state[ps[4]]["step"] = torch.tensor(10)  # set by hand to what the first ones have
+    opt.state[ps[4]]["step"] = torch.tensor(10)  # set by hand
     runs.clear()
     opt.step()
-    assert [_taken(runs)[p] for p in ps] == [11, 11, 6, 11, 11] and len(runs) == 2 and read == [5, 3]
+    assert [_taken(runs)[p] for p in ps] == [11, 11, 6, 11, 11] and read == [5]
+
+
+def test_count_tensors_of_a_capture_are_not_replaced(runs, monkeypatch):
+    """Replays advance and read the memory of the capture, whatever an eager
+    step finds there later."""
+    ps = _params(3)
+    opt = optim.AdamW(ps, capturable=True)
+    counts = [opt._init_state(p)["step"] for p in ps]
+    with monkeypatch.context() as inside:
+        inside.setattr(torch.cuda, "is_available", lambda: True)
+        inside.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        opt.step()
+    opt.step()
+    assert all(opt.state[p]["step"] is c for p, c in zip(ps, counts)) and [int(c) for c in counts] == [2, 2, 2]
 
 
 def test_oracle_keeps_values_that_are_not_finite_out_of_the_scale():
