@@ -331,8 +331,8 @@ metis_status metis_mxfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, c
  * ceil(rows / 128) * ceil(cols / 128) below 2^24 (METIS_E_UNSUPPORTED above).
  *
  * metis_int8_quantize_counted: the same with the step read from the int64 at
- * step_count in device memory when the kernels run (for graphs, whose replays
- * would otherwise all take the draws of one step).
+ * step_count in device memory when the kernels run, unless that is negative
+ * (for graphs, whose replays would otherwise all take the draws of `step`).
  *
  * metis_int8_gemm: C = diag(s_A) (A B^T) diag(s_B), row-major with leading
  * dimension ldc >= B->n_outer, binary32 or bf16 (c_dtype).  A and B have the
@@ -366,7 +366,7 @@ metis_status metis_int8_quantize(const void *M, int32_t dtype, int64_t rows, int
                                  void *stream);
 metis_status metis_int8_quantize_counted(const void *M, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
                                          int32_t axes, int32_t rounding, uint64_t seed, uint32_t tag,
-                                         const int64_t *step_count, const metis_i8 *ax0, const metis_i8 *ax1,
+                                         int64_t step, const int64_t *step_count, const metis_i8 *ax0, const metis_i8 *ax1,
                                          void *ws, size_t ws_bytes, void *stream);
 size_t metis_int8_gemm_workspace(int64_t M, int64_t N, int64_t k_len);
 metis_status metis_int8_gemm(const metis_i8 *A, const metis_i8 *B, void *C, int32_t c_dtype, int64_t ldc,

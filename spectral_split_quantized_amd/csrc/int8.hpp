@@ -43,9 +43,12 @@ struct I8QuantParams {
   int sr;
   uint64_t seed;
   uint32_t tag, step;
-  const int64_t* step_count;  // the step in device memory, or null: `step`
+  const int64_t* step_count;  // the step in device memory where not negative, or null
 
-  __device__ uint32_t step_now() const { return step_count ? (uint32_t)*step_count : step; }
+  __device__ uint32_t step_now() const {
+    const int64_t count = step_count ? *step_count : -1;
+    return count < 0 ? step : (uint32_t)count;
+  }
 };
 
 __device__ inline float i8_scale(float amax) { return fmaxf(__fdiv_rn(amax, 127.0f), 0x1p-126f); }

@@ -1217,7 +1217,7 @@ metis_status run_int8_quant(const void* M, int dtype, int64_t rows, int64_t cols
   return METIS_OK;
 }
 
-// the step from the host, or (step_count not null) from device memory
+// the step from the host or (step_count not null) from device memory
 metis_status int8_quantize_at(const void* M, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int32_t axes,
                               int32_t rounding, uint64_t seed, uint32_t tag, int64_t step,
                               const int64_t* step_count, const metis_i8* ax0, const metis_i8* ax1, void* ws,
@@ -1782,11 +1782,11 @@ metis_status metis_int8_quantize(const void* M, int32_t dtype, int64_t rows, int
 }
 
 metis_status metis_int8_quantize_counted(const void* M, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
-                                         int32_t axes, int32_t rounding, uint64_t seed, uint32_t tag,
+                                         int32_t axes, int32_t rounding, uint64_t seed, uint32_t tag, int64_t step,
                                          const int64_t* step_count, const metis_i8* ax0, const metis_i8* ax1, void* ws,
                                          size_t ws_bytes, void* stream) {
   if (!step_count || ((uintptr_t)step_count & 7)) return fail(METIS_E_INVALID, "int8_quantize: step count pointer");
-  return int8_quantize_at(M, dtype, rows, cols, ld, axes, rounding, seed, tag, 0, step_count, ax0, ax1, ws, ws_bytes,
+  return int8_quantize_at(M, dtype, rows, cols, ld, axes, rounding, seed, tag, step, step_count, ax0, ax1, ws, ws_bytes,
                           stream);
 }
 

@@ -141,7 +141,7 @@ class _Int8LinearFn(torch.autograd.Function):
         ctx.save_for_backward(q0 and q0.codes, q0 and q0.scales, q1 and q1.codes, q1 and q1.scales)
         ctx.lead, ctx.x_dtype, ctx.w_shape = x.shape[:-1], x.dtype, w.shape
         ctx.rounding, ctx.seed, ctx.tag = mod.rounding, mod.seed, mod.tags["D"]
-        ctx.step = mod._count if capturing and mod._count is not None else mod.step
+        ctx.step, ctx.count = mod.step, mod._captured_count() if capturing else None
         return y.reshape(*ctx.lead, w.shape[1])
 
     @staticmethod
@@ -156,7 +156,7 @@ class _Int8LinearFn(torch.autograd.Function):
             return dx, dw, None, None
         xc, xs, wc, ws = ctx.saved_tensors
         qd = metis.int8_quantize(d2, (metis.AXIS1 if need_x else 0) | (metis.AXIS0 if need_w else 0),
-                                 rounding=ctx.rounding, seed=ctx.seed, tag=ctx.tag, step=ctx.step)
+                                 rounding=ctx.rounding, seed=ctx.seed, tag=ctx.tag, step=ctx.step, step_count=ctx.count)
         if need_x:
             dx = _product(qd.ax1, metis.I8.wrap(wc, ws, ctx.w_shape[1]), ctx.x_dtype).reshape(*ctx.lead, ctx.w_shape[0])
         if need_w:
@@ -173,7 +173,7 @@ class Int8Linear(torch.nn.Module):
     default, with the draws of ``seed``, ``layer`` and the step that
     :func:`set_step` sets) or to nearest ("rne").  Passes captured into a graph
     read the step on the GPU: set it between replays, on their stream, and a
-    replay takes its draws.  Recording in a capture is refused while a graph
+    replay takes its draws (until then, those of the capture's step).  Recording in a capture is refused while a graph
     from outside it lives (so with torch.cuda.make_graphed_callables, which
     keeps its last warm-up pass).  x is bfloat16 or float32; y and its gradient have
     x's type, the weight (``in_features x out_features``) and its gradient are
@@ -204,20 +204,26 @@ class Int8Linear(torch.nn.Module):
 
     @step.setter
     def step(self, step):
-        if self._count is not None:
+        if self._replayed:
             if _capturing(self._count):
                 raise RuntimeError("set the step outside the capture: replays read the one that is set then")
             self._count.fill_(step)
         self._step = step
 
     def _make_count(self):
-        # the step on the weight's GPU, for captured passes; the same memory for
-        # as long as the weight stays there
-        if self.rounding != metis.SR or not self.weight.is_cuda:
-            self._count = None
-        elif self._count is None or self._count.device != self.weight.device:
+        # the step on the weight's GPU, for captured passes: -1 until it is set
+        # after the first of them.  The same memory for as long as the weight
+        # stays there.
+        if self._count is not None and self._count.device == self.weight.device:
+            return
+        self._count, self._replayed = None, False
+        if self.rounding == metis.SR and self.weight.is_cuda:
             with torch.inference_mode(False):
-                self._count = torch.full((), self._step, dtype=torch.int64, device=self.weight.device)
+                self._count = torch.full((), -1, dtype=torch.int64, device=self.weight.device)
+
+    def _captured_count(self):
+        self._replayed = self._count is not None
+        return self._count
 
     def _apply(self, fn, recurse=True):
         super()._apply(fn, recurse)

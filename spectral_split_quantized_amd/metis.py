@@ -99,7 +99,7 @@ def load():
     lib.metis_int8_quantize.argtypes = [P, i32, i64, i64, i64, i32, i32, ctypes.c_uint64, u32, i64,
                                         ctypes.POINTER(_I8), ctypes.POINTER(_I8), P, sz, P]
     lib.metis_int8_quantize.restype = i32
-    lib.metis_int8_quantize_counted.argtypes = [P, i32, i64, i64, i64, i32, i32, ctypes.c_uint64, u32, P,
+    lib.metis_int8_quantize_counted.argtypes = [P, i32, i64, i64, i64, i32, i32, ctypes.c_uint64, u32, i64, P,
                                                 ctypes.POINTER(_I8), ctypes.POINTER(_I8), P, sz, P]
     lib.metis_int8_quantize_counted.restype = i32
     lib.metis_int8_gemm_workspace.argtypes = [i64, i64, i64]
@@ -651,15 +651,15 @@ class I8Operand:
         self.ax1 = I8(rows, cols, device) if axes & AXIS1 else None
 
 
-def int8_quantize(M, axes=AXIS1, out=None, rounding=RNE, seed=0, tag=0, step=0, workspace=None):
+def int8_quantize(M, axes=AXIS1, out=None, rounding=RNE, seed=0, tag=0, step=0, workspace=None, step_count=None):
     """int8 codes and scales of M (metis_int8_quantize) along the requested
     axes, rounded to nearest (RNE) or stochastically (SR, draws from seed, tag
-    and step; a one-element int64 tensor is read when the kernels run)."""
+    and step, or where step_count, a one-element int64 tensor, is not negative
+    when the kernels run, of that step)."""
     _rows_check(M)
     rows, cols = M.shape
     dtype = _dtype_code(M)
-    counted = isinstance(step, torch.Tensor)
-    if counted and (step.dtype != torch.int64 or step.numel() != 1):
+    if step_count is not None and (step_count.dtype != torch.int64 or step_count.numel() != 1):
         raise ValueError("a step count tensor must be one int64")
     if out is None:
         out = I8Operand(rows, cols, axes, M.device)
@@ -671,14 +671,17 @@ def int8_quantize(M, axes=AXIS1, out=None, rounding=RNE, seed=0, tag=0, step=0, 
                              % (out.rows, out.cols, out.axes, rows, cols, axes))
         c0, c1 = out.ax0 and out.ax0._c(), out.ax1 and out.ax1._c()
         parts = [t for q in (out.ax0, out.ax1) if q for t in (q.codes, q.scales)]
-    with _on_device(M, *parts, *((step,) if counted else ())):
+    with _on_device(M, *parts, *(() if step_count is None else (step_count,))):
         lib = load()
         need = lib.metis_int8_quantize_workspace(rows, cols, axes) if axes & AXIS0 else 0  # rows alone need none
         ws = _space(workspace, need, M.device)
-        quantize = lib.metis_int8_quantize_counted if counted else lib.metis_int8_quantize
-        _check(quantize(M.data_ptr(), dtype, rows, cols, _leading(M), axes, rounding, seed, tag,
-                        step.data_ptr() if counted else step, c0 and ctypes.byref(c0), c1 and ctypes.byref(c1),
-                        _ptr(ws), need if ws is None else ws.numel(), _raw_stream()))
+        c0, c1, room = c0 and ctypes.byref(c0), c1 and ctypes.byref(c1), need if ws is None else ws.numel()
+        if step_count is None:
+            _check(lib.metis_int8_quantize(M.data_ptr(), dtype, rows, cols, _leading(M), axes, rounding, seed, tag, step,
+                                           c0, c1, _ptr(ws), room, _raw_stream()))
+        else:
+            _check(lib.metis_int8_quantize_counted(M.data_ptr(), dtype, rows, cols, _leading(M), axes, rounding, seed, tag,
+                                                   step, step_count.data_ptr(), c0, c1, _ptr(ws), room, _raw_stream()))
     return out
 
 

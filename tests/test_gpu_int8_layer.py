@@ -25,6 +25,7 @@ def _gpu():
         pytest.fail("GPU tests need an MI355X; none is visible")
     metis.load()
     torch.cuda.set_device(0)
+    metis.init_device()
 
 
 @pytest.mark.parametrize("axes", [metis.AXIS0, metis.AXIS1, BOTH])
@@ -33,9 +34,9 @@ def test_quantize_with_a_step_on_the_gpu(axes):
     g = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn(130, 333, generator=g, device="cuda")
     count = torch.zeros(1, dtype=torch.int64, device="cuda")
-    for step in (0, 1, 7, 2 ** 31 + 5):
-        count.fill_(step)
-        a = metis.int8_quantize(x, axes, rounding=metis.SR, seed=3, tag=9, step=count)
+    for step in (0, 1, 7, 2 ** 31 + 5, 4):
+        count.fill_(-1 if step == 4 else step)  # negative: the call's own step
+        a = metis.int8_quantize(x, axes, rounding=metis.SR, seed=3, tag=9, step=4, step_count=count)
         b = metis.int8_quantize(x, axes, rounding=metis.SR, seed=3, tag=9, step=step)
         for p, q in ((a.ax0, b.ax0), (a.ax1, b.ax1)):
             assert (p is None) == (q is None)
@@ -60,7 +61,7 @@ def test_captured_layer_takes_the_draws_of_the_step_that_is_set():
         with pytest.raises(RuntimeError, match="outside the capture"):
             set_step(lin, 12)
     seen = []
-    for step in (None, 12, 13, 13, 5):  # None: the step that was set before the capture
+    for step in (None, 12, 13, 13, 5):  # None: the step of the capture
         if step is not None:
             set_step(lin, step)
         assert lin.step == (11 if step is None else step)
@@ -80,17 +81,26 @@ def test_captured_layer_takes_the_draws_of_the_step_that_is_set():
 
 
 def test_step_follows_copies_and_moves():
+    x = torch.randn(5, 16, device="cuda", requires_grad=True)
     lin = Int8Linear(16, 8)
     lin.step = 4
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lin(x)
+        assert lin.to("cuda").float() is lin  # the graph's address stays
+    at = lin._count.data_ptr()
+    assert lin._count.item() == -1
+    lin.step = 5
+    assert lin.to("cuda").float()._count.data_ptr() == at and lin._count.item() == lin.step == 5
     twin = copy.deepcopy(lin)
     twin.step = 6
+    assert lin.step == 5 and twin.step == 6 and lin._count.item() == 5 and twin._count.data_ptr() != at
     moved = Int8Linear(16, 8, device="cpu")
     moved.step = 9
-    moved = moved.to("cuda").float()
-    assert [(m.step, m._count.item()) for m in (lin, twin, moved)] == [(4, 4), (6, 6), (9, 9)]
-    at = lin._count.data_ptr()  # a captured graph's address
-    assert lin.to("cuda").float()._count.data_ptr() == at
+    moved = moved.to("cuda")
+    assert moved.step == 9 and moved._count.is_cuda
     assert Int8Linear(16, 8, rounding="rne")._count is None and moved.cpu()._count is None
+    del y
 
 
 def _runs(a, b):

@@ -19,7 +19,7 @@ def test_step_count_pointer_and_tensor_are_checked():
 
     def counted(count, ax1=True, rounding=1):
         q = metis._I8(4096, 4096, 64, 48)
-        return lib.metis_int8_quantize_counted(D, 0, 64, 48, 48, 2, rounding, 0, 0, count, None,
+        return lib.metis_int8_quantize_counted(D, 0, 64, 48, 48, 2, rounding, 0, 0, 0, count, None,
                                                ctypes.byref(q) if ax1 else None, None, 0, None)
 
     assert counted(None) == metis.E_INVALID and counted(ctypes.c_void_p(4100)) == metis.E_INVALID
@@ -27,7 +27,7 @@ def test_step_count_pointer_and_tensor_are_checked():
     x = torch.zeros(4, 8)
     for bad in (torch.zeros(1), torch.zeros(2, dtype=torch.int64), torch.zeros(1, dtype=torch.int32)):
         with pytest.raises(ValueError, match="int64"):
-            metis.int8_quantize(x, step=bad)
+            metis.int8_quantize(x, step_count=bad)
 
 
 def test_step_survives_copies():
