@@ -405,8 +405,8 @@ metis_status metis_int8_linear(const void *X, int32_t dtype, int64_t tokens, int
  * every other value is fixed at the call).
  * No array that is written may appear twice in a call or overlap another one,
  * a gradient included; gradients may overlap each other.
- * A tensor has at most 4096 (2^24 - 1) elements (METIS_E_UNSUPPORTED above), here
- * and in metis_grad_norm.  Small tensors share launches; the tensor list is
+ * A tensor has at most 4096 * (2^24 - 1) elements (METIS_E_UNSUPPORTED above),
+ * here and in metis_grad_norm.  Small tensors share launches; the tensor list is
  * read before the call returns.
  *
  * metis_grad_norm: out[0] = the square root of the sum of squares over all
