@@ -444,6 +444,102 @@ size_t metis_grad_norm_workspace(const metis_adamw_tensor *tensors, int64_t coun
 metis_status metis_grad_norm(const metis_adamw_tensor *tensors, int64_t count, double max_norm, float *out,
                              void *ws, size_t ws_bytes, void *stream);
 
+/* -------------------------------------------- around the linear layers
+ * What a language model has between its linear layers, before and behind them:
+ * layer norm, dropout, the embedding and the loss over the vocabulary, each
+ * with its gradients.  dtypes are metis_dtype; rows are row-major with a
+ * leading dimension of at least their length; sums are binary32 (binary64
+ * for the total loss), in an order fixed by the sizes, and each output is
+ * rounded once to its type.  Pointers are aligned to their values (rows that
+ * are 16-byte aligned run faster); an output may not overlap an input
+ * unless it is said below.  Zero rows or tokens are no error.  Argument errors
+ * return synchronously; nothing is allocated.
+ *
+ * metis_layernorm_fwd: y = (x - mean) rstd * weight + bias for each row of
+ * cols values, rstd = 1 / sqrt(variance + eps), the variance that of all cols
+ * values.  weight and bias (w_dtype) may be NULL: 1 and 0.  y has y_dtype.
+ * mean and rstd (rows binary32 each, both or neither NULL) are kept for the
+ * backward pass.  Y may be X where the types are equal.
+ * metis_layernorm_bwd: from dY (y_dtype), X and the forward pass's mean, rstd:
+ * dX (x's type), dweight and dbias (w_dtype); each of them may be NULL.  dX may
+ * be dY where the types are equal.  ws holds metis_layernorm_bwd_workspace(rows, cols)
+ * bytes, 256-byte aligned, where dweight or dbias is wanted.  1 <= cols < 2^31.
+ *
+ * metis_dropout: element e = i * cols + j takes the 16-bit Philox draw h(e) of
+ * (seed, tag with role 8, step), as in stochastic rounding; with t = 65536 p
+ * rounded to the nearest integer, ties to even,
+ *   y = (h < t ? 0 : x * s) + residual,  s = 65536 / (65536 - t) in binary32
+ * (s = 0 for t = 65536), residual may be NULL (then nothing is added).  A
+ * dropped x counts as zero whatever it holds.  The same call on dY, without a
+ * residual, gives dX.  X, residual and Y have one type; Y may be X or the
+ * residual.  step_count: NULL, or the int64 in device memory that holds the
+ * step when the kernel runs, unless it is negative (for graphs).
+ * 0 <= p <= 1, rows * cols < 2^63.
+ *
+ * metis_embedding_fwd: row i of Y is scale times row ids[i] of W (vocab x cols;
+ * id_bits 32 or 64: int32 or int64 ids), the product in binary32.  A number
+ * outside [0, vocab) sets the numeric flag and gives a row of zeros.
+ * metis_embedding_bwd: row v of dW is scale times the sum of the rows of dY
+ * whose id is v, over ascending rows in binary32 (in pieces of 16 of the sorted
+ * tokens); rows of dW that no token points to, and row padding (negative:
+ * none), are zero.  All of dW is written.  ws holds
+ * metis_embedding_bwd_workspace(tokens, cols) bytes, 256-byte aligned.
+ * vocab < 2^31, tokens < 2^31, cols < 2^31.
+ *
+ * metis_cross_entropy_fwd: the logits of token i are l_v = x_i . w_v (x: tokens
+ * x cols; w: vocab x cols), never stored; lse[i] = log sum_v exp l_v and
+ * losses[i] = lse[i] - l_target.  A target equal to ignore_index, or outside
+ * [0, vocab) (which sets the numeric flag), leaves the token out: its loss is
+ * 0 and its gradients are 0, whatever its row of x holds.  losses may be NULL.
+ * total: NULL, or two binary32: total[0] the sum of the losses (mean = 0) or
+ * their mean over the tokens that are not left out (mean = 1; 0 if all are),
+ * total[1] the number of those tokens.
+ * metis_cross_entropy_bwd: the gradients of x and w (their types; dX and dW may
+ * each be NULL) given lse and the gradient of each loss, grad[i] (grad_each =
+ * 1) or grad[0] for all (grad_each = 0), divided by *count where count is not
+ * NULL (total + 1 of the forward pass, for the mean).  Logits are formed again
+ * in pieces of the vocabulary, so the workspace does not grow with it.
+ * bf16 operands enter the products as they are; binary32 operands as two bf16
+ * parts (relative error at most 2^-16) where a loss or a binary32 gradient
+ * needs both.  Probabilities are rounded to bf16 (two parts for a binary32
+ * gradient) before the products of the gradients.
+ * ws holds metis_cross_entropy_workspace(l, backward) bytes, 256-byte aligned.
+ * tokens, cols <= 2^22, vocab < 2^31 (METIS_E_UNSUPPORTED above). */
+metis_status metis_layernorm_fwd(const void *X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                 const void *weight, const void *bias, int32_t w_dtype, double eps, void *Y,
+                                 int32_t y_dtype, int64_t ldy, float *mean, float *rstd, void *stream);
+size_t metis_layernorm_bwd_workspace(int64_t rows, int64_t cols);
+metis_status metis_layernorm_bwd(const void *dY, int32_t y_dtype, int64_t lddy, const void *X, int32_t x_dtype,
+                                 int64_t rows, int64_t cols, int64_t ldx, const void *weight, int32_t w_dtype,
+                                 const float *mean, const float *rstd, void *dX, int64_t lddx, void *dweight,
+                                 void *dbias, void *ws, size_t ws_bytes, void *stream);
+metis_status metis_dropout(const void *X, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
+                           int64_t ldr, double p, uint64_t seed, uint32_t tag, int64_t step, const int64_t *step_count,
+                           void *Y, int64_t ldy, void *stream);
+metis_status metis_embedding_fwd(const void *W, int32_t w_dtype, int64_t vocab, int64_t cols, int64_t ldw,
+                                 const void *ids, int32_t id_bits, int64_t tokens, double scale, void *Y,
+                                 int32_t y_dtype, int64_t ldy, void *stream);
+size_t metis_embedding_bwd_workspace(int64_t tokens, int64_t cols);
+metis_status metis_embedding_bwd(const void *dY, int32_t y_dtype, int64_t tokens, int64_t cols, int64_t lddy,
+                                 const void *ids, int32_t id_bits, int64_t vocab, int64_t padding, double scale,
+                                 void *dW, int32_t w_dtype, int64_t lddw, void *ws, size_t ws_bytes, void *stream);
+
+typedef struct {
+  const void *x, *w, *targets;
+  int64_t tokens, vocab, cols;
+  int64_t ldx, ldw;
+  int64_t ignore_index;
+  int32_t x_dtype, w_dtype;
+  int32_t target_bits; /* 32 or 64 */
+} metis_loss;
+
+size_t metis_cross_entropy_workspace(const metis_loss *l, int32_t backward);
+metis_status metis_cross_entropy_fwd(const metis_loss *l, float *losses, float *lse, int32_t mean, float *total, void *ws,
+                                     size_t ws_bytes, void *stream);
+metis_status metis_cross_entropy_bwd(const metis_loss *l, const float *lse, const float *grad, int32_t grad_each,
+                                     const float *count, void *dX, int64_t lddx, void *dW, int64_t lddw, void *ws,
+                                     size_t ws_bytes, void *stream);
+
 /* Kernel timing for benchmarks.  metis_timing_enable(capacity) creates
  * capacity pairs of HIP events (0 disables timing and releases them); while
  * enabled, each main split-GEMM kernel (kind 0; d = M, N, K, K-extension) and

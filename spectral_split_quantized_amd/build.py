@@ -20,6 +20,8 @@ TENSORS_OUT = os.path.join(HERE, "_tensors.so")
 UNITS = [
     ("metis.hip", []),
     ("gemm_big.hip", ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"]),
+    ("model.hip", []),
+    ("gemm_bf16.hip", []),  # (the strategy above ends the compiler on one of its kernels)
 ]
 
 FLAGS = [
@@ -89,22 +91,23 @@ SAN_OUT = os.path.join(OBJ, "libmetis_san.so")
 
 
 def build_host_sanitized(verbose=False):
-    """_build/libmetis_san.so: the C-ABI translation unit (metis.hip, all of
-    the host-side argument checking, workspace carving and scheduling) with
-    host ASan + UBSan, linked with the regular GEMM unit.  Load it with
-    METIS_LIBRARY set to its path and the ASan runtime preloaded; only calls
-    that need no GPU can run where there is none."""
+    """_build/libmetis_san.so: the C-ABI translation units (metis.hip and
+    model.hip, all of the host-side argument checking, workspace carving and
+    scheduling) with host ASan + UBSan, linked with the regular GEMM units.
+    Load it with METIS_LIBRARY set to its path and the ASan runtime preloaded;
+    only calls that need no GPU can run where there is none."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     os.makedirs(OBJ, exist_ok=True)
-    gemm_obj = os.path.join(OBJ, "gemm_big.o")
-    if not os.path.exists(gemm_obj):
+    gemms = [os.path.join(OBJ, o) for o in ("gemm_big.o", "gemm_bf16.o")]
+    if not all(os.path.exists(o) for o in gemms):
         build(verbose)
-    obj = os.path.join(OBJ, "metis_san.o")
     flags = [f for f in FLAGS if f != "-O3"] + ["-O1", "-g"] + HOST_SANITIZE
-    _run([hipcc] + flags + ["-c", os.path.join(CSRC, "metis.hip"), "-o", obj], verbose)
+    objs = []
+    for src in ("metis", "model"):
+        objs.append(os.path.join(OBJ, src + "_san.o"))
+        _run([hipcc] + flags + ["-c", os.path.join(CSRC, src + ".hip"), "-o", objs[-1]], verbose)
     tmp = SAN_OUT + ".tmp"
-    _run([hipcc, "--offload-arch=gfx950", "-shared", "-fPIC"] + HOST_SANITIZE[:4] + [obj, gemm_obj, "-o", tmp],
-         verbose)
+    _run([hipcc, "--offload-arch=gfx950", "-shared", "-fPIC"] + HOST_SANITIZE[:4] + objs + gemms + ["-o", tmp], verbose)
     os.replace(tmp, SAN_OUT)
     return SAN_OUT
 

@@ -1,0 +1,434 @@
+// bf16_gemm.hpp -- A B^T of bf16 operands on gfx950's matrix instructions, with
+// the epilogues of the loss over a vocabulary.
+//
+// Both operands lie with K along the row, at a pitch that is a multiple of 64
+// values, zeros behind K.  A binary32 operand is a pair of bf16 planes, hi = x
+// rounded and lo = the rest rounded (off by 2^-16 of x at most), and the
+// product is the sum of up to three products of planes (hi hi, hi lo, lo hi;
+// lo lo is no larger than the planes' own error), which simply follow each
+// other along K.  Products of bf16 values are exact, sums are binary32.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "rows.hpp"
+
+namespace metis {
+
+enum BfOut : int {
+  kBfStats,  // softmax statistics of the rows
+  kBfProb,   // scaled probabilities minus one at the target, bf16 planes
+  kBfF32,    // C, binary32, stored or added; with splits one C for each
+  kBfBF16    // C, bf16
+};
+
+struct BfGemmParams {
+  int64_t M, N;
+  const uint8_t *a, *b;
+  int64_t pitch_a, pitch_b;   // bytes between rows, multiples of 128
+  int runs, run_stages;       // K: `runs` products of planes of run_stages stages of 64 each
+  int64_t at_a[3], at_b[3];   // where the planes of a run begin, bytes
+  int splits, split_stages;   // all stages cut into splits of split_stages (the last may be shorter)
+  // kBfF32, kBfBF16
+  void* C;
+  int64_t ldc;
+  int64_t split_ld;           // values between the C of two splits
+  int add;                    // kBfF32: C += (else C =)
+  // kBfStats, kBfProb: row i is token i, column j word v0 + j
+  int64_t v0;
+  const void* targets;        // [M]
+  int targets64;
+  int64_t vocab, ignore;
+  float2* stat;               // [ceil(N / 64) of all words][M]: largest logit, sum of exponentials
+  float* target_logit;        // [M]
+  const float* lse;           // [M]
+  const float* grad;          // [M], or one with `count`
+  const float* count;         // tokens that the loss is the mean over, or null
+  int grad_each;              // grad has a value for each token
+  uint16_t* prob;             // [M][ldp], and lo_plane values behind it the low planes
+  int64_t ldp, lo_plane;      // lo_plane 0: none
+};
+
+typedef __bf16 bf16x8v_t __attribute__((ext_vector_type(8)));
+typedef float f32x16v_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4v_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+// Global -> LDS load of 16 bytes a lane to LDS address lds + 16 lane (base and
+// lds wave-uniform), as assembly so that the compiler does not wait for the
+// loads in flight before every LDS read.  A wait state stands between the
+// write of M0 and its use, and five before the first use of a base, which a
+// vector instruction just before may have written.
+template <bool FIRST>
+__device__ __forceinline__ void bf_dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
+  if constexpr (FIRST)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+                 : "memory", "m0");
+}
+
+// the word of token `row`, or -1 where it has no part in the loss
+__device__ __forceinline__ int64_t target_of(const void* targets, int targets64, int64_t ignore, int64_t vocab, int64_t row) {
+  const int64_t t = targets64 ? ((const int64_t*)targets)[row] : (int64_t)((const int32_t*)targets)[row];
+  return t == ignore || t < 0 || t >= vocab ? -1 : t;
+}
+
+// WM x WN waves of TM x 2 tiles of 32 x 32, one workgroup for many tiles of C,
+// built as the int8 product (the instruction's lane takes the same 16
+// K-consecutive bytes): K-stages of 128 bytes (64 values) travel global -> LDS
+// by DMA into a ring of NS slots; a row's 16-byte chunk c lies at R * 128 +
+// (c ^ (R / 2 % 8)) * 16, so that lanes that read together hit all banks
+// once; each sub-step reads the next one's fragments under its matrix
+// instructions, and the loads run NS stages ahead of the products, across
+// tiles.  B is the instruction's first operand: a lane ends up with row
+// lane % 32 of a tile of C and columns 8 g + 4 (lane / 32) + v.
+//
+// Rows past M / N repeat the last row (never stored).
+template <int WM, int WN, int TM, int NS, int ER, BfOut OUT>
+__global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p) {
+  constexpr int TN = 2;
+  constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
+  constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128;
+  constexpr int PA = BM / 8 / NW, PB = BN / 8 / NW;
+  static_assert(PA * 8 * NW == BM && PB * 8 * NW == BN && (NS - 1) * (PA + PB) < 64, "DMA split");
+  __shared__ __attribute__((aligned(16))) uint8_t ring[NS * STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t ep[NW * ER * 128];
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = wave / WN, wn = wave % WN;
+  const uint32_t tiles_m = (uint32_t)ceil_div<int64_t>(p.M, BM), tiles_n = (uint32_t)ceil_div<int64_t>(p.N, BN);
+  const uint32_t total = tiles_m * tiles_n * p.splits, chunk = (total + 7) / 8;
+  const int stages = p.runs * p.run_stages;
+
+  // Workgroups go round the 8 XCDs; each XCD takes a contiguous run of tiles,
+  // in groups of 8 tile rows, so that its CUs share rows of both operands in
+  // its L2; the splits of one tile follow each other.  Sequence number q ->
+  // first row and column and the split, or none.
+  auto locate = [&](uint32_t q, int64_t& m0, int64_t& n0, int& split) {
+    const uint32_t ts = (q & 7) * chunk + (q >> 3);
+    if ((q >> 3) >= chunk || ts >= total) return false;
+    const uint32_t t = p.splits == 1 ? ts : ts / p.splits;
+    split = (int)(ts - t * p.splits);
+    const uint32_t g = t / (8 * tiles_n), in = t - g * 8 * tiles_n, rows = min(tiles_m - g * 8, 8u);
+    const uint32_t col = in / rows;
+    m0 = (int64_t)(g * 8 + in - col * rows) * BM;
+    n0 = (int64_t)col * BN;
+    return true;
+  };
+  uint32_t q = blockIdx.x, qi = q;  // of the products, of the loads
+  int64_t m0, n0;
+  int split;
+  if (!locate(q, m0, n0, split)) return;
+
+  // the loads: a DMA moves 8 rows, its lanes' offsets from the tile's first
+  // row fit 32 bits (256 rows at a pitch below 2^24 bytes)
+  const uint8_t *ga, *gb, *ra, *rb;  // at the next stage; of the tile's rows
+  uint32_t oa[PA], ob[PB];
+  int left, run, run_left;  // stages of the tile still to load; the run of planes and its stages left
+  auto begin_run = [&](int skip) {
+    ga = ra + p.at_a[run] + (int64_t)skip * 128;
+    gb = rb + p.at_b[run] + (int64_t)skip * 128;
+    run_left = p.run_stages - skip;
+  };
+  auto source = [&](int64_t m, int64_t n, int s) {
+    ra = p.a + m * p.pitch_a;
+    rb = p.b + n * p.pitch_b;
+    const int first = s * p.split_stages;
+    left = min(p.split_stages, stages - first);
+    run = first / p.run_stages;
+    begin_run(first - run * p.run_stages);
+    const int last_a = (int)min(p.M - 1 - m, (int64_t)BM), last_b = (int)min(p.N - 1 - n, (int64_t)BN);
+#pragma unroll
+    for (int d = 0; d < PA; ++d) {
+      const int r = (wave + d * NW) * 8 + (lane >> 3);
+      oa[d] = (uint32_t)min(r, last_a) * (uint32_t)p.pitch_a + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+    }
+#pragma unroll
+    for (int d = 0; d < PB; ++d) {
+      const int r = (wave + d * NW) * 8 + (lane >> 3);
+      ob[d] = (uint32_t)min(r, last_b) * (uint32_t)p.pitch_b + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+    }
+  };
+  const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)ring + wave * 1024;
+  auto issue = [&](int slot) {
+    if (left == 0) {  // on to the next tile, or, behind the last one, the same once more
+      int64_t m = m0, n = n0;
+      int s = split;
+      qi += gridDim.x;
+      locate(qi, m, n, s);
+      source(m, n, s);
+    } else if (run_left == 0) {
+      ++run;
+      begin_run(0);
+    }
+    const uint32_t at = base + slot * STAGE;
+    bf_dma16<true>(ga, oa[0], at);
+#pragma unroll
+    for (int d = 1; d < PA; ++d) bf_dma16<false>(ga, oa[d], at + d * NW * 1024);
+    bf_dma16<true>(gb, ob[0], at + A_BYTES);
+#pragma unroll
+    for (int d = 1; d < PB; ++d) bf_dma16<false>(gb, ob[d], at + A_BYTES + d * NW * 1024);
+    ga += 128;
+    gb += 128;
+    --left;
+    --run_left;
+  };
+
+  const int hh = lane >> 5, li = lane & 31, sx = (li >> 1) & 7;
+  f32x16v_t acc[TM][TN];
+  bf16x8v_t fa[2][TM], fb[2][TN];
+  auto read = [&](int slot, int kk) {
+    const uint8_t* const st = ring + slot * STAGE + li * 128 + ((2 * kk + hh) ^ sx) * 16;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) fa[kk & 1][i] = *(const bf16x8v_t*)(st + (wm * TM + i) * 4096);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb[kk & 1][j] = *(const bf16x8v_t*)(st + A_BYTES + (wn * TN + j) * 4096);
+  };
+  auto multiply = [&](int kk) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk & 1][j], fa[kk & 1][i], acc[i][j], 0, 0, 0);
+    // one LDS read after each of the first matrix instructions
+#pragma unroll
+    for (int t = 0; t < TM * TN; ++t) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (t < TM + TN) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // this wave's LDS reads are done and at most N of its loads in flight: with
+  // the barrier, a stage has landed and the one before it is read out
+  auto landed = [&](auto in_flight) {
+    constexpr int N = decltype(in_flight)::value;
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | (7 << 4) | (0 << 8));  // vmcnt(N) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // LDS operations of one wave complete in order; this keeps the compiler's order
+  auto wave_fence = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  };
+  using First = std::integral_constant<int, (NS - 1) * (PA + PB)>;
+  using Left = std::integral_constant<int, (NS - 2) * (PA + PB)>;
+
+  source(m0, n0, split);
+#pragma unroll
+  for (int s = 0; s < NS; ++s) issue(s);
+  landed(First{});
+  read(0, 0);
+  int slot = 0;
+  for (bool more = true; more;) {
+    const int nk = min(p.split_stages, stages - split * p.split_stages);
+    const int64_t row0 = m0 + wm * TM * 32, col0 = n0 + wn * TN * 32;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = f32x16v_t{};
+    for (int kt = 0; kt < nk; ++kt) {
+#pragma unroll
+      for (int kk = 0; kk < 3; ++kk) {
+        read(slot, kk + 1);
+        multiply(kk);
+      }
+      landed(Left{});
+      issue(slot);
+      slot = slot + 1 == NS ? 0 : slot + 1;
+      read(slot, 0);
+      multiply(3);
+    }
+
+    // the lane indices taken anew, so that what is made of them does not
+    // occupy registers all through the main loop
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    const int li = el & 31, hh = el >> 5, sx = (li >> 1) & 7;
+    // and the arguments read anew, so that they do not occupy scalar registers
+    auto args = (const __attribute__((address_space(4))) BfGemmParams*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(args));
+    const __attribute__((address_space(4))) BfGemmParams& p = *args;
+
+    if constexpr (OUT == kBfStats) {
+      // a row's 64 columns lie in two lanes, 32 values each
+      if (col0 < p.N) {
+        const int cols = (int)min((int64_t)64, p.N - col0);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const int64_t row = row0 + i * 32 + li;
+          const int64_t t = row < p.M ? target_of(p.targets, p.targets64, p.ignore, p.vocab, row) - p.v0 - col0 : -1;
+          const int at = t >= 0 && t < 64 ? (int)t : -1;
+          if (cols < 64) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3) >= cols) acc[i][j][e] = -__builtin_inff();
+          }
+          float m = -__builtin_inff();
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][j][e]);
+          const auto mm = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+          m = fmaxf(__uint_as_float(mm[0]), __uint_as_float(mm[1]));
+          const float off = m == -__builtin_inff() ? 0.0f : -m * kLog2E;
+          float s = 0.0f;
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2E, off));
+          const auto ss = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+          s = __uint_as_float(ss[0]) + __uint_as_float(ss[1]);
+          if (hh == 0 && row < p.M) p.stat[((p.v0 + col0) >> 6) * p.M + row] = make_float2(m, s);
+          if (__ballot(at >= 0)) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3) == at) p.target_logit[row] = acc[i][j][e];
+          }
+        }
+      }
+    } else {
+      constexpr bool BF = OUT != kBfF32;
+      uint8_t* const my = ep + wave * (ER * 128);
+      const int rr = el >> 3, rc = el & 7;  // read back: 8 rows of 8 chunks
+      // bf16: 32 rows of 64 columns a tile row, in chunks of 8 values; else 32
+      // rows of 32 columns, chunks of 4
+      constexpr int COLS = BF ? 64 : 32, PER = COLS / 8;
+      const bool lo_too = OUT == kBfProb && p.lo_plane != 0;
+      const int64_t N = OUT == kBfProb ? p.ldp : p.N, ld = OUT == kBfProb ? p.ldp : p.ldc;
+      uint16_t* const c16 = OUT == kBfProb ? p.prob : (uint16_t*)p.C;
+      const bool vec = OUT == kBfProb || (((uintptr_t)p.C & 15) == 0 && (p.ldc * (BF ? 2 : 4)) % 16 == 0);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        if constexpr (OUT == kBfProb) {
+          const int cols = (int)max((int64_t)0, min((int64_t)64, p.N - col0));
+          const int64_t row = min(row0 + i * 32 + li, p.M - 1);
+          const int64_t word = target_of(p.targets, p.targets64, p.ignore, p.vocab, row);
+          const int64_t t = word - p.v0 - col0;
+          const int at = word >= 0 && t >= 0 && t < 64 ? (int)t : -1;
+          float g = p.grad_each ? p.grad[row] : p.grad[0];
+          if (p.count) g /= p.count[0];
+          const float off = -p.lse[row] * kLog2E;
+          const bool some = word >= 0 && g != 0.0f;  // a token without a part: zeros, whatever its logits
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2E, off)) * g;
+              acc[i][j][e] = some ? v : 0.0f;
+            }
+          if (__ballot(some && at >= 0)) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (some && j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3) == at) acc[i][j][e] -= g;
+          }
+          if (cols < 64) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3) >= cols) acc[i][j][e] = 0.0f;
+          }
+        }
+#pragma unroll
+        for (int j0 = 0; j0 < TN; j0 += COLS / 32) {
+          for (int plane = 0; plane < 1 + (int)lo_too; ++plane) {
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += ER) {
+              if (ER == 32 || li / ER == r0 / ER) {
+#pragma unroll
+                for (int j = j0; j < j0 + COLS / 32; ++j)
+#pragma unroll
+                  for (int g = 0; g < 4; ++g) {
+                    float c[4];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) c[v] = acc[i][j][4 * g + v];
+                    uint8_t* const row = my + (li % ER) * 128;
+                    if constexpr (BF) {
+                      uint2 w = make_uint2(pack_bf16(c[0], c[1]), pack_bf16(c[2], c[3]));
+                      if (plane)
+                        w = make_uint2(pack_bf16(c[0] - unpack_bf16(w.x, 0), c[1] - unpack_bf16(w.x, 1)),
+                                       pack_bf16(c[2] - unpack_bf16(w.y, 0), c[3] - unpack_bf16(w.y, 1)));
+                      *(uint2*)(row + ((j * 4 + g) ^ sx) * 16 + hh * 8) = w;
+                    } else {
+                      *(float4*)(row + ((2 * g + hh) ^ sx) * 16) = make_float4(c[0], c[1], c[2], c[3]);
+                    }
+                  }
+              }
+              wave_fence();
+              const int64_t offset = OUT == kBfProb ? plane * p.lo_plane : split * p.split_ld;
+              if (vec) {
+#pragma unroll
+                for (int k = 0; k < ER / 8; ++k) {
+                  const int r = k * 8 + rr;
+                  u32x4v_t w = *(const u32x4v_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
+                  const int64_t row = row0 + i * 32 + r0 + r, col = col0 + j0 * 32 + rc * PER;
+                  if (row >= p.M) continue;
+                  const int64_t at = offset + row * ld + col;
+                  if (col + PER <= N) {
+                    u32x4v_t* const to = BF ? (u32x4v_t*)(c16 + at) : (u32x4v_t*)((float*)p.C + at);
+                    if constexpr (!BF) {
+                      if (p.add) {
+                        const u32x4v_t o = *to;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) + __uint_as_float(o[e]));
+                      }
+                    }
+                    *to = w;
+                  } else {
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) {
+                      if (col + e >= N) break;
+                      if constexpr (BF) {
+                        c16[at + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                      } else {
+                        float* const to = (float*)p.C + at + e;
+                        *to = __uint_as_float(w[e]) + (p.add ? *to : 0.0f);
+                      }
+                    }
+                  }
+                }
+              } else {
+                // rows of any alignment: neighbouring lanes write neighbouring values
+                constexpr int RS = 64 / COLS;  // rows a store
+                const int c = el & (COLS - 1);
+                const int64_t col = col0 + j0 * 32 + c;
+#pragma unroll
+                for (int k = 0; k < ER / RS; ++k) {
+                  const int r = k * RS + el / COLS;
+                  const uint8_t* const from = my + r * 128 + ((c / PER) ^ ((r >> 1) & 7)) * 16;
+                  const int64_t row = row0 + i * 32 + r0 + r;
+                  if (row >= p.M || col >= N) continue;
+                  const int64_t at = offset + row * ld + col;
+                  if constexpr (BF) {
+                    c16[at] = *((const uint16_t*)from + c % PER);
+                  } else {
+                    float* const to = (float*)p.C + at;
+                    *to = *((const float*)from + c % PER) + (p.add ? *to : 0.0f);
+                  }
+                }
+              }
+              wave_fence();
+            }
+          }
+        }
+      }
+    }
+    q += gridDim.x;
+    more = locate(q, m0, n0, split);
+  }
+  // no load may land in LDS that a later workgroup owns
+  __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (15 << 8));
+}
+
+}  // namespace metis

@@ -31,4 +31,14 @@ struct I8GemmParams;
 size_t i8_gemm_workspace(int64_t M, int64_t N, int64_t pitch);
 hipError_t launch_i8_gemm(const I8GemmParams& g, hipStream_t st);
 
+struct BfGemmParams;
+enum BfOut : int;
+
+// A B^T of bf16 planes (bf16_gemm.hpp).  splits > 1 (as bf_gemm_splits gives
+// it, at most bf_gemm_most_splits; kBfF32 only) writes one C for each part of
+// K; split_stages is set here.
+int bf_gemm_most_splits(int64_t M, int64_t N);
+int bf_gemm_splits(int64_t M, int64_t N, int stages);
+hipError_t launch_bf_gemm(const BfGemmParams& g, BfOut out, hipStream_t st);
+
 }  // namespace metis

@@ -17,6 +17,7 @@
 
 #include "../../include/metis.h"
 #include "common.hpp"
+#include "host.hpp"
 #include "gemm.hpp"
 #include "gemm_launch.hpp"
 #include "quant.hpp"
@@ -42,7 +43,9 @@ namespace {
 
 thread_local std::string g_last_error;
 
-metis_status fail(metis_status st, const char* fmt, ...) {
+}  // namespace
+
+metis_status metis::fail(metis_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -52,17 +55,7 @@ metis_status fail(metis_status st, const char* fmt, ...) {
   return st;
 }
 
-#define HIP_TRY(expr)                                                                     \
-  do {                                                                                    \
-    hipError_t e__ = (expr);                                                              \
-    if (e__ != hipSuccess) return fail(METIS_E_HIP, "%s: %s", #expr, hipGetErrorString(e__)); \
-  } while (0)
-
-#define LAUNCH_CHECK()                                                                    \
-  do {                                                                                    \
-    hipError_t e__ = hipGetLastError();                                                   \
-    if (e__ != hipSuccess) return fail(METIS_E_HIP, "kernel launch: %s", hipGetErrorString(e__)); \
-  } while (0)
+namespace {
 
 // ---------------------------------------------- benchmark instrumentation
 
@@ -146,10 +139,13 @@ const uint16_t* host_omega_table() {
 std::mutex g_dev_mu;
 bool g_dev_ready[64] = {false};
 void* g_scratch_ptr[64] = {nullptr};
+int* g_status_ptr[64] = {nullptr};
+
+}  // namespace
 
 // Once per device, with that device current: the Gaussian quantile table, the
 // numeric status word and the address of the static scratch array.
-metis_status ensure_device_tables() {
+metis_status metis::ensure_device_tables() {
   int dev = 0;
   HIP_TRY(hipGetDevice(&dev));
   if (dev < 0 || dev >= 64) return fail(METIS_E_UNSUPPORTED, "device index %d", dev);
@@ -162,10 +158,21 @@ metis_status ensure_device_tables() {
     HIP_TRY(hipGetSymbolAddress(&p, HIP_SYMBOL(scratch)));
     if (!p) return fail(METIS_E_HIP, "hipGetSymbolAddress(scratch) returned NULL");
     g_scratch_ptr[dev] = p;
+    HIP_TRY(hipGetSymbolAddress(&p, HIP_SYMBOL(g_metis_status)));
+    g_status_ptr[dev] = (int*)p;
     g_dev_ready[dev] = true;
   }
   return METIS_OK;
 }
+
+int* metis::device_status() {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return nullptr;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  return g_status_ptr[dev];
+}
+
+namespace {
 
 // This device's static scratch (after ensure_device_tables).
 void* device_scratch() {
@@ -177,27 +184,9 @@ void* device_scratch() {
 
 // ------------------------------------------------------------- workspace --
 
-struct Carver {
-  char* base;
-  size_t off = 0;
-  size_t cap;
-  explicit Carver(void* b, size_t c) : base((char*)b), cap(c) {}
-  template <typename T>
-  T* take(size_t count) {
-    off = (off + 255) & ~(size_t)255;
-    T* p = base ? (T*)(base + off) : nullptr;
-    off += count * sizeof(T);
-    return p;
-  }
-  size_t used() const { return (off + 255) & ~(size_t)255; }
-};
-
 inline int round_up(int a, int b) { return (a + b - 1) / b * b; }
-inline int64_t round_up64(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
 inline unsigned grid1(int64_t n, int block) { return (unsigned)((n + block - 1) / block); }
-
-bool dtype_ok(int32_t dt) { return dt == METIS_BF16 || dt == METIS_F32; }
 
 // --------------------------------------------------------- decomposition --
 
@@ -1710,7 +1699,7 @@ metis_status metis_status_sync(void* stream) {
   if (v != 0) {
     const int zero = 0;
     HIP_TRY(hipMemcpyToSymbol(HIP_SYMBOL(g_metis_status), &zero, sizeof(int)));
-    return fail(METIS_E_NUMERIC, "device numeric status 0x%x (1: non-finite input, 2: Cholesky, 4: sampler)", v);
+    return fail(METIS_E_NUMERIC, "device numeric status 0x%x (1: non-finite input, 2: Cholesky, 4: sampler, 8: token number)", v);
   }
   return METIS_OK;
 }

@@ -1,0 +1,596 @@
+// model.hip -- host side of the operators around the linear layers (layer
+// norm, dropout, embedding, loss over a vocabulary), declared in
+// include/metis.h.
+#include <math.h>
+
+#include <algorithm>
+
+#include "bf16_gemm.hpp"
+#include "dropout.hpp"
+#include "embedding.hpp"
+#include "gemm_launch.hpp"
+#include "host.hpp"
+#include "loss.hpp"
+#include "norm.hpp"
+
+using namespace metis;
+
+namespace {
+
+int64_t value_size(int32_t dt) { return dt == METIS_BF16 ? 2 : 4; }
+
+bool aligned(const void* p, int64_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+// rows of which any eight consecutive values from a multiple of eight can be
+// taken at once
+bool vec_rows(const void* p, int32_t dt, int64_t ld, int64_t rows) {
+  return aligned(p, 16) && (rows <= 1 || ld * value_size(dt) % 16 == 0);
+}
+
+// a grid for `items` over workgroups of `per`; kernels stride over the rest
+unsigned grid_for(int64_t items, int64_t per, int64_t most = 1 << 20) {
+  return (unsigned)std::min<int64_t>(std::max<int64_t>(ceil_div<int64_t>(items, per), 1), most);
+}
+
+metis_status rows_check(const char* what, const void* p, int32_t dt, int64_t rows, int64_t cols, int64_t ld) {
+  if (!dtype_ok(dt)) return fail(METIS_E_INVALID, "%s: dtype %d", what, dt);
+  if (rows < 0 || cols < 1 || cols > INT32_MAX || (rows > 1 && ld < cols))
+    return fail(METIS_E_INVALID, "%s: %lld rows of %lld, leading dimension %lld", what, (long long)rows, (long long)cols,
+                (long long)ld);
+  if (rows && !p) return fail(METIS_E_INVALID, "%s: null pointer", what);
+  if (!aligned(p, value_size(dt))) return fail(METIS_E_INVALID, "%s: misaligned pointer", what);
+  return METIS_OK;
+}
+
+metis_status ws_check(const char* what, const void* ws, size_t bytes, size_t need) {
+  if (need && (!ws || bytes < need)) return fail(METIS_E_WORKSPACE, "%s: workspace %zu < %zu", what, bytes, need);
+  if (need && !aligned(ws, 256)) return fail(METIS_E_INVALID, "%s: workspace not 256-byte aligned", what);
+  return METIS_OK;
+}
+
+#define TRY(expr)                     \
+  do {                                \
+    const metis_status s__ = (expr);  \
+    if (s__ != METIS_OK) return s__;  \
+  } while (0)
+
+// ------------------------------------------------------------- layer norm --
+
+// workgroups of the backward pass, each with a row of partial sums
+constexpr int64_t kNormGroups = 512;
+
+int64_t norm_threads(int64_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024; }
+
+int64_t norm_groups(int64_t rows, int64_t cols) {
+  if (cols > kNormCols) return std::min<int64_t>(ceil_div<int64_t>(rows, kNormSumRows), INT32_MAX);
+  const int64_t per = std::max<int64_t>(1, 256 / norm_threads(cols));
+  return std::min<int64_t>(ceil_div<int64_t>(rows, per), kNormGroups);
+}
+
+template <int VEC, int T, int NV>
+void launch_norm(const NormParams& p, bool bwd, unsigned grid, hipStream_t st) {
+  const dim3 block(norm_block(T));
+  if (bwd) hipLaunchKernelGGL((norm_bwd_kernel<VEC, T, NV>), dim3(grid), block, 0, st, p);
+  else hipLaunchKernelGGL((norm_fwd_kernel<VEC, T, NV>), dim3(grid), block, 0, st, p);
+}
+
+template <int VEC>
+void launch_norm_rows(const NormParams& p, bool bwd, hipStream_t st) {
+  constexpr int K = 8 / VEC;
+  const int64_t T = norm_threads(p.cols), per = std::max<int64_t>(1, 256 / T);
+  const int64_t most = bwd ? kNormGroups : T == 1024 ? 512 : 2048;
+  const unsigned grid = grid_for(p.rows, per, most);
+  if (T == 64) {
+    if (p.cols <= 512) launch_norm<VEC, 64, 1 * K>(p, bwd, grid, st);
+    else if (p.cols <= 1024) launch_norm<VEC, 64, 2 * K>(p, bwd, grid, st);
+    else launch_norm<VEC, 64, 4 * K>(p, bwd, grid, st);
+  } else if (T == 256) {
+    if (p.cols <= 4096) launch_norm<VEC, 256, 2 * K>(p, bwd, grid, st);
+    else launch_norm<VEC, 256, 4 * K>(p, bwd, grid, st);
+  } else {
+    launch_norm<VEC, 1024, 2 * K>(p, bwd, grid, st);
+  }
+}
+
+// -------------------------------------------------------------- embedding --
+
+struct EmbedWs {
+  uint32_t *key[2], *pos[2], *hist;
+  float* part;
+};
+
+EmbedWs carve_embed(Carver& cv, int64_t tokens, int64_t cols) {
+  EmbedWs w;
+  for (int i = 0; i < 2; ++i) {
+    w.key[i] = cv.take<uint32_t>(tokens);
+    w.pos[i] = cv.take<uint32_t>(tokens);
+  }
+  w.hist = cv.take<uint32_t>((size_t)kEmbedTiles * kEmbedDigits);
+  w.part = cv.take<float>((size_t)ceil_div<int64_t>(tokens, kEmbedRun) * 2 * cols);
+  return w;
+}
+
+metis_status ids_check(const char* what, const void* ids, int32_t bits, int64_t tokens, int64_t vocab) {
+  if (bits != 32 && bits != 64) return fail(METIS_E_INVALID, "%s: %d bits a token", what, bits);
+  if (tokens < 0 || vocab < 1) return fail(METIS_E_INVALID, "%s: %lld tokens, vocabulary %lld", what, (long long)tokens,
+                                           (long long)vocab);
+  if (tokens > INT32_MAX || vocab > INT32_MAX)
+    return fail(METIS_E_UNSUPPORTED, "%s: %lld tokens, vocabulary %lld", what, (long long)tokens, (long long)vocab);
+  if (tokens && (!ids || !aligned(ids, bits / 8))) return fail(METIS_E_INVALID, "%s: token pointer", what);
+  return METIS_OK;
+}
+
+// ------------------------------------------------------------------- loss --
+
+constexpr int64_t kLossMax = 1 << 22;
+
+// the parts of a product's operand: planes of rows
+struct Planes {
+  const uint8_t* at = nullptr;
+  int64_t pitch = 0;  // bytes
+  int64_t plane = 0;  // bytes between planes
+  int count = 1;
+};
+
+// whether rows can be an operand as they lie in memory
+bool operand_as_is(const void* p, int32_t dt, int64_t ld, int64_t rows, int64_t cols) {
+  return dt == METIS_BF16 && cols % 64 == 0 && vec_rows(p, dt, ld, rows) && (rows <= 1 || ld % 64 == 0) && ld < 1 << 23;
+}
+
+int64_t pad64(int64_t n) { return round_up64(n, 64); }
+
+// Words of one piece: about 2^27 probabilities, so that a piece's products
+// fill the chip many times over and its buffers stay at 256 MB each; the
+// pieces of a vocabulary are of equal size up to 256.
+int64_t loss_piece(int64_t tokens, int64_t vocab) {
+  const int64_t most = std::max<int64_t>(((int64_t)1 << 27) / std::max<int64_t>(tokens, 1), 4096);
+  const int64_t pieces = ceil_div<int64_t>(vocab, most);
+  return round_up64(ceil_div<int64_t>(vocab, pieces), 256);
+}
+
+struct LossPlan {
+  bool x_as_is, w_as_is, pair;  // pair: a gradient is binary32, P has two planes
+  int xp, wp;                   // planes of x and w
+  int64_t N, V, D, Dp, Np, piece;
+};
+
+LossPlan loss_plan(const metis_loss& l) {
+  LossPlan p;
+  p.N = l.tokens, p.V = l.vocab, p.D = l.cols;
+  p.Dp = pad64(p.D), p.Np = pad64(p.N);
+  p.x_as_is = operand_as_is(l.x, l.x_dtype, l.ldx, p.N, p.D);
+  p.w_as_is = operand_as_is(l.w, l.w_dtype, l.ldw, p.V, p.D);
+  p.xp = l.x_dtype == METIS_F32 ? 2 : 1;
+  p.wp = l.w_dtype == METIS_F32 ? 2 : 1;
+  p.pair = p.xp == 2 || p.wp == 2;
+  p.piece = loss_piece(p.N, p.V);
+  return p;
+}
+
+struct LossWs {
+  uint16_t *x, *w;             // planes of x, of a piece of w (where not as they are)
+  float2* stat;                // forward
+  float *target, *losses;
+  uint16_t *p, *pt, *wt, *xt;  // backward: P, P^T, the piece of w transposed, x transposed
+  float *dx, *part;            // dx summed over the pieces, parts of K
+};
+
+LossWs carve_loss(Carver& cv, const metis_loss& l, const LossPlan& p, bool backward) {
+  LossWs w{};
+  if (!p.x_as_is) w.x = cv.take<uint16_t>((size_t)p.xp * p.N * p.Dp);
+  if (!p.w_as_is) w.w = cv.take<uint16_t>((size_t)p.wp * std::min(p.piece, p.V) * p.Dp);
+  if (!backward) {
+    w.stat = cv.take<float2>((size_t)ceil_div<int64_t>(p.V, 64) * p.N);
+    w.target = cv.take<float>(p.N);
+    w.losses = cv.take<float>(p.N);
+    return w;
+  }
+  const int64_t words = pad64(std::min(p.piece, p.V));
+  const int pp = p.pair ? 2 : 1;
+  w.p = cv.take<uint16_t>((size_t)pp * p.N * words);
+  w.pt = cv.take<uint16_t>((size_t)pp * words * p.Np);
+  w.wt = cv.take<uint16_t>((size_t)(p.xp == 2 ? p.wp : 1) * p.D * words);
+  w.xt = cv.take<uint16_t>((size_t)(p.wp == 2 ? p.xp : 1) * p.D * p.Np);
+  w.dx = cv.take<float>((size_t)p.N * p.D);
+  const int s = bf_gemm_most_splits(p.N, p.D);
+  if (s > 1) w.part = cv.take<float>((size_t)s * p.N * p.D);
+  return w;
+}
+
+metis_status loss_check(const metis_loss* l, const char* what) {
+  if (!l) return fail(METIS_E_INVALID, "%s: null argument", what);
+  TRY(ids_check(what, l->targets, l->target_bits, l->tokens, l->vocab));
+  TRY(rows_check(what, l->x, l->x_dtype, l->tokens, l->cols, l->ldx));
+  TRY(rows_check(what, l->w, l->w_dtype, l->vocab, l->cols, l->ldw));
+  if (l->tokens > kLossMax || l->cols > kLossMax)
+    return fail(METIS_E_UNSUPPORTED, "%s: %lld tokens of %lld", what, (long long)l->tokens, (long long)l->cols);
+  return METIS_OK;
+}
+
+// planes of rows that cannot be an operand as they are, else the rows themselves
+metis_status as_operand(const void* src, int32_t dt, int64_t ld, int64_t rows, int64_t cols, bool as_is, int planes,
+                        uint16_t* dst, Planes* out, hipStream_t st) {
+  if (as_is) {
+    *out = {(const uint8_t*)src, rows > 1 ? ld * 2 : pad64(cols) * 2, 0, 1};
+    return METIS_OK;
+  }
+  const int64_t pitch = pad64(cols);
+  PlanesParams p{src, rows, cols, ld, dt == METIS_BF16, vec_rows(src, dt, ld, rows), dst, pitch, planes > 1 ? rows * pitch : 0};
+  hipLaunchKernelGGL(planes_kernel, dim3(grid_for(rows * (pitch / 8), 256)), dim3(256), 0, st, p);
+  LAUNCH_CHECK();
+  *out = {(const uint8_t*)dst, pitch * 2, rows * pitch * 2, planes};
+  return METIS_OK;
+}
+
+// planes of the transpose, zeros behind rows up to a multiple of 64
+metis_status transposed(const void* src, int32_t dt, int64_t ld, int64_t rows, int64_t cols, int planes, uint16_t* dst,
+                        const metis_loss* mask, Planes* out, hipStream_t st) {
+  const int64_t pitch = pad64(rows);
+  TransposeParams p{src, rows, cols, ld, dt == METIS_BF16, vec_rows(src, dt, ld, rows), dst, pitch,
+                    planes > 1 ? cols * pitch : 0, nullptr, 0, 0, 0};
+  if (mask) p.targets = mask->targets, p.targets64 = mask->target_bits == 64, p.vocab = mask->vocab, p.ignore = mask->ignore_index;
+  hipLaunchKernelGGL(transpose_kernel, dim3(grid_for(pitch / 64 * ceil_div<int64_t>(cols, 64), 1)), dim3(256), 0, st, p);
+  LAUNCH_CHECK();
+  *out = {(const uint8_t*)dst, pitch * 2, cols * pitch * 2, planes};
+  return METIS_OK;
+}
+
+// the operands and the products of their planes; `all`: with the low planes
+BfGemmParams product(const Planes& a, int64_t M, const Planes& b, int64_t N, int64_t K, bool all) {
+  BfGemmParams g{};
+  g.M = M, g.N = N;
+  g.a = a.at, g.b = b.at;
+  g.pitch_a = a.pitch, g.pitch_b = b.pitch;
+  g.run_stages = (int)(pad64(K) / 64);
+  g.splits = 1;
+  g.runs = 1;
+  if (all && b.count > 1) g.at_b[g.runs++] = b.plane;
+  if (all && a.count > 1) g.at_a[g.runs++] = a.plane;
+  return g;
+}
+
+metis_status run_product(const BfGemmParams& g, BfOut out, hipStream_t st) {
+  const hipError_t e = launch_bf_gemm(g, out, st);
+  return e == hipSuccess ? METIS_OK : fail(METIS_E_HIP, "product launch: %s", hipGetErrorString(e));
+}
+
+void set_targets(BfGemmParams& g, const metis_loss& l, int64_t v0) {
+  g.v0 = v0;
+  g.targets = l.targets;
+  g.targets64 = l.target_bits == 64;
+  g.vocab = l.vocab;
+  g.ignore = l.ignore_index;
+}
+
+const void* rows_from(const void* p, int32_t dt, int64_t ld, int64_t row) { return (const char*)p + row * ld * value_size(dt); }
+
+}  // namespace
+
+extern "C" {
+
+// ------------------------------------------------------------- layer norm --
+
+metis_status metis_layernorm_fwd(const void* X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void* weight,
+                                 const void* bias, int32_t w_dtype, double eps, void* Y, int32_t y_dtype, int64_t ldy,
+                                 float* mean, float* rstd, void* stream) {
+  TRY(rows_check("layernorm: X", X, x_dtype, rows, cols, ldx));
+  TRY(rows_check("layernorm: Y", Y, y_dtype, rows, cols, ldy));
+  if (!dtype_ok(w_dtype) || !aligned(weight, value_size(w_dtype)) || !aligned(bias, value_size(w_dtype)))
+    return fail(METIS_E_INVALID, "layernorm: weight or bias");
+  if (!(eps >= 0) || !isfinite(eps)) return fail(METIS_E_INVALID, "layernorm: eps %g", eps);
+  if (!mean != !rstd || !aligned(mean, 4) || !aligned(rstd, 4)) return fail(METIS_E_INVALID, "layernorm: mean and rstd");
+  if (rows == 0) return METIS_OK;
+  hipStream_t st = (hipStream_t)stream;
+  NormParams p{};
+  p.rows = rows, p.cols = (int)cols;
+  p.x = X, p.w = weight, p.b = bias;
+  p.ldx = ldx, p.ldy = ldy;
+  p.x_bf16 = x_dtype == METIS_BF16, p.w_bf16 = w_dtype == METIS_BF16, p.y_bf16 = y_dtype == METIS_BF16;
+  p.eps = (float)eps, p.inv = (float)(1.0 / (double)cols);
+  p.y = Y, p.mean = mean, p.rstd = rstd;
+  if (cols > kNormCols) {
+    hipLaunchKernelGGL(norm_fwd_long_kernel, dim3(grid_for(rows, 1, 512)), dim3(kNormThreads), 0, st, p);
+  } else if (vec_rows(X, x_dtype, ldx, rows) && vec_rows(Y, y_dtype, ldy, rows) && aligned(weight, 16) && aligned(bias, 16)) {
+    launch_norm_rows<8>(p, false, st);
+  } else {
+    launch_norm_rows<1>(p, false, st);
+  }
+  LAUNCH_CHECK();
+  return METIS_OK;
+}
+
+size_t metis_layernorm_bwd_workspace(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return 256;
+  return std::max<size_t>(256, (size_t)norm_groups(rows, cols) * 2 * cols * sizeof(float));
+}
+
+metis_status metis_layernorm_bwd(const void* dY, int32_t y_dtype, int64_t lddy, const void* X, int32_t x_dtype, int64_t rows,
+                                 int64_t cols, int64_t ldx, const void* weight, int32_t w_dtype, const float* mean,
+                                 const float* rstd, void* dX, int64_t lddx, void* dweight, void* dbias, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  TRY(rows_check("layernorm_bwd: dY", dY, y_dtype, rows, cols, lddy));
+  TRY(rows_check("layernorm_bwd: X", X, x_dtype, rows, cols, ldx));
+  if (dX) TRY(rows_check("layernorm_bwd: dX", dX, x_dtype, rows, cols, lddx));
+  if (!dtype_ok(w_dtype) || !aligned(weight, value_size(w_dtype)) || !aligned(dweight, value_size(w_dtype)) ||
+      !aligned(dbias, value_size(w_dtype)))
+    return fail(METIS_E_INVALID, "layernorm_bwd: weight, dweight or dbias");
+  if (rows && (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4))) return fail(METIS_E_INVALID, "layernorm_bwd: mean and rstd");
+  const bool sums = dweight || dbias;
+  if (sums) TRY(ws_check("layernorm_bwd", ws, ws_bytes, metis_layernorm_bwd_workspace(rows, cols)));
+  if (!dX && !sums) return METIS_OK;
+  hipStream_t st = (hipStream_t)stream;
+  NormParams p{};
+  p.rows = rows, p.cols = (int)cols;
+  p.x = X, p.w = weight;
+  p.ldx = ldx, p.lddy = lddy, p.lddx = lddx;
+  p.x_bf16 = x_dtype == METIS_BF16, p.w_bf16 = w_dtype == METIS_BF16, p.y_bf16 = y_dtype == METIS_BF16;
+  p.inv = (float)(1.0 / (double)cols);
+  p.mean = (float*)mean, p.rstd = (float*)rstd;
+  p.dy = dY, p.dx = dX;
+  p.part = sums ? (float*)ws : nullptr;
+  if (rows > 0) {
+    if (cols > kNormCols) {
+      if (sums) {  // first: dX may be dY
+        const dim3 grid((unsigned)ceil_div<int64_t>(cols, 256), (unsigned)std::min<int64_t>(norm_groups(rows, cols), 4096));
+        hipLaunchKernelGGL(norm_dw_long_kernel, grid, dim3(256), 0, st, p);
+        LAUNCH_CHECK();
+      }
+      if (dX) hipLaunchKernelGGL(norm_dx_long_kernel, dim3(grid_for(rows, 1, 512)), dim3(kNormThreads), 0, st, p);
+    } else if (vec_rows(X, x_dtype, ldx, rows) && vec_rows(dY, y_dtype, lddy, rows) &&
+               (!dX || vec_rows(dX, x_dtype, lddx, rows)) && aligned(weight, 16) && (!sums || cols % 4 == 0)) {
+      launch_norm_rows<8>(p, true, st);
+    } else {
+      launch_norm_rows<1>(p, true, st);
+    }
+    LAUNCH_CHECK();
+  }
+  if (sums) {  // (no rows: zeros)
+    hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)ceil_div<int64_t>(cols, 64), 2), dim3(1024), 0, st, (const float*)ws,
+                       rows > 0 ? norm_groups(rows, cols) : 0, (int)cols, dweight, dbias, (int)(w_dtype == METIS_BF16));
+    LAUNCH_CHECK();
+  }
+  return METIS_OK;
+}
+
+// ---------------------------------------------------------------- dropout --
+
+metis_status metis_dropout(const void* X, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, const void* residual,
+                           int64_t ldr, double p, uint64_t seed, uint32_t tag, int64_t step, const int64_t* step_count, void* Y,
+                           int64_t ldy, void* stream) {
+  TRY(rows_check("dropout: X", X, dtype, rows, cols, ldx));
+  TRY(rows_check("dropout: Y", Y, dtype, rows, cols, ldy));
+  if (residual) TRY(rows_check("dropout: residual", residual, dtype, rows, cols, ldr));
+  if (!(p >= 0 && p <= 1)) return fail(METIS_E_INVALID, "dropout: p %g", p);
+  if (step < 0) return fail(METIS_E_INVALID, "dropout: step %lld", (long long)step);
+  if (!aligned(step_count, 8)) return fail(METIS_E_INVALID, "dropout: step count pointer");
+  if (rows > INT64_MAX / cols) return fail(METIS_E_UNSUPPORTED, "dropout: %lld x %lld", (long long)rows, (long long)cols);
+  if (rows == 0) return METIS_OK;
+  const uint32_t t = (uint32_t)rint(65536.0 * p);
+  DropoutParams d{X, residual, Y, rows, cols, ldx, ldr, ldy, dtype == METIS_BF16, t,
+                  t < 65536 ? (float)(65536.0 / (65536 - t)) : 0.0f, seed, tag_with_role(tag, kRoleDropout), (uint32_t)step,
+                  step_count};
+  const bool flat = (rows == 1 || (ldx == cols && ldy == cols && (!residual || ldr == cols))) && aligned(X, 16) && aligned(Y, 16) &&
+                    aligned(residual, 16);
+  hipStream_t st = (hipStream_t)stream;
+  const dim3 grid(grid_for(ceil_div<int64_t>(rows * cols, 8), 256));
+  if (flat) {
+    d.cols = rows * cols;
+    hipLaunchKernelGGL((dropout_kernel<true>), grid, dim3(256), 0, st, d);
+  } else {
+    hipLaunchKernelGGL((dropout_kernel<false>), grid, dim3(256), 0, st, d);
+  }
+  LAUNCH_CHECK();
+  return METIS_OK;
+}
+
+// -------------------------------------------------------------- embedding --
+
+metis_status metis_embedding_fwd(const void* W, int32_t w_dtype, int64_t vocab, int64_t cols, int64_t ldw, const void* ids,
+                                 int32_t id_bits, int64_t tokens, double scale, void* Y, int32_t y_dtype, int64_t ldy,
+                                 void* stream) {
+  TRY(ids_check("embedding", ids, id_bits, tokens, vocab));
+  TRY(rows_check("embedding: W", W, w_dtype, vocab, cols, ldw));
+  TRY(rows_check("embedding: Y", Y, y_dtype, tokens, cols, ldy));
+  if (tokens == 0) return METIS_OK;
+  TRY(ensure_device_tables());
+  EmbedFwdParams p{W, vocab, cols, ldw, tokens, ldy, ids, id_bits == 64, w_dtype == METIS_BF16, y_dtype == METIS_BF16,
+                   vec_rows(W, w_dtype, ldw, vocab) && vec_rows(Y, y_dtype, ldy, tokens), (float)scale, Y, device_status()};
+  int T = 1;
+  while (T < 256 && T * (p.vec ? 8 : 1) < cols) T *= 2;
+  hipLaunchKernelGGL(embed_fwd_kernel, dim3(grid_for(tokens, 256 / T)), dim3(256), 0, (hipStream_t)stream, p, T);
+  LAUNCH_CHECK();
+  return METIS_OK;
+}
+
+size_t metis_embedding_bwd_workspace(int64_t tokens, int64_t cols) {
+  if (tokens <= 0 || cols <= 0) return 256;
+  Carver cv(nullptr, 0);
+  carve_embed(cv, tokens, cols);
+  return cv.used();
+}
+
+metis_status metis_embedding_bwd(const void* dY, int32_t y_dtype, int64_t tokens, int64_t cols, int64_t lddy, const void* ids,
+                                 int32_t id_bits, int64_t vocab, int64_t padding, double scale, void* dW, int32_t w_dtype,
+                                 int64_t lddw, void* ws, size_t ws_bytes, void* stream) {
+  TRY(ids_check("embedding_bwd", ids, id_bits, tokens, vocab));
+  TRY(rows_check("embedding_bwd: dY", dY, y_dtype, tokens, cols, lddy));
+  TRY(rows_check("embedding_bwd: dW", dW, w_dtype, vocab, cols, lddw));
+  if (padding >= vocab) return fail(METIS_E_INVALID, "embedding_bwd: padding token %lld of %lld", (long long)padding, (long long)vocab);
+  TRY(ws_check("embedding_bwd", ws, ws_bytes, metis_embedding_bwd_workspace(tokens, cols)));
+  TRY(ensure_device_tables());
+  hipStream_t st = (hipStream_t)stream;
+  Carver cv(ws, ws_bytes);
+  const EmbedWs w = carve_embed(cv, std::max<int64_t>(tokens, 1), cols);
+  EmbedSumParams s{};
+  if (tokens > 0) {
+    EmbedSortParams p{};
+    p.ids = ids, p.ids64 = id_bits == 64;
+    p.tokens = tokens, p.vocab = vocab, p.padding = padding;
+    p.hist = w.hist;
+    p.tile = kEmbedTile * ceil_div<int64_t>(tokens, (int64_t)kEmbedTile * kEmbedTiles);
+    p.tiles = (int)ceil_div<int64_t>(tokens, p.tile);
+    p.status = device_status();
+    int to = 0;
+    for (p.shift = 0; p.shift == 0 || vocab >> p.shift; p.shift += kEmbedBits, to ^= 1) {  // keys go up to vocab
+      p.first = p.shift == 0;
+      p.key = w.key[to ^ 1], p.pos = w.pos[to ^ 1];
+      p.key_to = w.key[to], p.pos_to = w.pos[to];
+      hipLaunchKernelGGL(embed_hist_kernel, dim3((unsigned)p.tiles), dim3(kEmbedTile), 0, st, p);
+      hipLaunchKernelGGL(embed_scatter_kernel, dim3((unsigned)p.tiles), dim3(kEmbedTile), 0, st, p);
+      LAUNCH_CHECK();
+    }
+    s.key = w.key[to ^ 1], s.pos = w.pos[to ^ 1];
+  }
+  s.tokens = tokens, s.vocab = vocab, s.cols = cols, s.lddy = lddy, s.lddw = lddw;
+  s.dy = dY, s.dw = dW;
+  s.dy_bf16 = y_dtype == METIS_BF16, s.dw_bf16 = w_dtype == METIS_BF16;
+  s.scale = (float)scale;
+  s.part = w.part;
+  s.runs = ceil_div<int64_t>(tokens, kEmbedRun);
+  s.zero_groups = grid_for(ceil_div<int64_t>(vocab, 64), 4, 8192);
+  if (s.runs + s.zero_groups > max_groups(256)) return fail(METIS_E_UNSUPPORTED, "embedding_bwd: %lld tokens", (long long)tokens);
+  const dim3 grid((unsigned)(s.runs + s.zero_groups));
+  if (vec_rows(dY, y_dtype, lddy, tokens) && vec_rows(dW, w_dtype, lddw, vocab))
+    hipLaunchKernelGGL((embed_sum_kernel<8>), grid, dim3(256), 0, st, s);
+  else
+    hipLaunchKernelGGL((embed_sum_kernel<1>), grid, dim3(256), 0, st, s);
+  LAUNCH_CHECK();
+  if (s.runs > 1) {
+    const dim3 join((unsigned)s.runs, (unsigned)std::min<int64_t>(ceil_div<int64_t>(cols, 256), 64));
+    hipLaunchKernelGGL(embed_join_kernel, join, dim3(256), 0, st, s);
+    LAUNCH_CHECK();
+  }
+  return METIS_OK;
+}
+
+// ------------------------------------------------------------------- loss --
+
+size_t metis_cross_entropy_workspace(const metis_loss* l, int32_t backward) {
+  if (!l || l->tokens <= 0 || l->vocab <= 0 || l->cols <= 0) return 256;
+  Carver cv(nullptr, 0);
+  carve_loss(cv, *l, loss_plan(*l), backward != 0);
+  return cv.used();
+}
+
+metis_status metis_cross_entropy_fwd(const metis_loss* l, float* losses, float* lse, int32_t mean, float* total, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  TRY(loss_check(l, "cross_entropy"));
+  if ((l->tokens && !lse) || !aligned(lse, 4) || !aligned(losses, 4) || !aligned(total, 4))
+    return fail(METIS_E_INVALID, "cross_entropy: output pointer");
+  if (mean != 0 && mean != 1) return fail(METIS_E_INVALID, "cross_entropy: mean %d", mean);
+  hipStream_t st = (hipStream_t)stream;
+  const int t64 = l->target_bits == 64;
+  if (l->tokens > 0) {
+    TRY(ws_check("cross_entropy", ws, ws_bytes, metis_cross_entropy_workspace(l, 0)));
+    TRY(ensure_device_tables());
+    const LossPlan p = loss_plan(*l);
+    Carver cv(ws, ws_bytes);
+    const LossWs w = carve_loss(cv, *l, p, false);
+    Planes x, v;
+    TRY(as_operand(l->x, l->x_dtype, l->ldx, p.N, p.D, p.x_as_is, p.xp, w.x, &x, st));
+    // a weight that needs no copies goes through in one piece
+    // (as long as its tiles can be counted in 32 bits)
+    const int64_t piece = p.w_as_is && ceil_div<int64_t>(p.N, 64) * ceil_div<int64_t>(p.V, 128) < 1 << 30 ? p.V : p.piece;
+    for (int64_t v0 = 0; v0 < p.V; v0 += piece) {
+      const int64_t n = std::min(piece, p.V - v0);
+      TRY(as_operand(rows_from(l->w, l->w_dtype, l->ldw, v0), l->w_dtype, l->ldw, n, p.D, p.w_as_is, p.wp, w.w, &v, st));
+      BfGemmParams g = product(x, p.N, v, n, p.D, true);
+      set_targets(g, *l, v0);
+      g.stat = w.stat, g.target_logit = w.target;
+      TRY(run_product(g, kBfStats, st));
+    }
+    if (!losses) losses = w.losses;
+    LossJoinParams j{w.stat, ceil_div<int64_t>(p.V, 64), p.N, w.target, l->targets, t64, l->vocab, l->ignore_index, losses, lse,
+                     device_status()};
+    hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)ceil_div<int64_t>(p.N, 64)), dim3(256), 0, st, j);
+    LAUNCH_CHECK();
+  }
+  if (total) {
+    hipLaunchKernelGGL(loss_total_kernel, dim3(1), dim3(1024), 0, st, (const float*)losses, l->targets, t64, l->vocab,
+                       l->ignore_index, l->tokens, mean, total);
+    LAUNCH_CHECK();
+  }
+  return METIS_OK;
+}
+
+metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, const float* grad, int32_t grad_each,
+                                     const float* count, void* dX, int64_t lddx, void* dW, int64_t lddw, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  TRY(loss_check(l, "cross_entropy_bwd"));
+  if (dX) TRY(rows_check("cross_entropy_bwd: dX", dX, l->x_dtype, l->tokens, l->cols, lddx));
+  if (dW) TRY(rows_check("cross_entropy_bwd: dW", dW, l->w_dtype, l->vocab, l->cols, lddw));
+  if (l->tokens && (!lse || !grad || !aligned(lse, 4) || !aligned(grad, 4) || !aligned(count, 4)))
+    return fail(METIS_E_INVALID, "cross_entropy_bwd: lse, grad or count");
+  if (grad_each != 0 && grad_each != 1) return fail(METIS_E_INVALID, "cross_entropy_bwd: grad_each %d", grad_each);
+  if (!dX && !dW) return METIS_OK;
+  hipStream_t st = (hipStream_t)stream;
+  const LossPlan p = loss_plan(*l);
+  if (p.N == 0) {
+    if (dW) {
+      hipLaunchKernelGGL(zero_rows_kernel, dim3(grid_for(p.V * p.D, 256)), dim3(256), 0, st, dW, (int)(l->w_dtype == METIS_BF16),
+                         p.V, p.D, lddw);
+      LAUNCH_CHECK();
+    }
+    return METIS_OK;
+  }
+  TRY(ws_check("cross_entropy_bwd", ws, ws_bytes, metis_cross_entropy_workspace(l, 1)));
+  TRY(ensure_device_tables());
+  Carver cv(ws, ws_bytes);
+  const LossWs w = carve_loss(cv, *l, p, true);
+  Planes x, v, xt, wt, pt;
+  TRY(as_operand(l->x, l->x_dtype, l->ldx, p.N, p.D, p.x_as_is, p.xp, w.x, &x, st));
+  if (dW) TRY(transposed(l->x, l->x_dtype, l->ldx, p.N, p.D, p.wp == 2 ? p.xp : 1, w.xt, l, &xt, st));
+  const bool dx_f32 = l->x_dtype == METIS_F32;
+  const bool one = p.piece >= p.V;
+  for (int64_t v0 = 0; v0 < p.V; v0 += p.piece) {
+    const int64_t n = std::min(p.piece, p.V - v0), np = pad64(n);
+    const void* wv = rows_from(l->w, l->w_dtype, l->ldw, v0);
+    TRY(as_operand(wv, l->w_dtype, l->ldw, n, p.D, p.w_as_is, p.wp, w.w, &v, st));
+    BfGemmParams g = product(x, p.N, v, n, p.D, true);
+    set_targets(g, *l, v0);
+    g.lse = lse, g.grad = grad, g.count = count, g.grad_each = grad_each;
+    g.prob = w.p, g.ldp = np, g.lo_plane = p.pair ? p.N * np : 0;
+    TRY(run_product(g, kBfProb, st));
+    const Planes pr{(const uint8_t*)w.p, np * 2, p.N * np * 2, p.pair ? 2 : 1};
+    if (dX) {
+      TRY(transposed(wv, l->w_dtype, l->ldw, n, p.D, p.xp == 2 ? p.wp : 1, w.wt, nullptr, &wt, st));
+      g = product(pr, p.N, wt, p.D, n, dx_f32);
+      const int splits = bf_gemm_splits(p.N, p.D, g.runs * g.run_stages);
+      // one piece: straight to dX; else summed in binary32, in dX itself where it is binary32
+      void* const sum = dx_f32 ? dX : (void*)w.dx;
+      const int64_t ld = dx_f32 ? lddx : p.D;
+      const bool direct = one && !dx_f32;
+      if (splits > 1) {
+        g.splits = splits;
+        g.C = w.part, g.ldc = p.D, g.split_ld = p.N * p.D;
+        TRY(run_product(g, kBfF32, st));
+        hipLaunchKernelGGL(split_join_kernel, dim3(grid_for(p.N * p.D, 256)), dim3(256), 0, st, (const float*)w.part, splits,
+                           p.N * p.D, p.N, p.D, direct ? dX : sum, (int)direct, direct ? lddx : ld, (int)(v0 > 0));
+        LAUNCH_CHECK();
+      } else {
+        g.C = direct ? dX : sum, g.ldc = direct ? lddx : ld;
+        g.add = v0 > 0;
+        TRY(run_product(g, direct ? kBfBF16 : kBfF32, st));
+      }
+    }
+    if (dW) {
+      TRY(transposed(w.p, METIS_BF16, np, p.N, n, 1, w.pt, nullptr, &pt, st));
+      if (p.wp == 2) {
+        Planes lo;
+        TRY(transposed(w.p + p.N * np, METIS_BF16, np, p.N, n, 1, w.pt + n * p.Np, nullptr, &lo, st));
+        pt.count = 2;
+      }
+      g = product(pt, n, xt, p.D, p.N, p.wp == 2);
+      g.C = (char*)dW + v0 * lddw * value_size(l->w_dtype), g.ldc = lddw;
+      TRY(run_product(g, p.wp == 2 ? kBfF32 : kBfBF16, st));
+    }
+  }
+  if (dX && !dx_f32 && !one) {
+    hipLaunchKernelGGL(split_join_kernel, dim3(grid_for(p.N * p.D, 256)), dim3(256), 0, st, (const float*)w.dx, 1, (int64_t)0,
+                       p.N, p.D, dX, 1, lddx, 0);
+    LAUNCH_CHECK();
+  }
+  return METIS_OK;
+}
+
+}  // extern "C"

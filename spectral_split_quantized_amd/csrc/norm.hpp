@@ -1,0 +1,266 @@
+// norm.hpp -- layer norm of rows, forward and backward.
+//
+//   mu = mean_j x_ij,  r = 1 / sqrt(mean_j (x_ij - mu)^2 + eps),
+//   h_ij = (x_ij - mu) r,  y_ij = h_ij w_j + b_j;
+// with g = dy w:
+//   dx_ij = r (g_ij - mean_j g_ij - h_ij mean_j (g_ij h_ij)),
+//   dw_j = sum_i dy_ij h_ij,  db_j = sum_i dy_ij.
+// Sums in binary32; the variance is that of the centred values, never a
+// difference of sums.  Only y and dx (and dw, db of bf16 weights) are rounded
+// to fewer bits, once.
+//
+// T threads share a row and hold it in registers, so that x is read once: a
+// wave up to 2048 columns, workgroups of 256 and 1024 threads up to 8192 and
+// 16384.  Each thread keeps its columns of w and b (and of the sums dw, db)
+// for all rows that it takes.  The sums of dw and db end in a row of partial
+// sums for each workgroup, added by a second kernel in the order of the
+// workgroups, so that equal calls give equal bits.  Longer rows are read from
+// memory again for each sum.
+#pragma once
+
+#include <type_traits>
+
+#include "rows.hpp"
+
+namespace metis {
+
+constexpr int kNormThreads = 1024;     // of a long row
+constexpr int kNormCols = 16384;       // longest row in registers
+constexpr int kNormSumRows = 64;       // rows of one partial sum of a long row's dw, db
+
+struct NormParams {
+  int64_t rows;
+  int cols;
+  const void *x, *w, *b;   // w, b or null
+  int64_t ldx;
+  int x_bf16, w_bf16, y_bf16;
+  float eps, inv;          // inv = 1 / cols
+  void* y;
+  int64_t ldy;
+  float *mean, *rstd;      // written forward (or null), read backward
+  // backward
+  const void* dy;          // y's type
+  int64_t lddy;
+  void* dx;                // x's type, or null
+  int64_t lddx;
+  float* part;             // [workgroups][2][cols], or null
+};
+
+// The columns of one thread: NV groups of VEC consecutive ones, the groups of
+// neighbouring threads next to each other.
+template <int VEC, int T, int NV>
+struct NormCols {
+  static constexpr int E = VEC * NV;
+  static __device__ __forceinline__ int first(int t, int k) { return (t + T * k) * VEC; }
+
+  static __device__ __forceinline__ void load(const void* p, int bf16, int64_t row, int cols, int t, float other, float* v) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = first(t, k);
+      if (VEC == 8 && c + 8 <= cols) {
+        load8(p, bf16, row + c, v + 8 * k);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[VEC * k + e] = c + e < cols ? load1(p, bf16, row + c + e) : other;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(void* p, int bf16, int64_t row, int cols, int t, const float* v) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = first(t, k);
+      if (VEC == 8 && c + 8 <= cols) {
+        store8(p, bf16, row + c, v + 8 * k);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (c + e < cols) store1(p, bf16, row + c + e, v[VEC * k + e]);
+      }
+    }
+  }
+};
+
+// threads of a workgroup
+constexpr int norm_block(int T) { return T < 256 ? 256 : T; }
+
+template <int VEC, int T, int NV>
+__global__ __launch_bounds__(norm_block(T)) void norm_fwd_kernel(NormParams p) {
+  using C = NormCols<VEC, T, NV>;
+  constexpr int E = C::E;
+  __shared__ float red[2][T / 64];
+  const int t = threadIdx.x & (T - 1);
+  float w[E], b[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) w[e] = 1.0f, b[e] = 0.0f;
+  if (p.w) C::load(p.w, p.w_bf16, 0, p.cols, t, 0.0f, w);
+  if (p.b) C::load(p.b, p.w_bf16, 0, p.cols, t, 0.0f, b);
+  const int64_t step = (int64_t)gridDim.x * (norm_block(T) / T);
+  for (int64_t row = (int64_t)blockIdx.x * (norm_block(T) / T) + threadIdx.x / T; row < p.rows; row += step) {
+    float x[E], s = 0.0f;
+    C::load(p.x, p.x_bf16, row * p.ldx, p.cols, t, 0.0f, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s += x[e];
+    const float mu = row_sum<T>(s, red[0]) * p.inv;
+    s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      x[e] -= mu;
+      s += C::first(t, e / VEC) + e % VEC < p.cols ? x[e] * x[e] : 0.0f;
+    }
+    const float r = 1.0f / sqrtf(row_sum<T>(s, red[1]) * p.inv + p.eps);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = x[e] * r * w[e] + b[e];
+    C::store(p.y, p.y_bf16, row * p.ldy, p.cols, t, x);
+    if (p.mean && t == 0) {
+      p.mean[row] = mu;
+      p.rstd[row] = r;
+    }
+  }
+}
+
+template <int VEC, int T, int NV>
+__global__ __launch_bounds__(norm_block(T)) void norm_bwd_kernel(NormParams p) {
+  using C = NormCols<VEC, T, NV>;
+  constexpr int E = C::E, G = norm_block(T) / T;  // rows at a time
+  __shared__ float red[2][T / 64];
+  const int t = threadIdx.x & (T - 1);
+  float w[E], dw[E], db[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) w[e] = 1.0f, dw[e] = db[e] = 0.0f;
+  if (p.w) C::load(p.w, p.w_bf16, 0, p.cols, t, 0.0f, w);
+  const int64_t step = (int64_t)gridDim.x * G;
+  for (int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / T; row < p.rows; row += step) {
+    float h[E], g[E], s = 0.0f, q = 0.0f;
+    const float mu = p.mean[row], r = p.rstd[row];
+    C::load(p.x, p.x_bf16, row * p.ldx, p.cols, t, mu, h);  // 0 behind the row
+    C::load(p.dy, p.y_bf16, row * p.lddy, p.cols, t, 0.0f, g);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      h[e] = (h[e] - mu) * r;
+      dw[e] += g[e] * h[e];
+      db[e] += g[e];
+      g[e] *= w[e];
+      s += g[e];
+      q += g[e] * h[e];
+    }
+    if (!p.dx) continue;
+    s = row_sum<T>(s, red[0]) * p.inv;
+    q = row_sum<T>(q, red[1]) * p.inv;
+#pragma unroll
+    for (int e = 0; e < E; ++e) g[e] = r * (g[e] - s - h[e] * q);
+    C::store(p.dx, p.x_bf16, row * p.lddx, p.cols, t, g);
+  }
+  if (!p.part) return;
+  float* const to = p.part + (int64_t)blockIdx.x * 2 * p.cols;
+  if constexpr (G > 1) {  // the waves of a workgroup one after the other
+    __shared__ float sums[2][64 * E];
+    for (int i = 0; i < G; ++i) {
+      if (threadIdx.x / T == i) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float* const a = &sums[0][e * 64 + t];
+          float* const c = &sums[1][e * 64 + t];
+          *a = dw[e] += i ? *a : 0.0f;
+          *c = db[e] += i ? *c : 0.0f;
+        }
+      }
+      __syncthreads();
+    }
+    if (threadIdx.x / T != G - 1) return;
+  }
+  C::store(to, 0, 0, p.cols, t, dw);
+  C::store(to + p.cols, 0, 0, p.cols, t, db);
+}
+
+// sum of f(column) over a row by all threads of a long row's workgroup
+template <typename F>
+__device__ inline float long_row_sum(int cols, float* red, F f) {
+  float s = 0.0f;
+  for (int c = threadIdx.x; c < cols; c += kNormThreads) s += f(c);
+  __syncthreads();  // the array's last use
+  return row_sum<kNormThreads>(s, red);
+}
+
+__global__ __launch_bounds__(kNormThreads) void norm_fwd_long_kernel(NormParams p) {
+  __shared__ float red[kNormThreads / 64];
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    auto x = [&](int c) { return load1(p.x, p.x_bf16, row * p.ldx + c); };
+    const float mu = long_row_sum(p.cols, red, x) * p.inv;
+    auto square = [&](int c) {
+      const float d = x(c) - mu;
+      return d * d;
+    };
+    const float r = 1.0f / sqrtf(long_row_sum(p.cols, red, square) * p.inv + p.eps);
+    for (int c = threadIdx.x; c < p.cols; c += kNormThreads) {
+      const float w = p.w ? load1(p.w, p.w_bf16, c) : 1.0f, b = p.b ? load1(p.b, p.w_bf16, c) : 0.0f;
+      store1(p.y, p.y_bf16, row * p.ldy + c, (x(c) - mu) * r * w + b);
+    }
+    if (p.mean && threadIdx.x == 0) {
+      p.mean[row] = mu;
+      p.rstd[row] = r;
+    }
+  }
+}
+
+__global__ __launch_bounds__(kNormThreads) void norm_dx_long_kernel(NormParams p) {
+  __shared__ float red[kNormThreads / 64];
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float mu = p.mean[row], r = p.rstd[row];
+    auto h = [&](int c) { return (load1(p.x, p.x_bf16, row * p.ldx + c) - mu) * r; };
+    auto g = [&](int c) { return load1(p.dy, p.y_bf16, row * p.lddy + c) * (p.w ? load1(p.w, p.w_bf16, c) : 1.0f); };
+    const float s = long_row_sum(p.cols, red, g) * p.inv;
+    const float q = long_row_sum(p.cols, red, [&](int c) { return g(c) * h(c); }) * p.inv;
+    for (int c = threadIdx.x; c < p.cols; c += kNormThreads)
+      store1(p.dx, p.x_bf16, row * p.lddx + c, r * (g(c) - s - h(c) * q));
+  }
+}
+
+// partial sums of dw and db over kNormSumRows rows, a column a thread
+__global__ __launch_bounds__(256) void norm_dw_long_kernel(NormParams p) {
+  const int c = (int)(blockIdx.x * 256 + threadIdx.x);
+  if (c >= p.cols) return;
+  for (int64_t group = blockIdx.y; group * kNormSumRows < p.rows; group += gridDim.y) {
+    float dw = 0.0f, db = 0.0f;
+    const int64_t end = min((group + 1) * kNormSumRows, p.rows);
+    for (int64_t row = group * kNormSumRows; row < end; ++row) {
+      const float dy = load1(p.dy, p.y_bf16, row * p.lddy + c);
+      dw += dy * ((load1(p.x, p.x_bf16, row * p.ldx + c) - p.mean[row]) * p.rstd[row]);
+      db += dy;
+    }
+    p.part[group * 2 * p.cols + c] = dw;
+    p.part[(group * 2 + 1) * p.cols + c] = db;
+  }
+}
+
+// dw (blockIdx.y 0) and db (1) from the partial sums: 64 columns a workgroup,
+// its 16 waves take every sixteenth partial sum, in order, and their sums are
+// added in order.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int64_t groups, int cols, void* dw, void* db,
+                                                        int w_bf16) {
+  __shared__ float red[16][64];
+  void* const to = blockIdx.y ? db : dw;
+  if (!to) return;
+  const int wave = threadIdx.x >> 6, c = (int)(blockIdx.x * 64 + (threadIdx.x & 63));
+  float s = 0.0f;
+  if (c < cols) {
+    const float* at = part + (int64_t)blockIdx.y * cols + c;
+    int64_t i = wave;
+    for (; i + 112 < groups; i += 128) {  // eight in flight
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = at[(i + 16 * k) * 2 * cols];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
+    for (; i < groups; i += 16) s += at[i * 2 * cols];
+  }
+  red[wave][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (wave || c >= cols) return;
+  s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) s += red[k][threadIdx.x];
+  store1(to, w_bf16, c, s);
+}
+
+}  // namespace metis

@@ -10,7 +10,8 @@ namespace metis {
 // ----------------------------------------------------------- status flag --
 
 // Per-device numeric failure flag (bit 0: non-finite input, bit 1: Cholesky
-// breakdown, bit 2: row-sample selection overflow).
+// breakdown, bit 2: row-sample selection overflow; bit 3: a token number
+// outside the vocabulary, kStatusToken of rows.hpp).
 __device__ int g_metis_status;
 
 __device__ inline void raise_status(int bits) { atomicOr(&g_metis_status, bits); }

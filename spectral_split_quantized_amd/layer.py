@@ -1,4 +1,6 @@
-"""A PyTorch linear layer whose three GEMMs run through the Metis path.
+"""PyTorch layers on the library: linear layers whose three GEMMs run through
+the Metis path or in int8, and what stands around them in a language model
+(layer norm, dropout, embedding, the loss over the vocabulary).
 
 "Metis: Training LLMs with FP4 Quantization" (整体框架): the weight W, the
 activation X and the output gradient D of a linear layer are each split into
@@ -8,7 +10,8 @@ dW = X^T D -- is evaluated through the split.  The right factor of each
 operand is cached and re-sketched every ``refresh`` steps (关键设计 3).
 
 This module is marshalling only: ``metis.prepare_operand`` and
-``metis.gemm_fwd`` / ``metis.gemm_bwd`` run every step in the HIP library.
+``metis.gemm_fwd`` / ``metis.gemm_bwd`` run every step in the HIP library, as
+do the calls of the other layers.
 The weight is stored as in the pages' notation, ``in_features x
 out_features`` (Y = X W), as an fp32 master.
 """
@@ -19,7 +22,7 @@ import torch
 
 from . import metis
 
-__all__ = ["MetisLinear", "Int8Linear", "Int8Frozen", "set_step"]
+__all__ = ["MetisLinear", "Int8Linear", "Int8Frozen", "LayerNorm", "Dropout", "Embedding", "LinearCrossEntropy", "set_step"]
 
 
 class _MetisLinearFn(torch.autograd.Function):
@@ -99,11 +102,92 @@ def _rows(x):
     return x if (cols <= 1 or x.stride(1) == 1) and (rows <= 1 or x.stride(0) >= cols) else x.contiguous()
 
 
-_EAGER = weakref.WeakSet()  # nodes of Int8Linear recorded outside a capture, while their graphs live
+_EAGER = weakref.WeakSet()  # nodes of the layers below recorded outside a capture, while their graphs live
 
 
 def _capturing(t):
     return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
+def _watch(ctx, layer, leaves, capturing):
+    """Refuses to record a graph in a capture while one from outside it
+    lives, of this layer or of another with one of the same leaves: both
+    would accumulate a leaf's gradient through one node, which belongs to
+    the other's stream, and joining that stream from a capture ends the
+    process.  (A living graph holds its leaves, so their ids are theirs.)"""
+    if not capturing:
+        ctx.layer, ctx.leaves = weakref.ref(layer), leaves
+        _EAGER.add(ctx)
+    elif any(c.layer() is layer or any(i in c.leaves for i in leaves) for c in _EAGER):
+        raise RuntimeError("a graph of this layer from outside the capture is alive, or one with the same weight or "
+                           "input: drop its outputs first")
+
+
+def _record(ctx, layer, record, *tensors):
+    """Whether this pass is recorded for gradients; if so, its node is watched.
+    ``record`` is the caller's grad mode (inside a forward it is always off,
+    and needs_input_grad says nothing of torch.no_grad())."""
+    need = [t for t, n in zip(tensors, ctx.needs_input_grad) if n] if record else []
+    if need:
+        _watch(ctx, layer, [id(t) for t in need if t.is_leaf], _capturing(need[0]))
+    return bool(need)
+
+
+class _Stepped(torch.nn.Module):
+    """The training step, which selects a layer's draws: ``step``, and the same
+    on the GPU for passes captured into a graph, which read it there."""
+
+    def _count_device(self):
+        """The GPU that the count lives on, or None."""
+        raise NotImplementedError
+
+    def _init_step(self):
+        self._step, self._count = 0, None
+        self._make_count()
+
+    @property
+    def step(self):
+        """The training step, which selects the draws."""
+        return self._step
+
+    @step.setter
+    def step(self, step):
+        if self._replayed:
+            if _capturing(self._count):
+                raise RuntimeError("set the step outside the capture: replays read the one that is set then")
+            self._count.fill_(step)
+        self._step = step
+
+    def _make_count(self):
+        # -1 until the step is set after the first captured pass.  The same
+        # memory for as long as the layer stays on its GPU.
+        device = self._count_device()
+        if self._count is not None and self._count.device == device:
+            return
+        self._count, self._replayed = None, False
+        if device is not None:
+            with torch.inference_mode(False):
+                self._count = torch.full((), -1, dtype=torch.int64, device=device)
+
+    def _captured_count(self):
+        self._replayed = self._count is not None
+        return self._count
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        self._make_count()
+        return self
+
+    def __getstate__(self):
+        state = super().__getstate__() if hasattr(super(), "__getstate__") else self.__dict__
+        return {k: v for k, v in state.items() if k != "_count"}
+
+    def __setstate__(self, state):
+        state = dict(state)
+        state.setdefault("_step", state.pop("step", 0))  # "step": saved before it was on the GPU too
+        super().__setstate__(state)
+        self._count = None
+        self._make_count()
 
 
 def _product(a, b, dtype):
@@ -130,7 +214,7 @@ class _Int8LinearFn(torch.autograd.Function):
         capturing = False
         if need_x or need_w:
             capturing = _capturing(x)
-            mod._watch(ctx, [id(t) for t, need in ((x, need_x), (w, need_w)) if need and t.is_leaf], capturing)
+            _watch(ctx, mod, [id(t) for t, need in ((x, need_x), (w, need_w)) if need and t.is_leaf], capturing)
         # the same orientations as above: X along both axes (Y and dW), W
         # along both (Y and dX); an orientation whose product is not wanted is
         # left out
@@ -164,7 +248,7 @@ class _Int8LinearFn(torch.autograd.Function):
         return dx, dw, None, None
 
 
-class Int8Linear(torch.nn.Module):
+class Int8Linear(_Stepped):
     """y = x W (no bias) with all three products in int8: X, W and the output
     gradient D carry one scale per token or channel, along the axis that each
     product reduces over.
@@ -193,71 +277,17 @@ class Int8Linear(torch.nn.Module):
             raise ValueError("weight must be in_features x out_features")
         self.weight = torch.nn.Parameter(weight.to(device=device, dtype=torch.float32).contiguous())
         self.rounding = metis.SR if rounding == "sr" else metis.RNE
-        self.seed, self._step, self._count = seed, 0, None
+        self.seed = seed
         self.tags = {"D": metis.make_tag(layer, metis.OPERAND_D)}
-        self._make_count()
+        self._init_step()
 
-    @property
-    def step(self):
-        """The training step, which selects the draws."""
-        return self._step
-
-    @step.setter
-    def step(self, step):
-        if self._replayed:
-            if _capturing(self._count):
-                raise RuntimeError("set the step outside the capture: replays read the one that is set then")
-            self._count.fill_(step)
-        self._step = step
-
-    def _make_count(self):
-        # the step on the weight's GPU, for captured passes: -1 until it is set
-        # after the first of them.  The same memory for as long as the weight
-        # stays there.
-        if self._count is not None and self._count.device == self.weight.device:
-            return
-        self._count, self._replayed = None, False
-        if self.rounding == metis.SR and self.weight.is_cuda:
-            with torch.inference_mode(False):
-                self._count = torch.full((), -1, dtype=torch.int64, device=self.weight.device)
-
-    def _captured_count(self):
-        self._replayed = self._count is not None
-        return self._count
-
-    def _apply(self, fn, recurse=True):
-        super()._apply(fn, recurse)
-        self._make_count()
-        return self
+    def _count_device(self):
+        return self.weight.device if self.rounding == metis.SR and self.weight.is_cuda else None
 
     @property
     def _eager(self):
         """This layer's nodes of graphs from outside a capture that live."""
         return [c for c in _EAGER if c.layer() is self]
-
-    def _watch(self, ctx, leaves, capturing):
-        """Refuses to record a graph in a capture while one from outside it
-        lives, of this layer or of another with the same weight or input: both
-        would accumulate a leaf's gradient through one node, which belongs to
-        the other's stream, and joining that stream from a capture ends the
-        process.  (A living graph holds its leaves, so their ids are theirs.)"""
-        if not capturing:
-            ctx.layer, ctx.leaves = weakref.ref(self), leaves
-            _EAGER.add(ctx)
-        elif any(c.layer() is self or any(i in c.leaves for i in leaves) for c in _EAGER):
-            raise RuntimeError("a graph of this layer from outside the capture is alive, or one with the same weight or "
-                               "input: drop its outputs first")
-
-    def __getstate__(self):
-        state = super().__getstate__() if hasattr(super(), "__getstate__") else self.__dict__
-        return {k: v for k, v in state.items() if k != "_count"}
-
-    def __setstate__(self, state):
-        state = dict(state)
-        state.setdefault("_step", state.pop("step", 0))  # "step": saved before it was on the GPU too
-        super().__setstate__(state)
-        self._count = None
-        self._make_count()
 
     def forward(self, x):
         if x.shape[-1] != self.weight.shape[0]:
@@ -315,8 +345,204 @@ class Int8Frozen(torch.nn.Module):
         return y.reshape(*x.shape[:-1], w.outer)
 
 
+# ------------------------------------------------ around the linear layers --
+
+def _parameter(weight, device):
+    """A layer's parameter: a Parameter as it is (shared between layers), a
+    tensor as a new one."""
+    return weight if isinstance(weight, torch.nn.Parameter) else torch.nn.Parameter(weight.to(device).contiguous())
+
+
+class _LayerNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, mod, record):
+        need = _record(ctx, mod, record, x, w, b)
+        x2 = _rows(x)
+        y, mean, rstd = metis.layernorm(x2, w, b, mod.eps, stats=need)
+        if need:
+            ctx.save_for_backward(x2, w, mean, rstd)
+            ctx.w_dtype = None if b is None else b.dtype
+        return y.view(x.shape)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x2, w, mean, rstd = ctx.saved_tensors
+        dx, dw, db = metis.layernorm_bwd(_rows(dy), x2, mean, rstd, w, *ctx.needs_input_grad[:3], w_dtype=ctx.w_dtype)
+        return dx if dx is None else dx.view(dy.shape), dw, db, None, None
+
+
+class LayerNorm(torch.nn.Module):
+    """Layer norm over the last dimension, with a weight and a bias (``affine``
+    False: without).  x is bfloat16 or float32, y and the gradient of x have
+    its type, the parameters and their gradients theirs (float32 unless
+    ``dtype`` or given tensors say otherwise).  Sums are in binary32."""
+
+    def __init__(self, features, eps=1e-5, affine=True, weight=None, bias=None, device="cuda", dtype=torch.float32):
+        super().__init__()
+        self.features, self.eps = features, eps
+        if not affine:
+            if weight is not None or bias is not None:
+                raise ValueError("a layer norm without parameters takes no weight and no bias")
+            self.weight = self.bias = None
+            return
+        if weight is None:
+            weight = torch.ones(features, dtype=dtype if bias is None else bias.dtype, device=device)
+        if bias is None:
+            bias = torch.zeros(features, dtype=weight.dtype, device=device)
+        if tuple(weight.shape) != (features,) or tuple(bias.shape) != (features,) or weight.dtype != bias.dtype:
+            raise ValueError("weight and bias must be %d values of one type" % features)
+        self.weight, self.bias = _parameter(weight, device), _parameter(bias, device)
+
+    def forward(self, x):
+        if x.shape[-1] != self.features:
+            raise ValueError("x has %d features, the layer %d" % (x.shape[-1], self.features))
+        return _LayerNormFn.apply(x, self.weight, self.bias, self, torch.is_grad_enabled())
+
+
+class _DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, mod, record):
+        _record(ctx, mod, record, x, residual)
+        ctx.draws = dict(p=mod.p, seed=mod.seed, tag=mod.tag, step=mod.step,
+                         step_count=mod._captured_count() if _capturing(x) else None)
+        y = metis.dropout(_rows(x), residual=None if residual is None else _rows(residual), **ctx.draws)
+        return y.view(x.shape)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        dx = metis.dropout(_rows(dy), **ctx.draws).view(dy.shape) if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None
+
+
+class Dropout(_Stepped):
+    """x with each value dropped with probability ``p`` (to the nearest
+    multiple of 2^-16) and the others scaled to keep the mean, plus
+    ``residual`` if one is given.  The mask is never stored: the backward pass
+    draws it again.
+
+    The draws are those of ``seed``, ``layer`` and the step that
+    :func:`set_step` sets, at the value's row-major position; a layer that runs
+    twice in a step draws the same mask twice, so each place of a model has a
+    Dropout with a ``layer`` number of its own.  Passes captured into a graph
+    read the step on the GPU, as Int8Linear's do: set it between replays, on
+    their stream.  In eval mode, or with p = 0, nothing is dropped.  x and the
+    residual are bfloat16 or float32, of one type and shape."""
+
+    def __init__(self, p=0.1, seed=0, layer=0, device="cuda"):
+        super().__init__()
+        if not 0 <= p <= 1:
+            raise ValueError("p must lie in [0, 1], got %r" % (p,))
+        self.p, self.seed, self.tag = p, seed, metis.make_tag(layer, metis.OPERAND_X)
+        self.register_buffer("_place", torch.empty(0, device=device), persistent=False)
+        self._init_step()
+
+    def _count_device(self):
+        return self._place.device if self._place.is_cuda else None
+
+    def forward(self, x, residual=None):
+        if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+            raise ValueError("the residual is %s %s, x %s %s" % (tuple(residual.shape), residual.dtype, tuple(x.shape), x.dtype))
+        if not self.training or self.p == 0:
+            return x if residual is None else x + residual
+        return _DropoutFn.apply(x, residual, self, torch.is_grad_enabled())
+
+
+class _EmbeddingFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, w, ids, mod, record):
+        flat = ids.reshape(-1).contiguous()
+        if _record(ctx, mod, record, w):
+            ctx.save_for_backward(flat)
+        ctx.vocab, ctx.w_dtype, ctx.padding, ctx.scale = w.shape[0], w.dtype, mod.padding_idx, mod.scale
+        return metis.embedding(w, flat, mod.scale, out_dtype=mod.out_dtype).view(*ids.shape, w.shape[1])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        dw = metis.embedding_bwd(_rows(dy), *ctx.saved_tensors, ctx.vocab, ctx.padding, ctx.scale, w_dtype=ctx.w_dtype)
+        return dw, None, None, None
+
+
+class Embedding(torch.nn.Module):
+    """``scale`` times the weight's rows (vocab x features) of the given token
+    numbers (int32 or int64), in the weight's type or ``out_dtype``.  The
+    gradient of a row is summed over its tokens in order, in binary32; row
+    ``padding_idx`` takes none.  A token number outside the vocabulary gives a
+    row of zeros, and the next ``metis.status_sync`` reports it."""
+
+    def __init__(self, vocab, features, scale=1.0, padding_idx=None, weight=None, out_dtype=None, device="cuda",
+                 dtype=torch.float32):
+        super().__init__()
+        if padding_idx is not None and not 0 <= padding_idx < vocab:
+            raise ValueError("padding_idx must lie in [0, %d), got %r" % (vocab, padding_idx))
+        if weight is None:
+            weight = torch.empty(vocab, features, dtype=dtype, device=device)
+            torch.nn.init.normal_(weight, std=0.02)
+        if tuple(weight.shape) != (vocab, features):
+            raise ValueError("weight must be vocab x features")
+        self.weight = _parameter(weight, device)
+        self.scale, self.padding_idx, self.out_dtype = scale, padding_idx, out_dtype
+
+    def forward(self, ids):
+        return _EmbeddingFn.apply(self.weight, ids, self, torch.is_grad_enabled())
+
+
+class _CrossEntropyFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, targets, mod, record):
+        need = _record(ctx, mod, record, x, w)
+        x2, flat = _rows(x), targets.reshape(-1).contiguous()
+        losses, lse, total = metis.cross_entropy(x2, w, flat, mod.ignore_index, mean=mod.reduction == "mean")
+        if need:
+            ctx.save_for_backward(x2, w, flat, lse, total)
+            ctx.reduction, ctx.ignore_index, ctx.x_shape = mod.reduction, mod.ignore_index, x.shape
+        return losses.view(targets.shape) if mod.reduction == "none" else total[0]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        x2, w, flat, lse, total = ctx.saved_tensors
+        g = g.reshape(-1).contiguous() if ctx.reduction == "none" else g
+        dx, dw = metis.cross_entropy_bwd(x2, w, flat, lse, g, total[1] if ctx.reduction == "mean" else None,
+                                         ctx.ignore_index, *ctx.needs_input_grad[:2])
+        return dx if dx is None else dx.view(ctx.x_shape), dw, None, None, None
+
+
+class LinearCrossEntropy(torch.nn.Module):
+    """The softmax cross entropy of the logits x W^T against target words, the
+    logits never stored: the last product of a language model and its loss in
+    one.  The weight is vocab x features and may be an Embedding's.
+
+    ``reduction``: "mean" over the tokens that have a target (0 where none
+    has), "sum", or "none" (the loss of each token).  A token whose target is
+    ``ignore_index`` is left out: no loss, zero gradients, whatever its row of x
+    holds; so is one whose target is not a word, which the next
+    ``metis.status_sync`` reports.  x and the weight are bfloat16 or float32 and
+    their gradients theirs; losses are float32."""
+
+    def __init__(self, features, vocab, weight=None, ignore_index=-100, reduction="mean", device="cuda", dtype=torch.float32):
+        super().__init__()
+        if reduction not in ("mean", "sum", "none"):
+            raise ValueError("reduction must be 'mean', 'sum' or 'none', got %r" % (reduction,))
+        if weight is None:
+            weight = torch.empty(vocab, features, dtype=dtype, device=device)
+            torch.nn.init.normal_(weight, std=features ** -0.5)
+        if tuple(weight.shape) != (vocab, features):
+            raise ValueError("weight must be vocab x features")
+        self.weight = _parameter(weight, device)
+        self.ignore_index, self.reduction = ignore_index, reduction
+
+    def forward(self, x, targets):
+        if x.shape[-1] != self.weight.shape[1] or targets.shape != x.shape[:-1]:
+            raise ValueError("x is %s and the targets %s for a weight of %s"
+                             % (tuple(x.shape), tuple(targets.shape), tuple(self.weight.shape)))
+        return _CrossEntropyFn.apply(x, self.weight, targets, self, torch.is_grad_enabled())
+
+
 def set_step(model, step):
-    """Set the training step of every MetisLinear and Int8Linear in ``model``."""
+    """Set the training step of every MetisLinear, Int8Linear and Dropout in ``model``."""
     for m in model.modules():
-        if isinstance(m, (MetisLinear, Int8Linear)):
+        if isinstance(m, (MetisLinear, Int8Linear, Dropout)):
             m.step = step

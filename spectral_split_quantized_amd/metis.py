@@ -52,6 +52,13 @@ class _I8(ctypes.Structure):
                 ("k_len", ctypes.c_int64)]
 
 
+class _Loss(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w", ctypes.c_void_p), ("targets", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ignore_index", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("target_bits", ctypes.c_int32)]
+
+
 class _AdamWConfig(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
@@ -116,6 +123,27 @@ def load():
     lib.metis_grad_norm_workspace.restype = sz
     lib.metis_grad_norm.argtypes = [P, i64, ctypes.c_double, P, P, sz, P]
     lib.metis_grad_norm.restype = i32
+    f64 = ctypes.c_double
+    lib.metis_layernorm_fwd.argtypes = [P, i32, i64, i64, i64, P, P, i32, f64, P, i32, i64, P, P, P]
+    lib.metis_layernorm_fwd.restype = i32
+    lib.metis_layernorm_bwd_workspace.argtypes = [i64, i64]
+    lib.metis_layernorm_bwd_workspace.restype = sz
+    lib.metis_layernorm_bwd.argtypes = [P, i32, i64, P, i32, i64, i64, i64, P, i32, P, P, P, i64, P, P, P, sz, P]
+    lib.metis_layernorm_bwd.restype = i32
+    lib.metis_dropout.argtypes = [P, i32, i64, i64, i64, P, i64, f64, ctypes.c_uint64, u32, i64, P, P, i64, P]
+    lib.metis_dropout.restype = i32
+    lib.metis_embedding_fwd.argtypes = [P, i32, i64, i64, i64, P, i32, i64, f64, P, i32, i64, P]
+    lib.metis_embedding_fwd.restype = i32
+    lib.metis_embedding_bwd_workspace.argtypes = [i64, i64]
+    lib.metis_embedding_bwd_workspace.restype = sz
+    lib.metis_embedding_bwd.argtypes = [P, i32, i64, i64, i64, P, i32, i64, i64, f64, P, i32, i64, P, sz, P]
+    lib.metis_embedding_bwd.restype = i32
+    lib.metis_cross_entropy_workspace.argtypes = [ctypes.POINTER(_Loss), i32]
+    lib.metis_cross_entropy_workspace.restype = sz
+    lib.metis_cross_entropy_fwd.argtypes = [ctypes.POINTER(_Loss), P, P, i32, P, P, sz, P]
+    lib.metis_cross_entropy_fwd.restype = i32
+    lib.metis_cross_entropy_bwd.argtypes = [ctypes.POINTER(_Loss), P, P, i32, P, P, i64, P, i64, P, sz, P]
+    lib.metis_cross_entropy_bwd.restype = i32
     lib.metis_decompose.argtypes = [P, i32, i64, i64, i64, ctypes.POINTER(Config), i32, u32, i64,
                                     ctypes.POINTER(_Factors), P, sz, P]
     lib.metis_decompose.restype = i32
@@ -825,3 +853,191 @@ def grad_norm(grads, max_norm=float("inf"), out=None, workspace=None):
     if out.dtype != torch.float32 or out.numel() != 2 or not out.is_contiguous() or out.get_device() != device:
         raise ValueError("out must be two float32 on the gradients' GPU")
     return _grad_norm_run(table, device, max_norm, out, workspace)
+
+
+# ---------------------------------------------- around the linear layers --
+
+def _matrix(T, rows, cols, name, dtype=None):
+    """A row-major matrix of the library's types."""
+    if T.dim() != 2 or (rows, cols) != tuple(T.shape) or (cols > 1 and T.stride(1) != 1) \
+            or T.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and T.dtype != dtype) \
+            or (rows > 1 and T.stride(0) < cols):
+        raise ValueError("%s must be a %d x %d row-major matrix, %s" % (name, rows, cols, dtype or "float32 or bfloat16"))
+    return T
+
+
+def _values(T, n, name, dtype=torch.float32):
+    """A contiguous vector of n values."""
+    if T.dtype != dtype or T.numel() != n or not T.is_contiguous():
+        raise ValueError("%s must be %d contiguous values, %s" % (name, n, dtype))
+    return T
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _count_ptr(step_count):
+    if step_count is None:
+        return None
+    if step_count.dtype != torch.int64 or step_count.numel() != 1:
+        raise ValueError("a step count tensor must be one int64")
+    return step_count.data_ptr()
+
+
+def layernorm(x, weight=None, bias=None, eps=1e-5, Y=None, out_dtype=None, stats=True):
+    """(y, mean, rstd) of the rows of x (metis_layernorm_fwd); weight and bias
+    have one type.  Y in x's type unless out_dtype or Y says otherwise; mean
+    and rstd are None where stats is false."""
+    rows, cols = x.shape
+    _matrix(x, rows, cols, "x")
+    wb = [t for t in (weight, bias) if t is not None]
+    for t in wb:
+        _dtype_code(t)
+        _values(t, cols, "weight and bias", wb[0].dtype)
+    if Y is None:
+        Y = torch.empty(rows, cols, dtype=out_dtype or x.dtype, device=x.device)
+    _matrix(Y, rows, cols, "Y")
+    mean = rstd = None
+    if stats:
+        mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=x.device)
+    with _on_device(x, Y, *wb):
+        _check(load().metis_layernorm_fwd(x.data_ptr(), _dtype_code(x), rows, cols, _leading(x), _at(weight), _at(bias),
+                                          _dtype_code(wb[0]) if wb else F32, eps, Y.data_ptr(), _dtype_code(Y), _leading(Y),
+                                          _at(mean), _at(rstd), _raw_stream()))
+    return Y, mean, rstd
+
+
+def layernorm_bwd(dy, x, mean, rstd, weight=None, want_dx=True, want_dweight=True, want_dbias=True, w_dtype=None, workspace=None):
+    """(dx, dweight, dbias) of layernorm (metis_layernorm_bwd), None where not
+    wanted; dweight and dbias in weight's type, or w_dtype."""
+    rows, cols = x.shape
+    _matrix(x, rows, cols, "x")
+    _matrix(dy, rows, cols, "dy")
+    if weight is not None:
+        _dtype_code(weight)
+        _values(weight, cols, "weight", weight.dtype)
+    _values(mean, rows, "mean")
+    _values(rstd, rows, "rstd")
+    w_dtype = w_dtype or (torch.float32 if weight is None else weight.dtype)
+    if weight is not None and weight.dtype != w_dtype:
+        raise ValueError("the gradients of weight have its type, %s" % weight.dtype)
+    dx = torch.empty(rows, cols, dtype=x.dtype, device=x.device) if want_dx else None
+    dw, db = (torch.empty(cols, dtype=w_dtype, device=x.device) if want else None for want in (want_dweight, want_dbias))
+    with _on_device(x, dy, mean, rstd, *(() if weight is None else (weight,))):
+        lib = load()
+        need = lib.metis_layernorm_bwd_workspace(rows, cols) if want_dweight or want_dbias else 0
+        ws = _space(workspace, need, x.device)
+        _check(lib.metis_layernorm_bwd(dy.data_ptr(), _dtype_code(dy), _leading(dy), x.data_ptr(), _dtype_code(x), rows, cols,
+                                       _leading(x), _at(weight), F32 if w_dtype == torch.float32 else BF16, mean.data_ptr(),
+                                       rstd.data_ptr(), _at(dx), cols, _at(dw), _at(db), _at(ws),
+                                       0 if ws is None else ws.numel(), _raw_stream()))
+    return dx, dw, db
+
+
+def dropout(x, p, residual=None, seed=0, tag=0, step=0, step_count=None, Y=None):
+    """x with each value dropped with probability p, the others scaled to keep
+    the mean, plus residual if given (metis_dropout): the draws are those of
+    seed, tag and step, or where step_count, a one-element int64 tensor, is not
+    negative when the kernel runs, of that step.  Y may be x or the residual."""
+    rows, cols = x.shape
+    _matrix(x, rows, cols, "x")
+    if Y is None:
+        Y = torch.empty(rows, cols, dtype=x.dtype, device=x.device)
+    _matrix(Y, rows, cols, "Y", x.dtype)
+    more = [t for t in (residual, step_count) if t is not None]
+    if residual is not None:
+        _matrix(residual, rows, cols, "residual", x.dtype)
+    with _on_device(x, Y, *more):
+        _check(load().metis_dropout(x.data_ptr(), _dtype_code(x), rows, cols, _leading(x), _at(residual),
+                                    0 if residual is None else _leading(residual), p, seed, tag, step, _count_ptr(step_count),
+                                    Y.data_ptr(), _leading(Y), _raw_stream()))
+    return Y
+
+
+def _ids(ids, name):
+    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError("%s must be a contiguous vector, int32 or int64" % name)
+    return 32 if ids.dtype == torch.int32 else 64
+
+
+def embedding(w, ids, scale=1.0, Y=None, out_dtype=None):
+    """scale times the rows ids of w (metis_embedding_fwd), in w's type unless
+    out_dtype or Y says otherwise."""
+    vocab, cols = w.shape
+    _matrix(w, vocab, cols, "w")
+    bits, tokens = _ids(ids, "ids"), ids.numel()
+    if Y is None:
+        Y = torch.empty(tokens, cols, dtype=out_dtype or w.dtype, device=w.device)
+    _matrix(Y, tokens, cols, "Y")
+    with _on_device(w, ids, Y):
+        _check(load().metis_embedding_fwd(w.data_ptr(), _dtype_code(w), vocab, cols, _leading(w), ids.data_ptr(), bits, tokens,
+                                          scale, Y.data_ptr(), _dtype_code(Y), _leading(Y), _raw_stream()))
+    return Y
+
+
+def embedding_bwd(dy, ids, vocab, padding=None, scale=1.0, dw=None, w_dtype=None, workspace=None):
+    """The gradient of embedding's w, vocab x cols (metis_embedding_bwd), in
+    dy's type unless w_dtype or dw says otherwise; padding: a token whose row
+    takes none."""
+    tokens, cols = dy.shape
+    _matrix(dy, tokens, cols, "dy")
+    bits = _ids(ids, "ids")
+    if ids.numel() != tokens:
+        raise ValueError("%d tokens, %d rows of dy" % (ids.numel(), tokens))
+    if dw is None:
+        dw = torch.empty(vocab, cols, dtype=w_dtype or dy.dtype, device=dy.device)
+    _matrix(dw, vocab, cols, "dw")
+    with _on_device(dy, ids, dw):
+        lib = load()
+        ws = _space(workspace, lib.metis_embedding_bwd_workspace(tokens, cols), dy.device)
+        _check(lib.metis_embedding_bwd(dy.data_ptr(), _dtype_code(dy), tokens, cols, _leading(dy), ids.data_ptr(), bits, vocab,
+                                       -1 if padding is None else padding, scale, dw.data_ptr(), _dtype_code(dw), _leading(dw),
+                                       ws.data_ptr(), ws.numel(), _raw_stream()))
+    return dw
+
+
+def _loss(x, w, targets, ignore_index):
+    (tokens, cols), vocab = x.shape, w.shape[0]
+    _matrix(x, tokens, cols, "x")
+    _matrix(w, vocab, cols, "w")
+    bits = _ids(targets, "targets")
+    if targets.numel() != tokens:
+        raise ValueError("%d targets of %d tokens" % (targets.numel(), tokens))
+    return _Loss(x.data_ptr(), w.data_ptr(), targets.data_ptr(), tokens, vocab, cols, _leading(x), _leading(w), ignore_index,
+                 _dtype_code(x), _dtype_code(w), bits)
+
+
+def cross_entropy(x, w, targets, ignore_index=-100, mean=True, workspace=None):
+    """(losses, lse, total) of the logits x w^T (metis_cross_entropy_fwd): each
+    token's loss and log-sum-exp, and two values, the mean loss over the tokens
+    that have a target (or the sum) and their number."""
+    l = _loss(x, w, targets, ignore_index)
+    losses, lse = torch.empty(2, l.tokens, dtype=torch.float32, device=x.device)
+    total = torch.empty(2, dtype=torch.float32, device=x.device)
+    with _on_device(x, w, targets):
+        lib = load()
+        ws = _space(workspace, lib.metis_cross_entropy_workspace(ctypes.byref(l), 0), x.device)
+        _check(lib.metis_cross_entropy_fwd(ctypes.byref(l), losses.data_ptr(), lse.data_ptr(), int(mean), total.data_ptr(),
+                                           ws.data_ptr(), ws.numel(), _raw_stream()))
+    return losses, lse, total
+
+
+def cross_entropy_bwd(x, w, targets, lse, grad, count=None, ignore_index=-100, want_dx=True, want_dw=True, workspace=None):
+    """(dx, dw) of cross_entropy (metis_cross_entropy_bwd), None where not
+    wanted: grad holds one value for each loss, or one for all; it is divided by
+    count (total[1], for the mean) where that is given."""
+    l = _loss(x, w, targets, ignore_index)
+    _values(lse, l.tokens, "lse")
+    each = grad.dim() > 0
+    _values(grad, l.tokens if each else 1, "grad")
+    if count is not None:
+        _values(count, 1, "count")
+    dx = torch.empty(l.tokens, l.cols, dtype=x.dtype, device=x.device) if want_dx else None
+    dw = torch.empty(l.vocab, l.cols, dtype=w.dtype, device=x.device) if want_dw else None
+    with _on_device(x, w, targets, lse, grad, *(() if count is None else (count,))):
+        lib = load()
+        ws = _space(workspace, lib.metis_cross_entropy_workspace(ctypes.byref(l), 1), x.device)
+        _check(lib.metis_cross_entropy_bwd(ctypes.byref(l), lse.data_ptr(), grad.data_ptr(), int(each), _at(count), _at(dx),
+                                           l.cols, _at(dw), l.cols, ws.data_ptr(), ws.numel(), _raw_stream()))
+    return dx, dw
