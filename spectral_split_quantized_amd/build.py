@@ -1,4 +1,5 @@
-"""Build libmetis.so in-tree with hipcc for gfx950, and _tensors.so.
+"""Build libmetis.so in-tree with hipcc for gfx950, and the host extensions
+_tensors.so and _layers.so.
 
 Usage: python -m spectral_split_quantized_amd.build
 """
@@ -11,7 +12,6 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 OUT = os.path.join(HERE, "libmetis.so")
-TENSORS_OUT = os.path.join(HERE, "_tensors.so")
 
 # translation units and their extra flags: the register-dequant GEMM is
 # scheduled for instruction-level parallelism (its expansion instructions
@@ -44,27 +44,36 @@ def _run(cmd, verbose):
 
 
 def build_tensors(verbose=False):
-    """_tensors.so: the extension that reads tensor lists (host code against
-    torch's headers)."""
+    """_tensors.so: the extension that reads tensor lists."""
+    return _build_extension("tensors", verbose)
+
+
+def build_layers(verbose=False):
+    """_layers.so: the extension of the layers' autograd nodes."""
+    return _build_extension("layers", verbose)
+
+
+def _build_extension(name, verbose):
+    """Host code against torch's headers, csrc/<name>.cpp -> _<name>.so."""
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    cmd = [hipcc, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, os.path.join(CSRC, "tensors.cpp"),
+    out = os.path.join(HERE, "_%s.so" % name)
+    cmd = [hipcc, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, os.path.join(CSRC, name + ".cpp"),
            "-I", sysconfig.get_paths()["include"]]
-    cmd += [a for d in include_paths() for a in ("-isystem", d)]
-    cmd += [a for d in library_paths() for a in ("-L", d)] + ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
-    tmp = TENSORS_OUT + ".tmp"
-    _run(cmd + ["-o", tmp], verbose)
-    os.replace(tmp, TENSORS_OUT)
-    return TENSORS_OUT
+    cmd += [a for d in include_paths("cuda") for a in ("-isystem", d)]
+    cmd += [a for d in library_paths() for a in ("-L", d)] + ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    _run(cmd + ["-o", out + ".tmp"], verbose)
+    os.replace(out + ".tmp", out)
+    return out
 
 
 def build(verbose=False):
-    """libmetis.so, then _tensors.so: the library needs no torch, so a failure
-    against torch's headers leaves it built."""
+    """libmetis.so, then the extensions: the library needs no torch, so a
+    failure against torch's headers leaves it built."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     os.makedirs(OBJ, exist_ok=True)
     objs = []
@@ -76,6 +85,7 @@ def build(verbose=False):
     _run([hipcc, "--offload-arch=gfx950", "-shared", "-fPIC"] + objs + ["-o", tmp], verbose)
     os.replace(tmp, OUT)
     build_tensors(verbose)
+    build_layers(verbose)
     return OUT
 
 

@@ -16,6 +16,7 @@ The weight is stored as in the pages' notation, ``in_features x
 out_features`` (Y = X W), as an fp32 master.
 """
 
+import ctypes
 import weakref
 
 import torch
@@ -102,35 +103,52 @@ def _rows(x):
     return x if (cols <= 1 or x.stride(1) == 1) and (rows <= 1 or x.stride(0) >= cols) else x.contiguous()
 
 
-_EAGER = weakref.WeakSet()  # nodes of the layers below recorded outside a capture, while their graphs live
+_EAGER = weakref.WeakSet()  # nodes of Int8Linear recorded outside a capture, while their graphs live
 
 
 def _capturing(t):
     return t.is_cuda and torch.cuda.is_current_stream_capturing()
 
 
-def _watch(ctx, layer, leaves, capturing):
+def _refuse_alive(leaves, layer=None):
     """Refuses to record a graph in a capture while one from outside it
-    lives, of this layer or of another with one of the same leaves: both
-    would accumulate a leaf's gradient through one node, which belongs to
-    the other's stream, and joining that stream from a capture ends the
-    process.  (A living graph holds its leaves, so their ids are theirs.)"""
-    if not capturing:
-        ctx.layer, ctx.leaves = weakref.ref(layer), leaves
-        _EAGER.add(ctx)
-    elif any(c.layer() is layer or any(i in c.leaves for i in leaves) for c in _EAGER):
+    lives, of this layer or with one of the same leaves: both would accumulate
+    a leaf's gradient through one node, which belongs to the other's stream,
+    and joining that stream from a capture ends the process.  (A living graph
+    holds its leaves, so their ids are theirs.)"""
+    ids = [id(t) for t in leaves]
+    if any((layer is not None and c.layer() is layer) or any(i in c.leaves for i in ids) for c in _EAGER) \
+            or any(_layers().alive(t) for t in leaves):
         raise RuntimeError("a graph of this layer from outside the capture is alive, or one with the same weight or "
                            "input: drop its outputs first")
 
 
-def _record(ctx, layer, record, *tensors):
-    """Whether this pass is recorded for gradients; if so, its node is watched.
-    ``record`` is the caller's grad mode (inside a forward it is always off,
-    and needs_input_grad says nothing of torch.no_grad())."""
-    need = [t for t, n in zip(tensors, ctx.needs_input_grad) if n] if record else []
-    if need:
-        _watch(ctx, layer, [id(t) for t in need if t.is_leaf], _capturing(need[0]))
-    return bool(need)
+def _watch(ctx, layer, leaves, capturing):
+    if capturing:
+        _refuse_alive(leaves, layer)
+    else:
+        ctx.layer, ctx.leaves = weakref.ref(layer), [id(t) for t in leaves]
+        _EAGER.add(ctx)
+
+
+_ext = None
+
+
+def _layers():
+    """The extension that holds the nodes of the layers around the linear ones
+    (raises if it has not been built)."""
+    global _ext
+    if _ext is None:
+        try:
+            from . import _layers as ext
+        except ImportError as e:
+            raise ImportError("_layers.so cannot be loaded (%s); run python -m spectral_split_quantized_amd.build" % e) from e
+        lib = metis.load()
+        names = ("last_error", "layernorm_fwd", "layernorm_bwd_workspace", "layernorm_bwd", "dropout", "embedding_fwd",
+                 "embedding_bwd_workspace", "embedding_bwd", "cross_entropy_workspace", "cross_entropy_fwd", "cross_entropy_bwd")
+        ext.init([ctypes.cast(getattr(lib, "metis_" + n), ctypes.c_void_p).value for n in names], metis.MetisError, _refuse_alive)
+        _ext = ext
+    return _ext
 
 
 class _Stepped(torch.nn.Module):
@@ -214,7 +232,7 @@ class _Int8LinearFn(torch.autograd.Function):
         capturing = False
         if need_x or need_w:
             capturing = _capturing(x)
-            _watch(ctx, mod, [id(t) for t, need in ((x, need_x), (w, need_w)) if need and t.is_leaf], capturing)
+            _watch(ctx, mod, [t for t, need in ((x, need_x), (w, need_w)) if need and t.is_leaf], capturing)
         # the same orientations as above: X along both axes (Y and dW), W
         # along both (Y and dX); an orientation whose product is not wanted is
         # left out
@@ -353,25 +371,6 @@ def _parameter(weight, device):
     return weight if isinstance(weight, torch.nn.Parameter) else torch.nn.Parameter(weight.to(device).contiguous())
 
 
-class _LayerNormFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, w, b, mod, record):
-        need = _record(ctx, mod, record, x, w, b)
-        x2 = _rows(x)
-        y, mean, rstd = metis.layernorm(x2, w, b, mod.eps, stats=need)
-        if need:
-            ctx.save_for_backward(x2, w, mean, rstd)
-            ctx.w_dtype = None if b is None else b.dtype
-        return y.view(x.shape)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dy):
-        x2, w, mean, rstd = ctx.saved_tensors
-        dx, dw, db = metis.layernorm_bwd(_rows(dy), x2, mean, rstd, w, *ctx.needs_input_grad[:3], w_dtype=ctx.w_dtype)
-        return dx if dx is None else dx.view(dy.shape), dw, db, None, None
-
-
 class LayerNorm(torch.nn.Module):
     """Layer norm over the last dimension, with a weight and a bias (``affine``
     False: without).  x is bfloat16 or float32, y and the gradient of x have
@@ -397,23 +396,7 @@ class LayerNorm(torch.nn.Module):
     def forward(self, x):
         if x.shape[-1] != self.features:
             raise ValueError("x has %d features, the layer %d" % (x.shape[-1], self.features))
-        return _LayerNormFn.apply(x, self.weight, self.bias, self, torch.is_grad_enabled())
-
-
-class _DropoutFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, residual, mod, record):
-        _record(ctx, mod, record, x, residual)
-        ctx.draws = dict(p=mod.p, seed=mod.seed, tag=mod.tag, step=mod.step,
-                         step_count=mod._captured_count() if _capturing(x) else None)
-        y = metis.dropout(_rows(x), residual=None if residual is None else _rows(residual), **ctx.draws)
-        return y.view(x.shape)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dy):
-        dx = metis.dropout(_rows(dy), **ctx.draws).view(dy.shape) if ctx.needs_input_grad[0] else None
-        return dx, dy if ctx.needs_input_grad[1] else None, None, None
+        return _layers().layer_norm(x, self.weight, self.bias, self.eps)
 
 
 class Dropout(_Stepped):
@@ -442,27 +425,14 @@ class Dropout(_Stepped):
         return self._place.device if self._place.is_cuda else None
 
     def forward(self, x, residual=None):
-        if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
-            raise ValueError("the residual is %s %s, x %s %s" % (tuple(residual.shape), residual.dtype, tuple(x.shape), x.dtype))
         if not self.training or self.p == 0:
-            return x if residual is None else x + residual
-        return _DropoutFn.apply(x, residual, self, torch.is_grad_enabled())
-
-
-class _EmbeddingFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, w, ids, mod, record):
-        flat = ids.reshape(-1).contiguous()
-        if _record(ctx, mod, record, w):
-            ctx.save_for_backward(flat)
-        ctx.vocab, ctx.w_dtype, ctx.padding, ctx.scale = w.shape[0], w.dtype, mod.padding_idx, mod.scale
-        return metis.embedding(w, flat, mod.scale, out_dtype=mod.out_dtype).view(*ids.shape, w.shape[1])
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dy):
-        dw = metis.embedding_bwd(_rows(dy), *ctx.saved_tensors, ctx.vocab, ctx.padding, ctx.scale, w_dtype=ctx.w_dtype)
-        return dw, None, None, None
+            if residual is None:
+                return x
+            if residual.shape != x.shape or residual.dtype != x.dtype:
+                raise ValueError("the residual must have x's shape and type")
+            return x + residual
+        count = self._captured_count() if _capturing(x) else None
+        return _layers().dropout(x, residual, self.p, self.seed, self.tag, self._step, count)
 
 
 class Embedding(torch.nn.Module):
@@ -484,30 +454,11 @@ class Embedding(torch.nn.Module):
             raise ValueError("weight must be vocab x features")
         self.weight = _parameter(weight, device)
         self.scale, self.padding_idx, self.out_dtype = scale, padding_idx, out_dtype
+        self._padding = -1 if padding_idx is None else padding_idx
+        self._out = -1 if out_dtype is None else metis.dtype_code(out_dtype)
 
     def forward(self, ids):
-        return _EmbeddingFn.apply(self.weight, ids, self, torch.is_grad_enabled())
-
-
-class _CrossEntropyFn(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, w, targets, mod, record):
-        need = _record(ctx, mod, record, x, w)
-        x2, flat = _rows(x), targets.reshape(-1).contiguous()
-        losses, lse, total = metis.cross_entropy(x2, w, flat, mod.ignore_index, mean=mod.reduction == "mean")
-        if need:
-            ctx.save_for_backward(x2, w, flat, lse, total)
-            ctx.reduction, ctx.ignore_index, ctx.x_shape = mod.reduction, mod.ignore_index, x.shape
-        return losses.view(targets.shape) if mod.reduction == "none" else total[0]
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, g):
-        x2, w, flat, lse, total = ctx.saved_tensors
-        g = g.reshape(-1).contiguous() if ctx.reduction == "none" else g
-        dx, dw = metis.cross_entropy_bwd(x2, w, flat, lse, g, total[1] if ctx.reduction == "mean" else None,
-                                         ctx.ignore_index, *ctx.needs_input_grad[:2])
-        return dx if dx is None else dx.view(ctx.x_shape), dw, None, None, None
+        return _layers().embedding(self.weight, ids, self.scale, self._padding, self._out)
 
 
 class LinearCrossEntropy(torch.nn.Module):
@@ -533,12 +484,10 @@ class LinearCrossEntropy(torch.nn.Module):
             raise ValueError("weight must be vocab x features")
         self.weight = _parameter(weight, device)
         self.ignore_index, self.reduction = ignore_index, reduction
+        self._reduction = ("none", "sum", "mean").index(reduction)
 
     def forward(self, x, targets):
-        if x.shape[-1] != self.weight.shape[1] or targets.shape != x.shape[:-1]:
-            raise ValueError("x is %s and the targets %s for a weight of %s"
-                             % (tuple(x.shape), tuple(targets.shape), tuple(self.weight.shape)))
-        return _CrossEntropyFn.apply(x, self.weight, targets, self, torch.is_grad_enabled())
+        return _layers().linear_cross_entropy(x, self.weight, targets, self.ignore_index, self._reduction)
 
 
 def set_step(model, step):

@@ -213,12 +213,17 @@ def _rows_check(M):
         raise ValueError("M must be a 2-D row-major view (stride(1) == 1), got strides %s" % (M.stride(),))
 
 
-def _dtype_code(t):
-    if t.dtype == torch.bfloat16:
+def dtype_code(dtype):
+    """The library's code of a torch type (metis_dtype)."""
+    if dtype == torch.bfloat16:
         return BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return F32
-    raise TypeError("operands must be bfloat16 or float32, got %s" % t.dtype)
+    raise TypeError("operands must be bfloat16 or float32, got %s" % dtype)
+
+
+def _dtype_code(t):
+    return dtype_code(t.dtype)
 
 
 def make_config(k, s=8, l_k=0, refresh=8, rounding=RNE, seed=0):
