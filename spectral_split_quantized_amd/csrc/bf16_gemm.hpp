@@ -1,8 +1,9 @@
 // bf16_gemm.hpp -- A B^T of bf16 operands on gfx950's matrix instructions, with
 // the epilogues of the loss over a vocabulary.
 //
-// Both operands lie with K along the row, at a pitch that is a multiple of 64
-// values, zeros behind K.  A binary32 operand is a pair of bf16 planes, hi = x
+// An operand lies with K along the row, at a pitch that is a multiple of 64
+// values, zeros behind K; or transposed, with K down the columns (rows of
+// k, each readable up to a multiple of 8 values).  A binary32 operand is a pair of bf16 planes, hi = x
 // rounded and lo = the rest rounded (off by 2^-16 of x at most), and the
 // product is the sum of up to three products of planes (hi hi, hi lo, lo hi;
 // lo lo is no larger than the planes' own error), which simply follow each
@@ -27,6 +28,7 @@ struct BfGemmParams {
   int64_t M, N;
   const uint8_t *a, *b;
   int64_t pitch_a, pitch_b;   // bytes between rows, multiples of 128
+  int64_t rows_a, rows_b;     // of a transposed operand: rows of K (the last repeats up to a whole stage)
   int runs, run_stages;       // K: `runs` products of planes of run_stages stages of 64 each
   int64_t at_a[3], at_b[3];   // where the planes of a run begin, bytes
   int splits, split_stages;   // all stages cut into splits of split_stages (the last may be shorter)
@@ -46,7 +48,7 @@ struct BfGemmParams {
   const float* grad;          // [M], or one with `count`
   const float* count;         // tokens that the loss is the mean over, or null
   int grad_each;              // grad has a value for each token
-  uint16_t* prob;             // [M][ldp], and lo_plane values behind it the low planes
+  uint16_t* prob;             // [M rounded up to 64][ldp], and lo_plane values behind it the low plane
   int64_t ldp, lo_plane;      // lo_plane 0: none
 };
 
@@ -77,6 +79,18 @@ __device__ __forceinline__ int64_t target_of(const void* targets, int targets64,
   return t == ignore || t < 0 || t >= vocab ? -1 : t;
 }
 
+// Four rows of K by sixteen columns of a transposed operand, from LDS rows of
+// bf16: of each sixteen lanes, lane 4 r + c names the columns 4 c .. 4 c + 3 of
+// row r, and lane i receives column i of the four rows.
+typedef short s16x4v_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4v_t lds_s16x4_t;
+
+__device__ __forceinline__ bf16x8v_t read_transposed(uint32_t at, uint32_t row4) {
+  const s16x4v_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(uintptr_t)at);
+  const s16x4v_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(uintptr_t)(at + row4));
+  return __builtin_bit_cast(bf16x8v_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // WM x WN waves of TM x 2 tiles of 32 x 32, one workgroup for many tiles of C,
 // built as the int8 product (the instruction's lane takes the same 16
 // K-consecutive bytes): K-stages of 128 bytes (64 values) travel global -> LDS
@@ -87,8 +101,14 @@ __device__ __forceinline__ int64_t target_of(const void* targets, int targets64,
 // tiles.  B is the instruction's first operand: a lane ends up with row
 // lane % 32 of a tile of C and columns 8 g + 4 (lane / 32) + v.
 //
+// TA, TB: that operand is transposed.  Its stage is 64 rows of K with the
+// tile's columns, and the fragments are read by the transposing LDS read, two
+// for eight values of K.  32 lanes read 64 bytes of each of four rows at a
+// time; chunk c of row k lies at c ^ (4 (k % 4)) (rows of 128 bytes:
+// c ^ (4 (k / 2 % 2))), which puts the four rows on different banks.
+//
 // Rows past M / N repeat the last row (never stored).
-template <int WM, int WN, int TM, int NS, int ER, BfOut OUT>
+template <int WM, int WN, int TM, int NS, int ER, BfOut OUT, bool TA, bool TB>
 __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p) {
   constexpr int TN = 2;
   constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
@@ -129,29 +149,36 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
   const uint8_t *ga, *gb, *ra, *rb;  // at the next stage; of the tile's rows
   uint32_t oa[PA], ob[PB];
   int left, run, run_left;  // stages of the tile still to load; the run of planes and its stages left
+  // bytes of a stage along K
+  const int64_t step_a = TA ? 64 * p.pitch_a : 128, step_b = TB ? 64 * p.pitch_b : 128;
   auto begin_run = [&](int skip) {
-    ga = ra + p.at_a[run] + (int64_t)skip * 128;
-    gb = rb + p.at_b[run] + (int64_t)skip * 128;
+    ga = ra + p.at_a[run] + skip * step_a;
+    gb = rb + p.at_b[run] + skip * step_b;
     run_left = p.run_stages - skip;
   };
+  // lane's row and chunk of the d-th DMA: K along the row, 8 rows of 8 chunks;
+  // transposed, rows of K of B / 8 chunks
+  auto row_of = [&](bool t, int B, int d) { return (wave + d * NW) * (t ? 512 / B : 8) + (t ? lane / (B / 8) : lane >> 3); };
+  auto offset = [&](bool t, int B, int d, int64_t pitch, int last) {
+    const int r = row_of(t, B, d);
+    if (!t) return (uint32_t)min(r, last) * (uint32_t)pitch + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+    const int c = (lane & (B / 8 - 1)) ^ (B >= 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1));
+    return (uint32_t)r * (uint32_t)pitch + 16 * min(c, last);
+  };
   auto source = [&](int64_t m, int64_t n, int s) {
-    ra = p.a + m * p.pitch_a;
-    rb = p.b + n * p.pitch_b;
+    ra = p.a + (TA ? m * 2 : m * p.pitch_a);
+    rb = p.b + (TB ? n * 2 : n * p.pitch_b);
     const int first = s * p.split_stages;
     left = min(p.split_stages, stages - first);
     run = first / p.run_stages;
     begin_run(first - run * p.run_stages);
-    const int last_a = (int)min(p.M - 1 - m, (int64_t)BM), last_b = (int)min(p.N - 1 - n, (int64_t)BN);
+    // the tile's last row, or last chunk of a transposed operand's rows
+    const int last_a = (int)min(TA ? (p.M - 1 - m) >> 3 : p.M - 1 - m, (int64_t)BM);
+    const int last_b = (int)min(TB ? (p.N - 1 - n) >> 3 : p.N - 1 - n, (int64_t)BN);
 #pragma unroll
-    for (int d = 0; d < PA; ++d) {
-      const int r = (wave + d * NW) * 8 + (lane >> 3);
-      oa[d] = (uint32_t)min(r, last_a) * (uint32_t)p.pitch_a + 16 * ((lane & 7) ^ ((r >> 1) & 7));
-    }
+    for (int d = 0; d < PA; ++d) oa[d] = offset(TA, BM, d, p.pitch_a, last_a);
 #pragma unroll
-    for (int d = 0; d < PB; ++d) {
-      const int r = (wave + d * NW) * 8 + (lane >> 3);
-      ob[d] = (uint32_t)min(r, last_b) * (uint32_t)p.pitch_b + 16 * ((lane & 7) ^ ((r >> 1) & 7));
-    }
+    for (int d = 0; d < PB; ++d) ob[d] = offset(TB, BN, d, p.pitch_b, last_b);
   };
   const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)ring + wave * 1024;
   auto issue = [&](int slot) {
@@ -166,14 +193,23 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
       begin_run(0);
     }
     const uint32_t at = base + slot * STAGE;
-    bf_dma16<true>(ga, oa[0], at);
+    // rows past a transposed operand's last one repeat it
+    const int64_t k0 = (int64_t)(p.run_stages - run_left) * 64;
+    auto load = [&](bool t, int B, int n, const uint8_t* g, const uint32_t* o, int64_t pitch, int64_t rows, uint32_t to) {
+      if (t && rows - k0 < 64) {
+        const int last = (int)(rows - 1 - k0);
 #pragma unroll
-    for (int d = 1; d < PA; ++d) bf_dma16<false>(ga, oa[d], at + d * NW * 1024);
-    bf_dma16<true>(gb, ob[0], at + A_BYTES);
+        for (int d = 0; d < n; ++d) bf_dma16<true>(g, o[d] - (uint32_t)max(row_of(t, B, d) - last, 0) * (uint32_t)pitch, to + d * NW * 1024);
+      } else {
+        bf_dma16<true>(g, o[0], to);
 #pragma unroll
-    for (int d = 1; d < PB; ++d) bf_dma16<false>(gb, ob[d], at + A_BYTES + d * NW * 1024);
-    ga += 128;
-    gb += 128;
+        for (int d = 1; d < n; ++d) bf_dma16<false>(g, o[d], to + d * NW * 1024);
+      }
+    };
+    load(TA, BM, PA, ga, oa, p.pitch_a, p.rows_a, at);
+    load(TB, BN, PB, gb, ob, p.pitch_b, p.rows_b, at + A_BYTES);
+    ga += step_a;
+    gb += step_b;
     --left;
     --run_left;
   };
@@ -181,12 +217,30 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
   const int hh = lane >> 5, li = lane & 31, sx = (li >> 1) & 7;
   f32x16v_t acc[TM][TN];
   bf16x8v_t fa[2][TM], fb[2][TN];
+  // transposed: the lane's place of the first four rows of K, before the
+  // tile's 64 bytes of columns, which its row's swizzle picks
+  const int tr = (lane & 15) >> 2;
+  auto place = [&](int B) { return (uint32_t)((8 * hh + tr) * (B * 2) + (lane >> 4 & 1) * 32 + (lane & 3) * 8); };
+  const int pick_a = BM >= 128 ? tr : tr >> 1, pick_b = BN >= 128 ? tr : tr >> 1;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)ring;
   auto read = [&](int slot, int kk) {
     const uint8_t* const st = ring + slot * STAGE + li * 128 + ((2 * kk + hh) ^ sx) * 16;
+    if constexpr (TA) {
+      const uint32_t at = lds0 + slot * STAGE + place(BM) + kk * 16 * (BM * 2);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) fa[kk & 1][i] = *(const bf16x8v_t*)(st + (wm * TM + i) * 4096);
+      for (int i = 0; i < TM; ++i) fa[kk & 1][i] = read_transposed(at + (((wm * TM + i) ^ pick_a) * 64), 4 * (BM * 2));
+    } else {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) fb[kk & 1][j] = *(const bf16x8v_t*)(st + A_BYTES + (wn * TN + j) * 4096);
+      for (int i = 0; i < TM; ++i) fa[kk & 1][i] = *(const bf16x8v_t*)(st + (wm * TM + i) * 4096);
+    }
+    if constexpr (TB) {
+      const uint32_t at = lds0 + slot * STAGE + A_BYTES + place(BN) + kk * 16 * (BN * 2);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) fb[kk & 1][j] = read_transposed(at + (((wn * TN + j) ^ pick_b) * 64), 4 * (BN * 2));
+    } else {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) fb[kk & 1][j] = *(const bf16x8v_t*)(st + A_BYTES + (wn * TN + j) * 4096);
+    }
   };
   auto multiply = [&](int kk) {
 #pragma unroll
@@ -194,11 +248,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
 #pragma unroll
       for (int j = 0; j < TN; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk & 1][j], fa[kk & 1][i], acc[i][j], 0, 0, 0);
-    // one LDS read after each of the first matrix instructions
+    // the LDS reads spread behind the first matrix instructions
+    constexpr int READS = TM * (1 + TA) + TN * (1 + TB), EACH = READS > TM * TN ? 2 : 1;
 #pragma unroll
     for (int t = 0; t < TM * TN; ++t) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (t < TM + TN) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (t * EACH < READS) __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -303,6 +358,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
       // rows of 32 columns, chunks of 4
       constexpr int COLS = BF ? 64 : 32, PER = COLS / 8;
       const bool lo_too = OUT == kBfProb && p.lo_plane != 0;
+      // P has rows up to a multiple of 64, zeros behind M
+      const int64_t M = OUT == kBfProb ? (p.M + 63) & ~(int64_t)63 : p.M;
       const int64_t N = OUT == kBfProb ? p.ldp : p.N, ld = OUT == kBfProb ? p.ldp : p.ldc;
       uint16_t* const c16 = OUT == kBfProb ? p.prob : (uint16_t*)p.C;
       const bool vec = OUT == kBfProb || (((uintptr_t)p.C & 15) == 0 && (p.ldc * (BF ? 2 : 4)) % 16 == 0);
@@ -310,8 +367,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
       for (int i = 0; i < TM; ++i) {
         if constexpr (OUT == kBfProb) {
           const int cols = (int)max((int64_t)0, min((int64_t)64, p.N - col0));
-          const int64_t row = min(row0 + i * 32 + li, p.M - 1);
-          const int64_t word = target_of(p.targets, p.targets64, p.ignore, p.vocab, row);
+          const int64_t r = row0 + i * 32 + li, row = min(r, p.M - 1);
+          const int64_t word = r < p.M ? target_of(p.targets, p.targets64, p.ignore, p.vocab, row) : -1;
           const int64_t t = word - p.v0 - col0;
           const int at = word >= 0 && t >= 0 && t < 64 ? (int)t : -1;
           float g = p.grad_each ? p.grad[row] : p.grad[0];
@@ -373,7 +430,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
                   const int r = k * 8 + rr;
                   u32x4v_t w = *(const u32x4v_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
                   const int64_t row = row0 + i * 32 + r0 + r, col = col0 + j0 * 32 + rc * PER;
-                  if (row >= p.M) continue;
+                  if (row >= M) continue;
                   const int64_t at = offset + row * ld + col;
                   if (col + PER <= N) {
                     u32x4v_t* const to = BF ? (u32x4v_t*)(c16 + at) : (u32x4v_t*)((float*)p.C + at);
@@ -408,7 +465,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
                   const int r = k * RS + el / COLS;
                   const uint8_t* const from = my + r * 128 + ((c / PER) ^ ((r >> 1) & 7)) * 16;
                   const int64_t row = row0 + i * 32 + r0 + r;
-                  if (row >= p.M || col >= N) continue;
+                  if (row >= M || col >= N) continue;
                   const int64_t at = offset + row * ld + col;
                   if constexpr (BF) {
                     c16[at] = *((const uint16_t*)from + c % PER);

@@ -13,10 +13,16 @@ void launch_tiles(const BfGemmParams& g, BfOut out, hipStream_t st) {
   // workgroups that fit the chip at once: one of 8 waves a CU, or two of 4
   const dim3 grid((unsigned)std::min<int64_t>(256 * (8 / (WM * WN)), ceil_div<int64_t>(units, 8) * 8));
   const dim3 block(WM * WN * 64);
-  if (out == kBfStats) hipLaunchKernelGGL((bf_gemm_kernel<WM, WN, TM, NS, ER, kBfStats>), grid, block, 0, st, g);
-  else if (out == kBfProb) hipLaunchKernelGGL((bf_gemm_kernel<WM, WN, TM, NS, ER, kBfProb>), grid, block, 0, st, g);
-  else if (out == kBfBF16) hipLaunchKernelGGL((bf_gemm_kernel<WM, WN, TM, NS, ER, kBfBF16>), grid, block, 0, st, g);
-  else hipLaunchKernelGGL((bf_gemm_kernel<WM, WN, TM, NS, ER, kBfF32>), grid, block, 0, st, g);
+#define LAUNCH(...) hipLaunchKernelGGL((bf_gemm_kernel<WM, WN, TM, NS, ER, __VA_ARGS__>), grid, block, 0, st, g)
+  // the logits' product has K along both rows, dx = P W has W transposed, dw =
+  // P^T x both
+  if (out == kBfStats) LAUNCH(kBfStats, false, false);
+  else if (out == kBfProb) LAUNCH(kBfProb, false, false);
+  else if (out == kBfBF16 && g.rows_a) LAUNCH(kBfBF16, true, true);
+  else if (out == kBfBF16) LAUNCH(kBfBF16, false, true);
+  else if (g.rows_a) LAUNCH(kBfF32, true, true);
+  else LAUNCH(kBfF32, false, true);
+#undef LAUNCH
 }
 
 int tile_of(int64_t M, int64_t N) {

@@ -21,15 +21,19 @@
 
 namespace metis {
 
-// bf16 planes of rows: dst[plane][row][pitch] with zeros behind cols; the high
-// plane is x rounded to bf16, the low one the rest rounded.  Eight values a
-// thread.
+// bf16 planes of rows: dst[plane][row][pitch] with zeros behind cols, in the
+// rows behind `rows` up to out_rows, and in the rows of tokens without a part
+// in the loss (targets not null); the high plane is x rounded to bf16, the low
+// one the rest rounded.  Eight values a thread.
 struct PlanesParams {
   const void* src;
   int64_t rows, cols, ld;
   int bf16, vec;
   uint16_t* dst;
-  int64_t pitch, plane;  // values; plane 0: high plane alone
+  int64_t out_rows, pitch, plane;  // pitch and plane in values; plane 0: high plane alone
+  const void* targets;
+  int targets64;
+  int64_t vocab, ignore;
 };
 
 __device__ __forceinline__ void store_planes(uint16_t* dst, int64_t at, int64_t plane, const float* v) {
@@ -44,67 +48,19 @@ __device__ __forceinline__ void store_planes(uint16_t* dst, int64_t at, int64_t 
 }
 
 __global__ __launch_bounds__(256) void planes_kernel(PlanesParams p) {
-  const int64_t per = p.pitch >> 3, total = p.rows * per;
+  const int64_t per = p.pitch >> 3, total = p.out_rows * per;
   for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
     const int64_t row = id / per, c = (id - row * per) * 8;
-    float v[8];
-    if (p.vec && c + 8 <= p.cols) {
-      load8(p.src, p.bf16, row * p.ld + c, v);
-    } else {
+    float v[8] = {};
+    if (row < p.rows && (!p.targets || target_of(p.targets, p.targets64, p.ignore, p.vocab, row) >= 0)) {
+      if (p.vec && c + 8 <= p.cols) {
+        load8(p.src, p.bf16, row * p.ld + c, v);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = c + e < p.cols ? load1(p.src, p.bf16, row * p.ld + c + e) : 0.0f;
+        for (int e = 0; e < 8; ++e) v[e] = c + e < p.cols ? load1(p.src, p.bf16, row * p.ld + c + e) : 0.0f;
+      }
     }
     store_planes(p.dst, row * p.pitch + c, p.plane, v);
-  }
-}
-
-// the same of the transpose: dst[plane][column][pitch], zeros behind rows and
-// in the columns of tokens without a part in the loss (targets not null).
-// Tiles of 64 x 64 through LDS.
-struct TransposeParams {
-  const void* src;
-  int64_t rows, cols, ld;
-  int bf16, vec;
-  uint16_t* dst;
-  int64_t pitch, plane;
-  const void* targets;
-  int targets64;
-  int64_t vocab, ignore;
-};
-
-__global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p) {
-  __shared__ float tile[64][65];
-  const int64_t tiles_r = (p.pitch + 63) >> 6, tiles = tiles_r * ((p.cols + 63) >> 6);
-  for (int64_t b = blockIdx.x; b < tiles; b += gridDim.x) {
-    const int64_t c0 = b / tiles_r * 64, r0 = b % tiles_r * 64;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = (threadIdx.x >> 3) + 32 * k, c = (threadIdx.x & 7) * 8;
-      const int64_t row = r0 + r, col = c0 + c;
-      float v[8] = {};
-      if (row < p.rows && (!p.targets || target_of(p.targets, p.targets64, p.ignore, p.vocab, row) >= 0)) {
-        if (p.vec && col + 8 <= p.cols) {
-          load8(p.src, p.bf16, row * p.ld + col, v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = col + e < p.cols ? load1(p.src, p.bf16, row * p.ld + col + e) : 0.0f;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) tile[r][c + e] = v[e];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = (threadIdx.x >> 3) + 32 * k, r = (threadIdx.x & 7) * 8;
-      if (c0 + c < p.cols && r0 + r < p.pitch) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = tile[r + e][c];
-        store_planes(p.dst, (c0 + c) * p.pitch + r0 + r, p.plane, v);
-      }
-    }
-    __syncthreads();
   }
 }
 

@@ -171,13 +171,13 @@ struct LossWs {
   uint16_t *x, *w;             // planes of x, of a piece of w (where not as they are)
   float2* stat;                // forward
   float *target, *losses;
-  uint16_t *p, *pt, *wt, *xt;  // backward: P, P^T, the piece of w transposed, x transposed
+  uint16_t* p;                 // backward: P of a piece
   float *dx, *part;            // dx summed over the pieces, parts of K
 };
 
 LossWs carve_loss(Carver& cv, const metis_loss& l, const LossPlan& p, bool backward) {
   LossWs w{};
-  if (!p.x_as_is) w.x = cv.take<uint16_t>((size_t)p.xp * p.N * p.Dp);
+  if (backward || !p.x_as_is) w.x = cv.take<uint16_t>((size_t)p.xp * p.Np * p.Dp);
   if (!p.w_as_is) w.w = cv.take<uint16_t>((size_t)p.wp * std::min(p.piece, p.V) * p.Dp);
   if (!backward) {
     w.stat = cv.take<float2>((size_t)ceil_div<int64_t>(p.V, 64) * p.N);
@@ -186,11 +186,7 @@ LossWs carve_loss(Carver& cv, const metis_loss& l, const LossPlan& p, bool backw
     return w;
   }
   const int64_t words = pad64(std::min(p.piece, p.V));
-  const int pp = p.pair ? 2 : 1;
-  w.p = cv.take<uint16_t>((size_t)pp * p.N * words);
-  w.pt = cv.take<uint16_t>((size_t)pp * words * p.Np);
-  w.wt = cv.take<uint16_t>((size_t)(p.xp == 2 ? p.wp : 1) * p.D * words);
-  w.xt = cv.take<uint16_t>((size_t)(p.wp == 2 ? p.xp : 1) * p.D * p.Np);
+  w.p = cv.take<uint16_t>((size_t)(p.pair ? 2 : 1) * p.Np * words);
   w.dx = cv.take<float>((size_t)p.N * p.D);
   const int s = bf_gemm_most_splits(p.N, p.D);
   if (s > 1) w.part = cv.take<float>((size_t)s * p.N * p.D);
@@ -207,31 +203,22 @@ metis_status loss_check(const metis_loss* l, const char* what) {
   return METIS_OK;
 }
 
-// planes of rows that cannot be an operand as they are, else the rows themselves
+// planes of rows that cannot be an operand as they are, else the rows
+// themselves; `mask`: always planes, rows up to a multiple of 64, zeros in those
+// of tokens that the loss leaves out
 metis_status as_operand(const void* src, int32_t dt, int64_t ld, int64_t rows, int64_t cols, bool as_is, int planes,
-                        uint16_t* dst, Planes* out, hipStream_t st) {
-  if (as_is) {
-    *out = {(const uint8_t*)src, rows > 1 ? ld * 2 : pad64(cols) * 2, 0, 1};
+                        uint16_t* dst, const metis_loss* mask, Planes* out, hipStream_t st) {
+  const int64_t pitch = pad64(cols), out_rows = mask ? pad64(rows) : rows;
+  if (as_is && !mask) {
+    *out = {(const uint8_t*)src, rows > 1 ? ld * 2 : pitch * 2, 0, 1};
     return METIS_OK;
   }
-  const int64_t pitch = pad64(cols);
-  PlanesParams p{src, rows, cols, ld, dt == METIS_BF16, vec_rows(src, dt, ld, rows), dst, pitch, planes > 1 ? rows * pitch : 0};
-  hipLaunchKernelGGL(planes_kernel, dim3(grid_for(rows * (pitch / 8), 256)), dim3(256), 0, st, p);
-  LAUNCH_CHECK();
-  *out = {(const uint8_t*)dst, pitch * 2, rows * pitch * 2, planes};
-  return METIS_OK;
-}
-
-// planes of the transpose, zeros behind rows up to a multiple of 64
-metis_status transposed(const void* src, int32_t dt, int64_t ld, int64_t rows, int64_t cols, int planes, uint16_t* dst,
-                        const metis_loss* mask, Planes* out, hipStream_t st) {
-  const int64_t pitch = pad64(rows);
-  TransposeParams p{src, rows, cols, ld, dt == METIS_BF16, vec_rows(src, dt, ld, rows), dst, pitch,
-                    planes > 1 ? cols * pitch : 0, nullptr, 0, 0, 0};
+  PlanesParams p{src, rows, cols, ld, dt == METIS_BF16, vec_rows(src, dt, ld, rows), dst, out_rows, pitch,
+                 planes > 1 ? out_rows * pitch : 0, nullptr, 0, 0, 0};
   if (mask) p.targets = mask->targets, p.targets64 = mask->target_bits == 64, p.vocab = mask->vocab, p.ignore = mask->ignore_index;
-  hipLaunchKernelGGL(transpose_kernel, dim3(grid_for(pitch / 64 * ceil_div<int64_t>(cols, 64), 1)), dim3(256), 0, st, p);
+  hipLaunchKernelGGL(planes_kernel, dim3(grid_for(out_rows * (pitch / 8), 256)), dim3(256), 0, st, p);
   LAUNCH_CHECK();
-  *out = {(const uint8_t*)dst, pitch * 2, cols * pitch * 2, planes};
+  *out = {(const uint8_t*)dst, pitch * 2, out_rows * pitch * 2, planes};
   return METIS_OK;
 }
 
@@ -487,13 +474,13 @@ metis_status metis_cross_entropy_fwd(const metis_loss* l, float* losses, float* 
     Carver cv(ws, ws_bytes);
     const LossWs w = carve_loss(cv, *l, p, false);
     Planes x, v;
-    TRY(as_operand(l->x, l->x_dtype, l->ldx, p.N, p.D, p.x_as_is, p.xp, w.x, &x, st));
+    TRY(as_operand(l->x, l->x_dtype, l->ldx, p.N, p.D, p.x_as_is, p.xp, w.x, nullptr, &x, st));
     // a weight that needs no copies goes through in one piece
     // (as long as its tiles can be counted in 32 bits)
     const int64_t piece = p.w_as_is && ceil_div<int64_t>(p.N, 64) * ceil_div<int64_t>(p.V, 128) < 1 << 30 ? p.V : p.piece;
     for (int64_t v0 = 0; v0 < p.V; v0 += piece) {
       const int64_t n = std::min(piece, p.V - v0);
-      TRY(as_operand(rows_from(l->w, l->w_dtype, l->ldw, v0), l->w_dtype, l->ldw, n, p.D, p.w_as_is, p.wp, w.w, &v, st));
+      TRY(as_operand(rows_from(l->w, l->w_dtype, l->ldw, v0), l->w_dtype, l->ldw, n, p.D, p.w_as_is, p.wp, w.w, nullptr, &v, st));
       BfGemmParams g = product(x, p.N, v, n, p.D, true);
       set_targets(g, *l, v0);
       g.stat = w.stat, g.target_logit = w.target;
@@ -537,24 +524,23 @@ metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, cons
   TRY(ensure_device_tables());
   Carver cv(ws, ws_bytes);
   const LossWs w = carve_loss(cv, *l, p, true);
-  Planes x, v, xt, wt, pt;
-  TRY(as_operand(l->x, l->x_dtype, l->ldx, p.N, p.D, p.x_as_is, p.xp, w.x, &x, st));
-  if (dW) TRY(transposed(l->x, l->x_dtype, l->ldx, p.N, p.D, p.wp == 2 ? p.xp : 1, w.xt, l, &xt, st));
+  Planes x, v;
+  TRY(as_operand(l->x, l->x_dtype, l->ldx, p.N, p.D, p.x_as_is, p.xp, w.x, l, &x, st));
   const bool dx_f32 = l->x_dtype == METIS_F32;
   const bool one = p.piece >= p.V;
   for (int64_t v0 = 0; v0 < p.V; v0 += p.piece) {
     const int64_t n = std::min(p.piece, p.V - v0), np = pad64(n);
     const void* wv = rows_from(l->w, l->w_dtype, l->ldw, v0);
-    TRY(as_operand(wv, l->w_dtype, l->ldw, n, p.D, p.w_as_is, p.wp, w.w, &v, st));
+    TRY(as_operand(wv, l->w_dtype, l->ldw, n, p.D, p.w_as_is, p.wp, w.w, nullptr, &v, st));
     BfGemmParams g = product(x, p.N, v, n, p.D, true);
     set_targets(g, *l, v0);
     g.lse = lse, g.grad = grad, g.count = count, g.grad_each = grad_each;
-    g.prob = w.p, g.ldp = np, g.lo_plane = p.pair ? p.N * np : 0;
+    g.prob = w.p, g.ldp = np, g.lo_plane = p.pair ? p.Np * np : 0;
     TRY(run_product(g, kBfProb, st));
-    const Planes pr{(const uint8_t*)w.p, np * 2, p.N * np * 2, p.pair ? 2 : 1};
+    const Planes pr{(const uint8_t*)w.p, np * 2, p.Np * np * 2, p.pair ? 2 : 1};
     if (dX) {
-      TRY(transposed(wv, l->w_dtype, l->ldw, n, p.D, p.xp == 2 ? p.wp : 1, w.wt, nullptr, &wt, st));
-      g = product(pr, p.N, wt, p.D, n, dx_f32);
+      g = product(pr, p.N, v, p.D, n, dx_f32);
+      g.rows_b = n;
       const int splits = bf_gemm_splits(p.N, p.D, g.runs * g.run_stages);
       // one piece: straight to dX; else summed in binary32, in dX itself where it is binary32
       void* const sum = dx_f32 ? dX : (void*)w.dx;
@@ -574,13 +560,8 @@ metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, cons
       }
     }
     if (dW) {
-      TRY(transposed(w.p, METIS_BF16, np, p.N, n, 1, w.pt, nullptr, &pt, st));
-      if (p.wp == 2) {
-        Planes lo;
-        TRY(transposed(w.p + p.N * np, METIS_BF16, np, p.N, n, 1, w.pt + n * p.Np, nullptr, &lo, st));
-        pt.count = 2;
-      }
-      g = product(pt, n, xt, p.D, p.N, p.wp == 2);
+      g = product(pr, n, x, p.D, p.N, p.wp == 2);
+      g.rows_a = g.rows_b = p.Np;
       g.C = (char*)dW + v0 * lddw * value_size(l->w_dtype), g.ldc = lddw;
       TRY(run_product(g, p.wp == 2 ? kBfF32 : kBfBF16, st));
     }
