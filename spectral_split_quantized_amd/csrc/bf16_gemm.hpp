@@ -44,6 +44,7 @@ struct BfGemmParams {
   int64_t vocab, ignore;
   float2* stat;               // [ceil(N / 64) of all words][M]: largest logit, sum of exponentials
   float* target_logit;        // [M]
+  uint32_t* done;             // kBfStats: set to zero
   const float* lse;           // [M]
   const float* grad;          // [M], or one with `count`
   const float* count;         // tokens that the loss is the mean over, or null
@@ -61,16 +62,11 @@ constexpr float kLog2E = 1.4426950408889634f;
 // Global -> LDS load of 16 bytes a lane to LDS address lds + 16 lane (base and
 // lds wave-uniform), as assembly so that the compiler does not wait for the
 // loads in flight before every LDS read.  A wait state stands between the
-// write of M0 and its use, and five before the first use of a base, which a
-// vector instruction just before may have written.
-template <bool FIRST>
+// write of M0 and its use.  (The base comes from scalar arithmetic: no vector
+// instruction writes it just before.)
 __device__ __forceinline__ void bf_dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  if constexpr (FIRST)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory", "m0");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
 }
 
 // the word of token `row`, or -1 where it has no part in the loss
@@ -165,6 +161,13 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
     const int c = (lane & (B / 8 - 1)) ^ (B >= 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1));
     return (uint32_t)r * (uint32_t)pitch + 16 * min(c, last);
   };
+  int last_a, last_b;
+  auto offsets = [&] {
+#pragma unroll
+    for (int d = 0; d < PA; ++d) oa[d] = offset(TA, BM, d, p.pitch_a, last_a);
+#pragma unroll
+    for (int d = 0; d < PB; ++d) ob[d] = offset(TB, BN, d, p.pitch_b, last_b);
+  };
   auto source = [&](int64_t m, int64_t n, int s) {
     ra = p.a + (TA ? m * 2 : m * p.pitch_a);
     rb = p.b + (TB ? n * 2 : n * p.pitch_b);
@@ -173,15 +176,20 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
     run = first / p.run_stages;
     begin_run(first - run * p.run_stages);
     // the tile's last row, or last chunk of a transposed operand's rows
-    const int last_a = (int)min(TA ? (p.M - 1 - m) >> 3 : p.M - 1 - m, (int64_t)BM);
-    const int last_b = (int)min(TB ? (p.N - 1 - n) >> 3 : p.N - 1 - n, (int64_t)BN);
-#pragma unroll
-    for (int d = 0; d < PA; ++d) oa[d] = offset(TA, BM, d, p.pitch_a, last_a);
-#pragma unroll
-    for (int d = 0; d < PB; ++d) ob[d] = offset(TB, BN, d, p.pitch_b, last_b);
+    last_a = (int)min(TA ? (p.M - 1 - m) >> 3 : p.M - 1 - m, (int64_t)BM);
+    last_b = (int)min(TB ? (p.N - 1 - n) >> 3 : p.N - 1 - n, (int64_t)BN);
+    offsets();
   };
   const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)ring + wave * 1024;
-  auto issue = [&](int slot) {
+  // A stage's loads come in two parts, one for each operand.  begin: on to the
+  // next stage; rows past a transposed operand's last one repeat it, which only
+  // a run's last stage has.
+  auto repeat_last = [&](int B, int n, uint32_t* o, int64_t pitch, int last) {
+    if (last >= 63) return;
+#pragma unroll
+    for (int d = 0; d < n; ++d) o[d] -= (uint32_t)max(row_of(true, B, d) - last, 0) * (uint32_t)pitch;
+  };
+  auto begin = [&] {
     if (left == 0) {  // on to the next tile, or, behind the last one, the same once more
       int64_t m = m0, n = n0;
       int s = split;
@@ -190,28 +198,24 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
       source(m, n, s);
     } else if (run_left == 0) {
       ++run;
+      offsets();
       begin_run(0);
     }
-    const uint32_t at = base + slot * STAGE;
-    // rows past a transposed operand's last one repeat it
-    const int64_t k0 = (int64_t)(p.run_stages - run_left) * 64;
-    auto load = [&](bool t, int B, int n, const uint8_t* g, const uint32_t* o, int64_t pitch, int64_t rows, uint32_t to) {
-      if (t && rows - k0 < 64) {
-        const int last = (int)(rows - 1 - k0);
-#pragma unroll
-        for (int d = 0; d < n; ++d) bf_dma16<true>(g, o[d] - (uint32_t)max(row_of(t, B, d) - last, 0) * (uint32_t)pitch, to + d * NW * 1024);
-      } else {
-        bf_dma16<true>(g, o[0], to);
-#pragma unroll
-        for (int d = 1; d < n; ++d) bf_dma16<false>(g, o[d], to + d * NW * 1024);
-      }
-    };
-    load(TA, BM, PA, ga, oa, p.pitch_a, p.rows_a, at);
-    load(TB, BN, PB, gb, ob, p.pitch_b, p.rows_b, at + A_BYTES);
-    ga += step_a;
-    gb += step_b;
-    --left;
-    --run_left;
+    if ((TA || TB) && run_left == 1) {
+      const int k0 = (p.run_stages - 1) * 64;
+      if (TA) repeat_last(BM, PA, oa, p.pitch_a, (int)(p.rows_a - 1 - k0));
+      if (TB) repeat_last(BN, PB, ob, p.pitch_b, (int)(p.rows_b - 1 - k0));
+    }
+  };
+  auto load_a = [&](int slot, int d) { bf_dma16(ga, oa[d], base + slot * STAGE + d * NW * 1024); };
+  auto load_b = [&](int slot, int d) {
+    bf_dma16(gb, ob[d], base + slot * STAGE + A_BYTES + d * NW * 1024);
+    if (d == PB - 1) {  // the stage's last
+      ga += step_a;
+      gb += step_b;
+      --left;
+      --run_left;
+    }
   };
 
   const int hh = lane >> 5, li = lane & 31, sx = (li >> 1) & 7;
@@ -223,39 +227,47 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
   auto place = [&](int B) { return (uint32_t)((8 * hh + tr) * (B * 2) + (lane >> 4 & 1) * 32 + (lane & 3) * 8); };
   const int pick_a = BM >= 128 ? tr : tr >> 1, pick_b = BN >= 128 ? tr : tr >> 1;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)ring;
-  auto read = [&](int slot, int kk) {
-    const uint8_t* const st = ring + slot * STAGE + li * 128 + ((2 * kk + hh) ^ sx) * 16;
+  auto read_a = [&](int slot, int kk, int i) {
     if constexpr (TA) {
       const uint32_t at = lds0 + slot * STAGE + place(BM) + kk * 16 * (BM * 2);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[kk & 1][i] = read_transposed(at + (((wm * TM + i) ^ pick_a) * 64), 4 * (BM * 2));
+      fa[kk & 1][i] = read_transposed(at + (((wm * TM + i) ^ pick_a) * 64), 4 * (BM * 2));
     } else {
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[kk & 1][i] = *(const bf16x8v_t*)(st + (wm * TM + i) * 4096);
-    }
-    if constexpr (TB) {
-      const uint32_t at = lds0 + slot * STAGE + A_BYTES + place(BN) + kk * 16 * (BN * 2);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) fb[kk & 1][j] = read_transposed(at + (((wn * TN + j) ^ pick_b) * 64), 4 * (BN * 2));
-    } else {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) fb[kk & 1][j] = *(const bf16x8v_t*)(st + A_BYTES + (wn * TN + j) * 4096);
+      fa[kk & 1][i] = *(const bf16x8v_t*)(ring + slot * STAGE + li * 128 + ((2 * kk + hh) ^ sx) * 16 + (wm * TM + i) * 4096);
     }
   };
-  auto multiply = [&](int kk) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk & 1][j], fa[kk & 1][i], acc[i][j], 0, 0, 0);
-    // the LDS reads spread behind the first matrix instructions
-    constexpr int READS = TM * (1 + TA) + TN * (1 + TB), EACH = READS > TM * TN ? 2 : 1;
+  auto read_b = [&](int slot, int kk, int j) {
+    if constexpr (TB) {
+      const uint32_t at = lds0 + slot * STAGE + A_BYTES + place(BN) + kk * 16 * (BN * 2);
+      fb[kk & 1][j] = read_transposed(at + (((wn * TN + j) ^ pick_b) * 64), 4 * (BN * 2));
+    } else {
+      fb[kk & 1][j] = *(const bf16x8v_t*)(ring + slot * STAGE + A_BYTES + li * 128 + ((2 * kk + hh) ^ sx) * 16 + (wn * TN + j) * 4096);
+    }
+  };
+  // the fragments in the order of their use: b0 a0 b1 a1 ...
+  auto read = [&](int slot, int kk, int f) {
+    if (f < 2 * TN && f < 2 * TM ? f & 1 : f < TM + TN && TM > TN) read_a(slot, kk, f < 2 * TN ? f >> 1 : f - TN);
+    else read_b(slot, kk, f < 2 * TM ? f >> 1 : f - TM);
+  };
+  // Sub-step kk: its matrix instructions, and between them, in this order, the
+  // LDS reads of the next one (of slot `from`) and the loads of one operand of
+  // a stage (into slot `to`): the loads of all waves at once would fill the
+  // memory pipe's queue and hold the matrix instructions behind them.
+  auto step = [&](int kk, int from, int to) {
 #pragma unroll
     for (int t = 0; t < TM * TN; ++t) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (t * EACH < READS) __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
+      const int i = t / TN, j = t % TN;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk & 1][j], fa[kk & 1][i], acc[i][j], 0, 0, 0);
+      constexpr int EACH = (TM + TN + TM * TN - 1) / (TM * TN);
+#pragma unroll
+      for (int f = t * EACH; f < (t + 1) * EACH && f < TM + TN; ++f) read(from, (kk + 1) & 3, f);
+      const int n = kk == 3 ? PA : kk == 0 ? PB : 0;
+#pragma unroll
+      for (int d = t * n / (TM * TN); d < (t + 1) * n / (TM * TN); ++d) {
+        if (kk == 3) load_a(to, d);
+        else load_b(to, d);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
   };
   // this wave's LDS reads are done and at most N of its loads in flight: with
   // the barrier, a stage has landed and the one before it is read out
@@ -270,15 +282,23 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
   };
-  using First = std::integral_constant<int, (NS - 1) * (PA + PB)>;
+  using First = std::integral_constant<int, (NS - 1) * (PA + PB) - PB>;
   using Left = std::integral_constant<int, (NS - 2) * (PA + PB)>;
 
   source(m0, n0, split);
 #pragma unroll
-  for (int s = 0; s < NS; ++s) issue(s);
+  for (int s = 0; s < NS; ++s) {
+    begin();
+#pragma unroll
+    for (int d = 0; d < PA; ++d) load_a(s, d);
+    if (s == NS - 1) break;  // the last one's second part comes in the first sub-step
+#pragma unroll
+    for (int d = 0; d < PB; ++d) load_b(s, d);
+  }
   landed(First{});
-  read(0, 0);
-  int slot = 0;
+#pragma unroll
+  for (int f = 0; f < TM + TN; ++f) read(0, 0, f);
+  int slot = 0, free_slot = NS - 1;
   for (bool more = true; more;) {
     const int nk = min(p.split_stages, stages - split * p.split_stages);
     const int64_t row0 = m0 + wm * TM * 32, col0 = n0 + wn * TN * 32;
@@ -287,16 +307,14 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x16v_t{};
     for (int kt = 0; kt < nk; ++kt) {
-#pragma unroll
-      for (int kk = 0; kk < 3; ++kk) {
-        read(slot, kk + 1);
-        multiply(kk);
-      }
+      step(0, slot, free_slot);
+      step(1, slot, 0);
+      step(2, slot, 0);
       landed(Left{});
-      issue(slot);
+      free_slot = slot;
       slot = slot + 1 == NS ? 0 : slot + 1;
-      read(slot, 0);
-      multiply(3);
+      begin();
+      step(3, slot, free_slot);
     }
 
     // the lane indices taken anew, so that what is made of them does not
@@ -310,9 +328,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
     const __attribute__((address_space(4))) BfGemmParams& p = *args;
 
     if constexpr (OUT == kBfStats) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
       // a row's 64 columns lie in two lanes, 32 values each
       if (col0 < p.N) {
         const int cols = (int)min((int64_t)64, p.N - col0);
+        auto column = [&](int j, int e) { return j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3); };
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
           const int64_t row = row0 + i * 32 + li;
@@ -323,7 +343,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
             for (int j = 0; j < TN; ++j)
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3) >= cols) acc[i][j][e] = -__builtin_inff();
+                if (column(j, e) >= cols) acc[i][j][e] = -__builtin_inff();
           }
           float m = -__builtin_inff();
 #pragma unroll
@@ -346,7 +366,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
             for (int j = 0; j < TN; ++j)
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3) == at) p.target_logit[row] = acc[i][j][e];
+                if (column(j, e) == at) p.target_logit[row] = acc[i][j][e];
           }
         }
       }
@@ -366,15 +386,16 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         if constexpr (OUT == kBfProb) {
-          const int cols = (int)max((int64_t)0, min((int64_t)64, p.N - col0));
           const int64_t r = row0 + i * 32 + li, row = min(r, p.M - 1);
           const int64_t word = r < p.M ? target_of(p.targets, p.targets64, p.ignore, p.vocab, row) : -1;
           const int64_t t = word - p.v0 - col0;
-          const int at = word >= 0 && t >= 0 && t < 64 ? (int)t : -1;
+          const int at = word >= 0 && t >= 0 && t < TN * 32 ? (int)t : -1;
+          const int cols = (int)max((int64_t)0, min((int64_t)(TN * 32), p.N - col0));
           float g = p.grad_each ? p.grad[row] : p.grad[0];
           if (p.count) g /= p.count[0];
           const float off = -p.lse[row] * kLog2E;
           const bool some = word >= 0 && g != 0.0f;  // a token without a part: zeros, whatever its logits
+          auto column = [&](int j, int e) { return j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3); };
 #pragma unroll
           for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -387,15 +408,16 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
             for (int j = 0; j < TN; ++j)
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (some && j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3) == at) acc[i][j][e] -= g;
+                if (some && column(j, e) == at) acc[i][j][e] -= g;
           }
-          if (cols < 64) {
+          if (cols < TN * 32) {
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3) >= cols) acc[i][j][e] = 0.0f;
+                if (column(j, e) >= cols) acc[i][j][e] = 0.0f;
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int j0 = 0; j0 < TN; j0 += COLS / 32) {

@@ -25,32 +25,61 @@ void launch_tiles(const BfGemmParams& g, BfOut out, hipStream_t st) {
 #undef LAUNCH
 }
 
-int tile_of(int64_t M, int64_t N) {
-  auto tiles = [&](int m, int n) { return ceil_div<int64_t>(M, m) * ceil_div<int64_t>(N, n); };
-  if (tiles(256, 256) >= 256) return 256;
-  return tiles(128, 128) >= 256 ? 128 : 64;
+// Tiles: rows, columns, and what a stage takes, in us, with one workgroup on a
+// CU and with two (measured on products that fill the chip once or many
+// times).
+struct Tile {
+  int m, n;
+  double one, two;
+};
+constexpr Tile kTiles[3] = {{256, 256, 1.6, 0}, {128, 128, 0.61, 1.1}, {64, 128, 0.37, 0.77}};
+
+// us that M x N x 64 stages take in `splits` parts of K: whole rounds of
+// workgroups and the rest of one, what a workgroup starts and ends with, and
+// the sums that the parts write and their join reads.
+double time_of(const Tile& t, int64_t M, int64_t N, int stages, int splits) {
+  const int64_t units = ceil_div<int64_t>(M, t.m) * ceil_div<int64_t>(N, t.n) * splits, slots = t.two ? 512 : 256;
+  const int64_t rounds = units / slots, rest = units % slots;
+  const double full = t.two ? t.two : t.one, part = rest == 0 ? 0 : rest <= 256 ? t.one : t.two;
+  const double us = (double)(rounds + (rest > 0)) * 2 + ceil_div(stages, splits) * (rounds * full + part);
+  return splits == 1 ? us : us + 4 + splits * (double)M * N * 8 / 4.5e6;
+}
+
+// the fastest tile and splits by that estimate (us measured, without the join):
+//   8192 x 768 x 25152: 256 x 256 whole 583, in 2 328, in 8 366; 128 x 128
+//     whole 422, in 2 425; 64 x 128 455
+//   1024 x 1024 x 30720: 256 x 256 in 8 91, in 16 66; 128 x 128 in 8 85; 64 x
+//     128 whole 178, in 4 86
+//   100 x 512 x 5760: 64 x 128 whole 38, in 12 8; 128 x 128 in 12 10
+//   37 x 50304 x 768: 64 x 128 15, 128 x 128 17, 256 x 256 23
+//   12608 x 768 x 8192: 256 x 256 187, 128 x 128 208, 64 x 128 212
+struct Plan {
+  int tile, splits;
+};
+
+Plan plan_of(int64_t M, int64_t N, int stages, int most_splits) {
+  Plan best{0, 1};
+  double us = 1e30;
+  for (int t = 0; t < 3; ++t)
+    for (int s = 1; s <= most_splits && s <= stages; s += s < 4 ? 1 : s < 8 ? 2 : 4) {
+      const int splits = ceil_div(stages, ceil_div(stages, s));  // none is empty
+      const double here = time_of(kTiles[t], M, N, stages, splits);
+      if (here < us) us = here, best = {t, splits};
+    }
+  return best;
 }
 
 }  // namespace
 
-int bf_gemm_most_splits(int64_t M, int64_t N) {
-  const int64_t t = ceil_div<int64_t>(M, 64) * ceil_div<int64_t>(N, 128);
-  return tile_of(M, N) != 64 || t >= 128 ? 1 : (int)std::min<int64_t>(256 / t, 32);
-}
-
-int bf_gemm_splits(int64_t M, int64_t N, int stages) {
-  const int s = std::min(bf_gemm_most_splits(M, N), stages / 16);
-  if (s < 2) return 1;
-  return ceil_div(stages, ceil_div(stages, s));  // none is empty
-}
+int bf_gemm_splits(int64_t M, int64_t N, int stages) { return plan_of(M, N, stages, kBfMostSplits).splits; }
 
 hipError_t launch_bf_gemm(const BfGemmParams& in, BfOut out, hipStream_t st) {
   BfGemmParams g = in;
   const int stages = g.runs * g.run_stages;
-  g.split_stages = (int)ceil_div<int64_t>(stages, g.splits);
-  const int tile = g.splits > 1 ? 64 : tile_of(g.M, g.N);
-  if (tile == 256) launch_tiles<2, 4, 4, 2, 32>(g, out, st);
-  else if (tile == 128) launch_tiles<2, 2, 2, 2, 32>(g, out, st);
+  const int tile = plan_of(g.M, g.N, stages, g.splits > 1 ? kBfMostSplits : 1).tile;
+  g.split_stages = ceil_div(stages, g.splits);
+  if (tile == 0) launch_tiles<2, 4, 4, 2, 32>(g, out, st);
+  else if (tile == 1) launch_tiles<2, 2, 2, 2, 32>(g, out, st);
   else launch_tiles<2, 2, 1, 3, 16>(g, out, st);
   return hipGetLastError();
 }

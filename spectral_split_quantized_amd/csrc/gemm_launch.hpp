@@ -35,10 +35,10 @@ struct BfGemmParams;
 enum BfOut : int;
 
 // A B^T of bf16 planes (bf16_gemm.hpp): kBfStats and kBfProb with K along the
-// rows, the others with B transposed, and A where rows_a is set.  splits > 1 (as bf_gemm_splits gives
-// it, at most bf_gemm_most_splits; kBfF32 only) writes one C for each part of
-// K; split_stages is set here.
-int bf_gemm_most_splits(int64_t M, int64_t N);
+// rows, the others with B transposed, and A where rows_a is set.  splits > 1
+// (as bf_gemm_splits gives it for the product's stages; kBfF32 only) writes
+// one C for each part of K; split_stages is set here.
+constexpr int kBfMostSplits = 32;
 int bf_gemm_splits(int64_t M, int64_t N, int stages);
 hipError_t launch_bf_gemm(const BfGemmParams& g, BfOut out, hipStream_t st);
 

@@ -64,8 +64,13 @@ __global__ __launch_bounds__(256) void planes_kernel(PlanesParams p) {
   }
 }
 
-// loss and log-sum-exp of each token from its statistics: four waves of a
-// workgroup share 64 tokens, each wave a quarter of the blocks in order.
+// Loss and log-sum-exp of each token from its statistics, 16 tokens a
+// workgroup: 64 threads share a token, each takes every 64th block in order,
+// and their results are joined in order.  The last workgroup to end (a counter
+// in the workspace, zeroed by the product's launch before) adds the losses:
+// total[0] their sum, or their mean over the tokens that have one (0 where
+// none has), total[1] the number of those tokens, in binary64 and in an order
+// that does not depend on which workgroup it is.
 struct LossJoinParams {
   const float2* stat;  // [blocks][tokens]
   int64_t blocks, tokens;
@@ -73,14 +78,18 @@ struct LossJoinParams {
   const void* targets;
   int targets64;
   int64_t vocab, ignore;
-  float *losses, *lse;  // losses may be null
+  float *losses, *lse;
+  int mean;
+  float* total;        // or null
+  uint32_t* done;
   int* status;
 };
 
-__global__ __launch_bounds__(256) void loss_join_kernel(LossJoinParams p) {
-  __shared__ float2 red[4][64];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 64 + lane;
+__global__ __launch_bounds__(1024) void loss_join_kernel(LossJoinParams p) {
+  __shared__ float2 red[64][16];
+  __shared__ bool last;
+  const int token = threadIdx.x & 15, part = threadIdx.x >> 4;
+  const int64_t row = (int64_t)blockIdx.x * 16 + token;
   float m = -__builtin_inff(), s = 0.0f;
   auto join = [&](float m2, float s2) {
     const float top = fmaxf(m, m2), at = top == -__builtin_inff() ? 0.0f : top;
@@ -89,53 +98,62 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoinParams p) {
     m = top;
   };
   if (row < p.tokens) {
-    const int64_t per = (p.blocks + 3) / 4, end = min(p.blocks, (wave + 1) * per);
-    int64_t b = wave * per;
-    for (; b + 8 <= end; b += 8) {
+    int64_t b = part;
+    for (; b + 448 < p.blocks; b += 512) {  // eight loads in flight
       float2 v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = p.stat[(b + k) * p.tokens + row];
+      for (int k = 0; k < 8; ++k) v[k] = p.stat[(b + 64 * k) * p.tokens + row];
 #pragma unroll
       for (int k = 0; k < 8; ++k) join(v[k].x, v[k].y);
     }
-    for (; b < end; ++b) {
+    for (; b < p.blocks; b += 64) {
       const float2 v = p.stat[b * p.tokens + row];
       join(v.x, v.y);
     }
   }
-  red[wave][lane] = make_float2(m, s);
+  red[part][token] = make_float2(m, s);
   __syncthreads();
-  if (wave || row >= p.tokens) return;
-  m = red[0][lane].x, s = red[0][lane].y;
-  for (int k = 1; k < 4; ++k) join(red[k][lane].x, red[k][lane].y);
-  const float lse = m + logf(s);
-  p.lse[row] = lse;
-  const int64_t t = p.targets64 ? ((const int64_t*)p.targets)[row] : (int64_t)((const int32_t*)p.targets)[row];
-  const bool in = t >= 0 && t < p.vocab;
-  if (t != p.ignore && !in) atomicOr(p.status, kStatusToken);
-  if (p.losses) p.losses[row] = t != p.ignore && in ? lse - p.target_logit[row] : 0.0f;
-}
-
-// total[0]: the sum of the losses, or their mean over the tokens that have one
-// (0 where none has); total[1]: the number of those tokens.  Summed in
-// binary64 in a fixed order.
-__global__ __launch_bounds__(1024) void loss_total_kernel(const float* losses, const void* targets, int targets64, int64_t vocab,
-                                                          int64_t ignore, int64_t tokens, int mean, float* total) {
-  __shared__ double red[2][16];
-  double s = 0.0, n = 0.0;
-  for (int64_t i = threadIdx.x; i < tokens; i += 1024) {
-    s += (double)losses[i];
-    n += target_of(targets, targets64, ignore, vocab, i) >= 0 ? 1.0 : 0.0;
+#pragma unroll
+  for (int half = 32; half > 0; half >>= 1) {
+    if (part < half) {
+      const float2 o = red[part + half][token];
+      join(o.x, o.y);
+      red[part][token] = make_float2(m, s);
+    }
+    __syncthreads();
   }
-  s = wave_sum_d(s);
+  if (part == 0 && row < p.tokens) {
+    const float lse = m + logf(s);
+    p.lse[row] = lse;
+    const int64_t t = target_of(p.targets, p.targets64, p.ignore, p.vocab, row);
+    const int64_t given = p.targets64 ? ((const int64_t*)p.targets)[row] : (int64_t)((const int32_t*)p.targets)[row];
+    if (t < 0 && given != p.ignore) atomicOr(p.status, kStatusToken);
+    __hip_atomic_store(p.losses + row, t >= 0 ? lse - p.target_logit[row] : 0.0f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (!p.total) return;
+  // The losses are stored past this XCD's L2 and have arrived before the count
+  // goes up (a fence would write back all of the L2, which holds nothing else
+  // that the last workgroup reads).
+  __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (15 << 8));
+  __syncthreads();
+  if (threadIdx.x == 0) last = __hip_atomic_fetch_add(p.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  double sum = 0.0, n = 0.0;
+  for (int64_t i = threadIdx.x; i < p.tokens; i += 1024) {
+    sum += (double)__hip_atomic_load(p.losses + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    n += target_of(p.targets, p.targets64, p.ignore, p.vocab, i) >= 0 ? 1.0 : 0.0;
+  }
+  sum = wave_sum_d(sum);
   n = wave_sum_d(n);
-  if ((threadIdx.x & 63) == 0) red[0][threadIdx.x >> 6] = s, red[1][threadIdx.x >> 6] = n;
+  __shared__ double sums[2][16];
+  if ((threadIdx.x & 63) == 0) sums[0][threadIdx.x >> 6] = sum, sums[1][threadIdx.x >> 6] = n;
   __syncthreads();
   if (threadIdx.x) return;
-  s = n = 0.0;
-  for (int k = 0; k < 16; ++k) s += red[0][k], n += red[1][k];
-  total[0] = (float)(mean ? (n > 0.0 ? s / n : 0.0) : s);
-  total[1] = (float)n;
+  sum = n = 0.0;
+  for (int k = 0; k < 16; ++k) sum += sums[0][k], n += sums[1][k];
+  p.total[0] = (float)(p.mean ? (n > 0.0 ? sum / n : 0.0) : sum);
+  p.total[1] = (float)n;
 }
 
 // C (+)= the sum of the splits' C in order, binary32 or rounded to bf16

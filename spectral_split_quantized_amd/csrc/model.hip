@@ -56,15 +56,17 @@ metis_status ws_check(const char* what, const void* ws, size_t bytes, size_t nee
 
 // ------------------------------------------------------------- layer norm --
 
-// workgroups of the backward pass, each with a row of partial sums
-constexpr int64_t kNormGroups = 512;
+constexpr int64_t kNormFwdGroups = 1280;
 
-int64_t norm_threads(int64_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024; }
+int64_t norm_threads(int64_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 512; }
 
+// Workgroups of 256 threads that are resident at once: 16 values a thread
+// leave room for three on a CU in the backward pass, 32 for two.
 int64_t norm_groups(int64_t rows, int64_t cols) {
   if (cols > kNormCols) return std::min<int64_t>(ceil_div<int64_t>(rows, kNormSumRows), INT32_MAX);
-  const int64_t per = std::max<int64_t>(1, 256 / norm_threads(cols));
-  return std::min<int64_t>(ceil_div<int64_t>(rows, per), kNormGroups);
+  const int64_t T = norm_threads(cols), per = std::max<int64_t>(1, 256 / T);
+  const int64_t most = cols <= 16 * T ? 768 : T == 512 ? 256 : 512;
+  return std::min<int64_t>(ceil_div<int64_t>(rows, per), most);
 }
 
 template <int VEC, int T, int NV>
@@ -78,8 +80,7 @@ template <int VEC>
 void launch_norm_rows(const NormParams& p, bool bwd, hipStream_t st) {
   constexpr int K = 8 / VEC;
   const int64_t T = norm_threads(p.cols), per = std::max<int64_t>(1, 256 / T);
-  const int64_t most = bwd ? kNormGroups : T == 1024 ? 512 : 2048;
-  const unsigned grid = grid_for(p.rows, per, most);
+  const unsigned grid = bwd ? (unsigned)norm_groups(p.rows, p.cols) : grid_for(p.rows, per, T == 512 ? 512 : kNormFwdGroups);
   if (T == 64) {
     if (p.cols <= 512) launch_norm<VEC, 64, 1 * K>(p, bwd, grid, st);
     else if (p.cols <= 1024) launch_norm<VEC, 64, 2 * K>(p, bwd, grid, st);
@@ -88,7 +89,7 @@ void launch_norm_rows(const NormParams& p, bool bwd, hipStream_t st) {
     if (p.cols <= 4096) launch_norm<VEC, 256, 2 * K>(p, bwd, grid, st);
     else launch_norm<VEC, 256, 4 * K>(p, bwd, grid, st);
   } else {
-    launch_norm<VEC, 1024, 2 * K>(p, bwd, grid, st);
+    launch_norm<VEC, 512, 4 * K>(p, bwd, grid, st);
   }
 }
 
@@ -139,13 +140,15 @@ bool operand_as_is(const void* p, int32_t dt, int64_t ld, int64_t rows, int64_t 
 
 int64_t pad64(int64_t n) { return round_up64(n, 64); }
 
-// Words of one piece: about 2^27 probabilities, so that a piece's products
-// fill the chip many times over and its buffers stay at 256 MB each; the
-// pieces of a vocabulary are of equal size up to 256.
-int64_t loss_piece(int64_t tokens, int64_t vocab) {
-  const int64_t most = std::max<int64_t>(((int64_t)1 << 27) / std::max<int64_t>(tokens, 1), 4096);
-  const int64_t pieces = ceil_div<int64_t>(vocab, most);
-  return round_up64(ceil_div<int64_t>(vocab, pieces), 256);
+// Words of one piece: at most about 2^28 probabilities (512 MB), and where
+// they allow it a number whose dw = P^T x fills whole rounds of the chip's 256
+// CUs with tiles of 256 x 256 (50257 words, 768 features, 8192 tokens: dw in
+// three pieces of 21760 and the rest, not in two of 25152, which take two
+// rounds of tiles each).
+int64_t loss_piece(int64_t tokens, int64_t vocab, int64_t cols) {
+  const int64_t most = std::max<int64_t>(((int64_t)1 << 28) / std::max<int64_t>(tokens, 1), 4096);
+  const int64_t round = std::max<int64_t>(256 / ceil_div<int64_t>(cols, 256), 1) * 256;
+  return round <= most ? most / round * round : most / 256 * 256;
 }
 
 struct LossPlan {
@@ -163,7 +166,7 @@ LossPlan loss_plan(const metis_loss& l) {
   p.xp = l.x_dtype == METIS_F32 ? 2 : 1;
   p.wp = l.w_dtype == METIS_F32 ? 2 : 1;
   p.pair = p.xp == 2 || p.wp == 2;
-  p.piece = loss_piece(p.N, p.V);
+  p.piece = loss_piece(p.N, p.V, p.D);
   return p;
 }
 
@@ -171,9 +174,16 @@ struct LossWs {
   uint16_t *x, *w;             // planes of x, of a piece of w (where not as they are)
   float2* stat;                // forward
   float *target, *losses;
+  uint32_t* done;              // counter of the join
   uint16_t* p;                 // backward: P of a piece
   float *dx, *part;            // dx summed over the pieces, parts of K
 };
+
+// parts of K of dx = P w over so many words
+int dx_splits(const LossPlan& p, int64_t words) {
+  const int runs = p.xp == 1 ? 1 : 1 + (p.wp == 2) + p.pair;  // as product() counts them
+  return words ? bf_gemm_splits(p.N, p.D, runs * (int)(pad64(words) / 64)) : 1;
+}
 
 LossWs carve_loss(Carver& cv, const metis_loss& l, const LossPlan& p, bool backward) {
   LossWs w{};
@@ -183,12 +193,14 @@ LossWs carve_loss(Carver& cv, const metis_loss& l, const LossPlan& p, bool backw
     w.stat = cv.take<float2>((size_t)ceil_div<int64_t>(p.V, 64) * p.N);
     w.target = cv.take<float>(p.N);
     w.losses = cv.take<float>(p.N);
+    w.done = cv.take<uint32_t>(1);
     return w;
   }
   const int64_t words = pad64(std::min(p.piece, p.V));
   w.p = cv.take<uint16_t>((size_t)(p.pair ? 2 : 1) * p.Np * words);
   w.dx = cv.take<float>((size_t)p.N * p.D);
-  const int s = bf_gemm_most_splits(p.N, p.D);
+  int s = dx_splits(p, words);
+  if (p.V > p.piece) s = std::max(s, dx_splits(p, pad64(p.V % p.piece)));
   if (s > 1) w.part = cv.take<float>((size_t)s * p.N * p.D);
   return w;
 }
@@ -484,17 +496,15 @@ metis_status metis_cross_entropy_fwd(const metis_loss* l, float* losses, float* 
       BfGemmParams g = product(x, p.N, v, n, p.D, true);
       set_targets(g, *l, v0);
       g.stat = w.stat, g.target_logit = w.target;
+      g.done = w.done;
       TRY(run_product(g, kBfStats, st));
     }
-    if (!losses) losses = w.losses;
-    LossJoinParams j{w.stat, ceil_div<int64_t>(p.V, 64), p.N, w.target, l->targets, t64, l->vocab, l->ignore_index, losses, lse,
-                     device_status()};
-    hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)ceil_div<int64_t>(p.N, 64)), dim3(256), 0, st, j);
+    LossJoinParams j{w.stat, ceil_div<int64_t>(p.V, 64), p.N, w.target, l->targets, t64, l->vocab, l->ignore_index,
+                     losses ? losses : w.losses, lse, mean, total, w.done, device_status()};
+    hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)ceil_div<int64_t>(p.N, 16)), dim3(1024), 0, st, j);
     LAUNCH_CHECK();
-  }
-  if (total) {
-    hipLaunchKernelGGL(loss_total_kernel, dim3(1), dim3(1024), 0, st, (const float*)losses, l->targets, t64, l->vocab,
-                       l->ignore_index, l->tokens, mean, total);
+  } else if (total) {
+    hipLaunchKernelGGL(zero_rows_kernel, dim3(1), dim3(256), 0, st, (void*)total, 0, (int64_t)1, (int64_t)2, (int64_t)2);
     LAUNCH_CHECK();
   }
   return METIS_OK;
@@ -541,7 +551,7 @@ metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, cons
     if (dX) {
       g = product(pr, p.N, v, p.D, n, dx_f32);
       g.rows_b = n;
-      const int splits = bf_gemm_splits(p.N, p.D, g.runs * g.run_stages);
+      const int splits = dx_splits(p, n);
       // one piece: straight to dX; else summed in binary32, in dX itself where it is binary32
       void* const sum = dx_f32 ? dX : (void*)w.dx;
       const int64_t ld = dx_f32 ? lddx : p.D;

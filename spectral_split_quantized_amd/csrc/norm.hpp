@@ -10,7 +10,7 @@
 // to fewer bits, once.
 //
 // T threads share a row and hold it in registers, so that x is read once: a
-// wave up to 2048 columns, workgroups of 256 and 1024 threads up to 8192 and
+// wave up to 2048 columns, workgroups of 256 and 512 threads up to 8192 and
 // 16384.  Each thread keeps its columns of w and b (and of the sums dw, db)
 // for all rows that it takes.  The sums of dw and db end in a row of partial
 // sums for each workgroup, added by a second kernel in the order of the
@@ -80,24 +80,85 @@ struct NormCols {
   }
 };
 
+// A row's values of one thread as they lie in memory, so that the next row's
+// loads are in flight while a row is worked on: two 16-byte words a group of
+// eight (bf16 fills the first), or a value a group of one.
+template <int VEC, int T, int NV>
+struct NormRaw {
+  uint4 q[VEC == 8 ? 2 * NV : 1];
+  uint32_t w[VEC == 8 ? 1 : NV];
+
+  __device__ __forceinline__ void load(const void* p, int bf16, int64_t row, int cols, int t) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = NormCols<VEC, T, NV>::first(t, k), n = cols - c;
+      if constexpr (VEC == 1) {
+        w[k] = n <= 0 ? 0 : bf16 ? ((const uint16_t*)p)[row + c] : ((const uint32_t*)p)[row + c];
+      } else if (bf16) {
+        const uint16_t* const at = (const uint16_t*)p + row + c;
+        if (n >= 8) {
+          q[2 * k] = *(const uint4*)at;
+        } else {
+          auto two = [&](int i) { return (i < n ? at[i] : 0) | (uint32_t)(i + 1 < n ? at[i + 1] : 0) << 16; };
+          q[2 * k] = make_uint4(two(0), two(2), two(4), two(6));
+        }
+      } else {
+        const uint32_t* const at = (const uint32_t*)p + row + c;
+        if (n >= 8) {
+          q[2 * k] = *(const uint4*)at;
+          q[2 * k + 1] = *((const uint4*)at + 1);
+        } else {
+          auto one = [&](int i) { return i < n ? at[i] : 0; };
+          q[2 * k] = make_uint4(one(0), one(1), one(2), one(3));
+          q[2 * k + 1] = make_uint4(one(4), one(5), one(6), one(7));
+        }
+      }
+    }
+  }
+
+  // the values, zeros behind the row
+  __device__ __forceinline__ void get(int bf16, float* v) const {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if constexpr (VEC == 1) {
+        v[k] = __uint_as_float(bf16 ? w[k] << 16 : w[k]);
+      } else {
+        const uint4 a = q[2 * k], b = q[2 * k + 1];
+        const uint32_t lo[4] = {a.x, a.y, a.z, a.w}, hi[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[8 * k + e] = bf16 ? unpack_bf16(lo[e >> 1], e) : __uint_as_float(e < 4 ? lo[e & 3] : hi[e & 3]);
+      }
+    }
+  }
+};
+
+// The next row's loads go ahead where a thread has registers for them.
+constexpr bool norm_ahead(int VEC, int NV) { return VEC * NV <= 16; }
+
 // threads of a workgroup
 constexpr int norm_block(int T) { return T < 256 ? 256 : T; }
 
 template <int VEC, int T, int NV>
 __global__ __launch_bounds__(norm_block(T)) void norm_fwd_kernel(NormParams p) {
   using C = NormCols<VEC, T, NV>;
-  constexpr int E = C::E;
+  constexpr int E = C::E, G = norm_block(T) / T;  // G rows at a time
   __shared__ float red[2][T / 64];
   const int t = threadIdx.x & (T - 1);
+  const int64_t step = (int64_t)gridDim.x * G;
+  int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / T;
+  NormRaw<VEC, T, NV> raw;
+  constexpr bool AHEAD = norm_ahead(VEC, NV);
+  if (AHEAD && row < p.rows) raw.load(p.x, p.x_bf16, row * p.ldx, p.cols, t);
   float w[E], b[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) w[e] = 1.0f, b[e] = 0.0f;
   if (p.w) C::load(p.w, p.w_bf16, 0, p.cols, t, 0.0f, w);
   if (p.b) C::load(p.b, p.w_bf16, 0, p.cols, t, 0.0f, b);
-  const int64_t step = (int64_t)gridDim.x * (norm_block(T) / T);
-  for (int64_t row = (int64_t)blockIdx.x * (norm_block(T) / T) + threadIdx.x / T; row < p.rows; row += step) {
+  for (; row < p.rows; row += step) {
     float x[E], s = 0.0f;
-    C::load(p.x, p.x_bf16, row * p.ldx, p.cols, t, 0.0f, x);
+    if (!AHEAD) raw.load(p.x, p.x_bf16, row * p.ldx, p.cols, t);
+    raw.get(p.x_bf16, x);
+    if (AHEAD && row + step < p.rows) raw.load(p.x, p.x_bf16, (row + step) * p.ldx, p.cols, t);
 #pragma unroll
     for (int e = 0; e < E; ++e) s += x[e];
     const float mu = row_sum<T>(s, red[0]) * p.inv;
@@ -121,22 +182,36 @@ __global__ __launch_bounds__(norm_block(T)) void norm_fwd_kernel(NormParams p) {
 template <int VEC, int T, int NV>
 __global__ __launch_bounds__(norm_block(T)) void norm_bwd_kernel(NormParams p) {
   using C = NormCols<VEC, T, NV>;
-  constexpr int E = C::E, G = norm_block(T) / T;  // rows at a time
-  __shared__ float red[2][T / 64];
+  constexpr int E = C::E, G = norm_block(T) / T;  // G rows at a time
+  __shared__ float red[2][2][T / 64];
   const int t = threadIdx.x & (T - 1);
+  const int64_t step = (int64_t)gridDim.x * G;
+  int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / T;
+  NormRaw<VEC, T, NV> xr, gr;
+  float mu = 0.0f, r = 0.0f;
+  auto fetch = [&](int64_t i) {
+    xr.load(p.x, p.x_bf16, i * p.ldx, p.cols, t);
+    gr.load(p.dy, p.y_bf16, i * p.lddy, p.cols, t);
+    mu = p.mean[i];
+    r = p.rstd[i];
+  };
+  constexpr bool AHEAD = norm_ahead(VEC, NV);
+  if (AHEAD && row < p.rows) fetch(row);
   float w[E], dw[E], db[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) w[e] = 1.0f, dw[e] = db[e] = 0.0f;
   if (p.w) C::load(p.w, p.w_bf16, 0, p.cols, t, 0.0f, w);
-  const int64_t step = (int64_t)gridDim.x * G;
-  for (int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / T; row < p.rows; row += step) {
+  int odd = 0;
+  for (; row < p.rows; row += step, odd ^= 1) {
     float h[E], g[E], s = 0.0f, q = 0.0f;
-    const float mu = p.mean[row], r = p.rstd[row];
-    C::load(p.x, p.x_bf16, row * p.ldx, p.cols, t, mu, h);  // 0 behind the row
-    C::load(p.dy, p.y_bf16, row * p.lddy, p.cols, t, 0.0f, g);
+    if (!AHEAD) fetch(row);
+    const float m0 = mu, r0 = r;
+    xr.get(p.x_bf16, h);
+    gr.get(p.y_bf16, g);
+    if (AHEAD && row + step < p.rows) fetch(row + step);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      h[e] = (h[e] - mu) * r;
+    for (int e = 0; e < E; ++e) {  // (g is 0 behind the row)
+      h[e] = (h[e] - m0) * r0;
       dw[e] += g[e] * h[e];
       db[e] += g[e];
       g[e] *= w[e];
@@ -144,10 +219,20 @@ __global__ __launch_bounds__(norm_block(T)) void norm_bwd_kernel(NormParams p) {
       q += g[e] * h[e];
     }
     if (!p.dx) continue;
-    s = row_sum<T>(s, red[0]) * p.inv;
-    q = row_sum<T>(q, red[1]) * p.inv;
+    // both sums with one barrier; the arrays alternate
+    s = wave_sum(s);
+    q = wave_sum(q);
+    if constexpr (T > 64) {
+      if ((threadIdx.x & 63) == 0) red[odd][0][threadIdx.x >> 6] = s, red[odd][1][threadIdx.x >> 6] = q;
+      __syncthreads();
+      s = q = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) g[e] = r * (g[e] - s - h[e] * q);
+      for (int k = 0; k < T / 64; ++k) s += red[odd][0][k], q += red[odd][1][k];
+    }
+    s *= p.inv;
+    q *= p.inv;
+#pragma unroll
+    for (int e = 0; e < E; ++e) g[e] = r0 * (g[e] - s - h[e] * q);
     C::store(p.dx, p.x_bf16, row * p.lddx, p.cols, t, g);
   }
   if (!p.part) return;

@@ -325,11 +325,11 @@ def test_cross_entropy_matches_the_oracle(tokens, vocab, cols, xt, wt, bits):
 def test_cross_entropy_in_several_pieces():
     say("cross entropy over pieces of the vocabulary")
     g = torch.Generator(device="cuda").manual_seed(4)
-    n, v, d = 1024, 140000, 64  # two pieces
+    n, v, d = 4096, 140001, 64  # three pieces of 65536 words and less
     x = torch.randn(n, d, generator=g, device="cuda").to(BF)
     w = (torch.randn(v, d, generator=g, device="cuda") * 0.3).to(BF)
     t = torch.randint(0, v, (n,), generator=g, device="cuda")
-    t[0], t[1], t[2] = v - 1, 70143, 70144
+    t[0], t[1], t[2] = v - 1, 65535, 65536
     losses, lse, total = metis.cross_entropy(x, w, t)
     z = x.double() @ w.double().T
     rlse = torch.logsumexp(z, 1)
