@@ -109,13 +109,25 @@ __global__ __launch_bounds__(kEmbedTile) void embed_scatter_kernel(EmbedSortPara
   __shared__ uint32_t base[kEmbedDigits], sums[kEmbedDigits / 64];
   __shared__ uint16_t count[W][kEmbedDigits];  // at most 64 each
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t begin = blockIdx.x * p.tile, end = min(begin + p.tile, p.tokens);
+  uint32_t key = 0, from = 0;
+  auto fetch = [&](int64_t i) {
+    key = embed_key(p, i);
+    from = p.first ? (uint32_t)i : p.pos[i];
+  };
+  if (begin + threadIdx.x < end) fetch(begin + threadIdx.x);
   // the digit's tokens of earlier tiles, and all of smaller digits
   uint32_t before = 0, all = 0;
   if (threadIdx.x < kEmbedDigits) {
-    for (int k = 0; k < p.tiles; ++k) {
-      const uint32_t c = p.hist[(int64_t)k * kEmbedDigits + threadIdx.x];
-      before += k < (int)blockIdx.x ? c : 0;
-      all += c;
+    for (int k0 = 0; k0 < p.tiles; k0 += 16) {  // 16 loads in flight
+      uint32_t c[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) c[k] = k0 + k < p.tiles ? p.hist[(int64_t)(k0 + k) * kEmbedDigits + threadIdx.x] : 0;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        before += k0 + k < (int)blockIdx.x ? c[k] : 0;
+        all += c[k];
+      }
     }
     uint32_t up = all;  // inclusive sums within the wave
 #pragma unroll
@@ -131,18 +143,13 @@ __global__ __launch_bounds__(kEmbedTile) void embed_scatter_kernel(EmbedSortPara
     for (int k = 0; k < wave; ++k) before += sums[k];
     base[threadIdx.x] = before;
   }
-  const int64_t begin = blockIdx.x * p.tile, end = min(begin + p.tile, p.tokens);
   for (int64_t i0 = begin; i0 < end; i0 += kEmbedTile) {
     for (int d = threadIdx.x; d < W * kEmbedDigits / 2; d += kEmbedTile) ((uint32_t*)count)[d] = 0;
     __syncthreads();
     const int64_t i = i0 + threadIdx.x;
     const bool have = i < end;
-    uint32_t key = 0, from = 0, digit = 0;
-    if (have) {
-      key = embed_key(p, i);
-      from = p.first ? (uint32_t)i : p.pos[i];
-      digit = key >> p.shift & (kEmbedDigits - 1);
-    }
+    if (i0 > begin && have) fetch(i);
+    const uint32_t digit = have ? key >> p.shift & (kEmbedDigits - 1) : 0;
     uint64_t same = __ballot(have);
 #pragma unroll
     for (int b = 0; b < kEmbedBits; ++b) {
@@ -155,7 +162,8 @@ __global__ __launch_bounds__(kEmbedTile) void embed_scatter_kernel(EmbedSortPara
     uint32_t to = 0;
     if (have) {
       to = base[digit] + rank;
-      for (int k = 0; k < wave; ++k) to += count[k][digit];
+#pragma unroll
+      for (int k = 0; k < W; ++k) to += k < wave ? count[k][digit] : 0;
       p.key_to[to] = key;
       p.pos_to[to] = from;
     }
@@ -273,26 +281,35 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedSumParams p) {
 }
 
 // Tokens whose rows lie in more than one run: the workgroup of the run where
-// one begins adds its partial sums in order.  A column a thread.
+// one begins adds its partial sums in order.  V columns a thread (4 where rows
+// of partial sums are 16-byte aligned); a token's runs are counted 64 at a time
+// by the lanes of a wave, and 16 partial sums are in flight.  (16384 tokens of
+// 4096 columns: 23 us with one column a thread, whose many workgroups mostly
+// look at their run and end; a workgroup that looks at 16 runs, 34.)
+template <int V>
 __global__ __launch_bounds__(256) void embed_join_kernel(EmbedSumParams p) {
-  const int64_t run = blockIdx.x, last = run * kEmbedRun + kEmbedRun - 1;  // the run's last sorted token
-  if (last + 1 >= p.tokens) return;
-  const uint32_t here = p.key[last];
-  if (here >= p.vocab || p.key[last + 1] != here) return;
-  if (run > 0 && p.key[run * kEmbedRun - 1] == here) return;  // begins earlier
-  for (int64_t c = blockIdx.y * 256 + threadIdx.x; c < p.cols; c += (int64_t)gridDim.y * 256) {
-    float s = p.part[(run * 2 + 1) * p.cols + c];
-    for (int64_t r = run + 1; r < p.runs && p.key[r * kEmbedRun] == here; r += 8) {
-      float v[8];
+  const int64_t run = blockIdx.x, next = (run + 1) * kEmbedRun;
+  if (next >= p.tokens) return;
+  const uint32_t here = p.key[next - 1], behind = p.key[next], before = run ? p.key[run * kEmbedRun - 1] : ~0u;
+  if (here >= p.vocab || behind != here || before == here) return;  // none begins here
+  int64_t end = run + 1;  // the first run that does not begin with the token
+  for (uint64_t same = ~0ull; same == ~0ull;) {
+    const int64_t r = end + (threadIdx.x & 63);
+    same = __ballot(r < p.runs && p.key[r * kEmbedRun] == here);
+    end += same == ~0ull ? 64 : __builtin_ctzll(~same);
+  }
+  typedef float vec_t __attribute__((ext_vector_type(V)));
+  for (int64_t c = (blockIdx.y * 256 + threadIdx.x) * V; c < p.cols; c += (int64_t)gridDim.y * 256 * V) {
+    vec_t s = *(const vec_t*)(p.part + (run * 2 + 1) * p.cols + c);
+    for (int64_t r = run + 1; r < end; r += 16) {
+      vec_t v[16];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const bool in = r + k < p.runs && p.key[(r + k) * kEmbedRun] == here;
-        v[k] = in ? p.part[(r + k) * 2 * p.cols + c] : 0.0f;
-      }
+      for (int k = 0; k < 16; ++k) v[k] = r + k < end ? *(const vec_t*)(p.part + (r + k) * 2 * p.cols + c) : vec_t{};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s += v[k];
+      for (int k = 0; k < 16; ++k) s += v[k];
     }
-    store1(p.dw, p.dw_bf16, here * p.lddw + c, s * p.scale);
+#pragma unroll
+    for (int e = 0; e < V; ++e) store1(p.dw, p.dw_bf16, here * p.lddw + c + e, s[e] * p.scale);
   }
 }
 

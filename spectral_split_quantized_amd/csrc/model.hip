@@ -455,8 +455,10 @@ metis_status metis_embedding_bwd(const void* dY, int32_t y_dtype, int64_t tokens
     hipLaunchKernelGGL((embed_sum_kernel<1>), grid, dim3(256), 0, st, s);
   LAUNCH_CHECK();
   if (s.runs > 1) {
-    const dim3 join((unsigned)s.runs, (unsigned)std::min<int64_t>(ceil_div<int64_t>(cols, 256), 64));
-    hipLaunchKernelGGL(embed_join_kernel, join, dim3(256), 0, st, s);
+    const int V = cols % 4 == 0 ? 4 : 1;
+    const dim3 join((unsigned)s.runs, (unsigned)std::min<int64_t>(ceil_div<int64_t>(cols, 256 * V), 64));
+    if (V == 4) hipLaunchKernelGGL((embed_join_kernel<4>), join, dim3(256), 0, st, s);
+    else hipLaunchKernelGGL((embed_join_kernel<1>), join, dim3(256), 0, st, s);
     LAUNCH_CHECK();
   }
   return METIS_OK;
