@@ -54,7 +54,7 @@ struct BfGemmParams {
 };
 
 typedef __bf16 bf16x8v_t __attribute__((ext_vector_type(8)));
-typedef float f32x16v_t __attribute__((ext_vector_type(16)));
+typedef float f32x4v_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4v_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2E = 1.4426950408889634f;
@@ -87,30 +87,37 @@ __device__ __forceinline__ bf16x8v_t read_transposed(uint32_t at, uint32_t row4)
   return __builtin_bit_cast(bf16x8v_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// WM x WN waves of TM x 2 tiles of 32 x 32, one workgroup for many tiles of C,
-// built as the int8 product (the instruction's lane takes the same 16
-// K-consecutive bytes): K-stages of 128 bytes (64 values) travel global -> LDS
-// by DMA into a ring of NS slots; a row's 16-byte chunk c lies at R * 128 +
-// (c ^ (R / 2 % 8)) * 16, so that lanes that read together hit all banks
-// once; each sub-step reads the next one's fragments under its matrix
-// instructions, and the loads run NS stages ahead of the products, across
-// tiles.  B is the instruction's first operand: a lane ends up with row
-// lane % 32 of a tile of C and columns 8 g + 4 (lane / 32) + v.
+// WM x WN waves of TM x 4 tiles of 16 x 16, one workgroup for many tiles of C.
+// K-stages of 128 bytes (64 values) travel global -> LDS by DMA into a ring of
+// NS slots; a row's 16-byte chunk c lies at R * 128 + (c ^ (R / 2 % 8)) * 16, so
+// that the 16 lanes that read together hit all banks once.  The matrix
+// instruction is 16 x 16 x 32 (lane l takes 8 K-consecutive values of row
+// l % 16 at 8 (l / 16)): the card's power holds random operands to 1.83 PFLOP/s
+// with it and to 1.30 with 32 x 32 x 16, in loops of nothing else.  B is its
+// first operand: a lane ends up with row lane % 16 of a tile of C and columns
+// 4 (lane / 16) + v.
+//
+// A stage is two sub-steps of 32 values; each reads the next one's fragments
+// under its matrix instructions.  In the second one every wave holds the
+// stage's fragments, so its slot takes the stage NS ahead; the loads run NS
+// stages ahead of the products, across tiles.
 //
 // TA, TB: that operand is transposed.  Its stage is 64 rows of K with the
 // tile's columns, and the fragments are read by the transposing LDS read, two
-// for eight values of K.  32 lanes read 64 bytes of each of four rows at a
-// time; chunk c of row k lies at c ^ (4 (k % 4)) (rows of 128 bytes:
-// c ^ (4 (k / 2 % 2))), which puts the four rows on different banks.
+// for eight values of K.  32 lanes read 32 bytes of each of eight rows at a
+// time, k .. k + 3 and k + 8 .. k + 11; chunk c of row k lies at
+// c ^ (4 (k % 4) + 2 (k / 8 % 2)) (rows of 128 bytes: c ^ (4 (k / 2 % 2) + 2 (k /
+// 8 % 2))), which puts them on different banks.
 //
 // Rows past M / N repeat the last row (never stored).
 template <int WM, int WN, int TM, int NS, int ER, BfOut OUT, bool TA, bool TB>
 __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p) {
-  constexpr int TN = 2;
-  constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
+  constexpr int TN = 4;
+  constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
   constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128;
   constexpr int PA = BM / 8 / NW, PB = BN / 8 / NW;
   static_assert(PA * 8 * NW == BM && PB * 8 * NW == BN && (NS - 1) * (PA + PB) < 64, "DMA split");
+  static_assert(ER % 16 == 0 && (TM * 16) % ER == 0, "epilogue rows");
   __shared__ __attribute__((aligned(16))) uint8_t ring[NS * STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t ep[NW * ER * 128];
 
@@ -158,7 +165,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
   auto offset = [&](bool t, int B, int d, int64_t pitch, int last) {
     const int r = row_of(t, B, d);
     if (!t) return (uint32_t)min(r, last) * (uint32_t)pitch + 16 * ((lane & 7) ^ ((r >> 1) & 7));
-    const int c = (lane & (B / 8 - 1)) ^ (B >= 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1));
+    const int c = (lane & (B / 8 - 1)) ^ ((B >= 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1)) + 2 * ((r >> 3) & 1));
     return (uint32_t)r * (uint32_t)pitch + 16 * min(c, last);
   };
   int last_a, last_b;
@@ -181,8 +188,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
     offsets();
   };
   const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)ring + wave * 1024;
-  // A stage's loads come in two parts, one for each operand.  begin: on to the
-  // next stage; rows past a transposed operand's last one repeat it, which only
+  // begin: on to the loads of the next stage; rows past a transposed operand's last one repeat it, which only
   // a run's last stage has.
   auto repeat_last = [&](int B, int n, uint32_t* o, int64_t pitch, int last) {
     if (last >= 63) return;
@@ -207,10 +213,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
       if (TB) repeat_last(BN, PB, ob, p.pitch_b, (int)(p.rows_b - 1 - k0));
     }
   };
-  auto load_a = [&](int slot, int d) { bf_dma16(ga, oa[d], base + slot * STAGE + d * NW * 1024); };
-  auto load_b = [&](int slot, int d) {
-    bf_dma16(gb, ob[d], base + slot * STAGE + A_BYTES + d * NW * 1024);
-    if (d == PB - 1) {  // the stage's last
+  // load d of the stage into a slot: A's, then B's
+  auto load = [&](int slot, int d) {
+    const uint32_t at = base + slot * STAGE;
+    if (d < PA) bf_dma16(ga, oa[d < PA ? d : 0], at + d * NW * 1024);
+    else bf_dma16(gb, ob[d < PA ? 0 : d - PA], at + A_BYTES + (d - PA) * NW * 1024);
+    if (d == PA + PB - 1) {
       ga += step_a;
       gb += step_b;
       --left;
@@ -218,53 +226,52 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
     }
   };
 
-  const int hh = lane >> 5, li = lane & 31, sx = (li >> 1) & 7;
-  f32x16v_t acc[TM][TN];
+  const int lq = lane >> 4, li = lane & 15, sx = (li >> 1) & 7;
+  f32x4v_t acc[TM][TN];
   bf16x8v_t fa[2][TM], fb[2][TN];
   // transposed: the lane's place of the first four rows of K, before the
-  // tile's 64 bytes of columns, which its row's swizzle picks
+  // fragment's 32 bytes of columns, which its row's swizzle picks
   const int tr = (lane & 15) >> 2;
-  auto place = [&](int B) { return (uint32_t)((8 * hh + tr) * (B * 2) + (lane >> 4 & 1) * 32 + (lane & 3) * 8); };
-  const int pick_a = BM >= 128 ? tr : tr >> 1, pick_b = BN >= 128 ? tr : tr >> 1;
+  auto place = [&](int B) { return (uint32_t)((8 * lq + tr) * (B * 2) + (lane & 3) * 8); };
+  const int pick_a = (BM >= 128 ? 2 * tr : 2 * (tr >> 1)) + (lq & 1), pick_b = (BN >= 128 ? 2 * tr : 2 * (tr >> 1)) + (lq & 1);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)ring;
   auto read_a = [&](int slot, int kk, int i) {
     if constexpr (TA) {
-      const uint32_t at = lds0 + slot * STAGE + place(BM) + kk * 16 * (BM * 2);
-      fa[kk & 1][i] = read_transposed(at + (((wm * TM + i) ^ pick_a) * 64), 4 * (BM * 2));
+      const uint32_t at = lds0 + slot * STAGE + place(BM) + kk * 32 * (BM * 2);
+      fa[kk][i] = read_transposed(at + (((wm * TM + i) ^ pick_a) * 32), 4 * (BM * 2));
     } else {
-      fa[kk & 1][i] = *(const bf16x8v_t*)(ring + slot * STAGE + li * 128 + ((2 * kk + hh) ^ sx) * 16 + (wm * TM + i) * 4096);
+      fa[kk][i] = *(const bf16x8v_t*)(ring + slot * STAGE + li * 128 + ((4 * kk + lq) ^ sx) * 16 + (wm * TM + i) * 2048);
     }
   };
   auto read_b = [&](int slot, int kk, int j) {
     if constexpr (TB) {
-      const uint32_t at = lds0 + slot * STAGE + A_BYTES + place(BN) + kk * 16 * (BN * 2);
-      fb[kk & 1][j] = read_transposed(at + (((wn * TN + j) ^ pick_b) * 64), 4 * (BN * 2));
+      const uint32_t at = lds0 + slot * STAGE + A_BYTES + place(BN) + kk * 32 * (BN * 2);
+      fb[kk][j] = read_transposed(at + (((wn * TN + j) ^ pick_b) * 32), 4 * (BN * 2));
     } else {
-      fb[kk & 1][j] = *(const bf16x8v_t*)(ring + slot * STAGE + A_BYTES + li * 128 + ((2 * kk + hh) ^ sx) * 16 + (wn * TN + j) * 4096);
+      fb[kk][j] = *(const bf16x8v_t*)(ring + slot * STAGE + A_BYTES + li * 128 + ((4 * kk + lq) ^ sx) * 16 + (wn * TN + j) * 2048);
     }
   };
-  // the fragments in the order of their use: b0 a0 b1 a1 ...
+  // the fragments in the order of their use
   auto read = [&](int slot, int kk, int f) {
-    if (f < 2 * TN && f < 2 * TM ? f & 1 : f < TM + TN && TM > TN) read_a(slot, kk, f < 2 * TN ? f >> 1 : f - TN);
-    else read_b(slot, kk, f < 2 * TM ? f >> 1 : f - TM);
+    if (f < TN) read_b(slot, kk, f);
+    else read_a(slot, kk, f - TN);
   };
-  // Sub-step kk: its matrix instructions, and between them, in this order, the
-  // LDS reads of the next one (of slot `from`) and the loads of one operand of
-  // a stage (into slot `to`): the loads of all waves at once would fill the
+  // Sub-step kk: its matrix instructions, and between them the LDS reads of the
+  // next one (of slot `from`) and, in the second, the loads of a stage (into
+  // slot `to`), one at a time: the loads of all waves at once would fill the
   // memory pipe's queue and hold the matrix instructions behind them.
   auto step = [&](int kk, int from, int to) {
+    constexpr int T = TM * TN, R = TM + TN, D = PA + PB;
 #pragma unroll
-    for (int t = 0; t < TM * TN; ++t) {
+    for (int t = 0; t < T; ++t) {
       const int i = t / TN, j = t % TN;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk & 1][j], fa[kk & 1][i], acc[i][j], 0, 0, 0);
-      constexpr int EACH = (TM + TN + TM * TN - 1) / (TM * TN);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kk][j], fa[kk][i], acc[i][j], 0, 0, 0);
+      // reads over the first three quarters, loads over the first half
 #pragma unroll
-      for (int f = t * EACH; f < (t + 1) * EACH && f < TM + TN; ++f) read(from, (kk + 1) & 3, f);
-      const int n = kk == 3 ? PA : kk == 0 ? PB : 0;
+      for (int f = t * R * 4 / (3 * T); f < (t + 1) * R * 4 / (3 * T) && f < R; ++f) read(from, kk ^ 1, f);
+      if (kk == 1) {
 #pragma unroll
-      for (int d = t * n / (TM * TN); d < (t + 1) * n / (TM * TN); ++d) {
-        if (kk == 3) load_a(to, d);
-        else load_b(to, d);
+        for (int d = t * D * 2 / T; d < (t + 1) * D * 2 / T && d < D; ++d) load(to, d);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -282,7 +289,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
   };
-  using First = std::integral_constant<int, (NS - 1) * (PA + PB) - PB>;
+  using First = std::integral_constant<int, (NS - 1) * (PA + PB)>;
   using Left = std::integral_constant<int, (NS - 2) * (PA + PB)>;
 
   source(m0, n0, split);
@@ -290,38 +297,33 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
   for (int s = 0; s < NS; ++s) {
     begin();
 #pragma unroll
-    for (int d = 0; d < PA; ++d) load_a(s, d);
-    if (s == NS - 1) break;  // the last one's second part comes in the first sub-step
-#pragma unroll
-    for (int d = 0; d < PB; ++d) load_b(s, d);
+    for (int d = 0; d < PA + PB; ++d) load(s, d);
   }
   landed(First{});
 #pragma unroll
   for (int f = 0; f < TM + TN; ++f) read(0, 0, f);
-  int slot = 0, free_slot = NS - 1;
+  int slot = 0;
   for (bool more = true; more;) {
     const int nk = min(p.split_stages, stages - split * p.split_stages);
-    const int64_t row0 = m0 + wm * TM * 32, col0 = n0 + wn * TN * 32;
+    const int64_t row0 = m0 + wm * TM * 16, col0 = n0 + wn * TN * 16;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j] = f32x16v_t{};
+      for (int j = 0; j < TN; ++j) acc[i][j] = f32x4v_t{};
     for (int kt = 0; kt < nk; ++kt) {
-      step(0, slot, free_slot);
-      step(1, slot, 0);
-      step(2, slot, 0);
+      step(0, slot, 0);
       landed(Left{});
-      free_slot = slot;
+      const int free_slot = slot;
       slot = slot + 1 == NS ? 0 : slot + 1;
       begin();
-      step(3, slot, free_slot);
+      step(1, slot, free_slot);
     }
 
     // the lane indices taken anew, so that what is made of them does not
     // occupy registers all through the main loop
     int el = lane;
     asm volatile("" : "+v"(el));
-    const int li = el & 31, hh = el >> 5, sx = (li >> 1) & 7;
+    const int li = el & 15, lq = el >> 4;
     // and the arguments read anew, so that they do not occupy scalar registers
     auto args = (const __attribute__((address_space(4))) BfGemmParams*)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(args));
@@ -329,44 +331,48 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
 
     if constexpr (OUT == kBfStats) {
       if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
-      // a row's 64 columns lie in two lanes, 32 values each
+      // a row's 64 columns lie in four lanes, 16 values each
       if (col0 < p.N) {
         const int cols = (int)min((int64_t)64, p.N - col0);
-        auto column = [&](int j, int e) { return j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3); };
+        auto column = [&](int j, int v) { return j * 16 + 4 * lq + v; };
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const int64_t row = row0 + i * 32 + li;
+          const int64_t row = row0 + i * 16 + li;
           const int64_t t = row < p.M ? target_of(p.targets, p.targets64, p.ignore, p.vocab, row) - p.v0 - col0 : -1;
           const int at = t >= 0 && t < 64 ? (int)t : -1;
           if (cols < 64) {
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (column(j, e) >= cols) acc[i][j][e] = -__builtin_inff();
+              for (int v = 0; v < 4; ++v)
+                if (column(j, v) >= cols) acc[i][j][v] = -__builtin_inff();
           }
           float m = -__builtin_inff();
 #pragma unroll
           for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][j][e]);
-          const auto mm = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-          m = fmaxf(__uint_as_float(mm[0]), __uint_as_float(mm[1]));
+            for (int v = 0; v < 4; ++v) m = fmaxf(m, acc[i][j][v]);
+          const auto m1 = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+          m = fmaxf(__uint_as_float(m1[0]), __uint_as_float(m1[1]));
+          const auto m2 = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+          m = fmaxf(__uint_as_float(m2[0]), __uint_as_float(m2[1]));
           const float off = m == -__builtin_inff() ? 0.0f : -m * kLog2E;
           float s = 0.0f;
 #pragma unroll
           for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2E, off));
-          const auto ss = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
-          s = __uint_as_float(ss[0]) + __uint_as_float(ss[1]);
-          if (hh == 0 && row < p.M) p.stat[((p.v0 + col0) >> 6) * p.M + row] = make_float2(m, s);
+            for (int v = 0; v < 4; ++v) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2E, off));
+          const auto s1 = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+          s = __uint_as_float(s1[0]) + __uint_as_float(s1[1]);
+          const auto s2 = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+          s = __uint_as_float(s2[0]) + __uint_as_float(s2[1]);
+          if (lq == 0 && row < p.M) p.stat[((p.v0 + col0) >> 6) * p.M + row] = make_float2(m, s);
           if (__ballot(at >= 0)) {
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (column(j, e) == at) p.target_logit[row] = acc[i][j][e];
+              for (int v = 0; v < 4; ++v)
+                if (column(j, v) == at) p.target_logit[row] = acc[i][j][v];
           }
         }
       }
@@ -374,7 +380,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
       constexpr bool BF = OUT != kBfF32;
       uint8_t* const my = ep + wave * (ER * 128);
       const int rr = el >> 3, rc = el & 7;  // read back: 8 rows of 8 chunks
-      // bf16: 32 rows of 64 columns a tile row, in chunks of 8 values; else 32
+      // bf16: ER rows of 64 columns at a time, in chunks of 8 values; else ER
       // rows of 32 columns, chunks of 4
       constexpr int COLS = BF ? 64 : 32, PER = COLS / 8;
       const bool lo_too = OUT == kBfProb && p.lo_plane != 0;
@@ -384,121 +390,120 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
       uint16_t* const c16 = OUT == kBfProb ? p.prob : (uint16_t*)p.C;
       const bool vec = OUT == kBfProb || (((uintptr_t)p.C & 15) == 0 && (p.ldc * (BF ? 2 : 4)) % 16 == 0);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
+      for (int i0 = 0; i0 < TM; i0 += ER / 16) {
         if constexpr (OUT == kBfProb) {
-          const int64_t r = row0 + i * 32 + li, row = min(r, p.M - 1);
-          const int64_t word = r < p.M ? target_of(p.targets, p.targets64, p.ignore, p.vocab, row) : -1;
-          const int64_t t = word - p.v0 - col0;
-          const int at = word >= 0 && t >= 0 && t < TN * 32 ? (int)t : -1;
-          const int cols = (int)max((int64_t)0, min((int64_t)(TN * 32), p.N - col0));
-          float g = p.grad_each ? p.grad[row] : p.grad[0];
-          if (p.count) g /= p.count[0];
-          const float off = -p.lse[row] * kLog2E;
-          const bool some = word >= 0 && g != 0.0f;  // a token without a part: zeros, whatever its logits
-          auto column = [&](int j, int e) { return j * 32 + 8 * (e >> 2) + 4 * hh + (e & 3); };
+          const int cols = (int)max((int64_t)0, min((int64_t)64, p.N - col0));
+          float each = 0.0f;
+          if (!p.grad_each) each = p.count ? p.grad[0] / p.count[0] : p.grad[0];
+          auto column = [&](int j, int v) { return j * 16 + 4 * lq + v; };
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
+          for (int i = i0; i < i0 + ER / 16; ++i) {
+            const int64_t r = row0 + i * 16 + li, row = min(r, p.M - 1);
+            const int64_t word = r < p.M ? target_of(p.targets, p.targets64, p.ignore, p.vocab, row) : -1;
+            const int64_t t = word - p.v0 - col0;
+            const int at = word >= 0 && t >= 0 && t < 64 ? (int)t : -1;
+            float g = each;
+            if (p.grad_each) g = p.count ? p.grad[row] / p.count[0] : p.grad[row];
+            const float off = -p.lse[row] * kLog2E;
+            const bool some = word >= 0 && g != 0.0f;  // a token without a part: zeros, whatever its logits
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2E, off)) * g;
-              acc[i][j][e] = some ? v : 0.0f;
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2E, off)) * g;
+                acc[i][j][v] = some ? x : 0.0f;
+              }
+            if (__ballot(some && at >= 0)) {
+#pragma unroll
+              for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                  if (some && column(j, v) == at) acc[i][j][v] -= g;
             }
-          if (__ballot(some && at >= 0)) {
+            if (cols < 64) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
+              for (int j = 0; j < TN; ++j)
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (some && column(j, e) == at) acc[i][j][e] -= g;
+                for (int v = 0; v < 4; ++v)
+                  if (column(j, v) >= cols) acc[i][j][v] = 0.0f;
+            }
           }
-          if (cols < TN * 32) {
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (column(j, e) >= cols) acc[i][j][e] = 0.0f;
-          }
-          __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int j0 = 0; j0 < TN; j0 += COLS / 32) {
+        for (int j0 = 0; j0 < TN; j0 += COLS / 16) {
           for (int plane = 0; plane < 1 + (int)lo_too; ++plane) {
 #pragma unroll
-            for (int r0 = 0; r0 < 32; r0 += ER) {
-              if (ER == 32 || li / ER == r0 / ER) {
+            for (int i = i0; i < i0 + ER / 16; ++i) {
+              const int r = (i - i0) * 16 + li;
+              uint8_t* const row = my + r * 128;
 #pragma unroll
-                for (int j = j0; j < j0 + COLS / 32; ++j)
-#pragma unroll
-                  for (int g = 0; g < 4; ++g) {
-                    float c[4];
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) c[v] = acc[i][j][4 * g + v];
-                    uint8_t* const row = my + (li % ER) * 128;
-                    if constexpr (BF) {
-                      uint2 w = make_uint2(pack_bf16(c[0], c[1]), pack_bf16(c[2], c[3]));
-                      if (plane)
-                        w = make_uint2(pack_bf16(c[0] - unpack_bf16(w.x, 0), c[1] - unpack_bf16(w.x, 1)),
-                                       pack_bf16(c[2] - unpack_bf16(w.y, 0), c[3] - unpack_bf16(w.y, 1)));
-                      *(uint2*)(row + ((j * 4 + g) ^ sx) * 16 + hh * 8) = w;
-                    } else {
-                      *(float4*)(row + ((2 * g + hh) ^ sx) * 16) = make_float4(c[0], c[1], c[2], c[3]);
-                    }
-                  }
-              }
-              wave_fence();
-              const int64_t offset = OUT == kBfProb ? plane * p.lo_plane : split * p.split_ld;
-              if (vec) {
-#pragma unroll
-                for (int k = 0; k < ER / 8; ++k) {
-                  const int r = k * 8 + rr;
-                  u32x4v_t w = *(const u32x4v_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
-                  const int64_t row = row0 + i * 32 + r0 + r, col = col0 + j0 * 32 + rc * PER;
-                  if (row >= M) continue;
-                  const int64_t at = offset + row * ld + col;
-                  if (col + PER <= N) {
-                    u32x4v_t* const to = BF ? (u32x4v_t*)(c16 + at) : (u32x4v_t*)((float*)p.C + at);
-                    if constexpr (!BF) {
-                      if (p.add) {
-                        const u32x4v_t o = *to;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) + __uint_as_float(o[e]));
-                      }
-                    }
-                    *to = w;
-                  } else {
-#pragma unroll
-                    for (int e = 0; e < PER; ++e) {
-                      if (col + e >= N) break;
-                      if constexpr (BF) {
-                        c16[at + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-                      } else {
-                        float* const to = (float*)p.C + at + e;
-                        *to = __uint_as_float(w[e]) + (p.add ? *to : 0.0f);
-                      }
-                    }
-                  }
-                }
-              } else {
-                // rows of any alignment: neighbouring lanes write neighbouring values
-                constexpr int RS = 64 / COLS;  // rows a store
-                const int c = el & (COLS - 1);
-                const int64_t col = col0 + j0 * 32 + c;
-#pragma unroll
-                for (int k = 0; k < ER / RS; ++k) {
-                  const int r = k * RS + el / COLS;
-                  const uint8_t* const from = my + r * 128 + ((c / PER) ^ ((r >> 1) & 7)) * 16;
-                  const int64_t row = row0 + i * 32 + r0 + r;
-                  if (row >= M || col >= N) continue;
-                  const int64_t at = offset + row * ld + col;
-                  if constexpr (BF) {
-                    c16[at] = *((const uint16_t*)from + c % PER);
-                  } else {
-                    float* const to = (float*)p.C + at;
-                    *to = *((const float*)from + c % PER) + (p.add ? *to : 0.0f);
-                  }
+              for (int j = j0; j < j0 + COLS / 16; ++j) {
+                const f32x4v_t c = acc[i][j];
+                if constexpr (BF) {
+                  uint2 w = make_uint2(pack_bf16(c[0], c[1]), pack_bf16(c[2], c[3]));
+                  if (plane)
+                    w = make_uint2(pack_bf16(c[0] - unpack_bf16(w.x, 0), c[1] - unpack_bf16(w.x, 1)),
+                                   pack_bf16(c[2] - unpack_bf16(w.y, 0), c[3] - unpack_bf16(w.y, 1)));
+                  *(uint2*)(row + ((2 * j + (lq >> 1)) ^ ((r >> 1) & 7)) * 16 + (lq & 1) * 8) = w;
+                } else {
+                  *(f32x4v_t*)(row + ((4 * (j - j0) + lq) ^ ((r >> 1) & 7)) * 16) = c;
                 }
               }
-              wave_fence();
             }
+            wave_fence();
+            const int64_t offset = OUT == kBfProb ? plane * p.lo_plane : split * p.split_ld;
+            if (vec) {
+#pragma unroll
+              for (int k = 0; k < ER / 8; ++k) {
+                const int r = k * 8 + rr;
+                u32x4v_t w = *(const u32x4v_t*)(my + r * 128 + (rc ^ ((r >> 1) & 7)) * 16);
+                const int64_t row = row0 + i0 * 16 + r, col = col0 + j0 * 16 + rc * PER;
+                if (row >= M) continue;
+                const int64_t at = offset + row * ld + col;
+                if (col + PER <= N) {
+                  u32x4v_t* const to = BF ? (u32x4v_t*)(c16 + at) : (u32x4v_t*)((float*)p.C + at);
+                  if constexpr (!BF) {
+                    if (p.add) {
+                      const u32x4v_t o = *to;
+#pragma unroll
+                      for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) + __uint_as_float(o[e]));
+                    }
+                  }
+                  *to = w;
+                } else {
+#pragma unroll
+                  for (int e = 0; e < PER; ++e) {
+                    if (col + e >= N) break;
+                    if constexpr (BF) {
+                      c16[at + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                    } else {
+                      float* const to = (float*)p.C + at + e;
+                      *to = __uint_as_float(w[e]) + (p.add ? *to : 0.0f);
+                    }
+                  }
+                }
+              }
+            } else {
+              // rows of any alignment: neighbouring lanes write neighbouring values
+              constexpr int RS = 64 / COLS;  // rows a store
+              const int c = el & (COLS - 1);
+              const int64_t col = col0 + j0 * 16 + c;
+#pragma unroll
+              for (int k = 0; k < ER / RS; ++k) {
+                const int r = k * RS + el / COLS;
+                const uint8_t* const from = my + r * 128 + ((c / PER) ^ ((r >> 1) & 7)) * 16;
+                const int64_t row = row0 + i0 * 16 + r;
+                if (row >= M || col >= N) continue;
+                const int64_t at = offset + row * ld + col;
+                if constexpr (BF) {
+                  c16[at] = *((const uint16_t*)from + c % PER);
+                } else {
+                  float* const to = (float*)p.C + at;
+                  *to = *((const float*)from + c % PER) + (p.add ? *to : 0.0f);
+                }
+              }
+            }
+            wave_fence();
           }
         }
       }

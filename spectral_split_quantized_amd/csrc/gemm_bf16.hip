@@ -9,7 +9,7 @@ namespace {
 
 template <int WM, int WN, int TM, int NS, int ER>
 void launch_tiles(const BfGemmParams& g, BfOut out, hipStream_t st) {
-  const int64_t units = ceil_div<int64_t>(g.M, WM * TM * 32) * ceil_div<int64_t>(g.N, WN * 64) * g.splits;
+  const int64_t units = ceil_div<int64_t>(g.M, WM * TM * 16) * ceil_div<int64_t>(g.N, WN * 64) * g.splits;
   // workgroups that fit the chip at once: one of 8 waves a CU, or two of 4
   const dim3 grid((unsigned)std::min<int64_t>(256 * (8 / (WM * WN)), ceil_div<int64_t>(units, 8) * 8));
   const dim3 block(WM * WN * 64);
@@ -78,9 +78,9 @@ hipError_t launch_bf_gemm(const BfGemmParams& in, BfOut out, hipStream_t st) {
   const int stages = g.runs * g.run_stages;
   const int tile = plan_of(g.M, g.N, stages, g.splits > 1 ? kBfMostSplits : 1).tile;
   g.split_stages = ceil_div(stages, g.splits);
-  if (tile == 0) launch_tiles<2, 4, 4, 2, 32>(g, out, st);
-  else if (tile == 1) launch_tiles<2, 2, 2, 2, 32>(g, out, st);
-  else launch_tiles<2, 2, 1, 3, 16>(g, out, st);
+  if (tile == 0) launch_tiles<2, 4, 8, 2, 32>(g, out, st);
+  else if (tile == 1) launch_tiles<2, 2, 4, 2, 32>(g, out, st);
+  else launch_tiles<2, 2, 2, 3, 16>(g, out, st);
   return hipGetLastError();
 }
 
