@@ -261,17 +261,20 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
   // slot `to`), one at a time: the loads of all waves at once would fill the
   // memory pipe's queue and hold the matrix instructions behind them.
   auto step = [&](int kk, int from, int to) {
-    constexpr int T = TM * TN, R = TM + TN, D = PA + PB;
+    // (16384 x 4096 x 8192, both transposed, in us: loads over the whole
+    // sub-step 832, over its first half 866; statistics of 8192 x 16384 x 4096
+    // 754 and 768, but probabilities 885 and 866, one transposed 846 and 833)
+    constexpr int T = TM * TN, R = TM + TN, D = PA + PB, SOON = TA || OUT == kBfStats ? 1 : 2;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const int i = t / TN, j = t % TN;
       acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kk][j], fa[kk][i], acc[i][j], 0, 0, 0);
-      // reads over the first three quarters, loads over the first half
+      // reads over the first three quarters
 #pragma unroll
       for (int f = t * R * 4 / (3 * T); f < (t + 1) * R * 4 / (3 * T) && f < R; ++f) read(from, kk ^ 1, f);
       if (kk == 1) {
 #pragma unroll
-        for (int d = t * D * 2 / T; d < (t + 1) * D * 2 / T && d < D; ++d) load(to, d);
+        for (int d = t * D * SOON / T; d < (t + 1) * D * SOON / T && d < D; ++d) load(to, d);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -335,11 +338,13 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
       if (col0 < p.N) {
         const int cols = (int)min((int64_t)64, p.N - col0);
         auto column = [&](int j, int v) { return j * 16 + 4 * lq + v; };
+        int64_t word[TM];  // all rows' loads in flight at once
+#pragma unroll
+        for (int i = 0; i < TM; ++i) word[i] = target_of(p.targets, p.targets64, p.ignore, p.vocab, min(row0 + i * 16 + li, p.M - 1));
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const int64_t row = row0 + i * 16 + li;
-          const int64_t t = row < p.M ? target_of(p.targets, p.targets64, p.ignore, p.vocab, row) - p.v0 - col0 : -1;
-          const int at = t >= 0 && t < 64 ? (int)t : -1;
+          const int64_t row = row0 + i * 16 + li, t = word[i] - p.v0 - col0;
+          const int at = row < p.M && word[i] >= 0 && t >= 0 && t < 64 ? (int)t : -1;
           if (cols < 64) {
 #pragma unroll
             for (int j = 0; j < TN; ++j)
@@ -510,6 +515,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
     }
     q += gridDim.x;
     more = locate(q, m0, n0, split);
+    // read again: their registers served the epilogue
+#pragma unroll
+    for (int f = 0; f < TM + TN; ++f) read(slot, 0, f);
   }
   // no load may land in LDS that a later workgroup owns
   __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (15 << 8));

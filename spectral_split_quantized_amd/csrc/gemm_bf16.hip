@@ -32,7 +32,7 @@ struct Tile {
   int m, n;
   double one, two;
 };
-constexpr Tile kTiles[3] = {{256, 256, 1.6, 0}, {128, 128, 0.61, 1.1}, {64, 128, 0.37, 0.77}};
+constexpr Tile kTiles[3] = {{256, 256, 1.55, 0}, {128, 128, 0.63, 0.98}, {64, 128, 0.31, 0.77}};
 
 // us that M x N x 64 stages take in `splits` parts of K: whole rounds of
 // workgroups and the rest of one, what a workgroup starts and ends with, and
@@ -46,13 +46,13 @@ double time_of(const Tile& t, int64_t M, int64_t N, int stages, int splits) {
 }
 
 // the fastest tile and splits by that estimate (us measured, without the join):
-//   8192 x 768 x 25152: 256 x 256 whole 583, in 2 328, in 8 366; 128 x 128
-//     whole 422, in 2 425; 64 x 128 455
-//   1024 x 1024 x 30720: 256 x 256 in 8 91, in 16 66; 128 x 128 in 8 85; 64 x
-//     128 whole 178, in 4 86
-//   100 x 512 x 5760: 64 x 128 whole 38, in 12 8; 128 x 128 in 12 10
-//   37 x 50304 x 768: 64 x 128 15, 128 x 128 17, 256 x 256 23
-//   12608 x 768 x 8192: 256 x 256 187, 128 x 128 208, 64 x 128 212
+//   8192 x 768 x 21760: 256 x 256 whole 502, in 2 279, in 8 322; 128 x 128
+//     whole 359, in 4 338; 64 x 128 383
+//   1024 x 1024 x 30720: 256 x 256 in 8 79, in 16 66; 128 x 128 in 8 85; 64 x
+//     128 whole 148, in 2 83
+//   100 x 512 x 5760: 64 x 128 whole 32, in 12 7; 128 x 128 in 12 9
+//   37 x 50304 x 768: 64 x 128 16, 128 x 128 16, 256 x 256 21
+//   12608 x 768 x 8192: 256 x 256 161, 128 x 128 189, 64 x 128 189
 struct Plan {
   int tile, splits;
 };
