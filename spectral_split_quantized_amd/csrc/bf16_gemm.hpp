@@ -1,13 +1,18 @@
-// bf16_gemm.hpp -- A B^T of bf16 operands on gfx950's matrix instructions, with
-// the epilogues of the loss over a vocabulary.
+// bf16_gemm.hpp -- A B^T of 16-bit operands on gfx950's matrix instructions,
+// with the epilogues of the loss over a vocabulary.
 //
 // An operand lies with K along the row, at a pitch that is a multiple of 64
-// values, zeros behind K; or transposed, with K down the columns (rows of
-// k, each readable up to a multiple of 8 values).  A binary32 operand is a pair of bf16 planes, hi = x
-// rounded and lo = the rest rounded (off by 2^-16 of x at most), and the
+// values, zeros behind K; or transposed, with K down the columns (rows of k,
+// each readable up to a multiple of 8 values).  Its values are bf16 as a user
+// has them, or binary16 planes made of them: x 2^s, with s such that the
+// operand's largest finite value lies in [2^14, 2^15).  One plane holds a bf16
+// operand (exactly, down to 2^-29 of the largest value); a binary32 operand is
+// a pair of planes, hi = x 2^s rounded and lo = the rest rounded, off by 2^-22 of x and
+// 2^-40 of the largest value at most.  (bf16 planes would be off by 2^-16.)  The
 // product is the sum of up to three products of planes (hi hi, hi lo, lo hi;
 // lo lo is no larger than the planes' own error), which simply follow each
-// other along K.  Products of bf16 values are exact, sums are binary32.
+// other along K; the epilogue takes the scales off.  Products of 16-bit values
+// are exact, sums are binary32.
 #pragma once
 
 #include <algorithm>
@@ -19,7 +24,7 @@ namespace metis {
 
 enum BfOut : int {
   kBfStats,  // softmax statistics of the rows
-  kBfProb,   // scaled probabilities minus one at the target, bf16 planes
+  kBfProb,   // scaled probabilities minus one at the target, binary16 planes
   kBfF32,    // C, binary32, stored or added; with splits one C for each
   kBfBF16    // C, bf16
 };
@@ -31,6 +36,7 @@ struct BfGemmParams {
   int64_t rows_a, rows_b;     // of a transposed operand: rows of K (the last repeats up to a whole stage)
   int runs, run_stages;       // K: `runs` products of planes of run_stages stages of 64 each
   int64_t at_a[3], at_b[3];   // where the planes of a run begin, bytes
+  const int *shift_a, *shift_b;  // the operands' s (null: 0)
   int splits, split_stages;   // all stages cut into splits of split_stages (the last may be shorter)
   // kBfF32, kBfBF16
   void* C;
@@ -49,11 +55,13 @@ struct BfGemmParams {
   const float* grad;          // [M], or one with `count`
   const float* count;         // tokens that the loss is the mean over, or null
   int grad_each;              // grad has a value for each token
+  const int* shift_p;         // P's s
   uint16_t* prob;             // [M rounded up to 64][ldp], and lo_plane values behind it the low plane
   int64_t ldp, lo_plane;      // lo_plane 0: none
 };
 
 typedef __bf16 bf16x8v_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8v_t __attribute__((ext_vector_type(8)));
 typedef float f32x4v_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4v_t __attribute__((ext_vector_type(4)));
 
@@ -68,6 +76,20 @@ __device__ __forceinline__ void bf_dma16(const uint8_t* base, uint32_t off, uint
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                : "memory", "m0");
 }
+
+// two values rounded to binary16 (nearest even), a in the low half
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), f16x2_t));
+}
+
+__device__ __forceinline__ float unpack_f16(uint32_t w, int i) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)(i & 1 ? w >> 16 : w));
+}
+
+// the rest of x behind its rounded value; none behind an infinity
+__device__ __forceinline__ float rest_f16(float x, float rounded) { return fabsf(rounded) <= 65504.0f ? x - rounded : 0.0f; }
 
 // the word of token `row`, or -1 where it has no part in the loss
 __device__ __forceinline__ int64_t target_of(const void* targets, int targets64, int64_t ignore, int64_t vocab, int64_t row) {
@@ -109,8 +131,11 @@ __device__ __forceinline__ bf16x8v_t read_transposed(uint32_t at, uint32_t row4)
 // c ^ (4 (k % 4) + 2 (k / 8 % 2)) (rows of 128 bytes: c ^ (4 (k / 2 % 2) + 2 (k /
 // 8 % 2))), which puts them on different banks.
 //
+// HALF: the operands are binary16 planes, else bf16.  (A product of random
+// operands takes 2 to 3 % longer with binary16, which draws more power.)
+//
 // Rows past M / N repeat the last row (never stored).
-template <int WM, int WN, int TM, int NS, int ER, BfOut OUT, bool TA, bool TB>
+template <int WM, int WN, int TM, int NS, int ER, BfOut OUT, bool TA, bool TB, bool HALF>
 __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p) {
   constexpr int TN = 4;
   constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
@@ -268,7 +293,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const int i = t / TN, j = t % TN;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kk][j], fa[kk][i], acc[i][j], 0, 0, 0);
+      if constexpr (HALF)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8v_t, fb[kk][j]),
+                                                           __builtin_bit_cast(f16x8v_t, fa[kk][i]), acc[i][j], 0, 0, 0);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kk][j], fa[kk][i], acc[i][j], 0, 0, 0);
       // reads over the first three quarters
 #pragma unroll
       for (int f = t * R * 4 / (3 * T); f < (t + 1) * R * 4 / (3 * T) && f < R; ++f) read(from, kk ^ 1, f);
@@ -331,6 +360,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
     auto args = (const __attribute__((address_space(4))) BfGemmParams*)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(args));
     const __attribute__((address_space(4))) BfGemmParams& p = *args;
+    // C = acc 2^down; as a factor of logits, kept above 0 (and -inf -inf)
+    const int down = HALF ? -(p.shift_a[0] + p.shift_b[0]) : 0;
+    const float unit = HALF ? __builtin_ldexpf(1.0f, max(down, -126)) : 1.0f, log2e = unit * kLog2E;
 
     if constexpr (OUT == kBfStats) {
       if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
@@ -361,23 +393,23 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
           m = fmaxf(__uint_as_float(m1[0]), __uint_as_float(m1[1]));
           const auto m2 = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
           m = fmaxf(__uint_as_float(m2[0]), __uint_as_float(m2[1]));
-          const float off = m == -__builtin_inff() ? 0.0f : -m * kLog2E;
+          const float off = m == -__builtin_inff() ? 0.0f : -m * log2e;
           float s = 0.0f;
 #pragma unroll
           for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2E, off));
+            for (int v = 0; v < 4; ++v) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], log2e, off));
           const auto s1 = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
           s = __uint_as_float(s1[0]) + __uint_as_float(s1[1]);
           const auto s2 = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false, false);
           s = __uint_as_float(s2[0]) + __uint_as_float(s2[1]);
-          if (lq == 0 && row < p.M) p.stat[((p.v0 + col0) >> 6) * p.M + row] = make_float2(m, s);
+          if (lq == 0 && row < p.M) p.stat[((p.v0 + col0) >> 6) * p.M + row] = make_float2(m * unit, s);
           if (__ballot(at >= 0)) {
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
               for (int v = 0; v < 4; ++v)
-                if (column(j, v) == at) p.target_logit[row] = acc[i][j][v];
+                if (column(j, v) == at) p.target_logit[row] = acc[i][j][v] * unit;
           }
         }
       }
@@ -398,6 +430,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
       for (int i0 = 0; i0 < TM; i0 += ER / 16) {
         if constexpr (OUT == kBfProb) {
           const int cols = (int)max((int64_t)0, min((int64_t)64, p.N - col0));
+          const int up = p.shift_p[0];
           float each = 0.0f;
           if (!p.grad_each) each = p.count ? p.grad[0] / p.count[0] : p.grad[0];
           auto column = [&](int j, int v) { return j * 16 + 4 * lq + v; };
@@ -410,12 +443,13 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
             float g = each;
             if (p.grad_each) g = p.count ? p.grad[row] / p.count[0] : p.grad[row];
             const float off = -p.lse[row] * kLog2E;
+            g = __builtin_ldexpf(g, up);
             const bool some = word >= 0 && g != 0.0f;  // a token without a part: zeros, whatever its logits
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
               for (int v = 0; v < 4; ++v) {
-                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2E, off)) * g;
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], log2e, off)) * g;
                 acc[i][j][v] = some ? x : 0.0f;
               }
             if (__ballot(some && at >= 0)) {
@@ -443,12 +477,22 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
               uint8_t* const row = my + r * 128;
 #pragma unroll
               for (int j = j0; j < j0 + COLS / 16; ++j) {
-                const f32x4v_t c = acc[i][j];
+                f32x4v_t c = acc[i][j];
+                if constexpr (OUT != kBfProb) {
+#pragma unroll
+                  for (int v = 0; v < 4; ++v) c[v] = __builtin_ldexpf(c[v], down);
+                }
                 if constexpr (BF) {
-                  uint2 w = make_uint2(pack_bf16(c[0], c[1]), pack_bf16(c[2], c[3]));
-                  if (plane)
-                    w = make_uint2(pack_bf16(c[0] - unpack_bf16(w.x, 0), c[1] - unpack_bf16(w.x, 1)),
-                                   pack_bf16(c[2] - unpack_bf16(w.y, 0), c[3] - unpack_bf16(w.y, 1)));
+                  uint2 w;
+                  if constexpr (OUT == kBfProb) {
+                    w = make_uint2(pack_f16(c[0], c[1]), pack_f16(c[2], c[3]));
+                    if (plane) {
+                      auto rest = [&](int v) { return rest_f16(c[v], unpack_f16(v < 2 ? w.x : w.y, v)); };
+                      w = make_uint2(pack_f16(rest(0), rest(1)), pack_f16(rest(2), rest(3)));
+                    }
+                  } else {
+                    w = make_uint2(pack_bf16(c[0], c[1]), pack_bf16(c[2], c[3]));
+                  }
                   *(uint2*)(row + ((2 * j + (lq >> 1)) ^ ((r >> 1) & 7)) * 16 + (lq & 1) * 8) = w;
                 } else {
                   *(f32x4v_t*)(row + ((4 * (j - j0) + lq) ^ ((r >> 1) & 7)) * 16) = c;

@@ -1,4 +1,4 @@
-// gemm_bf16.hip -- translation unit of the bf16 product (bf16_gemm.hpp), in
+// gemm_bf16.hip -- translation unit of the product of 16-bit operands (bf16_gemm.hpp), in
 // its own unit for the scheduling strategy that its loop wants.
 #include "bf16_gemm.hpp"
 #include "gemm_launch.hpp"
@@ -15,13 +15,14 @@ void launch_tiles(const BfGemmParams& g, BfOut out, hipStream_t st) {
   const dim3 block(WM * WN * 64);
 #define LAUNCH(...) hipLaunchKernelGGL((bf_gemm_kernel<WM, WN, TM, NS, ER, __VA_ARGS__>), grid, block, 0, st, g)
   // the logits' product has K along both rows, dx = P W has W transposed, dw =
-  // P^T x both
-  if (out == kBfStats) LAUNCH(kBfStats, false, false);
-  else if (out == kBfProb) LAUNCH(kBfProb, false, false);
-  else if (out == kBfBF16 && g.rows_a) LAUNCH(kBfBF16, true, true);
-  else if (out == kBfBF16) LAUNCH(kBfBF16, false, true);
-  else if (g.rows_a) LAUNCH(kBfF32, true, true);
-  else LAUNCH(kBfF32, false, true);
+  // P^T x both; all but the statistics of bf16 rows are of binary16 planes
+  if (out == kBfStats && !g.shift_a) LAUNCH(kBfStats, false, false, false);
+  else if (out == kBfStats) LAUNCH(kBfStats, false, false, true);
+  else if (out == kBfProb) LAUNCH(kBfProb, false, false, true);
+  else if (out == kBfBF16 && g.rows_a) LAUNCH(kBfBF16, true, true, true);
+  else if (out == kBfBF16) LAUNCH(kBfBF16, false, true, true);
+  else if (g.rows_a) LAUNCH(kBfF32, true, true, true);
+  else LAUNCH(kBfF32, false, true, true);
 #undef LAUNCH
 }
 

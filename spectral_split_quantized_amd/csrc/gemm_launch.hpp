@@ -34,8 +34,9 @@ hipError_t launch_i8_gemm(const I8GemmParams& g, hipStream_t st);
 struct BfGemmParams;
 enum BfOut : int;
 
-// A B^T of bf16 planes (bf16_gemm.hpp): kBfStats and kBfProb with K along the
-// rows, the others with B transposed, and A where rows_a is set.  splits > 1
+// A B^T of 16-bit operands (bf16_gemm.hpp): kBfStats and kBfProb with K along
+// the rows, the others with B transposed, and A where rows_a is set; of
+// binary16 planes, but for kBfStats without shifts, which is of bf16 rows.  splits > 1
 // (as bf_gemm_splits gives it for the product's stages; kBfF32 only) writes
 // one C for each part of K; split_stages is set here.
 constexpr int kBfMostSplits = 32;

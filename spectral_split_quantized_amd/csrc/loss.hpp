@@ -8,7 +8,7 @@
 // Forward: a product whose epilogue leaves, for each token and 64 words, the
 // largest logit and the sum of exponentials below it; they are joined here in
 // a fixed order.  Backward, for a piece of words at a time: the product again,
-// whose epilogue forms P (rounded to bf16, or to a pair of bf16 planes where a
+// whose epilogue forms P (rounded to binary16, or to a pair of planes where a
 // gradient is binary32), then the two products of the gradients.  So the
 // backward pass spends 8 operations where keeping all logits would spend 6,
 // and its memory does not grow with the vocabulary.
@@ -21,47 +21,164 @@
 
 namespace metis {
 
-// bf16 planes of rows: dst[plane][row][pitch] with zeros behind cols, in the
-// rows behind `rows` up to out_rows, and in the rows of tokens without a part
-// in the loss (targets not null); the high plane is x rounded to bf16, the low
-// one the rest rounded.  Eight values a thread.
-struct PlanesParams {
-  const void* src;
+// What the products take of rows that they cannot take as they lie in memory:
+// planes[row][pitch], zeros behind cols, in the rows behind `rows` up to
+// out_rows, and, masked, in the rows of tokens without a part in the loss.
+// `shift` null: bf16 rows copied.  Else the binary16 planes that the product's
+// file describes, whose scale comes from the largest finite value: one launch
+// takes the largest values (each workgroup leaves its own, so that nothing has
+// to be cleared before), the next joins them, leaves the s in `shift` and makes
+// the planes.  Both are bound by memory; a piece of a weight is small enough to
+// stay in the cache behind the memory (256 MB) between them.
+struct PlanesJob {
+  const void* src;  // null: no planes, just the s (of the gradients of the losses)
   int64_t rows, cols, ld;
-  int bf16, vec;
+  int bf16, masked;
   uint16_t* dst;
-  int64_t out_rows, pitch, plane;  // pitch and plane in values; plane 0: high plane alone
+  int64_t out_rows, pitch, plane;  // pitch and plane in values; plane 0: one plane
+  int* shift;
+  uint32_t* top;       // [kTopBlocks] largest values of the workgroups, their bits
+  const void* values;  // what `top` is taken of (src, or the gradients)
+  const float* count;  // null, or what `values` are divided by
+  int top_blocks, blocks;
+  int flat;  // the values of all rows follow each other
+};
+
+constexpr int kTopBlocks = 1024, kPlaneJobs = 3;
+
+struct PlanesParams {
+  PlanesJob job[kPlaneJobs];
   const void* targets;
   int targets64;
   int64_t vocab, ignore;
 };
 
-__device__ __forceinline__ void store_planes(uint16_t* dst, int64_t at, int64_t plane, const float* v) {
-  uint32_t h[4], l[4];
+// eight consecutive values at any address of theirs
+template <bool BF>
+__device__ __forceinline__ void load8_anywhere(const void* p, int64_t at, float* v) {
+  typedef uint32_t u32x4_2_t __attribute__((ext_vector_type(4), aligned(2)));
+  typedef uint32_t u32x4_4_t __attribute__((ext_vector_type(4), aligned(4)));
+  if constexpr (BF) {
+    const u32x4_2_t q = *(const u32x4_2_t*)((const uint16_t*)p + at);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    l[i] = pack_bf16(v[2 * i] - unpack_bf16(h[i], 0), v[2 * i + 1] - unpack_bf16(h[i], 1));
+    for (int i = 0; i < 8; ++i) v[i] = unpack_bf16(q[i >> 1], i);
+  } else {
+    const u32x4_4_t a = *(const u32x4_4_t*)((const float*)p + at), b = *(const u32x4_4_t*)((const float*)p + at + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i < 4 ? a[i & 3] : b[i & 3]);
   }
-  *(uint4*)(dst + at) = make_uint4(h[0], h[1], h[2], h[3]);
-  if (plane) *(uint4*)(dst + plane + at) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Calls f(row, column, v) for blocks of eight values of the rows up to out_rows
+// of `pitch` columns (a multiple of 8), zeros where there is no value: all
+// workgroups of a job share them, four loads in flight a thread.
+template <bool BF, class F>
+__device__ __forceinline__ void each8(const PlanesJob& j, const PlanesParams& p, int64_t out_rows, int64_t pitch, int block,
+                                      int blocks, const void* from, F f) {
+  constexpr int K = 4;
+  const int64_t per = pitch >> 3, total = out_rows * per;
+  const int64_t stride = (int64_t)blocks * 256;
+  for (int64_t id0 = (int64_t)block * 256 + threadIdx.x; id0 < total; id0 += K * stride) {
+    float v[K][8];
+    int64_t row[K];
+    int col[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t id = id0 + k * stride;
+      row[k] = total <= UINT32_MAX ? (int64_t)((uint32_t)id / (uint32_t)per) : id / per;
+      const int64_t c = (id - row[k] * per) * 8;
+      if (id >= total) row[k] = -1;
+      col[k] = (int)c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
+      if (row[k] < 0 || row[k] >= j.rows) continue;
+      if (j.masked && target_of(p.targets, p.targets64, p.ignore, p.vocab, row[k]) < 0) continue;
+      const int64_t at = row[k] * j.ld + c;
+      if (c + 8 <= j.cols) {
+        load8_anywhere<BF>(from, at, v[k]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < j.cols) v[k][e] = load1(from, BF, at + e);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (row[k] >= 0) f(row[k], col[k], v[k]);
+  }
+}
+
+__device__ __forceinline__ uint32_t top_of_workgroup(uint32_t top, uint32_t* red) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+  __syncthreads();
+  return max(max(red[0], red[1]), max(red[2], red[3]));
+}
+
+// the job of a workgroup and its number there
+__device__ __forceinline__ int job_of(const int* blocks, int& block) {
+  int j = 0;
+  block = blockIdx.x;
+  while (j + 1 < kPlaneJobs && block >= blocks[j]) block -= blocks[j++];
+  return j;
+}
+
+__global__ __launch_bounds__(256) void top_kernel(PlanesParams p) {
+  __shared__ uint32_t red[4];
+  const int blocks[kPlaneJobs] = {p.job[0].top_blocks, p.job[1].top_blocks, p.job[2].top_blocks};
+  int block;
+  PlanesJob j = p.job[job_of(blocks, block)];
+  if (j.flat) j.cols *= j.rows, j.rows = 1;
+  uint32_t top = 0;  // of values of one sign, larger bits are larger values
+  auto take = [&](int64_t, int, const float* v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t b = __float_as_uint(v[e]) & 0x7FFFFFFFu;
+      if (b < 0x7F800000u) top = max(top, b);
+    }
+  };
+  const int64_t pitch = (j.cols + 7) & ~(int64_t)7;
+  if (j.bf16) each8<true>(j, p, j.rows, pitch, block, j.top_blocks, j.values, take);
+  else each8<false>(j, p, j.rows, pitch, block, j.top_blocks, j.values, take);
+  top = top_of_workgroup(top, red);
+  if (threadIdx.x == 0) j.top[block] = top;
 }
 
 __global__ __launch_bounds__(256) void planes_kernel(PlanesParams p) {
-  const int64_t per = p.pitch >> 3, total = p.out_rows * per;
-  for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
-    const int64_t row = id / per, c = (id - row * per) * 8;
-    float v[8] = {};
-    if (row < p.rows && (!p.targets || target_of(p.targets, p.targets64, p.ignore, p.vocab, row) >= 0)) {
-      if (p.vec && c + 8 <= p.cols) {
-        load8(p.src, p.bf16, row * p.ld + c, v);
-      } else {
+  __shared__ uint32_t red[4];
+  const int blocks[kPlaneJobs] = {p.job[0].blocks, p.job[1].blocks, p.job[2].blocks};
+  int block;
+  const PlanesJob j = p.job[job_of(blocks, block)];
+  float scale = 1.0f;
+  if (j.shift) {
+    uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e < p.cols ? load1(p.src, p.bf16, row * p.ld + c + e) : 0.0f;
-      }
-    }
-    store_planes(p.dst, row * p.pitch + c, p.plane, v);
+    for (int k = 0; k < kTopBlocks / 256; ++k)
+      if (k * 256 + (int)threadIdx.x < j.top_blocks) top = max(top, j.top[k * 256 + threadIdx.x]);
+    top = top_of_workgroup(top, red);
+    if (j.count) top = __float_as_uint(__uint_as_float(top) / j.count[0]);
+    // (2^126 is the largest power of two whose inverse is no subnormal; no
+    // value but 0, or no finite quotient: 14)
+    const int s = top == 0 || top >= 0x7F800000u ? 14 : min(14 - ((int)(top >> 23) - 127), 126);
+    if (block == 0 && threadIdx.x == 0) *j.shift = s;
+    scale = __builtin_ldexpf(1.0f, s);
   }
+  if (!j.src) return;
+  auto store = [&](int64_t row, int col, const float* v) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = v[2 * i] * scale, b = v[2 * i + 1] * scale;
+      h[i] = j.shift ? pack_f16(a, b) : pack_bf16(a, b);
+      if (j.plane) l[i] = pack_f16(rest_f16(a, unpack_f16(h[i], 0)), rest_f16(b, unpack_f16(h[i], 1)));
+    }
+    uint16_t* const to = j.dst + row * j.pitch + col;
+    *(uint4*)to = make_uint4(h[0], h[1], h[2], h[3]);
+    if (j.plane) *(uint4*)(to + j.plane) = make_uint4(l[0], l[1], l[2], l[3]);
+  };
+  if (j.bf16) each8<true>(j, p, j.out_rows, j.pitch, block, j.blocks, j.src, store);
+  else each8<false>(j, p, j.out_rows, j.pitch, block, j.blocks, j.src, store);
 }
 
 // Loss and log-sum-exp of each token from its statistics, 16 tokens a
@@ -156,22 +273,34 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(LossJoinParams p) {
   p.total[1] = (float)n;
 }
 
-// C (+)= the sum of the splits' C in order, binary32 or rounded to bf16
+// C (+)= the sum of the splits' C in order, binary32 or rounded to bf16: V
+// neighbouring values a thread (four where rows allow it: 8192 x 4096 sums to
+// bf16 99 us with one, 37 with four).
+template <int V>
 __global__ __launch_bounds__(256) void split_join_kernel(const float* part, int splits, int64_t split_ld, int64_t rows,
                                                          int64_t cols, void* C, int bf16, int64_t ldc, int add) {
-  const int64_t n = rows * cols;
+  typedef float vec_t __attribute__((ext_vector_type(V)));
+  const int64_t per = cols / V, n = rows * per;
   for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < n; id += (int64_t)gridDim.x * 256) {
-    const int64_t row = id / cols, col = id - row * cols;
-    float s = 0.0f;
+    const int64_t row = n <= UINT32_MAX ? (int64_t)((uint32_t)id / (uint32_t)per) : id / per, col = (id - row * per) * V;
+    vec_t s = 0.0f;
     for (int k = 0; k < splits; k += 8) {
-      float v[8];
+      vec_t v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = k + u < splits ? part[(k + u) * split_ld + id] : 0.0f;
+      for (int u = 0; u < 8; ++u) v[u] = k + u < splits ? *(const vec_t*)(part + (k + u) * split_ld + id * V) : 0.0f;
 #pragma unroll
       for (int u = 0; u < 8; ++u) s += v[u];
     }
-    if (add) s += load1(C, bf16, row * ldc + col);
-    store1(C, bf16, row * ldc + col, s);
+    const int64_t at = row * ldc + col;
+    if constexpr (V == 1) {
+      if (add) s += load1(C, bf16, at);
+      store1(C, bf16, at, s[0]);
+    } else if (bf16) {
+      *(uint2*)((uint16_t*)C + at) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
+    } else {
+      if (add) s += *(const vec_t*)((const float*)C + at);
+      *(vec_t*)((float*)C + at) = s;
+    }
   }
 }
 

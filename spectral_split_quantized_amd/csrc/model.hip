@@ -131,6 +131,7 @@ struct Planes {
   int64_t pitch = 0;  // bytes
   int64_t plane = 0;  // bytes between planes
   int count = 1;
+  const int* shift = nullptr;  // binary16 planes: their s
 };
 
 // whether rows can be an operand as they lie in memory
@@ -152,7 +153,8 @@ int64_t loss_piece(int64_t tokens, int64_t vocab, int64_t cols) {
 }
 
 struct LossPlan {
-  bool x_as_is, w_as_is, pair;  // pair: a gradient is binary32, P has two planes
+  bool x_as_is, w_as_is;  // forward, both bf16
+  bool pair;              // an operand is binary32: P has two planes, forward is of binary16 planes too
   int xp, wp;                   // planes of x and w
   int64_t N, V, D, Dp, Np, piece;
 };
@@ -161,17 +163,19 @@ LossPlan loss_plan(const metis_loss& l) {
   LossPlan p;
   p.N = l.tokens, p.V = l.vocab, p.D = l.cols;
   p.Dp = pad64(p.D), p.Np = pad64(p.N);
-  p.x_as_is = operand_as_is(l.x, l.x_dtype, l.ldx, p.N, p.D);
-  p.w_as_is = operand_as_is(l.w, l.w_dtype, l.ldw, p.V, p.D);
   p.xp = l.x_dtype == METIS_F32 ? 2 : 1;
   p.wp = l.w_dtype == METIS_F32 ? 2 : 1;
   p.pair = p.xp == 2 || p.wp == 2;
+  p.x_as_is = !p.pair && operand_as_is(l.x, l.x_dtype, l.ldx, p.N, p.D);
+  p.w_as_is = !p.pair && operand_as_is(l.w, l.w_dtype, l.ldw, p.V, p.D);
   p.piece = loss_piece(p.N, p.V, p.D);
   return p;
 }
 
 struct LossWs {
   uint16_t *x, *w;             // planes of x, of a piece of w (where not as they are)
+  uint32_t* top;               // [3][kTopBlocks] largest values of x, w, the gradients of the losses
+  int* shift;                  // [3] their s
   float2* stat;                // forward
   float *target, *losses;
   uint32_t* done;              // counter of the join
@@ -188,7 +192,11 @@ int dx_splits(const LossPlan& p, int64_t words) {
 LossWs carve_loss(Carver& cv, const metis_loss& l, const LossPlan& p, bool backward) {
   LossWs w{};
   if (backward || !p.x_as_is) w.x = cv.take<uint16_t>((size_t)p.xp * p.Np * p.Dp);
-  if (!p.w_as_is) w.w = cv.take<uint16_t>((size_t)p.wp * std::min(p.piece, p.V) * p.Dp);
+  if (backward || !p.w_as_is) w.w = cv.take<uint16_t>((size_t)p.wp * std::min(p.piece, p.V) * p.Dp);
+  if (backward || p.pair) {
+    w.top = cv.take<uint32_t>(3 * kTopBlocks);
+    w.shift = cv.take<int>(3);
+  }
   if (!backward) {
     w.stat = cv.take<float2>((size_t)ceil_div<int64_t>(p.V, 64) * p.N);
     w.target = cv.take<float>(p.N);
@@ -215,23 +223,65 @@ metis_status loss_check(const metis_loss* l, const char* what) {
   return METIS_OK;
 }
 
-// planes of rows that cannot be an operand as they are, else the rows
-// themselves; `mask`: always planes, rows up to a multiple of 64, zeros in those
-// of tokens that the loss leaves out
-metis_status as_operand(const void* src, int32_t dt, int64_t ld, int64_t rows, int64_t cols, bool as_is, int planes,
-                        uint16_t* dst, const metis_loss* mask, Planes* out, hipStream_t st) {
-  const int64_t pitch = pad64(cols), out_rows = mask ? pad64(rows) : rows;
-  if (as_is && !mask) {
-    *out = {(const uint8_t*)src, rows > 1 ? ld * 2 : pitch * 2, 0, 1};
+// Planes of x (job 0) and w (job 1) and the s of the gradients of the losses
+// (job 2), as planes_kernel and top_kernel make them.
+struct PlaneJobs {
+  PlanesParams p{};
+  const LossWs& ws;
+  bool any = false, scaled = false;
+
+  PlaneJobs(const metis_loss& l, const LossWs& w) : ws(w) {
+    p.targets = l.targets, p.targets64 = l.target_bits == 64, p.vocab = l.vocab, p.ignore = l.ignore_index;
+  }
+  static int blocks_for(int64_t blocks_of_8, int most) {
+    return (int)std::min<int64_t>(std::max<int64_t>(ceil_div<int64_t>(blocks_of_8, 1024), 1), most);
+  }
+  // `half`: binary16 planes, `masked`: rows up to a multiple of 64 and zeros in
+  // those of tokens that the loss leaves out
+  Planes rows(int at, const void* src, int32_t dt, int64_t ld, int64_t rows, int64_t cols, int planes, uint16_t* dst, bool half,
+              bool masked) {
+    PlanesJob& j = p.job[at];
+    const int64_t pitch = pad64(cols), out_rows = masked ? pad64(rows) : rows;
+    j = PlanesJob{};
+    j.src = src, j.rows = rows, j.cols = cols, j.ld = ld;
+    j.bf16 = dt == METIS_BF16, j.masked = masked;
+    j.dst = dst, j.out_rows = out_rows, j.pitch = pitch, j.plane = planes > 1 ? out_rows * pitch : 0;
+    j.blocks = blocks_for(out_rows * (pitch / 8), 4096);
+    if (half) top_of(at, src, rows * ceil_div<int64_t>(cols, 8));
+    any = true;
+    return {(const uint8_t*)dst, pitch * 2, out_rows * pitch * 2, planes, j.shift};
+  }
+  const int* gradients(const float* grad, const float* count, int64_t tokens, bool each) {
+    PlanesJob& j = p.job[2];
+    j = PlanesJob{};
+    j.rows = each ? tokens : 1, j.cols = j.ld = 1, j.masked = each, j.count = count;
+    j.blocks = 1;
+    top_of(2, grad, j.rows);
+    return j.shift;
+  }
+  metis_status run(hipStream_t st) {
+    if (!any) return METIS_OK;
+    if (scaled) {
+      hipLaunchKernelGGL(top_kernel, dim3(p.job[0].top_blocks + p.job[1].top_blocks + p.job[2].top_blocks), dim3(256), 0, st, p);
+      LAUNCH_CHECK();
+    }
+    hipLaunchKernelGGL(planes_kernel, dim3(p.job[0].blocks + p.job[1].blocks + p.job[2].blocks), dim3(256), 0, st, p);
+    LAUNCH_CHECK();
     return METIS_OK;
   }
-  PlanesParams p{src, rows, cols, ld, dt == METIS_BF16, vec_rows(src, dt, ld, rows), dst, out_rows, pitch,
-                 planes > 1 ? out_rows * pitch : 0, nullptr, 0, 0, 0};
-  if (mask) p.targets = mask->targets, p.targets64 = mask->target_bits == 64, p.vocab = mask->vocab, p.ignore = mask->ignore_index;
-  hipLaunchKernelGGL(planes_kernel, dim3(grid_for(out_rows * (pitch / 8), 256)), dim3(256), 0, st, p);
-  LAUNCH_CHECK();
-  *out = {(const uint8_t*)dst, pitch * 2, out_rows * pitch * 2, planes};
-  return METIS_OK;
+
+ private:
+  void top_of(int at, const void* values, int64_t blocks_of_8) {
+    PlanesJob& j = p.job[at];
+    if (!j.masked && j.ld == j.cols) j.flat = 1;
+    j.values = values, j.top = ws.top + at * kTopBlocks, j.top_blocks = blocks_for(blocks_of_8, kTopBlocks), j.shift = ws.shift + at;
+    scaled = true;
+  }
+};
+
+// rows that are an operand as they lie in memory
+Planes as_is(const void* src, int64_t ld, int64_t rows, int64_t cols) {
+  return {(const uint8_t*)src, rows > 1 ? ld * 2 : cols * 2, 0, 1, nullptr};
 }
 
 // the operands and the products of their planes; `all`: with the low planes
@@ -241,6 +291,7 @@ BfGemmParams product(const Planes& a, int64_t M, const Planes& b, int64_t N, int
   g.a = a.at, g.b = b.at;
   g.pitch_a = a.pitch, g.pitch_b = b.pitch;
   g.run_stages = (int)(pad64(K) / 64);
+  g.shift_a = a.shift, g.shift_b = b.shift;
   g.splits = 1;
   g.runs = 1;
   if (all && b.count > 1) g.at_b[g.runs++] = b.plane;
@@ -251,6 +302,21 @@ BfGemmParams product(const Planes& a, int64_t M, const Planes& b, int64_t N, int
 metis_status run_product(const BfGemmParams& g, BfOut out, hipStream_t st) {
   const hipError_t e = launch_bf_gemm(g, out, st);
   return e == hipSuccess ? METIS_OK : fail(METIS_E_HIP, "product launch: %s", hipGetErrorString(e));
+}
+
+// C (+)= the sum of the splits (add: to a binary32 C)
+metis_status join_splits(const float* part, int splits, int64_t rows, int64_t cols, void* C, bool bf16, int64_t ldc, bool add,
+                         hipStream_t st) {
+  const bool four = cols % 4 == 0 && vec_rows(C, bf16 ? METIS_BF16 : METIS_F32, ldc, rows);
+  const int64_t n = rows * cols;
+  if (four)
+    hipLaunchKernelGGL(split_join_kernel<4>, dim3(grid_for(n / 4, 256)), dim3(256), 0, st, part, splits, n, rows, cols, C, (int)bf16,
+                       ldc, (int)add);
+  else
+    hipLaunchKernelGGL(split_join_kernel<1>, dim3(grid_for(n, 256)), dim3(256), 0, st, part, splits, n, rows, cols, C, (int)bf16, ldc,
+                       (int)add);
+  LAUNCH_CHECK();
+  return METIS_OK;
 }
 
 void set_targets(BfGemmParams& g, const metis_loss& l, int64_t v0) {
@@ -488,13 +554,17 @@ metis_status metis_cross_entropy_fwd(const metis_loss* l, float* losses, float* 
     Carver cv(ws, ws_bytes);
     const LossWs w = carve_loss(cv, *l, p, false);
     Planes x, v;
-    TRY(as_operand(l->x, l->x_dtype, l->ldx, p.N, p.D, p.x_as_is, p.xp, w.x, nullptr, &x, st));
     // a weight that needs no copies goes through in one piece
     // (as long as its tiles can be counted in 32 bits)
     const int64_t piece = p.w_as_is && ceil_div<int64_t>(p.N, 64) * ceil_div<int64_t>(p.V, 128) < 1 << 30 ? p.V : p.piece;
     for (int64_t v0 = 0; v0 < p.V; v0 += piece) {
       const int64_t n = std::min(piece, p.V - v0);
-      TRY(as_operand(rows_from(l->w, l->w_dtype, l->ldw, v0), l->w_dtype, l->ldw, n, p.D, p.w_as_is, p.wp, w.w, nullptr, &v, st));
+      PlaneJobs jobs(*l, w);
+      if (v0 == 0)
+        x = p.x_as_is ? as_is(l->x, l->ldx, p.N, p.D) : jobs.rows(0, l->x, l->x_dtype, l->ldx, p.N, p.D, p.xp, w.x, p.pair, false);
+      const void* wv = rows_from(l->w, l->w_dtype, l->ldw, v0);
+      v = p.w_as_is ? as_is(wv, l->ldw, n, p.D) : jobs.rows(1, wv, l->w_dtype, l->ldw, n, p.D, p.wp, w.w, p.pair, false);
+      TRY(jobs.run(st));
       BfGemmParams g = product(x, p.N, v, n, p.D, true);
       set_targets(g, *l, v0);
       g.stat = w.stat, g.target_logit = w.target;
@@ -536,20 +606,27 @@ metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, cons
   TRY(ensure_device_tables());
   Carver cv(ws, ws_bytes);
   const LossWs w = carve_loss(cv, *l, p, true);
-  Planes x, v;
-  TRY(as_operand(l->x, l->x_dtype, l->ldx, p.N, p.D, p.x_as_is, p.xp, w.x, l, &x, st));
+  Planes x;
+  const int* shift_p = nullptr;
   const bool dx_f32 = l->x_dtype == METIS_F32;
   const bool one = p.piece >= p.V;
   for (int64_t v0 = 0; v0 < p.V; v0 += p.piece) {
     const int64_t n = std::min(p.piece, p.V - v0), np = pad64(n);
     const void* wv = rows_from(l->w, l->w_dtype, l->ldw, v0);
-    TRY(as_operand(wv, l->w_dtype, l->ldw, n, p.D, p.w_as_is, p.wp, w.w, nullptr, &v, st));
+    PlaneJobs jobs(*l, w);
+    if (v0 == 0) {
+      x = jobs.rows(0, l->x, l->x_dtype, l->ldx, p.N, p.D, p.xp, w.x, true, true);
+      shift_p = jobs.gradients(grad, count, p.N, grad_each != 0);
+    }
+    const Planes v = jobs.rows(1, wv, l->w_dtype, l->ldw, n, p.D, p.wp, w.w, true, false);
+    TRY(jobs.run(st));
     BfGemmParams g = product(x, p.N, v, n, p.D, true);
     set_targets(g, *l, v0);
     g.lse = lse, g.grad = grad, g.count = count, g.grad_each = grad_each;
     g.prob = w.p, g.ldp = np, g.lo_plane = p.pair ? p.Np * np : 0;
+    g.shift_p = shift_p;
     TRY(run_product(g, kBfProb, st));
-    const Planes pr{(const uint8_t*)w.p, np * 2, p.Np * np * 2, p.pair ? 2 : 1};
+    const Planes pr{(const uint8_t*)w.p, np * 2, p.Np * np * 2, p.pair ? 2 : 1, shift_p};
     if (dX) {
       g = product(pr, p.N, v, p.D, n, dx_f32);
       g.rows_b = n;
@@ -562,9 +639,7 @@ metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, cons
         g.splits = splits;
         g.C = w.part, g.ldc = p.D, g.split_ld = p.N * p.D;
         TRY(run_product(g, kBfF32, st));
-        hipLaunchKernelGGL(split_join_kernel, dim3(grid_for(p.N * p.D, 256)), dim3(256), 0, st, (const float*)w.part, splits,
-                           p.N * p.D, p.N, p.D, direct ? dX : sum, (int)direct, direct ? lddx : ld, (int)(v0 > 0));
-        LAUNCH_CHECK();
+        TRY(join_splits(w.part, splits, p.N, p.D, direct ? dX : sum, direct, direct ? lddx : ld, v0 > 0, st));
       } else {
         g.C = direct ? dX : sum, g.ldc = direct ? lddx : ld;
         g.add = v0 > 0;
@@ -579,9 +654,7 @@ metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, cons
     }
   }
   if (dX && !dx_f32 && !one) {
-    hipLaunchKernelGGL(split_join_kernel, dim3(grid_for(p.N * p.D, 256)), dim3(256), 0, st, (const float*)w.dx, 1, (int64_t)0,
-                       p.N, p.D, dX, 1, lddx, 0);
-    LAUNCH_CHECK();
+    TRY(join_splits(w.dx, 1, p.N, p.D, dX, true, lddx, false, st));
   }
   return METIS_OK;
 }

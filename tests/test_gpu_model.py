@@ -250,22 +250,25 @@ def _loss_limits(X, W, T, up, xt, wt):
     use = (T >= 0) & (T < len(W))
     losses, lse, p = model.cross_entropy(X, W, T, -100)
     pair = F in (xt, wt)
-    # logits: sums of cols products.  bf16 has 8 significant bits, so the high
-    # part of a binary32 operand is off by 2^-8 of it at most, and the low part,
-    # the rest rounded, by 2^-8 of the rest: the pair by 2^-16.  A product of
-    # two pairs is off by that twice and by low times low, 2^-8 2^-8, left out:
-    # 3 2^-16.
-    size = np.abs(np.where(use[:, None], X, 0)) @ np.abs(W).T
-    dl = size * (X.shape[1] * U + (3 * 2.0 ** -16 if pair else 0))
+    # logits: sums of cols products.  binary16 has 11 significant bits, so the
+    # high part of a binary32 operand is off by 2^-11 of it at most, and the low
+    # part, the rest rounded, by 2^-11 of the rest: the pair by 2^-22.  A product
+    # of two pairs is off by that twice and by low times low, 2^-11 2^-11, left
+    # out: 3 2^-22.  Below its normal range binary16 is off by 2^-25, where the
+    # operand's largest value is 2^14 or more: 2^-39 of that.
+    XU = np.where(use[:, None], X, 0)
+    size = np.abs(XU) @ np.abs(W).T
+    small = 2.0 ** -39 * 2 * X.shape[1] * np.abs(XU).max() * np.abs(W).max()
+    dl = size * (X.shape[1] * U + (3 * 2.0 ** -22 if pair else 0)) + small
     at = np.where(use, T, 0)
     # log-sum-exp: the worst logit error, the sums' depth (64 values, then
     # blocks of 64 words in four parts), exponentials and logarithm
     dlse = dl.max(axis=1) + (64 + len(W) / 256 + 16) * 2 * U + 8 * U * (np.abs(lse) + size.max(axis=1))
     dloss = dlse + dl[np.arange(len(T)), at] + U * np.abs(lse)
     soft = np.abs(np.where(np.arange(len(W)) == at[:, None], p + 1, p)) * use[:, None]
-    step = 2.0 ** -16 if pair else 2.0 ** -8  # P as a pair, or rounded to bf16
+    step = 2.0 ** -22 if pair else 2.0 ** -11  # P as a pair, or rounded to binary16
     G = np.abs(up)[:, None]
-    dp = G * (soft * (dl + dlse[:, None] + 16 * U * (1 + size)) + 4 * U * (soft + np.abs(p))) + (step + 2 * U) * np.abs(p) * G
+    dp = G * (soft * (dl + dlse[:, None] + 16 * U * (1 + size)) + 4 * U * (soft + np.abs(p))) + (step + 2 * U) * np.abs(p) * G + 2.0 ** -39 * G.max()
     return losses, lse, dloss, dlse, p * up[:, None], dp * use[:, None]
 
 
@@ -298,16 +301,18 @@ def test_cross_entropy_matches_the_oracle(tokens, vocab, cols, xt, wt, bits):
     near(summed[0], np.array(rl.sum()), (dloss * use).sum() + 2 * U * abs(rl.sum()), "sum")
 
     def grads(dx, dw, P, dP, what):
-        # the gradients' other operand: bf16 as it is; binary32 as a pair (2^-16,
-        # and as much for low times low), or rounded to bf16 (2^-8) where the
-        # gradient itself is bf16
-        ow = 0.0 if wt == BF else (2.0 ** -15 if xt == F else 2.0 ** -8)
-        ox = 0.0 if xt == BF else (2.0 ** -15 if wt == F else 2.0 ** -8)
+        # the gradients' other operand: bf16 as it is; binary32 as a pair (2^-22,
+        # and as much for low times low), or rounded to binary16 (2^-11) where
+        # the gradient itself is bf16; 2^-39 of the largest value is added for
+        # what lies below binary16's normal range
+        ow = 0.0 if wt == BF else (2.0 ** -21 if xt == F else 2.0 ** -11)
+        ox = 0.0 if xt == BF else (2.0 ** -21 if wt == F else 2.0 ** -11)
         sx = np.abs(P) + dP
-        extra = 2.0 ** -8 if F in (xt, wt) else 0.0  # the high part of P alone, for a bf16 gradient
-        near(dx, P @ W, dP @ np.abs(W) + sx @ np.abs(W) * (vocab * U + ow + (extra if xt == BF else 0)), what + " dx")
+        dP = dP + 2.0 ** -39 * np.abs(P).max()
+        extra = 2.0 ** -11 if F in (xt, wt) else 0.0  # the high part of P alone, for a bf16 gradient
+        near(dx, P @ W, dP @ np.abs(W) + 2.0 ** -39 * np.abs(W).max() * sx.sum(1, keepdims=True) + sx @ np.abs(W) * (vocab * U + ow + (extra if xt == BF else 0)), what + " dx")
         XX = np.where(use[:, None], X, 0)
-        near(dw, P.T @ XX, dP.T @ np.abs(XX) + sx.T @ np.abs(XX) * (tokens * U + ox + (extra if wt == BF else 0)), what + " dw")
+        near(dw, P.T @ XX, dP.T @ np.abs(XX) + 2.0 ** -39 * np.abs(XX).max() * sx.sum(0)[:, None] + sx.T @ np.abs(XX) * (tokens * U + ox + (extra if wt == BF else 0)), what + " dw")
 
     dx, dw = metis.cross_entropy_bwd(x, w, t32, lse, up)
     grads(dx, dw, P, dP, "each")
@@ -342,9 +347,52 @@ def test_cross_entropy_in_several_pieces():
     one = torch.ones((), device="cuda")
     dx, dw = metis.cross_entropy_bwd(x, w, t, lse, one, total[1])
     sx, sw = p.abs() @ w.double().abs(), p.abs().T @ x.double().abs()
-    rel = 2.0 ** -8 + 64 * 2.0 ** -20  # P's rounding, and its own error (logits here below 64 in size)
+    rel = 2.0 ** -11 + 64 * 2.0 ** -20  # P's rounding, and its own error (logits here below 64 in size)
     assert ((dx - p @ w.double()).abs() <= sx * (rel + v / 8 * U) + 2.0 ** -8 * (p @ w.double()).abs()).all()
     assert ((dw - p.T @ x.double()).abs() <= sw * (rel + n * U) + 2.0 ** -8 * (p.T @ x.double()).abs()).all()
+
+
+@pytest.mark.parametrize("xs,ws,us", [(0, 0, 0), (60, -60, 0), (-70, 69, 40), (-120, 118, -90), (40, -41, 100)])
+@pytest.mark.parametrize("xt,wt", [(BF, BF), (F, F), (F, BF)])
+def test_cross_entropy_over_the_exponents(xt, wt, xs, ws, us):
+    """Operands and gradients of any size, in rows of sizes far apart: the planes' scale follows the largest value."""
+    say("cross entropy of x 2^%d, w 2^%d, gradients 2^%d %s %s" % (xs, ws, us, xt, wt))
+    tokens, vocab, cols = 70, 200, 96
+    g = torch.Generator(device="cuda").manual_seed(xs + 200)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x = (rnd(tokens, cols) * 2.0 ** xs).to(xt)
+    x[1::7] *= 2.0 ** -12
+    w = (rnd(vocab, cols) * 2.0 ** ws / cols ** 0.5).to(wt)
+    w[3::5] *= 2.0 ** -10
+    w[4] = 0
+    t = torch.randint(0, vocab, (tokens,), generator=g, device="cuda")
+    t[5] = -100
+    x[5] = float("nan")
+    up = rnd(tokens) * 2.0 ** us
+    up[::9] *= 2.0 ** -9
+    X, W, T = np.nan_to_num(f64(x)), f64(w), t.cpu().numpy()
+    use = T != -100
+    rl, rlse, dloss, dlse, P, dP = _loss_limits(X, W, T, f64(up), xt, wt)
+    losses, lse, _ = metis.cross_entropy(x, w, t)
+    near(losses, np.where(use, rl, 0), dloss * use, "losses")
+    dx, dw = metis.cross_entropy_bwd(x, w, t, lse, up)
+    XX = np.where(use[:, None], X, 0)
+    P, dP = np.where(use[:, None], P, 0), np.where(use[:, None], dP, 0)
+    ow = 2.0 ** -21 if wt == F else 0.0
+    ox = 0.0 if xt == BF else 2.0 ** -21 if wt == F else 2.0 ** -11
+    extra = 2.0 ** -11 if F in (xt, wt) and wt == BF else 0.0  # the high part of P alone
+    sx = np.abs(P) + dP
+    dP = dP + 2.0 ** -39 * np.abs(P).max()
+    near(dx, P @ W, dP @ np.abs(W) + sx @ np.abs(W) * (vocab * U + ow) + 2.0 ** -39 * np.abs(W).max() * sx.sum(1, keepdims=True), "dx")
+    want, tol = P.T @ XX, dP.T @ np.abs(XX) + sx.T @ np.abs(XX) * (tokens * U + ox + extra) + 2.0 ** -39 * np.abs(XX).max() * sx.sum(0)[:, None]
+    # gradients of 2^100 times an x of 2^40 lie beyond the type's largest value, 2^128: infinities of their sign
+    beyond = np.abs(want) - tol >= 2.0 ** 128
+    got = f64(dw)
+    assert (got[beyond] == np.sign(want[beyond]) * np.inf).all()
+    sure = np.abs(want) + tol < torch.finfo(wt).max
+    assert sure.all() or us + xs >= 120
+    near(dw[torch.from_numpy(sure).cuda()], want[sure], tol[sure], "dw")
+    metis.status_sync()
 
 
 def test_cross_entropy_leaves_tokens_out():
