@@ -499,10 +499,14 @@ metis_status metis_grad_norm(const metis_adamw_tensor *tensors, int64_t count, d
  * 1) or grad[0] for all (grad_each = 0), divided by *count where count is not
  * NULL (total + 1 of the forward pass, for the mean).  Logits are formed again
  * in pieces of the vocabulary, so the workspace does not grow with it.
- * bf16 operands enter the products as they are; binary32 operands as two bf16
- * parts (relative error at most 2^-16) where a loss or a binary32 gradient
- * needs both.  Probabilities are rounded to bf16 (two parts for a binary32
- * gradient) before the products of the gradients.
+ * The forward product takes two bf16 operands as they are.  Every other
+ * operand becomes binary16 under a common power of two that brings its largest
+ * finite value (of the tokens that have a target) into [2^14, 2^15): one value
+ * for bf16, two for binary32 where a loss or a binary32 gradient needs both;
+ * so do the gradients of the logits, two values where a gradient is binary32.
+ * One value is off by 2^-11 of itself at most (a bf16 operand by nothing), two
+ * by 2^-22, and either by 2^-40 of its operand's largest value.
+ * lse of a token that is left out is any value.
  * ws holds metis_cross_entropy_workspace(l, backward) bytes, 256-byte aligned.
  * tokens, cols <= 2^22, vocab < 2^31 (METIS_E_UNSUPPORTED above). */
 metis_status metis_layernorm_fwd(const void *X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ldx,

@@ -163,6 +163,8 @@ struct LayerNode : torch::autograd::Node {
     if (at::GradMode::is_enabled() && dy[0].requires_grad()) {
       auto refused = std::make_shared<torch::autograd::DelayedError>(
           "trying to differentiate twice a function whose gradient cannot be differentiated", (int64_t)out.size());
+      for (Tensor& t : out)  // the error stands behind outputs that require a gradient
+        if (t.defined()) t = t.detach().requires_grad_(true);
       return (*refused)(std::move(out));
     }
     return out;

@@ -141,13 +141,14 @@ bool operand_as_is(const void* p, int32_t dt, int64_t ld, int64_t rows, int64_t 
 
 int64_t pad64(int64_t n) { return round_up64(n, 64); }
 
-// Words of one piece: at most about 2^28 probabilities (512 MB), and where
+// Words of one piece: at most about 2^28 probabilities (512 MB) and 2^22 words
+// (the product counts the bytes of 256 rows of P in 32 bits), and where
 // they allow it a number whose dw = P^T x fills whole rounds of the chip's 256
 // CUs with tiles of 256 x 256 (50257 words, 768 features, 8192 tokens: dw in
 // three pieces of 21760 and the rest, not in two of 25152, which take two
 // rounds of tiles each).
 int64_t loss_piece(int64_t tokens, int64_t vocab, int64_t cols) {
-  const int64_t most = std::max<int64_t>(((int64_t)1 << 28) / std::max<int64_t>(tokens, 1), 4096);
+  const int64_t most = std::min<int64_t>(std::max<int64_t>(((int64_t)1 << 28) / std::max<int64_t>(tokens, 1), 4096), 1 << 22);
   const int64_t round = std::max<int64_t>(256 / ceil_div<int64_t>(cols, 256), 1) * 256;
   return round <= most ? most / round * round : most / 256 * 256;
 }
@@ -495,16 +496,25 @@ metis_status metis_embedding_bwd(const void* dY, int32_t y_dtype, int64_t tokens
     p.tile = kEmbedTile * ceil_div<int64_t>(tokens, (int64_t)kEmbedTile * kEmbedTiles);
     p.tiles = (int)ceil_div<int64_t>(tokens, p.tile);
     p.status = device_status();
-    int to = 0;
-    for (p.shift = 0; p.shift == 0 || vocab >> p.shift; p.shift += kEmbedBits, to ^= 1) {  // keys go up to vocab
-      p.first = p.shift == 0;
-      p.key = w.key[to ^ 1], p.pos = w.pos[to ^ 1];
-      p.key_to = w.key[to], p.pos_to = w.pos[to];
-      hipLaunchKernelGGL(embed_hist_kernel, dim3((unsigned)p.tiles), dim3(kEmbedTile), 0, st, p);
-      hipLaunchKernelGGL(embed_scatter_kernel, dim3((unsigned)p.tiles), dim3(kEmbedTile), 0, st, p);
+    int at = 0;  // where the sorted tokens lie
+    if (tokens <= kEmbedTile) {
+      p.first = 1;
+      p.key_to = w.key[0], p.pos_to = w.pos[0];
+      hipLaunchKernelGGL(embed_sort_kernel, dim3(1), dim3(kEmbedTile), 0, st, p);
       LAUNCH_CHECK();
+    } else {
+      at = 1;
+      for (p.shift = 0; p.shift == 0 || vocab >> p.shift; p.shift += kEmbedBits) {  // keys go up to vocab
+        p.first = p.shift == 0;
+        p.key = w.key[at], p.pos = w.pos[at];
+        at ^= 1;
+        p.key_to = w.key[at], p.pos_to = w.pos[at];
+        hipLaunchKernelGGL(embed_hist_kernel, dim3((unsigned)p.tiles), dim3(kEmbedTile), 0, st, p);
+        hipLaunchKernelGGL(embed_scatter_kernel, dim3((unsigned)p.tiles), dim3(kEmbedTile), 0, st, p);
+        LAUNCH_CHECK();
+      }
     }
-    s.key = w.key[to ^ 1], s.pos = w.pos[to ^ 1];
+    s.key = w.key[at], s.pos = w.pos[at];
   }
   s.tokens = tokens, s.vocab = vocab, s.cols = cols, s.lddy = lddy, s.lddw = lddw;
   s.dy = dY, s.dw = dW;
@@ -561,7 +571,7 @@ metis_status metis_cross_entropy_fwd(const metis_loss* l, float* losses, float* 
       const int64_t n = std::min(piece, p.V - v0);
       PlaneJobs jobs(*l, w);
       if (v0 == 0)
-        x = p.x_as_is ? as_is(l->x, l->ldx, p.N, p.D) : jobs.rows(0, l->x, l->x_dtype, l->ldx, p.N, p.D, p.xp, w.x, p.pair, false);
+        x = p.x_as_is ? as_is(l->x, l->ldx, p.N, p.D) : jobs.rows(0, l->x, l->x_dtype, l->ldx, p.N, p.D, p.xp, w.x, p.pair, p.pair);
       const void* wv = rows_from(l->w, l->w_dtype, l->ldw, v0);
       v = p.w_as_is ? as_is(wv, l->ldw, n, p.D) : jobs.rows(1, wv, l->w_dtype, l->ldw, n, p.D, p.wp, w.w, p.pair, false);
       TRY(jobs.run(st));

@@ -192,7 +192,7 @@ def test_dropout_step_on_the_gpu_and_far_elements():
 
 # --------------------------------------------------------------- embedding --
 
-@pytest.mark.parametrize("tokens,vocab,cols", [(1, 1, 1), (3, 5, 7), (16, 3, 8), (17, 600, 65), (1000, 10, 64), (1025, 70000, 20), (5000, 513, 770),
+@pytest.mark.parametrize("tokens,vocab,cols", [(1, 1, 1), (3, 5, 7), (16, 3, 8), (17, 600, 65), (1000, 10, 64), (1023, 300000, 8), (1024, 511, 8), (1024, 512, 12), (1025, 70000, 20), (5000, 513, 770),
                                                (300, 300000, 8), (40000, 50257, 16)])
 @pytest.mark.parametrize("wt,yt,bits", [(BF, BF, 64), (F, F, 32), (F, BF, 64), (BF, F, 32)])
 def test_embedding_matches_the_oracle(tokens, vocab, cols, wt, yt, bits):
@@ -408,6 +408,7 @@ def test_cross_entropy_leaves_tokens_out():
         dx, dw = metis.cross_entropy_bwd(x, w, t, lse, one, total[1])
         y = x.clone()
         y[5], y[60] = float("nan"), float("inf")
+        y[5, 1], y[60, 2] = 1e30, -1e30
         l2, lse2, total2 = metis.cross_entropy(y, w, t)
         dx2, dw2 = metis.cross_entropy_bwd(y, w, t, lse2, one, total2[1])
         assert torch.equal(losses, l2) and torch.equal(total, total2) and torch.equal(dx, dx2) and torch.equal(dw, dw2)
@@ -568,6 +569,183 @@ def test_capture_next_to_a_living_eager_graph_is_refused():
                 run()
     del keep, held
     torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits():
+    say("tables, rows and vocabularies past 2^32 bytes")
+    g = torch.Generator(device="cuda").manual_seed(12)
+    rows, cols = 140000, 16384  # 4.6 GB of bf16, 2.3e9 values
+    big = torch.zeros(rows, cols, dtype=BF, device="cuda")
+    some = torch.tensor([0, 65535, 131071, 131072, 139999], device="cuda")
+    big[some] = torch.randn(5, cols, generator=g, device="cuda").to(BF)
+    part = big[some]
+    ids = some[[4, 0, 3, 4, 2, 1]]
+    assert torch.equal(metis.embedding(big, ids), big[ids])
+    dy = torch.randn(6, cols, generator=g, device="cuda").to(BF)
+    dw = metis.embedding_bwd(dy, ids, rows)
+    near(dw[139999], f64(dy[0]) + f64(dy[3]), 4 * U * (np.abs(f64(dy[0])) + np.abs(f64(dy[3]))), "the last row")
+    assert torch.equal(dw[131072], dy[2]) and torch.equal(dw[0], dy[1]) and not dw[139998].any() and not dw[131070].any()
+    del dw
+    y, mean, rstd = metis.layernorm(big)
+    assert torch.equal(y[some], metis.layernorm(part)[0])
+    dx = metis.layernorm_bwd(big, big, mean, rstd, want_dweight=False, want_dbias=False)[0]
+    assert torch.equal(dx[some], metis.layernorm_bwd(part, part, mean[some], rstd[some], want_dweight=False, want_dbias=False)[0])
+    del dx
+    # the draws of a value follow from its place: those of the first rows again, and every row's share
+    y = metis.dropout(big.fill_(1), 0.25, seed=3, Y=y)
+    assert torch.equal(y[:100], metis.dropout(big[:100], 0.25, seed=3))
+    kept = (y[some] != 0).double().mean(1)
+    assert ((kept - 0.75).abs() < 6 * (0.25 * 0.75 / cols) ** 0.5).all()
+    assert not torch.equal(y[131072 + 65536 // 16384], y[65536 // 16384])
+    del y
+    big.normal_(generator=g)
+    x = torch.randn(3, cols, generator=g, device="cuda").to(BF) / cols ** 0.5
+    t = torch.tensor([139999, 0, 131073], device="cuda")
+    losses, lse, _ = metis.cross_entropy(x, big, t)
+    z = torch.cat([x.double() @ big[i:i + 10000].double().T for i in range(0, rows, 10000)], 1)
+    want = torch.logsumexp(z, 1) - z.gather(1, t[:, None])[:, 0]
+    # each logit is a sum of 16384 products, |x| |w| below 128 in all
+    assert ((losses - want).abs() <= 128 * cols * U + 1e-4).all()
+    up = torch.ones(3, device="cuda")
+    dx, dw = metis.cross_entropy_bwd(x, big, t, lse, up)
+    p = torch.softmax(z, 1)
+    p[torch.arange(3), t] -= 1
+    for v in (0, 1, 131071, 131073, 139999):
+        row = p[:, v] @ x.double()
+        size = p[:, v].abs() @ x.double().abs()
+        # P: rounded to binary16, and off by what the logits and the log-sum-exp are
+        assert ((dw[v].double() - row).abs() <= 2.0 ** -8 * row.abs() + size * (2.0 ** -11 + 3 * 128 * cols * U)).all(), v
+    metis.status_sync()
+
+
+def test_more_words_than_rows_of_probabilities_may_hold():
+    say("cross entropy over 9000001 words")
+    g = torch.Generator(device="cuda").manual_seed(13)
+    n, v = 3, 9000001
+    x = torch.randn(n, 2, generator=g, device="cuda").to(BF)
+    w = torch.randn(v, 2, generator=g, device="cuda").to(BF)
+    t = torch.tensor([v - 1, 1 << 22, 17], device="cuda")
+    losses, lse, _ = metis.cross_entropy(x, w, t)
+    z = x.double() @ w.double().T
+    rlse = torch.logsumexp(z, 1)
+    assert ((lse - rlse).abs() <= (64 + v / 4096 + 16) * 2 * U + 32 * U).all()  # sums of 64, 1 / 64 of the blocks in a row, then joined
+    dx, dw = metis.cross_entropy_bwd(x, w, t, lse, torch.ones(n, device="cuda"))
+    p = torch.exp(z - rlse[:, None])
+    p[torch.arange(n), t] -= 1
+    want, size = p @ w.double(), p.abs() @ w.double().abs()
+    # P rounded to binary16 (or off by 2^-25 of what 2^15 stands for), sums over words in parts and pieces
+    tiny = 2.0 ** -39 * w.double().abs().sum(0)
+    assert ((dx - want).abs() <= 2.0 ** -8 * want.abs() + size * (2.0 ** -11 + 1e-3) + tiny).all()
+    want, size = p.T @ x.double(), p.abs().T @ x.double().abs()
+    assert ((dw - want).abs() <= 2.0 ** -8 * want.abs() + size * (2.0 ** -11 + 1e-3) + 2.0 ** -39 * x.double().abs().sum(0)).all()
+    metis.status_sync()
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+def test_each_layer_in_a_graph_replayed_between_eager_work(dt):
+    say("each layer captured alone, replayed with eager passes between, %s" % dt)
+    g = torch.Generator(device="cuda").manual_seed(14)
+    n, c, v = 70, 96, 301
+    ln, em = LayerNorm(c), Embedding(v, c, padding_idx=3, out_dtype=dt)
+    drop = Dropout(0.3, seed=5)
+    heads = [LinearCrossEntropy(c, v, reduction=r, dtype=dt) for r in ("none", "sum", "mean")]
+    set_step(drop, 0)
+    x = torch.randn(n, c, generator=g, device="cuda").to(dt).requires_grad_(True)
+    res = torch.randn(n, c, generator=g, device="cuda").to(dt).requires_grad_(True)
+    ids = torch.randint(0, v, (n,), generator=g, device="cuda")
+    runs = [(lambda: ln(x), [x, ln.weight, ln.bias]), (lambda: drop(x, res), [x, res]), (lambda: em(ids), [em.weight])]
+    runs += [(lambda h=h: h(x, ids), [x, h.weight]) for h in heads]
+    for run, leaves in runs:
+        y = run()
+        up = torch.randn(y.shape, generator=g, device="cuda").to(y.dtype)
+        torch.autograd.grad(y, leaves, up)
+        del y
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = run()
+            grads = torch.autograd.grad(y, leaves, up)
+        y = y.detach()
+        for step in (1, 2, 3):
+            with torch.no_grad():
+                x.copy_(torch.randn(n, c, generator=g, device="cuda"))
+                ids.copy_(torch.randint(0, v, (n,), generator=g, device="cuda"))
+                ids[step::7] = -100 if leaves[-1] is not em.weight else 3
+                up.copy_(torch.randn(up.shape, generator=g, device="cuda"))
+            set_step(drop, step)
+            graph.replay()
+            torch.cuda.synchronize()
+            kept = [y.clone()] + [q.clone() for q in grads]
+            want = run()
+            eager = torch.autograd.grad(want, leaves, up)
+            assert all(torch.equal(a, b) for a, b in zip(kept, [want.detach(), *eager]))
+            del want
+    with pytest.raises(metis.MetisError):  # the embedding's first pass met the numbers -100 that dropout's passes left
+        metis.status_sync()
+    metis.status_sync()
+
+
+def test_what_autograd_may_ask_of_the_layers():
+    say("layers: a graph kept and used again, inputs changed in place, second derivatives, a loss scaled in place")
+    n, c, v = 20, 64, 51
+    ln, em, head, drop = LayerNorm(c), Embedding(v, c), LinearCrossEntropy(c, v), Dropout(0.5)
+    x = torch.randn(n, c, device="cuda", requires_grad=True)
+    ids = torch.randint(0, v, (n,), device="cuda")
+    for run, leaves in ((lambda: ln(x), [x, ln.weight]), (lambda: drop(x), [x]), (lambda: em(ids), [em.weight]), (lambda: head(x, ids), [x, head.weight])):
+        y = run()
+        up = torch.ones_like(y)
+        a = torch.autograd.grad(y, leaves, up, retain_graph=True)
+        b = torch.autograd.grad(y, leaves, up)
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    for run in (lambda: ln(x), lambda: em(ids), lambda: head(x, ids)):
+        y = run()
+        y.sum().backward()
+        with pytest.raises(RuntimeError):
+            y.sum().backward()  # what the pass kept is gone
+    y = ln(x * 1)
+    up = torch.ones_like(y, requires_grad=True)
+    (first,) = torch.autograd.grad(y, x, up, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate"):
+        first.sum().backward()
+    for run in (lambda q: ln(q), lambda q: head(q, ids)):
+        q = x * 1
+        y = run(q)
+        q += 1
+        with pytest.raises(RuntimeError, match="modified"):
+            y.sum().backward()
+    # a loss divided in place, as by the number of micro-batches
+    x.grad = None
+    want = torch.autograd.grad(head(x, ids) / 4, [x, head.weight])
+    loss = head(x, ids)
+    loss /= 4
+    assert all(torch.equal(p, q) for p, q in zip(torch.autograd.grad(loss, [x, head.weight]), want))
+    metis.status_sync()
+
+
+def test_two_streams_at_once():
+    say("the loss and the embedding on two streams at once")
+    g = torch.Generator(device="cuda").manual_seed(15)
+    x = [torch.randn(700, 128, generator=g, device="cuda").to(dt) for dt in (BF, F)]
+    w = [torch.randn(5000, 128, generator=g, device="cuda").to(dt) for dt in (BF, F)]
+    t = torch.randint(0, 5000, (700,), generator=g, device="cuda")
+    one = torch.ones((), device="cuda")
+
+    def run(i):
+        losses, lse, total = metis.cross_entropy(x[i], w[i], t)
+        dx, dw = metis.cross_entropy_bwd(x[i], w[i], t, lse, one, total[1])
+        return [losses, total, dx, dw, metis.embedding_bwd(x[i], t, 5000)]
+    want = [run(0), run(1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(i))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(a, b) for once in got[i] for a, b in zip(once, want[i]))
+    metis.status_sync()
 
 
 def test_layers_on_another_stream_and_without_gradients():
