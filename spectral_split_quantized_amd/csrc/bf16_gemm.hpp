@@ -153,17 +153,21 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
   const int stages = p.runs * p.run_stages;
 
   // Workgroups go round the 8 XCDs; each XCD takes a contiguous run of tiles,
-  // in groups of 8 tile rows, so that its CUs share rows of both operands in
-  // its L2; the splits of one tile follow each other.  Sequence number q ->
-  // first row and column and the split, or none.
+  // in groups of GR tile rows, so that its CUs share rows of both operands in
+  // its L2; the splits of one tile follow each other.  (us with groups of 4, 8
+  // and 16: statistics of 8192 x 128256 x 4096 5949, 5995, 6268; 32768 x 4096 x
+  // 8192, both transposed, 1582, 1675, 1792; probabilities of 8192 x 21760 x 768
+  // 317, 312, 338; 8192 x 4096 x 32768, one transposed, 1612, 1598, 1626.)
+  // Sequence number q -> first row and column and the split, or none.
+  constexpr uint32_t GR = TA || OUT == kBfStats ? 4 : 8;
   auto locate = [&](uint32_t q, int64_t& m0, int64_t& n0, int& split) {
     const uint32_t ts = (q & 7) * chunk + (q >> 3);
     if ((q >> 3) >= chunk || ts >= total) return false;
     const uint32_t t = p.splits == 1 ? ts : ts / p.splits;
     split = (int)(ts - t * p.splits);
-    const uint32_t g = t / (8 * tiles_n), in = t - g * 8 * tiles_n, rows = min(tiles_m - g * 8, 8u);
+    const uint32_t g = t / (GR * tiles_n), in = t - g * GR * tiles_n, rows = min(tiles_m - g * GR, GR);
     const uint32_t col = in / rows;
-    m0 = (int64_t)(g * 8 + in - col * rows) * BM;
+    m0 = (int64_t)(g * GR + in - col * rows) * BM;
     n0 = (int64_t)col * BN;
     return true;
   };
@@ -286,10 +290,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
   // slot `to`), one at a time: the loads of all waves at once would fill the
   // memory pipe's queue and hold the matrix instructions behind them.
   auto step = [&](int kk, int from, int to) {
-    // (16384 x 4096 x 8192, both transposed, in us: loads over the whole
-    // sub-step 832, over its first half 866; statistics of 8192 x 16384 x 4096
-    // 754 and 768, but probabilities 885 and 866, one transposed 846 and 833)
-    constexpr int T = TM * TN, R = TM + TN, D = PA + PB, SOON = TA || OUT == kBfStats ? 1 : 2;
+    // (us with the loads over the whole sub-step, its first half and its first
+    // quarter: 32768 x 4096 x 8192, both transposed, 1674, 1717, 1728;
+    // statistics of 8192 x 128256 x 4096 6098, 5980, 6040; probabilities of 8192
+    // x 32768 x 4096 1784, 1744, 1690; 8192 x 4096 x 32768, one transposed,
+    // 1628, 1610, 1595)
+    constexpr int T = TM * TN, R = TM + TN, D = PA + PB, SOON = TA ? 1 : OUT == kBfStats ? 2 : 4;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const int i = t / TN, j = t % TN;
