@@ -25,6 +25,7 @@ nvfp4      the NVFP4 fake quantiser (RNE and stochastic rounding) + dequant.
 linalg     cyclic Jacobi eigensolver, one-sided Jacobi SVD, shifted CholeskyQR3.
 rsvd       Omega table, row sampler, randomized sketch, projection/rediag,
            residual and the factor cache.
+model      layer norm, dropout, embedding and the loss over a vocabulary.
 split_gemm dense-dequant reference of the split forward and backward GEMMs.
 
 Parity status: every function is pinned by ``tests/test_oracle_*.py`` except

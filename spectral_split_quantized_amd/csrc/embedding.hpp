@@ -1,5 +1,10 @@
 // embedding.hpp -- rows of a table by token number, scaled, and the gradient
-// of the table from the tokens in sorted order.
+// of the table from the tokens in sorted order.  Both are bound by memory: the
+// rows read and written, and all of dW.
+//
+// (16384 tokens of a table of 128256 x 4096 bf16: forward 52 us, 5.2 TB/s;
+// backward 269 us, of which sorting 20, the sums and zeros 231 at 5.1 TB/s, the
+// joins 18.)
 //
 //   y_i = scale W[id_i],   dW_v = scale (sum over i with id_i = v of dy_i),
 // the sum in binary32 over ascending i within pieces of kEmbedRun sorted
@@ -23,7 +28,10 @@ namespace metis {
 
 constexpr int kEmbedBits = 9, kEmbedDigits = 1 << kEmbedBits;
 constexpr int kEmbedTile = 1024, kEmbedTiles = 256;
-constexpr int kEmbedRun = 16;  // sorted tokens whose rows one workgroup adds
+// Sorted tokens whose rows one workgroup adds (a whole call, in us, with 8, 16
+// and 32: 8192 tokens of 50257 x 768 binary32 54, 53, 57; 16384 of 5000 x 512
+// bf16 38.5, 33.6, 38.9; 16384 of 128256 x 4096 bf16 274, 269, 271).
+constexpr int kEmbedRun = 16;
 
 struct EmbedFwdParams {
   const void* w;

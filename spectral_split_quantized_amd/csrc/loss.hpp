@@ -11,7 +11,14 @@
 // whose epilogue forms P (rounded to binary16, or to a pair of planes where a
 // gradient is binary32), then the two products of the gradients.  So the
 // backward pass spends 8 operations where keeping all logits would spend 6,
-// and its memory does not grow with the vocabulary.
+// and its memory does not grow with the vocabulary.  Bound by the products:
+// 8192 tokens of 128256 words x 4096 bf16, forward 6.2 ms, backward 20.2, of
+// which the logits again 6.8, dx 6.4, dw 6.4, planes and largest values 0.7; a
+// large library product of that shape takes 5.8.
+//
+// dx and dw are products of binary16 because P in bf16, rounded by 2^-8 of
+// itself, left a bf16 dx off by 0.0025 of its norm where its own rounding gives
+// 0.0017; with binary16 (2^-11) it is 0.0017, for 4 % of the time.
 //
 // A token whose target is ignore_index, or not a word (which raises the status
 // flag), has loss 0 and gradients 0, whatever its x holds.

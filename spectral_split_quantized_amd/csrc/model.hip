@@ -56,16 +56,26 @@ metis_status ws_check(const char* what, const void* ws, size_t bytes, size_t nee
 
 // ------------------------------------------------------------- layer norm --
 
+// Workgroups of a forward pass, which stride over the rows (us with 640, 1280
+// and 4096: 16384 x 4096 bf16 48, 45, 42; 8192 x 768 binary32 11.6, 11.3, 12.5;
+// 4096 x 8192 bf16 25.5, 25.4, 29.2; 16384 x 1500 binary32 37, 38, 46).
 constexpr int64_t kNormFwdGroups = 1280;
 
+// Threads of a row (us forward and backward with a wave up to 2048 columns and
+// up to 1024: 16384 x 2048 bf16 25 + 41, 35 + 57; 16384 x 1500 binary32 38 +
+// 68, 41 + 87).
 int64_t norm_threads(int64_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 512; }
 
-// Workgroups of 256 threads that are resident at once: 16 values a thread
-// leave room for three on a CU in the backward pass, 32 for two.
+// Workgroups of a backward pass, two on a CU (one of 512 threads), each with a
+// partial sum of dw and db (us with half as many, these and twice as many:
+// 4096 x 8192 bf16 52, 45, 59; 16384 x 2048 bf16 49, 41, 47; with these and half
+// as many more, where registers leave room for three on a CU: 16384 x 4096
+// bf16 80, 85; 8192 x 768 binary32 20.5, 20.9).  Of longer rows one for each
+// kNormSumRows rows.
 int64_t norm_groups(int64_t rows, int64_t cols) {
   if (cols > kNormCols) return std::min<int64_t>(ceil_div<int64_t>(rows, kNormSumRows), INT32_MAX);
   const int64_t T = norm_threads(cols), per = std::max<int64_t>(1, 256 / T);
-  const int64_t most = cols <= 16 * T ? 768 : T == 512 ? 256 : 512;
+  const int64_t most = T == 512 ? 256 : 512;
   return std::min<int64_t>(ceil_div<int64_t>(rows, per), most);
 }
 
@@ -146,7 +156,9 @@ int64_t pad64(int64_t n) { return round_up64(n, 64); }
 // they allow it a number whose dw = P^T x fills whole rounds of the chip's 256
 // CUs with tiles of 256 x 256 (50257 words, 768 features, 8192 tokens: dw in
 // three pieces of 21760 and the rest, not in two of 25152, which take two
-// rounds of tiles each).
+// rounds of tiles each).  Backward pass in us with at most 2^27, 2^28 and 2^29
+// probabilities: 8192 x 50257 x 768 2193, 2136, 2174; 8192 x 128256 x 4096
+// 20470, 20183, 20632; 2048 x 50257 x 1024 binary32 1850, 1738, 1905.
 int64_t loss_piece(int64_t tokens, int64_t vocab, int64_t cols) {
   const int64_t most = std::min<int64_t>(std::max<int64_t>(((int64_t)1 << 28) / std::max<int64_t>(tokens, 1), 4096), 1 << 22);
   const int64_t round = std::max<int64_t>(256 / ceil_div<int64_t>(cols, 256), 1) * 256;
