@@ -193,7 +193,7 @@ def test_dropout_step_on_the_gpu_and_far_elements():
 # --------------------------------------------------------------- embedding --
 
 @pytest.mark.parametrize("tokens,vocab,cols", [(1, 1, 1), (3, 5, 7), (16, 3, 8), (17, 600, 65), (1000, 10, 64), (1023, 300000, 8), (1024, 511, 8), (1024, 512, 12), (1025, 70000, 20), (5000, 513, 770),
-                                               (300, 300000, 8), (40000, 50257, 16)])
+                                               (300, 300000, 8), (3000, 300000, 8), (40000, 50257, 16)])
 @pytest.mark.parametrize("wt,yt,bits", [(BF, BF, 64), (F, F, 32), (F, BF, 64), (BF, F, 32)])
 def test_embedding_matches_the_oracle(tokens, vocab, cols, wt, yt, bits):
     say("embedding %d of %d x %d %s %s %d" % (tokens, vocab, cols, wt, yt, bits))
@@ -615,6 +615,22 @@ def test_offsets_past_32_bits():
         size = p[:, v].abs() @ x.double().abs()
         # P: rounded to binary16, and off by what the logits and the log-sum-exp are
         assert ((dw[v].double() - row).abs() <= 2.0 ** -8 * row.abs() + size * (2.0 ** -11 + 3 * 128 * cols * U)).all(), v
+    metis.status_sync()
+
+
+def test_embedding_gradient_of_numbers_of_28_bits():
+    say("embedding: token numbers of 28 bits")
+    g = torch.Generator(device="cuda").manual_seed(16)
+    vocab = (1 << 27) + 5
+    for tokens in (1000, 5000):
+        ids = torch.randint(0, vocab, (tokens,), generator=g, device="cuda")
+        ids[::3] = ids[0]
+        ids[1], ids[2], ids[4] = vocab - 1, 1 << 18, vocab - 1
+        dy = torch.randn(tokens, 1, generator=g, device="cuda")
+        dw = metis.embedding_bwd(dy, ids, vocab)
+        want = torch.zeros(vocab, 1, dtype=torch.float64, device="cuda").index_add_(0, ids, dy.double())
+        size = torch.zeros(vocab, 1, dtype=torch.float64, device="cuda").index_add_(0, ids, dy.double().abs())
+        assert ((dw.double() - want).abs() <= (16 + tokens / 3 / 16 + 3) * U * size).all()
     metis.status_sync()
 
 
