@@ -49,7 +49,7 @@ double time_of(const Tile& t, int64_t M, int64_t N, int stages, int splits) {
 // the fastest tile and splits by that estimate (us measured, without the join):
 //   8192 x 768 x 21760: 256 x 256 whole 502, in 2 279, in 8 322; 128 x 128
 //     whole 359, in 4 338; 64 x 128 383
-//   1024 x 1024 x 30720: 256 x 256 in 8 79, in 16 66; 128 x 128 in 8 85; 64 x
+//   1024 x 1024 x 480 stages: 256 x 256 in 8 79, in 16 66; 128 x 128 in 8 85; 64 x
 //     128 whole 148, in 2 83
 //   100 x 512 x 5760: 64 x 128 whole 32, in 12 7; 128 x 128 in 12 9
 //   37 x 50304 x 768: 64 x 128 16, 128 x 128 16, 256 x 256 21
