@@ -530,7 +530,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
                       for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) + __uint_as_float(o[e]));
                     }
                   }
-                  *to = w;
+                  // P and gradients go past the caches, which the operands need (a
+                  // backward pass in us without and with it: 8192 x 50257 x 768 2061,
+                  // 2016; 4096 x 32000 x 2048 1416, 1398; 8192 x 128256 x 4096 18527,
+                  // 18652; binary32 sums, read again at once, gain nothing)
+                  if constexpr (BF) __builtin_nontemporal_store(w, to);
+                  else *to = w;
                 } else {
 #pragma unroll
                   for (int e = 0; e < PER; ++e) {
