@@ -3,7 +3,7 @@
 // rows read and written, and all of dW.
 //
 // (16384 tokens of a table of 128256 x 4096 bf16: forward 52 us, 5.2 TB/s;
-// backward 244 us, of which sorting 20, the sums and zeros 205 at 5.8 TB/s, the
+// backward 267 us, of which sorting 20, the sums and zeros 229 at 5.2 TB/s, the
 // joins 18.)
 //
 //   y_i = scale W[id_i],   dW_v = scale (sum over i with id_i = v of dy_i),
@@ -260,12 +260,9 @@ struct EmbedSumParams {
 // Workgroups below `runs`: the rows of kEmbedRun sorted tokens, a row's
 // columns over the threads.  A token whose tokens all lie here is written, the
 // others leave partial sums.  The rest: rows of dW without a token, 64 a wave,
-// each lane looking for one in the sorted tokens.  dW goes past the caches where
-// a wave writes whole lines (16384 tokens of 128256 x 4096 bf16: a call 268 us,
-// 244 so; binary32 sums, 32 bytes a lane, take 87 instead of 53 at 8192 of 50257 x
-// 768).
-typedef uint32_t bytes16_t __attribute__((ext_vector_type(4)));
-
+// each lane looking for one in the sorted tokens.  Zeros are
+// written 16 bytes a lane, whole lines at a time (8192 tokens of 50257 x 768
+// binary32: 28 us, with 32 bytes a lane 35; past the caches 35).
 template <int VEC>
 __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedSumParams p) {
   if (blockIdx.x >= p.runs) {
@@ -286,7 +283,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedSumParams p) {
         const int per = VEC == 1 ? 1 : p.dw_bf16 ? 8 : 4;
         for (int64_t c = lane * per; c < p.cols; c += 64 * per) {
           if (VEC == 8 && c + per <= p.cols) {
-            __builtin_nontemporal_store(bytes16_t{}, (bytes16_t*)((char*)p.dw + (row + c) * (p.dw_bf16 ? 2 : 4)));
+            *(uint4*)((char*)p.dw + (row + c) * (p.dw_bf16 ? 2 : 4)) = make_uint4(0, 0, 0, 0);
           } else {
             for (int e = 0; e < per; ++e)
               if (c + e < p.cols) store1(p.dw, p.dw_bf16, row + c + e, 0.0f);
@@ -340,11 +337,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedSumParams p) {
           const int64_t row = here * p.lddw + c;
 #pragma unroll
           for (int e = 0; e < VEC; ++e) s[e] *= p.scale;
-          if (VEC == 8 && m == 8 && p.dw_bf16) {
-            __builtin_nontemporal_store(
-                bytes16_t{pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]), pack_bf16(s[4], s[5]), pack_bf16(s[6], s[7])},
-                (bytes16_t*)((uint16_t*)p.dw + row));
-          } else if (VEC == 8 && m == 8) {
+          if (VEC == 8 && m == 8) {
             store8(p.dw, p.dw_bf16, row, s);
           } else {
             for (int e = 0; e < VEC; ++e)
