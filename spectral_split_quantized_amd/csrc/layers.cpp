@@ -23,6 +23,7 @@
 #include <memory>
 #include <mutex>
 #include <optional>
+#include <stdexcept>
 #include <string>
 #include <unordered_map>
 #include <vector>
@@ -52,13 +53,14 @@ struct Api {
 PyObject* error_class = nullptr;   // MetisError(status, message)
 PyObject* refuse_capture = nullptr;  // called with the leaves of a pass that a capture records
 
-// A refused argument: becomes the Python exception of that type.
-struct Refused {
+// A refused argument: becomes the Python exception of that type, or, in a
+// backward pass, whose threads take standard exceptions only, a RuntimeError.
+struct Refused : std::runtime_error {
   PyObject* type;
-  std::string what;
+  Refused(PyObject* t, const std::string& what) : std::runtime_error(what), type(t) {}
 };
 
-[[noreturn]] void refuse(PyObject* type, const std::string& what) { throw Refused{type, what}; }
+[[noreturn]] void refuse(PyObject* type, const std::string& what) { throw Refused(type, what); }
 
 // An entry point's error.
 struct Failed : std::runtime_error {
@@ -158,7 +160,8 @@ struct LayerNode : torch::autograd::Node {
     {
       at::AutoGradMode off(false);
       c10::DeviceGuard device(dy[0].device());
-      out = gradients(dy[0]);
+      // (autograd lets a sparse gradient of a dense output through)
+      out = gradients(dy[0].layout() == at::kStrided ? dy[0] : dy[0].to_dense());
     }
     if (at::GradMode::is_enabled() && dy[0].requires_grad()) {
       auto refused = std::make_shared<torch::autograd::DelayedError>(
@@ -484,7 +487,7 @@ PyObject* call(F f) {
   try {
     return f();
   } catch (const Refused& r) {
-    PyErr_SetString(r.type, r.what.c_str());
+    PyErr_SetString(r.type, r.what());
     return nullptr;
   } catch (const Failed& e) {
     if (PyObject* o = PyObject_CallFunction(error_class, "is", e.status, e.text.c_str())) {
