@@ -142,7 +142,8 @@ bool is_alive(const Tensor& t) {
   return living.count(t.unsafeGetTensorImpl()) != 0;
 }
 
-// A layer's node: its gradients are not differentiable again.
+// A layer's node: its gradients are not differentiable again, and say so where
+// that is asked for.
 struct LayerNode : torch::autograd::Node {
   std::vector<const void*> leaves;  // (a living graph holds them, so their addresses are theirs)
 
@@ -154,6 +155,9 @@ struct LayerNode : torch::autograd::Node {
 
   virtual variable_list gradients(const Tensor& dy) = 0;
 
+  // whether the gradients depend on the inputs, not on dy alone
+  virtual bool of_inputs() const { return false; }
+
   variable_list apply(variable_list&& dy) override {
     if (!dy[0].defined()) return variable_list(num_outputs());
     variable_list out;
@@ -163,7 +167,8 @@ struct LayerNode : torch::autograd::Node {
       // (autograd lets a sparse gradient of a dense output through)
       out = gradients(dy[0].layout() == at::kStrided ? dy[0] : dy[0].to_dense());
     }
-    if (at::GradMode::is_enabled() && dy[0].requires_grad()) {
+    // (a pass that builds a graph; the node exists because an input requires a gradient)
+    if (at::GradMode::is_enabled() && (dy[0].requires_grad() || of_inputs())) {
       auto refused = std::make_shared<torch::autograd::DelayedError>(
           "trying to differentiate twice a function whose gradient cannot be differentiated", (int64_t)out.size());
       for (Tensor& t : out)  // the error stands behind outputs that require a gradient
@@ -227,6 +232,7 @@ struct LayerNormNode : LayerNode {
   int32_t w_dtype = METIS_F32;
 
   std::string name() const override { return "MetisLayerNorm"; }
+  bool of_inputs() const override { return true; }
   void release_variables() override { x.reset_data(), w.reset_data(), stats.reset_data(); }
 
   variable_list gradients(const Tensor& dy) override {
@@ -403,6 +409,7 @@ struct LossNode : LayerNode {
   int reduction = kMean;
 
   std::string name() const override { return "MetisLinearCrossEntropy"; }
+  bool of_inputs() const override { return true; }
   void release_variables() override { x.reset_data(), w.reset_data(), targets.reset_data(), lse.reset_data(), total.reset_data(); }
 
   variable_list gradients(const Tensor& dy) override {

@@ -48,3 +48,38 @@ def test_a_sparse_gradient_is_taken():
         want = torch.autograd.grad(torch.nn.functional.embedding(rows, run(leaf)).square().sum(), leaf)[0]
         assert torch.equal(got, want)  # (no row is named more than twice, and two values have one sum)
     metis.status_sync()
+
+
+@pytest.mark.parametrize("name", ["norm", "loss"])
+def test_second_derivatives_raise_whatever_the_gradient_from_above(name):
+    """The gradients of a norm and of the loss depend on the inputs: a penalty
+    on them is not left out in silence where the gradient from above is a
+    constant."""
+    say("second derivatives: %s" % name)
+    run, leaf = {n: (r, x) for n, r, x in _layers()}[name]
+    want = torch.autograd.grad(run(leaf).sum(), leaf)[0]
+    y = run(leaf)
+    (first,) = torch.autograd.grad(y.sum(), leaf, create_graph=True)
+    assert torch.equal(first, want)
+    with pytest.raises(RuntimeError, match="differentiate"):
+        (y.sum() + first.square().sum()).backward()
+    with pytest.raises(RuntimeError, match="differentiate"):
+        torch.autograd.grad(first.sum(), leaf)
+    leaf.grad = None
+    run(leaf).sum().backward(create_graph=True)  # a graph that is not used is no error
+    assert torch.equal(leaf.grad.detach(), want)
+    leaf.grad = None
+
+
+@pytest.mark.parametrize("name", ["dropout", "embedding"])
+def test_gradients_that_depend_on_the_one_from_above_alone(name):
+    """Those of dropout and of the embedding are linear: with a constant from
+    above they are constants."""
+    say("first derivatives with a graph: %s" % name)
+    run, leaf = {n: (r, x) for n, r, x in _layers()}[name]
+    (first,) = torch.autograd.grad(run(leaf).sum(), leaf, create_graph=True)
+    assert not first.requires_grad and torch.equal(first, torch.autograd.grad(run(leaf).sum(), leaf)[0])
+    up = torch.ones_like(run(leaf)).requires_grad_(True)
+    (first,) = torch.autograd.grad(run(leaf), leaf, up, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate"):
+        first.sum().backward()
