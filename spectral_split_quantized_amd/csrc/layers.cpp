@@ -103,10 +103,17 @@ Rows rows_of(const Tensor& x, const char* what) {
   return {x.contiguous(), dtype, rows, cols, cols, true};
 }
 
+// The layers' kernels know nothing of tangents: they would be dropped.
+void no_tangent(const Tensor& t) {
+  if (t.defined() && t._fw_grad(0).defined()) refuse(PyExc_NotImplementedError, "the layers have no forward-mode derivatives");
+}
+
+// The GPU that a layer's operands are on.
 int device_of(std::initializer_list<const Tensor*> tensors) {
   int device = -1;
+  for (const Tensor* t : tensors) no_tangent(*t);
   for (const Tensor* t : tensors) {
-    if (!t || !t->defined()) continue;
+    if (!t->defined()) continue;
     if (!t->is_cuda() || (device >= 0 && t->get_device() != device))
       refuse(PyExc_ValueError, "the operands must be on one GPU, got one on " + t->device().str());
     device = (int)t->get_device();
@@ -160,6 +167,7 @@ struct LayerNode : torch::autograd::Node {
 
   variable_list apply(variable_list&& dy) override {
     if (!dy[0].defined()) return variable_list(num_outputs());
+    no_tangent(dy[0]);
     variable_list out;
     {
       at::AutoGradMode off(false);

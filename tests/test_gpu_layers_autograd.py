@@ -3,6 +3,7 @@ backward pass."""
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fwAD
 
 from spectral_split_quantized_amd import metis
 from spectral_split_quantized_amd.layer import Dropout, Embedding, LayerNorm, LinearCrossEntropy, set_step
@@ -83,3 +84,13 @@ def test_gradients_that_depend_on_the_one_from_above_alone(name):
     (first,) = torch.autograd.grad(run(leaf), leaf, up, create_graph=True)
     with pytest.raises(RuntimeError, match="differentiate"):
         first.sum().backward()
+
+
+def test_forward_mode_through_a_backward_pass_raises():
+    for name, run, leaf in _layers():
+        say("forward mode in a backward pass: %s" % name)
+        y = run(leaf)
+        with fwAD.dual_level():
+            up = fwAD.make_dual(torch.ones_like(y), torch.ones_like(y))
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                torch.autograd.grad(y, leaf, up)

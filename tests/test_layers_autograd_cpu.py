@@ -1,0 +1,38 @@
+"""Uses of the layers around the linear ones that they refuse before any GPU
+work, so that nothing is left out in silence."""
+
+import pytest
+import torch
+import torch.autograd.forward_ad as fwAD
+
+from spectral_split_quantized_amd.layer import Dropout, Embedding, LayerNorm, LinearCrossEntropy
+
+N, C, V = 3, 4, 5
+
+
+def _runs():
+    ids = torch.tensor([0, 1, 2])
+    ln, drop = LayerNorm(C, device="cpu"), Dropout(0.5, device="cpu")
+    head, em = LinearCrossEntropy(C, V, device="cpu"), Embedding(V, C, device="cpu")
+    return {"norm": ln, "dropout": drop, "residual": lambda x: drop(torch.zeros(N, C), x), "loss": lambda x: head(x, ids)}, em, ids
+
+
+@pytest.mark.parametrize("name", ["norm", "dropout", "residual", "loss", "embedding"])
+def test_forward_mode_is_refused(name):
+    runs, em, ids = _runs()
+    with fwAD.dual_level():
+        if name == "embedding":
+            from spectral_split_quantized_amd import layer
+            dual = fwAD.make_dual(em.weight.detach(), torch.ones(V, C))
+            run = lambda: layer._layers().embedding(dual, ids, 1.0, -1, -1)  # noqa: E731
+        else:
+            dual = fwAD.make_dual(torch.zeros(N, C), torch.ones(N, C))
+            run = lambda: runs[name](dual)  # noqa: E731
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            run()
+
+
+def test_forward_mode_of_a_parameter_is_refused():
+    ln = LayerNorm(C, device="cpu")
+    with fwAD.dual_level(), pytest.raises(NotImplementedError, match="forward-mode"):
+        torch.func.functional_call(ln, {"bias": fwAD.make_dual(torch.zeros(C), torch.ones(C))}, torch.zeros(N, C))
