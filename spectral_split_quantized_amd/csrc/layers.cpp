@@ -10,6 +10,7 @@
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/function.h>
@@ -18,6 +19,7 @@
 #include <torch/csrc/autograd/grad_mode.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/saved_variable.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 
 #include <initializer_list>
 #include <memory>
@@ -108,9 +110,19 @@ void no_tangent(const Tensor& t) {
   if (t.defined() && t._fw_grad(0).defined()) refuse(PyExc_NotImplementedError, "the layers have no forward-mode derivatives");
 }
 
+// A recorder of torch's operators would see the outputs' memory allocated and
+// nothing that fills it: what it records returns that memory as it is.
+void no_recorder() {
+  using Mode = c10::impl::TorchDispatchModeKey;
+  bool any = torch::jit::tracer::isTracing();
+  for (Mode m : {Mode::PROXY, Mode::FAKE, Mode::FUNCTIONAL}) any = any || c10::impl::TorchDispatchModeTLS::get_mode(m);
+  if (any) refuse(PyExc_NotImplementedError, "the layers cannot be traced (torch.jit.trace, make_fx, fake tensors)");
+}
+
 // The GPU that a layer's operands are on.
 int device_of(std::initializer_list<const Tensor*> tensors) {
   int device = -1;
+  no_recorder();
   for (const Tensor* t : tensors) no_tangent(*t);
   for (const Tensor* t : tensors) {
     if (!t->defined()) continue;
@@ -168,6 +180,7 @@ struct LayerNode : torch::autograd::Node {
   variable_list apply(variable_list&& dy) override {
     if (!dy[0].defined()) return variable_list(num_outputs());
     no_tangent(dy[0]);
+    no_recorder();
     variable_list out;
     {
       at::AutoGradMode off(false);

@@ -94,3 +94,25 @@ def test_forward_mode_through_a_backward_pass_raises():
             up = fwAD.make_dual(torch.ones_like(y), torch.ones_like(y))
             with pytest.raises(RuntimeError, match="forward-mode"):
                 torch.autograd.grad(y, leaf, up)
+
+
+def test_compiled_callers_break_the_graph_and_are_right():
+    """torch.compile leaves the layers' calls out of its graphs."""
+    for name, run, leaf in _layers():
+        say("compiled caller: %s" % name)
+        leaf.grad = None
+        want = run(leaf) * 2
+        want.sum().backward()
+        grad, leaf.grad = leaf.grad, None
+        got = torch.compile(lambda q: run(q) * 2, backend="eager")(leaf)
+        got.sum().backward()
+        assert torch.equal(got, want) and torch.equal(leaf.grad, grad)
+
+
+def test_a_backward_pass_cannot_be_recorded():
+    from torch.fx.experimental.proxy_tensor import make_fx
+    for name, run, leaf in _layers():
+        say("recording a backward pass: %s" % name)
+        y = run(leaf)
+        with pytest.raises(Exception, match="traced"):
+            make_fx(lambda up: torch.autograd.grad(y, leaf, up)[0])(torch.ones_like(y))

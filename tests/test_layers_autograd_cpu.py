@@ -36,3 +36,17 @@ def test_forward_mode_of_a_parameter_is_refused():
     ln = LayerNorm(C, device="cpu")
     with fwAD.dual_level(), pytest.raises(NotImplementedError, match="forward-mode"):
         torch.func.functional_call(ln, {"bias": fwAD.make_dual(torch.zeros(C), torch.ones(C))}, torch.zeros(N, C))
+
+
+@pytest.mark.parametrize("name", ["norm", "dropout", "residual", "loss", "embedding"])
+def test_tracing_is_refused(name):
+    """A trace would record the outputs' allocation and nothing that fills it."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+    runs, em, ids = _runs()
+    run, x = (em, ids) if name == "embedding" else (runs[name], torch.zeros(N, C))
+    with torch.no_grad():
+        with pytest.raises(NotImplementedError, match="traced"):
+            torch.jit.trace(run, x)
+        for mode in ("real", "fake"):
+            with pytest.raises(NotImplementedError, match="traced"):
+                make_fx(run, tracing_mode=mode)(x)
