@@ -83,6 +83,10 @@ int32_t float_type(const Tensor& t, const char* what) {
 
 at::ScalarType scalar_type(int32_t dtype) { return dtype == METIS_BF16 ? at::kBFloat16 : at::kFloat; }
 
+// A view whose values are negated when they are read ends up in memory: the
+// kernels read memory.
+Tensor plain(const Tensor& t) { return t.defined() && t.is_neg() ? t.resolve_neg() : t; }
+
 // The last dimension's rows of a tensor as the library takes them; a copy
 // where they do not lie so.
 struct Rows {
@@ -186,7 +190,7 @@ struct LayerNode : torch::autograd::Node {
       at::AutoGradMode off(false);
       c10::DeviceGuard device(dy[0].device());
       // (autograd lets a sparse gradient of a dense output through)
-      out = gradients(dy[0].layout() == at::kStrided ? dy[0] : dy[0].to_dense());
+      out = gradients(plain(dy[0].layout() == at::kStrided ? dy[0] : dy[0].to_dense()));
     }
     // (a pass that builds a graph; the node exists because an input requires a gradient)
     if (at::GradMode::is_enabled() && (dy[0].requires_grad() || of_inputs())) {
@@ -530,7 +534,7 @@ PyObject* call(F f) {
 PyObject* py_layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call([&] {
     count_args(n, 4);
-    return THPVariable_Wrap(layer_norm(tensor(a[0], "x"), maybe(a[1], "weight"), maybe(a[2], "bias"), number(a[3])));
+    return THPVariable_Wrap(layer_norm(plain(tensor(a[0], "x")), plain(maybe(a[1], "weight")), plain(maybe(a[2], "bias")), number(a[3])));
   });
 }
 
@@ -539,21 +543,23 @@ PyObject* py_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
     count_args(n, 7);
     const Draws d{number(a[2]), PyLong_AsUnsignedLongLongMask(a[3]), (uint32_t)integer(a[4]), integer(a[5]), maybe(a[6], "the count")};
     if (PyErr_Occurred()) throw python_error();
-    return THPVariable_Wrap(dropout(tensor(a[0], "x"), maybe(a[1], "the residual"), d));
+    return THPVariable_Wrap(dropout(plain(tensor(a[0], "x")), plain(maybe(a[1], "the residual")), d));
   });
 }
 
 PyObject* py_embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call([&] {
     count_args(n, 5);
-    return THPVariable_Wrap(embedding(tensor(a[0], "the weight"), tensor(a[1], "token numbers"), number(a[2]), integer(a[3]), (int32_t)integer(a[4])));
+    return THPVariable_Wrap(
+        embedding(plain(tensor(a[0], "the weight")), tensor(a[1], "token numbers"), number(a[2]), integer(a[3]), (int32_t)integer(a[4])));
   });
 }
 
 PyObject* py_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call([&] {
     count_args(n, 5);
-    return THPVariable_Wrap(linear_cross_entropy(tensor(a[0], "x"), tensor(a[1], "the weight"), tensor(a[2], "targets"), integer(a[3]), (int)integer(a[4])));
+    return THPVariable_Wrap(linear_cross_entropy(plain(tensor(a[0], "x")), plain(tensor(a[1], "the weight")), tensor(a[2], "targets"), integer(a[3]),
+                                                 (int)integer(a[4])));
   });
 }
 

@@ -206,6 +206,12 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _plain(t):
+    """The library reads memory: it has to hold the tensor's values."""
+    if t.is_neg():
+        raise ValueError("a view with negated values is not an operand; resolve_neg() makes one")
+
+
 def _rows_check(M):
     """The boundary takes row-major matrices with a leading dimension: the
     elements of a row must be contiguous."""
@@ -223,6 +229,8 @@ def dtype_code(dtype):
 
 
 def _dtype_code(t):
+    """An operand's metis_dtype."""
+    _plain(t)
     return dtype_code(t.dtype)
 
 
@@ -864,6 +872,7 @@ def grad_norm(grads, max_norm=float("inf"), out=None, workspace=None):
 
 def _matrix(T, rows, cols, name, dtype=None):
     """A row-major matrix of the library's types."""
+    _plain(T)
     if T.dim() != 2 or (rows, cols) != tuple(T.shape) or (cols > 1 and T.stride(1) != 1) \
             or T.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and T.dtype != dtype) \
             or (rows > 1 and T.stride(0) < cols):
@@ -873,6 +882,7 @@ def _matrix(T, rows, cols, name, dtype=None):
 
 def _values(T, n, name, dtype=torch.float32):
     """A contiguous vector of n values."""
+    _plain(T)
     if T.dtype != dtype or T.numel() != n or not T.is_contiguous():
         raise ValueError("%s must be %d contiguous values, %s" % (name, n, dtype))
     return T

@@ -116,3 +116,42 @@ def test_a_backward_pass_cannot_be_recorded():
         y = run(leaf)
         with pytest.raises(Exception, match="traced"):
             make_fx(lambda up: torch.autograd.grad(y, leaf, up)[0])(torch.ones_like(y))
+
+
+def _negated(t):
+    """-t as a view that is negated when it is read, and contiguous as it lies."""
+    v = torch._neg_view(t)
+    assert v.is_neg() and v.is_contiguous()
+    return v
+
+
+def test_negated_views_are_taken_with_their_sign():
+    """Of inputs, parameters and gradients."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    up = torch.randn(N, C, generator=g, device="cuda")
+    for name, run, leaf in _layers():
+        say("negated views: %s" % name)
+        with torch.no_grad():
+            want = run(-leaf) if name != "embedding" else -run(leaf)
+            head = LinearCrossEntropy(C, V, weight=torch.nn.Parameter(_negated(leaf.detach()))) if name == "embedding" else None
+        if head is None:
+            assert torch.equal(run(_negated(leaf)), want)
+            (got,) = torch.autograd.grad(run(_negated(leaf)).sum(), leaf)
+            q = -leaf.detach()
+            assert torch.equal(got, -torch.autograd.grad(run(q.requires_grad_(True)).sum(), q)[0])
+        else:
+            x = torch.randn(N, C, generator=g, device="cuda")
+            t = torch.arange(N, device="cuda")
+            assert torch.equal(head(x, t), LinearCrossEntropy(C, V, weight=-leaf.detach())(x, t))
+            em = Embedding(V, C, weight=torch.nn.Parameter(_negated(leaf.detach())))
+            assert torch.equal(em(t), -em.weight.detach().neg()[t])
+        y = run(leaf)
+        u = up if y.dim() > 1 else up[:, 0].contiguous()
+        (got,) = torch.autograd.grad(y, leaf, _negated(u))
+        assert torch.equal(got, torch.autograd.grad(run(leaf), leaf, -u)[0])
+    x = torch.randn(N, C, generator=g, device="cuda")
+    w, b = torch.randn(2, C, generator=g, device="cuda")
+    ln = LayerNorm(C, weight=torch.nn.Parameter(_negated(w)), bias=torch.nn.Parameter(_negated(b)))
+    assert torch.equal(ln(x), LayerNorm(C, weight=-w, bias=-b)(x))
+    drop = Dropout(0.5)
+    assert torch.equal(drop(x, _negated(x)), drop(x, -x))

@@ -5,6 +5,7 @@ import pytest
 import torch
 import torch.autograd.forward_ad as fwAD
 
+from spectral_split_quantized_amd import metis
 from spectral_split_quantized_amd.layer import Dropout, Embedding, LayerNorm, LinearCrossEntropy
 
 N, C, V = 3, 4, 5
@@ -50,3 +51,17 @@ def test_tracing_is_refused(name):
         for mode in ("real", "fake"):
             with pytest.raises(NotImplementedError, match="traced"):
                 make_fx(run, tracing_mode=mode)(x)
+
+
+def test_bindings_refuse_negated_views():
+    """They read memory, where such a view's values have the other sign."""
+    x = torch.ones(N, C)
+    neg, ids, vec = torch._neg_view(x), torch.tensor([0, 1, 2]), torch.ones(N)
+    for call in (lambda: metis.layernorm(neg), lambda: metis.layernorm(x, torch._neg_view(torch.ones(C))), lambda: metis.dropout(neg, 0.5),
+                 lambda: metis.dropout(x, 0.5, residual=neg), lambda: metis.embedding(neg, ids), lambda: metis.embedding_bwd(neg, ids, 5),
+                 lambda: metis.cross_entropy(neg, x, ids), lambda: metis.cross_entropy(x, neg, ids),
+                 lambda: metis.layernorm_bwd(x, x, torch._neg_view(vec), vec), lambda: metis.layernorm_bwd(neg, x, vec, vec),
+                 lambda: metis.cross_entropy_bwd(x, x, ids, torch._neg_view(vec), vec),
+                 lambda: metis.cross_entropy_bwd(x, x, ids, vec, torch._neg_view(vec)), lambda: metis.int8_quantize(neg, metis.AXIS0)):
+        with pytest.raises(ValueError, match="negated"):
+            call()
