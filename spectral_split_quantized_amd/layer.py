@@ -118,7 +118,7 @@ def _refuse_alive(leaves, layer=None):
     holds its leaves, so their ids are theirs.)"""
     ids = [id(t) for t in leaves]
     if any((layer is not None and c.layer() is layer) or any(i in c.leaves for i in ids) for c in _EAGER) \
-            or any(_layers().alive(t) for t in leaves):
+            or (_ext is not None and any(_ext.alive(t) for t in leaves)):  # (not loaded: it has no graphs)
         raise RuntimeError("a graph of this layer from outside the capture is alive, or one with the same weight or "
                            "input: drop its outputs first")
 

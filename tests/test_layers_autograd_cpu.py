@@ -65,3 +65,26 @@ def test_bindings_refuse_negated_views():
                  lambda: metis.cross_entropy_bwd(x, x, ids, vec, torch._neg_view(vec)), lambda: metis.int8_quantize(neg, metis.AXIS0)):
         with pytest.raises(ValueError, match="negated"):
             call()
+
+
+def test_captures_of_the_8_bit_layer_do_not_need_the_extension(monkeypatch):
+    """Where _layers.so has not been built it has no living graphs either."""
+    from spectral_split_quantized_amd import layer
+
+    def missing():
+        raise ImportError("_layers.so cannot be loaded")
+
+    monkeypatch.setattr(layer, "_ext", None)
+    monkeypatch.setattr(layer, "_layers", missing)
+    w, other = torch.nn.Parameter(torch.ones(2)), torch.nn.Parameter(torch.ones(2))
+
+    class Node:
+        pass
+
+    node, lin = Node(), layer.Int8Linear(C, C, device="cpu")
+    layer._watch(node, lin, [w], capturing=False)
+    layer._watch(Node(), None, [other], capturing=True)
+    with pytest.raises(RuntimeError, match="alive"):
+        layer._watch(Node(), None, [w], capturing=True)
+    with pytest.raises(RuntimeError, match="alive"):
+        layer._watch(Node(), lin, [other], capturing=True)
