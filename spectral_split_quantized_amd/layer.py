@@ -431,7 +431,11 @@ class Dropout(_Stepped):
             if residual.shape != x.shape or residual.dtype != x.dtype:
                 raise ValueError("the residual must have x's shape and type")
             return x + residual
-        count = self._captured_count() if _capturing(x) else None
+        count = None
+        if _capturing(x):
+            count = self._captured_count()
+            if count is None:  # replays would draw the capture's mask for ever
+                raise RuntimeError("a captured pass reads the step on the GPU: move the layer there first")
         return _layers().dropout(x, residual, self.p, self.seed, self.tag, self._step, count)
 
 

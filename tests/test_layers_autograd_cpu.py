@@ -88,3 +88,13 @@ def test_captures_of_the_8_bit_layer_do_not_need_the_extension(monkeypatch):
         layer._watch(Node(), None, [w], capturing=True)
     with pytest.raises(RuntimeError, match="alive"):
         layer._watch(Node(), lin, [other], capturing=True)
+
+
+def test_a_captured_dropout_needs_its_step_on_the_gpu(monkeypatch):
+    """A layer that was left on the CPU would give every replay the same mask."""
+    from spectral_split_quantized_amd import layer
+    drop = Dropout(0.5, device="cpu")
+    monkeypatch.setattr(layer, "_capturing", lambda t: True)
+    with pytest.raises(RuntimeError, match="move the layer"):
+        drop(torch.zeros(N, C))
+    assert drop.eval()(torch.zeros(N, C)).shape == (N, C)
