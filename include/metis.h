@@ -498,7 +498,9 @@ metis_status metis_grad_norm(const metis_adamw_tensor *tensors, int64_t count, d
  * each be NULL) given lse and the gradient of each loss, grad[i] (grad_each =
  * 1) or grad[0] for all (grad_each = 0), divided by *count where count is not
  * NULL (total + 1 of the forward pass, for the mean).  Logits are formed again
- * in pieces of the vocabulary, so the workspace does not grow with it.
+ * in pieces of the vocabulary, so the workspace does not grow with it: a piece
+ * has at most 2^28 probabilities (or 4096 words, where that is more) and 2^29
+ * values of w (or 256 words).
  * The forward product takes two bf16 operands as they are.  Every other
  * operand becomes binary16 under a common power of two that brings its largest
  * finite value (of the tokens that have a target) into [2^14, 2^15): one value

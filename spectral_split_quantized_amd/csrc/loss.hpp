@@ -35,8 +35,9 @@ namespace metis {
 // file describes, whose scale comes from the largest finite value: one launch
 // takes the largest values (each workgroup leaves its own, so that nothing has
 // to be cleared before), the next joins them, leaves the s in `shift` and makes
-// the planes.  Both are bound by memory; a piece of a weight is small enough to
-// stay in the cache behind the memory (256 MB) between them.
+// the planes.  Both are bound by memory; a piece of a bf16 weight that
+// 8192 tokens or more meet is small enough to stay in the cache behind the
+// memory (256 MB) between them, at up to 4096 features.
 struct PlanesJob {
   const void* src;  // null: no planes, just the s (of the gradients of the losses)
   int64_t rows, cols, ld;

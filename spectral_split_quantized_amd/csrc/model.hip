@@ -151,16 +151,24 @@ bool operand_as_is(const void* p, int32_t dt, int64_t ld, int64_t rows, int64_t 
 
 int64_t pad64(int64_t n) { return round_up64(n, 64); }
 
-// Words of one piece: at most about 2^28 probabilities (512 MB) and 2^22 words
-// (the product counts the bytes of 256 rows of P in 32 bits), and where
-// they allow it a number whose dw = P^T x fills whole rounds of the chip's 256
-// CUs with tiles of 256 x 256 (50257 words, 768 features, 8192 tokens: dw in
-// three pieces of 21760 and the rest, not in two of 25152, which take two
-// rounds of tiles each).  Backward pass in us with at most 2^27, 2^28 and 2^29
-// probabilities: 8192 x 50257 x 768 2193, 2136, 2174; 8192 x 128256 x 4096
-// 20470, 20183, 20632; 2048 x 50257 x 1024 binary32 1850, 1738, 1905.
-int64_t loss_piece(int64_t tokens, int64_t vocab, int64_t cols) {
-  const int64_t most = std::min<int64_t>(std::max<int64_t>(((int64_t)1 << 28) / std::max<int64_t>(tokens, 1), 4096), 1 << 22);
+// Words of one piece: at most about 2^28 probabilities, but 4096 words at least
+// (P takes 512 MB, or 8 KB a token; twice that for two planes); at most 2^29
+// values of the weight, but 256 words at least (its copy takes 1 GB, or 512
+// bytes a column; twice that for two planes); at most 2^22 words (the product
+// counts the bytes of 256 rows of P in 32 bits).  None of it grows with the
+// vocabulary.  Where they allow it, it is a number whose dw = P^T x fills whole
+// rounds of the chip's 256 CUs with tiles of 256 x 256 (50257 words, 768
+// features, 8192 tokens: dw in three pieces of 21760 and the rest, not in two
+// of 25152, which take two rounds of tiles each).  Backward pass in us with at
+// most 2^27, 2^28 and 2^29 probabilities: 8192 x 50257 x 768 2193, 2136, 2174;
+// 8192 x 128256 x 4096 20470, 20183, 20632; 2048 x 50257 x 1024 binary32 1850,
+// 1738, 1905; with at most 2^27, 2^28 and 2^29 values of the weight: 256 x
+// 128256 x 4096 1860, 1717, 1605; 64 tokens of it 1384, 1388, 1329, binary32
+// 3337, 3204, 3046.
+int64_t loss_piece(int64_t tokens, int64_t cols) {
+  const int64_t by_p = std::max<int64_t>(((int64_t)1 << 28) / std::max<int64_t>(tokens, 1), 4096);
+  const int64_t by_w = std::max<int64_t>(((int64_t)1 << 29) / pad64(cols), 256);
+  const int64_t most = std::min<int64_t>({by_p, by_w, 1 << 22});
   const int64_t round = std::max<int64_t>(256 / ceil_div<int64_t>(cols, 256), 1) * 256;
   return round <= most ? most / round * round : most / 256 * 256;
 }
@@ -181,7 +189,7 @@ LossPlan loss_plan(const metis_loss& l) {
   p.pair = p.xp == 2 || p.wp == 2;
   p.x_as_is = !p.pair && operand_as_is(l.x, l.x_dtype, l.ldx, p.N, p.D);
   p.w_as_is = !p.pair && operand_as_is(l.w, l.w_dtype, l.ldw, p.V, p.D);
-  p.piece = loss_piece(p.N, p.V, p.D);
+  p.piece = loss_piece(p.N, p.D);
   return p;
 }
 
@@ -193,7 +201,7 @@ struct LossWs {
   float *target, *losses;
   uint32_t* done;              // counter of the join
   uint16_t* p;                 // backward: P of a piece
-  float *dx, *part;            // dx summed over the pieces, parts of K
+  float *dx, *part;            // a bf16 dx summed over the pieces, parts of K
 };
 
 // parts of K of dx = P w over so many words
@@ -219,7 +227,7 @@ LossWs carve_loss(Carver& cv, const metis_loss& l, const LossPlan& p, bool backw
   }
   const int64_t words = pad64(std::min(p.piece, p.V));
   w.p = cv.take<uint16_t>((size_t)(p.pair ? 2 : 1) * p.Np * words);
-  w.dx = cv.take<float>((size_t)p.N * p.D);
+  if (l.x_dtype == METIS_BF16) w.dx = cv.take<float>((size_t)p.N * p.D);  // (a binary32 one is summed in place)
   int s = dx_splits(p, words);
   if (p.V > p.piece) s = std::max(s, dx_splits(p, pad64(p.V % p.piece)));
   if (s > 1) w.part = cv.take<float>((size_t)s * p.N * p.D);

@@ -206,3 +206,23 @@ def test_weights_can_be_shared():
     assert head.weight is e.weight
     assert set(dict(LayerNorm(4, device="cpu").named_parameters())) == {"weight", "bias"}
     assert not list(LayerNorm(4, affine=False, device="cpu").parameters())
+
+
+def test_cross_entropy_workspace_over_tokens_and_types():
+    """A piece's probabilities and its part of the weight are bounded, for few tokens and for many, in either type."""
+    up = lambda n: (n + 63) // 64 * 64  # noqa: E731
+    for tokens in (1, 64, 8192, 1 << 17, 1 << 20):
+        for cols in (64, 769, 4096, 1 << 20):
+            for xt, wt in ((0, 0), (1, 1), (0, 1), (1, 0)):
+                f = dict(tokens=tokens, cols=cols, ldx=cols, ldw=cols, x_dtype=xt, w_dtype=wt)
+                size = lambda backward, vocab: metis.load().metis_cross_entropy_workspace(ctypes.byref(_loss(vocab=vocab, **f)), backward)  # noqa: E731
+                both = 2 if xt or wt else 1
+                rows = up(tokens) * up(cols)
+                x, w, p = 2 * (xt + 1) * rows, 2 * (wt + 1) * max(1 << 29, 256 * up(cols)), 2 * both * max(1 << 28, 4096 * up(tokens))
+                dx = 0 if xt else 4 * tokens * cols
+                at = [size(1, v) for v in (1 << 20, 1 << 23, (1 << 31) - 1)]
+                # sums in parts of K: 32 at most, few where whole sums fill the chip
+                part = 4 * tokens * cols * (32 if tokens * cols < 1 << 25 else 8)
+                assert max(at) <= 1.02 * (x + w + p + dx + part) + (1 << 20), (f, at)
+                # forward: planes of x, of a piece of w, and the statistics, 8 bytes for 64 words
+                assert size(0, 1 << 23) <= x + w + ((1 << 23) // 64 * 8 + 8) * tokens + (1 << 20), f
