@@ -431,8 +431,9 @@ metis_status metis_layernorm_bwd(const void* dY, int32_t y_dtype, int64_t lddy, 
     LAUNCH_CHECK();
   }
   if (sums) {  // (no rows: zeros)
-    hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)ceil_div<int64_t>(cols, 64), 2), dim3(1024), 0, st, (const float*)ws,
-                       rows > 0 ? norm_groups(rows, cols) : 0, (int)cols, dweight, dbias, (int)(w_dtype == METIS_BF16));
+    // (a launch takes fewer than 2^32 work items a dimension)
+    hipLaunchKernelGGL(norm_sum_kernel, dim3(grid_for(cols, 64), 2), dim3(1024), 0, st, (const float*)ws,
+                       rows > 0 ? norm_groups(rows, cols) : 0, cols, dweight, dbias, (int)(w_dtype == METIS_BF16));
     LAUNCH_CHECK();
   }
   return METIS_OK;

@@ -261,10 +261,11 @@ __global__ __launch_bounds__(norm_block(T)) void norm_bwd_kernel(NormParams p) {
 }
 
 // sum of f(column) over a row by all threads of a long row's workgroup
+// (columns as unsigned numbers: they run past 2^31 in a last step)
 template <typename F>
-__device__ inline float long_row_sum(int cols, float* red, F f) {
+__device__ inline float long_row_sum(uint32_t cols, float* red, F f) {
   float s = 0.0f;
-  for (int c = threadIdx.x; c < cols; c += kNormThreads) s += f(c);
+  for (uint32_t c = threadIdx.x; c < cols; c += kNormThreads) s += f(c);
   __syncthreads();  // the array's last use
   return row_sum<kNormThreads>(s, red);
 }
@@ -272,14 +273,14 @@ __device__ inline float long_row_sum(int cols, float* red, F f) {
 __global__ __launch_bounds__(kNormThreads) void norm_fwd_long_kernel(NormParams p) {
   __shared__ float red[kNormThreads / 64];
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    auto x = [&](int c) { return load1(p.x, p.x_bf16, row * p.ldx + c); };
+    auto x = [&](uint32_t c) { return load1(p.x, p.x_bf16, row * p.ldx + c); };
     const float mu = long_row_sum(p.cols, red, x) * p.inv;
-    auto square = [&](int c) {
+    auto square = [&](uint32_t c) {
       const float d = x(c) - mu;
       return d * d;
     };
     const float r = 1.0f / sqrtf(long_row_sum(p.cols, red, square) * p.inv + p.eps);
-    for (int c = threadIdx.x; c < p.cols; c += kNormThreads) {
+    for (uint32_t c = threadIdx.x; c < (uint32_t)p.cols; c += kNormThreads) {
       const float w = p.w ? load1(p.w, p.w_bf16, c) : 1.0f, b = p.b ? load1(p.b, p.w_bf16, c) : 0.0f;
       store1(p.y, p.y_bf16, row * p.ldy + c, (x(c) - mu) * r * w + b);
     }
@@ -294,11 +295,11 @@ __global__ __launch_bounds__(kNormThreads) void norm_dx_long_kernel(NormParams p
   __shared__ float red[kNormThreads / 64];
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const float mu = p.mean[row], r = p.rstd[row];
-    auto h = [&](int c) { return (load1(p.x, p.x_bf16, row * p.ldx + c) - mu) * r; };
-    auto g = [&](int c) { return load1(p.dy, p.y_bf16, row * p.lddy + c) * (p.w ? load1(p.w, p.w_bf16, c) : 1.0f); };
+    auto h = [&](uint32_t c) { return (load1(p.x, p.x_bf16, row * p.ldx + c) - mu) * r; };
+    auto g = [&](uint32_t c) { return load1(p.dy, p.y_bf16, row * p.lddy + c) * (p.w ? load1(p.w, p.w_bf16, c) : 1.0f); };
     const float s = long_row_sum(p.cols, red, g) * p.inv;
-    const float q = long_row_sum(p.cols, red, [&](int c) { return g(c) * h(c); }) * p.inv;
-    for (int c = threadIdx.x; c < p.cols; c += kNormThreads)
+    const float q = long_row_sum(p.cols, red, [&](uint32_t c) { return g(c) * h(c); }) * p.inv;
+    for (uint32_t c = threadIdx.x; c < (uint32_t)p.cols; c += kNormThreads)
       store1(p.dx, p.x_bf16, row * p.lddx + c, r * (g(c) - s - h(c) * q));
   }
 }
@@ -320,35 +321,40 @@ __global__ __launch_bounds__(256) void norm_dw_long_kernel(NormParams p) {
   }
 }
 
-// dw (blockIdx.y 0) and db (1) from the partial sums: 64 columns a workgroup,
-// its 16 waves take every sixteenth partial sum, in order, and their sums are
-// added in order.
-__global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int64_t groups, int cols, void* dw, void* db,
+// dw (blockIdx.y 0) and db (1) from the partial sums: 64 columns a workgroup
+// at a time, its 16 waves take every sixteenth partial sum, in order, and their
+// sums are added in order.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int64_t groups, int64_t cols, void* dw, void* db,
                                                         int w_bf16) {
   __shared__ float red[16][64];
   void* const to = blockIdx.y ? db : dw;
   if (!to) return;
-  const int wave = threadIdx.x >> 6, c = (int)(blockIdx.x * 64 + (threadIdx.x & 63));
-  float s = 0.0f;
-  if (c < cols) {
-    const float* at = part + (int64_t)blockIdx.y * cols + c;
-    int64_t i = wave;
-    for (; i + 112 < groups; i += 128) {  // eight in flight
-      float v[8];
+  const int wave = threadIdx.x >> 6;
+  for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < cols; c0 += (int64_t)gridDim.x * 64) {
+    const int64_t c = c0 + (threadIdx.x & 63);
+    float s = 0.0f;
+    if (c < cols) {
+      const float* at = part + (int64_t)blockIdx.y * cols + c;
+      int64_t i = wave;
+      for (; i + 112 < groups; i += 128) {  // eight in flight
+        float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = at[(i + 16 * k) * 2 * cols];
+        for (int k = 0; k < 8; ++k) v[k] = at[(i + 16 * k) * 2 * cols];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s += v[k];
+        for (int k = 0; k < 8; ++k) s += v[k];
+      }
+      for (; i < groups; i += 16) s += at[i * 2 * cols];
     }
-    for (; i < groups; i += 16) s += at[i * 2 * cols];
-  }
-  red[wave][threadIdx.x & 63] = s;
-  __syncthreads();
-  if (wave || c >= cols) return;
-  s = 0.0f;
+    red[wave][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (!wave && c < cols) {
+      s = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) s += red[k][threadIdx.x];
-  store1(to, w_bf16, c, s);
+      for (int k = 0; k < 16; ++k) s += red[k][threadIdx.x];
+      store1(to, w_bf16, c, s);
+    }
+    __syncthreads();  // the array's next use
+  }
 }
 
 }  // namespace metis
