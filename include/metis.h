@@ -484,7 +484,8 @@ metis_status metis_grad_norm(const metis_adamw_tensor *tensors, int64_t count, d
  * tokens); rows of dW that no token points to, and row padding (negative:
  * none), are zero.  All of dW is written.  ws holds
  * metis_embedding_bwd_workspace(tokens, cols) bytes, 256-byte aligned.
- * vocab < 2^31, tokens < 2^31, cols < 2^31.
+ * vocab < 2^31, tokens < 2^31 (backward: 2^28 - 2^18), METIS_E_UNSUPPORTED
+ * above; cols < 2^31.
  *
  * metis_cross_entropy_fwd: the logits of token i are l_v = x_i . w_v (x: tokens
  * x cols; w: vocab x cols), never stored; lse[i] = log sum_v exp l_v and

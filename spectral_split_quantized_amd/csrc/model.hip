@@ -105,6 +105,11 @@ void launch_norm_rows(const NormParams& p, bool bwd, hipStream_t st) {
 
 // -------------------------------------------------------------- embedding --
 
+// Workgroups for the rows of zeros, at most, and the tokens whose runs fit one
+// launch beside them.
+constexpr int64_t kEmbedZeroGroups = 8192, kEmbedBwdTokens = (1 << 28) - (1 << 18);
+static_assert(kEmbedBwdTokens / kEmbedRun + kEmbedZeroGroups <= UINT32_MAX / 256, "one launch");
+
 struct EmbedWs {
   uint32_t *key[2], *pos[2], *hist;
   float* part;
@@ -502,6 +507,7 @@ metis_status metis_embedding_bwd(const void* dY, int32_t y_dtype, int64_t tokens
   TRY(ids_check("embedding_bwd", ids, id_bits, tokens, vocab));
   TRY(rows_check("embedding_bwd: dY", dY, y_dtype, tokens, cols, lddy));
   TRY(rows_check("embedding_bwd: dW", dW, w_dtype, vocab, cols, lddw));
+  if (tokens >= kEmbedBwdTokens) return fail(METIS_E_UNSUPPORTED, "embedding_bwd: %lld tokens", (long long)tokens);
   if (padding >= vocab) return fail(METIS_E_INVALID, "embedding_bwd: padding token %lld of %lld", (long long)padding, (long long)vocab);
   TRY(ws_check("embedding_bwd", ws, ws_bytes, metis_embedding_bwd_workspace(tokens, cols)));
   TRY(ensure_device_tables());
@@ -543,8 +549,7 @@ metis_status metis_embedding_bwd(const void* dY, int32_t y_dtype, int64_t tokens
   s.scale = (float)scale;
   s.part = w.part;
   s.runs = ceil_div<int64_t>(tokens, kEmbedRun);
-  s.zero_groups = grid_for(ceil_div<int64_t>(vocab, 64), 4, 8192);
-  if (s.runs + s.zero_groups > max_groups(256)) return fail(METIS_E_UNSUPPORTED, "embedding_bwd: %lld tokens", (long long)tokens);
+  s.zero_groups = grid_for(ceil_div<int64_t>(vocab, 64), 4, kEmbedZeroGroups);
   const dim3 grid((unsigned)(s.runs + s.zero_groups));
   if (vec_rows(dY, y_dtype, lddy, tokens) && vec_rows(dW, w_dtype, lddw, vocab))
     hipLaunchKernelGGL((embed_sum_kernel<8>), grid, dim3(256), 0, st, s);

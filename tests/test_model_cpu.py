@@ -226,3 +226,10 @@ def test_cross_entropy_workspace_over_tokens_and_types():
                 assert max(at) <= 1.02 * (x + w + p + dx + part) + (1 << 20), (f, at)
                 # forward: planes of x, of a piece of w, and the statistics, 8 bytes for 64 words
                 assert size(0, 1 << 23) <= x + w + ((1 << 23) // 64 * 8 + 8) * tokens + (1 << 20), f
+
+
+def test_embedding_gradient_of_too_many_tokens_is_refused_before_any_work():
+    limit = (1 << 28) - (1 << 18)
+    assert _embed_bwd(tokens=limit, cols=1, lddy=1, lddw=1, n=1 << 60) == metis.E_UNSUPPORTED
+    assert _embed_bwd(tokens=limit, cols=1, lddy=1, lddw=1, n=16) == metis.E_UNSUPPORTED
+    assert _embed_bwd(tokens=limit - 1, cols=1, lddy=1, lddw=1, n=16) == metis.E_WORKSPACE
