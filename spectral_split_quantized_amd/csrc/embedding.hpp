@@ -250,7 +250,7 @@ struct EmbedSumParams {
   const uint32_t *key, *pos;  // sorted
   int64_t tokens, vocab, cols, lddy, lddw;
   const void* dy;
-  int dy_bf16, dw_bf16, vec;
+  int dy_bf16, dw_bf16;
   float scale;
   void* dw;
   float* part;       // [runs][2][cols]: sums of a run's first and last token that a neighbour shares
