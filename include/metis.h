@@ -506,7 +506,9 @@ metis_status metis_grad_norm(const metis_adamw_tensor *tensors, int64_t count, d
  * operand becomes binary16 under a common power of two that brings its largest
  * finite value (of the tokens that have a target) into [2^14, 2^15): one value
  * for bf16, two for binary32 where a loss or a binary32 gradient needs both;
- * so do the gradients of the logits, two values where a gradient is binary32.
+ * so do the gradients of the logits, two values where a gradient is binary32,
+ * and, where each loss has a gradient (grad_each = 1), each token's under a power
+ * of two of its own, which dX's row is free of again; dW's x carries the inverse.
  * One value is off by 2^-11 of itself at most (a bf16 operand by nothing), two
  * by 2^-22, and either by 2^-40 of its operand's largest value.
  * lse of a token that is left out is any value.

@@ -54,8 +54,8 @@ struct BfGemmParams {
   const float* lse;           // [M]
   const float* grad;          // [M], or one with `count`
   const float* count;         // tokens that the loss is the mean over, or null
-  int grad_each;              // grad has a value for each token
-  const int* shift_p;         // P's s
+  int grad_each;              // grad has a value for each token, by which also P's s goes (dx: it is taken off row i)
+  const int* shift_p;         // P's s, where grad has one value (else 0)
   uint16_t* prob;             // [M rounded up to 64][ldp], and lo_plane values behind it the low plane
   int64_t ldp, lo_plane;      // lo_plane 0: none
 };
@@ -96,6 +96,16 @@ __device__ __forceinline__ int64_t target_of(const void* targets, int targets64,
   const int64_t t = targets64 ? ((const int64_t*)targets)[row] : (int64_t)((const int32_t*)targets)[row];
   return t == ignore || t < 0 || t >= vocab ? -1 : t;
 }
+
+// The gradient of token `row`'s loss.
+__device__ __forceinline__ float loss_gradient(const float* grad, const float* count, int each, int64_t row) {
+  const float g = grad[each ? row : 0];
+  return count ? g / count[0] : g;
+}
+
+// The s of the probabilities of a token with a gradient of its own: g 2^s lies
+// in [2^14, 2^15) in size (15 where g is 0 or not finite).
+__device__ __forceinline__ int gradient_shift(float g) { return 15 - __builtin_amdgcn_frexp_expf(g); }
 
 // Four rows of K by sixteen columns of a transposed operand, from LDS rows of
 // bf16: of each sixteen lanes, lane 4 r + c names the columns 4 c .. 4 c + 3 of
@@ -444,7 +454,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
           const int cols = (int)max((int64_t)0, min((int64_t)64, p.N - col0));
           const int up = p.shift_p[0];
           float each = 0.0f;
-          if (!p.grad_each) each = p.count ? p.grad[0] / p.count[0] : p.grad[0];
+          if (!p.grad_each) each = loss_gradient(p.grad, p.count, 0, 0);
           auto column = [&](int j, int v) { return j * 16 + 4 * lq + v; };
 #pragma unroll
           for (int i = i0; i < i0 + ER / 16; ++i) {
@@ -453,9 +463,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
             const int64_t t = word - p.v0 - col0;
             const int at = word >= 0 && t >= 0 && t < 64 ? (int)t : -1;
             float g = each;
-            if (p.grad_each) g = p.count ? p.grad[row] / p.count[0] : p.grad[row];
+            if (p.grad_each) g = loss_gradient(p.grad, p.count, 1, row);
             const float off = -p.lse[row] * kLog2E;
-            g = __builtin_ldexpf(g, up);
+            g = __builtin_ldexpf(g, p.grad_each ? gradient_shift(g) : up);
             const bool some = word >= 0 && g != 0.0f;  // a token without a part: zeros, whatever its logits
 #pragma unroll
             for (int j = 0; j < TN; ++j)
@@ -487,12 +497,16 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
             for (int i = i0; i < i0 + ER / 16; ++i) {
               const int r = (i - i0) * 16 + li;
               uint8_t* const row = my + r * 128;
+              int here = down;
+              if constexpr (OUT != kBfProb && !TA) {
+                if (p.grad_each) here -= gradient_shift(loss_gradient(p.grad, p.count, 1, min(row0 + i * 16 + li, p.M - 1)));
+              }
 #pragma unroll
               for (int j = j0; j < j0 + COLS / 16; ++j) {
                 f32x4v_t c = acc[i][j];
                 if constexpr (OUT != kBfProb) {
 #pragma unroll
-                  for (int v = 0; v < 4; ++v) c[v] = __builtin_ldexpf(c[v], down);
+                  for (int v = 0; v < 4; ++v) c[v] = __builtin_ldexpf(c[v], here);
                 }
                 if constexpr (BF) {
                   uint2 w;

@@ -47,18 +47,26 @@ struct PlanesJob {
   int* shift;
   uint32_t* top;       // [kTopBlocks] largest values of the workgroups, their bits
   const void* values;  // what `top` is taken of (src, or the gradients)
-  const float* count;  // null, or what `values` are divided by
+  const float* count;  // null, or what the gradients are divided by
+  const float* weigh;  // null, or a gradient for each row: the rows for P^T x, see below
   int top_blocks, blocks;
   int flat;  // the values of all rows follow each other
 };
 
-constexpr int kTopBlocks = 1024, kPlaneJobs = 3;
+// Where each token has a gradient g_i of its own, its row of P has an s_i of its
+// own, by which the row of dx is scaled back; in P^T x the tokens are summed, so
+// there the rows are x_i 2^-s_i (2^s with the s of them all), and a row counts as
+// much as its gradient lets it.  `top` holds exponents of them then, from 1 on:
+// their range is wider than binary32's.  A token with a gradient of 0 has no
+// part.
+constexpr int kTopBlocks = 1024, kPlaneJobs = 3, kWeighedZero = 512;
 
 struct PlanesParams {
   PlanesJob job[kPlaneJobs];
   const void* targets;
   int targets64;
   int64_t vocab, ignore;
+  int* zero;  // null, or set to zero
 };
 
 // eight consecutive values at any address of theirs
@@ -101,6 +109,7 @@ __device__ __forceinline__ void each8(const PlanesJob& j, const PlanesParams& p,
       for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
       if (row[k] < 0 || row[k] >= j.rows) continue;
       if (j.masked && target_of(p.targets, p.targets64, p.ignore, p.vocab, row[k]) < 0) continue;
+      if (j.weigh && loss_gradient(j.weigh, j.count, 1, row[k]) == 0.0f) continue;
       const int64_t at = row[k] * j.ld + c;
       if (c + 8 <= j.cols) {
         load8_anywhere<BF>(from, at, v[k]);
@@ -139,12 +148,15 @@ __global__ __launch_bounds__(256) void top_kernel(PlanesParams p) {
   PlanesJob j = p.job[job_of(blocks, block)];
   if (j.flat) j.cols *= j.rows, j.rows = 1;
   uint32_t top = 0;  // of values of one sign, larger bits are larger values
-  auto take = [&](int64_t, int, const float* v) {
+  auto take = [&](int64_t row, int, const float* v) {
+    uint32_t here = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const uint32_t b = __float_as_uint(v[e]) & 0x7FFFFFFFu;
-      if (b < 0x7F800000u) top = max(top, b);
+      if (b < 0x7F800000u) here = max(here, b);
     }
+    if (j.weigh && here) here = (here >> 23) + kWeighedZero - gradient_shift(loss_gradient(j.weigh, j.count, 1, row));
+    top = max(top, here);
   };
   const int64_t pitch = (j.cols + 7) & ~(int64_t)7;
   if (j.bf16) each8<true>(j, p, j.rows, pitch, block, j.top_blocks, j.values, take);
@@ -158,26 +170,34 @@ __global__ __launch_bounds__(256) void planes_kernel(PlanesParams p) {
   const int blocks[kPlaneJobs] = {p.job[0].blocks, p.job[1].blocks, p.job[2].blocks};
   int block;
   const PlanesJob j = p.job[job_of(blocks, block)];
+  if (p.zero && blockIdx.x == 0 && threadIdx.x == 0) *p.zero = 0;
   float scale = 1.0f;
+  int s = 0;
   if (j.shift) {
     uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < kTopBlocks / 256; ++k)
       if (k * 256 + (int)threadIdx.x < j.top_blocks) top = max(top, j.top[k * 256 + threadIdx.x]);
     top = top_of_workgroup(top, red);
-    if (j.count) top = __float_as_uint(__uint_as_float(top) / j.count[0]);
-    // (2^126 is the largest power of two whose inverse is no subnormal; no
-    // value but 0, or no finite quotient: 14)
-    const int s = top == 0 || top >= 0x7F800000u ? 14 : min(14 - ((int)(top >> 23) - 127), 126);
+    if (j.weigh) {
+      s = top == 0 ? 14 : 14 - ((int)top - kWeighedZero - 127);
+    } else {
+      if (j.count) top = __float_as_uint(__uint_as_float(top) / j.count[0]);
+      // (2^126 is the largest power of two whose inverse is no subnormal; no
+      // value but 0, or no finite quotient: 14)
+      s = top == 0 || top >= 0x7F800000u ? 14 : min(14 - ((int)(top >> 23) - 127), 126);
+      scale = __builtin_ldexpf(1.0f, s);
+    }
     if (block == 0 && threadIdx.x == 0) *j.shift = s;
-    scale = __builtin_ldexpf(1.0f, s);
   }
   if (!j.src) return;
   auto store = [&](int64_t row, int col, const float* v) {
     uint32_t h[4], l[4];
+    const int weight = j.weigh && row < j.rows ? s - gradient_shift(loss_gradient(j.weigh, j.count, 1, row)) : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = v[2 * i] * scale, b = v[2 * i + 1] * scale;
+      const float a = j.weigh ? __builtin_ldexpf(v[2 * i], weight) : v[2 * i] * scale;
+      const float b = j.weigh ? __builtin_ldexpf(v[2 * i + 1], weight) : v[2 * i + 1] * scale;
       h[i] = j.shift ? pack_f16(a, b) : pack_bf16(a, b);
       if (j.plane) l[i] = pack_f16(rest_f16(a, unpack_f16(h[i], 0)), rest_f16(b, unpack_f16(h[i], 1)));
     }

@@ -200,8 +200,9 @@ LossPlan loss_plan(const metis_loss& l) {
 
 struct LossWs {
   uint16_t *x, *w;             // planes of x, of a piece of w (where not as they are)
+  uint16_t* weighed;           // backward: planes of x by the tokens' gradients
   uint32_t* top;               // [3][kTopBlocks] largest values of x, w, the gradients of the losses
-  int* shift;                  // [3] their s
+  int* shift;                  // [3] their s, and a zero
   float2* stat;                // forward
   float *target, *losses;
   uint32_t* done;              // counter of the join
@@ -221,7 +222,7 @@ LossWs carve_loss(Carver& cv, const metis_loss& l, const LossPlan& p, bool backw
   if (backward || !p.w_as_is) w.w = cv.take<uint16_t>((size_t)p.wp * std::min(p.piece, p.V) * p.Dp);
   if (backward || p.pair) {
     w.top = cv.take<uint32_t>(3 * kTopBlocks);
-    w.shift = cv.take<int>(3);
+    w.shift = cv.take<int>(4);
   }
   if (!backward) {
     w.stat = cv.take<float2>((size_t)ceil_div<int64_t>(p.V, 64) * p.N);
@@ -230,6 +231,7 @@ LossWs carve_loss(Carver& cv, const metis_loss& l, const LossPlan& p, bool backw
     w.done = cv.take<uint32_t>(1);
     return w;
   }
+  w.weighed = cv.take<uint16_t>((size_t)p.xp * p.Np * p.Dp);
   const int64_t words = pad64(std::min(p.piece, p.V));
   w.p = cv.take<uint16_t>((size_t)(p.pair ? 2 : 1) * p.Np * words);
   if (l.x_dtype == METIS_BF16) w.dx = cv.take<float>((size_t)p.N * p.D);  // (a binary32 one is summed in place)
@@ -249,8 +251,9 @@ metis_status loss_check(const metis_loss* l, const char* what) {
   return METIS_OK;
 }
 
-// Planes of x (job 0) and w (job 1) and the s of the gradients of the losses
-// (job 2), as planes_kernel and top_kernel make them.
+// Planes of x (job 0) and w (job 1) and the s of the gradient of the losses, or
+// planes of x weighed by their gradients (job 2), as planes_kernel and top_kernel
+// make them.
 struct PlaneJobs {
   PlanesParams p{};
   const LossWs& ws;
@@ -277,10 +280,15 @@ struct PlaneJobs {
     any = true;
     return {(const uint8_t*)dst, pitch * 2, out_rows * pitch * 2, planes, j.shift};
   }
-  const int* gradients(const float* grad, const float* count, int64_t tokens, bool each) {
+  Planes weighed(const metis_loss& l, const LossPlan& plan, const float* grad, const float* count, uint16_t* dst) {
+    const Planes x = rows(2, l.x, l.x_dtype, l.ldx, plan.N, plan.D, plan.xp, dst, true, true);
+    p.job[2].weigh = grad, p.job[2].count = count;
+    return x;
+  }
+  const int* gradient(const float* grad, const float* count) {
     PlanesJob& j = p.job[2];
     j = PlanesJob{};
-    j.rows = each ? tokens : 1, j.cols = j.ld = 1, j.masked = each, j.count = count;
+    j.rows = 1, j.cols = j.ld = 1, j.count = count;
     j.blocks = 1;
     top_of(2, grad, j.rows);
     return j.shift;
@@ -642,8 +650,8 @@ metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, cons
   TRY(ensure_device_tables());
   Carver cv(ws, ws_bytes);
   const LossWs w = carve_loss(cv, *l, p, true);
-  Planes x;
-  const int* shift_p = nullptr;
+  Planes x, x_dw;
+  const int* shift_p = w.shift + 3;  // (each token's own: by its gradient, in all 0)
   const bool dx_f32 = l->x_dtype == METIS_F32;
   const bool one = p.piece >= p.V;
   for (int64_t v0 = 0; v0 < p.V; v0 += p.piece) {
@@ -652,7 +660,10 @@ metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, cons
     PlaneJobs jobs(*l, w);
     if (v0 == 0) {
       x = jobs.rows(0, l->x, l->x_dtype, l->ldx, p.N, p.D, p.xp, w.x, true, true);
-      shift_p = jobs.gradients(grad, count, p.N, grad_each != 0);
+      x_dw = x;
+      if (!grad_each) shift_p = jobs.gradient(grad, count);
+      else if (dW) x_dw = jobs.weighed(*l, p, grad, count, w.weighed);
+      jobs.p.zero = w.shift + 3;
     }
     const Planes v = jobs.rows(1, wv, l->w_dtype, l->ldw, n, p.D, p.wp, w.w, true, false);
     TRY(jobs.run(st));
@@ -666,6 +677,7 @@ metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, cons
     if (dX) {
       g = product(pr, p.N, v, p.D, n, dx_f32);
       g.rows_b = n;
+      g.grad = grad, g.count = count, g.grad_each = grad_each;
       const int splits = dx_splits(p, n);
       // one piece: straight to dX; else summed in binary32, in dX itself where it is binary32
       void* const sum = dx_f32 ? dX : (void*)w.dx;
@@ -683,7 +695,7 @@ metis_status metis_cross_entropy_bwd(const metis_loss* l, const float* lse, cons
       }
     }
     if (dW) {
-      g = product(pr, n, x, p.D, p.N, p.wp == 2);
+      g = product(pr, n, x_dw, p.D, p.N, p.wp == 2);
       g.rows_a = g.rows_b = p.Np;
       g.C = (char*)dW + v0 * lddw * value_size(l->w_dtype), g.ldc = lddw;
       TRY(run_product(g, p.wp == 2 ? kBfF32 : kBfBF16, st));

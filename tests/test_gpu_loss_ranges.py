@@ -1,11 +1,14 @@
 """The loss over a vocabulary at the ends of its ranges."""
 
+import numpy as np
 import pytest
 import torch
 
 from spectral_split_quantized_amd import metis
+from spectral_split_quantized_amd.layer import LinearCrossEntropy
 
 from gpu_helpers import say
+from test_gpu_model import _loss_limits, f64, near
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +66,56 @@ def test_few_tokens_over_several_pieces(xt, wt):
     assert ((dw - want).abs() <= tol + torch.finfo(wt).eps / 2 * (want.abs() + tol)).all()
     assert not dx[3].any()
     metis.status_sync()
+
+
+@pytest.mark.parametrize("tokens,vocab,cols", [(70, 200, 96), (3, 70, 7), (520, 2100, 320), (300, 5000, 64)])
+@pytest.mark.parametrize("xt,wt", [(BF, BF), (F, F), (BF, F), (F, BF)])
+def test_gradients_of_losses_far_apart(tokens, vocab, cols, xt, wt):
+    """Each token's probabilities have a scale of their own: a token's gradient
+    keeps its bits however large another token's is."""
+    say("cross entropy %d x %d x %d with gradients from 2^-70 to 2^70 %s %s" % (tokens, vocab, cols, xt, wt))
+    g = torch.Generator(device="cuda").manual_seed(tokens + cols)
+    x = torch.randn(tokens, cols, generator=g, device="cuda").to(xt)
+    w = (torch.randn(vocab, cols, generator=g, device="cuda") * 2 / cols ** 0.5).to(wt)
+    t = torch.randint(0, vocab, (tokens,), generator=g, device="cuda")
+    t[2::7] = -100
+    up = torch.randn(tokens, generator=g, device="cuda") * torch.exp2(torch.linspace(-70, 70, tokens, device="cuda").round())
+    up[5::11] = 0
+    x[2::14] = float("nan")  # (left out)
+    losses, lse, _ = metis.cross_entropy(x, w, t)
+    dx, dw = metis.cross_entropy_bwd(x, w, t, lse, up)
+    assert all(torch.equal(a, b) for a, b in zip(metis.cross_entropy_bwd(x, w, t, lse, up), (dx, dw)))
+    assert torch.equal(metis.cross_entropy_bwd(x, w, t, lse, up, want_dw=False)[0], dx)
+    assert torch.equal(metis.cross_entropy_bwd(x, w, t, lse, up, want_dx=False)[1], dw)
+    T = t.cpu().numpy()
+    use = T != -100
+    X, W, G = np.where(use[:, None], f64(x), 0), f64(w), f64(up)[:, None]
+    # P and its limits for gradients of one, then each row by its token's
+    P1, dP1 = _loss_limits(X, W, T, np.ones(tokens), xt, wt)[4:]
+    P, dP = P1 * G, dP1 * np.abs(G)
+    # the other operand: bf16 as it is, binary32 a pair, or rounded to binary16 where the gradient is bf16; and then P's
+    # high part alone
+    pair = F in (xt, wt)
+    ox, ow = (0 if xt == BF else 2.0 ** -21 if wt == F else 2.0 ** -11), (0 if wt == BF else 2.0 ** -21 if xt == F else 2.0 ** -11)
+    ex, ew = (2.0 ** -11 if pair and xt == BF else 0), (2.0 ** -11 if pair and wt == BF else 0)
+    size = np.abs(P) + dP
+    near(dx, P @ W, dP @ np.abs(W) + size @ np.abs(W) * (vocab * U + ow + ex) + 2.0 ** -39 * np.abs(W).max() * size.sum(1, keepdims=True), "dx")
+    assert not dx[5::11].any() and not dx[2::7].any()
+    # dw: x carries the inverse of P's scale, under a common one, and is off by 2^-39 of its largest value there at most; a
+    # scale is within a factor of two of its gradient
+    worst = (np.abs(X).max(1) * np.abs(G[:, 0])).max()
+    unit = (np.abs(P1) + dP1).sum(0)[:, None]
+    near(dw, P.T @ X, dP.T @ np.abs(X) + size.T @ np.abs(X) * (tokens * U + ox + ew) + 2.0 ** -38 * unit * worst, "dw")
+    metis.status_sync()
+
+
+def test_the_layer_weighs_each_token():
+    say("loss of each token, weighted over 30 orders of magnitude")
+    g = torch.Generator(device="cuda").manual_seed(23)
+    head = LinearCrossEntropy(64, 90, reduction="none")
+    x = torch.randn(70, 64, generator=g, device="cuda", requires_grad=True)
+    t = torch.randint(0, 90, (70,), generator=g, device="cuda")
+    each = torch.autograd.grad(head(x, t), x, torch.ones(70, device="cuda"))[0]
+    weights = torch.exp2(-torch.arange(70, device="cuda").float())
+    got = torch.autograd.grad(head(x, t), x, weights)[0]
+    assert torch.equal(got, each * weights[:, None])  # powers of two, and no other token's part
