@@ -6,7 +6,7 @@ import torch
 import torch.autograd.forward_ad as fwAD
 
 from spectral_split_quantized_amd import metis
-from spectral_split_quantized_amd.layer import Dropout, Embedding, LayerNorm, LinearCrossEntropy, set_step
+from spectral_split_quantized_amd.layer import Dropout, Embedding, LayerNorm, LinearCrossEntropy, MetisLinear, set_step
 
 from gpu_helpers import say
 
@@ -155,3 +155,45 @@ def test_negated_views_are_taken_with_their_sign():
     assert torch.equal(ln(x), LayerNorm(C, weight=-w, bias=-b)(x))
     drop = Dropout(0.5)
     assert torch.equal(drop(x, _negated(x)), drop(x, -x))
+
+
+def test_layers_around_the_split_linear_layer():
+    """Embedding, dropout, norm, MetisLinear, dropout with the residual, norm and loss in one graph: the gradients are the
+    library's calls', in a step that sketches and in one that reuses the factors."""
+    say("embedding, dropout, norm, MetisLinear, dropout, norm, loss: one graph")
+    vocab, cols, tokens = 301, 96, 128
+    g = torch.Generator(device="cuda").manual_seed(9)
+    em = Embedding(vocab, cols, scale=cols ** 0.5, weight=torch.randn(vocab, cols, generator=g, device="cuda") * 0.05)
+    lin = MetisLinear(cols, cols, 8, s=8, l_k=32, refresh=8, weight=torch.randn(cols, cols, generator=g, device="cuda") * cols ** -0.5)
+    drop1, drop2, norm1, norm2 = Dropout(0.1, layer=1), Dropout(0.2, layer=2), LayerNorm(cols), LayerNorm(cols)
+    head = LinearCrossEntropy(cols, vocab, weight=em.weight)
+    model = torch.nn.ModuleList([em, lin, drop1, drop2, norm1, norm2, head])
+    ids = torch.randint(0, vocab, (4, tokens // 4), generator=g, device="cuda")
+    t = ids.roll(-1, -1).clone()
+    t[:, -1] = -100
+    both, w, flat, ft = metis.AXIS0 | metis.AXIS1, em.weight.detach(), ids.reshape(-1), t.reshape(-1)
+    f = {n: metis.Factors(r, cols, 8) for n, r in (("X", tokens), ("W", cols), ("D", tokens))}
+    for step in (0, 1):
+        set_step(model, step)
+        model.zero_grad()
+        h = drop1(em(ids))
+        loss = head(norm2(drop2(lin(norm1(h)), h)), t)
+        loss.backward()
+        prepared = lambda m, n: metis.prepare_operand(m, lin.cfg, n != "W", lin.tags[n], step, f[n], both)  # noqa: E731,B023
+        h1 = metis.dropout(metis.embedding(w, flat, em.scale), 0.1, tag=drop1.tag, step=step)
+        n1, mu1, r1 = metis.layernorm(h1, norm1.weight, norm1.bias)
+        qx, qw = prepared(n1, "X"), prepared(lin.weight.detach(), "W")
+        h2 = metis.dropout(metis.gemm_fwd(qx, qw), 0.2, h1, 0, drop2.tag, step)
+        n2, mu2, r2 = metis.layernorm(h2, norm2.weight, norm2.bias)
+        _, lse, total = metis.cross_entropy(n2, w, ft)
+        assert torch.equal(loss.detach(), total[0])
+        d, dw = metis.cross_entropy_bwd(n2, w, ft, lse, torch.ones((), device="cuda"), total[1])
+        d, a, b = metis.layernorm_bwd(d, h2, mu2, r2, norm2.weight)
+        assert torch.equal(norm2.weight.grad, a) and torch.equal(norm2.bias.grad, b)
+        dx, dlin = metis.gemm_bwd(prepared(metis.dropout(d, 0.2, tag=drop2.tag, step=step), "D"), qw, qx)
+        assert torch.equal(lin.weight.grad, dlin)
+        d1, a, b = metis.layernorm_bwd(dx, h1, mu1, r1, norm1.weight)
+        assert torch.equal(norm1.weight.grad, a) and torch.equal(norm1.bias.grad, b)
+        d = metis.dropout(d + d1, 0.1, tag=drop1.tag, step=step)
+        assert torch.equal(em.weight.grad, dw + metis.embedding_bwd(d, flat, vocab, None, em.scale))
+    metis.status_sync()
