@@ -295,11 +295,16 @@ struct PlaneJobs {
   }
   metis_status run(hipStream_t st) {
     if (!any) return METIS_OK;
+    const bool weigh = p.job[2].weigh != nullptr;
     if (scaled) {
-      hipLaunchKernelGGL(top_kernel, dim3(p.job[0].top_blocks + p.job[1].top_blocks + p.job[2].top_blocks), dim3(256), 0, st, p);
+      const dim3 grid(p.job[0].top_blocks + p.job[1].top_blocks + p.job[2].top_blocks);
+      if (weigh) hipLaunchKernelGGL(top_kernel<true>, grid, dim3(256), 0, st, p);
+      else hipLaunchKernelGGL(top_kernel<false>, grid, dim3(256), 0, st, p);
       LAUNCH_CHECK();
     }
-    hipLaunchKernelGGL(planes_kernel, dim3(p.job[0].blocks + p.job[1].blocks + p.job[2].blocks), dim3(256), 0, st, p);
+    const dim3 grid(p.job[0].blocks + p.job[1].blocks + p.job[2].blocks);
+    if (weigh) hipLaunchKernelGGL(planes_kernel<true>, grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL(planes_kernel<false>, grid, dim3(256), 0, st, p);
     LAUNCH_CHECK();
     return METIS_OK;
   }
