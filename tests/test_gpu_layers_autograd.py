@@ -197,3 +197,36 @@ def test_layers_around_the_split_linear_layer():
         d = metis.dropout(d + d1, 0.1, tag=drop1.tag, step=step)
         assert torch.equal(em.weight.grad, dw + metis.embedding_bwd(d, flat, vocab, None, em.scale))
     metis.status_sync()
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_recomputed_activations_give_the_same_gradients(reentrant):
+    from torch.utils.checkpoint import checkpoint
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(N, C, generator=g, device="cuda", requires_grad=True)
+    t = torch.randint(0, V, (N,), generator=g, device="cuda")
+    ln, drop, head = LayerNorm(C), Dropout(0.3, seed=4), LinearCrossEntropy(C, V)
+    set_step(drop, 7)
+    say("recomputed activations, reentrant %s" % reentrant)
+    block = lambda q: head(drop(ln(q), q), t)  # noqa: E731
+    leaves = [x, ln.weight, ln.bias, head.weight]
+    block(x).backward()
+    want = [p.grad for p in leaves]
+    for p in leaves:
+        p.grad = None
+    checkpoint(block, x, use_reentrant=reentrant).backward()
+    assert all(torch.equal(p.grad, w) for p, w in zip(leaves, want))
+
+
+def test_transforms_over_batches_and_functions_raise():
+    for name, run, leaf in _layers():
+        say("transforms: %s" % name)
+        q = leaf.detach()
+        if name != "embedding":  # (its call here closes over the weight)
+            for transform in (lambda: torch.func.vmap(run)(q.expand(3, *q.shape)), lambda: torch.func.grad(lambda v: run(v).sum())(q),
+                              lambda: torch.func.jvp(run, (q,), (q,))):
+                with pytest.raises((RuntimeError, NotImplementedError, ValueError)):
+                    transform()
+        y = run(leaf)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(y, leaf, torch.ones(2, *y.shape, device="cuda"), is_grads_batched=True)
