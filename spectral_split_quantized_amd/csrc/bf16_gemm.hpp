@@ -143,9 +143,11 @@ __device__ __forceinline__ bf16x8v_t read_transposed(uint32_t at, uint32_t row4)
 //
 // Bound by what the matrix instructions draw and by the stages' loads from
 // memory, which run little more than a stage ahead (two stages of 64 KB fill the
-// LDS): 8192 x 16384 x 4096 with statistics 711 us, 1.55 PFLOP/s, both operands
-// in the cache behind the memory; 8192 x 128256 x 4096 5.95 ms, 1.45; the
-// epilogues' stores of P take 8192 x 32768 x 4096 to 1.67 ms, 1.32.
+// LDS): 8192 x 16384 x 4096 with statistics 756 us, 1.45 PFLOP/s, both operands
+// in the cache behind the memory; 8192 x 128256 x 4096 6.1 ms, 1.42; the
+// epilogues' stores of P take 8192 x 32768 x 4096 to 1.71 ms, 1.29.  (Cards
+// differ by a few percent: 770 us, 6.2 and 1.75 ms on another, 711 us, 5.95 and
+// 1.67 ms where the choices below were measured.)
 //
 // HALF: the operands are binary16 planes, else bf16.  (A product of random
 // operands takes 2 to 3 % longer with binary16, which draws more power.)
@@ -545,9 +547,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void bf_gemm_kernel(BfGemmParams p
                     }
                   }
                   // P and gradients go past the caches, which the operands need (a
-                  // backward pass in us without and with it: 8192 x 50257 x 768 2061,
-                  // 2016; 4096 x 32000 x 2048 1416, 1398; 8192 x 128256 x 4096 18527,
-                  // 18652; binary32 sums, read again at once, gain nothing)
+                  // backward pass in us without and with it, two runs of each: 8192 x
+                  // 50257 x 768 2150 and 2150, 2111 and 2109; 4096 x 32000 x 2048 1458
+                  // and 1458, 1448 and 1448; 8192 x 128256 x 4096 20938 and 20894, 20799
+                  // and 20910, no difference; 1024 x 50257 x 768 368 and 368, 372 and
+                  // 372; binary32 sums, read again at once, gain nothing)
                   if constexpr (BF) __builtin_nontemporal_store(w, to);
                   else *to = w;
                 } else {

@@ -5,8 +5,12 @@
 // with g = dy w:
 //   dx_ij = r (g_ij - mean_j g_ij - h_ij mean_j (g_ij h_ij)),
 //   dw_j = sum_i dy_ij h_ij,  db_j = sum_i dy_ij.
-// Bound by memory: 16384 x 4096 bf16 forward 47 us (5.7 TB/s), backward 83 + 5
-// (4.8 TB/s), the card's copy rate being 4.7 to 5.1.
+// Bound by memory: 16384 x 4096 bf16 forward 47 to 50 us (5.4 to 5.7 TB/s),
+// backward 83 to 87 + 5 (4.6 to 4.8 TB/s), the card's copy rate being 4.7 to 5.1.
+// Rows that 16 bytes do not divide go a value at a time: 16384 x 4095 bf16
+// forward 67 us, backward with the sums 122; of 4097, where a thread has twice
+// the columns and half of them are none, 121 and 277; binary32 8192 x 769 as
+// fast as x 768 (14 and 21).
 //
 // Sums in binary32; the variance is that of the centred values, never a
 // difference of sums.  Only y and dx (and dw, db of bf16 weights) are rounded

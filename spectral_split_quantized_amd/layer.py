@@ -9,6 +9,10 @@ every GEMM of the forward and backward pass -- Y = X W, dX = D W^T,
 dW = X^T D -- is evaluated through the split.  The right factor of each
 operand is cached and re-sketched every ``refresh`` steps (关键设计 3).
 
+The layers around the linear ones have first derivatives in reverse mode;
+second ones, forward mode, torch.func's transforms and tracing raise
+(torch.compile leaves their calls out of its graphs).
+
 This module is marshalling only: ``metis.prepare_operand`` and
 ``metis.gemm_fwd`` / ``metis.gemm_bwd`` run every step in the HIP library, as
 do the calls of the other layers.
