@@ -96,15 +96,18 @@ def test_forward_mode_through_a_backward_pass_raises():
                 torch.autograd.grad(y, leaf, up)
 
 
-def test_compiled_callers_break_the_graph_and_are_right():
+@pytest.mark.filterwarnings("ignore:Dynamo")
+@pytest.mark.parametrize("backend", ["eager", "aot_eager"])
+def test_compiled_callers_break_the_graph_and_are_right(backend):
     """torch.compile leaves the layers' calls out of its graphs."""
+    torch._dynamo.reset()
     for name, run, leaf in _layers():
-        say("compiled caller: %s" % name)
+        say("compiled caller: %s, %s" % (name, backend))
         leaf.grad = None
         want = run(leaf) * 2
         want.sum().backward()
         grad, leaf.grad = leaf.grad, None
-        got = torch.compile(lambda q: run(q) * 2, backend="eager")(leaf)
+        got = torch.compile(lambda q: run(q) * 2, backend=backend)(leaf)
         got.sum().backward()
         assert torch.equal(got, want) and torch.equal(leaf.grad, grad)
 
